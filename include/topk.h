@@ -307,6 +307,155 @@ int topk_scatter(const void* values, const int64_t* indices, int64_t rows, int64
  * TOPK_EINVAL.  Asynchronous; TOPK_EHIP if the launch fails. */
 int topk_stream_read(const void* data, size_t bytes, uint32_t* sink, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Operators around the selection.  A BatchTopK sparse autoencoder (Prof-K
+ * section 5) encodes its activations with one dense product, keeps the
+ * largest latents of the whole batch (topk over the flattened [1, rows * n]
+ * view), decodes those latents against the rows of a dictionary, and clips
+ * the norm of its gradients.  These are the product, the decode, their
+ * gradients and the clipping.
+ *
+ * Conventions beyond those at the top of this file:
+ *   - Types: float32 and bf16 (all tensors of one call alike; TOPK_EDTYPE for
+ *     others).  Sums, activations and their slopes are held in 32 bits (the
+ *     squares of a norm in 64) and rounded once, to nearest even, when an
+ *     output is written.
+ *   - Matrices are row-major with a row stride ("ld", in elements, at least
+ *     the row length) and element alignment.  16-byte aligned rows (address
+ *     and stride) are read faster.
+ *   - Sizes may be 0: an empty sum is 0.  No size or stride reaches 2^31.
+ *   - Every result is the same from call to call: no sum's order depends on
+ *     timing.
+ *   - `workspace`: 256-byte aligned device memory of at least the size that
+ *     the workspace function of the call gives; no initialisation, nothing
+ *     kept between calls.  It may be null when that size is 0.  One workspace
+ *     must not be used by two calls that may run at the same time (two
+ *     captured graphs replayed side by side included).
+ *   - Outputs must not overlap inputs, unless stated.  No allocation, memset
+ *     or synchronisation: every call can be captured in a HIP graph.
+ * ------------------------------------------------------------------------ */
+
+/* gelu is z * Phi(z) with the normal distribution function; silu is
+ * z / (1 + exp(-z)).  At -inf both are 0, with slope 0.  relu keeps NaN; its
+ * slope is 0 at 0. */
+typedef enum {
+  TOPK_ACT_NONE = 0,
+  TOPK_ACT_RELU = 1,
+  TOPK_ACT_GELU = 2,
+  TOPK_ACT_SILU = 3
+} topk_activation;
+
+/* y = act(z) + residual, z = x W^T + bias. */
+typedef struct {
+  const void* x;        /* [m, k], row stride ldx; with x_trans stored as [k, m] */
+  const void* w;        /* [n, k], row stride ldw; with w_trans stored as [k, n] */
+  const void* bias;     /* [n], or null */
+  const void* residual; /* [m, n], row stride ldr, or null; may be y itself (ldr == ldy) */
+  void* y;              /* [m, n], row stride ldy */
+  void* pre;            /* [m, n], row stride ldp: z, for the gradient; or null */
+  int64_t m, n, k;
+  int64_t ldx, ldw, ldr, ldy, ldp;
+  int32_t dtype, act;   /* topk_dtype (float32, bf16), topk_activation */
+  int32_t x_trans, w_trans;
+} topk_linear_args;
+
+/* Workspace bytes of one call (it depends on sizes, strides and alignment). */
+int topk_linear_workspace_size(const topk_linear_args* args, size_t* bytes);
+/* Errors: TOPK_EDTYPE, TOPK_EINVAL (sizes, strides, activation, null or
+ * misaligned pointers), TOPK_EWORKSPACE, TOPK_EHIP. */
+int topk_linear(const topk_linear_args* args, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of topk_linear from dy = dL/dy.  With dz = dy * act'(z):
+ *   dx = dz W, dw = dz^T x, db[j] = sum over rows of dz[:, j];
+ * the residual's gradient is dy itself.  dz is rounded to the tensors' type
+ * before the two products (their matrix operands); db sums it unrounded.
+ * `pre` is z as topk_linear wrote it; for relu without a residual y serves as
+ * well (positive at the same places).  Not read for TOPK_ACT_NONE. */
+typedef struct {
+  const void* dy;       /* [m, n], row stride ldd */
+  const void* pre;      /* [m, n], row stride ldp */
+  const void* x;        /* as in topk_linear_args; not read when dw is null */
+  const void* w;        /* not read when dx is null */
+  void* dx;             /* [m, k], row stride lddx; or null: not wanted */
+  void* dw;             /* [n, k], row stride lddw; or null */
+  void* db;             /* [n]; or null */
+  int64_t m, n, k;
+  int64_t ldd, ldp, ldx, ldw, lddx, lddw;
+  int32_t dtype, act;
+  int32_t x_trans, w_trans;
+} topk_linear_grad_args;
+
+int topk_linear_grad_workspace_size(const topk_linear_grad_args* args, size_t* bytes);
+int topk_linear_grad(const topk_linear_grad_args* args, void* workspace, size_t workspace_bytes,
+                     void* stream);
+
+/* A selection as topk returns it.  flat = 0: values and indices are [rows, k]
+ * and an index is a latent in [0, n).  flat != 0: they hold k entries of the
+ * flattened [rows, n] matrix (BatchTopK) and an index is row * n + latent.
+ * Entries with an index out of range (a relaxed recall's padded slots, -1)
+ * belong to no row: they add nothing and get a gradient of 0.  An index that
+ * occurs twice counts twice. */
+typedef struct {
+  const void* values;
+  const int64_t* indices;
+  int64_t rows, k, n;
+  int32_t flat, dtype;
+} topk_selection;
+
+/* Workspace bytes that serve topk_decode, topk_decode_grad and
+ * topk_encode_grad on this selection with rows of d elements (the pointers of
+ * `sel` are not read). */
+int topk_decode_workspace_size(const topk_selection* sel, int64_t d, size_t* bytes);
+
+/* out[r] = bias + sum over the entries e of row r of values[e] * weight[latent e]:
+ * weight [n, d] (row stride ldw), bias [d] or null, out [rows, d] (row stride
+ * ldo).  Rows without an entry are the bias, or 0.  Errors: TOPK_EDTYPE,
+ * TOPK_EINVAL, TOPK_EWORKSPACE, TOPK_EHIP. */
+int topk_decode(const topk_selection* sel, const void* weight, int64_t ldw, int64_t d,
+                const void* bias, void* out, int64_t ldo, void* workspace, size_t workspace_bytes,
+                void* stream);
+
+/* Gradients of topk_decode from grad = dL/dout [rows, d] (row stride ldg):
+ *   dvalues[e] = <grad[row e], weight[latent e]>, laid out as the values;
+ *   dweight[j] = sum over the entries e of latent j of values[e] * grad[row e]
+ *   ([n, d], row stride lddw, every row written);
+ *   dbias = the sum of grad's rows ([d]).
+ * Each output may be null: not wanted. */
+int topk_decode_grad(const topk_selection* sel, const void* weight, int64_t ldw, int64_t d,
+                     const void* grad, int64_t ldg, void* dvalues, void* dweight, int64_t lddw,
+                     void* dbias, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of the encoder through the selection: sel holds the selected
+ * entries of relu(x W^T + b) (x [rows, d], W [n, d]), grad_values = dL/dvalues,
+ * laid out as the values.  Only selected places with a value above 0 have a
+ * gradient c_e = grad_values[e]:
+ *   dx[r] = sum of c_e W[latent e]  ([rows, d], row stride lddx)
+ *   dweight[j] = sum of c_e x[row e] ([n, d], row stride lddw)
+ *   dbias[j] = sum of c_e            ([n])
+ * Each output may be null; weight is not read without dx, x not without dweight. */
+int topk_encode_grad(const topk_selection* sel, const void* grad_values, const void* x, int64_t ldx,
+                     const void* weight, int64_t ldw, int64_t d, void* dx, int64_t lddx,
+                     void* dweight, int64_t lddw, void* dbias, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/* Global 2-norm of `tensors` dense tensors (host arrays: device address,
+ * element count and topk_dtype of each; float32 and bf16 may be mixed; a
+ * count may be 0) into norm[0], a float in device memory.  topk_clip_grad_norm
+ * then scales every element by min(1, max_norm / (norm + eps)), in 32 bits,
+ * rounded to its type; when that factor is 1 nothing is written.  A norm of
+ * inf or NaN gives factors 0 and NaN, as the formula says; the norm tells.
+ * The host arrays are read before the call returns.  Tensors must not overlap
+ * one another when they are scaled (TOPK_EINVAL).  max_norm and eps: not
+ * negative, not NaN.  Errors: TOPK_EDTYPE, TOPK_EINVAL, TOPK_EWORKSPACE,
+ * TOPK_EHIP. */
+int topk_grad_norm_workspace_size(int64_t tensors, const int64_t* counts, size_t* bytes);
+int topk_grad_norm(const void* const* ptrs, const int64_t* counts, const int32_t* dtypes,
+                   int64_t tensors, float* norm, void* workspace, size_t workspace_bytes,
+                   void* stream);
+int topk_clip_grad_norm(void* const* ptrs, const int64_t* counts, const int32_t* dtypes,
+                        int64_t tensors, float max_norm, float eps, float* norm, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
 /* Short English text for a status code (static storage). */
 const char* topk_status_string(int status);
 

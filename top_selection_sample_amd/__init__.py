@@ -7,6 +7,14 @@
 each row in rank order (value descending, equal values by lower index), as
 the input's own bits and int64 row-local indices.  PyTorch only supplies
 device memory and the stream; the selection runs in libtopk_mi355x.so.
+
+Around the selection, for BatchTopK sparse autoencoders (differentiable):
+
+    values, indices = tss.encode(x, w_enc, b_enc, k_total)       # relu(x W^T + b), flattened top-k
+    out = tss.decode(values, indices, w_dec, rows=len(x), bias=b_dec)
+    norm = tss.clip_grad_norm([p.grad for p in params], 1.0)
+
+and the dense product on its own, ``linear`` (bias, activation, residual).
 """
 from __future__ import annotations
 
@@ -32,7 +40,9 @@ __all__ = ["topk", "plan", "profile_enable", "profile_read", "stream_read", "sca
            "POLICY_EXACT_TAIL", "POLICY_ALG1", "POLICY_TUNED", "dtype_code",
            "TAU_NONE", "TAU_FILTER_LISTS", "TAU_KTAU_LISTS", "TAU_KTAU_REGS", "TAU_KTAU_STREAM",
            "TAU_FORCED", "TAU_FILTER_RADIX", "TAU_FILTER_MERGE", "TAU_BIN_STREAMED", "TAU_BIN_RADIX",
-           "TEST_BARRIER_GIVEUP", "filter_trace"]
+           "TEST_BARRIER_GIVEUP", "filter_trace",
+           "linear", "linear_grad", "encode", "encode_grad", "decode", "decode_grad", "grad_norm",
+           "clip_grad_norm"]
 
 _TORCH_CODES = {torch.int32: 0, torch.float32: 1, torch.bfloat16: 2}
 _NAME_CODES = _lib.DTYPE_CODES
@@ -276,3 +286,8 @@ def batchtopk(acts: torch.Tensor, k_total: int, params: Params | None = None, ma
         out, m = res
         return out.reshape(acts.shape), m.reshape(acts.shape)
     return res.reshape(acts.shape)
+
+
+# the operators around the selection (they use topk above)
+from ._ops import (clip_grad_norm, decode, decode_grad, encode, encode_grad, grad_norm,  # noqa: E402
+                   linear, linear_grad)

@@ -33,7 +33,13 @@ TEST_BARRIER_GIVEUP = 1
 EXPORTS = ("topk_default_params", "topk_plan", "topk_workspace_size", "topk_workspace_init",
            "topk", "topk_ex", "topk_read_stats", "topk_profile_enable", "topk_profile_read",
            "topk_scatter", "topk_stream_read", "topk_status_string", "topk_noalloc",
-           "topk_filter_trace")
+           "topk_filter_trace",
+           "topk_linear_workspace_size", "topk_linear", "topk_linear_grad_workspace_size",
+           "topk_linear_grad", "topk_decode_workspace_size", "topk_decode", "topk_decode_grad",
+           "topk_encode_grad", "topk_grad_norm_workspace_size", "topk_grad_norm",
+           "topk_clip_grad_norm")
+# the activations of topk_linear's epilogue
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
 STAGES = ("sample", "tau", "filter", "refine", "exact", "sort")
 
 
@@ -69,6 +75,25 @@ class RowStats(ctypes.Structure):
                 ("tau_route", ctypes.c_uint32)]
 
 
+class LinearArgs(ctypes.Structure):
+    _fields_ = ([(f, ctypes.c_void_p) for f in ("x", "w", "bias", "residual", "y", "pre")]
+                + [(f, ctypes.c_int64) for f in ("m", "n", "k", "ldx", "ldw", "ldr", "ldy", "ldp")]
+                + [(f, ctypes.c_int32) for f in ("dtype", "act", "x_trans", "w_trans")])
+
+
+class LinearGradArgs(ctypes.Structure):
+    _fields_ = ([(f, ctypes.c_void_p) for f in ("dy", "pre", "x", "w", "dx", "dw", "db")]
+                + [(f, ctypes.c_int64) for f in ("m", "n", "k", "ldd", "ldp", "ldx", "ldw", "lddx",
+                                                 "lddw")]
+                + [(f, ctypes.c_int32) for f in ("dtype", "act", "x_trans", "w_trans")])
+
+
+class Selection(ctypes.Structure):
+    _fields_ = [("values", ctypes.c_void_p), ("indices", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("k", ctypes.c_int64), ("n", ctypes.c_int64), ("flat", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -90,6 +115,19 @@ def _load():
     L.topk_filter_trace.argtypes = [ctypes.c_void_p, ctypes.c_size_t]
     L.topk_stream_read.argtypes = [vp, sz, vp, vp]
     L.topk_scatter.argtypes = [vp, vp, i64, i64, i64, i32, vp, vp, vp]
+    L.topk_linear_workspace_size.argtypes = [P(LinearArgs), P(sz)]
+    L.topk_linear.argtypes = [P(LinearArgs), vp, sz, vp]
+    L.topk_linear_grad_workspace_size.argtypes = [P(LinearGradArgs), P(sz)]
+    L.topk_linear_grad.argtypes = [P(LinearGradArgs), vp, sz, vp]
+    L.topk_decode_workspace_size.argtypes = [P(Selection), i64, P(sz)]
+    L.topk_decode.argtypes = [P(Selection), vp, i64, i64, vp, vp, i64, vp, sz, vp]
+    L.topk_decode_grad.argtypes = [P(Selection), vp, i64, i64, vp, i64, vp, vp, i64, vp, vp, sz, vp]
+    L.topk_encode_grad.argtypes = [P(Selection), vp, vp, i64, vp, i64, i64, vp, i64, vp, i64, vp, vp,
+                                   sz, vp]
+    L.topk_grad_norm_workspace_size.argtypes = [i64, P(i64), P(sz)]
+    L.topk_grad_norm.argtypes = [P(vp), P(i64), P(ctypes.c_int32), i64, vp, vp, sz, vp]
+    L.topk_clip_grad_norm.argtypes = [P(vp), P(i64), P(ctypes.c_int32), i64, ctypes.c_float,
+                                      ctypes.c_float, vp, vp, sz, vp]
     L.topk_status_string.argtypes = [i32]
     L.topk_status_string.restype = ctypes.c_char_p
     for name in EXPORTS:

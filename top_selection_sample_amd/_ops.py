@@ -1,0 +1,523 @@
+"""The operators around the selection: the dense product with its epilogue,
+the sparse decode, their gradients, and the clipping of a global norm
+(include/topk.h, "Operators around the selection").
+
+Argument checks and marshalling only; every step runs in the HIP library.
+Scratch memory comes from torch's allocator for each call, so calls on
+different streams, and captured graphs, never share any.
+"""
+from __future__ import annotations
+
+import ctypes
+from contextlib import nullcontext
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import _lib
+
+_CODES = {torch.float32: 1, torch.bfloat16: 2}
+_byref = ctypes.byref
+
+
+def _code(t: torch.Tensor, what: str) -> int:
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{what}: unsupported dtype {t.dtype}; use float32 or bfloat16")
+    return code
+
+
+def _check(t, what: str, like: torch.Tensor, shape=None, dtype=None):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what}: need a tensor")
+    dtype = dtype or like.dtype
+    if t.device != like.device or t.dtype != dtype or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError(f"{what}: need a {dtype} tensor of shape {shape} on {like.device}, "
+                         f"not {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _gpu(t, what: str):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{what} must be a GPU tensor")
+
+
+def _on(dev):
+    """The library launches on the current device: switch when the tensors live elsewhere."""
+    return torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else nullcontext()
+
+
+def _stream(dev) -> int:
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _scratch(nbytes: int, dev):
+    return torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+
+
+def _ptr(t):
+    return t.data_ptr() if t is not None else None
+
+
+def _matrix(t: torch.Tensor, either: bool = False):
+    """(tensor, row stride, stored transposed) of a 2-D tensor: rows with unit
+    stride as they are; columns with unit stride too where the call takes
+    ``either`` order; any other layout (expanded, stepped) as a copy."""
+    r, c = t.shape
+    sr, sc = t.stride()
+    if (sc == 1 or c <= 1) and (sr >= c or r <= 1):
+        return t, max(sr if r > 1 else c, c, 1), 0
+    if either and (sr == 1 or r <= 1) and (sc >= r or c <= 1):
+        return t, max(sc if c > 1 else r, r, 1), 1
+    return t.contiguous(), max(c, 1), 0
+
+
+def _empty(*outs) -> bool:
+    """Whether no wanted output has an element (the library takes an empty output, a null address, for not wanted)."""
+    return not any(t is not None and t.numel() for t in outs)
+
+
+def _act_code(activation: str) -> int:
+    code = _lib.ACTIVATIONS.get(activation)
+    if code is None:
+        raise ValueError(f"activation: one of {', '.join(_lib.ACTIVATIONS)}, not {activation!r}")
+    return code
+
+
+def _wants_grad(*tensors) -> bool:
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
+# ---------------------------------------------------------------- linear
+def _linear_run(x, w, bias, act, residual, want_pre):
+    m, k = x.shape
+    n = w.shape[0]
+    dev = x.device
+    x, ldx, xt = _matrix(x, True)
+    w, ldw, wt = _matrix(w, True)
+    ldr = 0
+    if residual is not None:
+        residual, ldr, _ = _matrix(residual)
+    if bias is not None:
+        bias = bias.contiguous()
+    with _on(dev):
+        y = torch.empty((m, n), dtype=x.dtype, device=dev)
+        pre = torch.empty((m, n), dtype=x.dtype, device=dev) if want_pre else None
+        a = _lib.LinearArgs(x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(residual), y.data_ptr(),
+                            _ptr(pre), m, n, k, ldx, ldw, ldr, n, n, _CODES[x.dtype], act, xt, wt)
+        size = ctypes.c_size_t()
+        _lib.check(_lib.lib.topk_linear_workspace_size(_byref(a), _byref(size)), "linear")
+        ws = _scratch(size.value, dev)
+        _lib.check(_lib.lib.topk_linear(_byref(a), _ptr(ws), size.value, _stream(dev)), "linear")
+    return y, pre
+
+
+def _linear_grad_run(dy, x, w, act, pre, need):
+    m, n = dy.shape
+    k = w.shape[1]
+    dev = dy.device
+    dy, ldd, _ = _matrix(dy)
+    x, ldx, xt = _matrix(x, True)
+    w, ldw, wt = _matrix(w, True)
+    ldp = 0
+    if pre is not None:
+        pre, ldp, _ = _matrix(pre)
+    with _on(dev):
+        dx = torch.empty((m, k), dtype=dy.dtype, device=dev) if need[0] else None
+        dw = torch.empty((n, k), dtype=dy.dtype, device=dev) if need[1] else None
+        db = torch.empty((n,), dtype=dy.dtype, device=dev) if need[2] else None
+        if _empty(dx, dw, db):
+            return dx, dw, db
+        a = _lib.LinearGradArgs(dy.data_ptr(), _ptr(pre), x.data_ptr(), w.data_ptr(), _ptr(dx), _ptr(dw),
+                                _ptr(db), m, n, k, ldd, ldp, ldx, ldw, k, k, _CODES[dy.dtype], act, xt, wt)
+        size = ctypes.c_size_t()
+        _lib.check(_lib.lib.topk_linear_grad_workspace_size(_byref(a), _byref(size)), "linear_grad")
+        ws = _scratch(size.value, dev)
+        _lib.check(_lib.lib.topk_linear_grad(_byref(a), _ptr(ws), size.value, _stream(dev)),
+                   "linear_grad")
+    return dx, dw, db
+
+
+class _Linear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, bias, residual, act):
+        # relu's slope is read from y, unless the residual hides it; gelu and
+        # silu need the pre-activation
+        keep = act > 1 or (act == 1 and residual is not None)
+        y, pre = _linear_run(x, w, bias, act, residual, keep)
+        ctx.act, ctx.bias, ctx.residual = act, bias is not None, residual is not None
+        ctx.save_for_backward(x, w, pre if keep else y if act else None)
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, w, pre = ctx.saved_tensors
+        nx, nw, nb, nr, _ = ctx.needs_input_grad
+        dx = dw = db = None
+        if nx or nw or nb:
+            dx, dw, db = _linear_grad_run(dy, x, w, ctx.act, pre, (nx, nw, nb))
+        return dx, dw, db, dy if nr else None, None
+
+
+def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None,
+           activation: str = "none", residual: torch.Tensor | None = None) -> torch.Tensor:
+    """``act(x @ weight.T + bias) + residual`` in one pass.
+
+    ``x`` [..., k], ``weight`` [n, k] (as torch.nn.Linear keeps it; the
+    transpose of a [k, n] tensor is read in place), ``bias`` [n], ``residual``
+    [..., n]; float32 or bfloat16, all alike.  ``activation``: "none", "relu",
+    "gelu" (z * Phi(z)) or "silu".  Sums and the epilogue are held in 32 bits.
+    Differentiable (once).  Under HIP graph capture call ``linear`` with
+    gradients off and ``linear_grad``, which take no part in autograd's graph."""
+    _gpu(x, "x")
+    _code(x, "x")
+    act = _act_code(activation)
+    if x.dim() < 1 or not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("x: [..., k]; weight: [n, k]")
+    n, k = weight.shape
+    lead = x.shape[:-1]
+    _check(weight, "weight", x)
+    if x.shape[-1] != k:
+        raise ValueError(f"x has {x.shape[-1]} columns, weight {k}")
+    if bias is not None:
+        _check(bias, "bias", x, (n,))
+    if residual is not None:
+        _check(residual, "residual", x, tuple(lead) + (n,))
+    flat = x.dim() == 2
+    x2 = x if flat else x.reshape(lead.numel(), k)
+    r2 = residual if flat or residual is None else residual.reshape(lead.numel(), n)
+    if _wants_grad(x, weight, bias, residual):
+        y = _Linear.apply(x2, weight, bias, r2, act)
+    else:
+        y = _linear_run(x2, weight, bias, act, r2, False)[0]
+    return y if flat else y.reshape(*lead, n)
+
+
+def linear_grad(grad: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, activation: str = "none",
+                pre: torch.Tensor | None = None, need: tuple = (True, True, True)) -> tuple:
+    """Gradients (dx, dweight, dbias) of ``linear`` from ``grad`` = dL/dy.
+
+    ``grad`` [m, n], ``x`` [m, k], ``weight`` [n, k]; ``pre`` [m, n]: the
+    pre-activation ``linear(x, weight, bias)``, or for relu without a residual
+    the output (needed unless the activation is "none").  The residual's
+    gradient is ``grad``.  ``need``: which of the three to compute; None stands
+    for the others."""
+    _gpu(grad, "grad")
+    _code(grad, "grad")
+    act = _act_code(activation)
+    if grad.dim() != 2 or not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("grad: [m, n]; x: [m, k]; weight: [n, k]")
+    m, n = grad.shape
+    k = weight.shape[1]
+    _check(weight, "weight", grad, (n, k))
+    _check(x, "x", grad, (m, k))
+    if act:
+        if pre is None:
+            raise ValueError("pre: the pre-activation is needed")
+        _check(pre, "pre", grad, (m, n))
+    else:
+        pre = None
+    need = tuple(bool(b) for b in need)
+    if len(need) != 3:
+        raise ValueError("need: three truth values")
+    if not any(need):
+        return None, None, None
+    with torch.no_grad():
+        return _linear_grad_run(grad, x, weight, act, pre, need)
+
+
+# ---------------------------------------------------------------- decode
+def _selection(values, indices, rows, n):
+    """The selection's struct: 1-D values with rows = 1, or [rows, k], hold
+    latents; 1-D values of more rows hold flattened places."""
+    if values.dim() == 2:
+        return _lib.Selection(values.data_ptr(), indices.data_ptr(), values.shape[0], values.shape[1], n,
+                              0, _CODES[values.dtype])
+    return _lib.Selection(values.data_ptr(), indices.data_ptr(), rows, values.shape[0], n, 1,
+                          _CODES[values.dtype])
+
+
+def _decode_scratch(sel, d, dev):
+    size = ctypes.c_size_t()
+    _lib.check(_lib.lib.topk_decode_workspace_size(_byref(sel), d, _byref(size)), "decode")
+    return _scratch(size.value, dev), size.value
+
+
+def _decode_run(values, indices, weight, rows, bias):
+    n, d = weight.shape
+    dev = values.device
+    values, indices = values.contiguous(), indices.contiguous()
+    weight, ldw, _ = _matrix(weight)
+    if bias is not None:
+        bias = bias.contiguous()
+    with _on(dev):
+        out = torch.empty((rows, d), dtype=values.dtype, device=dev)
+        sel = _selection(values, indices, rows, n)
+        ws, size = _decode_scratch(sel, d, dev)
+        _lib.check(_lib.lib.topk_decode(_byref(sel), weight.data_ptr(), ldw, d, _ptr(bias),
+                                        out.data_ptr(), max(d, 1), _ptr(ws), size, _stream(dev)),
+                   "decode")
+    return out
+
+
+def _decode_grad_run(grad, values, indices, weight, need):
+    n, d = weight.shape
+    rows = grad.shape[0]
+    dev = grad.device
+    values, indices = values.contiguous(), indices.contiguous()
+    weight, ldw, _ = _matrix(weight)
+    grad, ldg, _ = _matrix(grad)
+    with _on(dev):
+        dv = torch.empty_like(values) if need[0] else None
+        dw = torch.empty((n, d), dtype=grad.dtype, device=dev) if need[1] else None
+        db = torch.empty((d,), dtype=grad.dtype, device=dev) if need[2] else None
+        if _empty(dv, dw, db):
+            return dv, dw, db
+        sel = _selection(values, indices, rows, n)
+        ws, size = _decode_scratch(sel, d, dev)
+        _lib.check(_lib.lib.topk_decode_grad(_byref(sel), weight.data_ptr(), ldw, d, grad.data_ptr(), ldg,
+                                             _ptr(dv), _ptr(dw), max(d, 1), _ptr(db), _ptr(ws), size,
+                                             _stream(dev)), "decode_grad")
+    return dv, dw, db
+
+
+class _Decode(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, values, indices, weight, rows, bias):
+        ctx.save_for_backward(values, indices, weight)
+        return _decode_run(values, indices, weight, rows, bias)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad):
+        values, indices, weight = ctx.saved_tensors
+        nv, _, nw, _, nb = ctx.needs_input_grad
+        dv, dw, db = _decode_grad_run(grad, values, indices, weight, (nv, nw, nb))
+        return dv, None, dw, None, db
+
+
+def _check_selection(values, indices, rows):
+    _gpu(values, "values")
+    _code(values, "values")
+    if values.dim() not in (1, 2):
+        raise ValueError("values, indices: [rows, k], or [k] of a flattened selection")
+    _check(indices, "indices", values, tuple(values.shape), torch.int64)
+    if values.dim() == 2:
+        if rows is not None and rows != values.shape[0]:
+            raise ValueError(f"rows is {rows}, values has {values.shape[0]}")
+        return values.shape[0]
+    if rows is None or rows < 0:
+        raise ValueError("rows: needed for a flattened selection")
+    return int(rows)
+
+
+def decode(values: torch.Tensor, indices: torch.Tensor, weight: torch.Tensor, rows: int | None = None,
+           bias: torch.Tensor | None = None) -> torch.Tensor:
+    """Sparse decode of a selection: ``out[r] = bias + sum of v_e * weight[latent_e]``
+    over the selected entries e of row r, without the dense activation.
+
+    ``values``, ``indices`` as ``topk`` returns them: [rows, k] with latents in
+    [0, n), or [k] of a flattened [rows, n] selection (then ``rows`` is
+    needed; an index is row * n + latent).  ``weight`` [n, d], ``bias`` [d].
+    Entries out of range (the -1 of padded slots) add nothing; an index that
+    occurs twice counts twice.  Returns [rows, d].  Differentiable (once) in
+    values, weight and bias."""
+    rows = _check_selection(values, indices, rows)
+    _check(weight, "weight", values)
+    if weight.dim() != 2:
+        raise ValueError("weight: [n, d]")
+    if bias is not None:
+        _check(bias, "bias", values, (weight.shape[1],))
+    if _wants_grad(values, weight, bias):
+        return _Decode.apply(values, indices, weight, rows, bias)
+    return _decode_run(values, indices, weight, rows, bias)
+
+
+def decode_grad(grad: torch.Tensor, values: torch.Tensor, indices: torch.Tensor, weight: torch.Tensor,
+                need: tuple = (True, True, True)) -> tuple:
+    """Gradients (dvalues, dweight, dbias) of ``decode`` from ``grad`` = dL/dout
+    [rows, d].  Entries out of range get a gradient of 0.  ``need``: which of
+    the three to compute; None stands for the others."""
+    _gpu(grad, "grad")
+    if grad.dim() != 2 or not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("grad: [rows, d]; weight: [n, d]")
+    rows = _check_selection(values, indices, grad.shape[0])
+    _check(weight, "weight", values)
+    _check(grad, "grad", values, (rows, weight.shape[1]))
+    need = tuple(bool(b) for b in need)
+    if len(need) != 3:
+        raise ValueError("need: three truth values")
+    if not any(need):
+        return None, None, None
+    with torch.no_grad():
+        return _decode_grad_run(grad, values, indices, weight, need)
+
+
+# ---------------------------------------------------------------- encode
+def _encode_grad_run(grad_values, values, indices, x, weight, need):
+    n, d = weight.shape
+    rows = x.shape[0]
+    dev = x.device
+    grad_values, values, indices = grad_values.contiguous(), values.contiguous(), indices.contiguous()
+    weight, ldw, _ = _matrix(weight)
+    x, ldx, _ = _matrix(x)
+    with _on(dev):
+        dx = torch.empty((rows, d), dtype=x.dtype, device=dev) if need[0] else None
+        dw = torch.empty((n, d), dtype=x.dtype, device=dev) if need[1] else None
+        db = torch.empty((n,), dtype=x.dtype, device=dev) if need[2] else None
+        if _empty(dx, dw, db):
+            return dx, dw, db
+        sel = _selection(values, indices, rows, n)
+        ws, size = _decode_scratch(sel, d, dev)
+        _lib.check(_lib.lib.topk_encode_grad(_byref(sel), grad_values.data_ptr(), x.data_ptr(), ldx,
+                                             weight.data_ptr(), ldw, d, _ptr(dx), max(d, 1), _ptr(dw),
+                                             max(d, 1), _ptr(db), _ptr(ws), size, _stream(dev)),
+                   "encode_grad")
+    return dx, dw, db
+
+
+class _Encode(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, k_total, params):
+        values, indices = _encode_run(x, weight, bias, k_total, params)
+        ctx.save_for_backward(x, weight, values, indices)
+        ctx.mark_non_differentiable(indices)
+        return values, indices
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_values, _):
+        x, weight, values, indices = ctx.saved_tensors
+        nx, nw, nb, _, _ = ctx.needs_input_grad
+        dx, dw, db = _encode_grad_run(grad_values, values, indices, x, weight, (nx, nw, nb))
+        return dx, dw, db, None, None
+
+
+def _encode_run(x, weight, bias, k_total, params):
+    from . import topk
+    acts = _linear_run(x, weight, bias, _lib.ACTIVATIONS["relu"], None, False)[0]
+    values, indices = topk(acts.reshape(1, -1), k_total, params=params)
+    return values[0], indices[0]
+
+
+def encode(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None, k_total: int,
+           params=None) -> tuple:
+    """The encoder of a BatchTopK sparse autoencoder (Prof-K section 5): the
+    ``k_total`` largest entries of ``relu(x @ weight.T + bias)`` over the whole
+    batch, as (values [k_total], flattened indices [k_total]) in rank order.
+
+    ``x`` [rows, d], ``weight`` [n, d], ``bias`` [n]; float32 or bfloat16.
+    Differentiable (once) in x, weight and bias through the selected entries
+    above 0 (the others have no gradient); the backward touches those entries
+    only.  ``params``: as ``topk``'s."""
+    _gpu(x, "x")
+    _code(x, "x")
+    if x.dim() != 2 or not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("x: [rows, d]; weight: [n, d]")
+    _check(weight, "weight", x)
+    if weight.shape[1] != x.shape[1]:
+        raise ValueError(f"x has {x.shape[1]} columns, weight {weight.shape[1]}")
+    if bias is not None:
+        _check(bias, "bias", x, (weight.shape[0],))
+    if not 1 <= k_total <= x.shape[0] * weight.shape[0]:
+        raise ValueError("k_total: from 1 to rows * n")
+    if _wants_grad(x, weight, bias):
+        return _Encode.apply(x, weight, bias, k_total, params)
+    return _encode_run(x, weight, bias, k_total, params)
+
+
+def encode_grad(grad_values: torch.Tensor, values: torch.Tensor, indices: torch.Tensor,
+                x: torch.Tensor, weight: torch.Tensor, need: tuple = (True, True, True)) -> tuple:
+    """Gradients (dx, dweight, dbias) of ``encode`` from ``grad_values`` =
+    dL/dvalues: with c_e = grad_values[e] where values[e] > 0 and 0 elsewhere,
+    ``dx[r] = sum of c_e * weight[latent_e]``, ``dweight[j] = sum of c_e * x[row_e]``,
+    ``dbias[j] = sum of c_e``.  A selection of [rows, k] (row-wise) is taken
+    as well.  ``need``: which of the three to compute; None stands for the others."""
+    _gpu(x, "x")
+    if x.dim() != 2 or not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("x: [rows, d]; weight: [n, d]")
+    rows = _check_selection(values, indices, x.shape[0])
+    _check(grad_values, "grad_values", values, tuple(values.shape))
+    _check(weight, "weight", values, (weight.shape[0], x.shape[1]))
+    _check(x, "x", values, (rows, weight.shape[1]))
+    need = tuple(bool(b) for b in need)
+    if len(need) != 3:
+        raise ValueError("need: three truth values")
+    if not any(need):
+        return None, None, None
+    with torch.no_grad():
+        return _encode_grad_run(grad_values, values, indices, x, weight, need)
+
+
+# ---------------------------------------------------------------- gradient norm
+def _dense(t: torch.Tensor) -> bool:
+    """Whether the elements fill one block of memory without gaps or overlap, in any order of the axes."""
+    if t.is_contiguous():
+        return True
+    at = 1
+    for stride, size in sorted((st, sz) for st, sz in zip(t.stride(), t.shape) if sz != 1):
+        if stride != at:
+            return False
+        at *= size
+    return True
+
+
+def _norm_args(tensors):
+    if isinstance(tensors, torch.Tensor):
+        tensors = [tensors]
+    ts = [t for t in tensors if t is not None]
+    if not ts:
+        return ts, None, None
+    dev = ts[0].device
+    for t in ts:
+        if not t.is_cuda or t.device != dev:
+            raise ValueError(f"tensors: all on one GPU (found {dev} and {t.device})")
+        if t.dtype not in _CODES:
+            raise TypeError(f"tensors: unsupported dtype {t.dtype}; use float32 or bfloat16")
+        if not _dense(t):
+            raise ValueError("tensors: need dense memory (no gaps, no expanded axes)")
+    n = len(ts)
+    args = ((ctypes.c_void_p * n)(*[t.data_ptr() for t in ts]),
+            (ctypes.c_int64 * n)(*[t.numel() for t in ts]),
+            (ctypes.c_int32 * n)(*[_CODES[t.dtype] for t in ts]), n)
+    return ts, dev, args
+
+
+def _norm_run(tensors, clip):
+    ts, dev, args = _norm_args(tensors)
+    if not ts:
+        return torch.zeros((), device="cuda")
+    with _on(dev):
+        norm = torch.empty((), dtype=torch.float32, device=dev)
+        size = ctypes.c_size_t()
+        _lib.check(_lib.lib.topk_grad_norm_workspace_size(args[3], args[1], _byref(size)), "grad_norm")
+        ws = _scratch(size.value, dev)
+        if clip is None:
+            _lib.check(_lib.lib.topk_grad_norm(*args, norm.data_ptr(), _ptr(ws), size.value, _stream(dev)),
+                       "grad_norm")
+        else:
+            _lib.check(_lib.lib.topk_clip_grad_norm(*args, *clip, norm.data_ptr(), _ptr(ws), size.value,
+                                                    _stream(dev)), "clip_grad_norm")
+            _written(ts)
+    return norm
+
+
+def _written(ts):
+    """Tell autograd that the tensors changed in place (inference tensors keep no count)."""
+    torch.autograd.graph.increment_version([t for t in ts if not t.is_inference()])
+
+
+@torch.no_grad()
+def grad_norm(tensors) -> torch.Tensor:
+    """The 2-norm of all elements of ``tensors`` (one tensor or several, dense,
+    float32 and bfloat16 mixed, None skipped), as a float32 scalar on their GPU."""
+    return _norm_run(tensors, None)
+
+
+@torch.no_grad()
+def clip_grad_norm(tensors, max_norm: float, eps: float = 1e-6) -> torch.Tensor:
+    """Scale ``tensors`` in place by min(1, max_norm / (norm + eps)), ``norm`` their
+    global 2-norm, which is returned as a float32 scalar on the GPU (no
+    synchronisation).  Tensors as in ``grad_norm``, none overlapping another
+    (TopkError).  A norm of inf or NaN scales by 0 or NaN: read the norm to tell."""
+    return _norm_run(tensors, (float(max_norm), float(eps)))

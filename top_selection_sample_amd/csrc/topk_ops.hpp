@@ -1,0 +1,118 @@
+// Internal interface of the operators around the selection (dense product,
+// sparse decode, gradient norm): the host checks call these launchers.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace tk {
+
+enum : int { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_SILU = 3 };
+
+// One operand of a product, [rows, red] with `red` the summed axis: element
+// (r, c) sits at p[r * ld + c], or at p[c * ld + r] when `trans`.
+struct Operand {
+  const void* p = nullptr;
+  int64_t ld = 0;
+  bool trans = false;
+};
+
+// C[m, n] = epilogue(A[m, k] B[n, k]^T)
+struct GemmArgs {
+  Operand a, b;
+  int64_t m = 0, n = 0, k = 0;
+  int dtype = 1;
+  int act = ACT_NONE;
+  const void* bias = nullptr;       // [n]
+  const void* residual = nullptr;   // [m, n], row stride ldr
+  int64_t ldr = 0;
+  void* c = nullptr;                // [m, n], row stride ldc
+  int64_t ldc = 0;
+  void* pre = nullptr;              // optional: the pre-activation, row stride ldp
+  int64_t ldp = 0;
+  int cus = 256;
+};
+
+size_t gemm_workspace(const GemmArgs& g);
+hipError_t launch_gemm(const GemmArgs& g, void* ws, hipStream_t s);
+
+// dz = dy * act'(pre) into `dz` (null: not wanted, act == ACT_NONE), and its
+// column sums into `db` (null: not wanted).
+struct SlopeArgs {
+  const void* dy = nullptr;
+  int64_t ldd = 0;
+  const void* pre = nullptr;
+  int64_t ldp = 0;
+  int64_t m = 0, n = 0;
+  int dtype = 1;
+  int act = ACT_NONE;
+  void* dz = nullptr;
+  int64_t ldz = 0;
+  void* db = nullptr;
+};
+
+size_t slope_workspace(const SlopeArgs& a);
+hipError_t launch_slope(const SlopeArgs& a, void* ws, hipStream_t s);
+
+// A selection: `total` entries.  flat: index = row * n + latent; otherwise
+// entry e belongs to row e / k and its index is the latent.
+struct Selection {
+  const void* values = nullptr;
+  const int64_t* indices = nullptr;
+  int64_t rows = 0, k = 0, n = 0, total = 0;
+  int dtype = 1;
+  bool flat = false;
+};
+
+// out[key] = bias + sum over the entries of `key` of coef * src[other]:
+// by_row: key = row, src has a row per latent; otherwise key = latent.
+struct SegArgs {
+  Selection sel;
+  bool by_row = true;
+  const void* coef = nullptr;       // values, or the gradient of the values
+  const void* gate = nullptr;       // entries whose gate value is not > 0 count as 0 (null: none)
+  const void* src = nullptr;
+  int64_t lds = 0;
+  int64_t d = 0;
+  const void* bias = nullptr;       // [d], by_row only
+  void* out = nullptr;
+  int64_t ldo = 0;
+  void* coef_sum = nullptr;         // optional: sum of coef per key
+};
+
+size_t seg_workspace(const Selection& sel, int64_t d, bool by_row);
+hipError_t launch_seg(const SegArgs& a, void* ws, hipStream_t s);
+
+// dv[e] = <g[row_e], w[latent_e]> (0 for padded entries)
+struct DotArgs {
+  Selection sel;
+  const void* g = nullptr;
+  int64_t ldg = 0;
+  const void* w = nullptr;
+  int64_t ldw = 0;
+  int64_t d = 0;
+  void* dv = nullptr;
+};
+hipError_t launch_dots(const DotArgs& a, hipStream_t s);
+
+// Global 2-norm of many tensors, and their scaling.
+struct NormArgs {
+  void* const* ptrs = nullptr;
+  const int64_t* counts = nullptr;
+  const int32_t* dtypes = nullptr;
+  int64_t tensors = 0;
+  bool scale = false;
+  float max_norm = 0.f, eps = 0.f;
+  float* norm = nullptr;
+  int cus = 256;
+};
+size_t norm_workspace(int64_t tensors, const int64_t* counts);
+hipError_t launch_norm(const NormArgs& a, void* ws, hipStream_t s);
+
+int device_cus_now();
+
+__host__ __device__ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+}  // namespace tk

@@ -1,0 +1,454 @@
+// C ABI of the operators around the selection: argument checks, workspace
+// carving, launches.  Nothing is enqueued before every check has passed.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+#include <utility>
+#include <vector>
+
+#include "../../include/topk.h"
+#include "topk_launch.hpp"
+#include "topk_ops.hpp"
+
+namespace {
+
+constexpr int64_t SIZE_MAX31 = (int64_t(1) << 31) - 1;
+
+bool bad_size(int64_t v) { return v < 0 || v > SIZE_MAX31; }
+
+int64_t elem(int dtype) { return dtype == TOPK_BF16 ? 2 : 4; }
+
+// A [rows, cols] matrix: its row stride fits, and its address unless it is empty.
+bool bad_matrix(const void* p, int64_t ld, int64_t rows, int64_t cols, int dtype) {
+  if (bad_size(ld) || (rows > 1 && ld < cols)) return true;
+  if (reinterpret_cast<uintptr_t>(p) % (uintptr_t)elem(dtype)) return true;
+  return !p && rows > 0 && cols > 0;
+}
+
+int check_ws(const void* ws, size_t have, size_t need) {
+  if (need == 0) return TOPK_OK;
+  if (!ws || reinterpret_cast<uintptr_t>(ws) % 256) return TOPK_EINVAL;
+  return have < need ? TOPK_EWORKSPACE : TOPK_OK;
+}
+
+int status(hipError_t e) { return e == hipSuccess ? TOPK_OK : TOPK_EHIP; }
+
+bool bad_dtype(int dtype) { return dtype != TOPK_F32 && dtype != TOPK_BF16; }
+
+// ---------------------------------------------------------------- linear
+int linear_gemm(const topk_linear_args* a, tk::GemmArgs* g) {
+  if (!a) return TOPK_EINVAL;
+  if (bad_dtype(a->dtype)) return TOPK_EDTYPE;
+  if (a->act < TOPK_ACT_NONE || a->act > TOPK_ACT_SILU) return TOPK_EINVAL;
+  if (bad_size(a->m) || bad_size(a->n) || bad_size(a->k)) return TOPK_EINVAL;
+  const int64_t m = a->m, n = a->n, k = a->k;
+  if (a->x_trans ? bad_matrix(a->x, a->ldx, k, m, a->dtype) : bad_matrix(a->x, a->ldx, m, k, a->dtype))
+    return TOPK_EINVAL;
+  if (a->w_trans ? bad_matrix(a->w, a->ldw, k, n, a->dtype) : bad_matrix(a->w, a->ldw, n, k, a->dtype))
+    return TOPK_EINVAL;
+  if (bad_matrix(a->y, a->ldy, m, n, a->dtype)) return TOPK_EINVAL;
+  if (a->bias && bad_matrix(a->bias, n, 1, n, a->dtype)) return TOPK_EINVAL;
+  if (a->residual && bad_matrix(a->residual, a->ldr, m, n, a->dtype)) return TOPK_EINVAL;
+  if (a->pre && bad_matrix(a->pre, a->ldp, m, n, a->dtype)) return TOPK_EINVAL;
+  g->a = tk::Operand{a->x, a->ldx, a->x_trans != 0};
+  g->b = tk::Operand{a->w, a->ldw, a->w_trans != 0};
+  g->m = m;
+  g->n = n;
+  g->k = k;
+  g->dtype = a->dtype;
+  g->act = a->act;
+  g->bias = a->bias;
+  g->residual = a->residual;
+  g->ldr = a->ldr;
+  g->c = a->y;
+  g->ldc = a->ldy;
+  g->pre = a->pre;
+  g->ldp = a->ldp;
+  g->cus = tk::device_cus_now();
+  return TOPK_OK;
+}
+
+// The three steps of a dense backward, and where each finds its scratch: dz
+// first, then a region that the steps, which run one after another, share.
+struct LinearGrad {
+  tk::SlopeArgs slope;
+  tk::GemmArgs dx, dw;
+  bool want_slope = false, want_dx = false, want_dw = false, own_dz = false;
+  size_t dz_bytes = 0, step_bytes = 0;
+};
+
+int linear_grad_plan(const topk_linear_grad_args* a, LinearGrad* p, char* ws) {
+  if (!a) return TOPK_EINVAL;
+  if (bad_dtype(a->dtype)) return TOPK_EDTYPE;
+  if (a->act < TOPK_ACT_NONE || a->act > TOPK_ACT_SILU) return TOPK_EINVAL;
+  if (bad_size(a->m) || bad_size(a->n) || bad_size(a->k)) return TOPK_EINVAL;
+  const int64_t m = a->m, n = a->n, k = a->k;
+  const int dt = a->dtype;
+  if (!a->dx && !a->dw && !a->db) return TOPK_EINVAL;
+  if (bad_matrix(a->dy, a->ldd, m, n, dt)) return TOPK_EINVAL;
+  if (a->act != TOPK_ACT_NONE && bad_matrix(a->pre, a->ldp, m, n, dt)) return TOPK_EINVAL;
+  if (a->dw && (a->x_trans ? bad_matrix(a->x, a->ldx, k, m, dt) : bad_matrix(a->x, a->ldx, m, k, dt)))
+    return TOPK_EINVAL;
+  if (a->dx && (a->w_trans ? bad_matrix(a->w, a->ldw, k, n, dt) : bad_matrix(a->w, a->ldw, n, k, dt)))
+    return TOPK_EINVAL;
+  if (a->dx && bad_matrix(a->dx, a->lddx, m, k, dt)) return TOPK_EINVAL;
+  if (a->dw && bad_matrix(a->dw, a->lddw, n, k, dt)) return TOPK_EINVAL;
+  if (a->db && bad_matrix(a->db, n, 1, n, dt)) return TOPK_EINVAL;
+  p->want_dx = a->dx != nullptr;
+  p->want_dw = a->dw != nullptr;
+  p->own_dz = a->act != TOPK_ACT_NONE && (p->want_dx || p->want_dw);
+  p->want_slope = p->own_dz || a->db;
+  const int64_t ldz = (n + 63) & ~(int64_t)63;   // 16-byte aligned rows in either type
+  p->dz_bytes = p->own_dz ? tk::align256((size_t)m * (size_t)ldz * (size_t)elem(dt)) : 0;
+  p->slope.dy = a->dy;
+  p->slope.ldd = a->ldd;
+  p->slope.pre = a->act != TOPK_ACT_NONE ? a->pre : nullptr;
+  p->slope.ldp = a->ldp;
+  p->slope.m = m;
+  p->slope.n = n;
+  p->slope.dtype = dt;
+  p->slope.act = a->act;
+  p->slope.dz = p->own_dz ? ws : nullptr;
+  p->slope.ldz = ldz;
+  p->slope.db = a->db;
+  const void* dz = p->own_dz ? static_cast<const void*>(ws) : a->dy;
+  const int64_t ld = p->own_dz ? ldz : a->ldd;
+  const int cus = tk::device_cus_now();
+  // dx[m, k] = dz[m, n] W[n, k]: the second operand's summed axis is n
+  p->dx.a = tk::Operand{dz, ld, false};
+  p->dx.b = tk::Operand{a->w, a->ldw, a->w_trans == 0};
+  p->dx.m = m;
+  p->dx.n = k;
+  p->dx.k = n;
+  p->dx.c = a->dx;
+  p->dx.ldc = a->lddx;
+  // dw[n, k] = dz^T x: the summed axis is m
+  p->dw.a = tk::Operand{dz, ld, true};
+  p->dw.b = tk::Operand{a->x, a->ldx, a->x_trans == 0};
+  p->dw.m = n;
+  p->dw.n = k;
+  p->dw.k = m;
+  p->dw.c = a->dw;
+  p->dw.ldc = a->lddw;
+  p->dx.dtype = p->dw.dtype = dt;
+  p->dx.cus = p->dw.cus = cus;
+  if (p->want_slope) p->step_bytes = std::max(p->step_bytes, tk::slope_workspace(p->slope));
+  if (p->want_dx) p->step_bytes = std::max(p->step_bytes, tk::gemm_workspace(p->dx));
+  if (p->want_dw) p->step_bytes = std::max(p->step_bytes, tk::gemm_workspace(p->dw));
+  return TOPK_OK;
+}
+
+// ---------------------------------------------------------------- selection
+int to_selection(const topk_selection* in, bool pointers, tk::Selection* s) {
+  if (!in) return TOPK_EINVAL;
+  if (bad_dtype(in->dtype)) return TOPK_EDTYPE;
+  if (bad_size(in->rows) || bad_size(in->k) || bad_size(in->n)) return TOPK_EINVAL;
+  const int64_t total = in->flat ? in->k : in->rows * in->k;
+  if (total > SIZE_MAX31) return TOPK_EINVAL;   // entries are numbered in 32 bits
+  if (pointers && total > 0) {
+    if (!in->values || !in->indices) return TOPK_EINVAL;
+    if (reinterpret_cast<uintptr_t>(in->values) % (uintptr_t)elem(in->dtype) ||
+        reinterpret_cast<uintptr_t>(in->indices) % 8)
+      return TOPK_EINVAL;
+  }
+  s->values = in->values;
+  s->indices = in->indices;
+  s->rows = in->rows;
+  s->k = in->k;
+  s->n = in->n;
+  s->total = total;
+  s->dtype = in->dtype;
+  s->flat = in->flat != 0;
+  return TOPK_OK;
+}
+
+size_t decode_ws(const tk::Selection& s, int64_t d) {
+  tk::SlopeArgs sums;
+  sums.m = s.rows;
+  sums.n = d;
+  sums.dtype = s.dtype;
+  sums.db = &sums;   // only whether it is wanted counts here
+  return std::max({tk::seg_workspace(s, d, true), tk::seg_workspace(s, d, false),
+                   tk::slope_workspace(sums)});
+}
+
+}  // namespace
+
+namespace tk {
+
+int device_cus_now() {
+  static std::atomic<int> cached[64];
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
+  const int v = cached[dev].load(std::memory_order_relaxed);
+  if (v > 0) return v;
+  int cus = 0;
+  if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0)
+    return 256;
+  cached[dev].store(cus, std::memory_order_relaxed);
+  return cus;
+}
+
+}  // namespace tk
+
+extern "C" {
+
+static_assert(sizeof(topk_linear_args) == 128, "topk_linear_args layout is part of the ABI");
+static_assert(sizeof(topk_linear_grad_args) == 144, "topk_linear_grad_args layout is part of the ABI");
+static_assert(sizeof(topk_selection) == 48, "topk_selection layout is part of the ABI");
+
+int topk_linear_workspace_size(const topk_linear_args* args, size_t* bytes) {
+  if (!bytes) return TOPK_EINVAL;
+  tk::GemmArgs g;
+  const int rc = linear_gemm(args, &g);
+  if (rc) return rc;
+  *bytes = tk::gemm_workspace(g);
+  return TOPK_OK;
+}
+
+int topk_linear(const topk_linear_args* args, void* workspace, size_t workspace_bytes, void* stream) {
+  tk::GemmArgs g;
+  int rc = linear_gemm(args, &g);
+  if (rc) return rc;
+  rc = check_ws(workspace, workspace_bytes, tk::gemm_workspace(g));
+  if (rc) return rc;
+  return status(tk::launch_gemm(g, workspace, static_cast<hipStream_t>(stream)));
+}
+
+int topk_linear_grad_workspace_size(const topk_linear_grad_args* args, size_t* bytes) {
+  if (!bytes) return TOPK_EINVAL;
+  LinearGrad p;
+  const int rc = linear_grad_plan(args, &p, nullptr);
+  if (rc) return rc;
+  *bytes = p.dz_bytes + p.step_bytes;
+  return TOPK_OK;
+}
+
+int topk_linear_grad(const topk_linear_grad_args* args, void* workspace, size_t workspace_bytes,
+                     void* stream) {
+  LinearGrad p;
+  char* ws = static_cast<char*>(workspace);
+  int rc = linear_grad_plan(args, &p, ws);
+  if (rc) return rc;
+  rc = check_ws(workspace, workspace_bytes, p.dz_bytes + p.step_bytes);
+  if (rc) return rc;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  void* step = ws ? ws + p.dz_bytes : nullptr;
+  hipError_t e = hipSuccess;
+  if (p.want_slope) e = tk::launch_slope(p.slope, step, s);
+  if (e == hipSuccess && p.want_dx) e = tk::launch_gemm(p.dx, step, s);
+  if (e == hipSuccess && p.want_dw) e = tk::launch_gemm(p.dw, step, s);
+  return status(e);
+}
+
+int topk_decode_workspace_size(const topk_selection* sel, int64_t d, size_t* bytes) {
+  if (!bytes) return TOPK_EINVAL;
+  tk::Selection s;
+  const int rc = to_selection(sel, false, &s);
+  if (rc) return rc;
+  if (bad_size(d)) return TOPK_EINVAL;
+  *bytes = decode_ws(s, d);
+  return TOPK_OK;
+}
+
+int topk_decode(const topk_selection* sel, const void* weight, int64_t ldw, int64_t d,
+                const void* bias, void* out, int64_t ldo, void* workspace, size_t workspace_bytes,
+                void* stream) {
+  tk::SegArgs a;
+  int rc = to_selection(sel, true, &a.sel);
+  if (rc) return rc;
+  const int dt = a.sel.dtype;
+  if (bad_size(d) || bad_matrix(weight, ldw, a.sel.n, d, dt) || bad_matrix(out, ldo, a.sel.rows, d, dt))
+    return TOPK_EINVAL;
+  if (bias && bad_matrix(bias, d, 1, d, dt)) return TOPK_EINVAL;
+  rc = check_ws(workspace, workspace_bytes, tk::seg_workspace(a.sel, d, true));
+  if (rc) return rc;
+  a.coef = a.sel.values;
+  a.src = weight;
+  a.lds = ldw;
+  a.d = d;
+  a.bias = bias;
+  a.out = out;
+  a.ldo = ldo;
+  return status(tk::launch_seg(a, workspace, static_cast<hipStream_t>(stream)));
+}
+
+int topk_decode_grad(const topk_selection* sel, const void* weight, int64_t ldw, int64_t d,
+                     const void* grad, int64_t ldg, void* dvalues, void* dweight, int64_t lddw,
+                     void* dbias, void* workspace, size_t workspace_bytes, void* stream) {
+  tk::Selection s;
+  int rc = to_selection(sel, true, &s);
+  if (rc) return rc;
+  const int dt = s.dtype;
+  if (bad_size(d) || (!dvalues && !dweight && !dbias)) return TOPK_EINVAL;
+  if (bad_matrix(grad, ldg, s.rows, d, dt)) return TOPK_EINVAL;
+  if (dvalues && bad_matrix(weight, ldw, s.n, d, dt)) return TOPK_EINVAL;
+  if (dvalues && bad_matrix(dvalues, s.total, 1, s.total, dt)) return TOPK_EINVAL;
+  if (dweight && bad_matrix(dweight, lddw, s.n, d, dt)) return TOPK_EINVAL;
+  if (dbias && bad_matrix(dbias, d, 1, d, dt)) return TOPK_EINVAL;
+  tk::SlopeArgs sums;
+  sums.dy = grad;
+  sums.ldd = ldg;
+  sums.m = s.rows;
+  sums.n = d;
+  sums.dtype = dt;
+  sums.db = dbias;
+  size_t need = dweight ? tk::seg_workspace(s, d, false) : 0;
+  if (dbias) need = std::max(need, tk::slope_workspace(sums));
+  rc = check_ws(workspace, workspace_bytes, need);
+  if (rc) return rc;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  hipError_t e = hipSuccess;
+  if (dvalues) {
+    tk::DotArgs a;
+    a.sel = s;
+    a.g = grad;
+    a.ldg = ldg;
+    a.w = weight;
+    a.ldw = ldw;
+    a.d = d;
+    a.dv = dvalues;
+    e = tk::launch_dots(a, st);
+  }
+  if (e == hipSuccess && dweight) {
+    tk::SegArgs a;
+    a.sel = s;
+    a.by_row = false;
+    a.coef = s.values;
+    a.src = grad;
+    a.lds = ldg;
+    a.d = d;
+    a.out = dweight;
+    a.ldo = lddw;
+    e = tk::launch_seg(a, workspace, st);
+  }
+  if (e == hipSuccess && dbias) e = tk::launch_slope(sums, workspace, st);
+  return status(e);
+}
+
+int topk_encode_grad(const topk_selection* sel, const void* grad_values, const void* x, int64_t ldx,
+                     const void* weight, int64_t ldw, int64_t d, void* dx, int64_t lddx,
+                     void* dweight, int64_t lddw, void* dbias, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+  tk::Selection s;
+  int rc = to_selection(sel, true, &s);
+  if (rc) return rc;
+  const int dt = s.dtype;
+  if (bad_size(d) || (!dx && !dweight && !dbias)) return TOPK_EINVAL;
+  if (bad_matrix(grad_values, s.total, 1, s.total, dt)) return TOPK_EINVAL;
+  if (dx && (bad_matrix(weight, ldw, s.n, d, dt) || bad_matrix(dx, lddx, s.rows, d, dt))) return TOPK_EINVAL;
+  if (dweight && (bad_matrix(x, ldx, s.rows, d, dt) || bad_matrix(dweight, lddw, s.n, d, dt)))
+    return TOPK_EINVAL;
+  if (dbias && bad_matrix(dbias, s.n, 1, s.n, dt)) return TOPK_EINVAL;
+  size_t need = dx ? tk::seg_workspace(s, d, true) : 0;
+  if (dweight || dbias) need = std::max(need, tk::seg_workspace(s, d, false));
+  rc = check_ws(workspace, workspace_bytes, need);
+  if (rc) return rc;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  tk::SegArgs a;
+  a.sel = s;
+  a.coef = grad_values;
+  a.gate = s.values;
+  hipError_t e = hipSuccess;
+  if (dx) {
+    a.by_row = true;
+    a.src = weight;
+    a.lds = ldw;
+    a.d = d;
+    a.out = dx;
+    a.ldo = lddx;
+    e = tk::launch_seg(a, workspace, st);
+  }
+  if (e == hipSuccess && (dweight || dbias)) {
+    a.by_row = false;
+    a.src = x;
+    a.lds = ldx;
+    a.d = dweight ? d : 0;
+    a.out = dweight;
+    a.ldo = lddw;
+    a.coef_sum = dbias;
+    e = tk::launch_seg(a, workspace, st);
+  }
+  return status(e);
+}
+
+int topk_grad_norm_workspace_size(int64_t tensors, const int64_t* counts, size_t* bytes) {
+  if (!bytes || bad_size(tensors) || (tensors && !counts)) return TOPK_EINVAL;
+  for (int64_t i = 0; i < tensors; ++i)
+    if (counts[i] < 0 || counts[i] > (int64_t(1) << 40)) return TOPK_EINVAL;
+  *bytes = tk::norm_workspace(tensors, counts);
+  return TOPK_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+int norm_call(tk::NormArgs& a, void* workspace, size_t workspace_bytes, void* stream) {
+  size_t need = 0;
+  int rc = topk_grad_norm_workspace_size(a.tensors, a.counts, &need);
+  if (rc) return rc;
+  if (!a.norm || reinterpret_cast<uintptr_t>(a.norm) % 4 || (a.tensors && (!a.ptrs || !a.dtypes)))
+    return TOPK_EINVAL;
+  for (int64_t i = 0; i < a.tensors; ++i) {
+    if (bad_dtype(a.dtypes[i])) return TOPK_EDTYPE;
+    if (reinterpret_cast<uintptr_t>(a.ptrs[i]) % (uintptr_t)elem(a.dtypes[i])) return TOPK_EINVAL;
+    if (a.counts[i] && !a.ptrs[i]) return TOPK_EINVAL;
+  }
+  rc = check_ws(workspace, workspace_bytes, need);
+  if (rc) return rc;
+  if (a.scale) {   // a tensor listed twice, or two views that share elements, would be scaled twice
+    try {
+      std::vector<std::pair<uintptr_t, uintptr_t>> span;
+      span.reserve((size_t)a.tensors);
+      for (int64_t i = 0; i < a.tensors; ++i) {
+        const uintptr_t p = reinterpret_cast<uintptr_t>(a.ptrs[i]);
+        if (a.counts[i]) span.emplace_back(p, p + (uintptr_t)(a.counts[i] * elem(a.dtypes[i])));
+      }
+      std::sort(span.begin(), span.end());
+      for (size_t i = 1; i < span.size(); ++i)
+        if (span[i].first < span[i - 1].second) return TOPK_EINVAL;
+    } catch (...) {
+      return TOPK_EINVAL;
+    }
+  }
+  a.cus = tk::device_cus_now();
+  return status(tk::launch_norm(a, workspace, static_cast<hipStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+int topk_grad_norm(const void* const* ptrs, const int64_t* counts, const int32_t* dtypes,
+                   int64_t tensors, float* norm, void* workspace, size_t workspace_bytes,
+                   void* stream) {
+  tk::NormArgs a;
+  a.ptrs = const_cast<void* const*>(ptrs);   // only read: nothing is scaled
+  a.counts = counts;
+  a.dtypes = dtypes;
+  a.tensors = tensors;
+  a.norm = norm;
+  return norm_call(a, workspace, workspace_bytes, stream);
+}
+
+int topk_clip_grad_norm(void* const* ptrs, const int64_t* counts, const int32_t* dtypes,
+                        int64_t tensors, float max_norm, float eps, float* norm, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  if (!(max_norm >= 0.f) || !(eps >= 0.f)) return TOPK_EINVAL;
+  tk::NormArgs a;
+  a.ptrs = ptrs;
+  a.counts = counts;
+  a.dtypes = dtypes;
+  a.tensors = tensors;
+  a.scale = true;
+  a.max_norm = max_norm;
+  a.eps = eps;
+  a.norm = norm;
+  return norm_call(a, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"
