@@ -3,6 +3,8 @@
 //
 //   y = act(x W^T + b) + residual
 //   dz = dy * act'(z);  dx = dz W;  dW = dz^T x;  db = column sums of dz
+#include <algorithm>
+
 #include "topk_ops_device.hpp"
 
 namespace tk {
@@ -16,79 +18,480 @@ struct Epi {
   void* c;
   void* pre;
   int64_t ldr, ldc, ldp;
+  uint32_t m, n;
+  int act;
+  int vec;       // rows of c, pre and residual are 16-byte aligned, bias too
 };
 
-// ---------------------------------------------------------------- product
-// 64 x 64 outputs per workgroup of 256 threads, 4 x 4 per thread, the summed
-// axis in steps of 16 through LDS.
-template <class T, int ACT>
-__global__ __launch_bounds__(256) void k_gemm_simple(const T* __restrict__ a, const T* __restrict__ b,
-                                                     uint32_t m, uint32_t n, uint32_t k,
-                                                     int64_t a_row, int64_t a_red, int64_t b_row,
-                                                     int64_t b_red, Epi e) {
-  __shared__ float sa[16][65], sb[16][65];
-  const uint32_t m0 = blockIdx.y * 64, n0 = blockIdx.x * 64;
-  const uint32_t tr = threadIdx.x / 16, tc = threadIdx.x % 16;
-  float acc[4][4] = {};
-  for (uint32_t k0 = 0; k0 < k; k0 += 16) {
-    for (uint32_t i = threadIdx.x; i < 1024; i += 256) {
-      const uint32_t r = i / 16, c = i % 16;
-      sa[c][r] = (m0 + r < m && k0 + c < k) ? to_f32(a[(m0 + r) * a_row + (k0 + c) * a_red]) : 0.f;
-      sb[c][r] = (n0 + r < n && k0 + c < k) ? to_f32(b[(n0 + r) * b_row + (k0 + c) * b_red]) : 0.f;
-    }
-    __syncthreads();
+// The activation of V values; the switch is the same for every lane.
+template <int V>
+__device__ __forceinline__ void act_any(float* v, int act) {
+  if (act == ACT_RELU) {
 #pragma unroll
-    for (uint32_t c = 0; c < 16; ++c) {
-      float x[4], y[4];
+    for (int i = 0; i < V; ++i) v[i] = act_of<ACT_RELU>(v[i]);
+  } else if (act == ACT_GELU) {
 #pragma unroll
-      for (uint32_t i = 0; i < 4; ++i) {
-        x[i] = sa[c][tr * 4 + i];
-        y[i] = sb[c][tc + i * 16];
-      }
+    for (int i = 0; i < V; ++i) v[i] = act_of<ACT_GELU>(v[i]);
+  } else if (act == ACT_SILU) {
 #pragma unroll
-      for (uint32_t i = 0; i < 4; ++i)
-#pragma unroll
-        for (uint32_t j = 0; j < 4; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
-    }
-    __syncthreads();
-  }
-#pragma unroll
-  for (uint32_t i = 0; i < 4; ++i) {
-    const uint32_t r = m0 + tr * 4 + i;
-    if (r >= m) continue;
-#pragma unroll
-    for (uint32_t j = 0; j < 4; ++j) {
-      const uint32_t c = n0 + tc + j * 16;
-      if (c >= n) continue;
-      float z = acc[i][j];
-      if (e.bias) z += to_f32(static_cast<const T*>(e.bias)[c]);
-      if (e.pre) static_cast<T*>(e.pre)[r * e.ldp + c] = from_f32<T>(z);
-      float y = act_of<ACT>(z);
-      if (e.residual) y += to_f32(static_cast<const T*>(e.residual)[r * e.ldr + c]);
-      static_cast<T*>(e.c)[r * e.ldc + c] = from_f32<T>(y);
-    }
+    for (int i = 0; i < V; ++i) v[i] = act_of<ACT_SILU>(v[i]);
   }
 }
 
-template <class T, int ACT>
-hipError_t run_simple(const GemmArgs& g, hipStream_t s) {
-  const Epi e{g.bias, g.residual, g.c, g.pre, g.ldr, g.ldc, g.ldp};
-  const dim3 grid((uint32_t)ceil_div(g.n, 64), (uint32_t)ceil_div(g.m, 64));
-  hipLaunchKernelGGL((k_gemm_simple<T, ACT>), grid, dim3(256), 0, s, static_cast<const T*>(g.a.p),
-                     static_cast<const T*>(g.b.p), (uint32_t)g.m, (uint32_t)g.n, (uint32_t)g.k,
-                     g.a.trans ? 1 : g.a.ld, g.a.trans ? g.a.ld : 1, g.b.trans ? 1 : g.b.ld,
-                     g.b.trans ? g.b.ld : 1, e);
-  return hipGetLastError();
+// V sums of row r from column c on, in order: bias, pre-activation,
+// activation, residual, one rounding, one store.  V is the 16-byte width
+// (aligned rows) or 1.
+template <class T, int V>
+__device__ __forceinline__ void finish(float* v, uint32_t r, uint32_t c, const Epi& e) {
+  if (e.bias) {
+    float b[V];
+    load_vec<T, V>(static_cast<const T*>(e.bias) + c, b);
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] += b[i];
+  }
+  if (e.pre) store_vec<T, V>(static_cast<T*>(e.pre) + (int64_t)r * e.ldp + c, v);
+  act_any<V>(v, e.act);
+  if (e.residual) {
+    float q[V];
+    load_vec<T, V>(static_cast<const T*>(e.residual) + (int64_t)r * e.ldr + c, q);
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] += q[i];
+  }
+  store_vec<T, V>(static_cast<T*>(e.c) + (int64_t)r * e.ldc + c, v);
+}
+
+// ---------------------------------------------------------------- product
+// Tiles of 128 bytes along the summed axis (64 bf16 or 32 f32) go from memory
+// straight to LDS (buffer loads with an LDS destination, 16 bytes a lane), two
+// stages deep; reads beyond a tensor's end return 0 there.  A wave's matrix
+// instructions take 16-byte fragments: 8 bf16 of one row (16x16x32), or 4 f32
+// used by four 16x16x4 instructions in turn; the summed axis is permuted the
+// same way in both operands.
+//
+// LDS layouts.  An operand whose summed axis is contiguous is kept as rows of
+// 128 bytes, the 16-byte chunk c of row r at place c ^ (r & 7), so that the
+// eight rows read in one clock use all banks once.  An operand stored the
+// other way round ("trans") is kept as it lies in memory, one line per summed
+// index; bf16 fragments are then read with the transposing LDS read, f32 ones
+// element by element, and the 16-row units of a line are rotated by the
+// summed index so that the lines read together lie in different banks.
+//
+// W's rows are the first operand of the matrix instruction and x's the second,
+// so a lane ends with four neighbouring columns of one output row.
+typedef __attribute__((address_space(3))) char lds_char;
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+struct KOperand {
+  const void* p;
+  int64_t ld;        // elements
+  uint32_t rows;     // valid rows
+  uint32_t red;      // valid extent of the summed axis
+};
+
+struct KGemm {
+  KOperand a, b;     // x and W
+  Epi e;
+  float* part;       // split sums: [split][m][ldpart]; null: the epilogue runs here
+  uint32_t ldpart;
+  uint32_t tiles_m, tiles_n, split, steps;   // steps: tiles of the summed axis per split
+  uint32_t all_steps;
+};
+
+template <class T> struct Elem;
+template <> struct Elem<bf16_t> { static constexpr int ES = 2, BK = 64, UNIT = 32; };
+template <> struct Elem<float> { static constexpr int ES = 4, BK = 32, UNIT = 64; };
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* p, int64_t bytes) {
+  const int n = bytes > 0x7FFFFFFF ? 0x7FFFFFFF : (bytes < 0 ? 0 : (int)bytes);
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, n, 0x00020000);
+}
+
+// Loads one operand's tile of R rows: R / 8 instructions of 1 KB, shared by W waves.
+template <class T, int R, bool TR, int W>
+struct Loader {
+  static constexpr int N = R / 8 / W;
+  uint32_t off[N];
+  uint32_t chunk;    // the lane's place on the summed axis within a step (not TR)
+  const char* base;
+  int64_t bytes;     // from base to the end of the valid data
+  int64_t step;      // bytes from one step to the next
+  uint32_t red;
+
+  __device__ void init(const KOperand& o, uint32_t r0, uint32_t wave, uint32_t lane) {
+    constexpr int ES = Elem<T>::ES;
+    const uint32_t rows = o.rows - r0 < R ? o.rows - r0 : R;
+    red = o.red;
+    if constexpr (!TR) {
+      base = static_cast<const char*>(o.p) + (int64_t)r0 * o.ld * ES;
+      bytes = ((int64_t)(rows - 1) * o.ld + o.red) * ES;
+      step = 128;
+      const uint32_t c = (lane % 8) ^ (lane / 8);
+      chunk = c * (16 / ES);
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const uint32_t row = (wave * N + j) * 8 + lane / 8;
+        off[j] = row * (uint32_t)o.ld * ES + c * 16;
+      }
+    } else {
+      constexpr uint32_t RB = R * ES, US = Elem<T>::UNIT;
+      base = static_cast<const char*>(o.p) + (int64_t)r0 * ES;
+      // rounded up to whole words: a range check that ends inside a word would drop its first half
+      bytes = ((((int64_t)o.red - 1) * o.ld + rows) * ES + 3) & ~(int64_t)3;
+      step = (int64_t)Elem<T>::BK * o.ld * ES;
+      chunk = 0;
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const uint32_t at = (wave * N + j) * 1024 + lane * 16;
+        const uint32_t k = at / RB, in = at % RB;
+        const uint32_t turn = ES == 2 ? (k & 3) : ((k >> 2) & 3);
+        off[j] = k * (uint32_t)o.ld * ES + (((in / US) ^ turn) * US) + in % US;
+      }
+    }
+  }
+
+  __device__ void issue(lds_char* dst, uint32_t kt, uint32_t wave) {
+    const int64_t at = (int64_t)kt * step;
+    const __amdgpu_buffer_rsrc_t r = rsrc_of(base + at, bytes - at);
+    bool in = true;
+    if constexpr (!TR) in = kt * Elem<T>::BK + chunk < red;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          r, reinterpret_cast<__attribute__((address_space(3))) void*>(dst + (wave * N + j) * 1024), 16,
+          in ? off[j] : 0x7FFFFFF0u, 0, 0, 0);
+  }
+};
+
+// Waits for this wave's loads to LDS: a barrier alone does not, and the
+// other waves read what they bring.
+__device__ __forceinline__ void wait_loads() {
+  __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
+}
+
+// The 16-byte fragments of 16 rows, sub-step s of a tile.
+template <class T, int R, bool TR>
+__device__ __forceinline__ u32x4 fragment(lds_char* t, uint32_t f, uint32_t s, uint32_t lane) {
+  const uint32_t i = lane % 16, g = lane / 16;
+  if constexpr (!TR) {
+    const uint32_t at = (f * 16 + i) * 128 + (((s * 4 + g) ^ (i & 7)) * 16);
+    return *reinterpret_cast<__attribute__((address_space(3))) u32x4*>(t + at);
+  } else if constexpr (Elem<T>::ES == 2) {
+    constexpr uint32_t RB = R * 2;
+    const uint32_t k = s * 32 + g * 8 + i / 4;
+    lds_char* at = t + k * RB + ((f ^ (i / 4)) * 32) + (i % 4) * 8;
+    union {
+      s16x4 h[2];
+      u32x4 v;
+    } q;
+    q.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        reinterpret_cast<__attribute__((address_space(3))) s16x4*>(at));
+    q.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        reinterpret_cast<__attribute__((address_space(3))) s16x4*>(at + 4 * RB));
+    return q.v;
+  } else {
+    constexpr uint32_t RB = R * 4;
+    const uint32_t k = s * 16 + g * 4;
+    lds_char* at = t + k * RB + ((f ^ g) * 64) + i * 4;
+    u32x4 v;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      v[j] = *reinterpret_cast<__attribute__((address_space(3))) uint32_t*>(at + j * RB);
+    return v;
+  }
 }
 
 template <class T>
-hipError_t run_act(const GemmArgs& g, hipStream_t s) {
-  switch (g.act) {
-    case ACT_RELU: return run_simple<T, ACT_RELU>(g, s);
-    case ACT_GELU: return run_simple<T, ACT_GELU>(g, s);
-    case ACT_SILU: return run_simple<T, ACT_SILU>(g, s);
-    default: return run_simple<T, ACT_NONE>(g, s);
+__device__ __forceinline__ f32x4 mma(u32x4 w, u32x4 x, f32x4 acc) {
+  if constexpr (Elem<T>::ES == 2) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w),
+                                                   __builtin_bit_cast(bf16x8, x), acc, 0, 0, 0);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(w[j]), __uint_as_float(x[j]), acc, 0, 0, 0);
+    return acc;
   }
+}
+
+// Tile of a workgroup.  Consecutive workgroups go to the eight dies in turn,
+// so each die gets a contiguous range of tiles, and walks it in bands of 16
+// row tiles: W's tile and the band's rows of x then stay in the die's L2.
+__device__ __forceinline__ void tile_of(uint32_t id, uint32_t total, uint32_t tm, uint32_t tn,
+                                        uint32_t* im, uint32_t* in) {
+  const uint32_t q = total / 8, r = total % 8, x = id % 8;
+  id = x * q + (x < r ? x : r) + id / 8;
+  constexpr uint32_t BAND = 16;
+  const uint32_t band = id / (BAND * tn);
+  const uint32_t rows = tm - band * BAND < BAND ? tm - band * BAND : BAND;
+  const uint32_t at = id - band * BAND * tn;
+  *im = band * BAND + at % rows;
+  *in = at / rows;
+}
+
+template <class T, int R, bool TA, bool TB>
+__global__ __launch_bounds__(256, 2) void k_gemm(KGemm p) {
+#ifdef __HIP_DEVICE_COMPILE__   // buffer resources exist in the device pass only
+  constexpr int F = R / 32;                 // fragments per wave in each direction
+  constexpr int STAGE = 2 * R * 128;        // bytes: both operands
+  __shared__ __align__(1024) char smem[2 * STAGE];
+  lds_char* lds = (lds_char*)smem;
+  const uint32_t lane = threadIdx.x % 64;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const uint32_t tiles = p.tiles_m * p.tiles_n;
+  const uint32_t sp = blockIdx.x / tiles;
+  uint32_t im, in;
+  tile_of(blockIdx.x - sp * tiles, tiles, p.tiles_m, p.tiles_n, &im, &in);
+  const uint32_t m0 = im * R, n0 = in * R;
+  const uint32_t k0 = sp * p.steps;
+  const uint32_t k1 = k0 + p.steps < p.all_steps ? k0 + p.steps : p.all_steps;
+  Loader<T, R, TA, 4> la;
+  Loader<T, R, TB, 4> lb;
+  la.init(p.a, m0, wave, lane);
+  lb.init(p.b, n0, wave, lane);
+  const uint32_t wm = (wave / 2) * F, wn = (wave % 2) * F;   // the wave's first fragments
+  f32x4 acc[F][F];
+#pragma unroll
+  for (int i = 0; i < F; ++i)
+#pragma unroll
+    for (int j = 0; j < F; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (k0 < k1) {
+    la.issue(lds, k0, wave);
+    lb.issue(lds + R * 128, k0, wave);
+  }
+  for (uint32_t kt = k0; kt < k1; ++kt) {
+    wait_loads();
+    __syncthreads();   // this step's tiles have arrived; the other stage is free
+    lds_char* ta = lds + ((kt - k0) & 1) * STAGE;
+    lds_char* tb = ta + R * 128;
+    u32x4 fa[2][F], fb[2][F];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int i = 0; i < F; ++i) {
+        fa[s][i] = fragment<T, R, TA>(ta, wm + i, s, lane);
+        fb[s][i] = fragment<T, R, TB>(tb, wn + i, s, lane);
+      }
+    if (kt + 1 < k1) {
+      lds_char* next = lds + ((kt + 1 - k0) & 1) * STAGE;
+      la.issue(next, kt + 1, wave);
+      lb.issue(next + R * 128, kt + 1, wave);
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int i = 0; i < F; ++i)
+#pragma unroll
+        for (int j = 0; j < F; ++j) acc[i][j] = mma<T>(fb[s][i], fa[s][j], acc[i][j]);
+  }
+  __syncthreads();
+  // 32 output rows at a time through a part of LDS that is the wave's own:
+  // in as four columns a lane, out as 16-byte pieces of rows.
+  constexpr uint32_t C = R / 2, LD = C + 4;
+  constexpr int V = Vec<T>::N;
+  constexpr uint32_t LANES = C / V, ROWS = 64 / LANES;
+  float* mine = reinterpret_cast<float*>(smem) + wave * 32 * LD;
+#pragma unroll
+  for (int j = 0; j < F; j += 2) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < F; ++i)
+        *reinterpret_cast<f32x4*>(mine + (h * 16 + lane % 16) * LD + i * 16 + (lane / 16) * 4) = acc[i][j + h];
+#pragma unroll 1
+    for (uint32_t q = 0; q < 32; q += ROWS) {
+      const uint32_t rr = q + lane / LANES, cc = (lane % LANES) * V;
+      const uint32_t r = m0 + (wm + j) * 16 + rr, c = n0 + wn * 16 + cc;
+      if (r >= p.e.m || c >= p.e.n) continue;
+      const float* src = mine + rr * LD + cc;
+      if (p.part || (p.e.vec && c + V <= p.e.n)) {
+        float v[V];
+#pragma unroll
+        for (int i = 0; i < V; i += 4) Vec<float>::load(src + i, v + i);
+        if (p.part) {
+          float* o = p.part + ((size_t)sp * p.e.m + r) * p.ldpart + c;
+#pragma unroll
+          for (int i = 0; i < V; i += 4)
+            if (c + i < p.ldpart) Vec<float>::store(o + i, v + i);
+        } else {
+          finish<T, V>(v, r, c, p.e);
+        }
+      } else {
+#pragma unroll 1
+        for (uint32_t i = 0; i < V && c + i < p.e.n; ++i) {
+          float z = src[i];
+          finish<T, 1>(&z, r, c + i, p.e);
+        }
+      }
+    }
+  }
+#endif
+}
+
+// Adds the partial sums of a split product in order, then the epilogue.
+template <class T>
+__global__ __launch_bounds__(256) void k_split_join(const float* __restrict__ part, uint32_t split,
+                                                    uint32_t ldpart, Epi e) {
+  constexpr int V = Vec<T>::N;
+  const uint32_t per_row = (e.n + V - 1) / V;
+  const uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= (uint64_t)per_row * e.m) return;
+  const uint32_t r = (uint32_t)(i / per_row), c = (uint32_t)(i % per_row) * V;
+  float v[V] = {};
+  for (uint32_t s = 0; s < split; ++s) {
+    const float* q = part + ((size_t)s * e.m + r) * ldpart + c;
+#pragma unroll
+    for (int j = 0; j < V; j += 4) {
+      if (c + j >= ldpart) break;
+      const f32x4 t = *reinterpret_cast<const f32x4*>(q + j);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v[j + u] += t[u];
+    }
+  }
+  if (e.vec && c + V <= e.n) {
+    finish<T, V>(v, r, c, e);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (c + j < e.n) finish<T, 1>(v + j, r, c + j, e);
+  }
+}
+
+// Copies lines of `red` elements to lines of `ldo`, zeros behind their end.
+template <class T>
+__global__ __launch_bounds__(256) void k_pack(const T* __restrict__ src, int64_t ld, uint32_t lines,
+                                              uint32_t red, T* __restrict__ dst, uint32_t ldo) {
+  constexpr int V = Vec<T>::N;
+  const uint32_t per = ldo / V;
+  const uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= (uint64_t)per * lines) return;
+  const uint32_t r = (uint32_t)(i / per), c = (uint32_t)(i % per) * V;
+  T v[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    v[j] = T{};
+    if (c + j < red) v[j] = src[(int64_t)r * ld + c + j];
+  }
+  *reinterpret_cast<u32x4*>(dst + (uint64_t)r * ldo + c) = *reinterpret_cast<const u32x4*>(v);
+}
+
+// How a product runs.
+struct Plan2 {
+  uint32_t tile = 128;
+  uint32_t tiles_m = 0, tiles_n = 0, split = 1, steps = 0, all_steps = 0;
+  bool pack_a = false, pack_b = false;
+  uint32_t lda = 0, ldb = 0;         // packed strides
+  uint32_t ldpart = 0;
+  size_t off_b = 0, off_part = 0, total = 0;
+};
+
+// Direct loads need 16-byte aligned lines, lines whose summed extent fills
+// 16-byte chunks (rows beyond it would be summed otherwise), and offsets
+// within a tile below 2^31.
+bool needs_pack(const Operand& o, int64_t rows, int64_t red, int64_t es) {
+  if (!rows || !red) return false;
+  const int64_t line = o.trans ? rows : red, lines = o.trans ? red : rows;
+  const int64_t ld = lines > 1 ? o.ld : line;
+  return reinterpret_cast<uintptr_t>(o.p) % 16 || (lines > 1 && (ld * es) % 16) ||
+         (!o.trans && (red * es) % 16) || ld * es * 128 >= (int64_t(1) << 31);
+}
+
+Plan2 plan_gemm(const GemmArgs& g) {
+  Plan2 p;
+  const int64_t es = g.dtype == DT_BF16 ? 2 : 4, v = 16 / es, bk = 128 / es;
+  p.pack_a = needs_pack(g.a, g.m, g.k, es);
+  p.pack_b = needs_pack(g.b, g.n, g.k, es);
+  auto packed = [&](const Operand& o, int64_t rows, size_t* bytes) {
+    const int64_t line = o.trans ? rows : g.k, lines = o.trans ? g.k : rows;
+    const int64_t ld = ceil_div(line, v) * v;
+    *bytes = align256((size_t)ld * (size_t)lines * (size_t)es);
+    return (uint32_t)ld;
+  };
+  size_t ba = 0, bb = 0;
+  if (p.pack_a) p.lda = packed(g.a, g.m, &ba);
+  if (p.pack_b) p.ldb = packed(g.b, g.n, &bb);
+  p.off_b = ba;
+  p.off_part = ba + bb;
+  p.total = p.off_part;
+  p.all_steps = (uint32_t)ceil_div(g.k, bk);
+  const int64_t big = ceil_div(g.m, 128) * ceil_div(g.n, 128);
+  p.tile = big >= g.cus ? 128 : 64;
+  p.tiles_m = (uint32_t)ceil_div(g.m, p.tile);
+  p.tiles_n = (uint32_t)ceil_div(g.n, p.tile);
+  const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
+  int64_t split = 1;
+  if (tiles < g.cus) split = std::min<int64_t>(g.cus * 2 / std::max<int64_t>(tiles, 1), p.all_steps / 4);
+  if (split < 1) split = 1;
+  p.steps = (uint32_t)ceil_div(std::max<int64_t>(p.all_steps, 1), split);
+  p.split = (uint32_t)ceil_div(std::max<int64_t>(p.all_steps, 1), p.steps);
+  if (p.split > 1) {
+    p.ldpart = (uint32_t)(ceil_div(g.n, 4) * 4);
+    p.total += align256((size_t)p.split * (size_t)g.m * p.ldpart * 4);
+  }
+  return p;
+}
+
+template <class T>
+hipError_t run_pack(const Operand& o, int64_t rows, int64_t red, uint32_t ldo, void* dst, hipStream_t s) {
+  const int64_t line = o.trans ? rows : red, lines = o.trans ? red : rows;
+  const int64_t n = (int64_t)(ldo / Vec<T>::N) * lines;
+  hipLaunchKernelGGL((k_pack<T>), dim3((uint32_t)ceil_div(n, 256)), dim3(256), 0, s,
+                     static_cast<const T*>(o.p), o.ld, (uint32_t)lines, (uint32_t)line, static_cast<T*>(dst), ldo);
+  return hipGetLastError();
+}
+
+template <class T, int R>
+void go(const KGemm& k, bool ta, bool tb, uint32_t grid, hipStream_t s) {
+  if (ta && tb) hipLaunchKernelGGL((k_gemm<T, R, true, true>), dim3(grid), dim3(256), 0, s, k);
+  else if (ta) hipLaunchKernelGGL((k_gemm<T, R, true, false>), dim3(grid), dim3(256), 0, s, k);
+  else if (tb) hipLaunchKernelGGL((k_gemm<T, R, false, true>), dim3(grid), dim3(256), 0, s, k);
+  else hipLaunchKernelGGL((k_gemm<T, R, false, false>), dim3(grid), dim3(256), 0, s, k);
+}
+
+bool aligned16(const void* p, int64_t ld, int64_t es) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld * es) % 16 == 0;
+}
+
+template <class T>
+hipError_t run_gemm(const GemmArgs& g, char* ws, hipStream_t s) {
+  const Plan2 p = plan_gemm(g);
+  const int64_t es = sizeof(T), v = 16 / es;
+  hipError_t e = hipSuccess;
+  if (p.pack_a) e = run_pack<T>(g.a, g.m, g.k, p.lda, ws, s);
+  if (e == hipSuccess && p.pack_b) e = run_pack<T>(g.b, g.n, g.k, p.ldb, ws + p.off_b, s);
+  if (e != hipSuccess) return e;
+  auto operand = [&](const Operand& o, int64_t rows, bool pack, uint32_t ldp, char* at) {
+    KOperand k;
+    const int64_t line = o.trans ? rows : g.k, lines = o.trans ? g.k : rows;
+    k.p = pack ? at : o.p;
+    k.ld = pack ? ldp : (lines > 1 ? o.ld : line);
+    k.rows = (uint32_t)rows;
+    // a packed line ends in zeros: it counts as whole chunks
+    k.red = (uint32_t)(pack && !o.trans ? ceil_div(g.k, v) * v : g.k);
+    return k;
+  };
+  KGemm k;
+  k.a = operand(g.a, g.m, p.pack_a, p.lda, ws);
+  k.b = operand(g.b, g.n, p.pack_b, p.ldb, ws + p.off_b);
+  k.e = Epi{g.bias, g.residual, g.c, g.pre, g.ldr, g.ldc, g.ldp, (uint32_t)g.m, (uint32_t)g.n, g.act, 0};
+  k.e.vec = aligned16(g.c, g.ldc, es) && (!g.residual || aligned16(g.residual, g.ldr, es)) &&
+            (!g.pre || aligned16(g.pre, g.ldp, es)) && aligned16(g.bias, 0, es);
+  k.part = p.split > 1 ? reinterpret_cast<float*>(ws + p.off_part) : nullptr;
+  k.ldpart = p.ldpart;
+  k.tiles_m = p.tiles_m;
+  k.tiles_n = p.tiles_n;
+  k.split = p.split;
+  k.steps = p.steps;
+  k.all_steps = p.all_steps;
+  const uint32_t grid = p.tiles_m * p.tiles_n * p.split;
+  if (p.tile == 128) go<T, 128>(k, g.a.trans, g.b.trans, grid, s);
+  else go<T, 64>(k, g.a.trans, g.b.trans, grid, s);
+  e = hipGetLastError();
+  if (e != hipSuccess || p.split == 1) return e;
+  const int64_t n = ceil_div(g.n, v) * g.m;
+  hipLaunchKernelGGL((k_split_join<T>), dim3((uint32_t)ceil_div(n, 256)), dim3(256), 0, s, k.part, p.split,
+                     p.ldpart, k.e);
+  return hipGetLastError();
 }
 
 // ---------------------------------------------------------------- slope pass
@@ -155,10 +558,6 @@ uint32_t slope_rows(int64_t m) {
   return (uint32_t)(least > SLOPE_ROWS ? least : SLOPE_ROWS);
 }
 
-bool aligned16(const void* p, int64_t ld, int64_t es) {
-  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld * es) % 16 == 0;
-}
-
 template <class T, int ACT>
 hipError_t run_slope(const SlopeArgs& a, void* ws, hipStream_t s) {
   const int64_t es = sizeof(T);
@@ -197,11 +596,14 @@ hipError_t run_slope_act(const SlopeArgs& a, void* ws, hipStream_t s) {
 
 }  // namespace
 
-size_t gemm_workspace(const GemmArgs&) { return 0; }
+size_t gemm_workspace(const GemmArgs& g) {
+  return g.m && g.n ? plan_gemm(g).total : 0;
+}
 
-hipError_t launch_gemm(const GemmArgs& g, void*, hipStream_t s) {
+hipError_t launch_gemm(const GemmArgs& g, void* ws, hipStream_t s) {
   if (g.m == 0 || g.n == 0) return hipSuccess;
-  return g.dtype == DT_BF16 ? run_act<bf16_t>(g, s) : run_act<float>(g, s);
+  return g.dtype == DT_BF16 ? run_gemm<bf16_t>(g, static_cast<char*>(ws), s)
+                            : run_gemm<float>(g, static_cast<char*>(ws), s);
 }
 
 size_t slope_workspace(const SlopeArgs& a) {
