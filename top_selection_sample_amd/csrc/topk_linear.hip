@@ -20,44 +20,60 @@ struct Epi {
   int64_t ldr, ldc, ldp;
   uint32_t m, n;
   int act;
+  int stream;    // store y past the caches
   int vec;       // rows of c, pre and residual are 16-byte aligned, bias too
 };
 
+// Outputs from 16 MB on are stored past the caches: they would push the
+// operands out (4096 x 512 x 65536 bf16 in 256-tiles: 358 us against 439;
+// x 12288: 59 us against 70).  Smaller ones stay for whoever reads them next.
+constexpr int64_t STREAM_BYTES = int64_t(16) << 20;
+
 // The activation of V values; the switch is the same for every lane.
-template <int V>
+template <class T, int V>
 __device__ __forceinline__ void act_any(float* v, int act) {
   if (act == ACT_RELU) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = act_of<ACT_RELU>(v[i]);
+    for (int i = 0; i < V; ++i) v[i] = act_of<ACT_RELU, T>(v[i]);
   } else if (act == ACT_GELU) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = act_of<ACT_GELU>(v[i]);
+    for (int i = 0; i < V; ++i) v[i] = act_of<ACT_GELU, T>(v[i]);
   } else if (act == ACT_SILU) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = act_of<ACT_SILU>(v[i]);
+    for (int i = 0; i < V; ++i) v[i] = act_of<ACT_SILU, T>(v[i]);
   }
 }
 
-// V sums of row r from column c on, in order: bias, pre-activation,
+// V sums of row r from column c on, in order: bias (given), pre-activation,
 // activation, residual, one rounding, one store.  V is the 16-byte width
 // (aligned rows) or 1.
 template <class T, int V>
-__device__ __forceinline__ void finish(float* v, uint32_t r, uint32_t c, const Epi& e) {
-  if (e.bias) {
-    float b[V];
-    load_vec<T, V>(static_cast<const T*>(e.bias) + c, b);
+__device__ __forceinline__ void finish(float* v, const float* bias, uint32_t r, uint32_t c, const Epi& e) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] += b[i];
-  }
+  for (int i = 0; i < V; ++i) v[i] += bias[i];
   if (e.pre) store_vec<T, V>(static_cast<T*>(e.pre) + (int64_t)r * e.ldp + c, v);
-  act_any<V>(v, e.act);
+  act_any<T, V>(v, e.act);
   if (e.residual) {
     float q[V];
     load_vec<T, V>(static_cast<const T*>(e.residual) + (int64_t)r * e.ldr + c, q);
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] += q[i];
   }
-  store_vec<T, V>(static_cast<T*>(e.c) + (int64_t)r * e.ldc + c, v);
+  T* y = static_cast<T*>(e.c) + (int64_t)r * e.ldc + c;
+  if (V > 1 && e.stream) {
+    stream_vec<T>(y, v);
+    asm volatile("");   // keeps the compiler from merging the two stores into a plain one
+  } else {
+    store_vec<T, V>(y, v);
+  }
+}
+
+// The bias of V columns, 0 where there is none.
+template <class T, int V>
+__device__ __forceinline__ void bias_of(float* b, uint32_t c, const Epi& e) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) b[i] = 0.f;
+  if (e.bias) load_vec<T, V>(static_cast<const T*>(e.bias) + c, b);
 }
 
 // ---------------------------------------------------------------- product
@@ -201,126 +217,151 @@ __device__ __forceinline__ u32x4 fragment(lds_char* t, uint32_t f, uint32_t s, u
   }
 }
 
-template <class T>
-__device__ __forceinline__ f32x4 mma(u32x4 w, u32x4 x, f32x4 acc) {
+// acc[i][j] += w[i] x[j].  The four f32 instructions of a fragment pair go
+// round all pairs in turn: one that waited for its own last result would
+// leave the matrix core idle.
+template <class T, int FM, int FN>
+__device__ __forceinline__ void mma_all(const u32x4* w, const u32x4* x, f32x4 (&acc)[FN][FM]) {
   if constexpr (Elem<T>::ES == 2) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w),
-                                                   __builtin_bit_cast(bf16x8, x), acc, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+      for (int j = 0; j < FM; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+            __builtin_bit_cast(bf16x8, w[i]), __builtin_bit_cast(bf16x8, x[j]), acc[i][j], 0, 0, 0);
   } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(w[j]), __uint_as_float(x[j]), acc, 0, 0, 0);
-    return acc;
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int j = 0; j < FM; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(w[i][u]), __uint_as_float(x[j][u]),
+                                                           acc[i][j], 0, 0, 0);
   }
 }
 
 // Tile of a workgroup.  Consecutive workgroups go to the eight dies in turn,
-// so each die gets a contiguous range of tiles, and walks it in bands of 16
-// row tiles: W's tile and the band's rows of x then stay in the die's L2.
+// so each die gets a contiguous range of tiles, and walks it in bands of
+// 1024 rows: W's tile and the band's rows of x then stay in the die's L2
+// (4096 x 512 x 65536 bf16 in 256-tiles: 358 us in bands of 4 tiles, 380 to
+// 451 in bands of 1, 8, 16 or 32).
 __device__ __forceinline__ void tile_of(uint32_t id, uint32_t total, uint32_t tm, uint32_t tn,
-                                        uint32_t* im, uint32_t* in) {
+                                        uint32_t* im, uint32_t* in, uint32_t band_rows) {
   const uint32_t q = total / 8, r = total % 8, x = id % 8;
   id = x * q + (x < r ? x : r) + id / 8;
-  constexpr uint32_t BAND = 16;
-  const uint32_t band = id / (BAND * tn);
-  const uint32_t rows = tm - band * BAND < BAND ? tm - band * BAND : BAND;
-  const uint32_t at = id - band * BAND * tn;
-  *im = band * BAND + at % rows;
+  const uint32_t band = id / (band_rows * tn);
+  const uint32_t rows = tm - band * band_rows < band_rows ? tm - band * band_rows : band_rows;
+  const uint32_t at = id - band * band_rows * tn;
+  *im = band * band_rows + at % rows;
   *in = at / rows;
 }
 
-template <class T, int R, bool TA, bool TB>
-__global__ __launch_bounds__(256, 2) void k_gemm(KGemm p) {
+// One step: the tiles of step kt are in `cur`; the loads of step kt + 1 go to
+// `next` while this step's fragments are read and multiplied.  The two stages
+// are separate LDS variables, so that the compiler knows that the loads in
+// flight do not write what the fragment reads read.
+template <class T, int TM, int TN, int FM, int FN, bool TA, bool TB, class LA, class LB>
+__device__ __forceinline__ void gemm_step(lds_char* cur, lds_char* next, LA& la, LB& lb, uint32_t kt,
+                                          bool more, uint32_t wave, uint32_t lane, uint32_t wm,
+                                          uint32_t wn, f32x4 (&acc)[FN][FM]) {
+  wait_loads();
+  __syncthreads();   // this step's tiles have arrived; the other stage is free
+  if (more) {
+    la.issue(next, kt + 1, wave);
+    lb.issue(next + TM * 128, kt + 1, wave);
+  }
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    u32x4 fa[FM], fb[FN];
+#pragma unroll
+    for (int i = 0; i < FN; ++i) fb[i] = fragment<T, TN, TB>(cur + TM * 128, wn + i, s, lane);
+#pragma unroll
+    for (int j = 0; j < FM; ++j) fa[j] = fragment<T, TM, TA>(cur, wm + j, s, lane);
+    mma_all<T, FM, FN>(fb, fa, acc);
+  }
+}
+
+template <class T, int TM, int TN, int NWM, int NWN, bool TA, bool TB>
+__global__ __launch_bounds__(NWM * NWN * 64, 2) void k_gemm(KGemm p) {
 #ifdef __HIP_DEVICE_COMPILE__   // buffer resources exist in the device pass only
-  constexpr int F = R / 32;                 // fragments per wave in each direction
-  constexpr int STAGE = 2 * R * 128;        // bytes: both operands
-  __shared__ __align__(1024) char smem[2 * STAGE];
-  lds_char* lds = (lds_char*)smem;
+  constexpr int W = NWM * NWN, FM = TM / 16 / NWM, FN = TN / 16 / NWN;
+  __shared__ __align__(1024) char stage0[(TM + TN) * 128];
+  __shared__ __align__(1024) char stage1[(TM + TN) * 128];
+  lds_char* s0 = (lds_char*)stage0;
+  lds_char* s1 = (lds_char*)stage1;
   const uint32_t lane = threadIdx.x % 64;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const uint32_t tiles = p.tiles_m * p.tiles_n;
   const uint32_t sp = blockIdx.x / tiles;
   uint32_t im, in;
-  tile_of(blockIdx.x - sp * tiles, tiles, p.tiles_m, p.tiles_n, &im, &in);
-  const uint32_t m0 = im * R, n0 = in * R;
+  tile_of(blockIdx.x - sp * tiles, tiles, p.tiles_m, p.tiles_n, &im, &in, 1024 / TM);
+  const uint32_t m0 = im * TM, n0 = in * TN;
   const uint32_t k0 = sp * p.steps;
   const uint32_t k1 = k0 + p.steps < p.all_steps ? k0 + p.steps : p.all_steps;
-  Loader<T, R, TA, 4> la;
-  Loader<T, R, TB, 4> lb;
+  Loader<T, TM, TA, W> la;
+  Loader<T, TN, TB, W> lb;
   la.init(p.a, m0, wave, lane);
   lb.init(p.b, n0, wave, lane);
-  const uint32_t wm = (wave / 2) * F, wn = (wave % 2) * F;   // the wave's first fragments
-  f32x4 acc[F][F];
+  const uint32_t wm = (wave / NWN) * FM, wn = (wave % NWN) * FN;   // the wave's first fragments
+  f32x4 acc[FN][FM];
 #pragma unroll
-  for (int i = 0; i < F; ++i)
+  for (int i = 0; i < FN; ++i)
 #pragma unroll
-    for (int j = 0; j < F; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < FM; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   if (k0 < k1) {
-    la.issue(lds, k0, wave);
-    lb.issue(lds + R * 128, k0, wave);
+    la.issue(s0, k0, wave);
+    lb.issue(s0 + TM * 128, k0, wave);
   }
-  for (uint32_t kt = k0; kt < k1; ++kt) {
-    wait_loads();
-    __syncthreads();   // this step's tiles have arrived; the other stage is free
-    lds_char* ta = lds + ((kt - k0) & 1) * STAGE;
-    lds_char* tb = ta + R * 128;
-    u32x4 fa[2][F], fb[2][F];
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-      for (int i = 0; i < F; ++i) {
-        fa[s][i] = fragment<T, R, TA>(ta, wm + i, s, lane);
-        fb[s][i] = fragment<T, R, TB>(tb, wn + i, s, lane);
-      }
-    if (kt + 1 < k1) {
-      lds_char* next = lds + ((kt + 1 - k0) & 1) * STAGE;
-      la.issue(next, kt + 1, wave);
-      lb.issue(next + R * 128, kt + 1, wave);
-    }
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-      for (int i = 0; i < F; ++i)
-#pragma unroll
-        for (int j = 0; j < F; ++j) acc[i][j] = mma<T>(fb[s][i], fa[s][j], acc[i][j]);
+  uint32_t kt = k0;
+  for (; kt + 1 < k1; kt += 2) {
+    gemm_step<T, TM, TN, FM, FN, TA, TB>(s0, s1, la, lb, kt, true, wave, lane, wm, wn, acc);
+    gemm_step<T, TM, TN, FM, FN, TA, TB>(s1, s0, la, lb, kt + 1, kt + 2 < k1, wave, lane, wm, wn, acc);
   }
+  if (kt < k1) gemm_step<T, TM, TN, FM, FN, TA, TB>(s0, s1, la, lb, kt, false, wave, lane, wm, wn, acc);
   __syncthreads();
-  // 32 output rows at a time through a part of LDS that is the wave's own:
-  // in as four columns a lane, out as 16-byte pieces of rows.
-  constexpr uint32_t C = R / 2, LD = C + 4;
+  // 32 output rows at a time through a part of LDS that is the wave's own: in
+  // as four columns a lane, out as 16-byte pieces of rows.  The four-column
+  // chunk u of row r lies at place u ^ (r mod chunks).  A lane keeps its
+  // columns, and so their bias, for all rows.
+  constexpr uint32_t C = TN / NWN, CH = C / 4;
   constexpr int V = Vec<T>::N;
   constexpr uint32_t LANES = C / V, ROWS = 64 / LANES;
-  float* mine = reinterpret_cast<float*>(smem) + wave * 32 * LD;
+  static_assert(W * 32 * C * 4 <= (TM + TN) * 128, "the rows fit one stage");
+  float* mine = reinterpret_cast<float*>(stage0) + wave * 32 * C;
+  const uint32_t cc = (lane % LANES) * V, c = n0 + wn * 16 + cc;
+  const bool whole = p.e.vec && c + V <= p.e.n;   // the lane's columns are one vector of every row
+  float bias[V] = {};
+  if (whole && !p.part) bias_of<T, V>(bias, c, p.e);
 #pragma unroll
-  for (int j = 0; j < F; j += 2) {
+  for (int j = 0; j < FM; j += 2) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int i = 0; i < F; ++i)
-        *reinterpret_cast<f32x4*>(mine + (h * 16 + lane % 16) * LD + i * 16 + (lane / 16) * 4) = acc[i][j + h];
+      for (int i = 0; i < FN; ++i) {
+        const uint32_t r = h * 16 + lane % 16, u = i * 4 + lane / 16;
+        *reinterpret_cast<f32x4*>(mine + r * C + (u ^ (r % CH)) * 4) = acc[i][j + h];
+      }
+    const uint32_t r0 = m0 + (wm + j) * 16;
 #pragma unroll 1
-    for (uint32_t q = 0; q < 32; q += ROWS) {
-      const uint32_t rr = q + lane / LANES, cc = (lane % LANES) * V;
-      const uint32_t r = m0 + (wm + j) * 16 + rr, c = n0 + wn * 16 + cc;
-      if (r >= p.e.m || c >= p.e.n) continue;
-      const float* src = mine + rr * LD + cc;
-      if (p.part || (p.e.vec && c + V <= p.e.n)) {
-        float v[V];
+    for (uint32_t rr = lane / LANES; rr < 32; rr += ROWS) {
+      if (r0 + rr >= p.e.m) break;
+      float v[V];
 #pragma unroll
-        for (int i = 0; i < V; i += 4) Vec<float>::load(src + i, v + i);
-        if (p.part) {
-          float* o = p.part + ((size_t)sp * p.e.m + r) * p.ldpart + c;
+      for (int i = 0; i < V; i += 4) Vec<float>::load(mine + rr * C + ((cc / 4 + i / 4) ^ (rr % CH)) * 4, v + i);
+      if (p.part) {
+        float* o = p.part + ((size_t)sp * p.e.m + r0 + rr) * p.ldpart + c;
 #pragma unroll
-          for (int i = 0; i < V; i += 4)
-            if (c + i < p.ldpart) Vec<float>::store(o + i, v + i);
-        } else {
-          finish<T, V>(v, r, c, p.e);
-        }
+        for (int i = 0; i < V; i += 4)
+          if (c + i < p.ldpart) Vec<float>::store(o + i, v + i);
+      } else if (whole) {
+        finish<T, V>(v, bias, r0 + rr, c, p.e);
       } else {
 #pragma unroll 1
         for (uint32_t i = 0; i < V && c + i < p.e.n; ++i) {
-          float z = src[i];
-          finish<T, 1>(&z, r, c + i, p.e);
+          float z = mine[rr * C + ((cc / 4 + i / 4) ^ (rr % CH)) * 4 + i % 4], b1;
+          bias_of<T, 1>(&b1, c + i, p.e);
+          finish<T, 1>(&z, &b1, r0 + rr, c + i, p.e);
         }
       }
     }
@@ -349,11 +390,17 @@ __global__ __launch_bounds__(256) void k_split_join(const float* __restrict__ pa
     }
   }
   if (e.vec && c + V <= e.n) {
-    finish<T, V>(v, r, c, e);
+    float b[V];
+    bias_of<T, V>(b, c, e);
+    finish<T, V>(v, b, r, c, e);
   } else {
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (c + j < e.n) finish<T, 1>(v + j, r, c + j, e);
+    for (int j = 0; j < V; ++j) {
+      if (c + j >= e.n) continue;
+      float b;
+      bias_of<T, 1>(&b, c + j, e);
+      finish<T, 1>(v + j, &b, r, c + j, e);
+    }
   }
 }
 
@@ -375,8 +422,81 @@ __global__ __launch_bounds__(256) void k_pack(const T* __restrict__ src, int64_t
   *reinterpret_cast<u32x4*>(dst + (uint64_t)r * ldo + c) = *reinterpret_cast<const u32x4*>(v);
 }
 
+// Few rows of x: the call is bound by reading W once.  A workgroup takes 16
+// rows of W (columns of y) and the whole summed axis; its four waves take
+// turns of 32-byte-per-row pieces of it, straight from memory into the matrix
+// instructions' operands, with all loads of a turn issued before the first is
+// used, and join their sums in LDS in wave order.  One token through 12288 x
+// 512 bf16: 12.6 MB.
+template <class T, int MF, bool WIDE>
+__device__ __forceinline__ u32x4 row_piece(const T* p, bool in, uint32_t k, uint32_t red) {
+  constexpr uint32_t V = Vec<T>::N;
+  u32x4 q = {0u, 0u, 0u, 0u};
+  if constexpr (WIDE) {
+    if (in && k < red) q = *reinterpret_cast<const u32x4*>(p + k);
+  } else {
+    T v[V];
+#pragma unroll
+    for (uint32_t i = 0; i < V; ++i) {
+      v[i] = T{};
+      if (in && k + i < red) v[i] = p[k + i];
+    }
+    q = __builtin_bit_cast(u32x4, v);
+  }
+  return q;
+}
+
+template <class T, int MF, bool WIDE>
+__global__ __launch_bounds__(256) void k_few_rows(KGemm p) {
+  constexpr uint32_t V = Vec<T>::N, PIECE = 4 * V, TURN = 4;   // summed elements per instruction, pieces per turn
+  __shared__ float join[4][MF][16][17];
+  const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  const uint32_t i = lane % 16, g = lane / 16;
+  const uint32_t n0 = blockIdx.x * 16, red = p.a.red;
+  const bool win = n0 + i < p.b.rows;
+  const T* w = static_cast<const T*>(p.b.p) + (int64_t)(win ? n0 + i : 0) * p.b.ld;
+  const T* x[MF];
+  bool xin[MF];
+#pragma unroll
+  for (int f = 0; f < MF; ++f) {
+    xin[f] = f * 16 + i < p.a.rows;
+    x[f] = static_cast<const T*>(p.a.p) + (int64_t)(xin[f] ? f * 16 + i : 0) * p.a.ld;
+  }
+  f32x4 acc[1][MF];
+#pragma unroll
+  for (int f = 0; f < MF; ++f) acc[0][f] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (uint32_t k0 = wave * TURN * PIECE; k0 < red; k0 += 4 * TURN * PIECE) {
+    u32x4 wf[TURN][1], xf[TURN][MF];
+#pragma unroll
+    for (uint32_t t = 0; t < TURN; ++t) {
+      wf[t][0] = row_piece<T, MF, WIDE>(w, win, k0 + t * PIECE + g * V, red);
+#pragma unroll
+      for (int f = 0; f < MF; ++f) xf[t][f] = row_piece<T, MF, WIDE>(x[f], xin[f], k0 + t * PIECE + g * V, red);
+    }
+#pragma unroll
+    for (uint32_t t = 0; t < TURN; ++t) mma_all<T, MF, 1>(wf[t], xf[t], acc);
+  }
+#pragma unroll
+  for (int f = 0; f < MF; ++f)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) join[wave][f][i][g * 4 + j] = acc[0][f][j];
+  __syncthreads();
+  const uint32_t c = n0 + threadIdx.x % 16;
+  if (c >= p.e.n) return;
+  float bias;
+  bias_of<T, 1>(&bias, c, p.e);
+#pragma unroll
+  for (int f = 0; f < MF; ++f) {
+    const uint32_t r = threadIdx.x / 16, at = threadIdx.x % 16;
+    if (f * 16 + r >= p.e.m) continue;
+    float z = (join[0][f][r][at] + join[1][f][r][at]) + (join[2][f][r][at] + join[3][f][r][at]);
+    finish<T, 1>(&z, &bias, f * 16 + r, c, p.e);
+  }
+}
+
 // How a product runs.
 struct Plan2 {
+  bool few = false;                  // k_few_rows
   uint32_t tile = 128;
   uint32_t tiles_m = 0, tiles_n = 0, split = 1, steps = 0, all_steps = 0;
   bool pack_a = false, pack_b = false;
@@ -396,9 +516,58 @@ bool needs_pack(const Operand& o, int64_t rows, int64_t red, int64_t es) {
          (!o.trans && (red * es) % 16) || ld * es * 128 >= (int64_t(1) << 31);
 }
 
+// Microseconds of one step of a tile on a compute unit that shares its time
+// among the tiles it holds, and with one alone; of a tile's start and end;
+// and the tiles a compute unit holds at once.  Measured: bf16 8192^3 in 64-,
+// 128- and 256-tiles 1768, 991 and 811 us, 4096 x 512 x 65536 626, 375 and
+// 358; f32 4096^3 in 64- and 128-tiles 1027 and 996 us.
+struct TileCost {
+  uint32_t tile, holds;
+  double shared, alone, ends;
+};
+constexpr TileCost COST_BF16[] = {{64, 4, 0.215, 0.7, 4}, {128, 2, 0.48, 0.8, 6}, {256, 1, 1.5, 1.5, 12}};
+constexpr TileCost COST_F32[] = {{64, 4, 0.5, 0.9, 4}, {128, 2, 1.94, 2.4, 6}};
+
+// The tile and the split of the summed axis that are estimated cheapest.
+void choose_tile(const GemmArgs& g, Plan2* p) {
+  const bool half = g.dtype == DT_BF16;
+  const int64_t steps = std::max<int64_t>(p->all_steps, 1);
+  double best = 1e300;
+  for (int i = 0; i < (half ? 3 : 2); ++i) {
+    const TileCost& t = half ? COST_BF16[i] : COST_F32[i];
+    // the 256-tile with both operands transposed does not fit the registers
+    if (t.tile == 256 && g.a.trans && g.b.trans) continue;
+    const int64_t tm = ceil_div(g.m, t.tile), tn = ceil_div(g.n, t.tile), tiles = tm * tn;
+    for (int64_t split = 1; split <= 64 && (split == 1 || (steps / split >= 2 && tiles * split <= 8 * g.cus)); ++split) {
+      const int64_t per = ceil_div(steps, split), parts = ceil_div(steps, per);
+      const int64_t most = ceil_div(tiles * parts, g.cus);   // tiles of the busiest compute unit
+      auto round = [&](int64_t together) {   // so many tiles side by side on a compute unit
+        return together ? (double)per * std::max(t.alone, (double)together * t.shared) + t.ends : 0.0;
+      };
+      double us = (double)(most / t.holds) * round(t.holds) + round(most % t.holds);
+      // joining the parts: a launch, and their way through memory
+      if (parts > 1) us += 4 + (double)g.m * (double)g.n * 8e-6 * (double)parts / 4;
+      if (us < best) {
+        best = us;
+        p->tile = t.tile;
+        p->tiles_m = (uint32_t)tm;
+        p->tiles_n = (uint32_t)tn;
+        p->steps = (uint32_t)per;
+        p->split = (uint32_t)parts;
+      }
+    }
+  }
+}
+
 Plan2 plan_gemm(const GemmArgs& g) {
   Plan2 p;
   const int64_t es = g.dtype == DT_BF16 ? 2 : 4, v = 16 / es, bk = 128 / es;
+  // At most 32 rows, both summed axes contiguous, and enough columns to spread
+  // over the card or a summed axis that four waves soon read.
+  if (g.m <= 32 && !g.a.trans && !g.b.trans && (g.n >= 2048 || g.k <= 2048)) {
+    p.few = true;
+    return p;
+  }
   p.pack_a = needs_pack(g.a, g.m, g.k, es);
   p.pack_b = needs_pack(g.b, g.n, g.k, es);
   auto packed = [&](const Operand& o, int64_t rows, size_t* bytes) {
@@ -414,16 +583,7 @@ Plan2 plan_gemm(const GemmArgs& g) {
   p.off_part = ba + bb;
   p.total = p.off_part;
   p.all_steps = (uint32_t)ceil_div(g.k, bk);
-  const int64_t big = ceil_div(g.m, 128) * ceil_div(g.n, 128);
-  p.tile = big >= g.cus ? 128 : 64;
-  p.tiles_m = (uint32_t)ceil_div(g.m, p.tile);
-  p.tiles_n = (uint32_t)ceil_div(g.n, p.tile);
-  const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
-  int64_t split = 1;
-  if (tiles < g.cus) split = std::min<int64_t>(g.cus * 2 / std::max<int64_t>(tiles, 1), p.all_steps / 4);
-  if (split < 1) split = 1;
-  p.steps = (uint32_t)ceil_div(std::max<int64_t>(p.all_steps, 1), split);
-  p.split = (uint32_t)ceil_div(std::max<int64_t>(p.all_steps, 1), p.steps);
+  choose_tile(g, &p);
   if (p.split > 1) {
     p.ldpart = (uint32_t)(ceil_div(g.n, 4) * 4);
     p.total += align256((size_t)p.split * (size_t)g.m * p.ldpart * 4);
@@ -440,12 +600,13 @@ hipError_t run_pack(const Operand& o, int64_t rows, int64_t red, uint32_t ldo, v
   return hipGetLastError();
 }
 
-template <class T, int R>
+template <class T, int R, int NWM, int NWN>
 void go(const KGemm& k, bool ta, bool tb, uint32_t grid, hipStream_t s) {
-  if (ta && tb) hipLaunchKernelGGL((k_gemm<T, R, true, true>), dim3(grid), dim3(256), 0, s, k);
-  else if (ta) hipLaunchKernelGGL((k_gemm<T, R, true, false>), dim3(grid), dim3(256), 0, s, k);
-  else if (tb) hipLaunchKernelGGL((k_gemm<T, R, false, true>), dim3(grid), dim3(256), 0, s, k);
-  else hipLaunchKernelGGL((k_gemm<T, R, false, false>), dim3(grid), dim3(256), 0, s, k);
+  const dim3 block(NWM * NWN * 64);
+  if (ta && tb) hipLaunchKernelGGL((k_gemm<T, R, R, NWM, NWN, true, true>), dim3(grid), block, 0, s, k);
+  else if (ta) hipLaunchKernelGGL((k_gemm<T, R, R, NWM, NWN, true, false>), dim3(grid), block, 0, s, k);
+  else if (tb) hipLaunchKernelGGL((k_gemm<T, R, R, NWM, NWN, false, true>), dim3(grid), block, 0, s, k);
+  else hipLaunchKernelGGL((k_gemm<T, R, R, NWM, NWN, false, false>), dim3(grid), block, 0, s, k);
 }
 
 bool aligned16(const void* p, int64_t ld, int64_t es) {
@@ -473,9 +634,21 @@ hipError_t run_gemm(const GemmArgs& g, char* ws, hipStream_t s) {
   KGemm k;
   k.a = operand(g.a, g.m, p.pack_a, p.lda, ws);
   k.b = operand(g.b, g.n, p.pack_b, p.ldb, ws + p.off_b);
-  k.e = Epi{g.bias, g.residual, g.c, g.pre, g.ldr, g.ldc, g.ldp, (uint32_t)g.m, (uint32_t)g.n, g.act, 0};
+  k.e = Epi{g.bias, g.residual, g.c, g.pre, g.ldr, g.ldc, g.ldp, (uint32_t)g.m, (uint32_t)g.n, g.act, 0, 0};
   k.e.vec = aligned16(g.c, g.ldc, es) && (!g.residual || aligned16(g.residual, g.ldr, es)) &&
             (!g.pre || aligned16(g.pre, g.ldp, es)) && aligned16(g.bias, 0, es);
+  if (p.few) {
+    const bool wide = !needs_pack(g.a, g.m, g.k, es) && !needs_pack(g.b, g.n, g.k, es);
+    const dim3 grid((uint32_t)ceil_div(g.n, 16));
+    if (g.m <= 16) {
+      if (wide) hipLaunchKernelGGL((k_few_rows<T, 1, true>), grid, dim3(256), 0, s, k);
+      else hipLaunchKernelGGL((k_few_rows<T, 1, false>), grid, dim3(256), 0, s, k);
+    } else {
+      if (wide) hipLaunchKernelGGL((k_few_rows<T, 2, true>), grid, dim3(256), 0, s, k);
+      else hipLaunchKernelGGL((k_few_rows<T, 2, false>), grid, dim3(256), 0, s, k);
+    }
+    return hipGetLastError();
+  }
   k.part = p.split > 1 ? reinterpret_cast<float*>(ws + p.off_part) : nullptr;
   k.ldpart = p.ldpart;
   k.tiles_m = p.tiles_m;
@@ -483,9 +656,18 @@ hipError_t run_gemm(const GemmArgs& g, char* ws, hipStream_t s) {
   k.split = p.split;
   k.steps = p.steps;
   k.all_steps = p.all_steps;
+  k.e.stream = g.m * g.n * es >= STREAM_BYTES;
   const uint32_t grid = p.tiles_m * p.tiles_n * p.split;
-  if (p.tile == 128) go<T, 128>(k, g.a.trans, g.b.trans, grid, s);
-  else go<T, 64>(k, g.a.trans, g.b.trans, grid, s);
+  bool done = false;
+  if constexpr (sizeof(T) == 2) {
+    if (p.tile == 256) {
+      go<T, 256, 2, 4>(k, g.a.trans, g.b.trans, grid, s);
+      done = true;
+    }
+  }
+  if (done) {
+  } else if (p.tile == 128) go<T, 128, 2, 2>(k, g.a.trans, g.b.trans, grid, s);
+  else go<T, 64, 2, 2>(k, g.a.trans, g.b.trans, grid, s);
   e = hipGetLastError();
   if (e != hipSuccess || p.split == 1) return e;
   const int64_t n = ceil_div(g.n, v) * g.m;
@@ -522,7 +704,7 @@ __global__ __launch_bounds__(256) void k_slope(const T* __restrict__ dy, const T
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
           if constexpr (ACT == ACT_RELU) v[i] = z[i] <= 0.f ? 0.f : v[i];
-          else v[i] *= slope_of<ACT>(z[i]);
+          else v[i] *= slope_of<ACT, T>(z[i]);
         }
         if (dz) store_vec<T, VEC>(dz + (int64_t)r * ldz + c, v);
       }
@@ -542,14 +724,20 @@ __global__ __launch_bounds__(256) void k_slope(const T* __restrict__ dy, const T
   }
 }
 
+// Four waves share the blocks of 64 columns.
 template <class T>
 __global__ __launch_bounds__(256) void k_join_rows(const float* __restrict__ part, T* __restrict__ out,
                                                    uint32_t blocks, uint32_t n) {
-  const uint32_t c = blockIdx.x * 256 + threadIdx.x;
-  if (c >= n) return;
+  __shared__ float join[4][64];
+  const uint32_t wave = threadIdx.x / 64, lane = threadIdx.x % 64, c = blockIdx.x * 64 + lane;
   float s = 0.f;
-  for (uint32_t b = 0; b < blocks; ++b) s += part[(size_t)b * n + c];
-  out[c] = from_f32<T>(s);
+  if (c < n) {
+#pragma unroll 8
+    for (uint32_t b = wave; b < blocks; b += 4) s += part[(size_t)b * n + c];
+  }
+  join[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && c < n) out[c] = from_f32<T>((join[0][lane] + join[1][lane]) + (join[2][lane] + join[3][lane]));
 }
 
 // Blocks of rows: 64 rows each, at most 65535 blocks (grid dimension y).
@@ -579,7 +767,7 @@ hipError_t run_slope(const SlopeArgs& a, void* ws, hipStream_t s) {
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !a.db) return e;
-  hipLaunchKernelGGL((k_join_rows<T>), dim3((uint32_t)ceil_div(a.n, 256)), dim3(256), 0, s, part,
+  hipLaunchKernelGGL((k_join_rows<T>), dim3((uint32_t)ceil_div(a.n, 64)), dim3(256), 0, s, part,
                      static_cast<T*>(a.db), blocks, (uint32_t)a.n);
   return hipGetLastError();
 }
@@ -615,10 +803,10 @@ hipError_t launch_slope(const SlopeArgs& a, void* ws, hipStream_t s) {
   if (a.n == 0 || (a.m == 0 && !a.db)) return hipSuccess;
   if (a.m == 0) {   // no rows: the sums are zero
     if (a.dtype == DT_BF16)
-      hipLaunchKernelGGL((k_join_rows<bf16_t>), dim3((uint32_t)ceil_div(a.n, 256)), dim3(256), 0, s,
+      hipLaunchKernelGGL((k_join_rows<bf16_t>), dim3((uint32_t)ceil_div(a.n, 64)), dim3(256), 0, s,
                          nullptr, static_cast<bf16_t*>(a.db), 0u, (uint32_t)a.n);
     else
-      hipLaunchKernelGGL((k_join_rows<float>), dim3((uint32_t)ceil_div(a.n, 256)), dim3(256), 0, s,
+      hipLaunchKernelGGL((k_join_rows<float>), dim3((uint32_t)ceil_div(a.n, 64)), dim3(256), 0, s,
                          nullptr, static_cast<float*>(a.db), 0u, (uint32_t)a.n);
     return hipGetLastError();
   }

@@ -82,25 +82,72 @@ __device__ __forceinline__ void store_vec(T* p, const float* v) {
   else Vec<T>::store(p, v);
 }
 
+// A whole vector past the caches.
+template <class T>
+__device__ __forceinline__ void stream_vec(T* p, const float* v) {
+  T q[Vec<T>::N];
+#pragma unroll
+  for (int i = 0; i < Vec<T>::N; ++i) q[i] = from_f32<T>(v[i]);
+  __builtin_nontemporal_store(__builtin_bit_cast(u32x4, q), reinterpret_cast<u32x4*>(p));
+}
+
 // Activations in 32 bits.  Far left of zero gelu and silu are 0 and their
 // slopes 0 (the formulas would give inf * 0 at -inf); NaN stays NaN.
-template <int ACT>
+//
+// Results that are rounded to bf16 (T = bf16_t) use the hardware's exponential
+// and reciprocal and, for the normal distribution function, the five-term
+// form 7.1.26 of Abramowitz and Stegun (off by at most 1.5e-7, where half a
+// bf16 step of a value near 1 is 2e-3); 32-bit results use the full functions.
+//
+// tail_of: 1 - Phi(|z|) and exp(-z^2 / 2).
+__device__ __forceinline__ float tail_of(float z, float* bell) {
+  const float x = fabsf(z) * 0.70710678118654752f;
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.f));
+  const float p = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f),
+                           0.254829592f);
+  *bell = __builtin_amdgcn_exp2f(-1.4426950408889634f * x * x);
+  return 0.5f * p * *bell;
+}
+
+template <int ACT, class T>
 __device__ __forceinline__ float act_of(float z) {
+  constexpr bool SHORT = sizeof(T) == 2;
   if constexpr (ACT == ACT_RELU) return z < 0.f ? 0.f : z;
-  if constexpr (ACT == ACT_GELU) return z < -1e4f ? 0.f : 0.5f * z * erfcf(z * -0.70710678118654752f);
-  if constexpr (ACT == ACT_SILU) return z < -1e4f ? 0.f : z / (1.f + expf(-z));
+  if constexpr (ACT == ACT_GELU) {
+    if constexpr (SHORT) {
+      float bell;
+      const float q = tail_of(z, &bell);
+      return z < -1e4f ? 0.f : z * (z < 0.f ? q : 1.f - q);
+    }
+    return z < -1e4f ? 0.f : 0.5f * z * erfcf(z * -0.70710678118654752f);
+  }
+  if constexpr (ACT == ACT_SILU) {
+    if constexpr (SHORT)
+      return z < -1e4f ? 0.f : z * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * z));
+    return z < -1e4f ? 0.f : z / (1.f + expf(-z));
+  }
   return z;
 }
-template <int ACT>
+template <int ACT, class T>
 __device__ __forceinline__ float slope_of(float z) {
+  constexpr bool SHORT = sizeof(T) == 2;
   if constexpr (ACT == ACT_RELU) return z <= 0.f ? 0.f : 1.f;
   if constexpr (ACT == ACT_GELU) {
-    const float s = 0.5f * erfcf(z * -0.70710678118654752f) +
-                    z * expf(-0.5f * z * z) * 0.39894228040143268f;
+    float phi, bell;
+    if constexpr (SHORT) {
+      const float q = tail_of(z, &bell);
+      phi = z < 0.f ? q : 1.f - q;
+    } else {
+      bell = expf(-0.5f * z * z);
+      phi = 0.5f * erfcf(z * -0.70710678118654752f);
+    }
+    const float s = fmaf(z * bell, 0.39894228040143268f, phi);
     return z > 1e4f ? 1.f : (z < -1e4f ? 0.f : s);
   }
   if constexpr (ACT == ACT_SILU) {
-    const float p = 1.f / (1.f + expf(-z));
+    float p;
+    if constexpr (SHORT) p = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * z));
+    else p = 1.f / (1.f + expf(-z));
     const float s = p * (1.f + z * (1.f - p));
     return z > 1e4f ? 1.f : (z < -1e4f ? 0.f : s);
   }
