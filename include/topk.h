@@ -323,7 +323,8 @@ int topk_stream_read(const void* data, size_t bytes, uint32_t* sink, void* strea
  *   - Matrices are row-major with a row stride ("ld", in elements, at least
  *     the row length) and element alignment.  16-byte aligned rows (address
  *     and stride) are read faster.
- *   - Sizes may be 0: an empty sum is 0.  No size or stride reaches 2^31.
+ *   - Sizes may be 0: an empty sum is 0.  No size or stride reaches 2^31, the
+ *     row width d of a decode stays below 2^22.
  *   - Every result is the same from call to call: no sum's order depends on
  *     timing.
  *   - `workspace`: 256-byte aligned device memory of at least the size that

@@ -17,7 +17,11 @@ namespace {
 
 constexpr int64_t SIZE_MAX31 = (int64_t(1) << 31) - 1;
 
+constexpr int64_t WIDTH_MAX = int64_t(1) << 22;   // row width of a decode (grid dimension y, 64 columns each)
+
 bool bad_size(int64_t v) { return v < 0 || v > SIZE_MAX31; }
+
+bool bad_width(int64_t d) { return d < 0 || d >= WIDTH_MAX; }
 
 int64_t elem(int dtype) { return dtype == TOPK_BF16 ? 2 : 4; }
 
@@ -249,7 +253,7 @@ int topk_decode_workspace_size(const topk_selection* sel, int64_t d, size_t* byt
   tk::Selection s;
   const int rc = to_selection(sel, false, &s);
   if (rc) return rc;
-  if (bad_size(d)) return TOPK_EINVAL;
+  if (bad_width(d)) return TOPK_EINVAL;
   *bytes = decode_ws(s, d);
   return TOPK_OK;
 }
@@ -261,7 +265,7 @@ int topk_decode(const topk_selection* sel, const void* weight, int64_t ldw, int6
   int rc = to_selection(sel, true, &a.sel);
   if (rc) return rc;
   const int dt = a.sel.dtype;
-  if (bad_size(d) || bad_matrix(weight, ldw, a.sel.n, d, dt) || bad_matrix(out, ldo, a.sel.rows, d, dt))
+  if (bad_width(d) || bad_matrix(weight, ldw, a.sel.n, d, dt) || bad_matrix(out, ldo, a.sel.rows, d, dt))
     return TOPK_EINVAL;
   if (bias && bad_matrix(bias, d, 1, d, dt)) return TOPK_EINVAL;
   rc = check_ws(workspace, workspace_bytes, tk::seg_workspace(a.sel, d, true));
@@ -283,7 +287,7 @@ int topk_decode_grad(const topk_selection* sel, const void* weight, int64_t ldw,
   int rc = to_selection(sel, true, &s);
   if (rc) return rc;
   const int dt = s.dtype;
-  if (bad_size(d) || (!dvalues && !dweight && !dbias)) return TOPK_EINVAL;
+  if (bad_width(d) || (!dvalues && !dweight && !dbias)) return TOPK_EINVAL;
   if (bad_matrix(grad, ldg, s.rows, d, dt)) return TOPK_EINVAL;
   if (dvalues && bad_matrix(weight, ldw, s.n, d, dt)) return TOPK_EINVAL;
   if (dvalues && bad_matrix(dvalues, s.total, 1, s.total, dt)) return TOPK_EINVAL;
@@ -337,7 +341,7 @@ int topk_encode_grad(const topk_selection* sel, const void* grad_values, const v
   int rc = to_selection(sel, true, &s);
   if (rc) return rc;
   const int dt = s.dtype;
-  if (bad_size(d) || (!dx && !dweight && !dbias)) return TOPK_EINVAL;
+  if (bad_width(d) || (!dx && !dweight && !dbias)) return TOPK_EINVAL;
   if (bad_matrix(grad_values, s.total, 1, s.total, dt)) return TOPK_EINVAL;
   if (dx && (bad_matrix(weight, ldw, s.n, d, dt) || bad_matrix(dx, lddx, s.rows, d, dt))) return TOPK_EINVAL;
   if (dweight && (bad_matrix(x, ldx, s.rows, d, dt) || bad_matrix(dweight, lddw, s.n, d, dt)))
