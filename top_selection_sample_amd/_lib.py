@@ -124,10 +124,9 @@ def _load():
     L.topk_decode_grad.argtypes = [P(Selection), vp, i64, i64, vp, i64, vp, vp, i64, vp, vp, sz, vp]
     L.topk_encode_grad.argtypes = [P(Selection), vp, vp, i64, vp, i64, i64, vp, i64, vp, i64, vp, vp,
                                    sz, vp]
-    L.topk_grad_norm_workspace_size.argtypes = [i64, P(i64), P(sz)]
-    L.topk_grad_norm.argtypes = [P(vp), P(i64), P(ctypes.c_int32), i64, vp, vp, sz, vp]
-    L.topk_clip_grad_norm.argtypes = [P(vp), P(i64), P(ctypes.c_int32), i64, ctypes.c_float,
-                                      ctypes.c_float, vp, vp, sz, vp]
+    L.topk_grad_norm_workspace_size.argtypes = [i64, vp, P(sz)]   # host arrays by address
+    L.topk_grad_norm.argtypes = [vp, vp, vp, i64, vp, vp, sz, vp]
+    L.topk_clip_grad_norm.argtypes = [vp, vp, vp, i64, ctypes.c_float, ctypes.c_float, vp, vp, sz, vp]
     L.topk_status_string.argtypes = [i32]
     L.topk_status_string.restype = ctypes.c_char_p
     for name in EXPORTS:

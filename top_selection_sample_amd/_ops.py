@@ -9,6 +9,7 @@ different streams, and captured graphs, never share any.
 from __future__ import annotations
 
 import ctypes
+from array import array
 from contextlib import nullcontext
 
 import torch
@@ -462,31 +463,26 @@ def _dense(t: torch.Tensor) -> bool:
     return True
 
 
-def _norm_args(tensors):
+def _norm_run(tensors, clip):
     if isinstance(tensors, torch.Tensor):
         tensors = [tensors]
     ts = [t for t in tensors if t is not None]
     if not ts:
-        return ts, None, None
-    dev = ts[0].device
-    for t in ts:
-        if not t.is_cuda or t.device != dev:
-            raise ValueError(f"tensors: all on one GPU (found {dev} and {t.device})")
-        if t.dtype not in _CODES:
-            raise TypeError(f"tensors: unsupported dtype {t.dtype}; use float32 or bfloat16")
-        if not _dense(t):
-            raise ValueError("tensors: need dense memory (no gaps, no expanded axes)")
-    n = len(ts)
-    args = ((ctypes.c_void_p * n)(*[t.data_ptr() for t in ts]),
-            (ctypes.c_int64 * n)(*[t.numel() for t in ts]),
-            (ctypes.c_int32 * n)(*[_CODES[t.dtype] for t in ts]), n)
-    return ts, dev, args
-
-
-def _norm_run(tensors, clip):
-    ts, dev, args = _norm_args(tensors)
-    if not ts:
         return torch.zeros((), device="cuda")
+    index = ts[0].get_device()
+    if index < 0 or any([t.get_device() != index for t in ts]):
+        raise ValueError(f"tensors: all on one GPU (found {', '.join(sorted({str(t.device) for t in ts}))})")
+    codes = [_CODES.get(t.dtype) for t in ts]
+    if None in codes:
+        raise TypeError(f"tensors: unsupported dtype {ts[codes.index(None)].dtype}; use float32 or bfloat16")
+    if not all([t.is_contiguous() for t in ts]) and not all(map(_dense, ts)):
+        raise ValueError("tensors: need dense memory (no gaps, no expanded axes)")
+    dev = ts[0].device
+    # flat host arrays, passed by address; they live until the call has read them
+    ptrs = array("Q", [t.data_ptr() for t in ts])
+    counts = array("q", [t.numel() for t in ts])
+    codes = array("i", codes)
+    args = (ptrs.buffer_info()[0], counts.buffer_info()[0], codes.buffer_info()[0], len(ts))
     with _on(dev):
         norm = torch.empty((), dtype=torch.float32, device=dev)
         size = ctypes.c_size_t()

@@ -38,11 +38,11 @@ __device__ __forceinline__ bf16_t from_f32<bf16_t>(float v) { return bf16_t{bf16
 template <class T> struct Vec;
 template <> struct Vec<float> {
   static constexpr int N = 4;
-  __device__ static void load(const float* p, float* v) {
-    const f32x4 q = *reinterpret_cast<const f32x4*>(p);
+  __device__ static void unpack(u32x4 q, float* v) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = q[i];
+    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(q[i]);
   }
+  __device__ static void load(const float* p, float* v) { unpack(*reinterpret_cast<const u32x4*>(p), v); }
   __device__ static void store(float* p, const float* v) {
     f32x4 q;
 #pragma unroll
@@ -52,14 +52,14 @@ template <> struct Vec<float> {
 };
 template <> struct Vec<bf16_t> {
   static constexpr int N = 8;
-  __device__ static void load(const bf16_t* p, float* v) {
-    const u32x4 q = *reinterpret_cast<const u32x4*>(p);
+  __device__ static void unpack(u32x4 q, float* v) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       v[2 * i] = __uint_as_float(q[i] << 16);
       v[2 * i + 1] = __uint_as_float(q[i] & 0xFFFF0000u);
     }
   }
+  __device__ static void load(const bf16_t* p, float* v) { unpack(*reinterpret_cast<const u32x4*>(p), v); }
   __device__ static void store(bf16_t* p, const float* v) {
     u32x4 q;
 #pragma unroll
