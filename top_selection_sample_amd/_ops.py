@@ -19,6 +19,7 @@ from . import _lib
 
 _CODES = {torch.float32: 1, torch.bfloat16: 2}
 _byref = ctypes.byref
+_T = torch.Tensor
 
 
 def _code(t: torch.Tensor, what: str) -> int:
@@ -32,7 +33,7 @@ def _check(t, what: str, like: torch.Tensor, shape=None, dtype=None):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what}: need a tensor")
     dtype = dtype or like.dtype
-    if t.device != like.device or t.dtype != dtype or (shape is not None and tuple(t.shape) != shape):
+    if t.dtype != dtype or t.get_device() != like.get_device() or (shape is not None and t.shape != shape):
         raise ValueError(f"{what}: need a {dtype} tensor of shape {shape} on {like.device}, "
                          f"not {t.dtype} {tuple(t.shape)} on {t.device}")
 
@@ -42,17 +43,20 @@ def _gpu(t, what: str):
         raise ValueError(f"{what} must be a GPU tensor")
 
 
-def _on(dev):
+_here = nullcontext()
+
+
+def _on(index: int):
     """The library launches on the current device: switch when the tensors live elsewhere."""
-    return torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else nullcontext()
+    return _here if index == torch._C._cuda_getDevice() else torch.cuda.device(index)
 
 
-def _stream(dev) -> int:
-    return torch.cuda.current_stream(dev).cuda_stream
+# the current stream's handle on a device
+_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _scratch(nbytes: int, dev):
-    return torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+def _scratch(nbytes: int, like):
+    return like.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
 
 
 def _ptr(t):
@@ -64,6 +68,8 @@ def _matrix(t: torch.Tensor, either: bool = False):
     stride as they are; columns with unit stride too where the call takes
     ``either`` order; any other layout (expanded, stepped) as a copy."""
     r, c = t.shape
+    if t.is_contiguous():
+        return t, c or 1, 0
     sr, sc = t.stride()
     if (sc == 1 or c <= 1) and (sr >= c or r <= 1):
         return t, max(sr if r > 1 else c, c, 1), 0
@@ -85,14 +91,18 @@ def _act_code(activation: str) -> int:
 
 
 def _wants_grad(*tensors) -> bool:
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                return True
+    return False
 
 
 # ---------------------------------------------------------------- linear
 def _linear_run(x, w, bias, act, residual, want_pre):
     m, k = x.shape
     n = w.shape[0]
-    dev = x.device
+    dev = x.get_device()
     x, ldx, xt = _matrix(x, True)
     w, ldw, wt = _matrix(w, True)
     ldr = 0
@@ -101,13 +111,13 @@ def _linear_run(x, w, bias, act, residual, want_pre):
     if bias is not None:
         bias = bias.contiguous()
     with _on(dev):
-        y = torch.empty((m, n), dtype=x.dtype, device=dev)
-        pre = torch.empty((m, n), dtype=x.dtype, device=dev) if want_pre else None
+        y = x.new_empty((m, n))
+        pre = x.new_empty((m, n)) if want_pre else None
         a = _lib.LinearArgs(x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(residual), y.data_ptr(),
                             _ptr(pre), m, n, k, ldx, ldw, ldr, n, n, _CODES[x.dtype], act, xt, wt)
         size = ctypes.c_size_t()
         _lib.check(_lib.lib.topk_linear_workspace_size(_byref(a), _byref(size)), "linear")
-        ws = _scratch(size.value, dev)
+        ws = _scratch(size.value, x)
         _lib.check(_lib.lib.topk_linear(_byref(a), _ptr(ws), size.value, _stream(dev)), "linear")
     return y, pre
 
@@ -115,7 +125,7 @@ def _linear_run(x, w, bias, act, residual, want_pre):
 def _linear_grad_run(dy, x, w, act, pre, need):
     m, n = dy.shape
     k = w.shape[1]
-    dev = dy.device
+    dev = dy.get_device()
     dy, ldd, _ = _matrix(dy)
     x, ldx, xt = _matrix(x, True)
     w, ldw, wt = _matrix(w, True)
@@ -123,16 +133,16 @@ def _linear_grad_run(dy, x, w, act, pre, need):
     if pre is not None:
         pre, ldp, _ = _matrix(pre)
     with _on(dev):
-        dx = torch.empty((m, k), dtype=dy.dtype, device=dev) if need[0] else None
-        dw = torch.empty((n, k), dtype=dy.dtype, device=dev) if need[1] else None
-        db = torch.empty((n,), dtype=dy.dtype, device=dev) if need[2] else None
+        dx = dy.new_empty((m, k)) if need[0] else None
+        dw = dy.new_empty((n, k)) if need[1] else None
+        db = dy.new_empty((n,)) if need[2] else None
         if _empty(dx, dw, db):
             return dx, dw, db
         a = _lib.LinearGradArgs(dy.data_ptr(), _ptr(pre), x.data_ptr(), w.data_ptr(), _ptr(dx), _ptr(dw),
                                 _ptr(db), m, n, k, ldd, ldp, ldx, ldw, k, k, _CODES[dy.dtype], act, xt, wt)
         size = ctypes.c_size_t()
         _lib.check(_lib.lib.topk_linear_grad_workspace_size(_byref(a), _byref(size)), "linear_grad")
-        ws = _scratch(size.value, dev)
+        ws = _scratch(size.value, dy)
         _lib.check(_lib.lib.topk_linear_grad(_byref(a), _ptr(ws), size.value, _stream(dev)),
                    "linear_grad")
     return dx, dw, db
@@ -183,7 +193,7 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = No
     if bias is not None:
         _check(bias, "bias", x, (n,))
     if residual is not None:
-        _check(residual, "residual", x, tuple(lead) + (n,))
+        _check(residual, "residual", x, (*lead, n))
     flat = x.dim() == 2
     x2 = x if flat else x.reshape(lead.numel(), k)
     r2 = residual if flat or residual is None else residual.reshape(lead.numel(), n)
@@ -238,23 +248,23 @@ def _selection(values, indices, rows, n):
                           _CODES[values.dtype])
 
 
-def _decode_scratch(sel, d, dev):
+def _decode_scratch(sel, d, like):
     size = ctypes.c_size_t()
     _lib.check(_lib.lib.topk_decode_workspace_size(_byref(sel), d, _byref(size)), "decode")
-    return _scratch(size.value, dev), size.value
+    return _scratch(size.value, like), size.value
 
 
 def _decode_run(values, indices, weight, rows, bias):
     n, d = weight.shape
-    dev = values.device
+    dev = values.get_device()
     values, indices = values.contiguous(), indices.contiguous()
     weight, ldw, _ = _matrix(weight)
     if bias is not None:
         bias = bias.contiguous()
     with _on(dev):
-        out = torch.empty((rows, d), dtype=values.dtype, device=dev)
+        out = values.new_empty((rows, d))
         sel = _selection(values, indices, rows, n)
-        ws, size = _decode_scratch(sel, d, dev)
+        ws, size = _decode_scratch(sel, d, values)
         _lib.check(_lib.lib.topk_decode(_byref(sel), weight.data_ptr(), ldw, d, _ptr(bias),
                                         out.data_ptr(), max(d, 1), _ptr(ws), size, _stream(dev)),
                    "decode")
@@ -264,18 +274,18 @@ def _decode_run(values, indices, weight, rows, bias):
 def _decode_grad_run(grad, values, indices, weight, need):
     n, d = weight.shape
     rows = grad.shape[0]
-    dev = grad.device
+    dev = grad.get_device()
     values, indices = values.contiguous(), indices.contiguous()
     weight, ldw, _ = _matrix(weight)
     grad, ldg, _ = _matrix(grad)
     with _on(dev):
         dv = torch.empty_like(values) if need[0] else None
-        dw = torch.empty((n, d), dtype=grad.dtype, device=dev) if need[1] else None
-        db = torch.empty((d,), dtype=grad.dtype, device=dev) if need[2] else None
+        dw = grad.new_empty((n, d)) if need[1] else None
+        db = grad.new_empty((d,)) if need[2] else None
         if _empty(dv, dw, db):
             return dv, dw, db
         sel = _selection(values, indices, rows, n)
-        ws, size = _decode_scratch(sel, d, dev)
+        ws, size = _decode_scratch(sel, d, values)
         _lib.check(_lib.lib.topk_decode_grad(_byref(sel), weight.data_ptr(), ldw, d, grad.data_ptr(), ldg,
                                              _ptr(dv), _ptr(dw), max(d, 1), _ptr(db), _ptr(ws), size,
                                              _stream(dev)), "decode_grad")
@@ -302,7 +312,7 @@ def _check_selection(values, indices, rows):
     _code(values, "values")
     if values.dim() not in (1, 2):
         raise ValueError("values, indices: [rows, k], or [k] of a flattened selection")
-    _check(indices, "indices", values, tuple(values.shape), torch.int64)
+    _check(indices, "indices", values, values.shape, torch.int64)
     if values.dim() == 2:
         if rows is not None and rows != values.shape[0]:
             raise ValueError(f"rows is {rows}, values has {values.shape[0]}")
@@ -358,18 +368,18 @@ def decode_grad(grad: torch.Tensor, values: torch.Tensor, indices: torch.Tensor,
 def _encode_grad_run(grad_values, values, indices, x, weight, need):
     n, d = weight.shape
     rows = x.shape[0]
-    dev = x.device
+    dev = x.get_device()
     grad_values, values, indices = grad_values.contiguous(), values.contiguous(), indices.contiguous()
     weight, ldw, _ = _matrix(weight)
     x, ldx, _ = _matrix(x)
     with _on(dev):
-        dx = torch.empty((rows, d), dtype=x.dtype, device=dev) if need[0] else None
-        dw = torch.empty((n, d), dtype=x.dtype, device=dev) if need[1] else None
-        db = torch.empty((n,), dtype=x.dtype, device=dev) if need[2] else None
+        dx = x.new_empty((rows, d)) if need[0] else None
+        dw = x.new_empty((n, d)) if need[1] else None
+        db = x.new_empty((n,)) if need[2] else None
         if _empty(dx, dw, db):
             return dx, dw, db
         sel = _selection(values, indices, rows, n)
-        ws, size = _decode_scratch(sel, d, dev)
+        ws, size = _decode_scratch(sel, d, values)
         _lib.check(_lib.lib.topk_encode_grad(_byref(sel), grad_values.data_ptr(), x.data_ptr(), ldx,
                                              weight.data_ptr(), ldw, d, _ptr(dx), max(d, 1), _ptr(dw),
                                              max(d, 1), _ptr(db), _ptr(ws), size, _stream(dev)),
@@ -438,7 +448,7 @@ def encode_grad(grad_values: torch.Tensor, values: torch.Tensor, indices: torch.
     if x.dim() != 2 or not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("x: [rows, d]; weight: [n, d]")
     rows = _check_selection(values, indices, x.shape[0])
-    _check(grad_values, "grad_values", values, tuple(values.shape))
+    _check(grad_values, "grad_values", values, values.shape)
     _check(weight, "weight", values, (weight.shape[0], x.shape[1]))
     _check(x, "x", values, (rows, weight.shape[1]))
     need = tuple(bool(b) for b in need)
@@ -470,47 +480,46 @@ def _norm_run(tensors, clip):
     if not ts:
         return torch.zeros((), device="cuda")
     index = ts[0].get_device()
-    if index < 0 or any([t.get_device() != index for t in ts]):
+    if index < 0 or set(map(_T.get_device, ts)) != {index}:
         raise ValueError(f"tensors: all on one GPU (found {', '.join(sorted({str(t.device) for t in ts}))})")
     codes = [_CODES.get(t.dtype) for t in ts]
     if None in codes:
         raise TypeError(f"tensors: unsupported dtype {ts[codes.index(None)].dtype}; use float32 or bfloat16")
-    if not all([t.is_contiguous() for t in ts]) and not all(map(_dense, ts)):
+    if not all(map(_T.is_contiguous, ts)) and not all(map(_dense, ts)):
         raise ValueError("tensors: need dense memory (no gaps, no expanded axes)")
-    dev = ts[0].device
     # flat host arrays, passed by address; they live until the call has read them
-    ptrs = array("Q", [t.data_ptr() for t in ts])
-    counts = array("q", [t.numel() for t in ts])
+    ptrs = array("Q", map(_T.data_ptr, ts))
+    counts = array("q", map(_T.numel, ts))
     codes = array("i", codes)
     args = (ptrs.buffer_info()[0], counts.buffer_info()[0], codes.buffer_info()[0], len(ts))
-    with _on(dev):
-        norm = torch.empty((), dtype=torch.float32, device=dev)
+    with _on(index):
+        norm = ts[0].new_empty((), dtype=torch.float32)
         size = ctypes.c_size_t()
         _lib.check(_lib.lib.topk_grad_norm_workspace_size(args[3], args[1], _byref(size)), "grad_norm")
-        ws = _scratch(size.value, dev)
+        ws = _scratch(size.value, norm)
         if clip is None:
-            _lib.check(_lib.lib.topk_grad_norm(*args, norm.data_ptr(), _ptr(ws), size.value, _stream(dev)),
+            _lib.check(_lib.lib.topk_grad_norm(*args, norm.data_ptr(), _ptr(ws), size.value, _stream(index)),
                        "grad_norm")
         else:
             _lib.check(_lib.lib.topk_clip_grad_norm(*args, *clip, norm.data_ptr(), _ptr(ws), size.value,
-                                                    _stream(dev)), "clip_grad_norm")
+                                                    _stream(index)), "clip_grad_norm")
             _written(ts)
     return norm
 
 
 def _written(ts):
     """Tell autograd that the tensors changed in place (inference tensors keep no count)."""
-    torch.autograd.graph.increment_version([t for t in ts if not t.is_inference()])
+    if any(map(_T.is_inference, ts)):
+        ts = [t for t in ts if not t.is_inference()]
+    torch.autograd.graph.increment_version(ts)
 
 
-@torch.no_grad()
 def grad_norm(tensors) -> torch.Tensor:
     """The 2-norm of all elements of ``tensors`` (one tensor or several, dense,
     float32 and bfloat16 mixed, None skipped), as a float32 scalar on their GPU."""
     return _norm_run(tensors, None)
 
 
-@torch.no_grad()
 def clip_grad_norm(tensors, max_norm: float, eps: float = 1e-6) -> torch.Tensor:
     """Scale ``tensors`` in place by min(1, max_norm / (norm + eps)), ``norm`` their
     global 2-norm, which is returned as a float32 scalar on the GPU (no

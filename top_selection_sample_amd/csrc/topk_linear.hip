@@ -267,18 +267,36 @@ __device__ __forceinline__ void gemm_step(lds_char* cur, lds_char* next, LA& la,
                                           uint32_t wn, f32x4 (&acc)[FN][FM]) {
   wait_loads();
   __syncthreads();   // this step's tiles have arrived; the other stage is free
-  if (more) {
-    la.issue(next, kt + 1, wave);
-    lb.issue(next + TM * 128, kt + 1, wave);
-  }
+  auto ahead = [&]() {
+    if (more) {
+      la.issue(next, kt + 1, wave);
+      lb.issue(next + TM * 128, kt + 1, wave);
+    }
+  };
+  if constexpr (FM * FN <= 16) {
+    // both halves' fragments first: the second half's reads are covered by the first half's products
+    u32x4 fa[2][FM], fb[2][FN];
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    u32x4 fa[FM], fb[FN];
+    for (int s = 0; s < 2; ++s) {
 #pragma unroll
-    for (int i = 0; i < FN; ++i) fb[i] = fragment<T, TN, TB>(cur + TM * 128, wn + i, s, lane);
+      for (int i = 0; i < FN; ++i) fb[s][i] = fragment<T, TN, TB>(cur + TM * 128, wn + i, s, lane);
 #pragma unroll
-    for (int j = 0; j < FM; ++j) fa[j] = fragment<T, TM, TA>(cur, wm + j, s, lane);
-    mma_all<T, FM, FN>(fb, fa, acc);
+      for (int j = 0; j < FM; ++j) fa[s][j] = fragment<T, TM, TA>(cur, wm + j, s, lane);
+    }
+    ahead();
+#pragma unroll
+    for (int s = 0; s < 2; ++s) mma_all<T, FM, FN>(fb[s], fa[s], acc);
+  } else {   // the registers hold one half's
+    ahead();
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      u32x4 fa[FM], fb[FN];
+#pragma unroll
+      for (int i = 0; i < FN; ++i) fb[i] = fragment<T, TN, TB>(cur + TM * 128, wn + i, s, lane);
+#pragma unroll
+      for (int j = 0; j < FM; ++j) fa[j] = fragment<T, TM, TA>(cur, wm + j, s, lane);
+      mma_all<T, FM, FN>(fb, fa, acc);
+    }
   }
 }
 
@@ -343,25 +361,40 @@ __global__ __launch_bounds__(NWM * NWN * 64, 2) void k_gemm(KGemm p) {
         *reinterpret_cast<f32x4*>(mine + r * C + (u ^ (r % CH)) * 4) = acc[i][j + h];
       }
     const uint32_t r0 = m0 + (wm + j) * 16;
+    if (p.part || p.e.vec) {
 #pragma unroll 1
-    for (uint32_t rr = lane / LANES; rr < 32; rr += ROWS) {
-      if (r0 + rr >= p.e.m) break;
-      float v[V];
+      for (uint32_t rr = lane / LANES; rr < 32; rr += ROWS) {
+        if (r0 + rr >= p.e.m) break;
+        float v[V];
 #pragma unroll
-      for (int i = 0; i < V; i += 4) Vec<float>::load(mine + rr * C + ((cc / 4 + i / 4) ^ (rr % CH)) * 4, v + i);
-      if (p.part) {
-        float* o = p.part + ((size_t)sp * p.e.m + r0 + rr) * p.ldpart + c;
+        for (int i = 0; i < V; i += 4) Vec<float>::load(mine + rr * C + ((cc / 4 + i / 4) ^ (rr % CH)) * 4, v + i);
+        if (p.part) {
+          float* o = p.part + ((size_t)sp * p.e.m + r0 + rr) * p.ldpart + c;
 #pragma unroll
-        for (int i = 0; i < V; i += 4)
-          if (c + i < p.ldpart) Vec<float>::store(o + i, v + i);
-      } else if (whole) {
-        finish<T, V>(v, bias, r0 + rr, c, p.e);
-      } else {
+          for (int i = 0; i < V; i += 4)
+            if (c + i < p.ldpart) Vec<float>::store(o + i, v + i);
+        } else if (whole) {
+          finish<T, V>(v, bias, r0 + rr, c, p.e);
+        } else {   // the last columns
 #pragma unroll 1
-        for (uint32_t i = 0; i < V && c + i < p.e.n; ++i) {
-          float z = mine[rr * C + ((cc / 4 + i / 4) ^ (rr % CH)) * 4 + i % 4], b1;
-          bias_of<T, 1>(&b1, c + i, p.e);
-          finish<T, 1>(&z, &b1, r0 + rr, c + i, p.e);
+          for (uint32_t i = 0; i < V && c + i < p.e.n; ++i) {
+            float z = mine[rr * C + ((cc / 4 + i / 4) ^ (rr % CH)) * 4 + i % 4], b1;
+            bias_of<T, 1>(&b1, c + i, p.e);
+            finish<T, 1>(&z, &b1, r0 + rr, c + i, p.e);
+          }
+        }
+      }
+    } else {   // rows at any alignment: a lane per column
+      const uint32_t c1 = lane % C;
+      const uint32_t col = n0 + wn * 16 + c1;
+      if (col < p.e.n) {
+        float b1;
+        bias_of<T, 1>(&b1, col, p.e);
+#pragma unroll 1
+        for (uint32_t rr = lane / C; rr < 32; rr += 64 / C) {
+          if (r0 + rr >= p.e.m) break;
+          float z = mine[rr * C + ((c1 / 4) ^ (rr % CH)) * 4 + c1 % 4];
+          finish<T, 1>(&z, &b1, r0 + rr, col, p.e);
         }
       }
     }
@@ -404,22 +437,35 @@ __global__ __launch_bounds__(256) void k_split_join(const float* __restrict__ pa
   }
 }
 
-// Copies lines of `red` elements to lines of `ldo`, zeros behind their end.
+// Copies lines of `red` elements to lines of `ldo`, zeros behind their end;
+// both operands of a product in one launch (`vecs` 0: not this one).
+struct KPack {
+  const void* src;
+  void* dst;
+  int64_t ld;
+  uint32_t red, ldo;
+  uint64_t vecs;       // 16-byte vectors written
+};
+
 template <class T>
-__global__ __launch_bounds__(256) void k_pack(const T* __restrict__ src, int64_t ld, uint32_t lines,
-                                              uint32_t red, T* __restrict__ dst, uint32_t ldo) {
+__global__ __launch_bounds__(256) void k_pack(KPack a, KPack b) {
   constexpr int V = Vec<T>::N;
-  const uint32_t per = ldo / V;
-  const uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= (uint64_t)per * lines) return;
-  const uint32_t r = (uint32_t)(i / per), c = (uint32_t)(i % per) * V;
+  uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x;
+  const bool second = i >= a.vecs;
+  if (second) i -= a.vecs;
+  const KPack p = second ? b : a;
+  if (i >= p.vecs) return;
+  const uint32_t per = p.ldo / V;
+  const uint64_t r = i / per;
+  const uint32_t c = (uint32_t)(i - r * per) * V;
+  const T* src = static_cast<const T*>(p.src) + (int64_t)r * p.ld + c;
   T v[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     v[j] = T{};
-    if (c + j < red) v[j] = src[(int64_t)r * ld + c + j];
+    if (c + j < p.red) v[j] = src[j];
   }
-  *reinterpret_cast<u32x4*>(dst + (uint64_t)r * ldo + c) = *reinterpret_cast<const u32x4*>(v);
+  *reinterpret_cast<u32x4*>(static_cast<T*>(p.dst) + r * p.ldo + c) = __builtin_bit_cast(u32x4, v);
 }
 
 // Few rows of x: the call is bound by reading W once.  A workgroup takes 16
@@ -525,8 +571,8 @@ struct TileCost {
   uint32_t tile, holds;
   double shared, alone, ends;
 };
-constexpr TileCost COST_BF16[] = {{64, 4, 0.215, 0.7, 4}, {128, 2, 0.48, 0.8, 6}, {256, 1, 1.5, 1.5, 12}};
-constexpr TileCost COST_F32[] = {{64, 4, 0.5, 0.9, 4}, {128, 2, 1.94, 2.4, 6}};
+constexpr TileCost COST_BF16[] = {{64, 4, 0.2, 0.7, 4}, {128, 2, 0.49, 0.8, 6}, {256, 1, 1.55, 1.55, 12}};
+constexpr TileCost COST_F32[] = {{64, 4, 0.5, 1.08, 4}, {128, 2, 1.93, 2.2, 6}};
 
 // The tile and the split of the summed axis that are estimated cheapest.
 void choose_tile(const GemmArgs& g, Plan2* p) {
@@ -592,19 +638,17 @@ Plan2 plan_gemm(const GemmArgs& g) {
 }
 
 template <class T>
-hipError_t run_pack(const Operand& o, int64_t rows, int64_t red, uint32_t ldo, void* dst, hipStream_t s) {
+KPack pack_of(const Operand& o, int64_t rows, int64_t red, uint32_t ldo, void* dst) {
   const int64_t line = o.trans ? rows : red, lines = o.trans ? red : rows;
-  const int64_t n = (int64_t)(ldo / Vec<T>::N) * lines;
-  hipLaunchKernelGGL((k_pack<T>), dim3((uint32_t)ceil_div(n, 256)), dim3(256), 0, s,
-                     static_cast<const T*>(o.p), o.ld, (uint32_t)lines, (uint32_t)line, static_cast<T*>(dst), ldo);
-  return hipGetLastError();
+  return KPack{o.p, dst, o.ld, (uint32_t)line, ldo, (uint64_t)(ldo / Vec<T>::N) * (uint64_t)lines};
 }
 
 template <class T, int R, int NWM, int NWN>
 void go(const KGemm& k, bool ta, bool tb, uint32_t grid, hipStream_t s) {
   const dim3 block(NWM * NWN * 64);
-  if (ta && tb) hipLaunchKernelGGL((k_gemm<T, R, R, NWM, NWN, true, true>), dim3(grid), block, 0, s, k);
-  else if (ta) hipLaunchKernelGGL((k_gemm<T, R, R, NWM, NWN, true, false>), dim3(grid), block, 0, s, k);
+  if (ta && tb) {   // (no 256-tile: see choose_tile)
+    if constexpr (R < 256) hipLaunchKernelGGL((k_gemm<T, R, R, NWM, NWN, true, true>), dim3(grid), block, 0, s, k);
+  } else if (ta) hipLaunchKernelGGL((k_gemm<T, R, R, NWM, NWN, true, false>), dim3(grid), block, 0, s, k);
   else if (tb) hipLaunchKernelGGL((k_gemm<T, R, R, NWM, NWN, false, true>), dim3(grid), block, 0, s, k);
   else hipLaunchKernelGGL((k_gemm<T, R, R, NWM, NWN, false, false>), dim3(grid), block, 0, s, k);
 }
@@ -618,9 +662,14 @@ hipError_t run_gemm(const GemmArgs& g, char* ws, hipStream_t s) {
   const Plan2 p = plan_gemm(g);
   const int64_t es = sizeof(T), v = 16 / es;
   hipError_t e = hipSuccess;
-  if (p.pack_a) e = run_pack<T>(g.a, g.m, g.k, p.lda, ws, s);
-  if (e == hipSuccess && p.pack_b) e = run_pack<T>(g.b, g.n, g.k, p.ldb, ws + p.off_b, s);
-  if (e != hipSuccess) return e;
+  if (p.pack_a || p.pack_b) {
+    KPack a{}, b{};
+    if (p.pack_a) a = pack_of<T>(g.a, g.m, g.k, p.lda, ws);
+    if (p.pack_b) b = pack_of<T>(g.b, g.n, g.k, p.ldb, ws + p.off_b);
+    hipLaunchKernelGGL((k_pack<T>), dim3((uint32_t)ceil_div((int64_t)(a.vecs + b.vecs), 256)), dim3(256), 0, s, a, b);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   auto operand = [&](const Operand& o, int64_t rows, bool pack, uint32_t ldp, char* at) {
     KOperand k;
     const int64_t line = o.trans ? rows : g.k, lines = o.trans ? g.k : rows;

@@ -68,21 +68,32 @@ struct Selection {
 // out[key] = bias + sum over the entries of `key` of coef * src[other]:
 // by_row: key = row, src has a row per latent; otherwise key = latent.
 struct SegArgs {
-  Selection sel;
   bool by_row = true;
-  const void* coef = nullptr;       // values, or the gradient of the values
-  const void* gate = nullptr;       // entries whose gate value is not > 0 count as 0 (null: none)
   const void* src = nullptr;
   int64_t lds = 0;
-  int64_t d = 0;
-  const void* bias = nullptr;       // [d], by_row only
-  void* out = nullptr;
+  const void* bias = nullptr;       // [d], or null
+  void* out = nullptr;              // null: not wanted
   int64_t ldo = 0;
-  void* coef_sum = nullptr;         // optional: sum of coef per key
+  void* coef_sum = nullptr;         // sum of coef per key; null: not wanted
+  // by latent only: dots[e] = <src[row_e], other[latent_e]> on the way; null: not wanted
+  const void* other = nullptr;
+  int64_t ldother = 0;
+  void* dots = nullptr;
 };
 
-size_t seg_workspace(const Selection& sel, int64_t d, bool by_row);
-hipError_t launch_seg(const SegArgs& a, void* ws, hipStream_t s);
+// One or two such sums over the same selection and coefficients.
+struct SegCall {
+  Selection sel;
+  const void* coef = nullptr;       // values, or the gradient of the values
+  const void* gate = nullptr;       // entries whose gate value is not > 0 count as 0 (null: none)
+  int64_t d = 0;
+  int parts = 0;
+  SegArgs part[2];
+};
+
+// Scratch of a call with a sum by row, by latent, or both.
+size_t seg_workspace(const Selection& sel, int64_t d, bool by_row, bool by_latent);
+hipError_t launch_seg(const SegCall& a, void* ws, hipStream_t s);
 
 // dv[e] = <g[row_e], w[latent_e]> (0 for padded entries)
 struct DotArgs {

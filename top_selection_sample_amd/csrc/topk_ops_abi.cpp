@@ -175,8 +175,7 @@ size_t decode_ws(const tk::Selection& s, int64_t d) {
   sums.n = d;
   sums.dtype = s.dtype;
   sums.db = &sums;   // only whether it is wanted counts here
-  return std::max({tk::seg_workspace(s, d, true), tk::seg_workspace(s, d, false),
-                   tk::slope_workspace(sums)});
+  return std::max(tk::seg_workspace(s, d, true, true), tk::slope_workspace(sums));
 }
 
 }  // namespace
@@ -261,22 +260,23 @@ int topk_decode_workspace_size(const topk_selection* sel, int64_t d, size_t* byt
 int topk_decode(const topk_selection* sel, const void* weight, int64_t ldw, int64_t d,
                 const void* bias, void* out, int64_t ldo, void* workspace, size_t workspace_bytes,
                 void* stream) {
-  tk::SegArgs a;
+  tk::SegCall a;
   int rc = to_selection(sel, true, &a.sel);
   if (rc) return rc;
   const int dt = a.sel.dtype;
   if (bad_width(d) || bad_matrix(weight, ldw, a.sel.n, d, dt) || bad_matrix(out, ldo, a.sel.rows, d, dt))
     return TOPK_EINVAL;
   if (bias && bad_matrix(bias, d, 1, d, dt)) return TOPK_EINVAL;
-  rc = check_ws(workspace, workspace_bytes, tk::seg_workspace(a.sel, d, true));
+  rc = check_ws(workspace, workspace_bytes, tk::seg_workspace(a.sel, d, true, false));
   if (rc) return rc;
   a.coef = a.sel.values;
-  a.src = weight;
-  a.lds = ldw;
   a.d = d;
-  a.bias = bias;
-  a.out = out;
-  a.ldo = ldo;
+  a.parts = 1;
+  a.part[0].src = weight;
+  a.part[0].lds = ldw;
+  a.part[0].bias = bias;
+  a.part[0].out = out;
+  a.part[0].ldo = ldo;
   return status(tk::launch_seg(a, workspace, static_cast<hipStream_t>(stream)));
 }
 
@@ -300,13 +300,28 @@ int topk_decode_grad(const topk_selection* sel, const void* weight, int64_t ldw,
   sums.n = d;
   sums.dtype = dt;
   sums.db = dbias;
-  size_t need = dweight ? tk::seg_workspace(s, d, false) : 0;
+  size_t need = dweight ? tk::seg_workspace(s, d, false, true) : 0;
   if (dbias) need = std::max(need, tk::slope_workspace(sums));
   rc = check_ws(workspace, workspace_bytes, need);
   if (rc) return rc;
   hipStream_t st = static_cast<hipStream_t>(stream);
   hipError_t e = hipSuccess;
-  if (dvalues) {
+  if (dweight) {   // with dvalues on the way
+    tk::SegCall a;
+    a.sel = s;
+    a.coef = s.values;
+    a.d = d;
+    a.parts = 1;
+    a.part[0].by_row = false;
+    a.part[0].src = grad;
+    a.part[0].lds = ldg;
+    a.part[0].out = dweight;
+    a.part[0].ldo = lddw;
+    a.part[0].other = dvalues ? weight : nullptr;
+    a.part[0].ldother = ldw;
+    a.part[0].dots = dvalues;
+    e = tk::launch_seg(a, workspace, st);
+  } else if (dvalues) {
     tk::DotArgs a;
     a.sel = s;
     a.g = grad;
@@ -316,18 +331,6 @@ int topk_decode_grad(const topk_selection* sel, const void* weight, int64_t ldw,
     a.d = d;
     a.dv = dvalues;
     e = tk::launch_dots(a, st);
-  }
-  if (e == hipSuccess && dweight) {
-    tk::SegArgs a;
-    a.sel = s;
-    a.by_row = false;
-    a.coef = s.values;
-    a.src = grad;
-    a.lds = ldg;
-    a.d = d;
-    a.out = dweight;
-    a.ldo = lddw;
-    e = tk::launch_seg(a, workspace, st);
   }
   if (e == hipSuccess && dbias) e = tk::launch_slope(sums, workspace, st);
   return status(e);
@@ -347,36 +350,30 @@ int topk_encode_grad(const topk_selection* sel, const void* grad_values, const v
   if (dweight && (bad_matrix(x, ldx, s.rows, d, dt) || bad_matrix(dweight, lddw, s.n, d, dt)))
     return TOPK_EINVAL;
   if (dbias && bad_matrix(dbias, s.n, 1, s.n, dt)) return TOPK_EINVAL;
-  size_t need = dx ? tk::seg_workspace(s, d, true) : 0;
-  if (dweight || dbias) need = std::max(need, tk::seg_workspace(s, d, false));
-  rc = check_ws(workspace, workspace_bytes, need);
+  rc = check_ws(workspace, workspace_bytes, tk::seg_workspace(s, d, dx != nullptr, dweight || dbias));
   if (rc) return rc;
-  hipStream_t st = static_cast<hipStream_t>(stream);
-  tk::SegArgs a;
+  tk::SegCall a;
   a.sel = s;
   a.coef = grad_values;
   a.gate = s.values;
-  hipError_t e = hipSuccess;
+  a.d = d;
   if (dx) {
-    a.by_row = true;
-    a.src = weight;
-    a.lds = ldw;
-    a.d = d;
-    a.out = dx;
-    a.ldo = lddx;
-    e = tk::launch_seg(a, workspace, st);
+    tk::SegArgs& p = a.part[a.parts++];
+    p.src = weight;
+    p.lds = ldw;
+    p.out = dx;
+    p.ldo = lddx;
   }
-  if (e == hipSuccess && (dweight || dbias)) {
-    a.by_row = false;
-    a.src = x;
-    a.lds = ldx;
-    a.d = dweight ? d : 0;
-    a.out = dweight;
-    a.ldo = lddw;
-    a.coef_sum = dbias;
-    e = tk::launch_seg(a, workspace, st);
+  if (dweight || dbias) {
+    tk::SegArgs& p = a.part[a.parts++];
+    p.by_row = false;
+    p.src = x;
+    p.lds = ldx;
+    p.out = dweight;
+    p.ldo = lddw;
+    p.coef_sum = dbias;
   }
-  return status(e);
+  return status(tk::launch_seg(a, workspace, static_cast<hipStream_t>(stream)));
 }
 
 int topk_grad_norm_workspace_size(int64_t tensors, const int64_t* counts, size_t* bytes) {

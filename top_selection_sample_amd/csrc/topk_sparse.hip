@@ -79,7 +79,8 @@ struct SortPlan {
   uint32_t passes = 1, width = 0;       // digit bits of a pass (0: the whole key)
   uint32_t max_bins = 0;
   uint32_t blocks = 0, per_block = 0;
-  size_t off_cnt = 0, off_coarse = 0, off_key = 0, off_pos = 0, off_skey = 0, off_other = 0, off_coef = 0, total_bytes = 0;
+  size_t off_cnt = 0, off_coarse = 0, off_key = 0, off_pos = 0, off_skey = 0, off_spos = 0, off_other = 0, off_coef = 0,
+         off_run = 0, total_bytes = 0;
 };
 
 uint32_t bins_of(const SortPlan& p, uint32_t pass) {
@@ -116,6 +117,8 @@ SortPlan sort_plan(int64_t keys, int64_t total) {
     p.off_pos = take((size_t)total * 8);
   }
   p.off_skey = take((size_t)total * 4);
+  p.off_spos = take((size_t)total * 4);
+  p.off_run = take((size_t)keys * 8);
   p.off_other = take((size_t)total * 4);
   p.off_coef = take((size_t)total * 4);
   p.total_bytes = at;
@@ -127,13 +130,19 @@ struct KPass {
   const uint32_t* key_in;     // null: from the selection
   const uint32_t* pos_in;
   uint32_t* key_out;
-  uint32_t* pos_out;          // null: the last pass, which writes what the sums read
-  uint32_t* other;
+  uint32_t* pos_out;
+  uint32_t* other;            // the last pass also writes what the sums read
   float* coef;
   uint32_t* cnt;              // [blocks][bins]
-  uint32_t* coarse;           // [blocks][bins / GROUP rounded up]
+  uint32_t* coarse;           // [groups][blocks]
+  uint32_t* run;              // [keys][2]: first entry and end of a key's run, cleared by the first pass
   uint32_t keys, total, per_block, bins, groups, shift, mask, digit_bits, blocks;
-  int by_row;
+  int by_row, last;
+};
+
+// A launch sorts by row and by latent side by side (grid dimension y).
+struct KPasses {
+  KPass p[2];
 };
 
 __device__ __forceinline__ uint32_t key_of(const KSel& s, const KPass& p, uint32_t e) {
@@ -143,14 +152,21 @@ __device__ __forceinline__ uint32_t key_of(const KSel& s, const KPass& p, uint32
   return p.by_row ? row : latent;
 }
 
-__global__ __launch_bounds__(SORT_THREADS) void k_count(KSel s, KPass p) {
+constexpr uint32_t NO_ENTRY = 0xFFFFFFFFu;
+
+__global__ __launch_bounds__(SORT_THREADS) void k_count(KSel s, KPasses ps) {
   extern __shared__ uint32_t hist[];
+  const KPass& p = ps.p[blockIdx.y];
   for (uint32_t i = threadIdx.x; i < p.bins; i += SORT_THREADS) hist[i] = 0;
   __syncthreads();
   const uint32_t e0 = blockIdx.x * p.per_block;
   const uint32_t e1 = p.total - e0 < p.per_block ? p.total : e0 + p.per_block;
   for (uint32_t e = e0 + threadIdx.x; e < e1; e += SORT_THREADS)
     atomicAdd(&hist[(key_of(s, p, e) >> p.shift) & p.mask], 1u);
+  if (!p.key_in) {
+    for (uint64_t i = (uint64_t)blockIdx.x * SORT_THREADS + threadIdx.x; i < p.keys; i += (uint64_t)gridDim.x * SORT_THREADS)
+      p.run[2 * i] = NO_ENTRY;
+  }
   __syncthreads();
   const uint32_t wave = threadIdx.x / 64, lane = threadIdx.x % 64;
   for (uint32_t g = wave; g < p.groups; g += SORT_THREADS / 64) {
@@ -158,33 +174,36 @@ __global__ __launch_bounds__(SORT_THREADS) void k_count(KSel s, KPass p) {
     const uint32_t v = b < p.bins ? hist[b] : 0u;
     if (b < p.bins) p.cnt[(size_t)blockIdx.x * p.bins + b] = v;
     const uint32_t sum = wave_sum(v);
-    if (lane == 0) p.coarse[(size_t)blockIdx.x * p.groups + g] = sum;
+    if (lane == 0) p.coarse[(size_t)g * p.blocks + blockIdx.x] = sum;
   }
 }
 
 // Workgroup g: places of the GROUP bins from g * GROUP on.  Sixteen waves
 // share the blocks; a lane is a bin.
-__global__ __launch_bounds__(SORT_THREADS) void k_scan(KPass p) {
+__global__ __launch_bounds__(SORT_THREADS) void k_scan(KPasses ps) {
   __shared__ uint32_t part[16][GROUP];
   __shared__ uint32_t before[16];
+  const KPass& p = ps.p[blockIdx.y];
   const uint32_t wave = threadIdx.x / 64, lane = threadIdx.x % 64, g = blockIdx.x;
-  uint32_t lower = 0;     // entries of the bins below this group
-  for (uint32_t b = wave; b < p.blocks; b += 16)
-    for (uint32_t c = lane; c < g; c += 64) lower += p.coarse[(size_t)b * p.groups + c];
-  lower = wave_sum(lower);
-  if (lane == 0) before[wave] = lower;
+  if (g >= p.groups) return;
   const uint32_t bin = g * GROUP + lane;
   const uint32_t per = (p.blocks + 15) / 16;
   const uint32_t b0 = wave * per < p.blocks ? wave * per : p.blocks;
   const uint32_t b1 = b0 + per < p.blocks ? b0 + per : p.blocks;
   uint32_t v[16];         // at most 256 blocks
+#pragma unroll
+  for (uint32_t i = 0; i < 16; ++i)
+    v[i] = (b0 + i < b1 && bin < p.bins) ? p.cnt[(size_t)(b0 + i) * p.bins + bin] : 0u;
+  uint32_t lower = 0;     // entries of the bins below this group
+  const uint32_t n = g * p.blocks;
+#pragma unroll 8
+  for (uint32_t i = threadIdx.x; i < n; i += SORT_THREADS) lower += p.coarse[i];
   uint32_t sum = 0;
 #pragma unroll
-  for (uint32_t i = 0; i < 16; ++i) {
-    v[i] = (b0 + i < b1 && bin < p.bins) ? p.cnt[(size_t)(b0 + i) * p.bins + bin] : 0u;
-    sum += v[i];
-  }
+  for (uint32_t i = 0; i < 16; ++i) sum += v[i];
   part[wave][lane] = sum;
+  lower = wave_sum(lower);
+  if (lane == 0) before[wave] = lower;
   __syncthreads();
   uint32_t base = 0, own = 0, all = 0;
 #pragma unroll
@@ -208,9 +227,10 @@ __global__ __launch_bounds__(SORT_THREADS) void k_scan(KPass p) {
 }
 
 template <class T>
-__global__ __launch_bounds__(SORT_THREADS) void k_place(KSel s, KPass p, const T* __restrict__ coef,
+__global__ __launch_bounds__(SORT_THREADS) void k_place(KSel s, KPasses ps, const T* __restrict__ coef,
                                                         const T* __restrict__ gate) {
   extern __shared__ uint32_t taken[];     // entries of each bin that the block has placed
+  const KPass& p = ps.p[blockIdx.y];
   for (uint32_t i = threadIdx.x; i < p.bins; i += SORT_THREADS) taken[i] = 0;
   __syncthreads();
   const uint32_t wave = threadIdx.x / 64, lane = threadIdx.x % 64;
@@ -219,8 +239,25 @@ __global__ __launch_bounds__(SORT_THREADS) void k_place(KSel s, KPass p, const T
   for (uint32_t c = e0; c < e1; c += SORT_THREADS) {
     const uint32_t e = c + threadIdx.x;
     const bool in = e < e1;
-    const uint32_t key = in ? key_of(s, p, e) : 0u;
+    uint32_t key = 0, pos = e, other = 0;
+    float w = 0.f;
+    if (in) {
+      if (p.key_in) {
+        key = p.key_in[e];
+        pos = p.pos_in[e];
+      }
+      if (!p.key_in || p.last) {
+        uint32_t row = 0, latent = 0;
+        const bool good = entry_of(s, pos, s.idx[pos], &row, &latent);
+        if (!p.key_in) key = good ? (p.by_row ? row : latent) : p.keys;
+        if (good && p.last) {
+          other = p.by_row ? latent : row;
+          w = coef_of(coef, gate, pos);
+        }
+      }
+    }
     const uint32_t d = (key >> p.shift) & p.mask;
+    uint32_t at = in ? p.cnt[(size_t)blockIdx.x * p.bins + d] : 0u;
     uint64_t same = __ballot(in);
     for (uint32_t b = 0; b < p.digit_bits; ++b) {
       const bool bit = d >> b & 1u;
@@ -228,9 +265,9 @@ __global__ __launch_bounds__(SORT_THREADS) void k_place(KSel s, KPass p, const T
       same &= bit ? m : ~m;
     }
     const uint32_t rank = __popcll(same & ((uint64_t(1) << lane) - 1));
-    uint32_t at = in ? p.cnt[(size_t)blockIdx.x * p.bins + d] + rank : 0u;
-    for (uint32_t w = 0; w < SORT_THREADS / 64; ++w) {
-      if (w == wave && in) {
+    at += rank;
+    for (uint32_t w2 = 0; w2 < SORT_THREADS / 64; ++w2) {
+      if (w2 == wave && in) {
         const uint32_t t = taken[d];
         at += t;
         if (rank == 0) taken[d] = t + (uint32_t)__popcll(same);
@@ -238,88 +275,150 @@ __global__ __launch_bounds__(SORT_THREADS) void k_place(KSel s, KPass p, const T
       __syncthreads();
     }
     if (in) {
-      const uint32_t pos = p.key_in ? p.pos_in[e] : e;
       p.key_out[at] = key;
-      if (p.pos_out) {
-        p.pos_out[at] = pos;
-      } else {
-        uint32_t row = 0, latent = 0;
-        const bool good = entry_of(s, pos, s.idx[pos], &row, &latent);
-        p.other[at] = good ? (p.by_row ? latent : row) : 0u;
-        p.coef[at] = good ? coef_of(coef, gate, pos) : 0.f;
+      p.pos_out[at] = pos;
+      if (p.last) {
+        p.other[at] = other;
+        p.coef[at] = w;
       }
     }
   }
 }
 
 // ---------------------------------------------------------------- sums
-constexpr uint32_t ROWS_AHEAD = 8;      // rows of src in flight per wave
-
 struct KSeg {
   const uint32_t* skey;
+  const uint32_t* spos;
   const uint32_t* other;
   const float* coef;
+  uint32_t* run;        // [keys][2]
   const void* src;
   const void* bias;
-  void* out;
+  void* out;            // null: not wanted
   void* coef_sum;
+  const void* wsrc;     // dots: a row per key
+  void* dots;
   float* part;          // [chunks][2][d]: a run that came in, a run that goes on
   float* part_c;        // [chunks][2]
-  int64_t lds, ldo;
+  int64_t lds, ldo, ldw;
   uint32_t keys, total, chunk, d;
 };
 
-// A wave sums the chunk's entries for 64 VEC columns.  The entries' keys,
-// source rows and coefficients are wave-uniform (read from one lane), so a
-// row's address is scalar and a run's end a scalar branch.
-template <class T, int VEC>
-__global__ __launch_bounds__(256) void k_seg(KSeg p) {
+// A launch sums by row and by latent side by side (grid dimension z).
+struct KSegs {
+  KSeg s[2];
+};
+
+// One lane's share of a row: NV vectors of VEC elements, 64 VEC apart, kept as
+// they were read until they are used.
+template <class T, int VEC, int NV>
+struct Row {
+  u32x4 q[NV];
+  __device__ __forceinline__ void load(const T* p, uint32_t c, uint32_t d, bool there) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const uint32_t at = c + v * 64 * VEC;
+      q[v] = u32x4{0u, 0u, 0u, 0u};
+      if (there && at < d) {
+        if constexpr (VEC == 1) q[v][0] = __float_as_uint(to_f32(p[at]));
+        else q[v] = *reinterpret_cast<const u32x4*>(p + at);
+      }
+    }
+  }
+  __device__ __forceinline__ void unpack(int v, float* f) const {
+    if constexpr (VEC == 1) f[0] = __uint_as_float(q[v][0]);
+    else Vec<T>::unpack(q[v], f);
+  }
+};
+
+// Eight sums over 64 lanes: each of the first three exchanges halves the
+// number of sums a lane carries, so lane l ends with the sum of entry l % 8.
+__device__ __forceinline__ float eight_sums(float* sum, uint32_t lane) {
+#pragma unroll
+  for (uint32_t h = 4; h; h >>= 1) {
+    const bool up = lane & h;
+#pragma unroll
+    for (uint32_t u = 0; u < h; ++u) {
+      const float keep = up ? sum[u + h] : sum[u], give = up ? sum[u] : sum[u + h];
+      sum[u] = keep + __shfl_xor(give, h);
+    }
+  }
+  float v = sum[0];
+#pragma unroll
+  for (uint32_t o = 8; o < 64; o <<= 1) v += __shfl_xor(v, o);
+  return v;
+}
+
+// A wave sums the chunk's entries for 64 VEC NV columns, AHEAD rows of src in
+// flight.  The entries' keys, source rows and coefficients are wave-uniform
+// (read from one lane), so a row's address is scalar and a run's end a scalar
+// branch.  With DOTS the wave also takes each entry's dot product of its
+// source row and its key's row of wsrc, which neighbouring entries of a run
+// find in the first-level cache.
+template <class T, int VEC, int NV, int AHEAD, bool DOTS>
+__global__ __launch_bounds__(256) void k_seg(KSegs ss) {
+  const KSeg& p = ss.s[blockIdx.z];
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
   const uint32_t chunk = blockIdx.x * 4 + wave;
   const uint64_t first = (uint64_t)chunk * p.chunk;
   if (first >= p.total) return;
   const uint32_t e0 = (uint32_t)first;
   const uint32_t e1 = p.total - e0 < p.chunk ? p.total : e0 + p.chunk;
-  const uint32_t c = (blockIdx.y * 64 + lane) * VEC;
-  const bool in = c < p.d;
+  const uint32_t c = (blockIdx.y * 64 * NV + lane) * VEC;
+  const bool one = blockIdx.y == 0 && lane == 0;
   const T* src = static_cast<const T*>(p.src);
-  const uint32_t before = e0 ? p.skey[e0 - 1] : 0xFFFFFFFFu;
-  const uint32_t behind = e1 < p.total ? p.skey[e1] : 0xFFFFFFFFu;
-  float acc[VEC] = {}, csum = 0.f;
+  const T* wsrc = static_cast<const T*>(p.wsrc);
+  const uint32_t before = e0 ? p.skey[e0 - 1] : NO_ENTRY;
+  const uint32_t behind = e1 < p.total ? p.skey[e1] : NO_ENTRY;
+  float acc[NV][VEC] = {}, csum = 0.f;
   uint32_t cur = p.skey[e0];
   bool came = cur == before;
+  if (one && !came && cur < p.keys) p.run[2 * (size_t)cur] = e0;
 
-  auto flush = [&](bool goes) {
+  auto flush = [&](uint32_t end, bool goes) {   // `end`: the entry behind the run
     if (cur < p.keys) {
+      if (one && !goes) p.run[2 * (size_t)cur + 1] = end;
       if (came || goes) {
         const size_t slot = (size_t)chunk * 2 + (came ? 0 : 1);
-        if (in) {
-          float* o = p.part + slot * p.d + c;
-          if constexpr (VEC == 1) {
-            o[0] = acc[0];
-          } else {
+        if (p.out) {
+          float* o = p.part + slot * p.d;
 #pragma unroll
-            for (int i = 0; i < VEC; i += 4) Vec<float>::store(o + i, acc + i);
+          for (int v = 0; v < NV; ++v) {
+            const uint32_t at = c + v * 64 * VEC;
+            if (at >= p.d) continue;
+            if constexpr (VEC == 1) {
+              o[at] = acc[v][0];
+            } else {
+#pragma unroll
+              for (int i = 0; i < VEC; i += 4) Vec<float>::store(o + at + i, acc[v] + i);
+            }
           }
         }
-        if (p.coef_sum && lane == 0 && blockIdx.y == 0) p.part_c[slot] = csum;
+        if (p.coef_sum && one) p.part_c[slot] = csum;
       } else {
-        if (in) {
-          if (p.bias) {
-            float b[VEC];
-            load_vec<T, VEC>(static_cast<const T*>(p.bias) + c, b);
+        if (p.out) {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) acc[i] += b[i];
+          for (int v = 0; v < NV; ++v) {
+            const uint32_t at = c + v * 64 * VEC;
+            if (at >= p.d) continue;
+            if (p.bias) {
+              float b[VEC];
+              load_vec<T, VEC>(static_cast<const T*>(p.bias) + at, b);
+#pragma unroll
+              for (int i = 0; i < VEC; ++i) acc[v][i] += b[i];
+            }
+            store_vec<T, VEC>(static_cast<T*>(p.out) + (int64_t)cur * p.ldo + at, acc[v]);
           }
-          store_vec<T, VEC>(static_cast<T*>(p.out) + (int64_t)cur * p.ldo + c, acc);
         }
-        if (p.coef_sum && lane == 0 && blockIdx.y == 0) static_cast<T*>(p.coef_sum)[cur] = from_f32<T>(csum);
+        if (p.coef_sum && one) static_cast<T*>(p.coef_sum)[cur] = from_f32<T>(csum);
       }
     }
     came = false;
     csum = 0.f;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) acc[i] = 0.f;
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) acc[v][i] = 0.f;
   };
 
   for (uint32_t b = e0; b < e1; b += 64) {
@@ -328,89 +427,100 @@ __global__ __launch_bounds__(256) void k_seg(KSeg p) {
     const uint32_t lk = mine ? p.skey[b + lane] : p.keys;
     const uint32_t lo = mine ? p.other[b + lane] : 0u;
     const float lc = mine ? p.coef[b + lane] : 0.f;
-    for (uint32_t i0 = 0; i0 < have; i0 += ROWS_AHEAD) {
-      float row[ROWS_AHEAD][VEC];
+    for (uint32_t i0 = 0; i0 < have; i0 += AHEAD) {
+      Row<T, VEC, NV> row[AHEAD], wrow[DOTS ? AHEAD : 1];
 #pragma unroll
-      for (uint32_t u = 0; u < ROWS_AHEAD; ++u) {
-        const uint32_t o = __builtin_amdgcn_readlane(lo, i0 + u);   // i0 + u < 64; lanes beyond `have` hold row 0
+      for (uint32_t u = 0; u < AHEAD; ++u) {   // i0 + u < 64; lanes beyond `have` hold no key
+        const uint32_t o = __builtin_amdgcn_readlane(lo, i0 + u);
         const uint32_t k = __builtin_amdgcn_readlane(lk, i0 + u);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) row[u][i] = 0.f;
-        if (in && k < p.keys) load_vec<T, VEC>(src + (int64_t)o * p.lds + c, row[u]);
+        row[u].load(src + (int64_t)o * p.lds, c, p.d, k < p.keys);
+        if constexpr (DOTS) wrow[u].load(wsrc + (int64_t)k * p.ldw, c, p.d, k < p.keys);
       }
+      float dot[AHEAD];
 #pragma unroll
-      for (uint32_t u = 0; u < ROWS_AHEAD; ++u) {
-        if (i0 + u >= have) break;
+      for (uint32_t u = 0; u < AHEAD; ++u) {
         const uint32_t k = __builtin_amdgcn_readlane(lk, i0 + u);
         const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(lc), i0 + u));
-        if (k != cur) {
-          flush(false);
+        if (k != cur && i0 + u < have) {
+          flush(b + i0 + u, false);
           cur = k;
+          if (one && cur < p.keys) p.run[2 * (size_t)cur] = b + i0 + u;
         }
         csum += w;
+        dot[u] = 0.f;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) acc[i] = fmaf(w, row[u][i], acc[i]);
+        for (int v = 0; v < NV; ++v) {
+          float f[VEC];
+          row[u].unpack(v, f);
+          if constexpr (DOTS) {
+            float g[VEC];
+            wrow[u].unpack(v, g);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) dot[u] = fmaf(f[i], g[i], dot[u]);
+          }
+          // (an entry behind the end has weight and row 0)
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) acc[v][i] = fmaf(w, f[i], acc[v][i]);
+        }
+      }
+      if constexpr (DOTS) {
+        static_assert(AHEAD == 8, "eight_sums");
+        const float v = eight_sums(dot, lane);
+        if (lane < AHEAD && i0 + lane < have) static_cast<T*>(p.dots)[p.spos[b + i0 + lane]] = from_f32<T>(v);
       }
     }
   }
-  flush(behind == cur);
+  flush(e1, behind == cur);
 }
 
-// First entry whose key is at least `key`.
-__device__ __forceinline__ uint32_t lower_bound(const uint32_t* __restrict__ skey, uint32_t total, uint32_t key) {
-  uint32_t lo = 0, hi = total;
-  while (lo < hi) {
-    const uint32_t mid = (lo + hi) / 2;
-    if (skey[mid] < key) lo = mid + 1;
-    else hi = mid;
-  }
-  return lo;
-}
-
-// Writes the keys without an entry, and joins the runs of several chunks: 64
+// Writes the keys without an entry, and joins the runs of several chunks: 16
 // keys per workgroup, a wave per key.
-constexpr uint32_t JOIN_KEYS = 64;
+constexpr uint32_t JOIN_KEYS = 16;
 
 template <class T, int VEC>
-__global__ __launch_bounds__(256) void k_join_runs(KSeg p) {
-  __shared__ uint32_t start[JOIN_KEYS + 1];
-  const uint32_t k0 = blockIdx.x * JOIN_KEYS;
-  if (threadIdx.x <= JOIN_KEYS) {
-    const uint32_t k = k0 + threadIdx.x;
-    start[threadIdx.x] = lower_bound(p.skey, p.total, k < p.keys ? k : p.keys);
-  }
-  __syncthreads();
+__global__ __launch_bounds__(256) void k_join_runs(KSegs ss) {
+  const KSeg& p = ss.s[blockIdx.z];
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
+  uint32_t first = NO_ENTRY, end = 0;     // lane i: the workgroup's key i
+  const uint64_t k0 = (uint64_t)blockIdx.x * JOIN_KEYS;
+  if (p.total && lane < JOIN_KEYS && k0 + lane < p.keys) {
+    first = p.run[2 * (k0 + lane)];
+    end = p.run[2 * (k0 + lane) + 1];
+  }
   for (uint32_t i = wave; i < JOIN_KEYS && k0 + i < p.keys; i += 4) {
-    const uint32_t key = k0 + i;
-    const uint32_t lo = __builtin_amdgcn_readfirstlane(start[i]), hi = __builtin_amdgcn_readfirstlane(start[i + 1]);
-    const uint32_t q0 = lo / p.chunk, q1 = hi > lo ? (hi - 1) / p.chunk : q0;
-    if (hi > lo && q0 == q1) continue;     // written by its chunk
-    for (uint32_t c = lane * VEC; c < p.d; c += 64 * VEC) {
-      float acc[VEC] = {};
-      if (hi > lo) {
-        const float* a = p.part + ((size_t)q0 * 2 + 1) * p.d + c;
+    const uint64_t key = k0 + i;
+    const uint32_t lo = __builtin_amdgcn_readlane(first, i), hi = __builtin_amdgcn_readlane(end, i);
+    const bool none = lo == NO_ENTRY;
+    const uint32_t q0 = none ? 0u : lo / p.chunk, q1 = none ? 0u : (hi - 1) / p.chunk;
+    if (!none && q0 == q1) continue;     // written by its chunk
+    if (p.out) {
+      for (uint32_t c = lane * VEC; c < p.d; c += 64 * VEC) {
+        float acc[VEC] = {};
+        if (!none) {
+          const float* a = p.part + ((size_t)q0 * 2 + 1) * p.d + c;
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) acc[j] = a[j];
-#pragma unroll 4
-        for (uint32_t q = q0 + 1; q <= q1; ++q) {
-          const float* b = p.part + (size_t)q * 2 * p.d + c;
+          for (int j = 0; j < VEC; ++j) acc[j] = a[j];
+#pragma unroll 8
+          for (uint32_t q = q0 + 1; q <= q1; ++q) {
+            const float* b = p.part + (size_t)q * 2 * p.d + c;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) acc[j] += b[j];
+          }
+        }
+        if (p.bias) {
+          float b[VEC];
+          load_vec<T, VEC>(static_cast<const T*>(p.bias) + c, b);
 #pragma unroll
           for (int j = 0; j < VEC; ++j) acc[j] += b[j];
         }
+        store_vec<T, VEC>(static_cast<T*>(p.out) + (int64_t)key * p.ldo + c, acc);
       }
-      if (p.bias) {
-        float b[VEC];
-        load_vec<T, VEC>(static_cast<const T*>(p.bias) + c, b);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) acc[j] += b[j];
-      }
-      store_vec<T, VEC>(static_cast<T*>(p.out) + (int64_t)key * p.ldo + c, acc);
     }
     if (p.coef_sum && lane == 0) {
       float s = 0.f;
-      if (hi > lo) {
+      if (!none) {
         s = p.part_c[(size_t)q0 * 2 + 1];
+#pragma unroll 8
         for (uint32_t q = q0 + 1; q <= q1; ++q) s += p.part_c[(size_t)q * 2];
       }
       static_cast<T*>(p.coef_sum)[key] = from_f32<T>(s);
@@ -424,6 +534,7 @@ __global__ __launch_bounds__(256) void k_join_runs(KSeg p) {
 // index, 256 at a time, and keeps those of its row, in order, in LDS.  The
 // waves' sums are joined in wave order.
 constexpr uint32_t KEEP = 1024;        // entries held in LDS
+constexpr uint32_t ROWS_AHEAD = 8;     // rows of src in flight per wave
 
 template <class T, int VEC>
 __global__ __launch_bounds__(256) void k_rows(KSel s, KSeg p, const T* __restrict__ coef,
@@ -532,20 +643,7 @@ __global__ __launch_bounds__(256) void k_dots(KSel s, const T* __restrict__ g, i
 #pragma unroll
       for (int i = 0; i < VEC; ++i) sum[u] = fmaf(a[u][i], b[u][i], sum[u]);
   }
-  // eight sums over 64 lanes: each of the first three exchanges halves the
-  // number of sums a lane carries, so lane l ends with the sum of entry l % 8
-#pragma unroll
-  for (uint32_t h = 4, o = 4; h; h >>= 1, o >>= 1) {
-    const bool up = lane & o;
-#pragma unroll
-    for (uint32_t u = 0; u < h; ++u) {
-      const float keep = up ? sum[u + h] : sum[u], give = up ? sum[u] : sum[u + h];
-      sum[u] = keep + __shfl_xor(give, o);
-    }
-  }
-  float v = sum[0];
-#pragma unroll
-  for (uint32_t o = 8; o < 64; o <<= 1) v += __shfl_xor(v, o);
+  const float v = eight_sums(sum, lane);
   if (lane < DOTS && e0 + lane < s.total) dv[e0 + lane] = from_f32<T>(v);
 }
 
@@ -573,9 +671,8 @@ struct SegPlan {
 SegPlan seg_plan(const Selection& s, int64_t d, bool by_row) {
   SegPlan p;
   p.sort = sort_plan(by_row ? s.rows : s.n, s.total);
-  const int64_t columns = std::max<int64_t>(1, ceil_div(d, 512));
   int64_t chunk = 64;
-  while (chunk > 8 && ceil_div(s.total, chunk) * columns < 2048) chunk /= 2;
+  while (chunk > 16 && ceil_div(s.total, chunk) < 2048) chunk /= 2;
   chunk *= std::max<int64_t>(1, ceil_div(s.total, chunk * 16384));
   p.chunk = (uint32_t)chunk;
   p.chunks = (uint32_t)ceil_div(s.total, chunk);
@@ -585,39 +682,53 @@ SegPlan seg_plan(const Selection& s, int64_t d, bool by_row) {
   return p;
 }
 
+// The sorts of one or two parts: their first passes share launches.
 template <class T>
-hipError_t run_sort(const SegArgs& a, const SortPlan& p, char* ws, hipStream_t s) {
+hipError_t run_sorts(const SegCall& a, const SegArgs* const* parts, const SegPlan* plans, char* const* ws, int n,
+                     hipStream_t s) {
   const KSel sel = ksel(a.sel);
   const T* coef = static_cast<const T*>(a.coef);
   const T* gate = static_cast<const T*>(a.gate);
-  for (uint32_t pass = 0; pass < p.passes; ++pass) {
-    KPass k;
-    const bool last = pass + 1 == p.passes;
-    uint32_t* keys = reinterpret_cast<uint32_t*>(ws + p.off_key);
-    uint32_t* pos = reinterpret_cast<uint32_t*>(ws + p.off_pos);
-    k.key_in = pass ? keys + (size_t)((pass - 1) & 1) * p.total : nullptr;
-    k.pos_in = pass ? pos + (size_t)((pass - 1) & 1) * p.total : nullptr;
-    k.key_out = last ? reinterpret_cast<uint32_t*>(ws + p.off_skey) : keys + (size_t)(pass & 1) * p.total;
-    k.pos_out = last ? nullptr : pos + (size_t)(pass & 1) * p.total;
-    k.other = reinterpret_cast<uint32_t*>(ws + p.off_other);
-    k.coef = reinterpret_cast<float*>(ws + p.off_coef);
-    k.cnt = reinterpret_cast<uint32_t*>(ws + p.off_cnt);
-    k.coarse = reinterpret_cast<uint32_t*>(ws + p.off_coarse);
-    k.keys = p.keys;
-    k.total = p.total;
-    k.per_block = p.per_block;
-    k.bins = bins_of(p, pass);
-    k.groups = (uint32_t)ceil_div(k.bins, GROUP);
-    k.shift = p.width * pass;
-    k.mask = p.width ? (1u << p.width) - 1 : 0xFFFFFFFFu;
-    k.digit_bits = 0;
-    while ((1u << k.digit_bits) < k.bins) ++k.digit_bits;
-    k.blocks = p.blocks;
-    k.by_row = a.by_row;
-    const size_t lds = (size_t)k.bins * 4;
-    hipLaunchKernelGGL(k_count, dim3(p.blocks), dim3(SORT_THREADS), lds, s, sel, k);
-    hipLaunchKernelGGL(k_scan, dim3(k.groups), dim3(SORT_THREADS), 0, s, k);
-    hipLaunchKernelGGL((k_place<T>), dim3(p.blocks), dim3(SORT_THREADS), lds, s, sel, k, coef, gate);
+  uint32_t most = 0;
+  for (int i = 0; i < n; ++i) most = std::max(most, plans[i].sort.passes);
+  for (uint32_t pass = 0; pass < most; ++pass) {
+    KPasses ks;
+    uint32_t y = 0, groups = 0, bins = 0, blocks = 0;
+    for (int i = 0; i < n; ++i) {
+      const SortPlan& p = plans[i].sort;
+      if (pass >= p.passes) continue;
+      KPass& k = ks.p[y++];
+      uint32_t* keys = reinterpret_cast<uint32_t*>(ws[i] + p.off_key);
+      uint32_t* pos = reinterpret_cast<uint32_t*>(ws[i] + p.off_pos);
+      k.last = pass + 1 == p.passes;
+      k.key_in = pass ? keys + (size_t)((pass - 1) & 1) * p.total : nullptr;
+      k.pos_in = pass ? pos + (size_t)((pass - 1) & 1) * p.total : nullptr;
+      k.key_out = k.last ? reinterpret_cast<uint32_t*>(ws[i] + p.off_skey) : keys + (size_t)(pass & 1) * p.total;
+      k.pos_out = k.last ? reinterpret_cast<uint32_t*>(ws[i] + p.off_spos) : pos + (size_t)(pass & 1) * p.total;
+      k.other = reinterpret_cast<uint32_t*>(ws[i] + p.off_other);
+      k.coef = reinterpret_cast<float*>(ws[i] + p.off_coef);
+      k.cnt = reinterpret_cast<uint32_t*>(ws[i] + p.off_cnt);
+      k.coarse = reinterpret_cast<uint32_t*>(ws[i] + p.off_coarse);
+      k.run = reinterpret_cast<uint32_t*>(ws[i] + p.off_run);
+      k.keys = p.keys;
+      k.total = p.total;
+      k.per_block = p.per_block;
+      k.bins = bins_of(p, pass);
+      k.groups = (uint32_t)ceil_div(k.bins, GROUP);
+      k.shift = p.width * pass;
+      k.mask = p.width ? (1u << p.width) - 1 : 0xFFFFFFFFu;
+      k.digit_bits = 0;
+      while ((1u << k.digit_bits) < k.bins) ++k.digit_bits;
+      k.blocks = blocks = p.blocks;     // the same for both: it follows from the entries
+      k.by_row = parts[i]->by_row;
+      groups = std::max(groups, k.groups);
+      bins = std::max(bins, k.bins);
+    }
+    if (y == 1) ks.p[1] = ks.p[0];
+    const size_t lds = (size_t)bins * 4;
+    hipLaunchKernelGGL(k_count, dim3(blocks, y), dim3(SORT_THREADS), lds, s, sel, ks);
+    hipLaunchKernelGGL(k_scan, dim3(groups, y), dim3(SORT_THREADS), 0, s, ks);
+    hipLaunchKernelGGL((k_place<T>), dim3(blocks, y), dim3(SORT_THREADS), lds, s, sel, ks, coef, gate);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -625,50 +736,109 @@ hipError_t run_sort(const SegArgs& a, const SortPlan& p, char* ws, hipStream_t s
 }
 
 template <class T>
-hipError_t run_seg(const SegArgs& a, char* ws, hipStream_t s) {
-  constexpr int64_t ES = sizeof(T), V = Vec<T>::N;
-  const bool wide = a.d % V == 0 && aligned16(a.src, a.lds, ES) && aligned16(a.out, a.ldo, ES) && aligned16(a.bias, 0, ES);
-  const int64_t span = 64 * (wide ? V : 1);
-  const uint32_t columns = (uint32_t)std::max<int64_t>(1, ceil_div(a.d, span));
-  KSeg k;
-  k.src = a.src;
-  k.bias = a.bias;
-  k.out = a.out;
-  k.coef_sum = a.coef_sum;
-  k.lds = a.lds;
-  k.ldo = a.ldo;
-  k.keys = (uint32_t)(a.by_row ? a.sel.rows : a.sel.n);
-  k.total = (uint32_t)a.sel.total;
-  k.d = (uint32_t)a.d;
-  if (a.by_row && rows_direct(a.sel)) {
-    const dim3 grid(k.keys, columns);
-    const T* coef = static_cast<const T*>(a.coef);
-    const T* gate = static_cast<const T*>(a.gate);
-    if (wide) hipLaunchKernelGGL((k_rows<T, (int)V>), grid, dim3(256), 0, s, ksel(a.sel), k, coef, gate);
-    else hipLaunchKernelGGL((k_rows<T, 1>), grid, dim3(256), 0, s, ksel(a.sel), k, coef, gate);
-    return hipGetLastError();
+bool wide_part(const SegArgs& a, int64_t d) {
+  constexpr int64_t ES = sizeof(T);
+  return d % Vec<T>::N == 0 && aligned16(a.src, a.lds, ES) && aligned16(a.out, a.ldo, ES) && aligned16(a.bias, 0, ES) &&
+         aligned16(a.other, a.ldother, ES);
+}
+
+template <class T>
+hipError_t launch_sums(const KSegs& ks, int n, bool wide, uint32_t chunks, int64_t d, bool dots, hipStream_t s) {
+  constexpr int V = Vec<T>::N;
+  const int64_t span = 64 * (wide ? V : 1), vecs = std::max<int64_t>(1, ceil_div(d, span));
+  if (chunks) {
+    const uint32_t x = (uint32_t)ceil_div(chunks, 4);
+    if (dots && vecs == 1) hipLaunchKernelGGL((k_seg<T, V, 1, 8, true>), dim3(x, 1, n), dim3(256), 0, s, ks);
+    else if (dots) hipLaunchKernelGGL((k_seg<T, V, 2, 8, true>), dim3(x, 1, n), dim3(256), 0, s, ks);
+    else if (wide) hipLaunchKernelGGL((k_seg<T, V, 1, 16, false>), dim3(x, (uint32_t)vecs, n), dim3(256), 0, s, ks);
+    else hipLaunchKernelGGL((k_seg<T, 1, 1, 16, false>), dim3(x, (uint32_t)vecs, n), dim3(256), 0, s, ks);
   }
-  const SegPlan p = seg_plan(a.sel, a.d, a.by_row);
-  const SortPlan& q = p.sort;
+  uint32_t keys = ks.s[0].keys;
+  if (n > 1) keys = std::max(keys, ks.s[1].keys);
+  const dim3 grid((uint32_t)ceil_div(keys, JOIN_KEYS), 1, n);
+  if (wide) hipLaunchKernelGGL((k_join_runs<T, V>), grid, dim3(256), 0, s, ks);
+  else hipLaunchKernelGGL((k_join_runs<T, 1>), grid, dim3(256), 0, s, ks);
+  return hipGetLastError();
+}
+
+template <class T>
+hipError_t run_seg(const SegCall& a, char* ws, hipStream_t s) {
+  constexpr int64_t V = Vec<T>::N;
+  const SegArgs* sorted[2];
+  SegPlan plans[2];
+  char* at[2];
+  KSegs ks;
+  int n = 0;
+  bool wide = true, dots = false;
+  for (int i = 0; i < a.parts; ++i) {
+    const SegArgs& p = a.part[i];
+    const int64_t keys = p.by_row ? a.sel.rows : a.sel.n;
+    const bool own_wide = wide_part<T>(p, a.d);
+    KSeg k{};
+    k.src = p.src;
+    k.bias = p.bias;
+    k.out = p.out;
+    k.coef_sum = p.coef_sum;
+    k.lds = p.lds;
+    k.ldo = p.ldo;
+    k.keys = (uint32_t)keys;
+    k.total = (uint32_t)a.sel.total;
+    k.d = (uint32_t)a.d;
+    if (p.dots) {
+      // fused where a lane holds its whole share of both rows
+      if (own_wide && a.d <= 128 * V && a.sel.total) {
+        dots = true;
+        k.wsrc = p.other;
+        k.ldw = p.ldother;
+        k.dots = p.dots;
+      } else {
+        DotArgs q;
+        q.sel = a.sel;
+        q.g = p.src;
+        q.ldg = p.lds;
+        q.w = p.other;
+        q.ldw = p.ldother;
+        q.d = a.d;
+        q.dv = p.dots;
+        const hipError_t e = launch_dots(q, s);
+        if (e != hipSuccess) return e;
+      }
+    }
+    if (keys == 0 || ((a.d == 0 || !p.out) && !p.coef_sum && !k.dots)) continue;
+    if (p.by_row && rows_direct(a.sel)) {
+      const uint32_t columns = (uint32_t)ceil_div(a.d, 64 * (own_wide ? V : 1));
+      const dim3 grid(k.keys, columns);
+      const T* coef = static_cast<const T*>(a.coef);
+      const T* gate = static_cast<const T*>(a.gate);
+      if (own_wide) hipLaunchKernelGGL((k_rows<T, (int)V>), grid, dim3(256), 0, s, ksel(a.sel), k, coef, gate);
+      else hipLaunchKernelGGL((k_rows<T, 1>), grid, dim3(256), 0, s, ksel(a.sel), k, coef, gate);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+      continue;
+    }
+    plans[n] = seg_plan(a.sel, a.d, p.by_row);
+    const SortPlan& q = plans[n].sort;
+    k.skey = reinterpret_cast<const uint32_t*>(ws + q.off_skey);
+    k.spos = reinterpret_cast<const uint32_t*>(ws + q.off_spos);
+    k.other = reinterpret_cast<const uint32_t*>(ws + q.off_other);
+    k.coef = reinterpret_cast<const float*>(ws + q.off_coef);
+    k.run = reinterpret_cast<uint32_t*>(ws + q.off_run);
+    k.part = reinterpret_cast<float*>(ws + plans[n].off_part);
+    k.part_c = reinterpret_cast<float*>(ws + plans[n].off_part_c);
+    k.chunk = plans[n].chunk;
+    wide = wide && own_wide;
+    sorted[n] = &p;
+    at[n] = ws;
+    ks.s[n++] = k;
+    ws += plans[n - 1].total;
+  }
+  if (!n) return hipSuccess;
+  if (n == 1) ks.s[1] = ks.s[0];
   if (a.sel.total) {
-    const hipError_t e = run_sort<T>(a, q, ws, s);
+    const hipError_t e = run_sorts<T>(a, sorted, plans, at, n, s);
     if (e != hipSuccess) return e;
   }
-  k.skey = reinterpret_cast<const uint32_t*>(ws + q.off_skey);
-  k.other = reinterpret_cast<const uint32_t*>(ws + q.off_other);
-  k.coef = reinterpret_cast<const float*>(ws + q.off_coef);
-  k.part = reinterpret_cast<float*>(ws + p.off_part);
-  k.part_c = reinterpret_cast<float*>(ws + p.off_part_c);
-  k.chunk = p.chunk;
-  if (p.chunks) {
-    const dim3 grid((uint32_t)ceil_div(p.chunks, 4), columns);
-    if (wide) hipLaunchKernelGGL((k_seg<T, (int)V>), grid, dim3(256), 0, s, k);
-    else hipLaunchKernelGGL((k_seg<T, 1>), grid, dim3(256), 0, s, k);
-  }
-  const dim3 grid((uint32_t)ceil_div(k.keys, JOIN_KEYS));
-  if (wide) hipLaunchKernelGGL((k_join_runs<T, (int)V>), grid, dim3(256), 0, s, k);
-  else hipLaunchKernelGGL((k_join_runs<T, 1>), grid, dim3(256), 0, s, k);
-  return hipGetLastError();
+  return launch_sums<T>(ks, n, wide, plans[0].chunks, a.d, dots, s);
 }
 
 template <class T>
@@ -686,14 +856,14 @@ hipError_t run_dots(const DotArgs& a, hipStream_t s) {
 
 }  // namespace
 
-size_t seg_workspace(const Selection& sel, int64_t d, bool by_row) {
-  if (by_row && rows_direct(sel)) return 0;
-  return seg_plan(sel, d, by_row).total;
+size_t seg_workspace(const Selection& sel, int64_t d, bool by_row, bool by_latent) {
+  size_t bytes = 0;
+  if (by_row && !rows_direct(sel)) bytes += seg_plan(sel, d, true).total;
+  if (by_latent) bytes += seg_plan(sel, d, false).total;
+  return bytes;
 }
 
-hipError_t launch_seg(const SegArgs& a, void* ws, hipStream_t s) {
-  const int64_t keys = a.by_row ? a.sel.rows : a.sel.n;
-  if (keys == 0 || (a.d == 0 && !a.coef_sum)) return hipSuccess;
+hipError_t launch_seg(const SegCall& a, void* ws, hipStream_t s) {
   return a.sel.dtype == DT_BF16 ? run_seg<bf16_t>(a, static_cast<char*>(ws), s)
                                 : run_seg<float>(a, static_cast<char*>(ws), s);
 }
