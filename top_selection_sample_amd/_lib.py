@@ -81,6 +81,11 @@ class LinearArgs(ctypes.Structure):
                 + [(f, ctypes.c_int32) for f in ("dtype", "act", "x_trans", "w_trans")])
 
 
+# the same layouts for struct.pack: a third of a ctypes structure's time
+LINEAR_FORMAT = "6Q8q4i"
+SELECTION_FORMAT = "2Q3q2i"
+
+
 class LinearGradArgs(ctypes.Structure):
     _fields_ = ([(f, ctypes.c_void_p) for f in ("dy", "pre", "x", "w", "dx", "dw", "db")]
                 + [(f, ctypes.c_int64) for f in ("m", "n", "k", "ldd", "ldp", "ldx", "ldw", "lddx",
@@ -115,14 +120,14 @@ def _load():
     L.topk_filter_trace.argtypes = [ctypes.c_void_p, ctypes.c_size_t]
     L.topk_stream_read.argtypes = [vp, sz, vp, vp]
     L.topk_scatter.argtypes = [vp, vp, i64, i64, i64, i32, vp, vp, vp]
-    L.topk_linear_workspace_size.argtypes = [P(LinearArgs), P(sz)]
-    L.topk_linear.argtypes = [P(LinearArgs), vp, sz, vp]
+    L.topk_linear_workspace_size.argtypes = [vp, P(sz)]
+    L.topk_linear.argtypes = [vp, vp, sz, vp]        # the structs by address, or packed into bytes
     L.topk_linear_grad_workspace_size.argtypes = [P(LinearGradArgs), P(sz)]
     L.topk_linear_grad.argtypes = [P(LinearGradArgs), vp, sz, vp]
-    L.topk_decode_workspace_size.argtypes = [P(Selection), i64, P(sz)]
-    L.topk_decode.argtypes = [P(Selection), vp, i64, i64, vp, vp, i64, vp, sz, vp]
-    L.topk_decode_grad.argtypes = [P(Selection), vp, i64, i64, vp, i64, vp, vp, i64, vp, vp, sz, vp]
-    L.topk_encode_grad.argtypes = [P(Selection), vp, vp, i64, vp, i64, i64, vp, i64, vp, i64, vp, vp,
+    L.topk_decode_workspace_size.argtypes = [vp, i64, P(sz)]
+    L.topk_decode.argtypes = [vp, vp, i64, i64, vp, vp, i64, vp, sz, vp]
+    L.topk_decode_grad.argtypes = [vp, vp, i64, i64, vp, i64, vp, vp, i64, vp, vp, sz, vp]
+    L.topk_encode_grad.argtypes = [vp, vp, vp, i64, vp, i64, i64, vp, i64, vp, i64, vp, vp,
                                    sz, vp]
     L.topk_grad_norm_workspace_size.argtypes = [i64, vp, P(sz)]   # host arrays by address
     L.topk_grad_norm.argtypes = [vp, vp, vp, i64, vp, vp, sz, vp]

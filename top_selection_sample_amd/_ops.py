@@ -9,8 +9,10 @@ different streams, and captured graphs, never share any.
 from __future__ import annotations
 
 import ctypes
+import struct
 from array import array
 from contextlib import nullcontext
+from operator import attrgetter
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -20,6 +22,9 @@ from . import _lib
 _CODES = {torch.float32: 1, torch.bfloat16: 2}
 _byref = ctypes.byref
 _T = torch.Tensor
+_pack_linear = struct.Struct(_lib.LINEAR_FORMAT).pack
+_pack_selection = struct.Struct(_lib.SELECTION_FORMAT).pack
+_dtype_of = attrgetter("dtype")
 
 
 def _code(t: torch.Tensor, what: str) -> int:
@@ -60,7 +65,7 @@ def _scratch(nbytes: int, like):
 
 
 def _ptr(t):
-    return t.data_ptr() if t is not None else None
+    return t.data_ptr() if t is not None else 0
 
 
 def _matrix(t: torch.Tensor, either: bool = False):
@@ -113,12 +118,15 @@ def _linear_run(x, w, bias, act, residual, want_pre):
     with _on(dev):
         y = x.new_empty((m, n))
         pre = x.new_empty((m, n)) if want_pre else None
-        a = _lib.LinearArgs(x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(residual), y.data_ptr(),
-                            _ptr(pre), m, n, k, ldx, ldw, ldr, n, n, _CODES[x.dtype], act, xt, wt)
-        size = ctypes.c_size_t()
-        _lib.check(_lib.lib.topk_linear_workspace_size(_byref(a), _byref(size)), "linear")
-        ws = _scratch(size.value, x)
-        _lib.check(_lib.lib.topk_linear(_byref(a), _ptr(ws), size.value, _stream(dev)), "linear")
+        a = _pack_linear(x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(residual), y.data_ptr(), _ptr(pre),
+                         m, n, k, ldx, ldw, ldr, n, n, _CODES[x.dtype], act, xt, wt)
+        stream = _stream(dev)
+        # few rows need no scratch: ask only when the call says so
+        if m > 32 or _lib.lib.topk_linear(a, None, 0, stream) != _lib.TOPK_OK:
+            size = ctypes.c_size_t()
+            _lib.check(_lib.lib.topk_linear_workspace_size(a, _byref(size)), "linear")
+            ws = _scratch(size.value, x)
+            _lib.check(_lib.lib.topk_linear(a, _ptr(ws), size.value, stream), "linear")
     return y, pre
 
 
@@ -239,18 +247,17 @@ def linear_grad(grad: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, activ
 
 # ---------------------------------------------------------------- decode
 def _selection(values, indices, rows, n):
-    """The selection's struct: 1-D values with rows = 1, or [rows, k], hold
-    latents; 1-D values of more rows hold flattened places."""
+    """The selection's struct: [rows, k] values hold latents, 1-D ones flattened places."""
     if values.dim() == 2:
-        return _lib.Selection(values.data_ptr(), indices.data_ptr(), values.shape[0], values.shape[1], n,
-                              0, _CODES[values.dtype])
-    return _lib.Selection(values.data_ptr(), indices.data_ptr(), rows, values.shape[0], n, 1,
-                          _CODES[values.dtype])
+        return _pack_selection(values.data_ptr(), indices.data_ptr(), values.shape[0], values.shape[1], n, 0,
+                               _CODES[values.dtype])
+    return _pack_selection(values.data_ptr(), indices.data_ptr(), rows, values.shape[0], n, 1,
+                           _CODES[values.dtype])
 
 
 def _decode_scratch(sel, d, like):
     size = ctypes.c_size_t()
-    _lib.check(_lib.lib.topk_decode_workspace_size(_byref(sel), d, _byref(size)), "decode")
+    _lib.check(_lib.lib.topk_decode_workspace_size(sel, d, _byref(size)), "decode")
     return _scratch(size.value, like), size.value
 
 
@@ -264,10 +271,12 @@ def _decode_run(values, indices, weight, rows, bias):
     with _on(dev):
         out = values.new_empty((rows, d))
         sel = _selection(values, indices, rows, n)
-        ws, size = _decode_scratch(sel, d, values)
-        _lib.check(_lib.lib.topk_decode(_byref(sel), weight.data_ptr(), ldw, d, _ptr(bias),
-                                        out.data_ptr(), max(d, 1), _ptr(ws), size, _stream(dev)),
-                   "decode")
+        stream = _stream(dev)
+        args = (sel, weight.data_ptr(), ldw, d, _ptr(bias), out.data_ptr(), d or 1)
+        # row-wise selections need no scratch: ask only when the call says so
+        if values.dim() != 2 or _lib.lib.topk_decode(*args, None, 0, stream) != _lib.TOPK_OK:
+            ws, size = _decode_scratch(sel, d, values)
+            _lib.check(_lib.lib.topk_decode(*args, _ptr(ws), size, stream), "decode")
     return out
 
 
@@ -286,7 +295,7 @@ def _decode_grad_run(grad, values, indices, weight, need):
             return dv, dw, db
         sel = _selection(values, indices, rows, n)
         ws, size = _decode_scratch(sel, d, values)
-        _lib.check(_lib.lib.topk_decode_grad(_byref(sel), weight.data_ptr(), ldw, d, grad.data_ptr(), ldg,
+        _lib.check(_lib.lib.topk_decode_grad(sel, weight.data_ptr(), ldw, d, grad.data_ptr(), ldg,
                                              _ptr(dv), _ptr(dw), max(d, 1), _ptr(db), _ptr(ws), size,
                                              _stream(dev)), "decode_grad")
     return dv, dw, db
@@ -380,7 +389,7 @@ def _encode_grad_run(grad_values, values, indices, x, weight, need):
             return dx, dw, db
         sel = _selection(values, indices, rows, n)
         ws, size = _decode_scratch(sel, d, values)
-        _lib.check(_lib.lib.topk_encode_grad(_byref(sel), grad_values.data_ptr(), x.data_ptr(), ldx,
+        _lib.check(_lib.lib.topk_encode_grad(sel, grad_values.data_ptr(), x.data_ptr(), ldx,
                                              weight.data_ptr(), ldw, d, _ptr(dx), max(d, 1), _ptr(dw),
                                              max(d, 1), _ptr(db), _ptr(ws), size, _stream(dev)),
                    "encode_grad")
@@ -476,21 +485,27 @@ def _dense(t: torch.Tensor) -> bool:
 def _norm_run(tensors, clip):
     if isinstance(tensors, torch.Tensor):
         tensors = [tensors]
-    ts = [t for t in tensors if t is not None]
+    ts = list(tensors)
+    try:
+        devices = set(map(_T.get_device, ts))
+    except TypeError:   # something that is no tensor: None is skipped
+        ts = [t for t in ts if t is not None]
+        devices = set(map(_T.get_device, ts))
     if not ts:
         return torch.zeros((), device="cuda")
-    index = ts[0].get_device()
-    if index < 0 or set(map(_T.get_device, ts)) != {index}:
+    index = devices.pop()
+    if index < 0 or devices:
         raise ValueError(f"tensors: all on one GPU (found {', '.join(sorted({str(t.device) for t in ts}))})")
-    codes = [_CODES.get(t.dtype) for t in ts]
-    if None in codes:
-        raise TypeError(f"tensors: unsupported dtype {ts[codes.index(None)].dtype}; use float32 or bfloat16")
+    dtypes = list(map(_dtype_of, ts))
+    for dtype in set(dtypes):
+        if dtype not in _CODES:
+            raise TypeError(f"tensors: unsupported dtype {dtype}; use float32 or bfloat16")
     if not all(map(_T.is_contiguous, ts)) and not all(map(_dense, ts)):
         raise ValueError("tensors: need dense memory (no gaps, no expanded axes)")
     # flat host arrays, passed by address; they live until the call has read them
     ptrs = array("Q", map(_T.data_ptr, ts))
     counts = array("q", map(_T.numel, ts))
-    codes = array("i", codes)
+    codes = array("i", map(_CODES.__getitem__, dtypes))
     args = (ptrs.buffer_info()[0], counts.buffer_info()[0], codes.buffer_info()[0], len(ts))
     with _on(index):
         norm = ts[0].new_empty((), dtype=torch.float32)
@@ -503,15 +518,8 @@ def _norm_run(tensors, clip):
         else:
             _lib.check(_lib.lib.topk_clip_grad_norm(*args, *clip, norm.data_ptr(), _ptr(ws), size.value,
                                                     _stream(index)), "clip_grad_norm")
-            _written(ts)
+            torch.autograd.graph.increment_version(ts)   # changed in place, which autograd cannot see
     return norm
-
-
-def _written(ts):
-    """Tell autograd that the tensors changed in place (inference tensors keep no count)."""
-    if any(map(_T.is_inference, ts)):
-        ts = [t for t in ts if not t.is_inference()]
-    torch.autograd.graph.increment_version(ts)
 
 
 def grad_norm(tensors) -> torch.Tensor:

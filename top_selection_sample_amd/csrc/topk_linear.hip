@@ -362,7 +362,7 @@ __global__ __launch_bounds__(NWM * NWN * 64, 2) void k_gemm(KGemm p) {
       }
     const uint32_t r0 = m0 + (wm + j) * 16;
     if (p.part || p.e.vec) {
-#pragma unroll 1
+#pragma unroll 2
       for (uint32_t rr = lane / LANES; rr < 32; rr += ROWS) {
         if (r0 + rr >= p.e.m) break;
         float v[V];
@@ -390,7 +390,7 @@ __global__ __launch_bounds__(NWM * NWN * 64, 2) void k_gemm(KGemm p) {
       if (col < p.e.n) {
         float b1;
         bias_of<T, 1>(&b1, col, p.e);
-#pragma unroll 1
+#pragma unroll 2
         for (uint32_t rr = lane / C; rr < 32; rr += 64 / C) {
           if (r0 + rr >= p.e.m) break;
           float z = mine[rr * C + ((c1 / 4) ^ (rr % CH)) * 4 + c1 % 4];

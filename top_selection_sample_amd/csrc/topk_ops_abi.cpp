@@ -409,7 +409,7 @@ int norm_call(tk::NormArgs& a, void* workspace, size_t workspace_bytes, void* st
         const uintptr_t p = reinterpret_cast<uintptr_t>(a.ptrs[i]);
         if (a.counts[i]) span.emplace_back(p, p + (uintptr_t)(a.counts[i] * elem(a.dtypes[i])));
       }
-      std::sort(span.begin(), span.end());
+      if (!std::is_sorted(span.begin(), span.end())) std::sort(span.begin(), span.end());
       for (size_t i = 1; i < span.size(); ++i)
         if (span[i].first < span[i - 1].second) return TOPK_EINVAL;
     } catch (...) {

@@ -79,8 +79,7 @@ struct SortPlan {
   uint32_t passes = 1, width = 0;       // digit bits of a pass (0: the whole key)
   uint32_t max_bins = 0;
   uint32_t blocks = 0, per_block = 0;
-  size_t off_cnt = 0, off_coarse = 0, off_key = 0, off_pos = 0, off_skey = 0, off_spos = 0, off_other = 0, off_coef = 0,
-         off_run = 0, total_bytes = 0;
+  size_t off_cnt = 0, off_coarse = 0, off_pair = 0, off_rec = 0, off_run = 0, total_bytes = 0;
 };
 
 uint32_t bins_of(const SortPlan& p, uint32_t pass) {
@@ -112,32 +111,25 @@ SortPlan sort_plan(int64_t keys, int64_t total) {
   };
   p.off_cnt = take((size_t)p.blocks * p.max_bins * 4);
   p.off_coarse = take((size_t)p.blocks * (p.max_bins / GROUP + 1) * 4);
-  if (p.passes > 1) {   // the even passes write here, the odd ones behind it
-    p.off_key = take((size_t)total * 8);
-    p.off_pos = take((size_t)total * 8);
-  }
-  p.off_skey = take((size_t)total * 4);
-  p.off_spos = take((size_t)total * 4);
+  if (p.passes > 1) p.off_pair = take((size_t)total * 16);   // two halves: the passes alternate
+  p.off_rec = take((size_t)total * 16);
   p.off_run = take((size_t)keys * 8);
-  p.off_other = take((size_t)total * 4);
-  p.off_coef = take((size_t)total * 4);
   p.total_bytes = at;
   return p;
 }
 
-// One pass over (key, entry) pairs; the first makes them from the selection.
+// One pass over (key, entry) pairs; the first makes them from the selection,
+// the last writes what the sums read: (key, the other index, coefficient,
+// entry), one 16-byte store to a place of its own instead of four.
 struct KPass {
-  const uint32_t* key_in;     // null: from the selection
-  const uint32_t* pos_in;
-  uint32_t* key_out;
-  uint32_t* pos_out;
-  uint32_t* other;            // the last pass also writes what the sums read
-  float* coef;
+  const u32x2* in;            // (key, entry); null: from the selection
+  u32x2* out;                 // null in the last pass, which writes records
+  u32x4* rec;
   uint32_t* cnt;              // [blocks][bins]
   uint32_t* coarse;           // [groups][blocks]
   uint32_t* run;              // [keys][2]: first entry and end of a key's run, cleared by the first pass
   uint32_t keys, total, per_block, bins, groups, shift, mask, digit_bits, blocks;
-  int by_row, last;
+  int by_row;
 };
 
 // A launch sorts by row and by latent side by side (grid dimension y).
@@ -146,7 +138,7 @@ struct KPasses {
 };
 
 __device__ __forceinline__ uint32_t key_of(const KSel& s, const KPass& p, uint32_t e) {
-  if (p.key_in) return p.key_in[e];
+  if (p.in) return p.in[e][0];
   uint32_t row, latent;
   if (!entry_of(s, e, s.idx[e], &row, &latent)) return p.keys;
   return p.by_row ? row : latent;
@@ -163,7 +155,7 @@ __global__ __launch_bounds__(SORT_THREADS) void k_count(KSel s, KPasses ps) {
   const uint32_t e1 = p.total - e0 < p.per_block ? p.total : e0 + p.per_block;
   for (uint32_t e = e0 + threadIdx.x; e < e1; e += SORT_THREADS)
     atomicAdd(&hist[(key_of(s, p, e) >> p.shift) & p.mask], 1u);
-  if (!p.key_in) {
+  if (!p.in) {
     for (uint64_t i = (uint64_t)blockIdx.x * SORT_THREADS + threadIdx.x; i < p.keys; i += (uint64_t)gridDim.x * SORT_THREADS)
       p.run[2 * i] = NO_ENTRY;
   }
@@ -242,18 +234,19 @@ __global__ __launch_bounds__(SORT_THREADS) void k_place(KSel s, KPasses ps, cons
     uint32_t key = 0, pos = e, other = 0;
     float w = 0.f;
     if (in) {
-      if (p.key_in) {
-        key = p.key_in[e];
-        pos = p.pos_in[e];
+      if (p.in) {
+        const u32x2 q = p.in[e];
+        key = q[0];
+        pos = q[1];
       }
-      if (!p.key_in || p.last) {
+      if (!p.in || !p.out) {
         uint32_t row = 0, latent = 0;
-        const bool good = entry_of(s, pos, s.idx[pos], &row, &latent);
-        if (!p.key_in) key = good ? (p.by_row ? row : latent) : p.keys;
-        if (good && p.last) {
-          other = p.by_row ? latent : row;
-          w = coef_of(coef, gate, pos);
-        }
+        const int64_t i = s.idx[pos];
+        if (!p.out) w = coef_of(coef, gate, pos);
+        const bool good = entry_of(s, pos, i, &row, &latent);
+        if (!p.in) key = good ? (p.by_row ? row : latent) : p.keys;
+        other = good ? (p.by_row ? latent : row) : 0u;
+        w = good ? w : 0.f;
       }
     }
     const uint32_t d = (key >> p.shift) & p.mask;
@@ -275,22 +268,15 @@ __global__ __launch_bounds__(SORT_THREADS) void k_place(KSel s, KPasses ps, cons
       __syncthreads();
     }
     if (in) {
-      p.key_out[at] = key;
-      p.pos_out[at] = pos;
-      if (p.last) {
-        p.other[at] = other;
-        p.coef[at] = w;
-      }
+      if (p.out) p.out[at] = u32x2{key, pos};
+      else p.rec[at] = u32x4{key, other, __float_as_uint(w), pos};
     }
   }
 }
 
 // ---------------------------------------------------------------- sums
 struct KSeg {
-  const uint32_t* skey;
-  const uint32_t* spos;
-  const uint32_t* other;
-  const float* coef;
+  const u32x4* rec;     // sorted (key, the other index, coefficient, entry)
   uint32_t* run;        // [keys][2]
   const void* src;
   const void* bias;
@@ -368,10 +354,10 @@ __global__ __launch_bounds__(256) void k_seg(KSegs ss) {
   const bool one = blockIdx.y == 0 && lane == 0;
   const T* src = static_cast<const T*>(p.src);
   const T* wsrc = static_cast<const T*>(p.wsrc);
-  const uint32_t before = e0 ? p.skey[e0 - 1] : NO_ENTRY;
-  const uint32_t behind = e1 < p.total ? p.skey[e1] : NO_ENTRY;
+  const uint32_t before = e0 ? p.rec[e0 - 1][0] : NO_ENTRY;
+  const uint32_t behind = e1 < p.total ? p.rec[e1][0] : NO_ENTRY;
   float acc[NV][VEC] = {}, csum = 0.f;
-  uint32_t cur = p.skey[e0];
+  uint32_t cur = p.rec[e0][0];
   bool came = cur == before;
   if (one && !came && cur < p.keys) p.run[2 * (size_t)cur] = e0;
 
@@ -424,9 +410,9 @@ __global__ __launch_bounds__(256) void k_seg(KSegs ss) {
   for (uint32_t b = e0; b < e1; b += 64) {
     const uint32_t have = e1 - b < 64 ? e1 - b : 64;
     const bool mine = lane < have;
-    const uint32_t lk = mine ? p.skey[b + lane] : p.keys;
-    const uint32_t lo = mine ? p.other[b + lane] : 0u;
-    const float lc = mine ? p.coef[b + lane] : 0.f;
+    u32x4 r = {p.keys, 0u, 0u, 0u};
+    if (mine) r = p.rec[b + lane];
+    const uint32_t lk = r[0], lo = r[1], lc = r[2], le = r[3];
     for (uint32_t i0 = 0; i0 < have; i0 += AHEAD) {
       Row<T, VEC, NV> row[AHEAD], wrow[DOTS ? AHEAD : 1];
 #pragma unroll
@@ -440,7 +426,7 @@ __global__ __launch_bounds__(256) void k_seg(KSegs ss) {
 #pragma unroll
       for (uint32_t u = 0; u < AHEAD; ++u) {
         const uint32_t k = __builtin_amdgcn_readlane(lk, i0 + u);
-        const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(lc), i0 + u));
+        const float w = __uint_as_float(__builtin_amdgcn_readlane(lc, i0 + u));
         if (k != cur && i0 + u < have) {
           flush(b + i0 + u, false);
           cur = k;
@@ -466,19 +452,54 @@ __global__ __launch_bounds__(256) void k_seg(KSegs ss) {
       if constexpr (DOTS) {
         static_assert(AHEAD == 8, "eight_sums");
         const float v = eight_sums(dot, lane);
-        if (lane < AHEAD && i0 + lane < have) static_cast<T*>(p.dots)[p.spos[b + i0 + lane]] = from_f32<T>(v);
+        const uint32_t e = __shfl(le, i0 + lane % AHEAD);   // (sums of lane l: entry l % 8)
+        if (lane < AHEAD && i0 + lane < have) static_cast<T*>(p.dots)[e] = from_f32<T>(v);
       }
     }
   }
   flush(e1, behind == cur);
 }
 
+// Adds the partial sums of chunks [q, end) of a run (its first chunk keeps
+// them in the second slot) for the VEC columns from c on.
+template <int VEC>
+__device__ __forceinline__ void add_parts(float* acc, const KSeg& p, uint32_t first, uint32_t q, uint32_t end, uint32_t c) {
+#pragma unroll 8
+  for (; q < end; ++q) {
+    const float* b = p.part + ((size_t)q * 2 + (q == first)) * p.d + c;
+    if constexpr (VEC == 1) {
+      acc[0] += b[0];
+    } else {
+#pragma unroll
+      for (int j = 0; j < VEC; j += 4) {
+        float v[4];
+        Vec<float>::load(b + j, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[j + i] += v[i];
+      }
+    }
+  }
+}
+
+template <class T, int VEC>
+__device__ __forceinline__ void write_key(const KSeg& p, uint64_t key, uint32_t c, float* acc) {
+  if (p.bias) {
+    float b[VEC];
+    load_vec<T, VEC>(static_cast<const T*>(p.bias) + c, b);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) acc[j] += b[j];
+  }
+  store_vec<T, VEC>(static_cast<T*>(p.out) + (int64_t)key * p.ldo + c, acc);
+}
+
 // Writes the keys without an entry, and joins the runs of several chunks: 16
-// keys per workgroup, a wave per key.
-constexpr uint32_t JOIN_KEYS = 16;
+// keys per workgroup, a wave per key; the runs of more than LONG chunks are
+// shared by the four waves.
+constexpr uint32_t JOIN_KEYS = 16, LONG = 12;
 
 template <class T, int VEC>
 __global__ __launch_bounds__(256) void k_join_runs(KSegs ss) {
+  __shared__ float join[4][64 * VEC];
   const KSeg& p = ss.s[blockIdx.z];
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
   uint32_t first = NO_ENTRY, end = 0;     // lane i: the workgroup's key i
@@ -487,43 +508,46 @@ __global__ __launch_bounds__(256) void k_join_runs(KSegs ss) {
     first = p.run[2 * (k0 + lane)];
     end = p.run[2 * (k0 + lane) + 1];
   }
+  // chunks [q0, q1) of each key's run; none: q1 = 0
+  const uint32_t lq0 = first == NO_ENTRY ? 0u : first / p.chunk, lq1 = first == NO_ENTRY ? 0u : (end - 1) / p.chunk + 1;
   for (uint32_t i = wave; i < JOIN_KEYS && k0 + i < p.keys; i += 4) {
-    const uint64_t key = k0 + i;
-    const uint32_t lo = __builtin_amdgcn_readlane(first, i), hi = __builtin_amdgcn_readlane(end, i);
-    const bool none = lo == NO_ENTRY;
-    const uint32_t q0 = none ? 0u : lo / p.chunk, q1 = none ? 0u : (hi - 1) / p.chunk;
-    if (!none && q0 == q1) continue;     // written by its chunk
-    if (p.out) {
-      for (uint32_t c = lane * VEC; c < p.d; c += 64 * VEC) {
-        float acc[VEC] = {};
-        if (!none) {
-          const float* a = p.part + ((size_t)q0 * 2 + 1) * p.d + c;
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) acc[j] = a[j];
-#pragma unroll 8
-          for (uint32_t q = q0 + 1; q <= q1; ++q) {
-            const float* b = p.part + (size_t)q * 2 * p.d + c;
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) acc[j] += b[j];
-          }
-        }
-        if (p.bias) {
-          float b[VEC];
-          load_vec<T, VEC>(static_cast<const T*>(p.bias) + c, b);
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) acc[j] += b[j];
-        }
-        store_vec<T, VEC>(static_cast<T*>(p.out) + (int64_t)key * p.ldo + c, acc);
-      }
-    }
+    const uint32_t q0 = __builtin_amdgcn_readlane(lq0, i), q1 = __builtin_amdgcn_readlane(lq1, i);
+    if (q1 == q0 + 1) continue;                  // written by its chunk
     if (p.coef_sum && lane == 0) {
       float s = 0.f;
-      if (!none) {
-        s = p.part_c[(size_t)q0 * 2 + 1];
 #pragma unroll 8
-        for (uint32_t q = q0 + 1; q <= q1; ++q) s += p.part_c[(size_t)q * 2];
+      for (uint32_t q = q0; q < q1; ++q) s += p.part_c[(size_t)q * 2 + (q == q0)];
+      static_cast<T*>(p.coef_sum)[k0 + i] = from_f32<T>(s);
+    }
+    if (!p.out || q1 - q0 > LONG) continue;
+    for (uint32_t c = lane * VEC; c < p.d; c += 64 * VEC) {
+      float acc[VEC] = {};
+      add_parts<VEC>(acc, p, q0, q0, q1, c);
+      write_key<T, VEC>(p, k0 + i, c, acc);
+    }
+  }
+  if (!p.out) return;
+  uint64_t many = __ballot(lane < JOIN_KEYS && lq1 - lq0 > LONG);
+  for (; many; many &= many - 1) {
+    const uint32_t i = (uint32_t)__ffsll((unsigned long long)many) - 1;
+    const uint32_t q0 = __builtin_amdgcn_readlane(lq0, i), q1 = __builtin_amdgcn_readlane(lq1, i);
+    const uint32_t per = (q1 - q0 + 3) / 4, a0 = q0 + wave * per, a1 = a0 + per < q1 ? a0 + per : q1;
+    for (uint32_t b = 0; b < p.d; b += 64 * VEC) {
+      const uint32_t c = b + lane * VEC;
+      float acc[VEC] = {};
+      if (c < p.d) add_parts<VEC>(acc, p, q0, a0, a1, c);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) join[wave][lane * VEC + j] = acc[j];
+      __syncthreads();
+      if (wave == 0 && c < p.d) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          const uint32_t a = lane * VEC + j;
+          acc[j] = (join[0][a] + join[1][a]) + (join[2][a] + join[3][a]);
+        }
+        write_key<T, VEC>(p, k0 + i, c, acc);
       }
-      static_cast<T*>(p.coef_sum)[key] = from_f32<T>(s);
+      __syncthreads();
     }
   }
 }
@@ -698,15 +722,11 @@ hipError_t run_sorts(const SegCall& a, const SegArgs* const* parts, const SegPla
       const SortPlan& p = plans[i].sort;
       if (pass >= p.passes) continue;
       KPass& k = ks.p[y++];
-      uint32_t* keys = reinterpret_cast<uint32_t*>(ws[i] + p.off_key);
-      uint32_t* pos = reinterpret_cast<uint32_t*>(ws[i] + p.off_pos);
-      k.last = pass + 1 == p.passes;
-      k.key_in = pass ? keys + (size_t)((pass - 1) & 1) * p.total : nullptr;
-      k.pos_in = pass ? pos + (size_t)((pass - 1) & 1) * p.total : nullptr;
-      k.key_out = k.last ? reinterpret_cast<uint32_t*>(ws[i] + p.off_skey) : keys + (size_t)(pass & 1) * p.total;
-      k.pos_out = k.last ? reinterpret_cast<uint32_t*>(ws[i] + p.off_spos) : pos + (size_t)(pass & 1) * p.total;
-      k.other = reinterpret_cast<uint32_t*>(ws[i] + p.off_other);
-      k.coef = reinterpret_cast<float*>(ws[i] + p.off_coef);
+      u32x2* pair = reinterpret_cast<u32x2*>(ws[i] + p.off_pair);
+      const bool last = pass + 1 == p.passes;
+      k.in = pass ? pair + (size_t)((pass - 1) & 1) * p.total : nullptr;
+      k.out = last ? nullptr : pair + (size_t)(pass & 1) * p.total;
+      k.rec = reinterpret_cast<u32x4*>(ws[i] + p.off_rec);
       k.cnt = reinterpret_cast<uint32_t*>(ws[i] + p.off_cnt);
       k.coarse = reinterpret_cast<uint32_t*>(ws[i] + p.off_coarse);
       k.run = reinterpret_cast<uint32_t*>(ws[i] + p.off_run);
@@ -818,10 +838,7 @@ hipError_t run_seg(const SegCall& a, char* ws, hipStream_t s) {
     }
     plans[n] = seg_plan(a.sel, a.d, p.by_row);
     const SortPlan& q = plans[n].sort;
-    k.skey = reinterpret_cast<const uint32_t*>(ws + q.off_skey);
-    k.spos = reinterpret_cast<const uint32_t*>(ws + q.off_spos);
-    k.other = reinterpret_cast<const uint32_t*>(ws + q.off_other);
-    k.coef = reinterpret_cast<const float*>(ws + q.off_coef);
+    k.rec = reinterpret_cast<const u32x4*>(ws + q.off_rec);
     k.run = reinterpret_cast<uint32_t*>(ws + q.off_run);
     k.part = reinterpret_cast<float*>(ws + plans[n].off_part);
     k.part_c = reinterpret_cast<float*>(ws + plans[n].off_part_c);
