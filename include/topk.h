@@ -321,10 +321,11 @@ int topk_stream_read(const void* data, size_t bytes, uint32_t* sink, void* strea
  *     squares of a norm in 64) and rounded once, to nearest even, when an
  *     output is written.
  *   - Matrices are row-major with a row stride ("ld", in elements, at least
- *     the row length) and element alignment.  16-byte aligned rows (address
- *     and stride) are read faster.
- *   - Sizes may be 0: an empty sum is 0.  No size or stride reaches 2^31, the
- *     row width d of a decode stays below 2^22.
+ *     the row length) and element alignment.  A product reads operands whose
+ *     rows are not all 16-byte aligned through a copy in its workspace.
+ *   - Sizes may be 0: an empty sum is 0.  No size or stride reaches 2^31; n and
+ *     k of a product (and m, where x_trans is set) and the row width d of a
+ *     decode stay below 2^22.
  *   - Every result is the same from call to call: no sum's order depends on
  *     timing.
  *   - `workspace`: 256-byte aligned device memory of at least the size that

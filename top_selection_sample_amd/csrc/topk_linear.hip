@@ -21,7 +21,6 @@ struct Epi {
   uint32_t m, n;
   int act;
   int stream;    // store y past the caches
-  int vec;       // rows of c, pre and residual are 16-byte aligned, bias too
 };
 
 // Outputs from 16 MB on are stored past the caches: they would push the
@@ -45,8 +44,7 @@ __device__ __forceinline__ void act_any(float* v, int act) {
 }
 
 // V sums of row r from column c on, in order: bias (given), pre-activation,
-// activation, residual, one rounding, one store.  V is the 16-byte width
-// (aligned rows) or 1.
+// activation, residual, one rounding, one store.  V is the 16-byte width or 1.
 template <class T, int V>
 __device__ __forceinline__ void finish(float* v, const float* bias, uint32_t r, uint32_t c, const Epi& e) {
 #pragma unroll
@@ -61,8 +59,10 @@ __device__ __forceinline__ void finish(float* v, const float* bias, uint32_t r, 
   }
   T* y = static_cast<T*>(e.c) + (int64_t)r * e.ldc + c;
   if (V > 1 && e.stream) {
+    // (the empty statements keep the compiler from merging the two stores into a plain one)
+    asm volatile("");
     stream_vec<T>(y, v);
-    asm volatile("");   // keeps the compiler from merging the two stores into a plain one
+    asm volatile("");
   } else {
     store_vec<T, V>(y, v);
   }
@@ -348,7 +348,7 @@ __global__ __launch_bounds__(NWM * NWN * 64, 2) void k_gemm(KGemm p) {
   static_assert(W * 32 * C * 4 <= (TM + TN) * 128, "the rows fit one stage");
   float* mine = reinterpret_cast<float*>(stage0) + wave * 32 * C;
   const uint32_t cc = (lane % LANES) * V, c = n0 + wn * 16 + cc;
-  const bool whole = p.e.vec && c + V <= p.e.n;   // the lane's columns are one vector of every row
+  const bool whole = c + V <= p.e.n;   // the lane's columns are one vector of every row
   float bias[V] = {};
   if (whole && !p.part) bias_of<T, V>(bias, c, p.e);
 #pragma unroll
@@ -361,40 +361,29 @@ __global__ __launch_bounds__(NWM * NWN * 64, 2) void k_gemm(KGemm p) {
         *reinterpret_cast<f32x4*>(mine + r * C + (u ^ (r % CH)) * 4) = acc[i][j + h];
       }
     const uint32_t r0 = m0 + (wm + j) * 16;
-    if (p.part || p.e.vec) {
 #pragma unroll 2
-      for (uint32_t rr = lane / LANES; rr < 32; rr += ROWS) {
-        if (r0 + rr >= p.e.m) break;
-        float v[V];
+    for (uint32_t rr = lane / LANES; rr < 32; rr += ROWS) {
+      if (r0 + rr >= p.e.m) break;
+      float v[V];
 #pragma unroll
-        for (int i = 0; i < V; i += 4) Vec<float>::load(mine + rr * C + ((cc / 4 + i / 4) ^ (rr % CH)) * 4, v + i);
-        if (p.part) {
-          float* o = p.part + ((size_t)sp * p.e.m + r0 + rr) * p.ldpart + c;
+      for (int i = 0; i < V; i += 4) {
+        const f32x4 q = *reinterpret_cast<const f32x4*>(mine + rr * C + ((cc / 4 + i / 4) ^ (rr % CH)) * 4);
 #pragma unroll
-          for (int i = 0; i < V; i += 4)
-            if (c + i < p.ldpart) Vec<float>::store(o + i, v + i);
-        } else if (whole) {
-          finish<T, V>(v, bias, r0 + rr, c, p.e);
-        } else {   // the last columns
-#pragma unroll 1
-          for (uint32_t i = 0; i < V && c + i < p.e.n; ++i) {
-            float z = mine[rr * C + ((cc / 4 + i / 4) ^ (rr % CH)) * 4 + i % 4], b1;
-            bias_of<T, 1>(&b1, c + i, p.e);
-            finish<T, 1>(&z, &b1, r0 + rr, c + i, p.e);
-          }
-        }
+        for (int u = 0; u < 4; ++u) v[i + u] = q[u];
       }
-    } else {   // rows at any alignment: a lane per column
-      const uint32_t c1 = lane % C;
-      const uint32_t col = n0 + wn * 16 + c1;
-      if (col < p.e.n) {
-        float b1;
-        bias_of<T, 1>(&b1, col, p.e);
-#pragma unroll 2
-        for (uint32_t rr = lane / C; rr < 32; rr += 64 / C) {
-          if (r0 + rr >= p.e.m) break;
-          float z = mine[rr * C + ((c1 / 4) ^ (rr % CH)) * 4 + c1 % 4];
-          finish<T, 1>(&z, &b1, r0 + rr, col, p.e);
+      if (p.part) {
+        float* o = p.part + ((size_t)sp * p.e.m + r0 + rr) * p.ldpart + c;
+#pragma unroll
+        for (int i = 0; i < V; i += 4)
+          if (c + i < p.ldpart) Vec<float>::store(o + i, v + i);
+      } else if (whole) {
+        finish<T, V>(v, bias, r0 + rr, c, p.e);
+      } else {   // the last columns
+#pragma unroll 1
+        for (uint32_t i = 0; i < V && c + i < p.e.n; ++i) {
+          float z = mine[rr * C + ((cc / 4 + i / 4) ^ (rr % CH)) * 4 + i % 4], b1;
+          bias_of<T, 1>(&b1, c + i, p.e);
+          finish<T, 1>(&z, &b1, r0 + rr, c + i, p.e);
         }
       }
     }
@@ -402,39 +391,87 @@ __global__ __launch_bounds__(NWM * NWN * 64, 2) void k_gemm(KGemm p) {
 #endif
 }
 
-// Adds the partial sums of a split product in order, then the epilogue.
+// Adds partial sums in order, then the epilogue: the parts of up to two split
+// products and the column sums' blocks (a product of one row) in one launch.
+struct KJoin {
+  const float* part;     // [split][m][ldpart]
+  uint32_t split, ldpart, blocks;
+  int tall;              // one row of many parts: 16 threads share a column's
+  Epi e;
+};
+struct KJoins {
+  KJoin j[3];
+};
+
 template <class T>
-__global__ __launch_bounds__(256) void k_split_join(const float* __restrict__ part, uint32_t split,
-                                                    uint32_t ldpart, Epi e) {
+__global__ __launch_bounds__(256) void k_join(KJoins js) {
   constexpr int V = Vec<T>::N;
-  const uint32_t per_row = (e.n + V - 1) / V;
-  const uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= (uint64_t)per_row * e.m) return;
+  uint32_t b = blockIdx.x, which = 0;
+  while (b >= js.j[which].blocks) b -= js.j[which++].blocks;
+  const KJoin& p = js.j[which];
+  if (p.tall) {
+    __shared__ float sums[16][17];
+    const uint32_t c = b * 16 + threadIdx.x % 16, group = threadIdx.x / 16;
+    float v = 0.f;
+    if (c < p.e.n) {
+#pragma unroll 4
+      for (uint32_t s = group; s < p.split; s += 16) v += p.part[(size_t)s * p.ldpart + c];
+    }
+    sums[group][threadIdx.x % 16] = v;
+    __syncthreads();
+    if (group == 0 && c < p.e.n) {
+      v = 0.f;
+#pragma unroll
+      for (uint32_t g = 0; g < 16; ++g) v += sums[g][threadIdx.x];
+      static_cast<T*>(p.e.c)[c] = from_f32<T>(v);
+    }
+    return;
+  }
+  const uint32_t per_row = (p.e.n + V - 1) / V;
+  const uint64_t i = (uint64_t)b * 256 + threadIdx.x;
+  if (i >= (uint64_t)per_row * p.e.m) return;
   const uint32_t r = (uint32_t)(i / per_row), c = (uint32_t)(i % per_row) * V;
   float v[V] = {};
-  for (uint32_t s = 0; s < split; ++s) {
-    const float* q = part + ((size_t)s * e.m + r) * ldpart + c;
+  const float* q = p.part + (size_t)r * p.ldpart + c;
+#pragma unroll 8
+  for (uint32_t s = 0; s < p.split; ++s) {
 #pragma unroll
     for (int j = 0; j < V; j += 4) {
-      if (c + j >= ldpart) break;
-      const f32x4 t = *reinterpret_cast<const f32x4*>(q + j);
+      if (c + j >= p.ldpart) continue;
+      const f32x4 t = *reinterpret_cast<const f32x4*>(q + j);   // ldpart is a multiple of 4
 #pragma unroll
       for (int u = 0; u < 4; ++u) v[j + u] += t[u];
     }
+    q += (size_t)p.e.m * p.ldpart;
   }
-  if (e.vec && c + V <= e.n) {
-    float b[V];
-    bias_of<T, V>(b, c, e);
-    finish<T, V>(v, b, r, c, e);
+  if (c + V <= p.e.n) {
+    float bias[V];
+    bias_of<T, V>(bias, c, p.e);
+    finish<T, V>(v, bias, r, c, p.e);
   } else {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      if (c + j >= e.n) continue;
-      float b;
-      bias_of<T, 1>(&b, c + j, e);
-      finish<T, 1>(v + j, &b, r, c + j, e);
+      if (c + j >= p.e.n) continue;
+      float bias;
+      bias_of<T, 1>(&bias, c + j, p.e);
+      finish<T, 1>(v + j, &bias, r, c + j, p.e);
     }
   }
+}
+
+template <class T>
+hipError_t run_joins(const KJoin* js, int n, hipStream_t s) {
+  KJoins k{};
+  uint32_t blocks = 0;
+  for (int i = 0; i < n; ++i) {
+    k.j[i] = js[i];
+    k.j[i].blocks = (uint32_t)(js[i].tall ? ceil_div(js[i].e.n, 16)
+                                          : ceil_div(ceil_div(js[i].e.n, Vec<T>::N) * (int64_t)js[i].e.m, 256));
+    blocks += k.j[i].blocks;
+  }
+  if (!blocks) return hipSuccess;
+  hipLaunchKernelGGL((k_join<T>), dim3(blocks), dim3(256), 0, s, k);
+  return hipGetLastError();
 }
 
 // Copies lines of `red` elements to lines of `ldo`, zeros behind their end;
@@ -459,13 +496,19 @@ __global__ __launch_bounds__(256) void k_pack(KPack a, KPack b) {
   const uint64_t r = i / per;
   const uint32_t c = (uint32_t)(i - r * per) * V;
   const T* src = static_cast<const T*>(p.src) + (int64_t)r * p.ld + c;
-  T v[V];
+  u32x4 q;
+  if (c + V <= p.red) {
+    q = read16(src);
+  } else {
+    T v[V];
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    v[j] = T{};
-    if (c + j < p.red) v[j] = src[j];
+    for (int j = 0; j < V; ++j) {
+      v[j] = T{};
+      if (c + j < p.red) v[j] = src[j];
+    }
+    q = __builtin_bit_cast(u32x4, v);
   }
-  *reinterpret_cast<u32x4*>(static_cast<T*>(p.dst) + r * p.ldo + c) = __builtin_bit_cast(u32x4, v);
+  *reinterpret_cast<u32x4*>(static_cast<T*>(p.dst) + r * p.ldo + c) = q;
 }
 
 // Few rows of x: the call is bound by reading W once.  A workgroup takes 16
@@ -474,25 +517,25 @@ __global__ __launch_bounds__(256) void k_pack(KPack a, KPack b) {
 // instructions' operands, with all loads of a turn issued before the first is
 // used, and join their sums in LDS in wave order.  One token through 12288 x
 // 512 bf16: 12.6 MB.
-template <class T, int MF, bool WIDE>
+template <class T>
 __device__ __forceinline__ u32x4 row_piece(const T* p, bool in, uint32_t k, uint32_t red) {
   constexpr uint32_t V = Vec<T>::N;
   u32x4 q = {0u, 0u, 0u, 0u};
-  if constexpr (WIDE) {
-    if (in && k < red) q = *reinterpret_cast<const u32x4*>(p + k);
-  } else {
+  if (in && k + V <= red) {
+    q = read16(p + k);
+  } else if (in && k < red) {
     T v[V];
 #pragma unroll
     for (uint32_t i = 0; i < V; ++i) {
       v[i] = T{};
-      if (in && k + i < red) v[i] = p[k + i];
+      if (k + i < red) v[i] = p[k + i];
     }
     q = __builtin_bit_cast(u32x4, v);
   }
   return q;
 }
 
-template <class T, int MF, bool WIDE>
+template <class T, int MF>
 __global__ __launch_bounds__(256) void k_few_rows(KGemm p) {
   constexpr uint32_t V = Vec<T>::N, PIECE = 4 * V, TURN = 4;   // summed elements per instruction, pieces per turn
   __shared__ float join[4][MF][16][17];
@@ -515,9 +558,9 @@ __global__ __launch_bounds__(256) void k_few_rows(KGemm p) {
     u32x4 wf[TURN][1], xf[TURN][MF];
 #pragma unroll
     for (uint32_t t = 0; t < TURN; ++t) {
-      wf[t][0] = row_piece<T, MF, WIDE>(w, win, k0 + t * PIECE + g * V, red);
+      wf[t][0] = row_piece<T>(w, win, k0 + t * PIECE + g * V, red);
 #pragma unroll
-      for (int f = 0; f < MF; ++f) xf[t][f] = row_piece<T, MF, WIDE>(x[f], xin[f], k0 + t * PIECE + g * V, red);
+      for (int f = 0; f < MF; ++f) xf[t][f] = row_piece<T>(x[f], xin[f], k0 + t * PIECE + g * V, red);
     }
 #pragma unroll
     for (uint32_t t = 0; t < TURN; ++t) mma_all<T, MF, 1>(wf[t], xf[t], acc);
@@ -559,7 +602,7 @@ bool needs_pack(const Operand& o, int64_t rows, int64_t red, int64_t es) {
   const int64_t line = o.trans ? rows : red, lines = o.trans ? red : rows;
   const int64_t ld = lines > 1 ? o.ld : line;
   return reinterpret_cast<uintptr_t>(o.p) % 16 || (lines > 1 && (ld * es) % 16) ||
-         (!o.trans && (red * es) % 16) || ld * es * 128 >= (int64_t(1) << 31);
+         (!o.trans && !o.padded && (red * es) % 16) || ld * es * 128 >= (int64_t(1) << 31);
 }
 
 // Microseconds of one step of a tile on a compute unit that shares its time
@@ -637,12 +680,6 @@ Plan2 plan_gemm(const GemmArgs& g) {
   return p;
 }
 
-template <class T>
-KPack pack_of(const Operand& o, int64_t rows, int64_t red, uint32_t ldo, void* dst) {
-  const int64_t line = o.trans ? rows : red, lines = o.trans ? red : rows;
-  return KPack{o.p, dst, o.ld, (uint32_t)line, ldo, (uint64_t)(ldo / Vec<T>::N) * (uint64_t)lines};
-}
-
 template <class T, int R, int NWM, int NWN>
 void go(const KGemm& k, bool ta, bool tb, uint32_t grid, hipStream_t s) {
   const dim3 block(NWM * NWN * 64);
@@ -653,97 +690,118 @@ void go(const KGemm& k, bool ta, bool tb, uint32_t grid, hipStream_t s) {
   else hipLaunchKernelGGL((k_gemm<T, R, R, NWM, NWN, false, false>), dim3(grid), block, 0, s, k);
 }
 
-bool aligned16(const void* p, int64_t ld, int64_t es) {
-  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld * es) % 16 == 0;
-}
-
+// A product in steps: copies of the operands that need one, the tiles, the
+// join of split sums (which several products share).
 template <class T>
-hipError_t run_gemm(const GemmArgs& g, char* ws, hipStream_t s) {
-  const Plan2 p = plan_gemm(g);
-  const int64_t es = sizeof(T), v = 16 / es;
-  hipError_t e = hipSuccess;
-  if (p.pack_a || p.pack_b) {
-    KPack a{}, b{};
-    if (p.pack_a) a = pack_of<T>(g.a, g.m, g.k, p.lda, ws);
-    if (p.pack_b) b = pack_of<T>(g.b, g.n, g.k, p.ldb, ws + p.off_b);
-    hipLaunchKernelGGL((k_pack<T>), dim3((uint32_t)ceil_div((int64_t)(a.vecs + b.vecs), 256)), dim3(256), 0, s, a, b);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
+struct Product {
+  static constexpr int64_t ES = sizeof(T), V = 16 / ES;
+  GemmArgs g;
+  Plan2 p;
+  char* ws;
+
+  Product(const GemmArgs& args, char* scratch) : g(args), p(plan_gemm(args)), ws(scratch) {}
+
+  KPack pack_of(const Operand& o, int64_t rows, uint32_t ldo, void* dst) const {
+    const int64_t line = o.trans ? rows : g.k, lines = o.trans ? g.k : rows;
+    return KPack{o.p, dst, o.ld, (uint32_t)line, ldo, (uint64_t)(ldo / V) * (uint64_t)lines};
   }
-  auto operand = [&](const Operand& o, int64_t rows, bool pack, uint32_t ldp, char* at) {
+  int packs(KPack* out) const {
+    int n = 0;
+    if (p.pack_a) out[n++] = pack_of(g.a, g.m, p.lda, ws);
+    if (p.pack_b) out[n++] = pack_of(g.b, g.n, p.ldb, ws + p.off_b);
+    return n;
+  }
+  KOperand operand(const Operand& o, int64_t rows, bool pack, uint32_t ldp, const char* at) const {
     KOperand k;
     const int64_t line = o.trans ? rows : g.k, lines = o.trans ? g.k : rows;
     k.p = pack ? at : o.p;
     k.ld = pack ? ldp : (lines > 1 ? o.ld : line);
     k.rows = (uint32_t)rows;
-    // a packed line ends in zeros: it counts as whole chunks
-    k.red = (uint32_t)(pack && !o.trans ? ceil_div(g.k, v) * v : g.k);
+    // a line that ends in zeros counts as whole chunks
+    k.red = (uint32_t)((pack || o.padded) && !o.trans ? ceil_div(g.k, V) * V : g.k);
     return k;
-  };
-  KGemm k;
-  k.a = operand(g.a, g.m, p.pack_a, p.lda, ws);
-  k.b = operand(g.b, g.n, p.pack_b, p.ldb, ws + p.off_b);
-  k.e = Epi{g.bias, g.residual, g.c, g.pre, g.ldr, g.ldc, g.ldp, (uint32_t)g.m, (uint32_t)g.n, g.act, 0, 0};
-  k.e.vec = aligned16(g.c, g.ldc, es) && (!g.residual || aligned16(g.residual, g.ldr, es)) &&
-            (!g.pre || aligned16(g.pre, g.ldp, es)) && aligned16(g.bias, 0, es);
-  if (p.few) {
-    const bool wide = !needs_pack(g.a, g.m, g.k, es) && !needs_pack(g.b, g.n, g.k, es);
-    const dim3 grid((uint32_t)ceil_div(g.n, 16));
-    if (g.m <= 16) {
-      if (wide) hipLaunchKernelGGL((k_few_rows<T, 1, true>), grid, dim3(256), 0, s, k);
-      else hipLaunchKernelGGL((k_few_rows<T, 1, false>), grid, dim3(256), 0, s, k);
-    } else {
-      if (wide) hipLaunchKernelGGL((k_few_rows<T, 2, true>), grid, dim3(256), 0, s, k);
-      else hipLaunchKernelGGL((k_few_rows<T, 2, false>), grid, dim3(256), 0, s, k);
+  }
+  Epi epilogue() const {
+    return Epi{g.bias, g.residual, g.c, g.pre, g.ldr, g.ldc, g.ldp, (uint32_t)g.m, (uint32_t)g.n, g.act,
+               g.m * g.n * ES >= STREAM_BYTES};
+  }
+  hipError_t tiles(hipStream_t s) const {
+    KGemm k{};
+    k.a = operand(g.a, g.m, p.pack_a, p.lda, ws);
+    k.b = operand(g.b, g.n, p.pack_b, p.ldb, ws + p.off_b);
+    k.e = epilogue();
+    if (p.few) {
+      const dim3 grid((uint32_t)ceil_div(g.n, 16));
+      if (g.m <= 16) hipLaunchKernelGGL((k_few_rows<T, 1>), grid, dim3(256), 0, s, k);
+      else hipLaunchKernelGGL((k_few_rows<T, 2>), grid, dim3(256), 0, s, k);
+      return hipGetLastError();
     }
+    k.part = p.split > 1 ? reinterpret_cast<float*>(ws + p.off_part) : nullptr;
+    k.ldpart = p.ldpart;
+    k.tiles_m = p.tiles_m;
+    k.tiles_n = p.tiles_n;
+    k.split = p.split;
+    k.steps = p.steps;
+    k.all_steps = p.all_steps;
+    const uint32_t grid = p.tiles_m * p.tiles_n * p.split;
+    if constexpr (ES == 2) {
+      if (p.tile == 256) {
+        go<T, 256, 2, 4>(k, g.a.trans, g.b.trans, grid, s);
+        return hipGetLastError();
+      }
+    }
+    if (p.tile == 128) go<T, 128, 2, 2>(k, g.a.trans, g.b.trans, grid, s);
+    else go<T, 64, 2, 2>(k, g.a.trans, g.b.trans, grid, s);
     return hipGetLastError();
   }
-  k.part = p.split > 1 ? reinterpret_cast<float*>(ws + p.off_part) : nullptr;
-  k.ldpart = p.ldpart;
-  k.tiles_m = p.tiles_m;
-  k.tiles_n = p.tiles_n;
-  k.split = p.split;
-  k.steps = p.steps;
-  k.all_steps = p.all_steps;
-  k.e.stream = g.m * g.n * es >= STREAM_BYTES;
-  const uint32_t grid = p.tiles_m * p.tiles_n * p.split;
-  bool done = false;
-  if constexpr (sizeof(T) == 2) {
-    if (p.tile == 256) {
-      go<T, 256, 2, 4>(k, g.a.trans, g.b.trans, grid, s);
-      done = true;
-    }
+  int joins(KJoin* out) const {
+    if (p.few || p.split == 1) return 0;
+    out[0] = KJoin{reinterpret_cast<const float*>(ws + p.off_part), p.split, p.ldpart, 0, 0, epilogue()};
+    return 1;
   }
-  if (done) {
-  } else if (p.tile == 128) go<T, 128, 2, 2>(k, g.a.trans, g.b.trans, grid, s);
-  else go<T, 64, 2, 2>(k, g.a.trans, g.b.trans, grid, s);
-  e = hipGetLastError();
-  if (e != hipSuccess || p.split == 1) return e;
-  const int64_t n = ceil_div(g.n, v) * g.m;
-  hipLaunchKernelGGL((k_split_join<T>), dim3((uint32_t)ceil_div(n, 256)), dim3(256), 0, s, k.part, p.split,
-                     p.ldpart, k.e);
+};
+
+template <class T>
+hipError_t run_packs(KPack* packs, int n, hipStream_t s) {
+  if (!n) return hipSuccess;
+  if (n == 1) packs[1] = KPack{};
+  hipLaunchKernelGGL((k_pack<T>), dim3((uint32_t)ceil_div((int64_t)(packs[0].vecs + packs[1].vecs), 256)), dim3(256),
+                     0, s, packs[0], packs[1]);
   return hipGetLastError();
+}
+
+template <class T>
+hipError_t run_gemm(const GemmArgs& g, char* ws, hipStream_t s) {
+  const Product<T> q(g, ws);
+  KPack packs[2];
+  KJoin join;
+  hipError_t e = run_packs<T>(packs, q.packs(packs), s);
+  if (e == hipSuccess) e = q.tiles(s);
+  if (e == hipSuccess) e = run_joins<T>(&join, q.joins(&join), s);
+  return e;
 }
 
 // ---------------------------------------------------------------- slope pass
 // dz = dy * act'(z), and the column sums of dz in 32 bits: a workgroup of
 // four waves takes 64 VEC columns and a block of rows; each lane sums its VEC
 // columns down the block's rows, the four waves join in LDS, and one partial
-// row per block goes to the workspace.  The sums are joined by k_join_rows in
-// block order.
-constexpr uint32_t SLOPE_ROWS = 64;   // rows per workgroup
-
+// row per block goes to the workspace, to be joined in block order.
 template <class T, int ACT, int VEC>
 __global__ __launch_bounds__(256) void k_slope(const T* __restrict__ dy, const T* __restrict__ pre,
                                                T* __restrict__ dz, float* __restrict__ part,
                                                uint32_t m, uint32_t n, int64_t ldd, int64_t ldp,
-                                               int64_t ldz, uint32_t rows_per) {
+                                               int64_t ldz, uint32_t rows_per, uint32_t ldpart) {
   const uint32_t wave = threadIdx.x / 64, lane = threadIdx.x % 64;
-  const uint32_t c = (blockIdx.x * 64 + lane) * VEC;
+  const uint32_t c0 = (blockIdx.x * 64 + lane) * VEC;
+  const uint32_t c = c0 < n ? column_of<VEC>(c0, n) : 0u;
   const uint32_t r0 = blockIdx.y * rows_per;
   const uint32_t r1 = r0 + rows_per < m ? r0 + rows_per : m;
+  // behind the last column: zeros up to whole 16 bytes
+  constexpr uint32_t CHUNK = Vec<T>::N;
+  const uint32_t fill = c0 < n && c0 + VEC >= n ? (n + CHUNK - 1) / CHUNK * CHUNK : n;
   float sum[VEC] = {};
-  if (c < n) {
+  if (c0 < n) {
+#pragma unroll 4
     for (uint32_t r = r0 + wave; r < r1; r += 4) {
       float v[VEC];
       load_vec<T, VEC>(dy + (int64_t)r * ldd + c, v);
@@ -755,7 +813,11 @@ __global__ __launch_bounds__(256) void k_slope(const T* __restrict__ dy, const T
           if constexpr (ACT == ACT_RELU) v[i] = z[i] <= 0.f ? 0.f : v[i];
           else v[i] *= slope_of<ACT, T>(z[i]);
         }
-        if (dz) store_vec<T, VEC>(dz + (int64_t)r * ldz + c, v);
+      }
+      if (dz) {
+        T* o = dz + (int64_t)r * ldz;
+        store_vec<T, VEC>(o + c, v);
+        for (uint32_t i = n; i < fill; ++i) o[i] = T{};
       }
 #pragma unroll
       for (int i = 0; i < VEC; ++i) sum[i] += v[i];
@@ -767,68 +829,132 @@ __global__ __launch_bounds__(256) void k_slope(const T* __restrict__ dy, const T
   for (int i = 0; i < VEC; ++i) join[wave][lane * VEC + i] = sum[i];
   __syncthreads();
   for (uint32_t i = threadIdx.x; i < 64 * VEC; i += 256) {
-    const uint32_t cc = blockIdx.x * 64 * VEC + i;
-    if (cc < n)
-      part[(size_t)blockIdx.y * n + cc] = (join[0][i] + join[1][i]) + (join[2][i] + join[3][i]);
+    const uint32_t cc = (blockIdx.x * 64 + i / VEC) * VEC;
+    if (cc < n)   // columns that two lanes hold get the same sum from both
+      part[(size_t)blockIdx.y * ldpart + column_of<VEC>(cc, n) + i % VEC] =
+          (join[0][i] + join[1][i]) + (join[2][i] + join[3][i]);
   }
 }
 
-// Four waves share the blocks of 64 columns.
-template <class T>
-__global__ __launch_bounds__(256) void k_join_rows(const float* __restrict__ part, T* __restrict__ out,
-                                                   uint32_t blocks, uint32_t n) {
-  __shared__ float join[4][64];
-  const uint32_t wave = threadIdx.x / 64, lane = threadIdx.x % 64, c = blockIdx.x * 64 + lane;
-  float s = 0.f;
-  if (c < n) {
-#pragma unroll 8
-    for (uint32_t b = wave; b < blocks; b += 4) s += part[(size_t)b * n + c];
-  }
-  join[wave][lane] = s;
-  __syncthreads();
-  if (wave == 0 && c < n) out[c] = from_f32<T>((join[0][lane] + join[1][lane]) + (join[2][lane] + join[3][lane]));
-}
-
-// Blocks of rows: 64 rows each, at most 65535 blocks (grid dimension y).
-uint32_t slope_rows(int64_t m) {
-  const int64_t least = ceil_div(m, 65535);
-  return (uint32_t)(least > SLOPE_ROWS ? least : SLOPE_ROWS);
-}
+// Blocks of 64 rows, at most 65535 of them (grid dimension y).
+uint32_t slope_rows(int64_t m) { return (uint32_t)std::max<int64_t>(64, ceil_div(m, 65535)); }
+uint32_t slope_blocks(int64_t m) { return (uint32_t)ceil_div(m, slope_rows(m)); }
+uint32_t slope_ld(int64_t n) { return (uint32_t)(ceil_div(n, 4) * 4); }
 
 template <class T, int ACT>
-hipError_t run_slope(const SlopeArgs& a, void* ws, hipStream_t s) {
-  const int64_t es = sizeof(T);
-  const uint32_t rows_per = slope_rows(a.m);
-  const uint32_t blocks = (uint32_t)ceil_div(a.m, rows_per);
-  float* part = a.db ? static_cast<float*>(ws) : nullptr;
-  const bool wide = a.n % Vec<T>::N == 0 && aligned16(a.dy, a.ldd, es) &&
-                    (!a.pre || aligned16(a.pre, a.ldp, es)) && (!a.dz || aligned16(a.dz, a.ldz, es));
+hipError_t run_slope(const SlopeArgs& a, float* part, hipStream_t s) {
+  constexpr int V = Vec<T>::N;
+  const bool wide = a.n >= V;
+  const dim3 grid((uint32_t)ceil_div(a.n, 64 * (wide ? V : 1)), slope_blocks(a.m));
   const T* dy = static_cast<const T*>(a.dy);
   const T* pre = static_cast<const T*>(a.pre);
   T* dz = static_cast<T*>(a.dz);
-  if (wide) {
-    hipLaunchKernelGGL((k_slope<T, ACT, Vec<T>::N>), dim3((uint32_t)ceil_div(a.n, 64 * Vec<T>::N), blocks),
-                       dim3(256), 0, s, dy, pre, dz, part, (uint32_t)a.m, (uint32_t)a.n, a.ldd, a.ldp,
-                       a.ldz, rows_per);
-  } else {
-    hipLaunchKernelGGL((k_slope<T, ACT, 1>), dim3((uint32_t)ceil_div(a.n, 64), blocks), dim3(256), 0, s,
-                       dy, pre, dz, part, (uint32_t)a.m, (uint32_t)a.n, a.ldd, a.ldp, a.ldz, rows_per);
-  }
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !a.db) return e;
-  hipLaunchKernelGGL((k_join_rows<T>), dim3((uint32_t)ceil_div(a.n, 64)), dim3(256), 0, s, part,
-                     static_cast<T*>(a.db), blocks, (uint32_t)a.n);
+  if (!a.db) part = nullptr;
+  if (wide)
+    hipLaunchKernelGGL((k_slope<T, ACT, V>), grid, dim3(256), 0, s, dy, pre, dz, part, (uint32_t)a.m, (uint32_t)a.n,
+                       a.ldd, a.ldp, a.ldz, slope_rows(a.m), slope_ld(a.n));
+  else
+    hipLaunchKernelGGL((k_slope<T, ACT, 1>), grid, dim3(256), 0, s, dy, pre, dz, part, (uint32_t)a.m, (uint32_t)a.n,
+                       a.ldd, a.ldp, a.ldz, slope_rows(a.m), slope_ld(a.n));
   return hipGetLastError();
 }
 
 template <class T>
-hipError_t run_slope_act(const SlopeArgs& a, void* ws, hipStream_t s) {
+hipError_t run_slope_act(const SlopeArgs& a, float* part, hipStream_t s) {
+  if (a.m == 0 || a.n == 0 || (!a.dz && !a.db)) return hipSuccess;
   switch (a.act) {
-    case ACT_RELU: return run_slope<T, ACT_RELU>(a, ws, s);
-    case ACT_GELU: return run_slope<T, ACT_GELU>(a, ws, s);
-    case ACT_SILU: return run_slope<T, ACT_SILU>(a, ws, s);
-    default: return run_slope<T, ACT_NONE>(a, ws, s);
+    case ACT_RELU: return run_slope<T, ACT_RELU>(a, part, s);
+    case ACT_GELU: return run_slope<T, ACT_GELU>(a, part, s);
+    case ACT_SILU: return run_slope<T, ACT_SILU>(a, part, s);
+    default: return run_slope<T, ACT_NONE>(a, part, s);
   }
+}
+
+// The column sums' join, as a product of one row whose parts are the blocks
+// (none for no rows: zeros).
+int slope_join(const SlopeArgs& a, const float* part, KJoin* out) {
+  if (!a.db || !a.n) return 0;
+  Epi e{};
+  e.c = a.db;
+  e.m = 1;
+  e.n = (uint32_t)a.n;
+  out[0] = KJoin{part, slope_blocks(a.m), slope_ld(a.n), 0, 1, e};
+  return 1;
+}
+
+// ---------------------------------------------------------------- gradients
+// Scratch: dz, then the column sums' parts, then each product's.
+struct GradPlan {
+  SlopeArgs slope;
+  GemmArgs dx, dw;
+  size_t off_sums = 0, off_dx = 0, off_dw = 0, total = 0;
+};
+
+GradPlan plan_grad(const GradArgs& a) {
+  GradPlan p;
+  const int64_t es = a.slope.dtype == DT_BF16 ? 2 : 4;
+  const int64_t m = a.slope.m, n = a.slope.n;
+  p.slope = a.slope;
+  const bool products = (a.dx || a.dw) && m && n;
+  // dz of its own where there is a slope to take, or where dy would have to be
+  // copied for the products anyway
+  const Operand dy{a.slope.dy, a.slope.ldd, false};
+  const bool own = products && (a.slope.act != ACT_NONE || needs_pack(dy, m, n, es));
+  Operand dz = dy;
+  if (own) {
+    p.slope.ldz = ceil_div(n, 64) * 64;
+    p.off_sums = align256((size_t)m * (size_t)p.slope.ldz * (size_t)es);
+    dz = Operand{nullptr, p.slope.ldz, false, true};
+  }
+  p.off_dx = p.off_sums + slope_workspace(a.slope);
+  auto product = [&](const Operand& x, const Operand& y, int64_t rows, int64_t cols, int64_t red, void* c, int64_t ldc) {
+    GemmArgs g;
+    g.a = x;
+    g.b = y;
+    g.m = rows;
+    g.n = cols;
+    g.k = red;
+    g.dtype = a.slope.dtype;
+    g.c = c;
+    g.ldc = ldc;
+    g.cus = a.cus;
+    return g;
+  };
+  Operand dzt = dz, wt = a.w, xt = a.x;
+  dzt.trans = true;
+  wt.trans = !wt.trans;   // the second operands' summed axes are n and m
+  xt.trans = !xt.trans;
+  p.dx = product(dz, wt, m, a.k, n, a.dx, a.lddx);
+  p.dw = product(dzt, xt, n, a.k, m, a.dw, a.lddw);
+  p.off_dw = p.off_dx + (a.dx ? gemm_workspace(p.dx) : 0);
+  p.total = p.off_dw + (a.dw ? gemm_workspace(p.dw) : 0);
+  return p;
+}
+
+template <class T>
+hipError_t run_grad(const GradArgs& a, char* ws, hipStream_t s) {
+  GradPlan p = plan_grad(a);
+  if (p.slope.ldz) {
+    p.slope.dz = ws;
+    p.dx.a.p = p.dw.a.p = ws;
+  }
+  float* sums = reinterpret_cast<float*>(ws + p.off_sums);
+  const bool dx = a.dx && p.dx.m && p.dx.n, dw = a.dw && p.dw.m && p.dw.n;
+  const Product<T> qx(p.dx, ws + p.off_dx), qw(p.dw, ws + p.off_dw);
+  KPack packs[4];
+  KJoin joins[3];
+  int np = 0, nj = 0;
+  if (dx) np += qx.packs(packs + np);
+  if (dw) np += qw.packs(packs + np);
+  hipError_t e = run_slope_act<T>(p.slope, sums, s);
+  for (int i = 0; i < np && e == hipSuccess; i += 2) e = run_packs<T>(packs + i, std::min(2, np - i), s);
+  if (e == hipSuccess && dx) e = qx.tiles(s);
+  if (e == hipSuccess && dw) e = qw.tiles(s);
+  if (dx) nj += qx.joins(joins + nj);
+  if (dw) nj += qw.joins(joins + nj);
+  nj += slope_join(p.slope, sums, joins + nj);
+  if (e == hipSuccess) e = run_joins<T>(joins, nj, s);
+  return e;
 }
 
 }  // namespace
@@ -844,22 +970,23 @@ hipError_t launch_gemm(const GemmArgs& g, void* ws, hipStream_t s) {
 }
 
 size_t slope_workspace(const SlopeArgs& a) {
-  if (!a.db) return 0;
-  return align256((size_t)ceil_div(a.m, slope_rows(a.m)) * (size_t)a.n * 4);
+  return a.db ? align256((size_t)slope_blocks(a.m) * slope_ld(a.n) * 4) : 0;
 }
 
 hipError_t launch_slope(const SlopeArgs& a, void* ws, hipStream_t s) {
-  if (a.n == 0 || (a.m == 0 && !a.db)) return hipSuccess;
-  if (a.m == 0) {   // no rows: the sums are zero
-    if (a.dtype == DT_BF16)
-      hipLaunchKernelGGL((k_join_rows<bf16_t>), dim3((uint32_t)ceil_div(a.n, 64)), dim3(256), 0, s,
-                         nullptr, static_cast<bf16_t*>(a.db), 0u, (uint32_t)a.n);
-    else
-      hipLaunchKernelGGL((k_join_rows<float>), dim3((uint32_t)ceil_div(a.n, 64)), dim3(256), 0, s,
-                         nullptr, static_cast<float*>(a.db), 0u, (uint32_t)a.n);
-    return hipGetLastError();
-  }
-  return a.dtype == DT_BF16 ? run_slope_act<bf16_t>(a, ws, s) : run_slope_act<float>(a, ws, s);
+  float* part = static_cast<float*>(ws);
+  KJoin join;
+  const int n = slope_join(a, part, &join);
+  hipError_t e = a.dtype == DT_BF16 ? run_slope_act<bf16_t>(a, part, s) : run_slope_act<float>(a, part, s);
+  if (e != hipSuccess) return e;
+  return a.dtype == DT_BF16 ? run_joins<bf16_t>(&join, n, s) : run_joins<float>(&join, n, s);
+}
+
+size_t grad_workspace(const GradArgs& a) { return plan_grad(a).total; }
+
+hipError_t launch_grad(const GradArgs& a, void* ws, hipStream_t s) {
+  return a.slope.dtype == DT_BF16 ? run_grad<bf16_t>(a, static_cast<char*>(ws), s)
+                                  : run_grad<float>(a, static_cast<char*>(ws), s);
 }
 
 }  // namespace tk

@@ -16,6 +16,7 @@ struct Operand {
   const void* p = nullptr;
   int64_t ld = 0;
   bool trans = false;
+  bool padded = false;   // not trans: rows go on with zeros up to whole 16 bytes
 };
 
 // C[m, n] = epilogue(A[m, k] B[n, k]^T)
@@ -37,8 +38,8 @@ struct GemmArgs {
 size_t gemm_workspace(const GemmArgs& g);
 hipError_t launch_gemm(const GemmArgs& g, void* ws, hipStream_t s);
 
-// dz = dy * act'(pre) into `dz` (null: not wanted, act == ACT_NONE), and its
-// column sums into `db` (null: not wanted).
+// dz = dy * act'(pre) into `dz` (null: not wanted), its rows filled up with
+// zeros to whole 16 bytes, and its column sums into `db` (null: not wanted).
 struct SlopeArgs {
   const void* dy = nullptr;
   int64_t ldd = 0;
@@ -54,6 +55,22 @@ struct SlopeArgs {
 
 size_t slope_workspace(const SlopeArgs& a);
 hipError_t launch_slope(const SlopeArgs& a, void* ws, hipStream_t s);
+
+// The gradients of a product: dx[m, k] = dz[m, n] W[n, k], dw[n, k] = dz^T x,
+// db.  `x` and `w` as operands of the product they come from.
+struct GradArgs {
+  SlopeArgs slope;       // dy, pre, sizes, type, activation and db; the rest is filled in
+  int64_t k = 0;
+  Operand x, w;
+  void* dx = nullptr;    // null: not wanted
+  int64_t lddx = 0;
+  void* dw = nullptr;
+  int64_t lddw = 0;
+  int cus = 256;
+};
+
+size_t grad_workspace(const GradArgs& a);
+hipError_t launch_grad(const GradArgs& a, void* ws, hipStream_t s);
 
 // A selection: `total` entries.  flat: index = row * n + latent; otherwise
 // entry e belongs to row e / k and its index is the latent.

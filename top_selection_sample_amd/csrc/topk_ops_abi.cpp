@@ -17,7 +17,9 @@ namespace {
 
 constexpr int64_t SIZE_MAX31 = (int64_t(1) << 31) - 1;
 
-constexpr int64_t WIDTH_MAX = int64_t(1) << 22;   // row width of a decode (grid dimension y, 64 columns each)
+// Longest row of a matrix operand: 128 of them stay below 2^31 bytes, the
+// range of the offsets within a tile.
+constexpr int64_t WIDTH_MAX = int64_t(1) << 22;
 
 bool bad_size(int64_t v) { return v < 0 || v > SIZE_MAX31; }
 
@@ -47,7 +49,7 @@ int linear_gemm(const topk_linear_args* a, tk::GemmArgs* g) {
   if (!a) return TOPK_EINVAL;
   if (bad_dtype(a->dtype)) return TOPK_EDTYPE;
   if (a->act < TOPK_ACT_NONE || a->act > TOPK_ACT_SILU) return TOPK_EINVAL;
-  if (bad_size(a->m) || bad_size(a->n) || bad_size(a->k)) return TOPK_EINVAL;
+  if (bad_size(a->m) || bad_width(a->n) || bad_width(a->k) || (a->x_trans && bad_width(a->m))) return TOPK_EINVAL;
   const int64_t m = a->m, n = a->n, k = a->k;
   if (a->x_trans ? bad_matrix(a->x, a->ldx, k, m, a->dtype) : bad_matrix(a->x, a->ldx, m, k, a->dtype))
     return TOPK_EINVAL;
@@ -75,20 +77,11 @@ int linear_gemm(const topk_linear_args* a, tk::GemmArgs* g) {
   return TOPK_OK;
 }
 
-// The three steps of a dense backward, and where each finds its scratch: dz
-// first, then a region that the steps, which run one after another, share.
-struct LinearGrad {
-  tk::SlopeArgs slope;
-  tk::GemmArgs dx, dw;
-  bool want_slope = false, want_dx = false, want_dw = false, own_dz = false;
-  size_t dz_bytes = 0, step_bytes = 0;
-};
-
-int linear_grad_plan(const topk_linear_grad_args* a, LinearGrad* p, char* ws) {
+int linear_grad(const topk_linear_grad_args* a, tk::GradArgs* g) {
   if (!a) return TOPK_EINVAL;
   if (bad_dtype(a->dtype)) return TOPK_EDTYPE;
   if (a->act < TOPK_ACT_NONE || a->act > TOPK_ACT_SILU) return TOPK_EINVAL;
-  if (bad_size(a->m) || bad_size(a->n) || bad_size(a->k)) return TOPK_EINVAL;
+  if (bad_size(a->m) || bad_width(a->n) || bad_width(a->k) || (a->x_trans && bad_width(a->m))) return TOPK_EINVAL;
   const int64_t m = a->m, n = a->n, k = a->k;
   const int dt = a->dtype;
   if (!a->dx && !a->dw && !a->db) return TOPK_EINVAL;
@@ -101,47 +94,23 @@ int linear_grad_plan(const topk_linear_grad_args* a, LinearGrad* p, char* ws) {
   if (a->dx && bad_matrix(a->dx, a->lddx, m, k, dt)) return TOPK_EINVAL;
   if (a->dw && bad_matrix(a->dw, a->lddw, n, k, dt)) return TOPK_EINVAL;
   if (a->db && bad_matrix(a->db, n, 1, n, dt)) return TOPK_EINVAL;
-  p->want_dx = a->dx != nullptr;
-  p->want_dw = a->dw != nullptr;
-  p->own_dz = a->act != TOPK_ACT_NONE && (p->want_dx || p->want_dw);
-  p->want_slope = p->own_dz || a->db;
-  const int64_t ldz = (n + 63) & ~(int64_t)63;   // 16-byte aligned rows in either type
-  p->dz_bytes = p->own_dz ? tk::align256((size_t)m * (size_t)ldz * (size_t)elem(dt)) : 0;
-  p->slope.dy = a->dy;
-  p->slope.ldd = a->ldd;
-  p->slope.pre = a->act != TOPK_ACT_NONE ? a->pre : nullptr;
-  p->slope.ldp = a->ldp;
-  p->slope.m = m;
-  p->slope.n = n;
-  p->slope.dtype = dt;
-  p->slope.act = a->act;
-  p->slope.dz = p->own_dz ? ws : nullptr;
-  p->slope.ldz = ldz;
-  p->slope.db = a->db;
-  const void* dz = p->own_dz ? static_cast<const void*>(ws) : a->dy;
-  const int64_t ld = p->own_dz ? ldz : a->ldd;
-  const int cus = tk::device_cus_now();
-  // dx[m, k] = dz[m, n] W[n, k]: the second operand's summed axis is n
-  p->dx.a = tk::Operand{dz, ld, false};
-  p->dx.b = tk::Operand{a->w, a->ldw, a->w_trans == 0};
-  p->dx.m = m;
-  p->dx.n = k;
-  p->dx.k = n;
-  p->dx.c = a->dx;
-  p->dx.ldc = a->lddx;
-  // dw[n, k] = dz^T x: the summed axis is m
-  p->dw.a = tk::Operand{dz, ld, true};
-  p->dw.b = tk::Operand{a->x, a->ldx, a->x_trans == 0};
-  p->dw.m = n;
-  p->dw.n = k;
-  p->dw.k = m;
-  p->dw.c = a->dw;
-  p->dw.ldc = a->lddw;
-  p->dx.dtype = p->dw.dtype = dt;
-  p->dx.cus = p->dw.cus = cus;
-  if (p->want_slope) p->step_bytes = std::max(p->step_bytes, tk::slope_workspace(p->slope));
-  if (p->want_dx) p->step_bytes = std::max(p->step_bytes, tk::gemm_workspace(p->dx));
-  if (p->want_dw) p->step_bytes = std::max(p->step_bytes, tk::gemm_workspace(p->dw));
+  g->slope.dy = a->dy;
+  g->slope.ldd = a->ldd;
+  g->slope.pre = a->act != TOPK_ACT_NONE ? a->pre : nullptr;
+  g->slope.ldp = a->ldp;
+  g->slope.m = m;
+  g->slope.n = n;
+  g->slope.dtype = dt;
+  g->slope.act = a->act;
+  g->slope.db = a->db;
+  g->k = k;
+  g->x = tk::Operand{a->x, a->ldx, a->x_trans != 0};
+  g->w = tk::Operand{a->w, a->ldw, a->w_trans != 0};
+  g->dx = a->dx;
+  g->lddx = a->lddx;
+  g->dw = a->dw;
+  g->lddw = a->lddw;
+  g->cus = tk::device_cus_now();
   return TOPK_OK;
 }
 
@@ -223,28 +192,21 @@ int topk_linear(const topk_linear_args* args, void* workspace, size_t workspace_
 
 int topk_linear_grad_workspace_size(const topk_linear_grad_args* args, size_t* bytes) {
   if (!bytes) return TOPK_EINVAL;
-  LinearGrad p;
-  const int rc = linear_grad_plan(args, &p, nullptr);
+  tk::GradArgs g;
+  const int rc = linear_grad(args, &g);
   if (rc) return rc;
-  *bytes = p.dz_bytes + p.step_bytes;
+  *bytes = tk::grad_workspace(g);
   return TOPK_OK;
 }
 
 int topk_linear_grad(const topk_linear_grad_args* args, void* workspace, size_t workspace_bytes,
                      void* stream) {
-  LinearGrad p;
-  char* ws = static_cast<char*>(workspace);
-  int rc = linear_grad_plan(args, &p, ws);
+  tk::GradArgs g;
+  int rc = linear_grad(args, &g);
   if (rc) return rc;
-  rc = check_ws(workspace, workspace_bytes, p.dz_bytes + p.step_bytes);
+  rc = check_ws(workspace, workspace_bytes, tk::grad_workspace(g));
   if (rc) return rc;
-  hipStream_t s = static_cast<hipStream_t>(stream);
-  void* step = ws ? ws + p.dz_bytes : nullptr;
-  hipError_t e = hipSuccess;
-  if (p.want_slope) e = tk::launch_slope(p.slope, step, s);
-  if (e == hipSuccess && p.want_dx) e = tk::launch_gemm(p.dx, step, s);
-  if (e == hipSuccess && p.want_dw) e = tk::launch_gemm(p.dw, step, s);
-  return status(e);
+  return status(tk::launch_grad(g, workspace, static_cast<hipStream_t>(stream)));
 }
 
 int topk_decode_workspace_size(const topk_selection* sel, int64_t d, size_t* bytes) {

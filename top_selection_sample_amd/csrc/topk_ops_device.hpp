@@ -34,7 +34,15 @@ __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ bf16_t from_f32<bf16_t>(float v) { return bf16_t{bf16_bits(v)}; }
 
-// 8 bf16 or 4 f32: one 16-byte vector of a row.
+// 8 bf16 or 4 f32: one 16-byte vector of a row.  Vectors are read and written
+// whole at any element alignment (global memory takes them; a row of odd length
+// costs a little more than an aligned one, and no more instructions).
+__device__ __forceinline__ u32x4 read16(const void* p) {
+  u32x4 q;
+  __builtin_memcpy(&q, p, 16);
+  return q;
+}
+
 template <class T> struct Vec;
 template <> struct Vec<float> {
   static constexpr int N = 4;
@@ -42,12 +50,16 @@ template <> struct Vec<float> {
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(q[i]);
   }
-  __device__ static void load(const float* p, float* v) { unpack(*reinterpret_cast<const u32x4*>(p), v); }
-  __device__ static void store(float* p, const float* v) {
-    f32x4 q;
+  __device__ static u32x4 pack(const float* v) {
+    u32x4 q;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = v[i];
-    *reinterpret_cast<f32x4*>(p) = q;
+    for (int i = 0; i < 4; ++i) q[i] = __float_as_uint(v[i]);
+    return q;
+  }
+  __device__ static void load(const float* p, float* v) { unpack(read16(p), v); }
+  __device__ static void store(float* p, const float* v) {
+    const u32x4 q = pack(v);
+    __builtin_memcpy(p, &q, 16);
   }
 };
 template <> struct Vec<bf16_t> {
@@ -59,18 +71,30 @@ template <> struct Vec<bf16_t> {
       v[2 * i + 1] = __uint_as_float(q[i] & 0xFFFF0000u);
     }
   }
-  __device__ static void load(const bf16_t* p, float* v) { unpack(*reinterpret_cast<const u32x4*>(p), v); }
-  __device__ static void store(bf16_t* p, const float* v) {
+  __device__ static u32x4 pack(const float* v) {
     u32x4 q;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       q[i] = (uint32_t)bf16_bits(v[2 * i]) | ((uint32_t)bf16_bits(v[2 * i + 1]) << 16);
-    *reinterpret_cast<u32x4*>(p) = q;
+    return q;
+  }
+  __device__ static void load(const bf16_t* p, float* v) { unpack(read16(p), v); }
+  __device__ static void store(bf16_t* p, const float* v) {
+    const u32x4 q = pack(v);
+    __builtin_memcpy(p, &q, 16);
   }
 };
 
-// VEC elements of a row that may end inside the vector: whole vectors when
-// VEC is the 16-byte width, single elements when VEC is 1.
+// The first of the VEC columns that a lane takes whose share begins at column
+// c: a row's last vector begins earlier, so that it ends with the row, and its
+// first columns are computed twice, the same both times.
+template <int VEC>
+__device__ __forceinline__ uint32_t column_of(uint32_t c, uint32_t d) {
+  if constexpr (VEC == 1) return c;
+  return c + VEC <= d ? c : d - VEC;   // d >= VEC
+}
+
+// VEC elements of a row: the 16-byte width, or 1.
 template <class T, int VEC>
 __device__ __forceinline__ void load_vec(const T* p, float* v) {
   if constexpr (VEC == 1) v[0] = to_f32(p[0]);
@@ -85,10 +109,8 @@ __device__ __forceinline__ void store_vec(T* p, const float* v) {
 // A whole vector past the caches.
 template <class T>
 __device__ __forceinline__ void stream_vec(T* p, const float* v) {
-  T q[Vec<T>::N];
-#pragma unroll
-  for (int i = 0; i < Vec<T>::N; ++i) q[i] = from_f32<T>(v[i]);
-  __builtin_nontemporal_store(__builtin_bit_cast(u32x4, q), reinterpret_cast<u32x4*>(p));
+  typedef u32x4 any_u32x4 __attribute__((aligned(2)));
+  __builtin_nontemporal_store(Vec<T>::pack(v), reinterpret_cast<any_u32x4*>(p));
 }
 
 // Activations in 32 bits.  Far left of zero gelu and silu are 0 and their

@@ -73,9 +73,11 @@ __device__ __forceinline__ float coef_of(const T* coef, const T* gate, uint32_t 
 constexpr uint32_t SORT_THREADS = 1024;
 constexpr uint32_t MAX_BINS = 16384;
 constexpr uint32_t GROUP = 64;          // bins of one k_scan workgroup
+constexpr uint32_t SMALL = 4096;        // entries that one workgroup sorts
 
 struct SortPlan {
   uint32_t keys = 0, total = 0;
+  bool small = false;                   // one workgroup sorts them all (k_sort_small)
   uint32_t passes = 1, width = 0;       // digit bits of a pass (0: the whole key)
   uint32_t max_bins = 0;
   uint32_t blocks = 0, per_block = 0;
@@ -93,6 +95,7 @@ SortPlan sort_plan(int64_t keys, int64_t total) {
   SortPlan p;
   p.keys = (uint32_t)keys;
   p.total = (uint32_t)total;
+  p.small = total <= SMALL;
   if (keys + 1 > (int64_t)MAX_BINS) {
     uint32_t bits = 0;
     while ((uint64_t(1) << bits) <= (uint64_t)keys) ++bits;   // the key `keys` itself is one
@@ -109,9 +112,11 @@ SortPlan sort_plan(int64_t keys, int64_t total) {
     at += align256(bytes);
     return here;
   };
-  p.off_cnt = take((size_t)p.blocks * p.max_bins * 4);
-  p.off_coarse = take((size_t)p.blocks * (p.max_bins / GROUP + 1) * 4);
-  if (p.passes > 1) p.off_pair = take((size_t)total * 16);   // two halves: the passes alternate
+  if (!p.small) {
+    p.off_cnt = take((size_t)p.blocks * p.max_bins * 4);
+    p.off_coarse = take((size_t)p.blocks * (p.max_bins / GROUP + 1) * 4);
+  }
+  if (!p.small && p.passes > 1) p.off_pair = take((size_t)total * 16);   // two halves: the passes alternate
   p.off_rec = take((size_t)total * 16);
   p.off_run = take((size_t)keys * 8);
   p.total_bytes = at;
@@ -274,6 +279,111 @@ __global__ __launch_bounds__(SORT_THREADS) void k_place(KSel s, KPasses ps, cons
   }
 }
 
+// Few entries: one workgroup sorts them in LDS, eight bits of the key at a
+// time, in one launch instead of three or six.  Each of its 16 waves holds
+// consecutive entries, at most four to a lane, and counts their digits on its
+// own (lanes with equal digits are found by ballots, so the order is kept);
+// the counts' prefix over digits, then waves, gives the places.  Workgroups
+// beyond the first only clear their share of the runs' bounds.
+template <class T>
+__global__ __launch_bounds__(SORT_THREADS) void k_sort_small(KSel s, KPasses ps, const T* __restrict__ coef,
+                                                             const T* __restrict__ gate) {
+  constexpr uint32_t ROUNDS = SMALL / SORT_THREADS, WAVES = SORT_THREADS / 64;
+  __shared__ uint32_t keys[SMALL], ents[SMALL], other[SMALL];
+  __shared__ uint32_t cnt[WAVES][256];
+  __shared__ uint32_t below[4];
+  const KPass& p = ps.p[blockIdx.y];
+  for (uint64_t i = (uint64_t)blockIdx.x * SORT_THREADS + threadIdx.x; i < p.keys; i += (uint64_t)gridDim.x * SORT_THREADS)
+    p.run[2 * i] = NO_ENTRY;
+  if (blockIdx.x) return;
+  const uint32_t wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+  const uint32_t rounds = (p.total + SORT_THREADS - 1) / SORT_THREADS;   // at most ROUNDS
+  const uint32_t first = wave * rounds * 64 + lane;
+  uint32_t key[ROUNDS], ent[ROUNDS];
+#pragma unroll
+  for (uint32_t r = 0; r < ROUNDS; ++r) {
+    const uint32_t e = first + r * 64;
+    key[r] = p.keys;
+    ent[r] = e;
+    if (r < rounds && e < p.total) {
+      uint32_t row = 0, latent = 0;
+      const bool good = entry_of(s, e, s.idx[e], &row, &latent);
+      key[r] = good ? (p.by_row ? row : latent) : p.keys;
+      other[e] = good ? (p.by_row ? latent : row) : 0u;
+    }
+  }
+  for (uint32_t shift = 0; shift < p.digit_bits; shift += 8) {
+    for (uint32_t i = lane; i < 256; i += 64) cnt[wave][i] = 0;
+    uint32_t rank[ROUNDS];
+#pragma unroll
+    for (uint32_t r = 0; r < ROUNDS; ++r) {
+      if (r >= rounds) break;
+      const bool in = first + r * 64 < p.total;
+      const uint32_t d = key[r] >> shift & 255u;
+      uint64_t same = __ballot(in);
+#pragma unroll
+      for (uint32_t b = 0; b < 8; ++b) {
+        const bool bit = d >> b & 1u;
+        const uint64_t m = __ballot(bit);
+        same &= bit ? m : ~m;
+      }
+      const uint32_t before = __popcll(same & ((uint64_t(1) << lane) - 1));
+      if (in) {
+        const uint32_t c = cnt[wave][d];
+        rank[r] = c + before;
+        if (before == 0) cnt[wave][d] = c + (uint32_t)__popcll(same);
+      }
+    }
+    __syncthreads();
+    if (threadIdx.x < 256) {     // a thread is a digit
+      uint32_t c[WAVES], sum = 0;
+#pragma unroll
+      for (uint32_t w = 0; w < WAVES; ++w) {
+        c[w] = cnt[w][threadIdx.x];
+        sum += c[w];
+      }
+      uint32_t up = sum;
+#pragma unroll
+      for (uint32_t o = 1; o < 64; o <<= 1) {
+        const uint32_t t = __shfl_up(up, o);
+        if (lane >= o) up += t;
+      }
+      if (lane == 63) below[wave] = up;
+      uint32_t at = up - sum;
+#pragma unroll
+      for (uint32_t w = 0; w < WAVES; ++w) {
+        cnt[w][threadIdx.x] = at;
+        at += c[w];
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (uint32_t r = 0; r < ROUNDS; ++r) {
+      if (r >= rounds || first + r * 64 >= p.total) break;
+      const uint32_t d = key[r] >> shift & 255u;
+      uint32_t at = cnt[wave][d] + rank[r];
+      for (uint32_t q = 0; q < d / 64; ++q) at += below[q];
+      keys[at] = key[r];
+      ents[at] = ent[r];
+    }
+    __syncthreads();
+#pragma unroll
+    for (uint32_t r = 0; r < ROUNDS; ++r) {
+      if (r >= rounds || first + r * 64 >= p.total) break;
+      key[r] = keys[first + r * 64];
+      ent[r] = ents[first + r * 64];
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (uint32_t r = 0; r < ROUNDS; ++r) {
+    const uint32_t i = first + r * 64;
+    if (r >= rounds || i >= p.total) break;
+    const float w = key[r] < p.keys ? coef_of(coef, gate, ent[r]) : 0.f;
+    p.rec[i] = u32x4{key[r], other[ent[r]], __float_as_uint(w), ent[r]};
+  }
+}
+
 // ---------------------------------------------------------------- sums
 struct KSeg {
   const u32x4* rec;     // sorted (key, the other index, coefficient, entry)
@@ -295,19 +405,34 @@ struct KSegs {
   KSeg s[2];
 };
 
-// One lane's share of a row: NV vectors of VEC elements, 64 VEC apart, kept as
-// they were read until they are used.
+// A lane's share of the d columns: NV vectors of VEC of them, 64 VEC apart.
+template <int VEC, int NV>
+struct Share {
+  uint32_t at[NV];     // first column of each vector
+  uint32_t twice[NV];  // its first columns that another lane holds too
+  bool in[NV];
+  __device__ __forceinline__ Share(uint32_t c, uint32_t d) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const uint32_t b = c + v * 64 * VEC;
+      in[v] = b < d;
+      at[v] = in[v] ? column_of<VEC>(b, d) : 0u;
+      twice[v] = in[v] ? b - at[v] : 0u;
+    }
+  }
+};
+
+// One lane's share of a row, kept as it was read until it is used.
 template <class T, int VEC, int NV>
 struct Row {
   u32x4 q[NV];
-  __device__ __forceinline__ void load(const T* p, uint32_t c, uint32_t d, bool there) {
+  __device__ __forceinline__ void load(const T* p, const Share<VEC, NV>& c, bool there) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const uint32_t at = c + v * 64 * VEC;
       q[v] = u32x4{0u, 0u, 0u, 0u};
-      if (there && at < d) {
-        if constexpr (VEC == 1) q[v][0] = __float_as_uint(to_f32(p[at]));
-        else q[v] = *reinterpret_cast<const u32x4*>(p + at);
+      if (there && c.in[v]) {
+        if constexpr (VEC == 1) q[v][0] = __float_as_uint(to_f32(p[c.at[v]]));
+        else q[v] = read16(p + c.at[v]);
       }
     }
   }
@@ -316,6 +441,16 @@ struct Row {
     else Vec<T>::unpack(q[v], f);
   }
 };
+
+template <int VEC>
+__device__ __forceinline__ void store_part(float* o, const float* v) {
+  if constexpr (VEC == 1) {
+    o[0] = v[0];
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; i += 4) Vec<float>::store(o + i, v + i);
+  }
+}
 
 // Eight sums over 64 lanes: each of the first three exchanges halves the
 // number of sums a lane carries, so lane l ends with the sum of entry l % 8.
@@ -341,7 +476,8 @@ __device__ __forceinline__ float eight_sums(float* sum, uint32_t lane) {
 // branch.  With DOTS the wave also takes each entry's dot product of its
 // source row and its key's row of wsrc, which neighbouring entries of a run
 // find in the first-level cache.
-template <class T, int VEC, int NV, int AHEAD, bool DOTS>
+// RAGGED: the last vector of a row begins in the one before it.
+template <class T, int VEC, int NV, int AHEAD, bool DOTS, bool RAGGED>
 __global__ __launch_bounds__(256) void k_seg(KSegs ss) {
   const KSeg& p = ss.s[blockIdx.z];
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
@@ -350,7 +486,7 @@ __global__ __launch_bounds__(256) void k_seg(KSegs ss) {
   if (first >= p.total) return;
   const uint32_t e0 = (uint32_t)first;
   const uint32_t e1 = p.total - e0 < p.chunk ? p.total : e0 + p.chunk;
-  const uint32_t c = (blockIdx.y * 64 * NV + lane) * VEC;
+  const Share<VEC, NV> cols((blockIdx.y * 64 * NV + lane) * VEC, p.d);
   const bool one = blockIdx.y == 0 && lane == 0;
   const T* src = static_cast<const T*>(p.src);
   const T* wsrc = static_cast<const T*>(p.wsrc);
@@ -367,26 +503,17 @@ __global__ __launch_bounds__(256) void k_seg(KSegs ss) {
       if (came || goes) {
         const size_t slot = (size_t)chunk * 2 + (came ? 0 : 1);
         if (p.out) {
-          float* o = p.part + slot * p.d;
 #pragma unroll
-          for (int v = 0; v < NV; ++v) {
-            const uint32_t at = c + v * 64 * VEC;
-            if (at >= p.d) continue;
-            if constexpr (VEC == 1) {
-              o[at] = acc[v][0];
-            } else {
-#pragma unroll
-              for (int i = 0; i < VEC; i += 4) Vec<float>::store(o + at + i, acc[v] + i);
-            }
-          }
+          for (int v = 0; v < NV; ++v)
+            if (cols.in[v]) store_part<VEC>(p.part + slot * p.d + cols.at[v], acc[v]);
         }
         if (p.coef_sum && one) p.part_c[slot] = csum;
       } else {
         if (p.out) {
 #pragma unroll
           for (int v = 0; v < NV; ++v) {
-            const uint32_t at = c + v * 64 * VEC;
-            if (at >= p.d) continue;
+            if (!cols.in[v]) continue;
+            const uint32_t at = cols.at[v];
             if (p.bias) {
               float b[VEC];
               load_vec<T, VEC>(static_cast<const T*>(p.bias) + at, b);
@@ -419,8 +546,8 @@ __global__ __launch_bounds__(256) void k_seg(KSegs ss) {
       for (uint32_t u = 0; u < AHEAD; ++u) {   // i0 + u < 64; lanes beyond `have` hold no key
         const uint32_t o = __builtin_amdgcn_readlane(lo, i0 + u);
         const uint32_t k = __builtin_amdgcn_readlane(lk, i0 + u);
-        row[u].load(src + (int64_t)o * p.lds, c, p.d, k < p.keys);
-        if constexpr (DOTS) wrow[u].load(wsrc + (int64_t)k * p.ldw, c, p.d, k < p.keys);
+        row[u].load(src + (int64_t)o * p.lds, cols, k < p.keys);
+        if constexpr (DOTS) wrow[u].load(wsrc + (int64_t)k * p.ldw, cols, k < p.keys);
       }
       float dot[AHEAD];
 #pragma unroll
@@ -441,6 +568,10 @@ __global__ __launch_bounds__(256) void k_seg(KSegs ss) {
           if constexpr (DOTS) {
             float g[VEC];
             wrow[u].unpack(v, g);
+            if constexpr (RAGGED) {   // columns that another lane takes
+#pragma unroll
+              for (int i = 0; i < VEC; ++i) g[i] = (uint32_t)i < cols.twice[v] ? 0.f : g[i];
+            }
 #pragma unroll
             for (int i = 0; i < VEC; ++i) dot[u] = fmaf(f[i], g[i], dot[u]);
           }
@@ -520,7 +651,8 @@ __global__ __launch_bounds__(256) void k_join_runs(KSegs ss) {
       static_cast<T*>(p.coef_sum)[k0 + i] = from_f32<T>(s);
     }
     if (!p.out || q1 - q0 > LONG) continue;
-    for (uint32_t c = lane * VEC; c < p.d; c += 64 * VEC) {
+    for (uint32_t b = lane * VEC; b < p.d; b += 64 * VEC) {
+      const uint32_t c = column_of<VEC>(b, p.d);
       float acc[VEC] = {};
       add_parts<VEC>(acc, p, q0, q0, q1, c);
       write_key<T, VEC>(p, k0 + i, c, acc);
@@ -533,13 +665,14 @@ __global__ __launch_bounds__(256) void k_join_runs(KSegs ss) {
     const uint32_t q0 = __builtin_amdgcn_readlane(lq0, i), q1 = __builtin_amdgcn_readlane(lq1, i);
     const uint32_t per = (q1 - q0 + 3) / 4, a0 = q0 + wave * per, a1 = a0 + per < q1 ? a0 + per : q1;
     for (uint32_t b = 0; b < p.d; b += 64 * VEC) {
-      const uint32_t c = b + lane * VEC;
+      const bool in = b + lane * VEC < p.d;
+      const uint32_t c = in ? column_of<VEC>(b + lane * VEC, p.d) : 0u;
       float acc[VEC] = {};
-      if (c < p.d) add_parts<VEC>(acc, p, q0, a0, a1, c);
+      if (in) add_parts<VEC>(acc, p, q0, a0, a1, c);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) join[wave][lane * VEC + j] = acc[j];
       __syncthreads();
-      if (wave == 0 && c < p.d) {
+      if (wave == 0 && in) {
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
           const uint32_t a = lane * VEC + j;
@@ -569,8 +702,9 @@ __global__ __launch_bounds__(256) void k_rows(KSel s, KSeg p, const T* __restric
   __shared__ float join[4][64 * VEC];
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
   const uint32_t row = blockIdx.x;
-  const uint32_t c = (blockIdx.y * 64 + lane) * VEC;
-  const bool in = c < p.d;
+  const Share<VEC, 1> cols((blockIdx.y * 64 + lane) * VEC, p.d);
+  const uint32_t c = cols.at[0];
+  const bool in = cols.in[0];
   const T* src = static_cast<const T*>(p.src);
   float acc[VEC] = {};
   const uint32_t e0 = s.flat ? 0u : row * s.k, e1 = s.flat ? s.total : e0 + s.k;
@@ -597,20 +731,22 @@ __global__ __launch_bounds__(256) void k_rows(KSel s, KSeg p, const T* __restric
     }
     // sum what is held
     for (uint32_t i0 = wave * ROWS_AHEAD; i0 < held; i0 += 4 * ROWS_AHEAD) {
-      float v[ROWS_AHEAD][VEC], w[ROWS_AHEAD];
+      Row<T, VEC, 1> v[ROWS_AHEAD];
+      float w[ROWS_AHEAD];
 #pragma unroll
       for (uint32_t u = 0; u < ROWS_AHEAD; ++u) {
         const bool there = i0 + u < held;
         const uint32_t o = __builtin_amdgcn_readfirstlane(there ? ent[i0 + u] : 0u);
         w[u] = there ? cf[i0 + u] : 0.f;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) v[u][i] = 0.f;
-        if (in && there) load_vec<T, VEC>(src + (int64_t)o * p.lds + c, v[u]);
+        v[u].load(src + (int64_t)o * p.lds, cols, there);
       }
 #pragma unroll
-      for (uint32_t u = 0; u < ROWS_AHEAD; ++u)
+      for (uint32_t u = 0; u < ROWS_AHEAD; ++u) {
+        float f[VEC];
+        v[u].unpack(0, f);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) acc[i] = fmaf(w[u], v[u][i], acc[i]);
+        for (int i = 0; i < VEC; ++i) acc[i] = fmaf(w[u], f[i], acc[i]);
+      }
     }
     held = 0;
     __syncthreads();
@@ -650,32 +786,30 @@ __global__ __launch_bounds__(256) void k_dots(KSel s, const T* __restrict__ g, i
   const bool good = lane < DOTS && e0 + lane < s.total && entry_of(s, e0 + lane, s.idx[e0 + lane], &row, &latent);
   const uint64_t ok = __ballot(good);
   float sum[DOTS] = {};
-  for (uint32_t c = lane * VEC; c < (d + 64 * VEC - 1) / (64 * VEC) * (64 * VEC); c += 64 * VEC) {
-    float a[DOTS][VEC], b[DOTS][VEC];
+  for (uint32_t b = 0; b < d; b += 64 * VEC) {
+    const Share<VEC, 1> cols(b + lane * VEC, d);
+    Row<T, VEC, 1> x[DOTS], y[DOTS];
 #pragma unroll
     for (uint32_t u = 0; u < DOTS; ++u) {
       const uint32_t r = __builtin_amdgcn_readlane(row, u), j = __builtin_amdgcn_readlane(latent, u);
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) a[u][i] = b[u][i] = 0.f;
-      if (c < d && (ok >> u & 1)) {
-        load_vec<T, VEC>(g + (int64_t)r * ldg + c, a[u]);
-        load_vec<T, VEC>(w + (int64_t)j * ldw + c, b[u]);
-      }
+      const bool there = ok >> u & 1;
+      x[u].load(g + (int64_t)r * ldg, cols, there);
+      y[u].load(w + (int64_t)j * ldw, cols, there);
     }
 #pragma unroll
-    for (uint32_t u = 0; u < DOTS; ++u)
+    for (uint32_t u = 0; u < DOTS; ++u) {
+      float f[VEC], h[VEC];
+      x[u].unpack(0, f);
+      y[u].unpack(0, h);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) sum[u] = fmaf(a[u][i], b[u][i], sum[u]);
+      for (int i = 0; i < VEC; ++i) sum[u] = fmaf(f[i], (uint32_t)i < cols.twice[0] ? 0.f : h[i], sum[u]);
+    }
   }
   const float v = eight_sums(sum, lane);
   if (lane < DOTS && e0 + lane < s.total) dv[e0 + lane] = from_f32<T>(v);
 }
 
 // ---------------------------------------------------------------- host side
-bool aligned16(const void* p, int64_t ld, int64_t es) {
-  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld * es) % 16 == 0;
-}
-
 // Rows straight from the selection: row-wise, or few enough reads that every
 // row may look at every index (4096 rows and entries: 128 MB out of the
 // caches, where the sort's three launches alone take longer).
@@ -713,6 +847,24 @@ hipError_t run_sorts(const SegCall& a, const SegArgs* const* parts, const SegPla
   const KSel sel = ksel(a.sel);
   const T* coef = static_cast<const T*>(a.coef);
   const T* gate = static_cast<const T*>(a.gate);
+  if (plans[0].sort.small) {   // (the same for both: it follows from the entries)
+    KPasses ks{};
+    uint32_t keys = 0;
+    for (int i = 0; i < n; ++i) {
+      const SortPlan& p = plans[i].sort;
+      KPass& k = ks.p[i];
+      k.rec = reinterpret_cast<u32x4*>(ws[i] + p.off_rec);
+      k.run = reinterpret_cast<uint32_t*>(ws[i] + p.off_run);
+      k.keys = p.keys;
+      k.total = p.total;
+      k.by_row = parts[i]->by_row;
+      while (k.digit_bits < 32 && (uint64_t(1) << k.digit_bits) <= p.keys) ++k.digit_bits;   // of the key `keys`
+      keys = std::max(keys, p.keys);
+    }
+    const uint32_t x = 1 + std::min<uint32_t>(keys / (4 * SORT_THREADS), 255);
+    hipLaunchKernelGGL((k_sort_small<T>), dim3(x, n), dim3(SORT_THREADS), 0, s, sel, ks, coef, gate);
+    return hipGetLastError();
+  }
   uint32_t most = 0;
   for (int i = 0; i < n; ++i) most = std::max(most, plans[i].sort.passes);
   for (uint32_t pass = 0; pass < most; ++pass) {
@@ -756,22 +908,19 @@ hipError_t run_sorts(const SegCall& a, const SegArgs* const* parts, const SegPla
 }
 
 template <class T>
-bool wide_part(const SegArgs& a, int64_t d) {
-  constexpr int64_t ES = sizeof(T);
-  return d % Vec<T>::N == 0 && aligned16(a.src, a.lds, ES) && aligned16(a.out, a.ldo, ES) && aligned16(a.bias, 0, ES) &&
-         aligned16(a.other, a.ldother, ES);
-}
-
-template <class T>
 hipError_t launch_sums(const KSegs& ks, int n, bool wide, uint32_t chunks, int64_t d, bool dots, hipStream_t s) {
   constexpr int V = Vec<T>::N;
   const int64_t span = 64 * (wide ? V : 1), vecs = std::max<int64_t>(1, ceil_div(d, span));
   if (chunks) {
     const uint32_t x = (uint32_t)ceil_div(chunks, 4);
-    if (dots && vecs == 1) hipLaunchKernelGGL((k_seg<T, V, 1, 8, true>), dim3(x, 1, n), dim3(256), 0, s, ks);
-    else if (dots) hipLaunchKernelGGL((k_seg<T, V, 2, 8, true>), dim3(x, 1, n), dim3(256), 0, s, ks);
-    else if (wide) hipLaunchKernelGGL((k_seg<T, V, 1, 16, false>), dim3(x, (uint32_t)vecs, n), dim3(256), 0, s, ks);
-    else hipLaunchKernelGGL((k_seg<T, 1, 1, 16, false>), dim3(x, (uint32_t)vecs, n), dim3(256), 0, s, ks);
+    const dim3 one(x, 1, n), all(x, (uint32_t)vecs, n);
+    const bool ragged = d % V;
+    if (dots && vecs == 1 && ragged) hipLaunchKernelGGL((k_seg<T, V, 1, 8, true, true>), one, dim3(256), 0, s, ks);
+    else if (dots && vecs == 1) hipLaunchKernelGGL((k_seg<T, V, 1, 8, true, false>), one, dim3(256), 0, s, ks);
+    else if (dots && ragged) hipLaunchKernelGGL((k_seg<T, V, 2, 8, true, true>), one, dim3(256), 0, s, ks);
+    else if (dots) hipLaunchKernelGGL((k_seg<T, V, 2, 8, true, false>), one, dim3(256), 0, s, ks);
+    else if (wide) hipLaunchKernelGGL((k_seg<T, V, 1, 16, false, false>), all, dim3(256), 0, s, ks);
+    else hipLaunchKernelGGL((k_seg<T, 1, 1, 16, false, false>), all, dim3(256), 0, s, ks);
   }
   uint32_t keys = ks.s[0].keys;
   if (n > 1) keys = std::max(keys, ks.s[1].keys);
@@ -789,11 +938,11 @@ hipError_t run_seg(const SegCall& a, char* ws, hipStream_t s) {
   char* at[2];
   KSegs ks;
   int n = 0;
-  bool wide = true, dots = false;
+  const bool wide = a.d >= V;   // rows of at least one vector
+  bool dots = false;
   for (int i = 0; i < a.parts; ++i) {
     const SegArgs& p = a.part[i];
     const int64_t keys = p.by_row ? a.sel.rows : a.sel.n;
-    const bool own_wide = wide_part<T>(p, a.d);
     KSeg k{};
     k.src = p.src;
     k.bias = p.bias;
@@ -806,7 +955,7 @@ hipError_t run_seg(const SegCall& a, char* ws, hipStream_t s) {
     k.d = (uint32_t)a.d;
     if (p.dots) {
       // fused where a lane holds its whole share of both rows
-      if (own_wide && a.d <= 128 * V && a.sel.total) {
+      if (wide && a.d <= 128 * V && a.sel.total) {
         dots = true;
         k.wsrc = p.other;
         k.ldw = p.ldother;
@@ -826,11 +975,11 @@ hipError_t run_seg(const SegCall& a, char* ws, hipStream_t s) {
     }
     if (keys == 0 || ((a.d == 0 || !p.out) && !p.coef_sum && !k.dots)) continue;
     if (p.by_row && rows_direct(a.sel)) {
-      const uint32_t columns = (uint32_t)ceil_div(a.d, 64 * (own_wide ? V : 1));
+      const uint32_t columns = (uint32_t)ceil_div(a.d, 64 * (wide ? V : 1));
       const dim3 grid(k.keys, columns);
       const T* coef = static_cast<const T*>(a.coef);
       const T* gate = static_cast<const T*>(a.gate);
-      if (own_wide) hipLaunchKernelGGL((k_rows<T, (int)V>), grid, dim3(256), 0, s, ksel(a.sel), k, coef, gate);
+      if (wide) hipLaunchKernelGGL((k_rows<T, (int)V>), grid, dim3(256), 0, s, ksel(a.sel), k, coef, gate);
       else hipLaunchKernelGGL((k_rows<T, 1>), grid, dim3(256), 0, s, ksel(a.sel), k, coef, gate);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
@@ -843,7 +992,6 @@ hipError_t run_seg(const SegCall& a, char* ws, hipStream_t s) {
     k.part = reinterpret_cast<float*>(ws + plans[n].off_part);
     k.part_c = reinterpret_cast<float*>(ws + plans[n].off_part_c);
     k.chunk = plans[n].chunk;
-    wide = wide && own_wide;
     sorted[n] = &p;
     at[n] = ws;
     ks.s[n++] = k;
@@ -860,8 +1008,8 @@ hipError_t run_seg(const SegCall& a, char* ws, hipStream_t s) {
 
 template <class T>
 hipError_t run_dots(const DotArgs& a, hipStream_t s) {
-  constexpr int64_t ES = sizeof(T), V = Vec<T>::N;
-  const bool wide = a.d % V == 0 && aligned16(a.g, a.ldg, ES) && aligned16(a.w, a.ldw, ES);
+  constexpr int64_t V = Vec<T>::N;
+  const bool wide = a.d >= V;
   const dim3 grid((uint32_t)ceil_div(a.sel.total, 4 * DOTS));
   const T* g = static_cast<const T*>(a.g);
   const T* w = static_cast<const T*>(a.w);
