@@ -244,8 +244,11 @@ __device__ __forceinline__ void mma_all(const u32x4* w, const u32x4* x, f32x4 (&
 // Tile of a workgroup.  Consecutive workgroups go to the eight dies in turn,
 // so each die gets a contiguous range of tiles, and walks it in bands of
 // 1024 rows: W's tile and the band's rows of x then stay in the die's L2
-// (4096 x 512 x 65536 bf16 in 256-tiles: 358 us in bands of 4 tiles, 380 to
-// 451 in bands of 1, 8, 16 or 32).
+// (4096 x 512 x 65536 bf16 in 256-tiles: 360 us in bands of 4 tiles, 380 to
+// 451 in bands of 1, 8, 16 or 32).  Each band begins 37 tiles further right:
+// dies that work on different bands would else store the same columns at the
+// same time, and where the row stride is a power of two those lie in the same
+// memory channels (338 us with the shift; 322 for rows of 65600).
 __device__ __forceinline__ void tile_of(uint32_t id, uint32_t total, uint32_t tm, uint32_t tn,
                                         uint32_t* im, uint32_t* in, uint32_t band_rows) {
   const uint32_t q = total / 8, r = total % 8, x = id % 8;
@@ -254,7 +257,7 @@ __device__ __forceinline__ void tile_of(uint32_t id, uint32_t total, uint32_t tm
   const uint32_t rows = tm - band * band_rows < band_rows ? tm - band * band_rows : band_rows;
   const uint32_t at = id - band * band_rows * tn;
   *im = band * band_rows + at % rows;
-  *in = at / rows;
+  *in = (at / rows + band * 37) % tn;
 }
 
 // One step: the tiles of step kt are in `cur`; the loads of step kt + 1 go to
@@ -272,6 +275,8 @@ __device__ __forceinline__ void gemm_step(lds_char* cur, lds_char* next, LA& la,
       la.issue(next, kt + 1, wave);
       lb.issue(next + TM * 128, kt + 1, wave);
     }
+    // the loads leave now: the scheduler would let them sink to the end of the step
+    __builtin_amdgcn_sched_barrier(0);
   };
   if constexpr (FM * FN <= 16) {
     // both halves' fragments first: the second half's reads are covered by the first half's products
