@@ -325,7 +325,8 @@ int topk_stream_read(const void* data, size_t bytes, uint32_t* sink, void* strea
  *     rows are not all 16-byte aligned through a copy in its workspace.
  *   - Sizes may be 0: an empty sum is 0.  No size or stride reaches 2^31; n and
  *     k of a product (and m, where x_trans is set) and the row width d of a
- *     decode stay below 2^22.
+ *     decode stay below 2^22, the rows and latents of a
+ *     selection below 2^28.
  *   - Every result is the same from call to call: no sum's order depends on
  *     timing.
  *   - `workspace`: 256-byte aligned device memory of at least the size that
@@ -422,7 +423,9 @@ int topk_decode(const topk_selection* sel, const void* weight, int64_t ldw, int6
  *   dweight[j] = sum over the entries e of latent j of values[e] * grad[row e]
  *   ([n, d], row stride lddw, every row written);
  *   dbias = the sum of grad's rows ([d]).
- * Each output may be null: not wanted. */
+ * Each output may be null: not wanted.  (dvalues is summed in another order
+ * when dweight is computed with it, so its last bit may differ from a call
+ * that asks for it alone.) */
 int topk_decode_grad(const topk_selection* sel, const void* weight, int64_t ldw, int64_t d,
                      const void* grad, int64_t ldg, void* dvalues, void* dweight, int64_t lddw,
                      void* dbias, void* workspace, size_t workspace_bytes, void* stream);

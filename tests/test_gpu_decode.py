@@ -90,6 +90,14 @@ def test_flattened(rows, total, n, d, dt):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,total,n,d", [(2000, 1_200_000, 3001, 9), (3, 4096, 300_000, 20), (3, 4097, 300_000, 20),
+                                            (9, 100_000, 20_000, 17)])
+def test_many_entries_and_many_latents(rows, total, n, d, dt):
+    idx = ints(14, rows * n, total)      # places may repeat
+    check_all(rnd(15, total, dt=dt), idx, rows, n, d, dt, f"{total} of {rows}x{n}")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("shape", ["one row", "one latent", "every fourth row", "last place"])
 def test_uneven(shape, dt):
     rows, n, d = 200, 6000, 48

@@ -51,6 +51,40 @@ def test_sizes(m, n, k, dt):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("m,n,k", [(2100, 4100, 136), (4136, 2049, 72), (4096, 4096, 64), (5000, 700, 1032), (300, 17000, 200)])
+def test_large_tiles(m, n, k, dt):
+    # the larger tiles, outputs that are stored past the caches, edges in both directions, either order of the operands
+    x, w, b, r = rnd(70, m, k, dt=dt), rnd(71, n, k, dt=dt, scale=k ** -0.5), rnd(72, n, dt=dt), rnd(73, m, n, dt=dt)
+    want = U.linear64(x, w, b, "silu", r)
+    xt, wt = x.t().contiguous().t(), w.t().contiguous().t()
+    for xx, ww in ((x, w), (x, wt), (xt, w), (xt, wt)):
+        U.within(tss().linear(xx, ww, b, activation="silu", residual=r), want[0], want[1], f"{m}x{n}x{k}")
+    dy = rnd(74, m, n, dt=dt)
+    refs, errs = U.linear_grad64(dy, x, w, r, "gelu")
+    for got, ref, err in zip(tss().linear_grad(dy, x, w, activation="gelu", pre=r), refs, errs):
+        U.within(got, ref, err, f"gradient {m}x{n}x{k}")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("m,n,k", [(4, 40, 64), (70, 130, 96), (4100, 4104, 64)])
+def test_residual_in_place_and_pre_activation_through_the_abi(m, n, k, dt):
+    import ctypes
+    lib = tss()._lib
+    x, w, y = rnd(75, m, k, dt=dt), rnd(76, n, k, dt=dt, scale=0.2), rnd(77, m, n + 3, dt=dt)
+    start, pre = y.clone(), torch.full((m, n + 1), 5.0, dtype=DT[dt], device="cuda")
+    a = lib.LinearArgs(x.data_ptr(), w.data_ptr(), None, y.data_ptr(), y.data_ptr(), pre.data_ptr(), m, n, k, k, k,
+                       n + 3, n + 3, n + 1, tss().dtype_code(DT[dt]), lib.ACTIVATIONS["gelu"], 0, 0)
+    size = ctypes.c_size_t()
+    assert lib.lib.topk_linear_workspace_size(ctypes.byref(a), ctypes.byref(size)) == 0
+    ws = torch.empty(size.value + 1, dtype=torch.uint8, device="cuda")
+    assert lib.lib.topk_linear(ctypes.byref(a), ws.data_ptr(), size.value, torch.cuda.current_stream().cuda_stream) == 0
+    ref, err, z = U.linear64(x, w, None, "gelu", start[:, :n])
+    U.within(y[:, :n], ref, err)
+    U.within(pre[:, :n], z, (k + 3) * U.U32 * (x.double().abs() @ w.double().abs().t().contiguous()))
+    assert torch.equal(y[:, n:], start[:, n:]) and bool((pre[:, n:] == 5).all())   # nothing behind the rows
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("act", ["none", "relu", "gelu", "silu"])
 @pytest.mark.parametrize("with_bias,with_res", [(0, 0), (1, 0), (0, 1), (1, 1)])
 def test_epilogue(act, with_bias, with_res, dt):

@@ -129,3 +129,26 @@ def test_captured_step_next_to_eager_ones():
         for a, p in zip(grads, eager):
             assert float((a - p.grad).norm()) <= 1e-5 * float(a.norm())
     held.backward()
+
+
+def test_autograd_is_refused_under_capture():
+    # a captured backward next to a live eager graph of the same leaves would end the process
+    T = tss()
+    x, params = model(torch.float32)
+    we, be, wd, bd = params
+    leaf = we.clone().requires_grad_(True)
+    eager = T.linear(x, leaf)
+    v, i = T.encode(x, we, be, 32)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for call in (lambda: T.linear(x, leaf), lambda: T.encode(x, leaf, be, 32),
+                     lambda: T.decode(v, i, leaf, rows=x.shape[0])):
+            with pytest.raises(RuntimeError, match="capture"):
+                call()
+        with torch.no_grad():
+            out = T.linear(x, leaf)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, eager)
+    eager.sum().backward()

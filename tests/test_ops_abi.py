@@ -39,7 +39,8 @@ def size_of(fn, a):
     (dict(y=None), EINVAL), (dict(ldx=31), EINVAL), (dict(ldw=1), EINVAL), (dict(ldy=15), EINVAL), (dict(ldx=-32), EINVAL),
     (dict(x=A + 1), EINVAL), (dict(bias=A + 1), EINVAL), (dict(residual=A, ldr=3), EINVAL), (dict(pre=A, ldp=0), EINVAL),
     (dict(x_trans=1, ldx=7), EINVAL), (dict(w_trans=1, ldw=15), EINVAL), (dict(dtype=1, y=A + 2), EINVAL),
-    (dict(ldy=1 << 31), EINVAL)])
+    (dict(ldy=1 << 31), EINVAL), (dict(k=1 << 22, ldx=1 << 22, ldw=1 << 22), EINVAL), (dict(n=1 << 22, ldy=1 << 22), EINVAL),
+    (dict(x_trans=1, m=1 << 22, ldx=1 << 22), EINVAL), (dict(m=(1 << 31) - 1, n=1 << 12, ldy=1 << 12), EINVAL)])
 def test_linear_refusals(kw, want):
     a = linear_args(**kw)
     assert size_of(L.topk_linear_workspace_size, a)[0] == want
@@ -86,7 +87,7 @@ def sel(**kw):
 @pytest.mark.parametrize("kw,want", [
     (dict(dtype=0), EDTYPE), (dict(dtype=3), EDTYPE), (dict(rows=-1), EINVAL), (dict(k=-1), EINVAL), (dict(n=1 << 31), EINVAL),
     (dict(values=None), EINVAL), (dict(indices=None), EINVAL), (dict(indices=A + 4), EINVAL), (dict(values=A + 2), EINVAL),
-    (dict(flat=0, rows=1 << 20, k=1 << 20), EINVAL)])
+    (dict(flat=0, rows=1 << 20, k=1 << 20), EINVAL), (dict(n=1 << 28), EINVAL), (dict(rows=1 << 28), EINVAL)])
 def test_selection_refusals(kw, want):
     s = ctypes.byref(sel(**kw))
     assert L.topk_decode(s, A, 64, 64, None, A, 64, A, 1 << 40, None) == want
@@ -100,6 +101,7 @@ def test_decode_refusals():
     assert L.topk_decode_workspace_size(s, 64, ctypes.byref(size)) == OK
     assert L.topk_decode_workspace_size(s, 64, None) == EINVAL
     assert L.topk_decode_workspace_size(s, -1, ctypes.byref(size)) == EINVAL
+    assert L.topk_decode_workspace_size(s, 1 << 22, ctypes.byref(size)) == EINVAL
     assert L.topk_decode_workspace_size(None, 64, ctypes.byref(size)) == EINVAL
     big = 1 << 40
     for args in ((None, 64, 64, None, A, 64), (A, 63, 64, None, A, 64), (A, 64, -1, None, A, 64), (A, 64, 64, A + 1, A, 64),

@@ -96,9 +96,16 @@ def _act_code(activation: str) -> int:
 
 
 def _wants_grad(*tensors) -> bool:
+    """Whether autograd records the call.  Not under graph capture: a captured
+    backward meets the gradient accumulators of whatever eager graph of the
+    same leaves is alive, on streams that are not captured, and that ends the
+    process; the *_grad functions take no part in autograd and can be captured."""
     if torch.is_grad_enabled():
         for t in tensors:
             if t is not None and t.requires_grad:
+                if torch.cuda.is_current_stream_capturing():
+                    raise RuntimeError("autograd cannot record this call under graph capture: call it with "
+                                       "gradients off (torch.no_grad) and its *_grad function")
                 return True
     return False
 
@@ -186,8 +193,8 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = No
     transpose of a [k, n] tensor is read in place), ``bias`` [n], ``residual``
     [..., n]; float32 or bfloat16, all alike.  ``activation``: "none", "relu",
     "gelu" (z * Phi(z)) or "silu".  Sums and the epilogue are held in 32 bits.
-    Differentiable (once).  Under HIP graph capture call ``linear`` with
-    gradients off and ``linear_grad``, which take no part in autograd's graph."""
+    Differentiable (once).  Under HIP graph capture autograd is refused: call
+    ``linear`` with gradients off, and ``linear_grad``."""
     _gpu(x, "x")
     _code(x, "x")
     act = _act_code(activation)
@@ -341,7 +348,8 @@ def decode(values: torch.Tensor, indices: torch.Tensor, weight: torch.Tensor, ro
     needed; an index is row * n + latent).  ``weight`` [n, d], ``bias`` [d].
     Entries out of range (the -1 of padded slots) add nothing; an index that
     occurs twice counts twice.  Returns [rows, d].  Differentiable (once) in
-    values, weight and bias."""
+    values, weight and bias; under graph capture with gradients off, and
+    ``decode_grad``."""
     rows = _check_selection(values, indices, rows)
     _check(weight, "weight", values)
     if weight.dim() != 2:
@@ -398,8 +406,8 @@ def _encode_grad_run(grad_values, values, indices, x, weight, need):
 
 class _Encode(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, weight, bias, k_total, params):
-        values, indices = _encode_run(x, weight, bias, k_total, params)
+    def forward(ctx, x, weight, bias, k_total, params, workspace):
+        values, indices = _encode_run(x, weight, bias, k_total, params, workspace)
         ctx.save_for_backward(x, weight, values, indices)
         ctx.mark_non_differentiable(indices)
         return values, indices
@@ -408,20 +416,20 @@ class _Encode(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, grad_values, _):
         x, weight, values, indices = ctx.saved_tensors
-        nx, nw, nb, _, _ = ctx.needs_input_grad
+        nx, nw, nb = ctx.needs_input_grad[:3]
         dx, dw, db = _encode_grad_run(grad_values, values, indices, x, weight, (nx, nw, nb))
-        return dx, dw, db, None, None
+        return dx, dw, db, None, None, None
 
 
-def _encode_run(x, weight, bias, k_total, params):
+def _encode_run(x, weight, bias, k_total, params, workspace):
     from . import topk
     acts = _linear_run(x, weight, bias, _lib.ACTIVATIONS["relu"], None, False)[0]
-    values, indices = topk(acts.reshape(1, -1), k_total, params=params)
+    values, indices = topk(acts.reshape(1, -1), k_total, params=params, workspace=workspace)
     return values[0], indices[0]
 
 
 def encode(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None, k_total: int,
-           params=None) -> tuple:
+           params=None, workspace=None) -> tuple:
     """The encoder of a BatchTopK sparse autoencoder (Prof-K section 5): the
     ``k_total`` largest entries of ``relu(x @ weight.T + bias)`` over the whole
     batch, as (values [k_total], flattened indices [k_total]) in rank order.
@@ -429,7 +437,8 @@ def encode(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None, k_t
     ``x`` [rows, d], ``weight`` [n, d], ``bias`` [n]; float32 or bfloat16.
     Differentiable (once) in x, weight and bias through the selected entries
     above 0 (the others have no gradient); the backward touches those entries
-    only.  ``params``: as ``topk``'s."""
+    only.  Under graph capture with gradients off, and ``encode_grad``.  ``params``, ``workspace``: as ``topk``'s (a captured call needs a
+    workspace of its own)."""
     _gpu(x, "x")
     _code(x, "x")
     if x.dim() != 2 or not isinstance(weight, torch.Tensor) or weight.dim() != 2:
@@ -442,8 +451,8 @@ def encode(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None, k_t
     if not 1 <= k_total <= x.shape[0] * weight.shape[0]:
         raise ValueError("k_total: from 1 to rows * n")
     if _wants_grad(x, weight, bias):
-        return _Encode.apply(x, weight, bias, k_total, params)
-    return _encode_run(x, weight, bias, k_total, params)
+        return _Encode.apply(x, weight, bias, k_total, params, workspace)
+    return _encode_run(x, weight, bias, k_total, params, workspace)
 
 
 def encode_grad(grad_values: torch.Tensor, values: torch.Tensor, indices: torch.Tensor,

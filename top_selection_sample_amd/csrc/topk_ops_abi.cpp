@@ -23,6 +23,12 @@ constexpr int64_t WIDTH_MAX = int64_t(1) << 22;
 
 bool bad_size(int64_t v) { return v < 0 || v > SIZE_MAX31; }
 
+constexpr int64_t KEYS_MAX = int64_t(1) << 28;    // rows and latents of a selection: two digits of 14 bits
+
+// Elements of a matrix (2^42 of them are more than any device holds): tile and
+// workgroup counts then stay within 32 bits.
+bool bad_area(int64_t a, int64_t b) { return a > 0 && b > (int64_t(1) << 42) / a; }
+
 bool bad_width(int64_t d) { return d < 0 || d >= WIDTH_MAX; }
 
 int64_t elem(int dtype) { return dtype == TOPK_BF16 ? 2 : 4; }
@@ -49,7 +55,9 @@ int linear_gemm(const topk_linear_args* a, tk::GemmArgs* g) {
   if (!a) return TOPK_EINVAL;
   if (bad_dtype(a->dtype)) return TOPK_EDTYPE;
   if (a->act < TOPK_ACT_NONE || a->act > TOPK_ACT_SILU) return TOPK_EINVAL;
-  if (bad_size(a->m) || bad_width(a->n) || bad_width(a->k) || (a->x_trans && bad_width(a->m))) return TOPK_EINVAL;
+  if (bad_size(a->m) || bad_width(a->n) || bad_width(a->k) || (a->x_trans && bad_width(a->m)) ||
+      bad_area(a->m, a->n) || bad_area(a->m, a->k))
+    return TOPK_EINVAL;
   const int64_t m = a->m, n = a->n, k = a->k;
   if (a->x_trans ? bad_matrix(a->x, a->ldx, k, m, a->dtype) : bad_matrix(a->x, a->ldx, m, k, a->dtype))
     return TOPK_EINVAL;
@@ -81,7 +89,9 @@ int linear_grad(const topk_linear_grad_args* a, tk::GradArgs* g) {
   if (!a) return TOPK_EINVAL;
   if (bad_dtype(a->dtype)) return TOPK_EDTYPE;
   if (a->act < TOPK_ACT_NONE || a->act > TOPK_ACT_SILU) return TOPK_EINVAL;
-  if (bad_size(a->m) || bad_width(a->n) || bad_width(a->k) || (a->x_trans && bad_width(a->m))) return TOPK_EINVAL;
+  if (bad_size(a->m) || bad_width(a->n) || bad_width(a->k) || (a->x_trans && bad_width(a->m)) ||
+      bad_area(a->m, a->n) || bad_area(a->m, a->k))
+    return TOPK_EINVAL;
   const int64_t m = a->m, n = a->n, k = a->k;
   const int dt = a->dtype;
   if (!a->dx && !a->dw && !a->db) return TOPK_EINVAL;
@@ -119,6 +129,7 @@ int to_selection(const topk_selection* in, bool pointers, tk::Selection* s) {
   if (!in) return TOPK_EINVAL;
   if (bad_dtype(in->dtype)) return TOPK_EDTYPE;
   if (bad_size(in->rows) || bad_size(in->k) || bad_size(in->n)) return TOPK_EINVAL;
+  if (in->rows >= KEYS_MAX || in->n >= KEYS_MAX) return TOPK_EINVAL;
   const int64_t total = in->flat ? in->k : in->rows * in->k;
   if (total > SIZE_MAX31) return TOPK_EINVAL;   // entries are numbered in 32 bits
   if (pointers && total > 0) {

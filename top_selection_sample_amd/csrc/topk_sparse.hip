@@ -62,8 +62,8 @@ __device__ __forceinline__ float coef_of(const T* coef, const T* gate, uint32_t 
 }
 
 // ---------------------------------------------------------------- grouping
-// Stable counting sort of the entries by key, digits of at most 14 bits, the
-// lowest first; up to 16383 keys need one pass.  Each of `blocks` workgroups
+// Stable counting sort of the entries by key, one or two digits of at most 14
+// bits, the lower first; up to 16383 keys need one pass (keys are below 2^28).  Each of `blocks` workgroups
 // counts the digits of its consecutive entries (k_count); k_scan turns the
 // counts into the place of each block's first entry of each digit; k_place
 // writes the entries there.  Within a block the order is kept by taking 1024
@@ -99,7 +99,7 @@ SortPlan sort_plan(int64_t keys, int64_t total) {
   if (keys + 1 > (int64_t)MAX_BINS) {
     uint32_t bits = 0;
     while ((uint64_t(1) << bits) <= (uint64_t)keys) ++bits;   // the key `keys` itself is one
-    p.passes = (bits + 13) / 14;
+    p.passes = bits > 14 ? 2 : 1;
     p.width = (bits + p.passes - 1) / p.passes;
   }
   p.max_bins = p.width ? 1u << p.width : p.keys + 1;
@@ -116,7 +116,7 @@ SortPlan sort_plan(int64_t keys, int64_t total) {
     p.off_cnt = take((size_t)p.blocks * p.max_bins * 4);
     p.off_coarse = take((size_t)p.blocks * (p.max_bins / GROUP + 1) * 4);
   }
-  if (!p.small && p.passes > 1) p.off_pair = take((size_t)total * 16);   // two halves: the passes alternate
+  if (!p.small && p.passes > 1) p.off_pair = take((size_t)total * 8);
   p.off_rec = take((size_t)total * 16);
   p.off_run = take((size_t)keys * 8);
   p.total_bytes = at;
@@ -876,8 +876,8 @@ hipError_t run_sorts(const SegCall& a, const SegArgs* const* parts, const SegPla
       KPass& k = ks.p[y++];
       u32x2* pair = reinterpret_cast<u32x2*>(ws[i] + p.off_pair);
       const bool last = pass + 1 == p.passes;
-      k.in = pass ? pair + (size_t)((pass - 1) & 1) * p.total : nullptr;
-      k.out = last ? nullptr : pair + (size_t)(pass & 1) * p.total;
+      k.in = pass ? pair : nullptr;    // at most two passes
+      k.out = last ? nullptr : pair;
       k.rec = reinterpret_cast<u32x4*>(ws[i] + p.off_rec);
       k.cnt = reinterpret_cast<uint32_t*>(ws[i] + p.off_cnt);
       k.coarse = reinterpret_cast<uint32_t*>(ws[i] + p.off_coarse);
