@@ -81,16 +81,16 @@ __device__ __forceinline__ void bias_of(float* b, uint32_t c, const Epi& e) {
 // straight to LDS (buffer loads with an LDS destination, 16 bytes a lane), two
 // stages deep; reads beyond a tensor's end return 0 there.  A wave's matrix
 // instructions take 16-byte fragments: 8 bf16 of one row (16x16x32), or 4 f32
-// used by four 16x16x4 instructions in turn; the summed axis is permuted the
+// used by four 32x32x2 instructions in turn; the summed axis is permuted the
 // same way in both operands.
 //
 // LDS layouts.  An operand whose summed axis is contiguous is kept as rows of
 // 128 bytes, the 16-byte chunk c of row r at place c ^ (r & 7), so that the
 // eight rows read in one clock use all banks once.  An operand stored the
 // other way round ("trans") is kept as it lies in memory, one line per summed
-// index; bf16 fragments are then read with the transposing LDS read, f32 ones
-// element by element, and the 16-row units of a line are rotated by the
-// summed index so that the lines read together lie in different banks.
+// index; f32 fragments are then read element by element, bf16 ones with the
+// transposing LDS read, for which the 16-row units of a line are rotated by
+// the summed index so that the lines read together lie in different banks.
 //
 // W's rows are the first operand of the matrix instruction and x's the second,
 // so a lane ends with four neighbouring columns of one output row.
@@ -114,9 +114,19 @@ struct KGemm {
   uint32_t all_steps;
 };
 
+// FR: rows of a fragment; SUB: fragments along a step.  32-bit fragments are
+// 32 rows high: 32x32x2 runs at 140 to 154 TFLOP/s with one to four waves on a
+// SIMD, 16x16x4 at 114 to 138.
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 template <class T> struct Elem;
-template <> struct Elem<bf16_t> { static constexpr int ES = 2, BK = 64, UNIT = 32; };
-template <> struct Elem<float> { static constexpr int ES = 4, BK = 32, UNIT = 64; };
+template <> struct Elem<bf16_t> {
+  static constexpr int ES = 2, BK = 64, FR = 16, SUB = 2;
+  typedef f32x4 Acc;
+};
+template <> struct Elem<float> {
+  static constexpr int ES = 4, BK = 32, FR = 32, SUB = 4;
+  typedef f32x16 Acc;
+};
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* p, int64_t bytes) {
   const int n = bytes > 0x7FFFFFFF ? 0x7FFFFFFF : (bytes < 0 ? 0 : (int)bytes);
@@ -150,7 +160,7 @@ struct Loader {
         off[j] = row * (uint32_t)o.ld * ES + c * 16;
       }
     } else {
-      constexpr uint32_t RB = R * ES, US = Elem<T>::UNIT;
+      constexpr uint32_t RB = R * ES, US = 32;
       base = static_cast<const char*>(o.p) + (int64_t)r0 * ES;
       // rounded up to whole words: a range check that ends inside a word would drop its first half
       bytes = ((((int64_t)o.red - 1) * o.ld + rows) * ES + 3) & ~(int64_t)3;
@@ -160,7 +170,7 @@ struct Loader {
       for (int j = 0; j < N; ++j) {
         const uint32_t at = (wave * N + j) * 1024 + lane * 16;
         const uint32_t k = at / RB, in = at % RB;
-        const uint32_t turn = ES == 2 ? (k & 3) : ((k >> 2) & 3);
+        const uint32_t turn = ES == 2 ? (k & 3) : 0;
         off[j] = k * (uint32_t)o.ld * ES + (((in / US) ^ turn) * US) + in % US;
       }
     }
@@ -185,12 +195,13 @@ __device__ __forceinline__ void wait_loads() {
   __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
 }
 
-// The 16-byte fragments of 16 rows, sub-step s of a tile.
+// A lane's 16 bytes of fragment f (FR rows), sub-step s of a tile.
 template <class T, int R, bool TR>
 __device__ __forceinline__ u32x4 fragment(lds_char* t, uint32_t f, uint32_t s, uint32_t lane) {
-  const uint32_t i = lane % 16, g = lane / 16;
+  constexpr uint32_t FR = Elem<T>::FR, G = 64 / FR;    // G lanes share a row
+  const uint32_t i = lane % FR, g = lane / FR;
   if constexpr (!TR) {
-    const uint32_t at = (f * 16 + i) * 128 + (((s * 4 + g) ^ (i & 7)) * 16);
+    const uint32_t at = (f * FR + i) * 128 + (((s * G + g) ^ (i & 7)) * 16);
     return *reinterpret_cast<__attribute__((address_space(3))) u32x4*>(t + at);
   } else if constexpr (Elem<T>::ES == 2) {
     constexpr uint32_t RB = R * 2;
@@ -207,8 +218,7 @@ __device__ __forceinline__ u32x4 fragment(lds_char* t, uint32_t f, uint32_t s, u
     return q.v;
   } else {
     constexpr uint32_t RB = R * 4;
-    const uint32_t k = s * 16 + g * 4;
-    lds_char* at = t + k * RB + ((f ^ g) * 64) + i * 4;
+    lds_char* at = t + (s * 8 + g * 4) * RB + (f * 32 + i) * 4;   // 32 lanes use all banks once
     u32x4 v;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -220,8 +230,8 @@ __device__ __forceinline__ u32x4 fragment(lds_char* t, uint32_t f, uint32_t s, u
 // acc[i][j] += w[i] x[j].  The four f32 instructions of a fragment pair go
 // round all pairs in turn: one that waited for its own last result would
 // leave the matrix core idle.
-template <class T, int FM, int FN>
-__device__ __forceinline__ void mma_all(const u32x4* w, const u32x4* x, f32x4 (&acc)[FN][FM]) {
+template <class T, int FM, int FN, class Acc>
+__device__ __forceinline__ void mma_all(const u32x4* w, const u32x4* x, Acc (&acc)[FN][FM]) {
   if constexpr (Elem<T>::ES == 2) {
 #pragma unroll
     for (int i = 0; i < FN; ++i)
@@ -235,9 +245,11 @@ __device__ __forceinline__ void mma_all(const u32x4* w, const u32x4* x, f32x4 (&
 #pragma unroll
       for (int i = 0; i < FN; ++i)
 #pragma unroll
-        for (int j = 0; j < FM; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(w[i][u]), __uint_as_float(x[j][u]),
-                                                           acc[i][j], 0, 0, 0);
+        for (int j = 0; j < FM; ++j) {
+          const float a = __uint_as_float(w[i][u]), b = __uint_as_float(x[j][u]);
+          if constexpr (sizeof(Acc) == 64) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(a, b, acc[i][j], 0, 0, 0);
+          else acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, acc[i][j], 0, 0, 0);
+        }
   }
 }
 
@@ -264,10 +276,11 @@ __device__ __forceinline__ void tile_of(uint32_t id, uint32_t total, uint32_t tm
 // `next` while this step's fragments are read and multiplied.  The two stages
 // are separate LDS variables, so that the compiler knows that the loads in
 // flight do not write what the fragment reads read.
-template <class T, int TM, int TN, int FM, int FN, bool TA, bool TB, class LA, class LB>
+template <class T, int TM, int TN, int FM, int FN, bool TA, bool TB, class LA, class LB, class Acc>
 __device__ __forceinline__ void gemm_step(lds_char* cur, lds_char* next, LA& la, LB& lb, uint32_t kt,
                                           bool more, uint32_t wave, uint32_t lane, uint32_t wm,
-                                          uint32_t wn, f32x4 (&acc)[FN][FM]) {
+                                          uint32_t wn, Acc (&acc)[FN][FM]) {
+  constexpr int SUB = Elem<T>::SUB;
   wait_loads();
   __syncthreads();   // this step's tiles have arrived; the other stage is free
   auto ahead = [&]() {
@@ -279,10 +292,10 @@ __device__ __forceinline__ void gemm_step(lds_char* cur, lds_char* next, LA& la,
     __builtin_amdgcn_sched_barrier(0);
   };
   if constexpr (FM * FN <= 16) {
-    // both halves' fragments first: the second half's reads are covered by the first half's products
-    u32x4 fa[2][FM], fb[2][FN];
+    // all fragments first: the later ones' reads are covered by the first ones' products
+    u32x4 fa[SUB][FM], fb[SUB][FN];
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < SUB; ++s) {
 #pragma unroll
       for (int i = 0; i < FN; ++i) fb[s][i] = fragment<T, TN, TB>(cur + TM * 128, wn + i, s, lane);
 #pragma unroll
@@ -290,11 +303,11 @@ __device__ __forceinline__ void gemm_step(lds_char* cur, lds_char* next, LA& la,
     }
     ahead();
 #pragma unroll
-    for (int s = 0; s < 2; ++s) mma_all<T, FM, FN>(fb[s], fa[s], acc);
-  } else {   // the registers hold one half's
+    for (int s = 0; s < SUB; ++s) mma_all<T, FM, FN>(fb[s], fa[s], acc);
+  } else {   // the registers hold one sub-step's
     ahead();
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < SUB; ++s) {
       u32x4 fa[FM], fb[FN];
 #pragma unroll
       for (int i = 0; i < FN; ++i) fb[i] = fragment<T, TN, TB>(cur + TM * 128, wn + i, s, lane);
@@ -308,7 +321,8 @@ __device__ __forceinline__ void gemm_step(lds_char* cur, lds_char* next, LA& la,
 template <class T, int TM, int TN, int NWM, int NWN, bool TA, bool TB>
 __global__ __launch_bounds__(NWM * NWN * 64, 2) void k_gemm(KGemm p) {
 #ifdef __HIP_DEVICE_COMPILE__   // buffer resources exist in the device pass only
-  constexpr int W = NWM * NWN, FM = TM / 16 / NWM, FN = TN / 16 / NWN;
+  constexpr int FR = Elem<T>::FR, W = NWM * NWN, FM = TM / FR / NWM, FN = TN / FR / NWN;
+  typedef typename Elem<T>::Acc Acc;
   __shared__ __align__(1024) char stage0[(TM + TN) * 128];
   __shared__ __align__(1024) char stage1[(TM + TN) * 128];
   lds_char* s0 = (lds_char*)stage0;
@@ -327,11 +341,13 @@ __global__ __launch_bounds__(NWM * NWN * 64, 2) void k_gemm(KGemm p) {
   la.init(p.a, m0, wave, lane);
   lb.init(p.b, n0, wave, lane);
   const uint32_t wm = (wave / NWN) * FM, wn = (wave % NWN) * FN;   // the wave's first fragments
-  f32x4 acc[FN][FM];
+  Acc acc[FN][FM];
 #pragma unroll
   for (int i = 0; i < FN; ++i)
 #pragma unroll
-    for (int j = 0; j < FM; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < FM; ++j)
+#pragma unroll
+      for (int u = 0; u < FR * FR / 64; ++u) acc[i][j][u] = 0.f;
   if (k0 < k1) {
     la.issue(s0, k0, wave);
     lb.issue(s0 + TM * 128, k0, wave);
@@ -352,20 +368,25 @@ __global__ __launch_bounds__(NWM * NWN * 64, 2) void k_gemm(KGemm p) {
   constexpr uint32_t LANES = C / V, ROWS = 64 / LANES;
   static_assert(W * 32 * C * 4 <= (TM + TN) * 128, "the rows fit one stage");
   float* mine = reinterpret_cast<float*>(stage0) + wave * 32 * C;
-  const uint32_t cc = (lane % LANES) * V, c = n0 + wn * 16 + cc;
+  const uint32_t cc = (lane % LANES) * V, c = n0 + wn * FR + cc;
   const bool whole = c + V <= p.e.n;   // the lane's columns are one vector of every row
   float bias[V] = {};
   if (whole && !p.part) bias_of<T, V>(bias, c, p.e);
+  constexpr int HIGH = 32 / FR;        // fragments that 32 rows take
 #pragma unroll
-  for (int j = 0; j < FM; j += 2) {
+  for (int j = 0; j < FM; j += HIGH) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < HIGH; ++h)
 #pragma unroll
-      for (int i = 0; i < FN; ++i) {
-        const uint32_t r = h * 16 + lane % 16, u = i * 4 + lane / 16;
-        *reinterpret_cast<f32x4*>(mine + r * C + (u ^ (r % CH)) * 4) = acc[i][j + h];
-      }
-    const uint32_t r0 = m0 + (wm + j) * 16;
+      for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int q = 0; q < FR * FR / 256; ++q) {   // four columns each, 8 apart in a fragment of 32
+          const uint32_t r = h * FR + lane % FR, u = i * (FR / 4) + q * 2 + lane / FR;
+          const Acc& v = acc[i][j + h];
+          *reinterpret_cast<f32x4*>(mine + r * C + (u ^ (r % CH)) * 4) =
+              f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+        }
+    const uint32_t r0 = m0 + (wm + j) * FR;
 #pragma unroll 2
     for (uint32_t rr = lane / LANES; rr < 32; rr += ROWS) {
       if (r0 + rr >= p.e.m) break;
@@ -620,7 +641,7 @@ struct TileCost {
   double shared, alone, ends;
 };
 constexpr TileCost COST_BF16[] = {{64, 4, 0.2, 0.7, 4}, {128, 2, 0.49, 0.8, 6}, {256, 1, 1.55, 1.55, 12}};
-constexpr TileCost COST_F32[] = {{64, 4, 0.5, 1.08, 4}, {128, 2, 1.93, 2.2, 6}};
+constexpr TileCost COST_F32[] = {{64, 4, 0.45, 0.95, 4}, {128, 2, 1.75, 2.0, 6}};
 
 // The tile and the split of the summed axis that are estimated cheapest.
 void choose_tile(const GemmArgs& g, Plan2* p) {
