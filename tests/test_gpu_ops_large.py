@@ -1,0 +1,62 @@
+"""GPU: operators at strides, rows and entries near the ends of their ranges."""
+import pytest
+import torch
+
+from top_selection_sample_amd import decode, decode_grad, linear
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("strided", ["x", "weight"])
+def test_rows_of_a_tile_spread_over_more_than_2_31_bytes(strided):
+    g = torch.Generator("cuda").manual_seed(3)
+    big, few, k, ld = 512, 32768, 64, 5_000_000
+    wide = torch.empty(big * ld, dtype=torch.bfloat16, device="cuda").as_strided((big, k), (ld, 1))
+    wide.copy_(torch.randn(big, k, device="cuda", generator=g))
+    other = torch.randn(few, k, device="cuda", generator=g).bfloat16()
+    y = linear(wide, other) if strided == "x" else linear(other, wide).T
+    ref = wide.double() @ other.double().T
+    bound = (wide.double().abs() @ other.double().abs().T) * (k * 2.0 ** -24) + ref.abs() * 2.0 ** -8
+    assert ((y.double() - ref).abs() <= bound).all()
+
+
+def test_more_rows_than_one_grid_dimension_of_tiles_holds():
+    """2^24 tiles of 64 rows and 2^30 rows to pack; each output is one product, rounded once."""
+    m = (1 << 30) + 70
+    x = torch.randn(m, 1, device="cuda", generator=torch.Generator("cuda").manual_seed(4))
+    w = torch.tensor([[1.25]], device="cuda")
+    y = linear(x, w)
+    assert torch.equal(y, x * 1.25)
+
+
+def test_decode_of_more_rows_than_one_grid_dimension_holds():
+    rows, n, d = (1 << 24) + 5, 100, 8
+    g = torch.Generator("cuda").manual_seed(5)
+    values = torch.randn(rows, 1, device="cuda", generator=g)
+    indices = torch.randint(0, n, (rows, 1), device="cuda", generator=g)
+    weight = torch.randn(n, d, device="cuda", generator=g)
+    assert torch.equal(decode(values, indices, weight), values * weight[indices[:, 0]])
+
+
+def test_dots_of_more_entries_than_one_grid_dimension_holds():
+    rows, k, n = (1 << 15) + 1, 1 << 14, 100
+    g = torch.Generator("cuda").manual_seed(6)
+    values = torch.ones(rows, k, device="cuda", dtype=torch.bfloat16)
+    indices = torch.randint(0, n, (rows, k), device="cuda", generator=g)
+    weight = torch.randint(-8, 8, (n, 1), device="cuda", generator=g).bfloat16()
+    grad = torch.randint(-8, 8, (rows, 1), device="cuda", generator=g).bfloat16()
+    dv = decode_grad(grad, values, indices, weight, (True, False, False))[0]
+    for at in range(0, rows, 4096):   # products of small whole numbers are exact
+        assert torch.equal(dv[at:at + 4096], grad[at:at + 4096] * weight[indices[at:at + 4096], 0])
+
+
+def test_gradient_of_the_most_latents():
+    n, d = (1 << 28) - 1, 1
+    indices = torch.tensor([[0, 5, n - 1], [n - 1, n, -1]], device="cuda")
+    values = torch.tensor([[1.0, 2.0, 3.0], [4.0, 5.0, 6.0]], device="cuda", dtype=torch.bfloat16)
+    grad = torch.tensor([[2.0], [8.0]], device="cuda", dtype=torch.bfloat16)
+    weight = torch.zeros(n, d, device="cuda", dtype=torch.bfloat16)
+    dw = decode_grad(grad, values, indices, weight, (False, True, False))[1]
+    at = torch.nonzero(dw[:, 0])[:, 0]
+    assert at.tolist() == [0, 5, n - 1]
+    assert dw[at, 0].tolist() == [2.0, 4.0, 6.0 + 32.0]

@@ -330,9 +330,11 @@ __global__ __launch_bounds__(NWM * NWN * 64, 2) void k_gemm(KGemm p) {
   const uint32_t lane = threadIdx.x % 64;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const uint32_t tiles = p.tiles_m * p.tiles_n;
-  const uint32_t sp = blockIdx.x / tiles;
+  const uint32_t id = block_id();
+  const uint32_t sp = id / tiles;
+  if (sp >= p.split) return;
   uint32_t im, in;
-  tile_of(blockIdx.x - sp * tiles, tiles, p.tiles_m, p.tiles_n, &im, &in, 1024 / TM);
+  tile_of(id - sp * tiles, tiles, p.tiles_m, p.tiles_n, &im, &in, 1024 / TM);
   const uint32_t m0 = im * TM, n0 = in * TN;
   const uint32_t k0 = sp * p.steps;
   const uint32_t k1 = k0 + p.steps < p.all_steps ? k0 + p.steps : p.all_steps;
@@ -513,7 +515,7 @@ struct KPack {
 template <class T>
 __global__ __launch_bounds__(256) void k_pack(KPack a, KPack b) {
   constexpr int V = Vec<T>::N;
-  uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x;
+  uint64_t i = (uint64_t)block_id() * 256 + threadIdx.x;
   const bool second = i >= a.vecs;
   if (second) i -= a.vecs;
   const KPack p = second ? b : a;
@@ -621,14 +623,14 @@ struct Plan2 {
 };
 
 // Direct loads need 16-byte aligned lines, lines whose summed extent fills
-// 16-byte chunks (rows beyond it would be summed otherwise), and offsets
-// within a tile below 2^31.
+// 16-byte chunks (rows beyond it would be summed otherwise), and strides
+// that keep the offsets within a tile in range.
 bool needs_pack(const Operand& o, int64_t rows, int64_t red, int64_t es) {
   if (!rows || !red) return false;
   const int64_t line = o.trans ? rows : red, lines = o.trans ? red : rows;
   const int64_t ld = lines > 1 ? o.ld : line;
   return reinterpret_cast<uintptr_t>(o.p) % 16 || (lines > 1 && (ld * es) % 16) ||
-         (!o.trans && !o.padded && (red * es) % 16) || ld * es * 128 >= (int64_t(1) << 31);
+         (!o.trans && !o.padded && (red * es) % 16) || ld >= WIDTH_MAX;
 }
 
 // Microseconds of one step of a tile on a compute unit that shares its time
@@ -707,13 +709,13 @@ Plan2 plan_gemm(const GemmArgs& g) {
 }
 
 template <class T, int R, int NWM, int NWN>
-void go(const KGemm& k, bool ta, bool tb, uint32_t grid, hipStream_t s) {
+void go(const KGemm& k, bool ta, bool tb, dim3 grid, hipStream_t s) {
   const dim3 block(NWM * NWN * 64);
   if (ta && tb) {   // (no 256-tile: see choose_tile)
-    if constexpr (R < 256) hipLaunchKernelGGL((k_gemm<T, R, R, NWM, NWN, true, true>), dim3(grid), block, 0, s, k);
-  } else if (ta) hipLaunchKernelGGL((k_gemm<T, R, R, NWM, NWN, true, false>), dim3(grid), block, 0, s, k);
-  else if (tb) hipLaunchKernelGGL((k_gemm<T, R, R, NWM, NWN, false, true>), dim3(grid), block, 0, s, k);
-  else hipLaunchKernelGGL((k_gemm<T, R, R, NWM, NWN, false, false>), dim3(grid), block, 0, s, k);
+    if constexpr (R < 256) hipLaunchKernelGGL((k_gemm<T, R, R, NWM, NWN, true, true>), grid, block, 0, s, k);
+  } else if (ta) hipLaunchKernelGGL((k_gemm<T, R, R, NWM, NWN, true, false>), grid, block, 0, s, k);
+  else if (tb) hipLaunchKernelGGL((k_gemm<T, R, R, NWM, NWN, false, true>), grid, block, 0, s, k);
+  else hipLaunchKernelGGL((k_gemm<T, R, R, NWM, NWN, false, false>), grid, block, 0, s, k);
 }
 
 // A product in steps: copies of the operands that need one, the tiles, the
@@ -769,7 +771,7 @@ struct Product {
     k.split = p.split;
     k.steps = p.steps;
     k.all_steps = p.all_steps;
-    const uint32_t grid = p.tiles_m * p.tiles_n * p.split;
+    const dim3 grid = wide_grid((uint64_t)p.tiles_m * p.tiles_n * p.split);
     if constexpr (ES == 2) {
       if (p.tile == 256) {
         go<T, 256, 2, 4>(k, g.a.trans, g.b.trans, grid, s);
@@ -791,8 +793,8 @@ template <class T>
 hipError_t run_packs(KPack* packs, int n, hipStream_t s) {
   if (!n) return hipSuccess;
   if (n == 1) packs[1] = KPack{};
-  hipLaunchKernelGGL((k_pack<T>), dim3((uint32_t)ceil_div((int64_t)(packs[0].vecs + packs[1].vecs), 256)), dim3(256),
-                     0, s, packs[0], packs[1]);
+  hipLaunchKernelGGL((k_pack<T>), wide_grid((packs[0].vecs + packs[1].vecs + 255) / 256), dim3(256), 0, s, packs[0],
+                     packs[1]);
   return hipGetLastError();
 }
 

@@ -10,6 +10,11 @@ namespace tk {
 
 enum : int { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_SILU = 3 };
 
+// Rows of a matrix operand are shorter than this, in elements: those of a tile
+// (256 of bf16, 128 of f32) then stay below 2^31 bytes, the range of the
+// offsets within it.
+constexpr int64_t WIDTH_MAX = int64_t(1) << 22;
+
 // One operand of a product, [rows, red] with `red` the summed axis: element
 // (r, c) sits at p[r * ld + c], or at p[c * ld + r] when `trans`.
 struct Operand {

@@ -17,10 +17,6 @@ namespace {
 
 constexpr int64_t SIZE_MAX31 = (int64_t(1) << 31) - 1;
 
-// Longest row of a matrix operand: 128 of them stay below 2^31 bytes, the
-// range of the offsets within a tile.
-constexpr int64_t WIDTH_MAX = int64_t(1) << 22;
-
 bool bad_size(int64_t v) { return v < 0 || v > SIZE_MAX31; }
 
 constexpr int64_t KEYS_MAX = int64_t(1) << 28;    // rows and latents of a selection: two digits of 14 bits
@@ -29,7 +25,7 @@ constexpr int64_t KEYS_MAX = int64_t(1) << 28;    // rows and latents of a selec
 // workgroup counts then stay within 32 bits.
 bool bad_area(int64_t a, int64_t b) { return a > 0 && b > (int64_t(1) << 42) / a; }
 
-bool bad_width(int64_t d) { return d < 0 || d >= WIDTH_MAX; }
+bool bad_width(int64_t d) { return d < 0 || d >= tk::WIDTH_MAX; }
 
 int64_t elem(int dtype) { return dtype == TOPK_BF16 ? 2 : 4; }
 

@@ -176,6 +176,15 @@ __device__ __forceinline__ float slope_of(float z) {
   return 1.f;
 }
 
+// A launch over any number of workgroups that 32 bits count: along one
+// dimension of a grid HIP takes fewer than 2^32 threads.  Workgroups from
+// `blocks` on have to leave.
+constexpr uint32_t GRID_X = 1u << 22;
+inline dim3 wide_grid(uint64_t blocks, uint32_t z = 1) {
+  return dim3((uint32_t)(blocks < GRID_X ? blocks : GRID_X), (uint32_t)((blocks + GRID_X - 1) / GRID_X), z);
+}
+__device__ __forceinline__ uint32_t block_id() { return blockIdx.y * GRID_X + blockIdx.x; }
+
 template <class V>
 __device__ __forceinline__ V wave_sum(V v) {
 #pragma unroll

@@ -634,7 +634,7 @@ __global__ __launch_bounds__(256) void k_join_runs(KSegs ss) {
   const KSeg& p = ss.s[blockIdx.z];
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
   uint32_t first = NO_ENTRY, end = 0;     // lane i: the workgroup's key i
-  const uint64_t k0 = (uint64_t)blockIdx.x * JOIN_KEYS;
+  const uint64_t k0 = (uint64_t)block_id() * JOIN_KEYS;
   if (p.total && lane < JOIN_KEYS && k0 + lane < p.keys) {
     first = p.run[2 * (k0 + lane)];
     end = p.run[2 * (k0 + lane) + 1];
@@ -644,11 +644,11 @@ __global__ __launch_bounds__(256) void k_join_runs(KSegs ss) {
   for (uint32_t i = wave; i < JOIN_KEYS && k0 + i < p.keys; i += 4) {
     const uint32_t q0 = __builtin_amdgcn_readlane(lq0, i), q1 = __builtin_amdgcn_readlane(lq1, i);
     if (q1 == q0 + 1) continue;                  // written by its chunk
-    if (p.coef_sum && lane == 0) {
+    if (p.coef_sum) {
       float s = 0.f;
-#pragma unroll 8
-      for (uint32_t q = q0; q < q1; ++q) s += p.part_c[(size_t)q * 2 + (q == q0)];
-      static_cast<T*>(p.coef_sum)[k0 + i] = from_f32<T>(s);
+      for (uint32_t q = q0 + lane; q < q1; q += 64) s += p.part_c[(size_t)q * 2 + (q == q0)];
+      s = wave_sum(s);
+      if (lane == 0) static_cast<T*>(p.coef_sum)[k0 + i] = from_f32<T>(s);
     }
     if (!p.out || q1 - q0 > LONG) continue;
     for (uint32_t b = lane * VEC; b < p.d; b += 64 * VEC) {
@@ -701,8 +701,9 @@ __global__ __launch_bounds__(256) void k_rows(KSel s, KSeg p, const T* __restric
   __shared__ uint32_t found[4];
   __shared__ float join[4][64 * VEC];
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
-  const uint32_t row = blockIdx.x;
-  const Share<VEC, 1> cols((blockIdx.y * 64 + lane) * VEC, p.d);
+  const uint32_t row = block_id();
+  if (row >= s.rows) return;
+  const Share<VEC, 1> cols((blockIdx.z * 64 + lane) * VEC, p.d);
   const uint32_t c = cols.at[0];
   const bool in = cols.in[0];
   const T* src = static_cast<const T*>(p.src);
@@ -779,7 +780,7 @@ __global__ __launch_bounds__(256) void k_dots(KSel s, const T* __restrict__ g, i
                                               const T* __restrict__ w, int64_t ldw, uint32_t d,
                                               T* __restrict__ dv) {
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
-  const uint64_t first = ((uint64_t)blockIdx.x * 4 + wave) * DOTS;
+  const uint64_t first = ((uint64_t)block_id() * 4 + wave) * DOTS;
   if (first >= s.total) return;
   const uint32_t e0 = (uint32_t)first;
   uint32_t row = 0, latent = 0;
@@ -924,7 +925,7 @@ hipError_t launch_sums(const KSegs& ks, int n, bool wide, uint32_t chunks, int64
   }
   uint32_t keys = ks.s[0].keys;
   if (n > 1) keys = std::max(keys, ks.s[1].keys);
-  const dim3 grid((uint32_t)ceil_div(keys, JOIN_KEYS), 1, n);
+  const dim3 grid = wide_grid((uint64_t)ceil_div(keys, JOIN_KEYS), n);
   if (wide) hipLaunchKernelGGL((k_join_runs<T, V>), grid, dim3(256), 0, s, ks);
   else hipLaunchKernelGGL((k_join_runs<T, 1>), grid, dim3(256), 0, s, ks);
   return hipGetLastError();
@@ -976,7 +977,7 @@ hipError_t run_seg(const SegCall& a, char* ws, hipStream_t s) {
     if (keys == 0 || ((a.d == 0 || !p.out) && !p.coef_sum && !k.dots)) continue;
     if (p.by_row && rows_direct(a.sel)) {
       const uint32_t columns = (uint32_t)ceil_div(a.d, 64 * (wide ? V : 1));
-      const dim3 grid(k.keys, columns);
+      const dim3 grid = wide_grid(k.keys, columns);
       const T* coef = static_cast<const T*>(a.coef);
       const T* gate = static_cast<const T*>(a.gate);
       if (wide) hipLaunchKernelGGL((k_rows<T, (int)V>), grid, dim3(256), 0, s, ksel(a.sel), k, coef, gate);
@@ -1010,7 +1011,7 @@ template <class T>
 hipError_t run_dots(const DotArgs& a, hipStream_t s) {
   constexpr int64_t V = Vec<T>::N;
   const bool wide = a.d >= V;
-  const dim3 grid((uint32_t)ceil_div(a.sel.total, 4 * DOTS));
+  const dim3 grid = wide_grid((uint64_t)ceil_div(a.sel.total, 4 * DOTS));
   const T* g = static_cast<const T*>(a.g);
   const T* w = static_cast<const T*>(a.w);
   T* dv = static_cast<T*>(a.dv);
