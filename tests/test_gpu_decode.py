@@ -270,3 +270,23 @@ def test_graphs_streams_and_repeats(total, dt):
         for _, out in graphs:
             for a, b in zip(out, want):
                 assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,k,n,d", [(1, 257, 3000, 512), (1, 40_000, 5000, 20), (5, 700, 900, 1), (7, 1030, 300, 3), (3, 2048, 8192, 1028),
+                                        (40, 5000, 70, 65), (2047, 600, 50, 8), (2049, 300, 50, 8)])
+def test_few_rows_of_many_entries(rows, k, n, d, dt):
+    idx = ints(31, n, rows, k)
+    idx[:, -3:] = -1
+    if rows > 2:
+        idx[1] = -1                      # a row with no entry, a row with one part without any
+        idx[2, :300] = n
+    check_all(rnd(32, rows, k, dt=dt), idx, rows, n, d, dt, f"row-wise {rows}x{k} of {n}, {d} wide")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,total,n,d", [(1, 8192, 9000, 40), (3, 8191, 70, 520), (64, 2000, 300, 5), (900, 6000, 8, 65)])
+def test_short_flattened_selections_in_parts(rows, total, n, d, dt):
+    idx = ints(33, rows * n, total)
+    idx[::5] = idx[0]
+    check_all(rnd(34, total, dt=dt), idx, rows, n, d, dt, f"flat {total} of {rows}x{n}, {d} wide")

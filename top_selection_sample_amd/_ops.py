@@ -280,7 +280,7 @@ def _decode_run(values, indices, weight, rows, bias):
         sel = _selection(values, indices, rows, n)
         stream = _stream(dev)
         args = (sel, weight.data_ptr(), ldw, d, _ptr(bias), out.data_ptr(), d or 1)
-        # row-wise selections need no scratch: ask only when the call says so
+        # row-wise selections seldom need scratch: ask only when the call says so
         if values.dim() != 2 or _lib.lib.topk_decode(*args, None, 0, stream) != _lib.TOPK_OK:
             ws, size = _decode_scratch(sel, d, values)
             _lib.check(_lib.lib.topk_decode(*args, _ptr(ws), size, stream), "decode")

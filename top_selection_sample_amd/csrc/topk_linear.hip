@@ -1010,6 +1010,17 @@ hipError_t launch_slope(const SlopeArgs& a, void* ws, hipStream_t s) {
   return a.dtype == DT_BF16 ? run_joins<bf16_t>(&join, n, s) : run_joins<float>(&join, n, s);
 }
 
+hipError_t launch_join(const JoinArgs& a, hipStream_t s) {
+  Epi e{};
+  e.bias = a.bias;
+  e.c = a.out;
+  e.ldc = a.ldo;
+  e.m = (uint32_t)a.m;
+  e.n = (uint32_t)a.n;
+  const KJoin join{a.part, a.split, a.ldpart, 0, 0, e};
+  return a.dtype == DT_BF16 ? run_joins<bf16_t>(&join, 1, s) : run_joins<float>(&join, 1, s);
+}
+
 size_t grad_workspace(const GradArgs& a) { return plan_grad(a).total; }
 
 hipError_t launch_grad(const GradArgs& a, void* ws, hipStream_t s) {

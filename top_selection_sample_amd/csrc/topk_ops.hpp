@@ -61,6 +61,19 @@ struct SlopeArgs {
 size_t slope_workspace(const SlopeArgs& a);
 hipError_t launch_slope(const SlopeArgs& a, void* ws, hipStream_t s);
 
+// out[r] = bias + part[0][r] + part[1][r] + ..., in this order: sums that were
+// split, with rows of `ldpart` floats (a multiple of 4).
+struct JoinArgs {
+  const float* part = nullptr;      // [split][m][ldpart]
+  uint32_t split = 0, ldpart = 0;
+  int64_t m = 0, n = 0;
+  int dtype = 1;
+  const void* bias = nullptr;       // [n], or null
+  void* out = nullptr;              // [m, n], row stride ldo
+  int64_t ldo = 0;
+};
+hipError_t launch_join(const JoinArgs& a, hipStream_t s);
+
 // The gradients of a product: dx[m, k] = dz[m, n] W[n, k], dw[n, k] = dz^T x,
 // db.  `x` and `w` as operands of the product they come from.
 struct GradArgs {

@@ -690,11 +690,18 @@ __global__ __launch_bounds__(256) void k_join_runs(KSegs ss) {
 // waves share the row's entries.  Flattened ones: the workgroup reads every
 // index, 256 at a time, and keeps those of its row, in order, in LDS.  The
 // waves' sums are joined in wave order.
+//
+// A wave has ROWS_AHEAD rows on their way at a time, so a workgroup takes about
+// 10 us for 256 entries, wherever it runs: few rows of many entries are split
+// over several workgroups, each with `chunk` of them, whose sums go to the
+// workspace and are added in order by a second launch (one row of 1024, 4096
+// and 65536 entries of 512 bf16: 38, 164 and 2697 us unsplit; 15, 19 and 69
+// split; 18, 34 and 173 through the sort).
 constexpr uint32_t KEEP = 1024;        // entries held in LDS
 constexpr uint32_t ROWS_AHEAD = 8;     // rows of src in flight per wave
 
 template <class T, int VEC>
-__global__ __launch_bounds__(256) void k_rows(KSel s, KSeg p, const T* __restrict__ coef,
+__global__ __launch_bounds__(256) void k_rows(KSel s, KSeg p, uint32_t splits, const T* __restrict__ coef,
                                               const T* __restrict__ gate) {
   __shared__ uint32_t ent[KEEP];
   __shared__ float cf[KEEP];
@@ -703,12 +710,14 @@ __global__ __launch_bounds__(256) void k_rows(KSel s, KSeg p, const T* __restric
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
   const uint32_t row = block_id();
   if (row >= s.rows) return;
-  const Share<VEC, 1> cols((blockIdx.z * 64 + lane) * VEC, p.d);
+  const uint32_t split = blockIdx.z % splits;
+  const Share<VEC, 1> cols((blockIdx.z / splits * 64 + lane) * VEC, p.d);
   const uint32_t c = cols.at[0];
   const bool in = cols.in[0];
   const T* src = static_cast<const T*>(p.src);
   float acc[VEC] = {};
-  const uint32_t e0 = s.flat ? 0u : row * s.k, e1 = s.flat ? s.total : e0 + s.k;
+  const uint32_t first = s.flat ? 0u : row * s.k, end = s.flat ? s.total : first + s.k;
+  const uint32_t e0 = first + split * p.chunk, e1 = end - e0 < p.chunk ? end : e0 + p.chunk;
   uint32_t held = 0;     // entries in LDS; the same in every thread
   for (uint32_t b = e0; b < e1 || held; b += 256) {
     if (b < e1) {
@@ -761,13 +770,8 @@ __global__ __launch_bounds__(256) void k_rows(KSel s, KSeg p, const T* __restric
       const uint32_t a = lane * VEC + i;
       acc[i] = (join[0][a] + join[1][a]) + (join[2][a] + join[3][a]);
     }
-    if (p.bias) {
-      float b[VEC];
-      load_vec<T, VEC>(static_cast<const T*>(p.bias) + c, b);
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) acc[i] += b[i];
-    }
-    store_vec<T, VEC>(static_cast<T*>(p.out) + (int64_t)row * p.ldo + c, acc);
+    if (splits > 1) store_part<VEC>(p.part + ((size_t)split * s.rows + row) * ((p.d + 3) / 4 * 4) + c, acc);
+    else write_key<T, VEC>(p, row, c, acc);
   }
 }
 
@@ -816,6 +820,27 @@ __global__ __launch_bounds__(256) void k_dots(KSel s, const T* __restrict__ g, i
 // caches, where the sort's three launches alone take longer).
 bool rows_direct(const Selection& s) {
   return !s.flat || (s.total <= 8192 && s.rows * s.total <= (int64_t(1) << 24));
+}
+
+// How the entries that a row's workgroup goes through are split: into pieces of
+// 256 or more while the rows alone do not give eight workgroups for each of
+// 256 compute units, at most 64 (the join reads them one after another).
+struct RowsPlan {
+  uint32_t columns = 1, splits = 1, chunk = 1, ldpart = 0;
+  size_t bytes = 0;
+};
+
+RowsPlan rows_plan(const Selection& s, int64_t d) {
+  RowsPlan p;
+  const int64_t v = s.dtype == DT_BF16 ? 8 : 4, span = s.flat ? s.total : s.k;
+  p.columns = (uint32_t)std::max<int64_t>(1, ceil_div(d, 64 * (d >= v ? v : 1)));
+  const int64_t room = 2048 / std::max<int64_t>(1, s.rows * (int64_t)p.columns);
+  const int64_t splits = std::max<int64_t>(1, std::min<int64_t>({room, 64, ceil_div(span, 256)}));
+  p.chunk = (uint32_t)(ceil_div(std::max<int64_t>(1, span), splits * 256) * 256);
+  p.splits = (uint32_t)std::max<int64_t>(1, ceil_div(span, p.chunk));
+  p.ldpart = (uint32_t)(ceil_div(d, 4) * 4);
+  if (p.splits > 1) p.bytes = align256((size_t)p.splits * (size_t)s.rows * p.ldpart * 4);
+  return p;
 }
 
 struct SegPlan {
@@ -976,13 +1001,29 @@ hipError_t run_seg(const SegCall& a, char* ws, hipStream_t s) {
     }
     if (keys == 0 || ((a.d == 0 || !p.out) && !p.coef_sum && !k.dots)) continue;
     if (p.by_row && rows_direct(a.sel)) {
-      const uint32_t columns = (uint32_t)ceil_div(a.d, 64 * (wide ? V : 1));
-      const dim3 grid = wide_grid(k.keys, columns);
+      const RowsPlan q = rows_plan(a.sel, a.d);
+      const dim3 grid = wide_grid(k.keys, q.columns * q.splits);
+      k.chunk = q.chunk;
+      k.part = reinterpret_cast<float*>(ws);
+      ws += q.bytes;
       const T* coef = static_cast<const T*>(a.coef);
       const T* gate = static_cast<const T*>(a.gate);
-      if (wide) hipLaunchKernelGGL((k_rows<T, (int)V>), grid, dim3(256), 0, s, ksel(a.sel), k, coef, gate);
-      else hipLaunchKernelGGL((k_rows<T, 1>), grid, dim3(256), 0, s, ksel(a.sel), k, coef, gate);
-      const hipError_t e = hipGetLastError();
+      if (wide) hipLaunchKernelGGL((k_rows<T, (int)V>), grid, dim3(256), 0, s, ksel(a.sel), k, q.splits, coef, gate);
+      else hipLaunchKernelGGL((k_rows<T, 1>), grid, dim3(256), 0, s, ksel(a.sel), k, q.splits, coef, gate);
+      hipError_t e = hipGetLastError();
+      if (e == hipSuccess && q.splits > 1) {
+        JoinArgs j;
+        j.part = k.part;
+        j.split = q.splits;
+        j.ldpart = q.ldpart;
+        j.m = keys;
+        j.n = a.d;
+        j.dtype = a.sel.dtype;
+        j.bias = p.bias;
+        j.out = p.out;
+        j.ldo = p.ldo;
+        e = launch_join(j, s);
+      }
       if (e != hipSuccess) return e;
       continue;
     }
@@ -1024,7 +1065,7 @@ hipError_t run_dots(const DotArgs& a, hipStream_t s) {
 
 size_t seg_workspace(const Selection& sel, int64_t d, bool by_row, bool by_latent) {
   size_t bytes = 0;
-  if (by_row && !rows_direct(sel)) bytes += seg_plan(sel, d, true).total;
+  if (by_row) bytes += rows_direct(sel) ? rows_plan(sel, d).bytes : seg_plan(sel, d, true).total;
   if (by_latent) bytes += seg_plan(sel, d, false).total;
   return bytes;
 }
