@@ -398,6 +398,7 @@ struct KSeg {
   float* part_c;        // [chunks][2]
   int64_t lds, ldo, ldw;
   uint32_t keys, total, chunk, d;
+  uint32_t join;        // keys of one workgroup of k_join_runs
 };
 
 // A launch sums by row and by latent side by side (grid dimension z).
@@ -623,10 +624,12 @@ __device__ __forceinline__ void write_key(const KSeg& p, uint64_t key, uint32_t 
   store_vec<T, VEC>(static_cast<T*>(p.out) + (int64_t)key * p.ldo + c, acc);
 }
 
-// Writes the keys without an entry, and joins the runs of several chunks: 16
-// keys per workgroup, a wave per key; the runs of more than LONG chunks are
-// shared by the four waves.
+// Writes the keys without an entry, and joins the runs of several chunks: up to
+// 16 keys per workgroup, a wave per key; the runs of more than LONG chunks are
+// shared by the four waves.  Few keys mean long runs, one workgroup each.
 constexpr uint32_t JOIN_KEYS = 16, LONG = 12;
+
+uint32_t join_keys(uint32_t keys) { return std::min(JOIN_KEYS, std::max(1u, keys / 1024)); }
 
 template <class T, int VEC>
 __global__ __launch_bounds__(256) void k_join_runs(KSegs ss) {
@@ -634,14 +637,14 @@ __global__ __launch_bounds__(256) void k_join_runs(KSegs ss) {
   const KSeg& p = ss.s[blockIdx.z];
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
   uint32_t first = NO_ENTRY, end = 0;     // lane i: the workgroup's key i
-  const uint64_t k0 = (uint64_t)block_id() * JOIN_KEYS;
-  if (p.total && lane < JOIN_KEYS && k0 + lane < p.keys) {
+  const uint64_t k0 = (uint64_t)block_id() * p.join;
+  if (p.total && lane < p.join && k0 + lane < p.keys) {
     first = p.run[2 * (k0 + lane)];
     end = p.run[2 * (k0 + lane) + 1];
   }
   // chunks [q0, q1) of each key's run; none: q1 = 0
   const uint32_t lq0 = first == NO_ENTRY ? 0u : first / p.chunk, lq1 = first == NO_ENTRY ? 0u : (end - 1) / p.chunk + 1;
-  for (uint32_t i = wave; i < JOIN_KEYS && k0 + i < p.keys; i += 4) {
+  for (uint32_t i = wave; i < p.join && k0 + i < p.keys; i += 4) {
     const uint32_t q0 = __builtin_amdgcn_readlane(lq0, i), q1 = __builtin_amdgcn_readlane(lq1, i);
     if (q1 == q0 + 1) continue;                  // written by its chunk
     if (p.coef_sum) {
@@ -659,7 +662,7 @@ __global__ __launch_bounds__(256) void k_join_runs(KSegs ss) {
     }
   }
   if (!p.out) return;
-  uint64_t many = __ballot(lane < JOIN_KEYS && lq1 - lq0 > LONG);
+  uint64_t many = __ballot(lane < p.join && lq1 - lq0 > LONG);
   for (; many; many &= many - 1) {
     const uint32_t i = (uint32_t)__ffsll((unsigned long long)many) - 1;
     const uint32_t q0 = __builtin_amdgcn_readlane(lq0, i), q1 = __builtin_amdgcn_readlane(lq1, i);
@@ -816,10 +819,12 @@ __global__ __launch_bounds__(256) void k_dots(KSel s, const T* __restrict__ g, i
 
 // ---------------------------------------------------------------- host side
 // Rows straight from the selection: row-wise, or few enough reads that every
-// row may look at every index (4096 rows and entries: 128 MB out of the
-// caches, where the sort's three launches alone take longer).
+// row may look at every index.  512 bf16, against the way through the sort:
+// 2048 rows and 4096 entries 24.4 us to 26, 8192 entries 42.6 to 25.8; 256
+// rows and 8192 entries 17 to 26; 16 rows and 65536 entries 43 to 37, one row
+// 69 to 172.
 bool rows_direct(const Selection& s) {
-  return !s.flat || (s.total <= 8192 && s.rows * s.total <= (int64_t(1) << 24));
+  return !s.flat || (s.rows * s.total <= (int64_t(1) << 23) && (s.total <= 16384 || s.rows <= 8));
 }
 
 // How the entries that a row's workgroup goes through are split: into pieces of
@@ -948,9 +953,9 @@ hipError_t launch_sums(const KSegs& ks, int n, bool wide, uint32_t chunks, int64
     else if (wide) hipLaunchKernelGGL((k_seg<T, V, 1, 16, false, false>), all, dim3(256), 0, s, ks);
     else hipLaunchKernelGGL((k_seg<T, 1, 1, 16, false, false>), all, dim3(256), 0, s, ks);
   }
-  uint32_t keys = ks.s[0].keys;
-  if (n > 1) keys = std::max(keys, ks.s[1].keys);
-  const dim3 grid = wide_grid((uint64_t)ceil_div(keys, JOIN_KEYS), n);
+  int64_t joins = 0;
+  for (int i = 0; i < n; ++i) joins = std::max(joins, ceil_div(ks.s[i].keys, ks.s[i].join));
+  const dim3 grid = wide_grid((uint64_t)joins, n);
   if (wide) hipLaunchKernelGGL((k_join_runs<T, V>), grid, dim3(256), 0, s, ks);
   else hipLaunchKernelGGL((k_join_runs<T, 1>), grid, dim3(256), 0, s, ks);
   return hipGetLastError();
@@ -979,6 +984,7 @@ hipError_t run_seg(const SegCall& a, char* ws, hipStream_t s) {
     k.keys = (uint32_t)keys;
     k.total = (uint32_t)a.sel.total;
     k.d = (uint32_t)a.d;
+    k.join = join_keys(k.keys);
     if (p.dots) {
       // fused where a lane holds its whole share of both rows
       if (wide && a.d <= 128 * V && a.sel.total) {
