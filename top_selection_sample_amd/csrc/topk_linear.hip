@@ -108,10 +108,10 @@ struct KOperand {
 struct KGemm {
   KOperand a, b;     // x and W
   Epi e;
-  float* part;       // split sums: [split][m][ldpart]; null: the epilogue runs here
-  uint32_t ldpart;
-  uint32_t tiles_m, tiles_n, split, steps;   // steps: tiles of the summed axis per split
-  uint32_t all_steps;
+  float* part;       // sums of split tiles: [split][rest][TM][TN]
+  uint32_t tiles_m, tiles_n;
+  uint32_t whole, rest, split;   // the first `whole` tiles run the epilogue, the others are split
+  uint32_t steps, all_steps;     // steps along the summed axis of a piece, and of a whole tile
 };
 
 // FR: rows of a fragment; SUB: fragments along a step.  32-bit fragments are
@@ -253,18 +253,23 @@ __device__ __forceinline__ void mma_all(const u32x4* w, const u32x4* x, Acc (&ac
   }
 }
 
-// Tile of a workgroup.  Consecutive workgroups go to the eight dies in turn,
-// so each die gets a contiguous range of tiles, and walks it in bands of
-// 1024 rows: W's tile and the band's rows of x then stay in the die's L2
-// (4096 x 512 x 65536 bf16 in 256-tiles: 360 us in bands of 4 tiles, 380 to
-// 451 in bands of 1, 8, 16 or 32).  Each band begins 37 tiles further right:
-// dies that work on different bands would else store the same columns at the
-// same time, and where the row stride is a power of two those lie in the same
-// memory channels (338 us with the shift; 322 for rows of 65600).
-__device__ __forceinline__ void tile_of(uint32_t id, uint32_t total, uint32_t tm, uint32_t tn,
-                                        uint32_t* im, uint32_t* in, uint32_t band_rows) {
+// Consecutive workgroups go to the eight dies in turn, so each die gets a
+// contiguous range of a launch's tiles.
+__device__ __forceinline__ uint32_t die_order(uint32_t id, uint32_t total) {
   const uint32_t q = total / 8, r = total % 8, x = id % 8;
-  id = x * q + (x < r ? x : r) + id / 8;
+  return x * q + (x < r ? x : r) + id / 8;
+}
+
+// A range of tiles walks the product in bands of 1024 rows: W's tile and the
+// band's rows of x then stay in the die's L2 (4096 x 512 x 65536 bf16 in
+// 256-tiles: 360 us in bands of 4 tiles, 380 to 451 in bands of 1, 8, 16 or
+// 32).  Each band begins 37 tiles further right: dies that work on different
+// bands would else store the same columns at the same time, and where the row
+// stride is a power of two those lie in the same memory channels (338 us with
+// the shift; 322 for rows of 65600).
+__device__ __forceinline__ void place_of(uint32_t id, uint32_t tm, uint32_t tn, uint32_t tile, uint32_t* im,
+                                         uint32_t* in) {
+  const uint32_t band_rows = 1024 / tile;
   const uint32_t band = id / (band_rows * tn);
   const uint32_t rows = tm - band * band_rows < band_rows ? tm - band * band_rows : band_rows;
   const uint32_t at = id - band * band_rows * tn;
@@ -329,15 +334,22 @@ __global__ __launch_bounds__(NWM * NWN * 64, 2) void k_gemm(KGemm p) {
   lds_char* s1 = (lds_char*)stage1;
   const uint32_t lane = threadIdx.x % 64;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  const uint32_t tiles = p.tiles_m * p.tiles_n;
   const uint32_t id = block_id();
-  const uint32_t sp = id / tiles;
-  if (sp >= p.split) return;
+  if (id >= p.whole + p.rest * p.split) return;
+  uint32_t tile, piece = 0, k0 = 0, k1 = p.all_steps;
+  const bool split = id >= p.whole;
+  if (!split) {
+    tile = die_order(id, p.whole);
+  } else {
+    const uint32_t sp = (id - p.whole) / p.rest, at = die_order(id - p.whole - sp * p.rest, p.rest);
+    tile = p.whole + at;
+    piece = sp * p.rest + at;
+    k0 = sp * p.steps;
+    if (k1 - k0 > p.steps) k1 = k0 + p.steps;
+  }
   uint32_t im, in;
-  tile_of(id - sp * tiles, tiles, p.tiles_m, p.tiles_n, &im, &in, 1024 / TM);
+  place_of(tile, p.tiles_m, p.tiles_n, TM, &im, &in);
   const uint32_t m0 = im * TM, n0 = in * TN;
-  const uint32_t k0 = sp * p.steps;
-  const uint32_t k1 = k0 + p.steps < p.all_steps ? k0 + p.steps : p.all_steps;
   Loader<T, TM, TA, W> la;
   Loader<T, TN, TB, W> lb;
   la.init(p.a, m0, wave, lane);
@@ -373,7 +385,7 @@ __global__ __launch_bounds__(NWM * NWN * 64, 2) void k_gemm(KGemm p) {
   const uint32_t cc = (lane % LANES) * V, c = n0 + wn * FR + cc;
   const bool whole = c + V <= p.e.n;   // the lane's columns are one vector of every row
   float bias[V] = {};
-  if (whole && !p.part) bias_of<T, V>(bias, c, p.e);
+  if (whole && !split) bias_of<T, V>(bias, c, p.e);
   constexpr int HIGH = 32 / FR;        // fragments that 32 rows take
 #pragma unroll
   for (int j = 0; j < FM; j += HIGH) {
@@ -399,11 +411,10 @@ __global__ __launch_bounds__(NWM * NWN * 64, 2) void k_gemm(KGemm p) {
 #pragma unroll
         for (int u = 0; u < 4; ++u) v[i + u] = q[u];
       }
-      if (p.part) {
-        float* o = p.part + ((size_t)sp * p.e.m + r0 + rr) * p.ldpart + c;
+      if (split) {
+        float* o = p.part + ((size_t)piece * TM + (wm + j) * FR + rr) * TN + wn * FR + cc;
 #pragma unroll
-        for (int i = 0; i < V; i += 4)
-          if (c + i < p.ldpart) Vec<float>::store(o + i, v + i);
+        for (int i = 0; i < V; i += 4) Vec<float>::store(o + i, v + i);
       } else if (whole) {
         finish<T, V>(v, bias, r0 + rr, c, p.e);
       } else {   // the last columns
@@ -419,12 +430,15 @@ __global__ __launch_bounds__(NWM * NWN * 64, 2) void k_gemm(KGemm p) {
 #endif
 }
 
-// Adds partial sums in order, then the epilogue: the parts of up to two split
-// products and the column sums' blocks (a product of one row) in one launch.
+// Adds partial sums in a fixed order, then the epilogue: the split tiles of up
+// to two products, and the column sums' blocks (a product of one row), in one
+// launch.  A thread takes 16 bytes of y; where there are many parts several
+// threads share them, and add theirs in LDS.
 struct KJoin {
-  const float* part;     // [split][m][ldpart]
-  uint32_t split, ldpart, blocks;
-  int tall;              // one row of many parts: 16 threads share a column's
+  const float* part;     // [split][m][ldpart], or, for split tiles, [split][rest][tile][tile]
+  uint32_t split, ldpart;
+  uint32_t whole, rest, tile, tiles_m, tiles_n;   // rest 0: rows
+  uint32_t ways, blocks;
   Epi e;
 };
 struct KJoins {
@@ -434,44 +448,60 @@ struct KJoins {
 template <class T>
 __global__ __launch_bounds__(256) void k_join(KJoins js) {
   constexpr int V = Vec<T>::N;
+  __shared__ __align__(16) float sums[256 * V];
   uint32_t b = blockIdx.x, which = 0;
   while (b >= js.j[which].blocks) b -= js.j[which++].blocks;
   const KJoin& p = js.j[which];
-  if (p.tall) {
-    __shared__ float sums[16][17];
-    const uint32_t c = b * 16 + threadIdx.x % 16, group = threadIdx.x / 16;
-    float v = 0.f;
-    if (c < p.e.n) {
-#pragma unroll 4
-      for (uint32_t s = group; s < p.split; s += 16) v += p.part[(size_t)s * p.ldpart + c];
-    }
-    sums[group][threadIdx.x % 16] = v;
-    __syncthreads();
-    if (group == 0 && c < p.e.n) {
-      v = 0.f;
-#pragma unroll
-      for (uint32_t g = 0; g < 16; ++g) v += sums[g][threadIdx.x];
-      static_cast<T*>(p.e.c)[c] = from_f32<T>(v);
-    }
-    return;
+  const uint32_t each = 256 / p.ways, group = threadIdx.x / each;
+  const uint64_t i = (uint64_t)b * each + threadIdx.x % each;
+  uint32_t r, c, limit = ~0u;
+  const float* q;
+  size_t next;
+  bool in;
+  if (p.rest) {
+    const uint32_t per_row = p.tile / V, t = (uint32_t)(i / (p.tile * per_row)), at = (uint32_t)(i % (p.tile * per_row));
+    uint32_t im = 0, jn = 0;
+    if (t < p.rest) place_of(p.whole + t, p.tiles_m, p.tiles_n, p.tile, &im, &jn);
+    r = im * p.tile + at / per_row;
+    c = jn * p.tile + at % per_row * V;
+    in = t < p.rest && r < p.e.m && c < p.e.n;
+    q = p.part + i * V;
+    next = (size_t)p.rest * p.tile * p.tile;
+  } else {
+    const uint32_t per_row = (p.e.n + V - 1) / V;
+    r = (uint32_t)(i / per_row);
+    c = (uint32_t)(i % per_row) * V;
+    in = i < (uint64_t)per_row * p.e.m;
+    q = p.part + (size_t)r * p.ldpart + c;
+    next = (size_t)p.e.m * p.ldpart;
+    limit = p.ldpart;      // a multiple of 4
   }
-  const uint32_t per_row = (p.e.n + V - 1) / V;
-  const uint64_t i = (uint64_t)b * 256 + threadIdx.x;
-  if (i >= (uint64_t)per_row * p.e.m) return;
-  const uint32_t r = (uint32_t)(i / per_row), c = (uint32_t)(i % per_row) * V;
   float v[V] = {};
-  const float* q = p.part + (size_t)r * p.ldpart + c;
+  if (in) {
+    q += group * next;
 #pragma unroll 8
-  for (uint32_t s = 0; s < p.split; ++s) {
+    for (uint32_t s = group; s < p.split; s += p.ways) {
 #pragma unroll
-    for (int j = 0; j < V; j += 4) {
-      if (c + j >= p.ldpart) continue;
-      const f32x4 t = *reinterpret_cast<const f32x4*>(q + j);   // ldpart is a multiple of 4
+      for (int j = 0; j < V; j += 4) {
+        if (c + j >= limit) continue;
+        const f32x4 t = *reinterpret_cast<const f32x4*>(q + j);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) v[j + u] += t[u];
+        for (int u = 0; u < 4; ++u) v[j + u] += t[u];
+      }
+      q += p.ways * next;
     }
-    q += (size_t)p.e.m * p.ldpart;
   }
+  if (p.ways > 1) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) sums[threadIdx.x * V + j] = v[j];
+    __syncthreads();
+    if (group) return;
+    for (uint32_t g = 1; g < p.ways; ++g) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[j] += sums[(g * each + threadIdx.x) * V + j];
+    }
+  }
+  if (!in) return;
   if (c + V <= p.e.n) {
     float bias[V];
     bias_of<T, V>(bias, c, p.e);
@@ -492,10 +522,13 @@ hipError_t run_joins(const KJoin* js, int n, hipStream_t s) {
   KJoins k{};
   uint32_t blocks = 0;
   for (int i = 0; i < n; ++i) {
-    k.j[i] = js[i];
-    k.j[i].blocks = (uint32_t)(js[i].tall ? ceil_div(js[i].e.n, 16)
-                                          : ceil_div(ceil_div(js[i].e.n, Vec<T>::N) * (int64_t)js[i].e.m, 256));
-    blocks += k.j[i].blocks;
+    KJoin& j = k.j[i];
+    j = js[i];
+    j.ways = j.split <= 8 ? 1 : j.split <= 32 ? 4 : 16;   // a thread's loads fit one round trip
+    const int64_t vecs = j.rest ? (int64_t)j.rest * j.tile * j.tile / Vec<T>::N
+                                : ceil_div(j.e.n, Vec<T>::N) * (int64_t)j.e.m;
+    j.blocks = (uint32_t)ceil_div(vecs, 256 / j.ways);
+    blocks += j.blocks;
   }
   if (!blocks) return hipSuccess;
   hipLaunchKernelGGL((k_join<T>), dim3(blocks), dim3(256), 0, s, k);
@@ -540,11 +573,11 @@ __global__ __launch_bounds__(256) void k_pack(KPack a, KPack b) {
 }
 
 // Few rows of x: the call is bound by reading W once.  A workgroup takes 16
-// rows of W (columns of y) and the whole summed axis; its four waves take
-// turns of 32-byte-per-row pieces of it, straight from memory into the matrix
+// rows of W (columns of y) and the whole summed axis; its W waves take turns
+// of 256 bytes per row of it, straight from memory into the matrix
 // instructions' operands, with all loads of a turn issued before the first is
-// used, and join their sums in LDS in wave order.  One token through 12288 x
-// 512 bf16: 12.6 MB.
+// used, and join their sums in LDS in wave order.  One row through 12288 x 512
+// bf16 (12.6 MB): 4.4 us, 2.9 TB/s; its launch takes longer than that.
 template <class T>
 __device__ __forceinline__ u32x4 row_piece(const T* p, bool in, uint32_t k, uint32_t red) {
   constexpr uint32_t V = Vec<T>::N;
@@ -563,10 +596,10 @@ __device__ __forceinline__ u32x4 row_piece(const T* p, bool in, uint32_t k, uint
   return q;
 }
 
-template <class T, int MF>
-__global__ __launch_bounds__(256) void k_few_rows(KGemm p) {
+template <class T, int MF, int W>
+__global__ __launch_bounds__(W * 64) void k_few_rows(KGemm p) {
   constexpr uint32_t V = Vec<T>::N, PIECE = 4 * V, TURN = 4;   // summed elements per instruction, pieces per turn
-  __shared__ float join[4][MF][16][17];
+  __shared__ float join[W][MF][16][17];
   const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64;
   const uint32_t i = lane % 16, g = lane / 16;
   const uint32_t n0 = blockIdx.x * 16, red = p.a.red;
@@ -582,7 +615,7 @@ __global__ __launch_bounds__(256) void k_few_rows(KGemm p) {
   f32x4 acc[1][MF];
 #pragma unroll
   for (int f = 0; f < MF; ++f) acc[0][f] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (uint32_t k0 = wave * TURN * PIECE; k0 < red; k0 += 4 * TURN * PIECE) {
+  for (uint32_t k0 = wave * TURN * PIECE; k0 < red; k0 += W * TURN * PIECE) {
     u32x4 wf[TURN][1], xf[TURN][MF];
 #pragma unroll
     for (uint32_t t = 0; t < TURN; ++t) {
@@ -599,14 +632,16 @@ __global__ __launch_bounds__(256) void k_few_rows(KGemm p) {
     for (int j = 0; j < 4; ++j) join[wave][f][i][g * 4 + j] = acc[0][f][j];
   __syncthreads();
   const uint32_t c = n0 + threadIdx.x % 16;
-  if (c >= p.e.n) return;
+  if (threadIdx.x >= 256 || c >= p.e.n) return;
   float bias;
   bias_of<T, 1>(&bias, c, p.e);
 #pragma unroll
   for (int f = 0; f < MF; ++f) {
     const uint32_t r = threadIdx.x / 16, at = threadIdx.x % 16;
     if (f * 16 + r >= p.e.m) continue;
-    float z = (join[0][f][r][at] + join[1][f][r][at]) + (join[2][f][r][at] + join[3][f][r][at]);
+    float z = 0.f;
+#pragma unroll
+    for (int q = 0; q < W; ++q) z += join[q][f][r][at];
     finish<T, 1>(&z, &bias, f * 16 + r, c, p.e);
   }
 }
@@ -615,10 +650,9 @@ __global__ __launch_bounds__(256) void k_few_rows(KGemm p) {
 struct Plan2 {
   bool few = false;                  // k_few_rows
   uint32_t tile = 128;
-  uint32_t tiles_m = 0, tiles_n = 0, split = 1, steps = 0, all_steps = 0;
+  uint32_t tiles_m = 0, tiles_n = 0, whole = 0, rest = 0, split = 1, steps = 0, all_steps = 0;
   bool pack_a = false, pack_b = false;
   uint32_t lda = 0, ldb = 0;         // packed strides
-  uint32_t ldpart = 0;
   size_t off_b = 0, off_part = 0, total = 0;
 };
 
@@ -645,7 +679,13 @@ struct TileCost {
 constexpr TileCost COST_BF16[] = {{64, 4, 0.2, 0.7, 4}, {128, 2, 0.49, 0.8, 6}, {256, 1, 1.55, 1.55, 12}};
 constexpr TileCost COST_F32[] = {{64, 4, 0.45, 0.95, 4}, {128, 2, 1.75, 2.0, 6}};
 
-// The tile and the split of the summed axis that are estimated cheapest.
+// Ways to split a summed axis that are looked at.
+constexpr int64_t SPLITS[] = {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 14, 16, 20, 24, 28, 32, 40, 48, 56, 64};
+
+// The tile, and the tiles whose summed axis is split, that are estimated
+// cheapest: none, all, or those behind the last full round of the compute
+// units (1001 x 515 x 4099 f32 in 64-tiles is 1040 of them on 256 units of
+// four: whole, the last 16 cost as much again as a quarter of the others).
 void choose_tile(const GemmArgs& g, Plan2* p) {
   const bool half = g.dtype == DT_BF16;
   const int64_t steps = std::max<int64_t>(p->all_steps, 1);
@@ -655,22 +695,37 @@ void choose_tile(const GemmArgs& g, Plan2* p) {
     // the 256-tile with both operands transposed does not fit the registers
     if (t.tile == 256 && g.a.trans && g.b.trans) continue;
     const int64_t tm = ceil_div(g.m, t.tile), tn = ceil_div(g.n, t.tile), tiles = tm * tn;
-    for (int64_t split = 1; split <= 64 && (split == 1 || (steps / split >= 2 && tiles * split <= 8 * g.cus)); ++split) {
-      const int64_t per = ceil_div(steps, split), parts = ceil_div(steps, per);
-      const int64_t most = ceil_div(tiles * parts, g.cus);   // tiles of the busiest compute unit
-      auto round = [&](int64_t together) {   // so many tiles side by side on a compute unit
-        return together ? (double)per * std::max(t.alone, (double)together * t.shared) + t.ends : 0.0;
-      };
-      double us = (double)(most / t.holds) * round(t.holds) + round(most % t.holds);
-      // joining the parts: a launch, and their way through memory
-      if (parts > 1) us += 4 + (double)g.m * (double)g.n * 8e-6 * (double)parts / 4;
-      if (us < best) {
-        best = us;
-        p->tile = t.tile;
-        p->tiles_m = (uint32_t)tm;
-        p->tiles_n = (uint32_t)tn;
-        p->steps = (uint32_t)per;
-        p->split = (uint32_t)parts;
+    const int64_t slots = (int64_t)g.cus * t.holds;
+    // so many pieces of so many steps side by side on a compute unit
+    auto round = [&](int64_t together, int64_t per) {
+      return together ? (double)per * std::max(t.alone, (double)together * t.shared) + t.ends : 0.0;
+    };
+    const int64_t wholes[] = {0, tiles / g.cus * g.cus, tiles / slots * slots};
+    for (int w = 0; w < 3; ++w) {
+      const int64_t whole = wholes[w], rest = tiles - whole;
+      if (!rest || (w && whole == wholes[w - 1])) continue;
+      for (const int64_t split : SPLITS) {
+        if (split > 1 && (steps / split < 2 || rest * split > 2 * slots)) break;
+        const int64_t per = ceil_div(steps, split), parts = ceil_div(steps, per);
+        const int64_t a = whole / g.cus, b = ceil_div(rest * parts, g.cus);   // of the busiest compute unit
+        const int64_t left = a % t.holds;
+        double us = (double)(a / t.holds) * round(t.holds, steps);
+        if (!left) us += (double)(b / t.holds) * round(t.holds, per) + round(b % t.holds, per);
+        else
+          us += std::max((double)steps * t.alone, (double)(left * steps + b * per) * t.shared) +
+                t.ends * (double)ceil_div(left + b, t.holds);
+        // joining the parts: a launch, and their way through memory
+        if (parts > 1) us += 4 + (double)g.m * (double)g.n * (double)rest / (double)tiles * (double)parts * 2e-6;
+        if (us < best) {
+          best = us;
+          p->tile = t.tile;
+          p->tiles_m = (uint32_t)tm;
+          p->tiles_n = (uint32_t)tn;
+          p->steps = (uint32_t)per;
+          p->split = (uint32_t)parts;
+          p->whole = (uint32_t)(parts > 1 ? whole : tiles);
+          p->rest = (uint32_t)(parts > 1 ? rest : 0);
+        }
       }
     }
   }
@@ -679,9 +734,13 @@ void choose_tile(const GemmArgs& g, Plan2* p) {
 Plan2 plan_gemm(const GemmArgs& g) {
   Plan2 p;
   const int64_t es = g.dtype == DT_BF16 ? 2 : 4, v = 16 / es, bk = 128 / es;
-  // At most 32 rows, both summed axes contiguous, and enough columns to spread
-  // over the card or a summed axis that four waves soon read.
-  if (g.m <= 32 && !g.a.trans && !g.b.trans && (g.n >= 2048 || g.k <= 2048)) {
+  // Few rows and a summed axis that one workgroup soon reads: one launch.
+  // bf16, 16 rows, against split tiles: 64 x 4096 (n x k) 9.4 us to 15.4,
+  // 16384 x 4096 30 to 28, 512 x 12288 23 to 15; f32 4096 x 4096 19 to 29.
+  // Beyond 16 rows x is read twice as often as by the tiles: 32 rows of bf16,
+  // 4096 x 4096 14 us to 16, 16384 x 4096 46 to 28.
+  if (!g.a.trans && !g.b.trans && ((g.m <= 16 && g.k * es <= 16384) ||
+                                   (g.m <= 32 && g.k * es <= 8192 && g.n * g.k <= (int64_t(1) << 24)))) {
     p.few = true;
     return p;
   }
@@ -701,10 +760,7 @@ Plan2 plan_gemm(const GemmArgs& g) {
   p.total = p.off_part;
   p.all_steps = (uint32_t)ceil_div(g.k, bk);
   choose_tile(g, &p);
-  if (p.split > 1) {
-    p.ldpart = (uint32_t)(ceil_div(g.n, 4) * 4);
-    p.total += align256((size_t)p.split * (size_t)g.m * p.ldpart * 4);
-  }
+  p.total += (size_t)p.split * p.rest * p.tile * p.tile * 4;
   return p;
 }
 
@@ -760,18 +816,24 @@ struct Product {
     k.e = epilogue();
     if (p.few) {
       const dim3 grid((uint32_t)ceil_div(g.n, 16));
-      if (g.m <= 16) hipLaunchKernelGGL((k_few_rows<T, 1>), grid, dim3(256), 0, s, k);
-      else hipLaunchKernelGGL((k_few_rows<T, 2>), grid, dim3(256), 0, s, k);
+      // 16 waves where each has a turn, unless the workgroups alone fill the card
+      // (4096 x 4096 f32 16.8 us against 21.4; 16384 x 4096 56 against 54.7)
+      const bool deep = g.k * ES >= 4096 && g.n < 16384;
+      if (g.m <= 16 && deep) hipLaunchKernelGGL((k_few_rows<T, 1, 16>), grid, dim3(1024), 0, s, k);
+      else if (g.m <= 16) hipLaunchKernelGGL((k_few_rows<T, 1, 4>), grid, dim3(256), 0, s, k);
+      else if (deep) hipLaunchKernelGGL((k_few_rows<T, 2, 16>), grid, dim3(1024), 0, s, k);
+      else hipLaunchKernelGGL((k_few_rows<T, 2, 4>), grid, dim3(256), 0, s, k);
       return hipGetLastError();
     }
-    k.part = p.split > 1 ? reinterpret_cast<float*>(ws + p.off_part) : nullptr;
-    k.ldpart = p.ldpart;
+    k.part = reinterpret_cast<float*>(ws + p.off_part);
     k.tiles_m = p.tiles_m;
     k.tiles_n = p.tiles_n;
+    k.whole = p.whole;
+    k.rest = p.rest;
     k.split = p.split;
     k.steps = p.steps;
     k.all_steps = p.all_steps;
-    const dim3 grid = wide_grid((uint64_t)p.tiles_m * p.tiles_n * p.split);
+    const dim3 grid = wide_grid(p.whole + (uint64_t)p.rest * p.split);
     if constexpr (ES == 2) {
       if (p.tile == 256) {
         go<T, 256, 2, 4>(k, g.a.trans, g.b.trans, grid, s);
@@ -783,8 +845,16 @@ struct Product {
     return hipGetLastError();
   }
   int joins(KJoin* out) const {
-    if (p.few || p.split == 1) return 0;
-    out[0] = KJoin{reinterpret_cast<const float*>(ws + p.off_part), p.split, p.ldpart, 0, 0, epilogue()};
+    if (!p.rest) return 0;
+    KJoin& j = out[0] = KJoin{};
+    j.part = reinterpret_cast<const float*>(ws + p.off_part);
+    j.split = p.split;
+    j.whole = p.whole;
+    j.rest = p.rest;
+    j.tile = p.tile;
+    j.tiles_m = p.tiles_m;
+    j.tiles_n = p.tiles_n;
+    j.e = epilogue();
     return 1;
   }
 };
@@ -902,11 +972,13 @@ hipError_t run_slope_act(const SlopeArgs& a, float* part, hipStream_t s) {
 // (none for no rows: zeros).
 int slope_join(const SlopeArgs& a, const float* part, KJoin* out) {
   if (!a.db || !a.n) return 0;
-  Epi e{};
-  e.c = a.db;
-  e.m = 1;
-  e.n = (uint32_t)a.n;
-  out[0] = KJoin{part, slope_blocks(a.m), slope_ld(a.n), 0, 1, e};
+  KJoin& j = out[0] = KJoin{};
+  j.part = part;
+  j.split = slope_blocks(a.m);
+  j.ldpart = slope_ld(a.n);
+  j.e.c = a.db;
+  j.e.m = 1;
+  j.e.n = (uint32_t)a.n;
   return 1;
 }
 
@@ -1011,13 +1083,15 @@ hipError_t launch_slope(const SlopeArgs& a, void* ws, hipStream_t s) {
 }
 
 hipError_t launch_join(const JoinArgs& a, hipStream_t s) {
-  Epi e{};
-  e.bias = a.bias;
-  e.c = a.out;
-  e.ldc = a.ldo;
-  e.m = (uint32_t)a.m;
-  e.n = (uint32_t)a.n;
-  const KJoin join{a.part, a.split, a.ldpart, 0, 0, e};
+  KJoin join{};
+  join.part = a.part;
+  join.split = a.split;
+  join.ldpart = a.ldpart;
+  join.e.bias = a.bias;
+  join.e.c = a.out;
+  join.e.ldc = a.ldo;
+  join.e.m = (uint32_t)a.m;
+  join.e.n = (uint32_t)a.n;
   return a.dtype == DT_BF16 ? run_joins<bf16_t>(&join, 1, s) : run_joins<float>(&join, 1, s);
 }
 
