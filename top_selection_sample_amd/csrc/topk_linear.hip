@@ -23,11 +23,6 @@ struct Epi {
   int stream;    // store y past the caches
 };
 
-// Outputs from 16 MB on are stored past the caches: they would push the
-// operands out (4096 x 512 x 65536 bf16 in 256-tiles: 358 us against 439;
-// x 12288: 59 us against 70).  Smaller ones stay for whoever reads them next.
-constexpr int64_t STREAM_BYTES = int64_t(16) << 20;
-
 // The activation of V values; the switch is the same for every lane.
 template <class T, int V>
 __device__ __forceinline__ void act_any(float* v, int act) {

@@ -106,6 +106,12 @@ __device__ __forceinline__ void store_vec(T* p, const float* v) {
   else Vec<T>::store(p, v);
 }
 
+// Outputs from 16 MB on are stored past the caches: they would push out what
+// the rest of the launch reads (the product of 4096 x 512 x 65536 bf16, in its
+// first form 358 us against 439; the encoder's gradient at 65536 latents 92.6
+// against 96.9).  Smaller ones stay for whoever reads them next.
+constexpr int64_t STREAM_BYTES = int64_t(16) << 20;
+
 // A whole vector past the caches.
 template <class T>
 __device__ __forceinline__ void stream_vec(T* p, const float* v) {

@@ -398,6 +398,7 @@ struct KSeg {
   float* part_c;        // [chunks][2]
   int64_t lds, ldo, ldw;
   uint32_t keys, total, chunk, d;
+  int stream;           // store out past the caches
   uint32_t join;        // keys of one workgroup of k_join_runs
 };
 
@@ -442,6 +443,19 @@ struct Row {
     else Vec<T>::unpack(q[v], f);
   }
 };
+
+// VEC elements of an output row.
+template <class T, int VEC>
+__device__ __forceinline__ void store_out(T* o, const float* v, int stream) {
+  if (VEC > 1 && stream) {
+    // (the empty statements keep the compiler from merging the two stores into a plain one)
+    asm volatile("");
+    stream_vec<T>(o, v);
+    asm volatile("");
+  } else {
+    store_vec<T, VEC>(o, v);
+  }
+}
 
 template <int VEC>
 __device__ __forceinline__ void store_part(float* o, const float* v) {
@@ -521,7 +535,7 @@ __global__ __launch_bounds__(256) void k_seg(KSegs ss) {
 #pragma unroll
               for (int i = 0; i < VEC; ++i) acc[v][i] += b[i];
             }
-            store_vec<T, VEC>(static_cast<T*>(p.out) + (int64_t)cur * p.ldo + at, acc[v]);
+            store_out<T, VEC>(static_cast<T*>(p.out) + (int64_t)cur * p.ldo + at, acc[v], p.stream);
           }
         }
         if (p.coef_sum && one) static_cast<T*>(p.coef_sum)[cur] = from_f32<T>(csum);
@@ -621,32 +635,57 @@ __device__ __forceinline__ void write_key(const KSeg& p, uint64_t key, uint32_t 
 #pragma unroll
     for (int j = 0; j < VEC; ++j) acc[j] += b[j];
   }
-  store_vec<T, VEC>(static_cast<T*>(p.out) + (int64_t)key * p.ldo + c, acc);
+  store_out<T, VEC>(static_cast<T*>(p.out) + (int64_t)key * p.ldo + c, acc, p.stream);
 }
 
-// Writes the keys without an entry, and joins the runs of several chunks: up to
-// 16 keys per workgroup, a wave per key; the runs of more than LONG chunks are
-// shared by the four waves.  Few keys mean long runs, one workgroup each.
-constexpr uint32_t JOIN_KEYS = 16, LONG = 12;
+// Writes the keys without an entry, and joins the runs of several chunks.  A
+// workgroup takes `join` keys, a lane of every wave each to look at; the waves
+// share first the empty ones, whose stores wait for nothing, then the runs
+// that cross a chunk's edge.  There is at most one of those per chunk, so the
+// keys of a workgroup are as many as to hold two at most.
+// Runs of more than LONG chunks are shared by the four waves.
+constexpr uint32_t LONG = 12;
 
-uint32_t join_keys(uint32_t keys) { return std::min(JOIN_KEYS, std::max(1u, keys / 1024)); }
+uint32_t join_keys(uint32_t keys, uint32_t chunks) {
+  return (uint32_t)std::min<uint64_t>(64, std::max<uint64_t>(1, 2ull * keys / std::max(1u, chunks)));
+}
 
 template <class T, int VEC>
 __global__ __launch_bounds__(256) void k_join_runs(KSegs ss) {
   __shared__ float join[4][64 * VEC];
   const KSeg& p = ss.s[blockIdx.z];
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
-  uint32_t first = NO_ENTRY, end = 0;     // lane i: the workgroup's key i
   const uint64_t k0 = (uint64_t)block_id() * p.join;
-  if (p.total && lane < p.join && k0 + lane < p.keys) {
+  if (k0 >= p.keys) return;
+  const bool mine = lane < p.join && k0 + lane < p.keys;
+  uint32_t first = NO_ENTRY, end = 0;     // of the lane's key
+  if (p.total && mine) {
     first = p.run[2 * (k0 + lane)];
     end = p.run[2 * (k0 + lane) + 1];
   }
-  // chunks [q0, q1) of each key's run; none: q1 = 0
+  // chunks [q0, q1) of the run; none: q1 = 0
   const uint32_t lq0 = first == NO_ENTRY ? 0u : first / p.chunk, lq1 = first == NO_ENTRY ? 0u : (end - 1) / p.chunk + 1;
-  for (uint32_t i = wave; i < p.join && k0 + i < p.keys; i += 4) {
+  const bool none = mine && lq1 == 0;
+  if (p.coef_sum && none && wave == 0) static_cast<T*>(p.coef_sum)[k0 + lane] = from_f32<T>(0.f);
+  const uint64_t empty = __ballot(none);
+  if (p.out && empty) {
+    for (uint32_t b = lane * VEC; b < p.d; b += 64 * VEC) {
+      const uint32_t c = column_of<VEC>(b, p.d);
+      float v[VEC] = {};
+      if (p.bias) load_vec<T, VEC>(static_cast<const T*>(p.bias) + c, v);
+      uint32_t turn = 0;
+      for (uint64_t m = empty; m; m &= m - 1) {
+        if (turn++ % 4 != wave) continue;
+        const uint64_t key = k0 + (uint32_t)__ffsll((unsigned long long)m) - 1;
+        store_out<T, VEC>(static_cast<T*>(p.out) + (int64_t)key * p.ldo + c, v, p.stream);
+      }
+    }
+  }
+  uint32_t turn = 0;
+  for (uint64_t m = __ballot(mine && lq1 > lq0 + 1); m; m &= m - 1) {   // (one chunk: written there)
+    if (turn++ % 4 != wave) continue;
+    const uint32_t i = (uint32_t)__ffsll((unsigned long long)m) - 1;
     const uint32_t q0 = __builtin_amdgcn_readlane(lq0, i), q1 = __builtin_amdgcn_readlane(lq1, i);
-    if (q1 == q0 + 1) continue;                  // written by its chunk
     if (p.coef_sum) {
       float s = 0.f;
       for (uint32_t q = q0 + lane; q < q1; q += 64) s += p.part_c[(size_t)q * 2 + (q == q0)];
@@ -662,9 +701,8 @@ __global__ __launch_bounds__(256) void k_join_runs(KSegs ss) {
     }
   }
   if (!p.out) return;
-  uint64_t many = __ballot(lane < p.join && lq1 - lq0 > LONG);
-  for (; many; many &= many - 1) {
-    const uint32_t i = (uint32_t)__ffsll((unsigned long long)many) - 1;
+  for (uint64_t m = __ballot(mine && lq1 - lq0 > LONG); m; m &= m - 1) {
+    const uint32_t i = (uint32_t)__ffsll((unsigned long long)m) - 1;
     const uint32_t q0 = __builtin_amdgcn_readlane(lq0, i), q1 = __builtin_amdgcn_readlane(lq1, i);
     const uint32_t per = (q1 - q0 + 3) / 4, a0 = q0 + wave * per, a1 = a0 + per < q1 ? a0 + per : q1;
     for (uint32_t b = 0; b < p.d; b += 64 * VEC) {
@@ -698,8 +736,9 @@ __global__ __launch_bounds__(256) void k_join_runs(KSegs ss) {
 // 10 us for 256 entries, wherever it runs: few rows of many entries are split
 // over several workgroups, each with `chunk` of them, whose sums go to the
 // workspace and are added in order by a second launch (one row of 1024, 4096
-// and 65536 entries of 512 bf16: 38, 164 and 2697 us unsplit; 15, 19 and 69
-// split; 18, 34 and 173 through the sort).
+// and 65536 entries of 512 bf16: 38, 164 and 2697 us unsplit; 15, 16 and 24
+// split; 18, 34 and 173 through the sort).  1024 rows of 256 entries of 512
+// bf16, out of 64 MB of weights: 39 us, 6.9 TB/s of source rows.
 constexpr uint32_t KEEP = 1024;        // entries held in LDS
 constexpr uint32_t ROWS_AHEAD = 8;     // rows of src in flight per wave
 
@@ -820,16 +859,17 @@ __global__ __launch_bounds__(256) void k_dots(KSel s, const T* __restrict__ g, i
 // ---------------------------------------------------------------- host side
 // Rows straight from the selection: row-wise, or few enough reads that every
 // row may look at every index.  512 bf16, against the way through the sort:
-// 2048 rows and 4096 entries 24.4 us to 26, 8192 entries 42.6 to 25.8; 256
-// rows and 8192 entries 17 to 26; 16 rows and 65536 entries 43 to 37, one row
-// 69 to 172.
+// 64 rows and 65536 entries 30.5 us to 31.6, 128 rows 39 to 31; 1024 rows and
+// 4096 entries 20 to 25, 8192 entries 29 to 25; 16 rows and 65536 entries 22 to
+// 38; 8 rows and 2^20 entries 199 to 330.
 bool rows_direct(const Selection& s) {
-  return !s.flat || (s.rows * s.total <= (int64_t(1) << 23) && (s.total <= 16384 || s.rows <= 8));
+  if (!s.flat) return true;
+  return s.rows <= 8 ? s.total <= (int64_t(1) << 20) : s.total <= 65536 && s.rows * s.total <= (int64_t(1) << 22);
 }
 
 // How the entries that a row's workgroup goes through are split: into pieces of
 // 256 or more while the rows alone do not give eight workgroups for each of
-// 256 compute units, at most 64 (the join reads them one after another).
+// 256 compute units, at most 256 (16 threads of the join share their sums).
 struct RowsPlan {
   uint32_t columns = 1, splits = 1, chunk = 1, ldpart = 0;
   size_t bytes = 0;
@@ -840,7 +880,7 @@ RowsPlan rows_plan(const Selection& s, int64_t d) {
   const int64_t v = s.dtype == DT_BF16 ? 8 : 4, span = s.flat ? s.total : s.k;
   p.columns = (uint32_t)std::max<int64_t>(1, ceil_div(d, 64 * (d >= v ? v : 1)));
   const int64_t room = 2048 / std::max<int64_t>(1, s.rows * (int64_t)p.columns);
-  const int64_t splits = std::max<int64_t>(1, std::min<int64_t>({room, 64, ceil_div(span, 256)}));
+  const int64_t splits = std::max<int64_t>(1, std::min<int64_t>({room, 256, ceil_div(span, 256)}));
   p.chunk = (uint32_t)(ceil_div(std::max<int64_t>(1, span), splits * 256) * 256);
   p.splits = (uint32_t)std::max<int64_t>(1, ceil_div(span, p.chunk));
   p.ldpart = (uint32_t)(ceil_div(d, 4) * 4);
@@ -984,7 +1024,7 @@ hipError_t run_seg(const SegCall& a, char* ws, hipStream_t s) {
     k.keys = (uint32_t)keys;
     k.total = (uint32_t)a.sel.total;
     k.d = (uint32_t)a.d;
-    k.join = join_keys(k.keys);
+    k.stream = keys * a.d * (int64_t)sizeof(T) >= STREAM_BYTES;
     if (p.dots) {
       // fused where a lane holds its whole share of both rows
       if (wide && a.d <= 128 * V && a.sel.total) {
@@ -1040,6 +1080,7 @@ hipError_t run_seg(const SegCall& a, char* ws, hipStream_t s) {
     k.part = reinterpret_cast<float*>(ws + plans[n].off_part);
     k.part_c = reinterpret_cast<float*>(ws + plans[n].off_part_c);
     k.chunk = plans[n].chunk;
+    k.join = join_keys(k.keys, plans[n].chunks);
     sorted[n] = &p;
     at[n] = ws;
     ks.s[n++] = k;
