@@ -318,6 +318,12 @@ __device__ __forceinline__ void gemm_step(lds_char* cur, lds_char* next, LA& la,
   }
 }
 
+// Measured beside the vendor library's plain product of the same operands
+// (normal random numbers; the rates follow the clock, which follows the data):
+// bf16 8192^3 890 us against 798, 4096^3 109 against 97; 4096 x 512 x 65536,
+// which the store of 537 MB bounds as much as the products, 365 against 320
+// (with bias and relu over an autoencoder's numbers 310 against 342); f32
+// 4096^3 1090 against 1007.
 template <class T, int TM, int TN, int NWM, int NWN, bool TA, bool TB>
 __global__ __launch_bounds__(NWM * NWN * 64, 2) void k_gemm(KGemm p) {
 #ifdef __HIP_DEVICE_COMPILE__   // buffer resources exist in the device pass only
@@ -428,7 +434,9 @@ __global__ __launch_bounds__(NWM * NWN * 64, 2) void k_gemm(KGemm p) {
 // Adds partial sums in a fixed order, then the epilogue: the split tiles of up
 // to two products, and the column sums' blocks (a product of one row), in one
 // launch.  A thread takes 16 bytes of y; where there are many parts several
-// threads share them, and add theirs in LDS.
+// threads share them, and add theirs in LDS: 64 parts read one after another
+// would take longer than the tiles (33 x 12288 x 512 bf16: 33 us against 15).
+// Four parts of 4096 x 512 bf16 and 64 of 12288 column sums: 9.8 us, 3.8 TB/s.
 struct KJoin {
   const float* part;     // [split][m][ldpart], or, for split tiles, [split][rest][tile][tile]
   uint32_t split, ldpart;
@@ -531,7 +539,8 @@ hipError_t run_joins(const KJoin* js, int n, hipStream_t s) {
 }
 
 // Copies lines of `red` elements to lines of `ldo`, zeros behind their end;
-// both operands of a product in one launch (`vecs` 0: not this one).
+// both operands of a product in one launch (`vecs` 0: not this one).  Rows of
+// 515 f32 of 1001 x 515 and 4099 x 515: 6.7 us, 3.1 TB/s.
 struct KPack {
   const void* src;
   void* dst;
@@ -875,8 +884,9 @@ hipError_t run_gemm(const GemmArgs& g, char* ws, hipStream_t s) {
 }
 
 // ---------------------------------------------------------------- slope pass
-// dz = dy * act'(z), and the column sums of dz in 32 bits: a workgroup of
-// four waves takes 64 VEC columns and a block of rows; each lane sums its VEC
+// dz = dy * act'(z), and the column sums of dz in 32 bits.  Bound by memory:
+// 4096 x 12288 bf16 with relu reads 201 MB and writes 101, 55 us, 5.5 TB/s.  A
+// workgroup of four waves takes 64 VEC columns and a block of rows; each lane sums its VEC
 // columns down the block's rows, the four waves join in LDS, and one partial
 // row per block goes to the workspace, to be joined in block order.
 template <class T, int ACT, int VEC>
