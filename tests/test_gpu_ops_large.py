@@ -2,9 +2,17 @@
 import pytest
 import torch
 
-from top_selection_sample_amd import decode, decode_grad, linear
+import ops_util as U
+from top_selection_sample_amd import decode, decode_grad, linear, linear_grad
 
 pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
 
 
 @pytest.mark.parametrize("strided", ["x", "weight"])
@@ -60,3 +68,36 @@ def test_gradient_of_the_most_latents():
     at = torch.nonzero(dw[:, 0])[:, 0]
     assert at.tolist() == [0, 5, n - 1]
     assert dw[at, 0].tolist() == [2.0, 4.0, 6.0 + 32.0]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("m,n,k", [(1001, 4099, 515), (1024, 4160, 512), (2100, 2200, 2048), (1090, 8200, 520), (4200, 4352, 1024)])
+def test_tiles_behind_the_last_full_round(m, n, k, dt):
+    # those are split along the summed axis and joined, the others are not
+    g = torch.Generator().manual_seed(8)
+    draw = lambda *shape, scale=1.0: (torch.randn(*shape, generator=g) * scale).to(DT[dt]).cuda()
+    x, w, b, r = draw(m, k), draw(n, k, scale=k ** -0.5), draw(n), draw(m, n)
+    want = U.linear64(x, w, b, "silu", r)
+    xt, wt = x.t().contiguous().t(), w.t().contiguous().t()
+    for xx, ww in ((x, w), (x, wt), (xt, w), (xt, wt)):
+        U.within(linear(xx, ww, b, "silu", r), want[0], want[1], f"{m}x{n}x{k}")
+    assert torch.equal(linear(x, w, b, "silu", r), linear(x, w, b, "silu", r))
+    dy = draw(m, n)
+    refs, errs = U.linear_grad64(dy, x, w, r, "gelu")
+    for got, ref, err in zip(linear_grad(dy, x, w, activation="gelu", pre=r), refs, errs):
+        U.within(got, ref, err, f"gradient {m}x{n}x{k}")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("m,n,k", [(1, 16, 4096), (16, 300, 8191), (3, 4097, 2049), (31, 65, 4095), (17, 40, 1025),
+                                   (33, 64, 8192), (20, 7, 100_000), (129, 65, 20_001)])
+def test_deep_products_of_few_rows(m, n, k, dt):
+    g = torch.Generator().manual_seed(9)
+    draw = lambda *shape, scale=1.0: (torch.randn(*shape, generator=g) * scale).to(DT[dt]).cuda()
+    x, w, b, r = draw(m, k), draw(n, k, scale=k ** -0.5), draw(n), draw(m, n)
+    want = U.linear64(x, w, b, "gelu", r)
+    U.within(linear(x, w, b, "gelu", r), want[0], want[1], f"{m}x{n}x{k}")
+    dy = draw(m, n)
+    refs, errs = U.linear_grad64(dy, x, w, r, "relu")
+    for got, ref, err in zip(linear_grad(dy, x, w, activation="relu", pre=r), refs, errs):
+        U.within(got, ref, err, f"gradient {m}x{n}x{k}")
