@@ -106,6 +106,7 @@ struct KGemm {
   float* part;       // sums of split tiles: [split][rest][TM][TN]
   uint32_t tiles_m, tiles_n;
   uint32_t whole, rest, split;   // the first `whole` tiles run the epilogue, the others are split
+  uint32_t pieces;               // whole + rest * split: the workgroups
   uint32_t steps, all_steps;     // steps along the summed axis of a piece, and of a whole tile
 };
 
@@ -318,25 +319,13 @@ __device__ __forceinline__ void gemm_step(lds_char* cur, lds_char* next, LA& la,
   }
 }
 
-// Measured beside the vendor library's plain product of the same operands
-// (normal random numbers; the rates follow the clock, which follows the data):
-// bf16 8192^3 890 us against 798, 4096^3 109 against 97; 4096 x 512 x 65536,
-// which the store of 537 MB bounds as much as the products, 365 against 320
-// (with bias and relu over an autoencoder's numbers 310 against 342); f32
-// 4096^3 1090 against 1007.
+// Workgroup `id` of a product: a tile, or a piece of one.
 template <class T, int TM, int TN, int NWM, int NWN, bool TA, bool TB>
-__global__ __launch_bounds__(NWM * NWN * 64, 2) void k_gemm(KGemm p) {
-#ifdef __HIP_DEVICE_COMPILE__   // buffer resources exist in the device pass only
+__device__ __forceinline__ void gemm_tile(const KGemm& p, uint32_t id, lds_char* s0, lds_char* s1, char* stage0) {
   constexpr int FR = Elem<T>::FR, W = NWM * NWN, FM = TM / FR / NWM, FN = TN / FR / NWN;
   typedef typename Elem<T>::Acc Acc;
-  __shared__ __align__(1024) char stage0[(TM + TN) * 128];
-  __shared__ __align__(1024) char stage1[(TM + TN) * 128];
-  lds_char* s0 = (lds_char*)stage0;
-  lds_char* s1 = (lds_char*)stage1;
   const uint32_t lane = threadIdx.x % 64;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  const uint32_t id = block_id();
-  if (id >= p.whole + p.rest * p.split) return;
   uint32_t tile, piece = 0, k0 = 0, k1 = p.all_steps;
   const bool split = id >= p.whole;
   if (!split) {
@@ -428,6 +417,39 @@ __global__ __launch_bounds__(NWM * NWN * 64, 2) void k_gemm(KGemm p) {
       }
     }
   }
+}
+
+// Measured beside the vendor library's plain product of the same operands
+// (normal random numbers; the rates follow the clock, which follows the data):
+// bf16 8192^3 890 us against 798, 4096^3 109 against 97; 4096 x 512 x 65536,
+// which the store of 537 MB bounds as much as the products, 365 against 320
+// (with bias and relu over an autoencoder's numbers 310 against 342); f32
+// 4096^3 1090 against 1007.
+template <class T, int TM, int TN, int NWM, int NWN, bool TA, bool TB>
+__global__ __launch_bounds__(NWM * NWN * 64, 2) void k_gemm(KGemm p) {
+#ifdef __HIP_DEVICE_COMPILE__   // buffer resources exist in the device pass only
+  __shared__ __align__(1024) char stage0[(TM + TN) * 128];
+  __shared__ __align__(1024) char stage1[(TM + TN) * 128];
+  const uint32_t id = block_id();
+  if (id >= p.pieces) return;
+  gemm_tile<T, TM, TN, NWM, NWN, TA, TB>(p, id, (lds_char*)stage0, (lds_char*)stage1, stage0);
+#endif
+}
+
+// Both products of a gradient, dx = dz W and dW = dz^T x, side by side: the
+// workgroups of one fill the compute units that the other's last ones leave.
+// The one with the longer pieces goes first (`b_first`).
+template <class T, int TM, int TN, int NWM, int NWN>
+__global__ __launch_bounds__(NWM * NWN * 64, 2) void k_gemm_pair(KGemm a, KGemm b, int b_first) {
+#ifdef __HIP_DEVICE_COMPILE__
+  __shared__ __align__(1024) char stage0[(TM + TN) * 128];
+  __shared__ __align__(1024) char stage1[(TM + TN) * 128];
+  const uint32_t id = block_id(), first = b_first ? b.pieces : a.pieces;
+  if (id >= a.pieces + b.pieces) return;
+  if ((id < first) == (b_first != 0))
+    gemm_tile<T, TM, TN, NWM, NWN, true, true>(b, id < first ? id : id - first, (lds_char*)stage0, (lds_char*)stage1, stage0);
+  else
+    gemm_tile<T, TM, TN, NWM, NWN, false, true>(a, id < first ? id : id - first, (lds_char*)stage0, (lds_char*)stage1, stage0);
 #endif
 }
 
@@ -813,11 +835,24 @@ struct Product {
     return Epi{g.bias, g.residual, g.c, g.pre, g.ldr, g.ldc, g.ldp, (uint32_t)g.m, (uint32_t)g.n, g.act,
                g.m * g.n * ES >= STREAM_BYTES};
   }
-  hipError_t tiles(hipStream_t s) const {
+  KGemm args() const {
     KGemm k{};
     k.a = operand(g.a, g.m, p.pack_a, p.lda, ws);
     k.b = operand(g.b, g.n, p.pack_b, p.ldb, ws + p.off_b);
     k.e = epilogue();
+    k.part = reinterpret_cast<float*>(ws + p.off_part);
+    k.tiles_m = p.tiles_m;
+    k.tiles_n = p.tiles_n;
+    k.whole = p.whole;
+    k.rest = p.rest;
+    k.split = p.split;
+    k.pieces = p.whole + p.rest * p.split;
+    k.steps = p.steps;
+    k.all_steps = p.all_steps;
+    return k;
+  }
+  hipError_t tiles(hipStream_t s) const {
+    const KGemm k = args();
     if (p.few) {
       const dim3 grid((uint32_t)ceil_div(g.n, 16));
       // 16 waves where each has a turn, unless the workgroups alone fill the card
@@ -829,15 +864,7 @@ struct Product {
       else hipLaunchKernelGGL((k_few_rows<T, 2, 4>), grid, dim3(256), 0, s, k);
       return hipGetLastError();
     }
-    k.part = reinterpret_cast<float*>(ws + p.off_part);
-    k.tiles_m = p.tiles_m;
-    k.tiles_n = p.tiles_n;
-    k.whole = p.whole;
-    k.rest = p.rest;
-    k.split = p.split;
-    k.steps = p.steps;
-    k.all_steps = p.all_steps;
-    const dim3 grid = wide_grid(p.whole + (uint64_t)p.rest * p.split);
+    const dim3 grid = wide_grid(k.pieces);
     if constexpr (ES == 2) {
       if (p.tile == 256) {
         go<T, 256, 2, 4>(k, g.a.trans, g.b.trans, grid, s);
@@ -1036,6 +1063,24 @@ GradPlan plan_grad(const GradArgs& a) {
   return p;
 }
 
+// Whether one launch can take both products: the same tile, dz and the
+// others as they lie when x and W are stored by rows, no product of few rows.
+template <class T>
+bool pairs(const Product<T>& x, const Product<T>& w) {
+  return !x.p.few && !w.p.few && x.p.tile == w.p.tile && x.p.tile < 256 && !x.g.a.trans && x.g.b.trans &&
+         w.g.a.trans && w.g.b.trans;
+}
+
+template <class T>
+hipError_t run_pair(const Product<T>& x, const Product<T>& w, hipStream_t s) {
+  const KGemm a = x.args(), b = w.args();
+  const uint32_t la = a.whole ? a.all_steps : a.steps, lb = b.whole ? b.all_steps : b.steps;
+  const dim3 grid = wide_grid((uint64_t)a.pieces + b.pieces);
+  if (x.p.tile == 128) hipLaunchKernelGGL((k_gemm_pair<T, 128, 128, 2, 2>), grid, dim3(256), 0, s, a, b, lb > la);
+  else hipLaunchKernelGGL((k_gemm_pair<T, 64, 64, 2, 2>), grid, dim3(256), 0, s, a, b, lb > la);
+  return hipGetLastError();
+}
+
 template <class T>
 hipError_t run_grad(const GradArgs& a, char* ws, hipStream_t s) {
   GradPlan p = plan_grad(a);
@@ -1053,8 +1098,12 @@ hipError_t run_grad(const GradArgs& a, char* ws, hipStream_t s) {
   if (dw) np += qw.packs(packs + np);
   hipError_t e = run_slope_act<T>(p.slope, sums, s);
   for (int i = 0; i < np && e == hipSuccess; i += 2) e = run_packs<T>(packs + i, std::min(2, np - i), s);
-  if (e == hipSuccess && dx) e = qx.tiles(s);
-  if (e == hipSuccess && dw) e = qw.tiles(s);
+  if (e == hipSuccess && dx && dw && pairs(qx, qw)) {
+    e = run_pair(qx, qw, s);
+  } else {
+    if (e == hipSuccess && dx) e = qx.tiles(s);
+    if (e == hipSuccess && dw) e = qw.tiles(s);
+  }
   if (dx) nj += qx.joins(joins + nj);
   if (dw) nj += qw.joins(joins + nj);
   nj += slope_join(p.slope, sums, joins + nj);
