@@ -437,8 +437,9 @@ def encode(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None, k_t
     ``x`` [rows, d], ``weight`` [n, d], ``bias`` [n]; float32 or bfloat16.
     Differentiable (once) in x, weight and bias through the selected entries
     above 0 (the others have no gradient); the backward touches those entries
-    only.  Under graph capture with gradients off, and ``encode_grad``.  ``params``, ``workspace``: as ``topk``'s (a captured call needs a
-    workspace of its own)."""
+    only.  Under graph capture with gradients off, and ``encode_grad``.
+    ``params``, ``workspace``: as ``topk``'s (a captured call needs a workspace
+    of its own)."""
     _gpu(x, "x")
     _code(x, "x")
     if x.dim() != 2 or not isinstance(weight, torch.Tensor) or weight.dim() != 2:
@@ -506,7 +507,8 @@ def _norm_run(tensors, clip):
     if index < 0 or devices:
         raise ValueError(f"tensors: all on one GPU (found {', '.join(sorted({str(t.device) for t in ts}))})")
     dtypes = list(map(_dtype_of, ts))
-    for dtype in set(dtypes):
+    kinds = set(dtypes)
+    for dtype in kinds:
         if dtype not in _CODES:
             raise TypeError(f"tensors: unsupported dtype {dtype}; use float32 or bfloat16")
     if not all(map(_T.is_contiguous, ts)) and not all(map(_dense, ts)):
@@ -514,7 +516,8 @@ def _norm_run(tensors, clip):
     # flat host arrays, passed by address; they live until the call has read them
     ptrs = array("Q", map(_T.data_ptr, ts))
     counts = array("q", map(_T.numel, ts))
-    codes = array("i", map(_CODES.__getitem__, dtypes))
+    codes = (array("i", map(_CODES.__getitem__, dtypes)) if len(kinds) > 1
+             else array("i", [_CODES[dtypes[0]]]) * len(ts))
     args = (ptrs.buffer_info()[0], counts.buffer_info()[0], codes.buffer_info()[0], len(ts))
     with _on(index):
         norm = ts[0].new_empty((), dtype=torch.float32)

@@ -437,8 +437,10 @@ __global__ __launch_bounds__(NWM * NWN * 64, 2) void k_gemm(KGemm p) {
 }
 
 // Both products of a gradient, dx = dz W and dW = dz^T x, side by side: the
-// workgroups of one fill the compute units that the other's last ones leave.
-// The one with the longer pieces goes first (`b_first`).
+// workgroups of one fill the compute units that the other's last ones leave
+// (the whole call, 4096 x 512 x 12288 bf16 208 us in two launches, 201 in one;
+// 2048 x 1024 x 4096 f32 311, 292).  The one with the longer pieces goes first
+// (`b_first`).
 template <class T, int TM, int TN, int NWM, int NWN>
 __global__ __launch_bounds__(NWM * NWN * 64, 2) void k_gemm_pair(KGemm a, KGemm b, int b_first) {
 #ifdef __HIP_DEVICE_COMPILE__
