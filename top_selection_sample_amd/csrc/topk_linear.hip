@@ -574,9 +574,8 @@ struct KPack {
 };
 
 template <class T>
-__global__ __launch_bounds__(256) void k_pack(KPack a, KPack b) {
+__device__ __forceinline__ void pack_vec(const KPack& a, const KPack& b, uint64_t i) {
   constexpr int V = Vec<T>::N;
-  uint64_t i = (uint64_t)block_id() * 256 + threadIdx.x;
   const bool second = i >= a.vecs;
   if (second) i -= a.vecs;
   const KPack p = second ? b : a;
@@ -600,11 +599,16 @@ __global__ __launch_bounds__(256) void k_pack(KPack a, KPack b) {
   *reinterpret_cast<u32x4*>(static_cast<T*>(p.dst) + r * p.ldo + c) = q;
 }
 
+template <class T>
+__global__ __launch_bounds__(256) void k_pack(KPack a, KPack b) {
+  pack_vec<T>(a, b, (uint64_t)block_id() * 256 + threadIdx.x);
+}
+
 // Few rows of x: the call is bound by reading W once.  A workgroup takes 16
-// rows of W (columns of y) and the whole summed axis; its W waves take turns
-// of 256 bytes per row of it, straight from memory into the matrix
-// instructions' operands, with all loads of a turn issued before the first is
-// used, and join their sums in LDS in wave order.  One row through 12288 x 512
+// rows of W (columns of y), 16 or 32 rows of x and the whole summed axis; its
+// W waves take turns of 256 bytes per row of it, straight from memory into the
+// matrix instructions' operands, with all loads of a turn issued before the
+// first is used, and join their sums in LDS in wave order.  One row through 12288 x 512
 // bf16 (12.6 MB): 4.4 us, 2.9 TB/s; its launch takes longer than that.
 template <class T>
 __device__ __forceinline__ u32x4 row_piece(const T* p, bool in, uint32_t k, uint32_t red) {
@@ -630,15 +634,16 @@ __global__ __launch_bounds__(W * 64) void k_few_rows(KGemm p) {
   __shared__ float join[W][MF][16][17];
   const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64;
   const uint32_t i = lane % 16, g = lane / 16;
-  const uint32_t n0 = blockIdx.x * 16, red = p.a.red;
+  const uint32_t n0 = blockIdx.x * 16, m0 = blockIdx.y * 16 * MF, red = p.a.red;
   const bool win = n0 + i < p.b.rows;
   const T* w = static_cast<const T*>(p.b.p) + (int64_t)(win ? n0 + i : 0) * p.b.ld;
   const T* x[MF];
   bool xin[MF];
 #pragma unroll
   for (int f = 0; f < MF; ++f) {
-    xin[f] = f * 16 + i < p.a.rows;
-    x[f] = static_cast<const T*>(p.a.p) + (int64_t)(xin[f] ? f * 16 + i : 0) * p.a.ld;
+    const uint32_t row = m0 + f * 16 + i;
+    xin[f] = row < p.a.rows;
+    x[f] = static_cast<const T*>(p.a.p) + (int64_t)(xin[f] ? row : 0) * p.a.ld;
   }
   f32x4 acc[1][MF];
 #pragma unroll
@@ -665,12 +670,12 @@ __global__ __launch_bounds__(W * 64) void k_few_rows(KGemm p) {
   bias_of<T, 1>(&bias, c, p.e);
 #pragma unroll
   for (int f = 0; f < MF; ++f) {
-    const uint32_t r = threadIdx.x / 16, at = threadIdx.x % 16;
-    if (f * 16 + r >= p.e.m) continue;
+    const uint32_t r = threadIdx.x / 16, at = threadIdx.x % 16, row = m0 + f * 16 + r;
+    if (row >= p.e.m) continue;
     float z = 0.f;
 #pragma unroll
     for (int q = 0; q < W; ++q) z += join[q][f][r][at];
-    finish<T, 1>(&z, &bias, f * 16 + r, c, p.e);
+    finish<T, 1>(&z, &bias, row, c, p.e);
   }
 }
 
@@ -767,8 +772,16 @@ Plan2 plan_gemm(const GemmArgs& g) {
   // 16384 x 4096 30 to 28, 512 x 12288 23 to 15; f32 4096 x 4096 19 to 29.
   // Beyond 16 rows x is read twice as often as by the tiles: 32 rows of bf16,
   // 4096 x 4096 14 us to 16, 16384 x 4096 46 to 28.
-  if (!g.a.trans && !g.b.trans && ((g.m <= 16 && g.k * es <= 16384) ||
-                                   (g.m <= 32 && g.k * es <= 8192 && g.n * g.k <= (int64_t(1) << 24)))) {
+  // More rows of a small product whose operands would have to be copied first
+  // go the same way, 32 at a time: the copy's launch costs more than the rows
+  // that are read again, out of the caches (x of m rows, n x k; bf16 206 x 1810
+  // x 157 9.9 us to 13.8, 1000 x 1000 x 131 13.0 to 13.9, 500 x 2000 x 259 17.5 to
+  // 14.1, 837 x 4439 x 31 22.7 to 14.0; f32 300 x 1000 x 515 11.9 to 19.4).
+  const int64_t line = g.k * es, blocks = ceil_div(g.m, 32) * ceil_div(g.n, 16);
+  const bool pack = needs_pack(g.a, g.m, g.k, es) || needs_pack(g.b, g.n, g.k, es);
+  if (!g.a.trans && !g.b.trans && ((g.m <= 16 && line <= 16384) ||
+                                   (g.m <= 32 && line <= 8192 && g.n * g.k <= (int64_t(1) << 24)) ||
+                                   (pack && line <= 8192 && blocks <= 2048 && blocks * 48 * g.k <= (int64_t(1) << 24)))) {
     p.few = true;
     return p;
   }
@@ -856,7 +869,7 @@ struct Product {
   hipError_t tiles(hipStream_t s) const {
     const KGemm k = args();
     if (p.few) {
-      const dim3 grid((uint32_t)ceil_div(g.n, 16));
+      const dim3 grid((uint32_t)ceil_div(g.n, 16), (uint32_t)ceil_div(g.m, g.m <= 16 ? 16 : 32));
       // 16 waves where each has a turn, unless the workgroups alone fill the card
       // (4096 x 4096 f32 16.8 us against 21.4; 16384 x 4096 56 against 54.7)
       const bool deep = g.k * ES >= 4096 && g.n < 16384;
@@ -915,19 +928,40 @@ hipError_t run_gemm(const GemmArgs& g, char* ws, hipStream_t s) {
 // ---------------------------------------------------------------- slope pass
 // dz = dy * act'(z), and the column sums of dz in 32 bits.  Bound by memory:
 // 4096 x 12288 bf16 with relu reads 201 MB and writes 101, 55 us, 5.5 TB/s.  A
-// workgroup of four waves takes 64 VEC columns and a block of rows; each lane sums its VEC
-// columns down the block's rows, the four waves join in LDS, and one partial
-// row per block goes to the workspace, to be joined in block order.
+// workgroup of four waves takes 64 VEC columns and a block of rows; each lane
+// sums its VEC columns down the block's rows, the four waves join in LDS, and
+// one partial row per block goes to the workspace, to be joined in block
+// order; a single block writes the sums themselves.  The workgroups behind
+// copy the products' other operands where they need it: small calls take as
+// long as their launches.
+template <class T>
+struct KSlope {
+  const T* dy;
+  const T* pre;
+  T* dz;             // null: not wanted
+  float* part;       // null: no column sums, or `db` takes them
+  T* db;
+  int64_t ldd, ldp, ldz;
+  uint32_t m, n, rows_per, ldpart;
+  uint32_t columns, blocks;   // workgroups side by side, and in all
+};
+
 template <class T, int ACT, int VEC>
-__global__ __launch_bounds__(256) void k_slope(const T* __restrict__ dy, const T* __restrict__ pre,
-                                               T* __restrict__ dz, float* __restrict__ part,
-                                               uint32_t m, uint32_t n, int64_t ldd, int64_t ldp,
-                                               int64_t ldz, uint32_t rows_per, uint32_t ldpart) {
+__global__ __launch_bounds__(256) void k_slope(KSlope<T> p, KPack pack_a, KPack pack_b) {
+  const uint32_t id = block_id();
+  if (id >= p.blocks) {
+    pack_vec<T>(pack_a, pack_b, (uint64_t)(id - p.blocks) * 256 + threadIdx.x);
+    return;
+  }
+  const T* __restrict__ dy = p.dy;
+  const T* __restrict__ pre = p.pre;
+  T* __restrict__ dz = p.dz;
+  const uint32_t bx = id % p.columns, by = id / p.columns, n = p.n;
   const uint32_t wave = threadIdx.x / 64, lane = threadIdx.x % 64;
-  const uint32_t c0 = (blockIdx.x * 64 + lane) * VEC;
+  const uint32_t c0 = (bx * 64 + lane) * VEC;
   const uint32_t c = c0 < n ? column_of<VEC>(c0, n) : 0u;
-  const uint32_t r0 = blockIdx.y * rows_per;
-  const uint32_t r1 = r0 + rows_per < m ? r0 + rows_per : m;
+  const uint32_t r0 = by * p.rows_per;
+  const uint32_t r1 = p.m - r0 < p.rows_per ? p.m : r0 + p.rows_per;
   // behind the last column: zeros up to whole 16 bytes
   constexpr uint32_t CHUNK = Vec<T>::N;
   const uint32_t fill = c0 < n && c0 + VEC >= n ? (n + CHUNK - 1) / CHUNK * CHUNK : n;
@@ -936,10 +970,10 @@ __global__ __launch_bounds__(256) void k_slope(const T* __restrict__ dy, const T
 #pragma unroll 4
     for (uint32_t r = r0 + wave; r < r1; r += 4) {
       float v[VEC];
-      load_vec<T, VEC>(dy + (int64_t)r * ldd + c, v);
+      load_vec<T, VEC>(dy + (int64_t)r * p.ldd + c, v);
       if constexpr (ACT != ACT_NONE) {
         float z[VEC];
-        load_vec<T, VEC>(pre + (int64_t)r * ldp + c, z);
+        load_vec<T, VEC>(pre + (int64_t)r * p.ldp + c, z);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
           if constexpr (ACT == ACT_RELU) v[i] = z[i] <= 0.f ? 0.f : v[i];
@@ -947,7 +981,7 @@ __global__ __launch_bounds__(256) void k_slope(const T* __restrict__ dy, const T
         }
       }
       if (dz) {
-        T* o = dz + (int64_t)r * ldz;
+        T* o = dz + (int64_t)r * p.ldz;
         store_vec<T, VEC>(o + c, v);
         for (uint32_t i = n; i < fill; ++i) o[i] = T{};
       }
@@ -955,57 +989,70 @@ __global__ __launch_bounds__(256) void k_slope(const T* __restrict__ dy, const T
       for (int i = 0; i < VEC; ++i) sum[i] += v[i];
     }
   }
-  if (!part) return;
+  if (!p.part && !p.db) return;
   __shared__ float join[4][64 * VEC];
 #pragma unroll
   for (int i = 0; i < VEC; ++i) join[wave][lane * VEC + i] = sum[i];
   __syncthreads();
   for (uint32_t i = threadIdx.x; i < 64 * VEC; i += 256) {
-    const uint32_t cc = (blockIdx.x * 64 + i / VEC) * VEC;
-    if (cc < n)   // columns that two lanes hold get the same sum from both
-      part[(size_t)blockIdx.y * ldpart + column_of<VEC>(cc, n) + i % VEC] =
-          (join[0][i] + join[1][i]) + (join[2][i] + join[3][i]);
+    const uint32_t cc = (bx * 64 + i / VEC) * VEC;
+    if (cc >= n) continue;
+    // (columns that two lanes hold get the same sum from both)
+    const uint32_t at = column_of<VEC>(cc, n) + i % VEC;
+    const float v = (join[0][i] + join[1][i]) + (join[2][i] + join[3][i]);
+    if (p.part) p.part[(size_t)by * p.ldpart + at] = v;
+    else p.db[at] = from_f32<T>(v);
   }
 }
 
-// Blocks of 64 rows, at most 65535 of them (grid dimension y).
-uint32_t slope_rows(int64_t m) { return (uint32_t)std::max<int64_t>(64, ceil_div(m, 65535)); }
+// Blocks of 64 rows, at most 65535 of them, or one of up to 128: a block more
+// would take the join's launch.
+uint32_t slope_rows(int64_t m) { return m <= 128 ? 128u : (uint32_t)std::max<int64_t>(64, ceil_div(m, 65535)); }
 uint32_t slope_blocks(int64_t m) { return (uint32_t)ceil_div(m, slope_rows(m)); }
 uint32_t slope_ld(int64_t n) { return (uint32_t)(ceil_div(n, 4) * 4); }
 
 template <class T, int ACT>
-hipError_t run_slope(const SlopeArgs& a, float* part, hipStream_t s) {
+hipError_t run_slope(const SlopeArgs& a, float* part, const KPack* packs, hipStream_t s) {
   constexpr int V = Vec<T>::N;
-  const bool wide = a.n >= V;
-  const dim3 grid((uint32_t)ceil_div(a.n, 64 * (wide ? V : 1)), slope_blocks(a.m));
-  const T* dy = static_cast<const T*>(a.dy);
-  const T* pre = static_cast<const T*>(a.pre);
-  T* dz = static_cast<T*>(a.dz);
-  if (!a.db) part = nullptr;
-  if (wide)
-    hipLaunchKernelGGL((k_slope<T, ACT, V>), grid, dim3(256), 0, s, dy, pre, dz, part, (uint32_t)a.m, (uint32_t)a.n,
-                       a.ldd, a.ldp, a.ldz, slope_rows(a.m), slope_ld(a.n));
-  else
-    hipLaunchKernelGGL((k_slope<T, ACT, 1>), grid, dim3(256), 0, s, dy, pre, dz, part, (uint32_t)a.m, (uint32_t)a.n,
-                       a.ldd, a.ldp, a.ldz, slope_rows(a.m), slope_ld(a.n));
+  const bool wide = a.n >= V, one = slope_blocks(a.m) == 1;
+  KSlope<T> k;
+  k.dy = static_cast<const T*>(a.dy);
+  k.pre = static_cast<const T*>(a.pre);
+  k.dz = static_cast<T*>(a.dz);
+  k.part = a.db && !one ? part : nullptr;
+  k.db = one ? static_cast<T*>(a.db) : nullptr;
+  k.ldd = a.ldd;
+  k.ldp = a.ldp;
+  k.ldz = a.ldz;
+  k.m = (uint32_t)a.m;
+  k.n = (uint32_t)a.n;
+  k.rows_per = slope_rows(a.m);
+  k.ldpart = slope_ld(a.n);
+  k.columns = (uint32_t)ceil_div(a.n, 64 * (wide ? V : 1));
+  k.blocks = k.columns * slope_blocks(a.m);
+  const dim3 grid = wide_grid(k.blocks + (packs[0].vecs + packs[1].vecs + 255) / 256);
+  if (wide) hipLaunchKernelGGL((k_slope<T, ACT, V>), grid, dim3(256), 0, s, k, packs[0], packs[1]);
+  else hipLaunchKernelGGL((k_slope<T, ACT, 1>), grid, dim3(256), 0, s, k, packs[0], packs[1]);
   return hipGetLastError();
 }
 
+bool slope_wanted(const SlopeArgs& a) { return a.m && a.n && (a.dz || a.db); }
+
 template <class T>
-hipError_t run_slope_act(const SlopeArgs& a, float* part, hipStream_t s) {
-  if (a.m == 0 || a.n == 0 || (!a.dz && !a.db)) return hipSuccess;
+hipError_t run_slope_act(const SlopeArgs& a, float* part, const KPack* packs, hipStream_t s) {
+  if (!slope_wanted(a)) return hipSuccess;
   switch (a.act) {
-    case ACT_RELU: return run_slope<T, ACT_RELU>(a, part, s);
-    case ACT_GELU: return run_slope<T, ACT_GELU>(a, part, s);
-    case ACT_SILU: return run_slope<T, ACT_SILU>(a, part, s);
-    default: return run_slope<T, ACT_NONE>(a, part, s);
+    case ACT_RELU: return run_slope<T, ACT_RELU>(a, part, packs, s);
+    case ACT_GELU: return run_slope<T, ACT_GELU>(a, part, packs, s);
+    case ACT_SILU: return run_slope<T, ACT_SILU>(a, part, packs, s);
+    default: return run_slope<T, ACT_NONE>(a, part, packs, s);
   }
 }
 
 // The column sums' join, as a product of one row whose parts are the blocks
-// (none for no rows: zeros).
+// (none for no rows: zeros).  One block has written them.
 int slope_join(const SlopeArgs& a, const float* part, KJoin* out) {
-  if (!a.db || !a.n) return 0;
+  if (!a.db || !a.n || slope_blocks(a.m) == 1) return 0;
   KJoin& j = out[0] = KJoin{};
   j.part = part;
   j.split = slope_blocks(a.m);
@@ -1093,13 +1140,16 @@ hipError_t run_grad(const GradArgs& a, char* ws, hipStream_t s) {
   float* sums = reinterpret_cast<float*>(ws + p.off_sums);
   const bool dx = a.dx && p.dx.m && p.dx.n, dw = a.dw && p.dw.m && p.dw.n;
   const Product<T> qx(p.dx, ws + p.off_dx), qw(p.dw, ws + p.off_dw);
-  KPack packs[4];
+  KPack packs[6] = {};
   KJoin joins[3];
   int np = 0, nj = 0;
   if (dx) np += qx.packs(packs + np);
   if (dw) np += qw.packs(packs + np);
-  hipError_t e = run_slope_act<T>(p.slope, sums, s);
-  for (int i = 0; i < np && e == hipSuccess; i += 2) e = run_packs<T>(packs + i, std::min(2, np - i), s);
+  // the copies ride in the pass over dy, unless one is of its result
+  const KPack none[2] = {};
+  const bool ride = slope_wanted(p.slope) && np <= 2 && !(dx && qx.p.pack_a) && !(dw && qw.p.pack_a);
+  hipError_t e = run_slope_act<T>(p.slope, sums, ride ? packs : none, s);
+  for (int i = 0; i < np && !ride && e == hipSuccess; i += 2) e = run_packs<T>(packs + i, std::min(2, np - i), s);
   if (e == hipSuccess && dx && dw && pairs(qx, qw)) {
     e = run_pair(qx, qw, s);
   } else {
@@ -1133,7 +1183,8 @@ hipError_t launch_slope(const SlopeArgs& a, void* ws, hipStream_t s) {
   float* part = static_cast<float*>(ws);
   KJoin join;
   const int n = slope_join(a, part, &join);
-  hipError_t e = a.dtype == DT_BF16 ? run_slope_act<bf16_t>(a, part, s) : run_slope_act<float>(a, part, s);
+  const KPack none[2] = {};
+  hipError_t e = a.dtype == DT_BF16 ? run_slope_act<bf16_t>(a, part, none, s) : run_slope_act<float>(a, part, none, s);
   if (e != hipSuccess) return e;
   return a.dtype == DT_BF16 ? run_joins<bf16_t>(&join, n, s) : run_joins<float>(&join, n, s);
 }
