@@ -946,6 +946,20 @@ struct KSlope {
   uint32_t columns, blocks;   // workgroups side by side, and in all
 };
 
+constexpr uint32_t SLOPE_AHEAD = 8;
+
+// A lane's elements of a row as they were read: 16 bytes, or one element.
+template <class T, int VEC>
+__device__ __forceinline__ u32x4 raw_vec(const T* p) {
+  if constexpr (VEC == 1) return u32x4{__float_as_uint(to_f32(p[0])), 0u, 0u, 0u};
+  else return read16(p);
+}
+template <class T, int VEC>
+__device__ __forceinline__ void unpack_vec(u32x4 q, float* v) {
+  if constexpr (VEC == 1) v[0] = __uint_as_float(q[0]);
+  else Vec<T>::unpack(q, v);
+}
+
 template <class T, int ACT, int VEC>
 __global__ __launch_bounds__(256) void k_slope(KSlope<T> p, KPack pack_a, KPack pack_b) {
   const uint32_t id = block_id();
@@ -966,14 +980,24 @@ __global__ __launch_bounds__(256) void k_slope(KSlope<T> p, KPack pack_a, KPack 
   constexpr uint32_t CHUNK = Vec<T>::N;
   const uint32_t fill = c0 < n && c0 + VEC >= n ? (n + CHUNK - 1) / CHUNK * CHUNK : n;
   float sum[VEC] = {};
-  if (c0 < n) {
-#pragma unroll 4
-    for (uint32_t r = r0 + wave; r < r1; r += 4) {
+  // all loads of SLOPE_AHEAD rows leave before the first is used
+  for (uint32_t rr = r0 + wave; rr < r1 && c0 < n; rr += 4 * SLOPE_AHEAD) {
+    u32x4 qd[SLOPE_AHEAD], qz[SLOPE_AHEAD];
+#pragma unroll
+    for (uint32_t u = 0; u < SLOPE_AHEAD; ++u) {
+      const uint32_t r = rr + 4 * u < r1 ? rr + 4 * u : rr;
+      qd[u] = raw_vec<T, VEC>(dy + (int64_t)r * p.ldd + c);
+      if constexpr (ACT != ACT_NONE) qz[u] = raw_vec<T, VEC>(pre + (int64_t)r * p.ldp + c);
+    }
+#pragma unroll
+    for (uint32_t u = 0; u < SLOPE_AHEAD; ++u) {
+      const uint32_t r = rr + 4 * u;
+      if (r >= r1) break;
       float v[VEC];
-      load_vec<T, VEC>(dy + (int64_t)r * p.ldd + c, v);
+      unpack_vec<T, VEC>(qd[u], v);
       if constexpr (ACT != ACT_NONE) {
         float z[VEC];
-        load_vec<T, VEC>(pre + (int64_t)r * p.ldp + c, z);
+        unpack_vec<T, VEC>(qz[u], z);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
           if constexpr (ACT == ACT_RELU) v[i] = z[i] <= 0.f ? 0.f : v[i];
@@ -1005,16 +1029,27 @@ __global__ __launch_bounds__(256) void k_slope(KSlope<T> p, KPack pack_a, KPack 
   }
 }
 
-// Blocks of 64 rows, at most 65535 of them, or one of up to 128: a block more
-// would take the join's launch.
-uint32_t slope_rows(int64_t m) { return m <= 128 ? 128u : (uint32_t)std::max<int64_t>(64, ceil_div(m, 65535)); }
-uint32_t slope_blocks(int64_t m) { return (uint32_t)ceil_div(m, slope_rows(m)); }
+// Workgroups side by side.
+uint32_t slope_columns(const SlopeArgs& a) {
+  const int64_t v = a.dtype == DT_BF16 ? 8 : 4;
+  return (uint32_t)ceil_div(a.n, 64 * (a.n >= v ? v : 1));
+}
+// Rows of a block: 64, fewer while there is less than a workgroup for each of
+// 256 compute units (a row of gelu or silu takes a wave alone 1.6 us: 225 x 35
+// bf16 30 us in blocks of 64), more beyond 65535 blocks.  A few rows are one
+// block, which spares the join's launch.
+uint32_t slope_rows(const SlopeArgs& a) {
+  if (a.m <= (a.act > ACT_RELU ? 16 : 64)) return 64;
+  const int64_t share = ceil_div(a.m * slope_columns(a), 256 * 4) * 4;
+  return (uint32_t)std::max(std::min<int64_t>(64, share), ceil_div(a.m, 65535));
+}
+uint32_t slope_blocks(const SlopeArgs& a) { return (uint32_t)ceil_div(a.m, slope_rows(a)); }
 uint32_t slope_ld(int64_t n) { return (uint32_t)(ceil_div(n, 4) * 4); }
 
 template <class T, int ACT>
 hipError_t run_slope(const SlopeArgs& a, float* part, const KPack* packs, hipStream_t s) {
   constexpr int V = Vec<T>::N;
-  const bool wide = a.n >= V, one = slope_blocks(a.m) == 1;
+  const bool wide = a.n >= V, one = slope_blocks(a) == 1;
   KSlope<T> k;
   k.dy = static_cast<const T*>(a.dy);
   k.pre = static_cast<const T*>(a.pre);
@@ -1026,10 +1061,10 @@ hipError_t run_slope(const SlopeArgs& a, float* part, const KPack* packs, hipStr
   k.ldz = a.ldz;
   k.m = (uint32_t)a.m;
   k.n = (uint32_t)a.n;
-  k.rows_per = slope_rows(a.m);
+  k.rows_per = slope_rows(a);
   k.ldpart = slope_ld(a.n);
-  k.columns = (uint32_t)ceil_div(a.n, 64 * (wide ? V : 1));
-  k.blocks = k.columns * slope_blocks(a.m);
+  k.columns = slope_columns(a);
+  k.blocks = k.columns * slope_blocks(a);
   const dim3 grid = wide_grid(k.blocks + (packs[0].vecs + packs[1].vecs + 255) / 256);
   if (wide) hipLaunchKernelGGL((k_slope<T, ACT, V>), grid, dim3(256), 0, s, k, packs[0], packs[1]);
   else hipLaunchKernelGGL((k_slope<T, ACT, 1>), grid, dim3(256), 0, s, k, packs[0], packs[1]);
@@ -1052,10 +1087,10 @@ hipError_t run_slope_act(const SlopeArgs& a, float* part, const KPack* packs, hi
 // The column sums' join, as a product of one row whose parts are the blocks
 // (none for no rows: zeros).  One block has written them.
 int slope_join(const SlopeArgs& a, const float* part, KJoin* out) {
-  if (!a.db || !a.n || slope_blocks(a.m) == 1) return 0;
+  if (!a.db || !a.n || slope_blocks(a) == 1) return 0;
   KJoin& j = out[0] = KJoin{};
   j.part = part;
-  j.split = slope_blocks(a.m);
+  j.split = slope_blocks(a);
   j.ldpart = slope_ld(a.n);
   j.e.c = a.db;
   j.e.m = 1;
@@ -1176,7 +1211,7 @@ hipError_t launch_gemm(const GemmArgs& g, void* ws, hipStream_t s) {
 }
 
 size_t slope_workspace(const SlopeArgs& a) {
-  return a.db ? align256((size_t)slope_blocks(a.m) * slope_ld(a.n) * 4) : 0;
+  return a.db ? align256((size_t)slope_blocks(a) * slope_ld(a.n) * 4) : 0;
 }
 
 hipError_t launch_slope(const SlopeArgs& a, void* ws, hipStream_t s) {
