@@ -747,8 +747,8 @@ void choose_tile(const GemmArgs& g, Plan2* p) {
         else
           us += std::max((double)steps * t.alone, (double)(left * steps + b * per) * t.shared) +
                 t.ends * (double)ceil_div(left + b, t.holds);
-        // joining the parts: a launch, and their way through memory
-        if (parts > 1) us += 4 + (double)g.m * (double)g.n * (double)rest / (double)tiles * (double)parts * 2e-6;
+        // joining the parts: a launch (4 us on the device, 5 of the host), and their way through memory
+        if (parts > 1) us += 6 + (double)g.m * (double)g.n * (double)rest / (double)tiles * (double)parts * 2e-6;
         if (us < best) {
           best = us;
           p->tile = t.tile;
