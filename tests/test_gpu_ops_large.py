@@ -101,3 +101,24 @@ def test_deep_products_of_few_rows(m, n, k, dt):
     refs, errs = U.linear_grad64(dy, x, w, r, "relu")
     for got, ref, err in zip(linear_grad(dy, x, w, activation="relu", pre=r), refs, errs):
         U.within(got, ref, err, f"gradient {m}x{n}x{k}")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("m,n", [(3067, 4686), (2100, 4103), (2500, 4161), (600, 1031), (70, 69), (130, 129)])
+def test_last_columns_and_a_residual_in_place(m, n, dt):
+    k = 64
+    g = torch.Generator().manual_seed(10)
+    draw = lambda *shape, scale=1.0: (torch.randn(*shape, generator=g) * scale).to(DT[dt]).cuda()
+    x, w, b, r = draw(m, k), draw(n, k, scale=0.2), draw(n), draw(m, n)
+    want = U.linear64(x, w, b, "silu", r)
+    U.within(linear(x, w, b, "silu", r), want[0], want[1], f"{m}x{n}")
+    import ctypes
+    from top_selection_sample_amd import _lib, dtype_code
+    y = r.clone()
+    a = _lib.LinearArgs(x.data_ptr(), w.data_ptr(), b.data_ptr(), y.data_ptr(), y.data_ptr(), None, m, n, k, k, k, n, n, n,
+                        dtype_code(DT[dt]), _lib.ACTIVATIONS["silu"], 0, 0)
+    size = ctypes.c_size_t()
+    assert _lib.lib.topk_linear_workspace_size(ctypes.byref(a), ctypes.byref(size)) == 0
+    ws = torch.empty(size.value + 1, dtype=torch.uint8, device="cuda")
+    assert _lib.lib.topk_linear(ctypes.byref(a), ws.data_ptr(), size.value, torch.cuda.current_stream().cuda_stream) == 0
+    U.within(y, want[0], want[1], f"in place {m}x{n}")

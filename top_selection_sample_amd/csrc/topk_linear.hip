@@ -63,12 +63,47 @@ __device__ __forceinline__ void finish(float* v, const float* bias, uint32_t r, 
   }
 }
 
+// The same for a row's last columns, `have` < V of them, element by element:
+// all loads first, so that they wait together.
+template <class T, int V>
+__device__ __forceinline__ void finish_some(float* v, const float* bias, uint32_t r, uint32_t c, uint32_t have,
+                                            const Epi& e) {
+  float q[V];
+  if (e.residual) {
+    const T* p = static_cast<const T*>(e.residual) + (int64_t)r * e.ldr + c;
+#pragma unroll
+    for (int i = 0; i < V; ++i) q[i] = (uint32_t)i < have ? to_f32(p[i]) : 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] += bias[i];
+  if (e.pre) {
+    T* p = static_cast<T*>(e.pre) + (int64_t)r * e.ldp + c;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if ((uint32_t)i < have) p[i] = from_f32<T>(v[i]);
+  }
+  act_any<T, V>(v, e.act);
+  if (e.residual) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] += q[i];
+  }
+  T* y = static_cast<T*>(e.c) + (int64_t)r * e.ldc + c;
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if ((uint32_t)i < have) y[i] = from_f32<T>(v[i]);
+}
+
 // The bias of V columns, 0 where there is none.
 template <class T, int V>
 __device__ __forceinline__ void bias_of(float* b, uint32_t c, const Epi& e) {
 #pragma unroll
   for (int i = 0; i < V; ++i) b[i] = 0.f;
   if (e.bias) load_vec<T, V>(static_cast<const T*>(e.bias) + c, b);
+}
+template <class T, int V>
+__device__ __forceinline__ void bias_some(float* b, uint32_t c, uint32_t have, const Epi& e) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) b[i] = e.bias && (uint32_t)i < have ? to_f32(static_cast<const T*>(e.bias)[c + i]) : 0.f;
 }
 
 // ---------------------------------------------------------------- product
@@ -372,10 +407,22 @@ __device__ __forceinline__ void gemm_tile(const KGemm& p, uint32_t id, lds_char*
   constexpr uint32_t LANES = C / V, ROWS = 64 / LANES;
   static_assert(W * 32 * C * 4 <= (TM + TN) * 128, "the rows fit one stage");
   float* mine = reinterpret_cast<float*>(stage0) + wave * 32 * C;
-  const uint32_t cc = (lane % LANES) * V, c = n0 + wn * FR + cc;
+  uint32_t cc = (lane % LANES) * V, c = n0 + wn * FR + cc;
+  // A row's last vector begins earlier, so that it ends with the row, and two
+  // lanes store the same values to the columns between (3067 x 4686 bf16 15.6
+  // us; 30.7 with those columns one by one, which the last tiles' waves did
+  // after all others).  Not where y is its own residual: the one could read
+  // what the other has stored.
+  const bool slid = !split && c < p.e.n && c + V > p.e.n && p.e.n >= n0 + wn * FR + V && p.e.residual != p.e.c;
+  if (slid) {
+    cc -= c + V - p.e.n;
+    c = p.e.n - V;
+  }
   const bool whole = c + V <= p.e.n;   // the lane's columns are one vector of every row
   float bias[V] = {};
+  const uint32_t have = c < p.e.n ? p.e.n - c : 0u;
   if (whole && !split) bias_of<T, V>(bias, c, p.e);
+  else if (TM < 256 && !split) bias_some<T, V>(bias, c, have, p.e);
   constexpr int HIGH = 32 / FR;        // fragments that 32 rows take
 #pragma unroll
   for (int j = 0; j < FM; j += HIGH) {
@@ -395,11 +442,16 @@ __device__ __forceinline__ void gemm_tile(const KGemm& p, uint32_t id, lds_char*
     for (uint32_t rr = lane / LANES; rr < 32; rr += ROWS) {
       if (r0 + rr >= p.e.m) break;
       float v[V];
+      if (slid) {
 #pragma unroll
-      for (int i = 0; i < V; i += 4) {
-        const f32x4 q = *reinterpret_cast<const f32x4*>(mine + rr * C + ((cc / 4 + i / 4) ^ (rr % CH)) * 4);
+        for (int i = 0; i < V; ++i) v[i] = mine[rr * C + (((cc + i) / 4) ^ (rr % CH)) * 4 + (cc + i) % 4];
+      } else {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) v[i + u] = q[u];
+        for (int i = 0; i < V; i += 4) {
+          const f32x4 q = *reinterpret_cast<const f32x4*>(mine + rr * C + ((cc / 4 + i / 4) ^ (rr % CH)) * 4);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) v[i + u] = q[u];
+        }
       }
       if (split) {
         float* o = p.part + ((size_t)piece * TM + (wm + j) * FR + rr) * TN + wn * FR + cc;
@@ -407,9 +459,11 @@ __device__ __forceinline__ void gemm_tile(const KGemm& p, uint32_t id, lds_char*
         for (int i = 0; i < V; i += 4) Vec<float>::store(o + i, v + i);
       } else if (whole) {
         finish<T, V>(v, bias, r0 + rr, c, p.e);
-      } else {   // the last columns
+      } else if constexpr (TM < 256) {   // the last columns
+        if (have) finish_some<T, V>(v, bias, r0 + rr, c, have, p.e);
+      } else {   // (one by one: the registers are full)
 #pragma unroll 1
-        for (uint32_t i = 0; i < V && c + i < p.e.n; ++i) {
+        for (uint32_t i = 0; i < have; ++i) {
           float z = mine[rr * C + ((cc / 4 + i / 4) ^ (rr % CH)) * 4 + i % 4], b1;
           bias_of<T, 1>(&b1, c + i, p.e);
           finish<T, 1>(&z, &b1, r0 + rr, c + i, p.e);
@@ -534,13 +588,9 @@ __global__ __launch_bounds__(256) void k_join(KJoins js) {
     bias_of<T, V>(bias, c, p.e);
     finish<T, V>(v, bias, r, c, p.e);
   } else {
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      if (c + j >= p.e.n) continue;
-      float bias;
-      bias_of<T, 1>(&bias, c + j, p.e);
-      finish<T, 1>(v + j, &bias, r, c + j, p.e);
-    }
+    float bias[V];
+    bias_some<T, V>(bias, c, p.e.n - c, p.e);
+    finish_some<T, V>(v, bias, r, c, p.e.n - c, p.e);
   }
 }
 
@@ -716,10 +766,10 @@ constexpr TileCost COST_F32[] = {{64, 4, 0.45, 0.95, 4}, {128, 2, 1.75, 2.0, 6}}
 constexpr int64_t SPLITS[] = {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 14, 16, 20, 24, 28, 32, 40, 48, 56, 64};
 
 // The tile, and the tiles whose summed axis is split, that are estimated
-// cheapest: none, all, or those behind the last full round of the compute
+// cheapest (returned, in microseconds): none, all, or those behind the last full round of the compute
 // units (1001 x 515 x 4099 f32 in 64-tiles is 1040 of them on 256 units of
 // four: whole, the last 16 cost as much again as a quarter of the others).
-void choose_tile(const GemmArgs& g, Plan2* p) {
+double choose_tile(const GemmArgs& g, Plan2* p) {
   const bool half = g.dtype == DT_BF16;
   const int64_t steps = std::max<int64_t>(p->all_steps, 1);
   double best = 1e300;
@@ -762,6 +812,7 @@ void choose_tile(const GemmArgs& g, Plan2* p) {
       }
     }
   }
+  return best;
 }
 
 Plan2 plan_gemm(const GemmArgs& g) {
@@ -772,16 +823,9 @@ Plan2 plan_gemm(const GemmArgs& g) {
   // 16384 x 4096 30 to 28, 512 x 12288 23 to 15; f32 4096 x 4096 19 to 29.
   // Beyond 16 rows x is read twice as often as by the tiles: 32 rows of bf16,
   // 4096 x 4096 14 us to 16, 16384 x 4096 46 to 28.
-  // More rows of a small product whose operands would have to be copied first
-  // go the same way, 32 at a time: the copy's launch costs more than the rows
-  // that are read again, out of the caches (x of m rows, n x k; bf16 206 x 1810
-  // x 157 9.9 us to 13.8, 1000 x 1000 x 131 13.0 to 13.9, 500 x 2000 x 259 17.5 to
-  // 14.1, 837 x 4439 x 31 22.7 to 14.0; f32 300 x 1000 x 515 11.9 to 19.4).
-  const int64_t line = g.k * es, blocks = ceil_div(g.m, 32) * ceil_div(g.n, 16);
-  const bool pack = needs_pack(g.a, g.m, g.k, es) || needs_pack(g.b, g.n, g.k, es);
+  const int64_t line = g.k * es;
   if (!g.a.trans && !g.b.trans && ((g.m <= 16 && line <= 16384) ||
-                                   (g.m <= 32 && line <= 8192 && g.n * g.k <= (int64_t(1) << 24)) ||
-                                   (pack && line <= 8192 && blocks <= 2048 && blocks * 48 * g.k <= (int64_t(1) << 24)))) {
+                                   (g.m <= 32 && line <= 8192 && g.n * g.k <= (int64_t(1) << 24)))) {
     p.few = true;
     return p;
   }
@@ -800,7 +844,22 @@ Plan2 plan_gemm(const GemmArgs& g) {
   p.off_part = ba + bb;
   p.total = p.off_part;
   p.all_steps = (uint32_t)ceil_div(g.k, bk);
-  choose_tile(g, &p);
+  const double us = choose_tile(g, &p);
+  // More rows of a small product whose operands would have to be copied first
+  // go the same way, 32 at a time, where the rows read again, out of the
+  // caches, cost less than the copies and their launch (x of m rows, n x k; bf16
+  // 206 x 1810 x 157 9.9 us to 13.8, 1000 x 1000 x 131 13.0 to 13.9, 500 x 2000 x 259
+  // 17.5 to 14.1, 837 x 4439 x 31 22.7 to 14.0; f32 300 x 1000 x 515 11.9 to 19.4,
+  // 100 x 5000 x 515 19.8 to 25.9, 500 x 2000 x 259 18.0 to 15.1).
+  if ((ba || bb) && !g.a.trans && !g.b.trans && line <= 8192) {
+    const double blocks = (double)ceil_div(g.m, 32) * (double)ceil_div(g.n, 16);
+    const double few = blocks * (1.5e-3 + (double)(48 * g.k) / (es == 2 ? 2.5e6 : 2.0e6));
+    if (few + 4 < us + 6 + (double)(ba + bb) / 1.5e6) {
+      p = Plan2();
+      p.few = true;
+      return p;
+    }
+  }
   p.total += (size_t)p.split * p.rest * p.tile * p.tile * 4;
   return p;
 }
@@ -846,9 +905,13 @@ struct Product {
     k.red = (uint32_t)((pack || o.padded) && !o.trans ? ceil_div(g.k, V) * V : g.k);
     return k;
   }
+  // Rows that begin inside a line are stored in pieces that the caches have to
+  // put together (2000 x 65537 bf16 169 us past them, 91 through them; where a
+  // residual comes through the caches too, 180 and 201).
+  static bool aligned(const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * ES % 16 == 0; }
   Epi epilogue() const {
     return Epi{g.bias, g.residual, g.c, g.pre, g.ldr, g.ldc, g.ldp, (uint32_t)g.m, (uint32_t)g.n, g.act,
-               g.m * g.n * ES >= STREAM_BYTES};
+               g.m * g.n * ES >= STREAM_BYTES && (g.residual || aligned(g.c, g.ldc))};
   }
   KGemm args() const {
     KGemm k{};
