@@ -1,0 +1,82 @@
+"""GPU: operators at the edges of their operands: what lies beside and behind a
+matrix stays out of the results, and outputs at odd argument combinations."""
+import ctypes
+import math
+
+import pytest
+
+import ops_util as U
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def tss():
+    import top_selection_sample_amd
+    return top_selection_sample_amd
+
+
+def rnd(seed, *shape, dt="f32", scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g) * scale).to(DT[dt]).cuda()
+
+
+def among_nan(t, left, right):
+    """The same matrix as columns of a wider one, NaN on both sides and behind the last row."""
+    rows, cols = t.shape
+    big = torch.full((rows + 1, left + cols + right), math.nan, dtype=t.dtype, device="cuda")
+    big[:rows, left:left + cols] = t
+    return big[:rows, left:left + cols]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "silu"])
+@pytest.mark.parametrize("left,right", [(0, 8), (0, 1), (3, 10)])
+@pytest.mark.parametrize("m,n,k", [(1, 13, 48), (3, 35, 48), (8, 13, 48), (17, 13, 64), (20, 35, 40), (32, 7, 200),
+                                   (200, 13, 48), (200, 35, 72), (300, 259, 130)])
+def test_gradients_of_a_weight_stored_by_columns(m, n, k, left, right, act, dt):
+    # tied weights: linear(x, v.t()); few rows and small products read such a weight where it lies
+    x, w, dy, pre = (rnd(1, m, k, dt=dt), rnd(2, n, k, dt=dt, scale=0.2), rnd(3, m, n, dt=dt), rnd(4, m, n, dt=dt))
+    refs, errs = U.linear_grad64(dy, x, w, pre, act)
+    tied = among_nan(w.t().contiguous(), left, right).t()
+    got = tss().linear_grad(among_nan(dy, left, right), x, tied, activation=act,
+                            pre=None if act == "none" else among_nan(pre, right, left))
+    for g, ref, err, what in zip(got, refs, errs, ("dx", "dw", "db")):
+        U.within(g, ref, err, f"{what} {m}x{n}x{k} {act} {dt}")
+    got = tss().linear_grad(dy, among_nan(x.t().contiguous(), left, right).t(), among_nan(w, left, right),
+                            activation=act, pre=None if act == "none" else pre)
+    for g, ref, err, what in zip(got, refs, errs, ("dx", "dw", "db")):
+        U.within(g, ref, err, f"{what} {m}x{n}x{k} {act} {dt}, x by columns")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("m,n,k", [(1, 13, 33), (20, 7, 35), (200, 35, 13), (300, 259, 131)])
+def test_product_of_operands_among_nan(m, n, k, dt):
+    x, w, b, r = rnd(5, m, k, dt=dt), rnd(6, n, k, dt=dt), rnd(7, n, dt=dt), rnd(8, m, n, dt=dt)
+    ref, err, _ = U.linear64(x, w, b, "relu", r)
+    for by_rows in (True, False):
+        for left, right in ((0, 8), (1, 3)):
+            put = (lambda t: among_nan(t, left, right)) if by_rows else (
+                lambda t: among_nan(t.t().contiguous(), left, right).t())
+            U.within(tss().linear(put(x), put(w), among_nan(b[None], left, right)[0], "relu", among_nan(r, left, right)),
+                     ref, err, f"{m}x{n}x{k} {dt}")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_autograd_of_tied_weights(dt):
+    # the reconstruction h @ v of a tied autoencoder, v's rows of odd length: v.t() is the weight
+    m, n, k = 8, 13, 48
+    h, v, c = rnd(9, m, k, dt=dt), rnd(10, k, n, dt=dt, scale=0.2), rnd(11, m, n, dt=dt)
+    refs, errs = U.linear_grad64(c, h, v.t(), None, "none")
+    h.requires_grad_(True)
+    v.requires_grad_(True)
+    tss().linear(h, v.t()).backward(c)
+    U.within(h.grad, refs[0], errs[0], "h")
+    U.within(v.grad, refs[1].t(), errs[1].t(), "v")

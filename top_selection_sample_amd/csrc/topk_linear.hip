@@ -901,8 +901,10 @@ struct Product {
     k.p = pack ? at : o.p;
     k.ld = pack ? ldp : (lines > 1 ? o.ld : line);
     k.rows = (uint32_t)rows;
-    // a line that ends in zeros counts as whole chunks
-    k.red = (uint32_t)((pack || o.padded) && !o.trans ? ceil_div(g.k, V) * V : g.k);
+    // for the tiles a line that ends in zeros counts as whole chunks; the few
+    // rows' kernel masks the last chunk itself, of both operands alike, and the
+    // other one's lines may go on with anything
+    k.red = (uint32_t)((pack || o.padded) && !o.trans && !p.few ? ceil_div(g.k, V) * V : g.k);
     return k;
   }
   // Rows that begin inside a line are stored in pieces that the caches have to
