@@ -80,3 +80,33 @@ def test_autograd_of_tied_weights(dt):
     tss().linear(h, v.t()).backward(c)
     U.within(h.grad, refs[0], errs[0], "h")
     U.within(v.grad, refs[1].t(), errs[1].t(), "v")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("flat", [True, False])
+@pytest.mark.parametrize("rows,k,n,d", [(5, 30, 40, 512), (40, 300, 9000, 24), (3, 4, 20_000, 1100), (7, 3, 5, 3)])
+def test_bias_gradient_of_the_encoder_alone_reads_no_rows(rows, k, n, d, flat, dt):
+    # x is not read without dweight, and weight not without dx: both null
+    lib = tss()._lib
+    g = torch.Generator().manual_seed(12)
+    idx = torch.randint(0, rows * n, (rows * k,), generator=g) if flat else torch.randint(0, n, (rows, k), generator=g)
+    idx[..., -1] = -1
+    v, gv = rnd(13, *idx.shape, dt=dt), rnd(14, *idx.shape, dt=dt)
+    idx = idx.cuda()
+    db = torch.full((n,), 7.0, dtype=DT[dt], device="cuda")
+    sel = ctypes.byref(lib.Selection(v.data_ptr(), idx.data_ptr(), rows, idx.numel() if flat else k, n, flat,
+                                     tss().dtype_code(DT[dt])))
+    size = ctypes.c_size_t()
+    assert lib.lib.topk_decode_workspace_size(sel, d, ctypes.byref(size)) == 0
+    ws = torch.empty(size.value, dtype=torch.uint8, device="cuda")
+    assert lib.lib.topk_encode_grad(sel, gv.data_ptr(), None, 0, None, 0, d, None, 0, None, 0, db.data_ptr(),
+                                    ws.data_ptr(), size.value, torch.cuda.current_stream().cuda_stream) == 0
+    e, _, j = U.entries(idx, rows, n)
+    c = torch.where(v.reshape(-1).cpu()[e] > 0, gv.reshape(-1).cpu()[e].double(), 0.0)
+    ref, err = U.group64(c, j, torch.zeros_like(j), n, torch.ones(1, 1))
+    U.within(db.cpu(), ref[:, 0], err[:, 0])
+    # beside dx, and against the call that computes all three
+    x, w = rnd(15, rows, d, dt=dt), rnd(16, n, d, dt=dt)
+    dx, _, alone = tss().encode_grad(gv, v, idx, x, w, need=(1, 0, 1))
+    want = tss().encode_grad(gv, v, idx, x, w)
+    assert torch.equal(alone, want[2]) and torch.equal(db, want[2]) and torch.equal(dx, want[0])

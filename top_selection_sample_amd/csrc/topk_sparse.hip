@@ -1039,7 +1039,7 @@ hipError_t run_seg(const SegCall& a, char* ws, hipStream_t s) {
     k.ldo = p.ldo;
     k.keys = (uint32_t)keys;
     k.total = (uint32_t)a.sel.total;
-    k.d = (uint32_t)a.d;
+    k.d = p.out || p.dots ? (uint32_t)a.d : 0u;   // without an output src is not read, and may be null
     k.stream = keys * a.d * (int64_t)sizeof(T) >= STREAM_BYTES;
     if (p.dots) {
       // fused where a lane holds its whole share of both rows
@@ -1108,7 +1108,7 @@ hipError_t run_seg(const SegCall& a, char* ws, hipStream_t s) {
     const hipError_t e = run_sorts<T>(a, sorted, plans, at, n, s);
     if (e != hipSuccess) return e;
   }
-  return launch_sums<T>(ks, n, wide, plans[0].chunks, a.d, dots, s);
+  return launch_sums<T>(ks, n, wide, plans[0].chunks, std::max(ks.s[0].d, ks.s[1].d), dots, s);
 }
 
 template <class T>
