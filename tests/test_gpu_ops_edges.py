@@ -110,3 +110,24 @@ def test_bias_gradient_of_the_encoder_alone_reads_no_rows(rows, k, n, d, flat, d
     dx, _, alone = tss().encode_grad(gv, v, idx, x, w, need=(1, 0, 1))
     want = tss().encode_grad(gv, v, idx, x, w)
     assert torch.equal(alone, want[2]) and torch.equal(db, want[2]) and torch.equal(dx, want[0])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("total", [5, 6000])
+@pytest.mark.parametrize("d", [3, 64, 1030])
+def test_values_have_no_gradient_where_there_are_no_latents(d, total, dt):
+    # no latent: every entry is out of range, and gets 0, also when an (empty) dweight is wanted beside it
+    lib = tss()._lib
+    v, g = rnd(17, total, dt=dt), rnd(18, 4, d, dt=dt)
+    idx = torch.arange(total, device="cuda")
+    dv, db = torch.full((total,), 7.0, dtype=DT[dt], device="cuda"), torch.full((d,), 7.0, dtype=DT[dt], device="cuda")
+    somewhere = torch.zeros(64, dtype=DT[dt], device="cuda")     # stands for the empty matrices; nothing is written there
+    sel = ctypes.byref(lib.Selection(v.data_ptr(), idx.data_ptr(), 4, total, 0, 1, tss().dtype_code(DT[dt])))
+    size = ctypes.c_size_t()
+    assert lib.lib.topk_decode_workspace_size(sel, d, ctypes.byref(size)) == 0
+    ws = torch.empty(size.value + 1, dtype=torch.uint8, device="cuda")
+    assert lib.lib.topk_decode_grad(sel, somewhere.data_ptr(), d, d, g.data_ptr(), d, dv.data_ptr(), somewhere.data_ptr(),
+                                    d, db.data_ptr(), ws.data_ptr(), size.value,
+                                    torch.cuda.current_stream().cuda_stream) == 0
+    assert not dv.any() and not somewhere.any()
+    U.within(db, g.double().sum(0), 7 * U.U32 * g.double().abs().sum(0))

@@ -1042,8 +1042,9 @@ hipError_t run_seg(const SegCall& a, char* ws, hipStream_t s) {
     k.d = p.out || p.dots ? (uint32_t)a.d : 0u;   // without an output src is not read, and may be null
     k.stream = keys * a.d * (int64_t)sizeof(T) >= STREAM_BYTES;
     if (p.dots) {
-      // fused where a lane holds its whole share of both rows
-      if (wide && a.d <= 128 * V && a.sel.total) {
+      // fused where a lane holds its whole share of both rows (and there is a
+      // sum to fuse with: without latents every entry gets its 0 from k_dots)
+      if (wide && a.d <= 128 * V && a.sel.total && keys) {
         dots = true;
         k.wsrc = p.other;
         k.ldw = p.ldother;
