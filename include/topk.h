@@ -340,7 +340,10 @@ int topk_stream_read(const void* data, size_t bytes, uint32_t* sink, void* strea
 
 /* gelu is z * Phi(z) with the normal distribution function; silu is
  * z / (1 + exp(-z)).  At -inf both are 0, with slope 0.  relu keeps NaN; its
- * slope is 0 at 0. */
+ * slope is 0 at 0.  Before the last rounding gelu's Phi is off by at most 2e-4
+ * of its value where the result is bf16 (a tenth of half a step), and by
+ * (1.3 z^2 + 18) 2^-24 of it in float32; silu left of -87, where it is below
+ * 2e-36, may be 0. */
 typedef enum {
   TOPK_ACT_NONE = 0,
   TOPK_ACT_RELU = 1,

@@ -131,3 +131,31 @@ def test_values_have_no_gradient_where_there_are_no_latents(d, total, dt):
                                     torch.cuda.current_stream().cuda_stream) == 0
     assert not dv.any() and not somewhere.any()
     U.within(db, g.double().sum(0), 7 * U.U32 * g.double().abs().sum(0))
+
+
+def gelu_tail_errors(z, dt):
+    """Relative errors of the normal distribution function and of z times its density, left of 0.
+
+    bf16: the function is fitted to 1.8e-4 of its value, the rest of its evaluation (a reciprocal, a polynomial of six
+    steps, an exponential) adds less than 1e-5; f32: erfc's argument is off by 1.3 roundings, which erfc takes
+    z^2 + 1 times, and erfc itself by at most 16.  The density: an exponent of z^2 / 2 off by at most 5 roundings
+    (bf16) or 2 (f32), the exponential and three products."""
+    z2 = z * z
+    if dt == "bf16":
+        return 2e-4, (2.5 * z2 + 16) * U.U32
+    return (1.3 * (z2 + 1) + 16) * U.U32, (z2 + 16) * U.U32
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("few", [True, False])
+def test_gelu_and_its_slope_far_left_of_zero(few, dt):
+    # relative to the value: an absolute bound near 1 says nothing of values of 1e-6 and 1e-30
+    z = torch.linspace(-12.5, -3, 4001, device="cuda").to(DT[dt])[:, None].contiguous()
+    one = torch.ones(1, 1, dtype=DT[dt], device="cuda")
+    z64 = z.double()
+    tail, bell = 0.5 * torch.special.erfc(-z64 / math.sqrt(2)), torch.exp(-z64 * z64 / 2) / math.sqrt(2 * math.pi)
+    e_tail, e_bell = gelu_tail_errors(z64, dt)
+    y = torch.cat([tss().linear(p, one, activation="gelu") for p in z.split(16 if few else 4001)])
+    U.within(y, z64 * tail, (z64 * tail).abs() * (e_tail + 2 * U.U32), "gelu")
+    dx = tss().linear_grad(torch.ones_like(z), z, one, activation="gelu", pre=z, need=(1, 0, 0))[0]
+    U.within(dx, tail + z64 * bell, tail * e_tail + (z64 * bell).abs() * e_bell + 2 * U.U32 * (z64 * bell).abs(), "slope")

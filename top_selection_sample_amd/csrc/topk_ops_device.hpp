@@ -123,16 +123,26 @@ __device__ __forceinline__ void stream_vec(T* p, const float* v) {
 // slopes 0 (the formulas would give inf * 0 at -inf); NaN stays NaN.
 //
 // Results that are rounded to bf16 (T = bf16_t) use the hardware's exponential
-// and reciprocal and, for the normal distribution function, the five-term
-// form 7.1.26 of Abramowitz and Stegun (off by at most 1.5e-7, where half a
-// bf16 step of a value near 1 is 2e-3); 32-bit results use the full functions.
+// and reciprocal and, for the normal distribution function, a form of six
+// terms; 32-bit results use the full functions.
 //
-// tail_of: 1 - Phi(|z|) and exp(-z^2 / 2).
+// tail_of: 1 - Phi(|z|) and exp(-z^2 / 2).  With x = |z| / sqrt(2) the first is
+// erfc(x) / 2 = exp(-x^2) P(t) / 2, t = 1 / (1 + 0.42 x), P without a constant
+// term.  P's coefficients are the least-maximum fit (a linear program over 6000
+// points of 0 <= x <= 40) of erfc(x) exp(x^2) to an error that is at most 2e-4
+// of the value and 1e-7 of 1: left of zero gelu is z times this alone, so what
+// counts there is the error relative to it.  Evaluated in 32 bits it is off by
+// at most 1.8e-4 of its value, a tenth of the smallest half step of bf16, and
+// by 2.7e-7 in all (form 7.1.26 of Abramowitz and Stegun, one term shorter, is
+// fitted to 1.5e-7 of 1 only: off by 0.6% of the value at z = -7, 2% at -10).
 __device__ __forceinline__ float tail_of(float z, float* bell) {
   const float x = fabsf(z) * 0.70710678118654752f;
-  const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.f));
-  const float p = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f),
-                           0.254829592f);
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.42f, x, 1.f));
+  float p = fmaf(t, -0.157329574f, 0.454156995f);
+  p = fmaf(t, p, -0.0476845726f);
+  p = fmaf(t, p, 0.286179572f);
+  p = fmaf(t, p, 0.227307111f);
+  p = t * fmaf(t, p, 0.237370476f);
   *bell = __builtin_amdgcn_exp2f(-1.4426950408889634f * x * x);
   return 0.5f * p * *bell;
 }
