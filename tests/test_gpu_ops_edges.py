@@ -159,3 +159,45 @@ def test_gelu_and_its_slope_far_left_of_zero(few, dt):
     U.within(y, z64 * tail, (z64 * tail).abs() * (e_tail + 2 * U.U32), "gelu")
     dx = tss().linear_grad(torch.ones_like(z), z, one, activation="gelu", pre=z, need=(1, 0, 0))[0]
     U.within(dx, tail + z64 * bell, tail * e_tail + (z64 * bell).abs() * e_bell + 2 * U.U32 * (z64 * bell).abs(), "slope")
+
+
+def test_forward_mode_is_refused():
+    # a result without a tangent would be read as one of zero, by these calls and by a backward inside a dual level
+    import torch.autograd.forward_ad as fw
+    T = tss()
+    x, w, b = rnd(20, 5, 8), rnd(21, 6, 8), rnd(22, 6)
+    v, i = T.encode(x, w, b, 7)
+    wd, g, gv = rnd(23, 6, 4), rnd(24, 5, 4), rnd(25, 7)
+    plain = T.linear(x, w, b)
+
+    def calls(d):
+        yield lambda: T.linear(d(x), w, b)
+        yield lambda: T.linear(x, w, d(b))
+        yield lambda: T.linear(x, w, b, residual=d(plain))
+        yield lambda: T.linear_grad(d(plain), x, w)
+        yield lambda: T.linear_grad(plain, x, d(w))
+        yield lambda: T.encode(x, d(w), b, 7)
+        yield lambda: T.encode_grad(d(gv), v, i, x, w)
+        yield lambda: T.encode_grad(gv, v, i, d(x), w)
+        yield lambda: T.decode(d(v), i, wd, rows=5)
+        yield lambda: T.decode(v, i, wd, rows=5, bias=d(wd[0].contiguous()))
+        yield lambda: T.decode_grad(g, v, i, d(wd))
+        yield lambda: T.grad_norm([x, d(w)])
+        yield lambda: T.clip_grad_norm(d(x.clone()), 1e-3)
+
+    keep = x.clone()
+    with fw.dual_level():
+        for call in calls(lambda t: fw.make_dual(t, torch.ones_like(t))):
+            with pytest.raises(RuntimeError, match="forward-mode"):
+                call()
+        for requires in (False, True):
+            with pytest.raises(RuntimeError, match="forward-mode"):
+                T.linear(fw.make_dual(x.clone().requires_grad_(requires), torch.ones_like(x)), w, b)
+        leaf = x.clone().requires_grad_(True)
+        y = T.linear(leaf, w, b, activation="gelu")
+        with pytest.raises(RuntimeError, match="forward-mode"):
+            torch.autograd.grad(y, leaf, fw.make_dual(torch.ones_like(y), torch.ones_like(y)))
+        assert torch.equal(T.linear(x, w, b), plain)       # tensors without a tangent go on as ever
+        for call in calls(lambda t: t):
+            call()
+    assert torch.equal(x, keep)

@@ -160,3 +160,22 @@ def test_python_refusals():
                  lambda: tss.grad_norm([x]), lambda: tss.clip_grad_norm([x], 1.0)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_tensors_with_a_tangent_are_refused():
+    import torch.autograd.forward_ad as fw
+    from top_selection_sample_amd import _ops
+    x, w = torch.zeros(3, 4), torch.zeros(5, 4)
+    assert not _ops._wants_grad(x, None, w)
+    with fw.dual_level():
+        d = fw.make_dual(x, torch.ones(3, 4))
+        assert not _ops._wants_grad(x, None, w)
+        for call in (lambda: _ops._wants_grad(w, d), lambda: _ops._wants_grad(None, w.requires_grad_(True), d),
+                     lambda: _ops._linear_grad_run(d, x, w, 0, None, (True, True, True)),
+                     lambda: _ops._decode_grad_run(x, x, x, d, (True, True, True)),
+                     lambda: _ops._encode_grad_run(d, x, x, x, w, (True, True, True)),
+                     lambda: _ops._norm_run([x, d], None), lambda: _ops._norm_run(d, (1.0, 1e-6))):
+            with pytest.raises(RuntimeError, match="forward-mode"):
+                call()
+        with fw._set_fwd_grad_enabled(False):
+            assert not _ops._wants_grad(d)

@@ -15,6 +15,7 @@ from contextlib import nullcontext
 from operator import attrgetter
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import _lib
@@ -95,11 +96,23 @@ def _act_code(activation: str) -> int:
     return code
 
 
+def _no_tangents(*tensors):
+    """Forward-mode derivatives do not pass through the library: a result without
+    a tangent would be read as one of zero."""
+    if forward_ad._current_level >= 0 and torch._C._is_fwd_grad_enabled():
+        for t in tensors:
+            if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+                raise RuntimeError("forward-mode derivatives are not supported: take the tangent off "
+                                   "(torch.autograd.forward_ad.unpack_dual) or use backward derivatives")
+
+
 def _wants_grad(*tensors) -> bool:
     """Whether autograd records the call.  Not under graph capture: a captured
     backward meets the gradient accumulators of whatever eager graph of the
     same leaves is alive, on streams that are not captured, and that ends the
-    process; the *_grad functions take no part in autograd and can be captured."""
+    process; the *_grad functions take no part in autograd and can be captured.
+    Refuses tensors that carry a tangent."""
+    _no_tangents(*tensors)
     if torch.is_grad_enabled():
         for t in tensors:
             if t is not None and t.requires_grad:
@@ -138,6 +151,7 @@ def _linear_run(x, w, bias, act, residual, want_pre):
 
 
 def _linear_grad_run(dy, x, w, act, pre, need):
+    _no_tangents(dy, x, w, pre)
     m, n = dy.shape
     k = w.shape[1]
     dev = dy.get_device()
@@ -193,8 +207,9 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = No
     transpose of a [k, n] tensor is read in place), ``bias`` [n], ``residual``
     [..., n]; float32 or bfloat16, all alike.  ``activation``: "none", "relu",
     "gelu" (z * Phi(z)) or "silu".  Sums and the epilogue are held in 32 bits.
-    Differentiable (once).  Under HIP graph capture autograd is refused: call
-    ``linear`` with gradients off, and ``linear_grad``."""
+    Differentiable (once, backward; tensors with a forward-mode tangent are
+    refused).  Under HIP graph capture autograd is refused: call ``linear`` with
+    gradients off, and ``linear_grad``."""
     _gpu(x, "x")
     _code(x, "x")
     act = _act_code(activation)
@@ -288,6 +303,7 @@ def _decode_run(values, indices, weight, rows, bias):
 
 
 def _decode_grad_run(grad, values, indices, weight, need):
+    _no_tangents(grad, values, weight)
     n, d = weight.shape
     rows = grad.shape[0]
     dev = grad.get_device()
@@ -383,6 +399,7 @@ def decode_grad(grad: torch.Tensor, values: torch.Tensor, indices: torch.Tensor,
 
 # ---------------------------------------------------------------- encode
 def _encode_grad_run(grad_values, values, indices, x, weight, need):
+    _no_tangents(grad_values, values, x, weight)
     n, d = weight.shape
     rows = x.shape[0]
     dev = x.get_device()
@@ -501,6 +518,7 @@ def _norm_run(tensors, clip):
     except TypeError:   # something that is no tensor: None is skipped
         ts = [t for t in ts if t is not None]
         devices = set(map(_T.get_device, ts))
+    _no_tangents(*ts)
     if not ts:
         return torch.zeros((), device="cuda")
     index = devices.pop()
