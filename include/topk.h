@@ -356,7 +356,7 @@ typedef struct {
   const void* x;        /* [m, k], row stride ldx; with x_trans stored as [k, m] */
   const void* w;        /* [n, k], row stride ldw; with w_trans stored as [k, n] */
   const void* bias;     /* [n], or null */
-  const void* residual; /* [m, n], row stride ldr, or null; may be y itself (ldr == ldy) */
+  const void* residual; /* [m, n], row stride ldr, or null; may be y itself (then ldr == ldy, or TOPK_EINVAL) */
   void* y;              /* [m, n], row stride ldy */
   void* pre;            /* [m, n], row stride ldp: z, for the gradient; or null */
   int64_t m, n, k;

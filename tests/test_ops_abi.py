@@ -179,3 +179,12 @@ def test_tensors_with_a_tangent_are_refused():
                 call()
         with fw._set_fwd_grad_enabled(False):
             assert not _ops._wants_grad(d)
+
+
+def test_a_residual_in_place_has_the_strides_of_the_result():
+    for kw, want in ((dict(residual=A, ldr=17), EINVAL), (dict(residual=A, ldr=16, ldy=20), EINVAL), (dict(residual=A, ldr=16), OK),
+                     (dict(residual=A, ldr=20, ldy=20), OK), (dict(residual=A, ldr=99, m=1), OK), (dict(residual=A, ldr=9, m=0), OK),
+                     (dict(residual=A, ldr=9, n=0), OK), (dict(residual=2 * A, ldr=17), OK)):
+        assert size_of(L.topk_linear_workspace_size, linear_args(**kw))[0] == want, kw
+        if want != OK:
+            assert L.topk_linear(ctypes.byref(linear_args(**kw)), A, 1 << 40, None) == want

@@ -63,6 +63,8 @@ int linear_gemm(const topk_linear_args* a, tk::GemmArgs* g) {
   if (a->bias && bad_matrix(a->bias, n, 1, n, a->dtype)) return TOPK_EINVAL;
   if (a->residual && bad_matrix(a->residual, a->ldr, m, n, a->dtype)) return TOPK_EINVAL;
   if (a->pre && bad_matrix(a->pre, a->ldp, m, n, a->dtype)) return TOPK_EINVAL;
+  // y over its own residual, but with rows elsewhere: one row's result would land on another's residual
+  if (a->residual && a->residual == a->y && a->ldr != a->ldy && m > 1 && n > 0) return TOPK_EINVAL;
   g->a = tk::Operand{a->x, a->ldx, a->x_trans != 0};
   g->b = tk::Operand{a->w, a->ldw, a->w_trans != 0};
   g->m = m;
