@@ -201,3 +201,18 @@ def test_forward_mode_is_refused():
         for call in calls(lambda t: t):
             call()
     assert torch.equal(x, keep)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("act", ["none", "relu"])
+@pytest.mark.parametrize("m,n,k", [(1, 13, 7), (1, 1, 1), (1, 1, 65), (40, 1, 33), (200, 1, 131), (1, 131, 33), (1, 4099, 515),
+                                   (2, 3, 5), (33, 2, 3)])
+def test_gradients_of_one_line_with_nan_behind_it(m, n, k, act, dt):
+    # one row of x or of W: a summed axis of one, whose line ends inside a word
+    x, w, dy, pre = (rnd(1, m, k, dt=dt), rnd(2, n, k, dt=dt, scale=0.2), rnd(3, m, n, dt=dt), rnd(4, m, n, dt=dt))
+    refs, errs = U.linear_grad64(dy, x, w, pre, act)
+    for left in (0, 8):
+        put = lambda t: among_nan(t, left, 24)   # noqa: E731
+        got = tss().linear_grad(put(dy), put(x), put(w), activation=act, pre=None if act == "none" else put(pre))
+        for g, ref, err, what in zip(got, refs, errs, ("dx", "dw", "db")):
+            U.within(g, ref, err, f"{what} {m}x{n}x{k} {act} {dt}")
