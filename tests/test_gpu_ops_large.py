@@ -122,3 +122,12 @@ def test_last_columns_and_a_residual_in_place(m, n, dt):
     ws = torch.empty(size.value + 1, dtype=torch.uint8, device="cuda")
     assert _lib.lib.topk_linear(ctypes.byref(a), ws.data_ptr(), size.value, torch.cuda.current_stream().cuda_stream) == 0
     U.within(y, want[0], want[1], f"in place {m}x{n}")
+
+
+def test_few_columns_of_more_rows_than_a_second_grid_dimension_holds():
+    # 32 rows to a workgroup: more than 65536 of them
+    m = (1 << 21) + 70
+    g = torch.Generator("cuda").manual_seed(11)
+    x = torch.randint(-8, 8, (m, 3), device="cuda", generator=g).bfloat16()
+    w = torch.randint(-8, 8, (2, 3), device="cuda", generator=g).bfloat16()
+    assert torch.equal(linear(x, w), (x.float()[:, None, :] * w.float()[None]).sum(2).bfloat16())

@@ -678,13 +678,17 @@ __device__ __forceinline__ u32x4 row_piece(const T* p, bool in, uint32_t k, uint
   return q;
 }
 
+// Blocks of rows along the grid's second dimension, which takes 65536 at most;
+// the third goes on.  (One dimension and a division: 4.28 us against 4.08.)
+constexpr uint32_t FEW_Y = 32768;
+
 template <class T, int MF, int W>
 __global__ __launch_bounds__(W * 64) void k_few_rows(KGemm p) {
   constexpr uint32_t V = Vec<T>::N, PIECE = 4 * V, TURN = 4;   // summed elements per instruction, pieces per turn
   __shared__ float join[W][MF][16][17];
   const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64;
   const uint32_t i = lane % 16, g = lane / 16;
-  const uint32_t n0 = blockIdx.x * 16, m0 = blockIdx.y * 16 * MF, red = p.a.red;
+  const uint32_t n0 = blockIdx.x * 16, m0 = (blockIdx.z * FEW_Y + blockIdx.y) * 16 * MF, red = p.a.red;
   const bool win = n0 + i < p.b.rows;
   const T* w = static_cast<const T*>(p.b.p) + (int64_t)(win ? n0 + i : 0) * p.b.ld;
   const T* x[MF];
@@ -934,7 +938,8 @@ struct Product {
   hipError_t tiles(hipStream_t s) const {
     const KGemm k = args();
     if (p.few) {
-      const dim3 grid((uint32_t)ceil_div(g.n, 16), (uint32_t)ceil_div(g.m, g.m <= 16 ? 16 : 32));
+      const uint32_t rows = (uint32_t)ceil_div(g.m, g.m <= 16 ? 16 : 32);
+      const dim3 grid((uint32_t)ceil_div(g.n, 16), std::min(rows, FEW_Y), (uint32_t)ceil_div(rows, FEW_Y));
       // 16 waves where each has a turn, unless the workgroups alone fill the card
       // (4096 x 4096 f32 16.8 us against 21.4; 16384 x 4096 56 against 54.7)
       const bool deep = g.k * ES >= 4096 && g.n < 16384;
