@@ -131,3 +131,37 @@ def test_few_columns_of_more_rows_than_a_second_grid_dimension_holds():
     x = torch.randint(-8, 8, (m, 3), device="cuda", generator=g).bfloat16()
     w = torch.randint(-8, 8, (2, 3), device="cuda", generator=g).bfloat16()
     assert torch.equal(linear(x, w), (x.float()[:, None, :] * w.float()[None]).sum(2).bfloat16())
+
+
+def test_tiles_beyond_one_grid_dimension():
+    """2^22 + 2 tiles of 64 rows.  Aligned operands of more than 32 rows take the tiles, whatever
+    the estimates for unaligned ones say; of one step and one column the smallest are cheapest."""
+    m, k = (1 << 28) + 70, 8
+    g = torch.Generator("cuda").manual_seed(12)
+    x = torch.randint(-8, 8, (m, k), device="cuda", generator=g, dtype=torch.bfloat16)
+    w = torch.randint(-8, 8, (1, k), device="cuda", generator=g, dtype=torch.bfloat16)
+    assert x.data_ptr() % 16 == 0 and w.data_ptr() % 16 == 0
+    y = linear(x, w)
+    for at in range(0, m, 1 << 25):   # sums of small whole numbers are exact, and rounded once
+        part = x[at:at + (1 << 25)]
+        assert torch.equal(y[at:at + (1 << 25)], (part.float() * w.float()).sum(1, keepdim=True).bfloat16())
+
+
+def test_copies_beyond_one_grid_dimension():
+    """More than 2^30 16-byte pieces to copy, 256 to a workgroup, for rows of odd length that are
+    too long for the kernel that reads them as they lie."""
+    import ctypes
+    from top_selection_sample_amd import _lib, dtype_code
+    k, padded = 4097, 4104
+    m = (1 << 30) // (padded // 8) + 38
+    g = torch.Generator("cuda").manual_seed(13)
+    x = torch.randint(-2, 3, (m, k), device="cuda", generator=g, dtype=torch.bfloat16)
+    w = torch.randint(-2, 3, (1, k), device="cuda", generator=g, dtype=torch.bfloat16)
+    a = _lib.LinearArgs(x.data_ptr(), w.data_ptr(), None, None, w.data_ptr(), None, m, 1, k, k, k, 0, 1, 0,
+                        dtype_code(torch.bfloat16), 0, 0, 0)
+    size = ctypes.c_size_t()
+    assert _lib.lib.topk_linear_workspace_size(ctypes.byref(a), ctypes.byref(size)) == 0
+    assert m * (padded // 8) > (1 << 30) and size.value >= m * padded * 2     # the copy is made
+    y = linear(x, w)
+    for at in range(0, m, 1 << 16):   # whole numbers below 2^24: exact in any order, and rounded once
+        assert torch.equal(y[at:at + (1 << 16)], (x[at:at + (1 << 16)].float() @ w.float().t()).bfloat16())
