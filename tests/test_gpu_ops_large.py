@@ -165,3 +165,31 @@ def test_copies_beyond_one_grid_dimension():
     y = linear(x, w)
     for at in range(0, m, 1 << 16):   # whole numbers below 2^24: exact in any order, and rounded once
         assert torch.equal(y[at:at + (1 << 16)], (x[at:at + (1 << 16)].float() @ w.float().t()).bfloat16())
+
+
+def test_more_rows_by_columns_than_a_product_reads_in_place():
+    # x stored by columns, 2^22 rows and more: read through a copy
+    m, n, k = (1 << 22) + 5, 3, 8
+    g = torch.Generator("cuda").manual_seed(14)
+    x = torch.randint(-8, 8, (k, m), device="cuda", generator=g, dtype=torch.bfloat16).t()
+    w = torch.randint(-8, 8, (n, k), device="cuda", generator=g, dtype=torch.bfloat16)
+    assert torch.equal(linear(x, w), (x.float() @ w.float().t()).bfloat16())   # exact, and rounded once
+    dy = torch.randint(-1, 2, (m, n), device="cuda", generator=g, dtype=torch.bfloat16)
+    dx, dw, db = linear_grad(dy, x, w)
+    assert torch.equal(dx, (dy.float() @ w.float()).bfloat16())
+    # whole numbers below 2^24 on the way (random signs): exact in any order
+    assert torch.equal(dw, (dy.double().t().contiguous() @ x.double()).bfloat16())
+    assert torch.equal(db, dy.double().sum(0).bfloat16())
+
+
+def test_rows_further_apart_than_2_31_elements():
+    # two rows of a matrix too wide to be named by its stride: read through a copy
+    ld, k, n = (1 << 31) + 24, 40, 5
+    g = torch.Generator("cuda").manual_seed(15)
+    x = torch.empty(2 * ld, dtype=torch.bfloat16, device="cuda").as_strided((2, k), (ld, 1))
+    x.copy_(torch.randint(-8, 8, (2, k), device="cuda", generator=g))
+    w = torch.randint(-8, 8, (n, k), device="cuda", generator=g, dtype=torch.bfloat16)
+    want = (x.float() @ w.float().t()).bfloat16()
+    assert torch.equal(linear(x, w), want) and torch.equal(linear(w, x), want.t())
+    values, indices = torch.ones(1, 2, dtype=torch.bfloat16, device="cuda"), torch.tensor([[1, 0]], device="cuda")
+    assert torch.equal(decode(values, indices, x), x.float().sum(0, keepdim=True).bfloat16())

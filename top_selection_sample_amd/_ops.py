@@ -69,17 +69,22 @@ def _ptr(t):
     return t.data_ptr() if t is not None else 0
 
 
+_WIDTH_MAX = 1 << 22    # lines that a product reads in place are shorter
+_STRIDE_MAX = 1 << 31
+
+
 def _matrix(t: torch.Tensor, either: bool = False):
     """(tensor, row stride, stored transposed) of a 2-D tensor: rows with unit
     stride as they are; columns with unit stride too where the call takes
-    ``either`` order; any other layout (expanded, stepped) as a copy."""
+    ``either`` order; any other layout (expanded, stepped, lines that are too
+    long or too far apart for the library) as a copy."""
     r, c = t.shape
     if t.is_contiguous():
         return t, c or 1, 0
     sr, sc = t.stride()
-    if (sc == 1 or c <= 1) and (sr >= c or r <= 1):
+    if (sc == 1 or c <= 1) and (c <= sr < _STRIDE_MAX or r <= 1):
         return t, max(sr if r > 1 else c, c, 1), 0
-    if either and (sr == 1 or r <= 1) and (sc >= r or c <= 1):
+    if either and (sr == 1 or r <= 1) and (r <= sc < _STRIDE_MAX or c <= 1) and r < _WIDTH_MAX:
         return t, max(sc if c > 1 else r, r, 1), 1
     return t.contiguous(), max(c, 1), 0
 
