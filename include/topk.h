@@ -322,7 +322,8 @@ int topk_stream_read(const void* data, size_t bytes, uint32_t* sink, void* strea
  *     output is written.
  *   - Matrices are row-major with a row stride ("ld", in elements, at least
  *     the row length) and element alignment.  A product reads operands whose
- *     rows are not all 16-byte aligned through a copy in its workspace.
+ *     rows are not all 16-byte aligned through a copy in its workspace, except
+ *     for small ones, which read them as they lie.
  *   - Sizes may be 0: an empty sum is 0.  No size or stride reaches 2^31; n and
  *     k of a product (and m, where x_trans is set) and the row width d of a
  *     decode stay below 2^22, the rows and latents of a

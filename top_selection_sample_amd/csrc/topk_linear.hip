@@ -293,11 +293,11 @@ __device__ __forceinline__ uint32_t die_order(uint32_t id, uint32_t total) {
 
 // A range of tiles walks the product in bands of 1024 rows: W's tile and the
 // band's rows of x then stay in the die's L2 (4096 x 512 x 65536 bf16 in
-// 256-tiles: 360 us in bands of 4 tiles, 380 to 451 in bands of 1, 8, 16 or
-// 32).  Each band begins 37 tiles further right: dies that work on different
+// 256-tiles, in the form that they had when this was chosen: 360 us in bands of
+// 4 tiles, 380 to 451 in bands of 1, 8, 16 or 32).  Each band begins 37 tiles further right: dies that work on different
 // bands would else store the same columns at the same time, and where the row
 // stride is a power of two those lie in the same memory channels (338 us with
-// the shift; 322 for rows of 65600).
+// the shift, 322 for rows of 65600, both then; the present form 313 and 322).
 __device__ __forceinline__ void place_of(uint32_t id, uint32_t tm, uint32_t tn, uint32_t tile, uint32_t* im,
                                          uint32_t* in) {
   const uint32_t band_rows = 1024 / tile;
@@ -474,11 +474,12 @@ __device__ __forceinline__ void gemm_tile(const KGemm& p, uint32_t id, lds_char*
 }
 
 // Measured beside the vendor library's plain product of the same operands
-// (normal random numbers; the rates follow the clock, which follows the data):
-// bf16 8192^3 890 us against 798, 4096^3 109 against 97; 4096 x 512 x 65536,
-// which the store of 537 MB bounds as much as the products, 365 against 320
-// (with bias and relu over an autoencoder's numbers 310 against 342); f32
-// 4096^3 1090 against 1007.
+// (normal random numbers, both on one card; the rates follow the clock, which
+// follows the data and differs by a tenth from card to card): bf16 8192^3 796 us
+// against 708, 4096^3 101 against 97; 4096 x 512 x 65536, which the store of 537
+// MB bounds as much as the products, 313 against 308 (with bias and relu and an
+// autoencoder's weights 324; 320 to 334 on two other cards, the library's plain
+// product 342 on one of them); f32 4096^3 1026 against 922.
 template <class T, int TM, int TN, int NWM, int NWN, bool TA, bool TB>
 __global__ __launch_bounds__(NWM * NWN * 64, 2) void k_gemm(KGemm p) {
 #ifdef __HIP_DEVICE_COMPILE__   // buffer resources exist in the device pass only
@@ -756,9 +757,10 @@ bool needs_pack(const Operand& o, int64_t rows, int64_t red, int64_t es) {
 
 // Microseconds of one step of a tile on a compute unit that shares its time
 // among the tiles it holds, and with one alone; of a tile's start and end;
-// and the tiles a compute unit holds at once.  Measured: bf16 8192^3 in 64-,
-// 128- and 256-tiles 1768, 991 and 811 us, 4096 x 512 x 65536 626, 375 and
-// 358; f32 4096^3 in 64- and 128-tiles 1027 and 996 us.
+// and the tiles a compute unit holds at once.  Measured, each tile forced, in the
+// form that the tiles had then: bf16 8192^3 in 64-, 128- and 256-tiles 1768, 991
+// and 811 us, 4096 x 512 x 65536 626, 375 and 358; f32 4096^3 in 64- and
+// 128-tiles 1027 and 996 us.
 struct TileCost {
   uint32_t tile, holds;
   double shared, alone, ends;
