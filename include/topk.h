@@ -465,6 +465,166 @@ int topk_clip_grad_norm(void* const* ptrs, const int64_t* counts, const int32_t*
                         int64_t tensors, float max_norm, float eps, float* norm, void* workspace,
                         size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Operators on a language model's selections: the experts of its tokens, the
+ * entries of its attention cache, its next token.  The conventions of the
+ * operators above hold, and:
+ *   - rows that are only moved (dispatch, evict) keep their bits;
+ *   - strides of caches are in elements, from 0 to 2^42, the innermost axis
+ *     contiguous; lengths (int64, one a sequence) are read on the device and
+ *     taken as at least 0 and at most the room n.  What lies behind a
+ *     sequence's end is never looked at.
+ * ------------------------------------------------------------------------ */
+
+/* Tokens sorted by expert.  experts [tokens, k] are indices as topk returns
+ * them for the rows of a router's scores; entry e = token * k + choice.  The
+ * entries are sorted by expert, equal experts by e, and those with an index
+ * outside [0, n_experts) (padded slots, copies dropped at a capacity) come
+ * last:
+ *   rows[p]    = x[token] of the entry at place p; zeros for the last ones
+ *                ([tokens * k, d], row stride ldr)
+ *   places[e]  = p, or -1 for the last ones ([tokens, k])
+ *   offsets[i] = the first place of expert i; offsets[n_experts] = the end of
+ *                the last expert ([n_experts + 1])
+ * topk_combine without weights of rows' gradient is the gradient of x. */
+typedef struct {
+  const void* x;             /* [tokens, d], row stride ldx */
+  const int64_t* experts;
+  void* rows;
+  int64_t* places;
+  int64_t* offsets;
+  int64_t tokens, k, n_experts, d, ldx, ldr;   /* tokens * k < 2^31, n_experts <= 8192, d < 2^22 */
+  int32_t dtype, reserved;
+} topk_dispatch_args;
+
+int topk_dispatch_workspace_size(int64_t tokens, int64_t k, int64_t n_experts, size_t* bytes);
+/* Errors (of all calls of this section): TOPK_EDTYPE, TOPK_EINVAL (sizes,
+ * strides, null or misaligned pointers), TOPK_EWORKSPACE, TOPK_EHIP. */
+int topk_dispatch(const topk_dispatch_args* args, void* workspace, size_t workspace_bytes, void* stream);
+
+/* out[t] = sum over j of weights[t, j] * y[places[t, j]], j rising.  A place
+ * outside [0, n) adds nothing; one that occurs twice counts twice.  No
+ * workspace. */
+typedef struct {
+  const void* y;             /* [n, d], row stride ldy */
+  const int64_t* places;     /* [tokens, k] */
+  const void* weights;       /* [tokens, k], of wdtype; null: all 1 */
+  void* out;                 /* [tokens, d], row stride ldo */
+  int64_t tokens, k, n, d, ldy, ldo;
+  int32_t dtype, wdtype;     /* wdtype: dtype, or float32 */
+} topk_combine_args;
+
+int topk_combine(const topk_combine_args* args, void* stream);
+
+/* Gradients of topk_combine from grad = dL/dout:
+ *   dy[p] = sum over the entries e at place p of weights[e] * grad[token e]
+ *           (every row written: 0 where there is none)
+ *   dweights[e] = <grad[token e], y[places[e]]>; 0 where the place is out of range
+ * Each output may be null: not wanted; y is not read without dweights. */
+typedef struct {
+  const void* grad;          /* [tokens, d], row stride ldg */
+  const void* y;
+  const int64_t* places;
+  const void* weights;
+  void* dy;                  /* [n, d], row stride lddy */
+  void* dweights;            /* [tokens, k], of wdtype */
+  int64_t tokens, k, n, d, ldg, ldy, lddy;
+  int32_t dtype, wdtype;
+} topk_combine_grad_args;
+
+int topk_combine_grad_workspace_size(const topk_combine_grad_args* args, size_t* bytes);
+int topk_combine_grad(const topk_combine_grad_args* args, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Attention of one new token for each sequence over its cache.  Query head i
+ * reads key-value head i / (heads / kv_heads).  With p = softmax over the
+ * sequence's entries j of scale * <q, k_j>:
+ *   out = sum of p_j v_j;  scores[j] += sum of p_j over the heads that share
+ *   the key-value head.
+ * A sequence of length 0 has an output of 0 and adds nothing.  In bf16 the
+ * probabilities are rounded to bf16 for the product with v (its matrix
+ * operand); the sums of p and the scores take them unrounded. */
+typedef struct {
+  const void* q;             /* [batch, heads, d], strides sqb, sqh */
+  const void* k;             /* [batch, kv_heads, n, d], strides skb, skh, skn */
+  const void* v;             /* likewise, svb, svh, svn */
+  const int64_t* lengths;    /* [batch], or null: all n */
+  float* scores;             /* [batch, kv_heads, n], strides ssb, ssh, no two rows overlapping; null: not wanted */
+  void* out;                 /* [batch, heads, d], strides sob, soh */
+  int64_t batch, heads, kv_heads, n, d;   /* heads a multiple of kv_heads, up to 4096 times; d <= 256 */
+  int64_t sqb, sqh, skb, skh, skn, svb, svh, svn, ssb, ssh, sob, soh;
+  float scale;
+  int32_t dtype;
+} topk_attend_args;
+
+int topk_attend_workspace_size(const topk_attend_args* args, size_t* bytes);
+int topk_attend(const topk_attend_args* args, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Eviction from a cache by accumulated attention weight.  Of each sequence and
+ * head of more than `budget` entries, `budget` stay: the `recent` newest ones
+ * (the last), and of the others those with the largest scores, equal ones by
+ * lower index (0 and -0 are equal, NaN is above all).  The entries that stay
+ * keep their order; a sequence of at most `budget` entries keeps all.
+ *   k_out, v_out, scores_out: what stays, from row 0 on
+ *   kept: the old index of each, -1 behind the last ([batch, heads, budget])
+ *   lengths_out[b] = min(lengths[b], budget)
+ * Rows of the outputs behind a sequence's last are set to 0 up to `budget`
+ * where `fill` is set, and left as they were where it is not. */
+typedef struct {
+  const void* k;             /* [batch, heads, n, d], strides skb, skh, skn */
+  const void* v;
+  const float* scores;       /* [batch, heads, n], strides ssb, ssh */
+  const int64_t* lengths;    /* [batch], or null: all n */
+  void* k_out;               /* [batch, heads, at least budget, d], strides okb, okh, okn */
+  void* v_out;
+  float* scores_out;         /* [batch, heads, at least budget], strides osb, osh */
+  int64_t* kept;
+  int64_t* lengths_out;
+  int64_t batch, heads, n, d, budget, recent;   /* 0 <= recent <= budget, budget >= 1 */
+  int64_t skb, skh, skn, svb, svh, svn, ssb, ssh;
+  int64_t okb, okh, okn, ovb, ovh, ovn, osb, osh;
+  int32_t dtype, fill;
+} topk_evict_args;
+
+int topk_evict_workspace_size(const topk_evict_args* args, size_t* bytes);
+int topk_evict(const topk_evict_args* args, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The next token of each row of logits, from a number u in [0, 1).  With m the
+ * row's largest logit and w_i = exp((z_i - m) / temperature), the row's tokens
+ * in the order of their logits, the largest first and equal ones by lower
+ * index:
+ *   1. the first top_k stay (top_k <= 0: all);
+ *   2. of those the shortest beginning whose w add up to at least top_p times
+ *      the sum (one at least; top_p >= 1: all);
+ *   3. of those the ones with w_i >= min(min_p, 1).
+ * The token is the first, by index, at which the sum of the w that stayed
+ * exceeds u times their whole sum S; logprob = log(w / S).  A temperature not
+ * above 0 takes the first of the order, with logprob 0.  A logit of NaN counts
+ * as -inf; a token of -inf is never taken, and a row of nothing else gives
+ * token -1 and logprob -inf.  Tokens equal to an infinite m have w = 1.
+ *
+ * w is held in 64 bits, as whole multiples of 2^-(62 - ceil(log2 n)), and so
+ * every sum is exact: the token does not depend on how the row was divided.
+ *
+ * Each of the four settings is a number for all rows, or, where its pointer is
+ * not null, an array of one for each row in device memory. */
+typedef struct {
+  const void* logits;        /* [rows, n], row stride ld */
+  const float* u;            /* [rows] */
+  int64_t* tokens;           /* [rows] */
+  float* logprobs;           /* [rows] */
+  const float* temperatures;
+  const int64_t* top_ks;
+  const float* top_ps;
+  const float* min_ps;
+  int64_t rows, n, ld;       /* n from 1 to 2^24 */
+  int64_t top_k;
+  float temperature, top_p, min_p;
+  int32_t dtype;
+} topk_sample_args;
+
+int topk_sample_workspace_size(const topk_sample_args* args, size_t* bytes);
+int topk_sample(const topk_sample_args* args, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Short English text for a status code (static storage). */
 const char* topk_status_string(int status);
 

@@ -15,6 +15,14 @@ Around the selection, for BatchTopK sparse autoencoders (differentiable):
     norm = tss.clip_grad_norm([p.grad for p in params], 1.0)
 
 and the dense product on its own, ``linear`` (bias, activation, residual).
+
+On the selections of a language model:
+
+    tokens, logprobs = tss.sample(logits, u, temperature=0.8, top_k=50, top_p=0.95)
+    rows, places, offsets = tss.dispatch(x, experts, n_experts)   # sorted by expert (differentiable)
+    out = tss.combine(y, places, weights)                         # and back (differentiable)
+    out = tss.attend(q, k, v, lengths, scores=scores)             # adds its probabilities to scores
+    k, v, scores, kept, lengths = tss.evict(k, v, scores, budget, recent, lengths)
 """
 from __future__ import annotations
 
@@ -42,7 +50,8 @@ __all__ = ["topk", "plan", "profile_enable", "profile_read", "stream_read", "sca
            "TAU_FORCED", "TAU_FILTER_RADIX", "TAU_FILTER_MERGE", "TAU_BIN_STREAMED", "TAU_BIN_RADIX",
            "TEST_BARRIER_GIVEUP", "filter_trace",
            "linear", "linear_grad", "encode", "encode_grad", "decode", "decode_grad", "grad_norm",
-           "clip_grad_norm"]
+           "clip_grad_norm",
+           "sample", "dispatch", "combine", "combine_grad", "attend", "evict"]
 
 _TORCH_CODES = {torch.int32: 0, torch.float32: 1, torch.bfloat16: 2}
 _NAME_CODES = _lib.DTYPE_CODES
@@ -291,3 +300,5 @@ def batchtopk(acts: torch.Tensor, k_total: int, params: Params | None = None, ma
 # the operators around the selection (they use topk above)
 from ._ops import (clip_grad_norm, decode, decode_grad, encode, encode_grad, grad_norm,  # noqa: E402
                    linear, linear_grad)
+# the operators on a language model's selections
+from ._model_ops import attend, combine, combine_grad, dispatch, evict, sample  # noqa: E402

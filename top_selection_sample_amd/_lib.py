@@ -37,7 +37,11 @@ EXPORTS = ("topk_default_params", "topk_plan", "topk_workspace_size", "topk_work
            "topk_linear_workspace_size", "topk_linear", "topk_linear_grad_workspace_size",
            "topk_linear_grad", "topk_decode_workspace_size", "topk_decode", "topk_decode_grad",
            "topk_encode_grad", "topk_grad_norm_workspace_size", "topk_grad_norm",
-           "topk_clip_grad_norm")
+           "topk_clip_grad_norm",
+           "topk_dispatch_workspace_size", "topk_dispatch", "topk_combine",
+           "topk_combine_grad_workspace_size", "topk_combine_grad",
+           "topk_attend_workspace_size", "topk_attend", "topk_evict_workspace_size", "topk_evict",
+           "topk_sample_workspace_size", "topk_sample")
 # the activations of topk_linear's epilogue
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
 STAGES = ("sample", "tau", "filter", "refine", "exact", "sort")
@@ -99,6 +103,15 @@ class Selection(ctypes.Structure):
                 ("dtype", ctypes.c_int32)]
 
 
+# structs that are only ever packed, in the order of their fields
+DISPATCH_FORMAT = "5Q6q2i"
+COMBINE_FORMAT = "4Q6q2i"
+COMBINE_GRAD_FORMAT = "6Q7q2i"
+ATTEND_FORMAT = "6Q17qfi"
+EVICT_FORMAT = "9Q22q2i"
+SAMPLE_FORMAT = "8Q4q3fi"
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -132,6 +145,12 @@ def _load():
     L.topk_grad_norm_workspace_size.argtypes = [i64, vp, P(sz)]   # host arrays by address
     L.topk_grad_norm.argtypes = [vp, vp, vp, i64, vp, vp, sz, vp]
     L.topk_clip_grad_norm.argtypes = [vp, vp, vp, i64, ctypes.c_float, ctypes.c_float, vp, vp, sz, vp]
+    L.topk_dispatch_workspace_size.argtypes = [i64, i64, i64, P(sz)]
+    L.topk_combine.argtypes = [vp, vp]
+    for name in ("dispatch", "combine_grad", "attend", "evict", "sample"):
+        getattr(L, "topk_" + name).argtypes = [vp, vp, sz, vp]
+        if name != "dispatch":
+            getattr(L, f"topk_{name}_workspace_size").argtypes = [vp, P(sz)]
     L.topk_status_string.argtypes = [i32]
     L.topk_status_string.restype = ctypes.c_char_p
     for name in EXPORTS:

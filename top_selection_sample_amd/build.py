@@ -9,8 +9,9 @@ from concurrent.futures import ThreadPoolExecutor
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libtopk_mi355x.so")
-SOURCES = ["topk_kernels.hip", "topk_linear.hip", "topk_sparse.hip", "topk_norm.hip", "topk_plan.cpp",
-           "topk_abi.cpp", "topk_ops_abi.cpp"]
+SOURCES = ["topk_kernels.hip", "topk_linear.hip", "topk_sparse.hip", "topk_norm.hip", "topk_route.hip",
+           "topk_cache.hip", "topk_draw.hip", "topk_plan.cpp", "topk_abi.cpp", "topk_ops_abi.cpp",
+           "topk_model_abi.cpp"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 # -amdgpu-kernarg-preload-count: the first 14 argument words of every kernel
 # arrive in scalar registers with the launch instead of being loaded from the

@@ -1,0 +1,713 @@
+// A cache of keys and values that keeps what attention looked at.
+//
+//   attend   s_ij = scale <q_i, k_j>,  p_i = softmax(s_i),  out_i = sum_j p_ij v_j,
+//            scores_j += sum of p_ij over the heads i that share the keys
+//   evict    the entries with the largest scores, and the newest, in their old order
+//
+// Both are bound by the cache that they read.
+#include <algorithm>
+
+#include "topk_model.hpp"
+#include "topk_ops_device.hpp"
+
+namespace tk {
+
+namespace {
+
+constexpr float LOG2E = 1.4426950408889634f;
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ uint32_t length_of(const int64_t* lengths, uint64_t b, uint32_t n) {
+  if (!lengths) return n;
+  const int64_t v = lengths[b];
+  return v < 0 ? 0u : v > (int64_t)n ? n : (uint32_t)v;
+}
+
+// ---------------------------------------------------------------- attend
+// One key-value head serves `group` query heads, taken 16 at a time as one side
+// of the matrix instructions; the keys are the other.  A wave takes STEP keys
+// at a time:
+//
+//   S[key, head] = K Q^T: a lane's registers of K are one vector of a key's row
+//     as it lies in memory, and S lands with a head to a lane and four keys to
+//     a register quad;
+//   O[head, column] += P V: the order of the summed keys is free, so P is used
+//     where S left it, and V is loaded by whole vectors of the rows that match
+//     (bf16: pairs of rows are interleaved by v_perm; f32: as they are).
+//
+// So neither operand goes through LDS.  The running maximum is raised only when
+// some logit exceeds it, which a ballot tells: the exchange between lanes that
+// this takes is rare.
+constexpr uint32_t ATT_WAVES = 4;
+constexpr uint32_t ATT_THREADS = 64 * ATT_WAVES;
+constexpr uint32_t HEADS = 16;          // query heads of a workgroup
+constexpr uint32_t JOIN_THREADS = 256;
+constexpr uint32_t JOIN_KEYS = 4 * JOIN_THREADS;
+
+struct AttArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  const int64_t* lengths;
+  float* scores;      // null: not wanted
+  void* out;
+  float* logits;      // [batch * heads][n], in units of log 2; null: not wanted
+  float* part;        // [batch * heads][splits][d]
+  float* ml;          // [batch * heads][splits][2]: maximum and sum
+  int64_t sqb, sqh, skb, skh, skn, svb, svh, svn, ssb, ssh, sob, soh;
+  uint64_t work;      // workgroups
+  uint32_t kv_heads, group, blocks16, n, d, splits, per;   // per: keys of a split
+  float scale2;
+};
+
+template <class T> struct Att;
+template <> struct Att<bf16_t> {
+  static constexpr uint32_t STEP = 32, KVEC = 8, KCHUNK = 32;
+  typedef bf16x8 Frag;
+};
+template <> struct Att<float> {
+  static constexpr uint32_t STEP = 16, KVEC = 4, KCHUNK = 16;
+  typedef f32x4 Frag;
+};
+
+// One vector of a row from column c on (c + N <= d, or d < N: what the row has, then zeros).
+template <class T, uint32_t N, bool NARROW>
+__device__ __forceinline__ void load_cols(const T* row, uint32_t c, uint32_t d, T* v) {
+  if constexpr (NARROW) {
+#pragma unroll
+    for (uint32_t i = 0; i < N; ++i) {
+      v[i] = T{};
+      if (c + i < d) v[i] = row[c + i];
+    }
+  } else {
+    __builtin_memcpy(v, row + c, N * sizeof(T));
+  }
+}
+
+// KC: chunks of a key's columns; VB: blocks of 16 * VW columns of V.
+template <class T, uint32_t KC, uint32_t VB, uint32_t VW, bool NARROW>
+__global__ __launch_bounds__(ATT_THREADS) void k_attend(AttArgs a) {
+  typedef Att<T> C;
+  constexpr uint32_t TILES = C::STEP / 16;
+  extern __shared__ float shared[];
+  const uint64_t id = block_id();
+  if (id >= a.work) return;
+  const uint32_t split = (uint32_t)(id % a.splits);
+  const uint64_t rest = id / a.splits;
+  const uint32_t hb = (uint32_t)(rest % a.blocks16);
+  const uint64_t bh = rest / a.blocks16;
+  const uint64_t b = bh / a.kv_heads, h = bh % a.kv_heads;
+  const uint32_t len = length_of(a.lengths, b, a.n);
+  const uint32_t s0 = split * a.per;
+  const uint32_t h0 = hb * HEADS, heads = min(HEADS, a.group - h0);   // of this workgroup
+  const uint32_t d = a.d;
+  const uint64_t first = bh * a.group + h0;                           // its first head, of all
+  T* out = static_cast<T*>(a.out) + b * a.sob + (h * a.group + h0) * a.soh;
+  if (s0 >= len) {
+    if (len == 0 && split == 0)
+      for (uint32_t i = threadIdx.x; i < heads * d; i += ATT_THREADS) out[(uint64_t)(i / d) * a.soh + i % d] = from_f32<T>(0.f);
+    return;
+  }
+  const uint32_t s1 = len - s0 < a.per ? len : s0 + a.per;
+  const uint32_t wave = threadIdx.x / 64, lane = threadIdx.x % 64, col = lane % 16, g = lane / 16;
+  const T* kbase = static_cast<const T*>(a.k) + b * a.skb + h * a.skh;
+  const T* vbase = static_cast<const T*>(a.v) + b * a.svb + h * a.svh;
+  const bool mine = col < heads;
+  const T* qrow = static_cast<const T*>(a.q) + b * a.sqb + (h * a.group + h0 + (mine ? col : 0)) * a.sqh;
+
+  // Q as the second operand.  A row's last vector begins earlier, so that it
+  // ends with the row: what the vector before it has is 0 here.
+  typename C::Frag q[KC];
+  uint32_t kcol[KC];
+#pragma unroll
+  for (uint32_t c = 0; c < KC; ++c) {
+    const uint32_t want = c * C::KCHUNK + g * C::KVEC;
+    kcol[c] = NARROW ? want : min(want, d - C::KVEC);
+    T t[C::KVEC];
+#pragma unroll
+    for (uint32_t i = 0; i < C::KVEC; ++i) {
+      const uint32_t at = kcol[c] + i;
+      t[i] = T{};
+      if (mine && at >= want && at < d) t[i] = qrow[at];
+    }
+    __builtin_memcpy(&q[c], t, sizeof(q[c]));
+  }
+  uint32_t vcol[VB];
+#pragma unroll
+  for (uint32_t x = 0; x < VB; ++x) {
+    const uint32_t want = x * 16 * VW + col * VW;
+    vcol[x] = NARROW ? want : min(want, d - VW);
+  }
+  f32x4 o[VB][VW];
+#pragma unroll
+  for (uint32_t x = 0; x < VB; ++x)
+#pragma unroll
+    for (uint32_t j = 0; j < VW; ++j) o[x][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  float m = -INFINITY, l = 0.f;   // of head `col`: m alike in the four lanes that share it, l of this lane's keys
+  float* logit_row = a.logits ? a.logits + (first + (mine ? col : 0)) * a.n : nullptr;
+
+  for (uint32_t base = s0 + wave * C::STEP; base < s1; base += ATT_WAVES * C::STEP) {
+    const bool tail = s1 - base < C::STEP;
+    // K
+    T kv[TILES][KC][C::KVEC];
+#pragma unroll
+    for (uint32_t t = 0; t < TILES; ++t) {
+      const uint32_t key = min(base + t * 16 + col, s1 - 1);
+      const T* row = kbase + (int64_t)key * a.skn;
+#pragma unroll
+      for (uint32_t c = 0; c < KC; ++c) load_cols<T, C::KVEC, NARROW>(row, kcol[c], d, kv[t][c]);
+    }
+    // V: this lane's keys, in the order in which S holds them
+    T vv[TILES * 4][VB][VW];
+#pragma unroll
+    for (uint32_t i = 0; i < TILES * 4; ++i) {
+      const uint32_t key = base + (i / 4) * 16 + g * 4 + i % 4;
+      const T* row = vbase + (int64_t)min(key, s1 - 1) * a.svn;
+#pragma unroll
+      for (uint32_t x = 0; x < VB; ++x) load_cols<T, VW, NARROW>(row, vcol[x], d, vv[i][x]);
+      if (tail && key >= s1) {   // the rows behind the last may hold anything: 0 * inf
+#pragma unroll
+        for (uint32_t x = 0; x < VB; ++x)
+#pragma unroll
+          for (uint32_t j = 0; j < VW; ++j) vv[i][x][j] = T{};
+      }
+    }
+    float s[TILES * 4];
+#pragma unroll
+    for (uint32_t t = 0; t < TILES; ++t) {
+      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (uint32_t c = 0; c < KC; ++c) {
+        typename C::Frag kf;
+        __builtin_memcpy(&kf, kv[t][c], sizeof(kf));
+        if constexpr (sizeof(T) == 2) {
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, q[c], acc, 0, 0, 0);
+        } else {
+#pragma unroll
+          for (uint32_t j = 0; j < 4; ++j) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(kf[j], q[c][j], acc, 0, 0, 0);
+        }
+      }
+#pragma unroll
+      for (uint32_t r = 0; r < 4; ++r) s[t * 4 + r] = acc[r] * a.scale2;
+    }
+    if (logit_row && mine) {
+#pragma unroll
+      for (uint32_t i = 0; i < TILES * 4; ++i) {
+        const uint32_t key = base + (i / 4) * 16 + g * 4 + i % 4;
+        if (key < s1) logit_row[key] = s[i];
+      }
+    }
+    if (tail) {
+#pragma unroll
+      for (uint32_t i = 0; i < TILES * 4; ++i)
+        if (base + (i / 4) * 16 + g * 4 + i % 4 >= s1) s[i] = -INFINITY;
+    }
+    float top = s[0];
+#pragma unroll
+    for (uint32_t i = 1; i < TILES * 4; ++i) top = fmaxf(top, s[i]);
+    if (__any(top > m)) {
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const float now = fmaxf(m, top);
+      const float down = m == -INFINITY ? 0.f : exp2f(m - now);
+      l *= down;
+      m = now;
+#pragma unroll
+      for (uint32_t r = 0; r < 4; ++r) {
+        const float f = __shfl(down, (int)(g * 4 + r));
+#pragma unroll
+        for (uint32_t x = 0; x < VB; ++x)
+#pragma unroll
+          for (uint32_t j = 0; j < VW; ++j) o[x][j][r] *= f;
+      }
+    }
+    const float ref = m == -INFINITY ? 0.f : m;
+    float p[TILES * 4];
+#pragma unroll
+    for (uint32_t i = 0; i < TILES * 4; ++i) {
+      p[i] = __builtin_amdgcn_exp2f(s[i] - ref);
+      l += p[i];
+    }
+    if constexpr (sizeof(T) == 2) {
+      const u32x4 pk = Vec<bf16_t>::pack(p);
+      bf16x8 pf;
+      __builtin_memcpy(&pf, &pk, 16);
+#pragma unroll
+      for (uint32_t x = 0; x < VB; ++x)
+#pragma unroll
+        for (uint32_t j = 0; j < VW; ++j) {
+          u32x4 w;
+#pragma unroll
+          for (uint32_t i = 0; i < 4; ++i) w[i] = (uint32_t)vv[2 * i][x][j].u | (uint32_t)vv[2 * i + 1][x][j].u << 16;
+          bf16x8 vf;
+          __builtin_memcpy(&vf, &w, 16);
+          o[x][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf, vf, o[x][j], 0, 0, 0);
+        }
+    } else {
+#pragma unroll
+      for (uint32_t i = 0; i < 4; ++i)
+#pragma unroll
+        for (uint32_t x = 0; x < VB; ++x)
+#pragma unroll
+          for (uint32_t j = 0; j < VW; ++j) o[x][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(p[i], to_f32(vv[i][x][j]), o[x][j], 0, 0, 0);
+    }
+  }
+  l += __shfl_xor(l, 16);
+  l += __shfl_xor(l, 32);
+
+  // the waves' parts through LDS: [wave][head][d], then (m, l) of each
+  float* wo = shared;
+  float* wm = shared + ATT_WAVES * heads * d;
+  float* wl = wm + ATT_WAVES * HEADS;
+  if (g == 0) {
+    wm[wave * HEADS + col] = m;
+    wl[wave * HEADS + col] = l;
+  }
+#pragma unroll
+  for (uint32_t r = 0; r < 4; ++r) {
+    const uint32_t head = g * 4 + r;
+    if (head >= heads) continue;
+    float* row = wo + (wave * heads + head) * d;
+#pragma unroll
+    for (uint32_t x = 0; x < VB; ++x)
+#pragma unroll
+      for (uint32_t j = 0; j < VW; ++j)
+        if (vcol[x] + j < d) row[vcol[x] + j] = o[x][j][r];
+  }
+  __syncthreads();
+  if (threadIdx.x < HEADS) {   // one maximum and sum for the workgroup; the waves' factors in place of their maxima
+    float top = -INFINITY, sum = 0.f;
+    for (uint32_t w = 0; w < ATT_WAVES; ++w) top = fmaxf(top, wm[w * HEADS + threadIdx.x]);
+    for (uint32_t w = 0; w < ATT_WAVES; ++w) {
+      const float mw = wm[w * HEADS + threadIdx.x];
+      const float f = mw == -INFINITY ? 1.f : exp2f(mw - top);
+      wm[w * HEADS + threadIdx.x] = f;
+      sum += f * wl[w * HEADS + threadIdx.x];
+    }
+    wl[threadIdx.x] = sum;
+    wl[HEADS + threadIdx.x] = top == -INFINITY ? 0.f : top;
+  }
+  __syncthreads();
+  const bool alone = a.splits == 1;
+  for (uint32_t i = threadIdx.x; i < heads * d; i += ATT_THREADS) {
+    const uint32_t head = i / d, c = i % d;
+    float v = 0.f;
+#pragma unroll
+    for (uint32_t w = 0; w < ATT_WAVES; ++w) v = fmaf(wm[w * HEADS + head], wo[(w * heads + head) * d + c], v);
+    if (alone) out[(uint64_t)head * a.soh + c] = from_f32<T>(v / wl[head]);
+    else a.part[((first + head) * a.splits + split) * d + c] = v;
+  }
+  if (!alone || a.blocks16 > 1) {
+    if (threadIdx.x < heads) {
+      float* ml = a.ml + ((first + threadIdx.x) * a.splits + split) * 2;
+      ml[0] = wl[HEADS + threadIdx.x];
+      ml[1] = wl[threadIdx.x];
+    }
+    return;
+  }
+  if (!a.scores) return;
+  // the whole row was this workgroup's: its logits, just written, become probabilities
+  __threadfence_block();
+  __syncthreads();
+  float* srow = a.scores + b * a.ssb + h * a.ssh;
+  for (uint32_t key = threadIdx.x; key < len; key += ATT_THREADS) {
+    float sum = 0.f;
+    for (uint32_t i = 0; i < heads; ++i) sum += exp2f(a.logits[(first + i) * a.n + key] - wl[HEADS + i]) / wl[i];
+    srow[key] += sum;
+  }
+}
+
+// The splits' parts of a key-value head: workgroups below `group` write a head's
+// output, the others add up JOIN_KEYS keys' probabilities each.
+template <class T>
+__global__ __launch_bounds__(JOIN_THREADS) void k_attend_join(AttArgs a, uint32_t outs, uint32_t chunks) {
+  extern __shared__ float shared[];   // scores: a maximum and the inverse of a sum for each head
+  const uint64_t id = block_id();
+  if (id >= a.work) return;
+  const uint32_t part = (uint32_t)(id % (outs + chunks));
+  const uint64_t bh = id / (outs + chunks);
+  const uint64_t b = bh / a.kv_heads, h = bh % a.kv_heads;
+  const uint32_t len = length_of(a.lengths, b, a.n);
+  const uint32_t live = (len + a.per - 1) / a.per;
+  if (len == 0) return;   // the output is written, no weights are added
+  const uint32_t wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+  if (part < outs) {
+    const uint64_t head = bh * a.group + part;
+    const float* ml = a.ml + head * a.splits * 2;
+    float top = -INFINITY;
+    for (uint32_t s = 0; s < live; ++s) top = fmaxf(top, ml[2 * s]);
+    T* out = static_cast<T*>(a.out) + b * a.sob + (h * a.group + part) * a.soh;
+    for (uint32_t c = threadIdx.x; c < a.d; c += JOIN_THREADS) {
+      float sum = 0.f, v = 0.f;
+      for (uint32_t s = 0; s < live; ++s) {
+        const float f = exp2f(ml[2 * s] - top);
+        sum = fmaf(f, ml[2 * s + 1], sum);
+        v = fmaf(f, a.part[(head * a.splits + s) * a.d + c], v);
+      }
+      out[c] = from_f32<T>(v / sum);
+    }
+    return;
+  }
+  const uint32_t k0 = (part - outs) * JOIN_KEYS;
+  if (k0 >= len) return;
+  for (uint32_t i = wave; i < a.group; i += JOIN_THREADS / 64) {
+    const float* ml = a.ml + (bh * a.group + i) * a.splits * 2;
+    float top = -INFINITY, sum = 0.f;
+    for (uint32_t s = lane; s < live; s += 64) top = fmaxf(top, ml[2 * s]);
+#pragma unroll
+    for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+    for (uint32_t s = lane; s < live; s += 64) sum = fmaf(exp2f(ml[2 * s] - top), ml[2 * s + 1], sum);
+    sum = wave_sum(sum);
+    if (lane == 0) {
+      shared[2 * i] = top;
+      shared[2 * i + 1] = 1.f / sum;
+    }
+  }
+  __syncthreads();
+  float* srow = a.scores + b * a.ssb + h * a.ssh;
+#pragma unroll
+  for (uint32_t x = 0; x < JOIN_KEYS / JOIN_THREADS; ++x) {
+    const uint32_t key = k0 + x * JOIN_THREADS + threadIdx.x;
+    if (key >= len) break;
+    float sum = 0.f;
+    for (uint32_t i = 0; i < a.group; ++i) sum = fmaf(exp2f(a.logits[(bh * a.group + i) * a.n + key] - shared[2 * i]), shared[2 * i + 1], sum);
+    srow[key] += sum;
+  }
+}
+
+struct AttPlan {
+  uint32_t blocks16 = 1, splits = 1, per = 0;
+  size_t off_logits = 0, off_part = 0, off_ml = 0, total = 0;
+};
+
+// Splits: enough workgroups for four to a compute unit, as long as each of a
+// workgroup's waves has a step of keys.
+AttPlan attend_plan(const topk_attend_args& a, int cus) {
+  AttPlan p;
+  if (!a.batch || !a.heads || !a.n || !a.d) return p;
+  const int64_t group = a.heads / a.kv_heads;
+  p.blocks16 = (uint32_t)ceil_div(group, HEADS);
+  const int64_t rows = a.batch * a.kv_heads * p.blocks16;
+  const int64_t least = ATT_WAVES * (a.dtype == TOPK_BF16 ? Att<bf16_t>::STEP : Att<float>::STEP);
+  const int64_t want = std::max<int64_t>(1, std::min(ceil_div(4 * cus, rows), ceil_div(a.n, least)));
+  p.per = (uint32_t)(ceil_div(ceil_div(a.n, want), least) * least);
+  p.splits = (uint32_t)ceil_div(a.n, p.per);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += align256(bytes);
+    return here;
+  };
+  const size_t heads = (size_t)(a.batch * a.heads);
+  if (a.scores) p.off_logits = take(heads * a.n * 4);
+  if (p.splits > 1) p.off_part = take(heads * p.splits * a.d * 4);
+  if (p.splits > 1 || p.blocks16 > 1) p.off_ml = take(heads * p.splits * 8);
+  p.total = at;
+  return p;
+}
+
+template <class T, uint32_t KC, uint32_t VB, uint32_t VW, bool NARROW>
+void attend_one(const AttArgs& a, hipStream_t s) {
+  const uint32_t heads = std::min(a.group, HEADS);
+  const size_t lds = (ATT_WAVES * heads * a.d + 2 * ATT_WAVES * HEADS) * sizeof(float);
+  k_attend<T, KC, VB, VW, NARROW><<<wide_grid(a.work), ATT_THREADS, lds, s>>>(a);
+}
+
+void attend_typed(const AttArgs& a, bf16_t, hipStream_t s) {
+  if (a.d < 8) attend_one<bf16_t, 1, 1, 4, true>(a, s);
+  else if (a.d <= 64) attend_one<bf16_t, 2, 1, 4, false>(a, s);
+  else if (a.d <= 96) attend_one<bf16_t, 3, 1, 8, false>(a, s);
+  else if (a.d <= 128) attend_one<bf16_t, 4, 1, 8, false>(a, s);
+  else if (a.d <= 192) attend_one<bf16_t, 6, 2, 8, false>(a, s);
+  else attend_one<bf16_t, 8, 2, 8, false>(a, s);
+}
+void attend_typed(const AttArgs& a, float, hipStream_t s) {
+  if (a.d < 4) attend_one<float, 1, 1, 4, true>(a, s);
+  else if (a.d <= 64) attend_one<float, 4, 1, 4, false>(a, s);
+  else if (a.d <= 96) attend_one<float, 6, 2, 4, false>(a, s);
+  else if (a.d <= 128) attend_one<float, 8, 2, 4, false>(a, s);
+  else if (a.d <= 192) attend_one<float, 12, 3, 4, false>(a, s);
+  else attend_one<float, 16, 4, 4, false>(a, s);
+}
+
+template <class T>
+hipError_t attend_call(const topk_attend_args& in, const AttPlan& p, char* ws, hipStream_t s) {
+  AttArgs a;
+  a.q = in.q;
+  a.k = in.k;
+  a.v = in.v;
+  a.lengths = in.lengths;
+  a.scores = in.scores;
+  a.out = in.out;
+  a.sqb = in.sqb, a.sqh = in.sqh;
+  a.skb = in.skb, a.skh = in.skh, a.skn = in.skn;
+  a.svb = in.svb, a.svh = in.svh, a.svn = in.svn;
+  a.ssb = in.ssb, a.ssh = in.ssh;
+  a.sob = in.sob, a.soh = in.soh;
+  a.kv_heads = (uint32_t)in.kv_heads;
+  a.group = (uint32_t)(in.heads / in.kv_heads);
+  a.blocks16 = p.blocks16;
+  a.n = (uint32_t)in.n;
+  a.d = (uint32_t)in.d;
+  a.splits = p.splits;
+  a.per = p.per;
+  a.scale2 = in.scale * LOG2E;
+  a.logits = in.scores ? reinterpret_cast<float*>(ws + p.off_logits) : nullptr;
+  a.part = reinterpret_cast<float*>(ws + p.off_part);
+  a.ml = reinterpret_cast<float*>(ws + p.off_ml);
+  const uint64_t rows = (uint64_t)in.batch * a.kv_heads;
+  a.work = rows * p.blocks16 * p.splits;
+  attend_typed(a, T{}, s);
+  const uint32_t outs = p.splits > 1 ? a.group : 0;
+  const uint32_t chunks = in.scores && (p.splits > 1 || p.blocks16 > 1) ? (a.n + JOIN_KEYS - 1) / JOIN_KEYS : 0;
+  if (outs + chunks) {
+    a.work = rows * (outs + chunks);
+    k_attend_join<T><<<wide_grid(a.work), JOIN_THREADS, a.group * 8, s>>>(a, outs, chunks);
+  }
+  return hipGetLastError();
+}
+
+// An empty cache: every sequence attends to nothing.
+template <class T>
+__global__ __launch_bounds__(JOIN_THREADS) void k_attend_nothing(T* __restrict__ out, int64_t sob, int64_t soh, uint32_t heads,
+                                                                 uint32_t d, uint64_t items) {
+  const uint64_t i = (uint64_t)block_id() * JOIN_THREADS + threadIdx.x;
+  if (i >= items) return;
+  const uint64_t row = i / d;
+  out[(int64_t)(row / heads) * sob + (int64_t)(row % heads) * soh + i % d] = from_f32<T>(0.f);
+}
+
+template <class T>
+hipError_t attend_nothing(const topk_attend_args& a, hipStream_t s) {
+  const uint64_t items = (uint64_t)(a.batch * a.heads) * (uint64_t)a.d;
+  k_attend_nothing<T><<<wide_grid((items + JOIN_THREADS - 1) / JOIN_THREADS), JOIN_THREADS, 0, s>>>(
+      static_cast<T*>(a.out), a.sob, a.soh, (uint32_t)a.heads, (uint32_t)a.d, items);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------- evict
+// k_evict_pick: a workgroup for each key-value head of each sequence.  Its
+// scores are radix-selected, eight bits at a time, for the key of the last
+// entry that stays and the number of equal ones; then every wave counts what
+// stays of its share, and writes it in order behind the waves before it.
+constexpr uint32_t PICK_THREADS = 1024;
+constexpr uint32_t PICK_WAVES = PICK_THREADS / 64;
+constexpr uint32_t COPY_THREADS = 256;
+constexpr uint32_t COPY_AHEAD = 4;      // slots that a lane copies at a time
+
+// Larger scores have larger keys; 0 and -0 are equal, NaN is above all.
+__device__ __forceinline__ uint32_t score_key(float v) {
+  if (v != v) return 0xFFFFFFFFu;
+  const uint32_t u = __float_as_uint(v + 0.f);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+struct EvictArgs {
+  const void* k;
+  const void* v;
+  const float* scores;
+  const int64_t* lengths;
+  void* k_out;
+  void* v_out;
+  float* scores_out;
+  int64_t* kept;          // [batch * heads][budget]
+  int64_t* lengths_out;
+  int64_t skb, skh, skn, svb, svh, svn, ssb, ssh;
+  int64_t okb, okh, okn, ovb, ovh, ovn, osb, osh;
+  uint64_t work;
+  uint32_t heads, n, d, budget, recent, fill;
+};
+
+__global__ __launch_bounds__(PICK_THREADS) void k_evict_pick(EvictArgs a) {
+  __shared__ uint32_t hist[256];
+  __shared__ uint32_t strict[PICK_WAVES], ties[PICK_WAVES];
+  __shared__ uint32_t found, left;
+  const uint64_t bh = block_id();
+  if (bh >= a.work) return;
+  const uint64_t b = bh / a.heads, h = bh % a.heads;
+  const uint32_t tid = threadIdx.x, wave = tid / 64, lane = tid % 64;
+  const uint32_t len = length_of(a.lengths, b, a.n);
+  const uint32_t kept = min(len, a.budget);
+  if (h == 0 && tid == 0) a.lengths_out[b] = kept;
+  const float* srow = a.scores + b * a.ssb + h * a.ssh;
+  float* so = a.scores_out + b * a.osb + h * a.osh;
+  int64_t* ko = a.kept + bh * a.budget;
+  for (uint32_t i = kept + tid; i < a.budget; i += PICK_THREADS) {
+    ko[i] = -1;
+    if (a.fill) so[i] = 0.f;
+  }
+  const uint32_t old = len <= a.budget ? 0u : len - a.recent;   // entries that have to earn their place
+  uint32_t need = kept - (len - old);                           // and how many of them do
+  uint32_t key = 0;          // the least key that stays
+  if (old && need) {
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      if (tid < 256) hist[tid] = 0;
+      __syncthreads();
+      for (uint32_t i = tid; i < old; i += PICK_THREADS) {
+        const uint32_t x = score_key(srow[i]);
+        if (shift == 24 || (x ^ key) >> (shift + 8) == 0) atomicAdd(&hist[x >> shift & 255u], 1u);
+      }
+      __syncthreads();
+      if (tid < 64) {   // bins from the highest down, four to a lane
+        uint32_t c[4], sum = 0;
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) sum += c[i] = hist[255 - (lane * 4 + i)];
+        uint32_t up = sum;
+#pragma unroll
+        for (uint32_t o = 1; o < 64; o <<= 1) {
+          const uint32_t t = __shfl_up(up, o);
+          if (lane >= o) up += t;
+        }
+        uint32_t above = up - sum;
+        if (above < need && need <= up) {
+#pragma unroll
+          for (uint32_t i = 0; i < 4; ++i) {
+            if (above < need && need <= above + c[i]) {
+              found = 255 - (lane * 4 + i);
+              left = need - above;
+            }
+            above += c[i];
+          }
+        }
+      }
+      __syncthreads();
+      key |= found << shift;
+      need = left;
+    }
+  }
+  // `need` of the entries equal to `key` stay: the first ones
+  const uint32_t per = ((len + PICK_THREADS - 1) / PICK_THREADS) * 64;
+  const uint32_t w0 = min(wave * per, len), w1 = min(w0 + per, len);
+  const bool any = old && a.budget > a.recent;
+  uint32_t ns = 0, nt = 0;
+  for (uint32_t c = w0; c < w1; c += 64) {
+    const uint32_t i = c + lane;
+    const uint32_t x = i < old && any ? score_key(srow[i]) : 0u;
+    const bool in = i < w1;
+    ns += __popcll(__ballot(in && (i >= old || (any && x > key))));
+    nt += __popcll(__ballot(in && i < old && any && x == key));
+  }
+  if (lane == 0) {
+    strict[wave] = ns;
+    ties[wave] = nt;
+  }
+  __syncthreads();
+  uint32_t at = 0, tie = 0;
+  for (uint32_t w = 0; w < wave; ++w) {
+    at += strict[w];
+    tie += ties[w];
+  }
+  const uint64_t below = (uint64_t(1) << lane) - 1;
+  for (uint32_t c = w0; c < w1; c += 64) {
+    const uint32_t i = c + lane;
+    const bool in = i < w1;
+    const float v = in ? srow[i] : 0.f;
+    const uint32_t x = i < old && any ? score_key(v) : 0u;
+    const bool sure = in && (i >= old || (any && x > key)), equal = in && i < old && any && x == key;
+    const uint64_t ms = __ballot(sure), mt = __ballot(equal);
+    const uint32_t rank = tie + __popcll(mt & below);
+    const uint32_t slot = at + __popcll(ms & below) + min(rank, need);
+    if (sure || (equal && rank < need)) {
+      ko[slot] = i;
+      so[slot] = v;
+    }
+    at += __popcll(ms);
+    tie += __popcll(mt);
+  }
+}
+
+// The kept rows of K and V.  LANES lanes to a row; a lane has the rows of
+// COPY_AHEAD slots of both in flight.
+template <class U, int VEC>
+__global__ __launch_bounds__(COPY_THREADS) void k_evict_copy(EvictArgs a, uint32_t lanes, uint32_t pieces) {
+  typedef Bits<U, VEC> B;
+  const uint64_t id = block_id();
+  if (id >= a.work) return;
+  const uint64_t bh = id / pieces;
+  const uint64_t b = bh / a.heads, h = bh % a.heads;
+  const uint32_t rows = COPY_THREADS / lanes;
+  const uint32_t slot0 = (uint32_t)(id % pieces) * rows * COPY_AHEAD + threadIdx.x / lanes;
+  const int64_t* kept = a.kept + bh * a.budget;
+  const U* kb = static_cast<const U*>(a.k) + b * a.skb + h * a.skh;
+  const U* vb = static_cast<const U*>(a.v) + b * a.svb + h * a.svh;
+  U* ko = static_cast<U*>(a.k_out) + b * a.okb + h * a.okh;
+  U* vo = static_cast<U*>(a.v_out) + b * a.ovb + h * a.ovh;
+  int64_t from[COPY_AHEAD];
+#pragma unroll
+  for (uint32_t i = 0; i < COPY_AHEAD; ++i) {
+    const uint32_t slot = slot0 + i * rows;
+    from[i] = slot < a.budget ? kept[slot] : -2;
+    if (from[i] == -1 && !a.fill) from[i] = -2;   // left as it was
+  }
+  for (uint32_t c = threadIdx.x % lanes * VEC; c < a.d; c += lanes * VEC) {
+    const uint32_t at = column_of<VEC>(c, a.d);
+    typename B::type kr[COPY_AHEAD], vr[COPY_AHEAD];
+#pragma unroll
+    for (uint32_t i = 0; i < COPY_AHEAD; ++i) {
+      kr[i] = vr[i] = B::zero();
+      if (from[i] >= 0) {
+        kr[i] = B::load(kb + from[i] * a.skn + at);
+        vr[i] = B::load(vb + from[i] * a.svn + at);
+      }
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < COPY_AHEAD; ++i) {
+      if (from[i] == -2) continue;
+      const int64_t slot = slot0 + i * rows;
+      B::store(ko + slot * a.okn + at, kr[i]);
+      B::store(vo + slot * a.ovn + at, vr[i]);
+    }
+  }
+}
+
+template <class U, int VEC>
+hipError_t evict_copy(EvictArgs a, hipStream_t s) {
+  uint32_t lanes = 1;
+  while (lanes < 64 && lanes * VEC < a.d) lanes *= 2;
+  const uint32_t per = COPY_THREADS / lanes * COPY_AHEAD;
+  const uint32_t pieces = (a.budget + per - 1) / per;
+  a.work *= pieces;
+  k_evict_copy<U, VEC><<<wide_grid(a.work), COPY_THREADS, 0, s>>>(a, lanes, pieces);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t attend_workspace(const topk_attend_args& a, int cus) { return attend_plan(a, cus).total; }
+
+hipError_t launch_attend(const topk_attend_args& a, void* ws, int cus, hipStream_t s) {
+  if (!a.batch || !a.heads || !a.d) return hipSuccess;
+  if (!a.n) return a.dtype == TOPK_BF16 ? attend_nothing<bf16_t>(a, s) : attend_nothing<float>(a, s);
+  const AttPlan p = attend_plan(a, cus);
+  char* w = static_cast<char*>(ws);
+  return a.dtype == TOPK_BF16 ? attend_call<bf16_t>(a, p, w, s) : attend_call<float>(a, p, w, s);
+}
+
+size_t evict_workspace(const topk_evict_args&) { return 0; }
+
+hipError_t launch_evict(const topk_evict_args& in, void*, hipStream_t s) {
+  if (!in.batch || !in.heads) return hipSuccess;
+  EvictArgs a;
+  a.k = in.k, a.v = in.v, a.scores = in.scores, a.lengths = in.lengths;
+  a.k_out = in.k_out, a.v_out = in.v_out, a.scores_out = in.scores_out;
+  a.kept = in.kept, a.lengths_out = in.lengths_out;
+  a.skb = in.skb, a.skh = in.skh, a.skn = in.skn, a.svb = in.svb, a.svh = in.svh, a.svn = in.svn;
+  a.ssb = in.ssb, a.ssh = in.ssh;
+  a.okb = in.okb, a.okh = in.okh, a.okn = in.okn, a.ovb = in.ovb, a.ovh = in.ovh, a.ovn = in.ovn;
+  a.osb = in.osb, a.osh = in.osh;
+  a.heads = (uint32_t)in.heads;
+  a.n = (uint32_t)in.n;
+  a.d = (uint32_t)in.d;
+  a.budget = (uint32_t)in.budget;
+  a.recent = (uint32_t)in.recent;
+  a.fill = in.fill != 0;
+  a.work = (uint64_t)in.batch * a.heads;
+  k_evict_pick<<<wide_grid(a.work), PICK_THREADS, 0, s>>>(a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !a.budget || !a.d) return e;
+  if (in.dtype == TOPK_BF16) return a.d >= 8 ? evict_copy<uint16_t, 8>(a, s) : evict_copy<uint16_t, 1>(a, s);
+  return a.d >= 4 ? evict_copy<uint32_t, 4>(a, s) : evict_copy<uint32_t, 1>(a, s);
+}
+
+}  // namespace tk

@@ -106,6 +106,26 @@ __device__ __forceinline__ void store_vec(T* p, const float* v) {
   else Vec<T>::store(p, v);
 }
 
+// Rows that are moved, not computed: VEC elements of a row by their bits (a
+// type's own load and store may quiet a NaN).
+template <class U, int VEC> struct Bits {
+  typedef u32x4 type;
+  __device__ static type load(const U* p) { return read16(p); }
+  __device__ static type zero() { return u32x4{0, 0, 0, 0}; }
+  __device__ static void store(U* p, type v) { __builtin_memcpy(p, &v, 16); }
+  __device__ static void stream(U* p, type v) {
+    typedef u32x4 any_u32x4 __attribute__((aligned(2)));
+    __builtin_nontemporal_store(v, reinterpret_cast<any_u32x4*>(p));
+  }
+};
+template <class U> struct Bits<U, 1> {
+  typedef U type;
+  __device__ static type load(const U* p) { return *p; }
+  __device__ static type zero() { return 0; }
+  __device__ static void store(U* p, type v) { *p = v; }
+  __device__ static void stream(U* p, type v) { *p = v; }
+};
+
 // Outputs from 16 MB on are stored past the caches: they would push out what
 // the rest of the launch reads (the product of 4096 x 512 x 65536 bf16, in its
 // first form 358 us against 439; the encoder's gradient at 65536 latents 92.6
