@@ -71,25 +71,32 @@ template <> struct Att<float> {
   typedef f32x4 Frag;
 };
 
-// One vector of a row from column c on (c + N <= d, or d < N: what the row has, then zeros).
+// One vector of a row, at its column c (c + N <= d, or d < N: what the row has, then zeros).
 template <class T, uint32_t N, bool NARROW>
-__device__ __forceinline__ void load_cols(const T* row, uint32_t c, uint32_t d, T* v) {
+__device__ __forceinline__ void load_cols(const T* at, uint32_t c, uint32_t d, T* v) {
   if constexpr (NARROW) {
 #pragma unroll
     for (uint32_t i = 0; i < N; ++i) {
       v[i] = T{};
-      if (c + i < d) v[i] = row[c + i];
+      if (c + i < d) v[i] = at[i];
     }
   } else {
-    __builtin_memcpy(v, row + c, N * sizeof(T));
+    __builtin_memcpy(v, at, N * sizeof(T));
   }
+}
+
+// An element at a byte offset below 2^32 from an address that all lanes share:
+// the form that a load takes from a scalar register and one vector register.
+template <class T>
+__device__ __forceinline__ const T* at_offset(const T* base, uint32_t bytes) {
+  return reinterpret_cast<const T*>(reinterpret_cast<const char*>(base) + bytes);
 }
 
 // KC: chunks of a key's columns; VB: blocks of 16 * VW columns of V.
 template <class T, uint32_t KC, uint32_t VB, uint32_t VW, bool NARROW>
-__global__ __launch_bounds__(ATT_THREADS) void k_attend(AttArgs a) {
+__global__ __launch_bounds__(ATT_THREADS, KC * VB > 8 ? 1 : 2) void k_attend(AttArgs a) {
   typedef Att<T> C;
-  constexpr uint32_t TILES = C::STEP / 16;
+  constexpr uint32_t TILES = C::STEP / 16, KEYS = TILES * 4;   // KEYS: a lane's keys of a step
   extern __shared__ float shared[];
   const uint64_t id = block_id();
   if (id >= a.work) return;
@@ -110,30 +117,26 @@ __global__ __launch_bounds__(ATT_THREADS) void k_attend(AttArgs a) {
     return;
   }
   const uint32_t s1 = len - s0 < a.per ? len : s0 + a.per;
-  const uint32_t wave = threadIdx.x / 64, lane = threadIdx.x % 64, col = lane % 16, g = lane / 16;
-  const T* kbase = static_cast<const T*>(a.k) + b * a.skb + h * a.skh;
-  const T* vbase = static_cast<const T*>(a.v) + b * a.svb + h * a.svh;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const uint32_t lane = threadIdx.x % 64, col = lane % 16, g = lane / 16;
   const bool mine = col < heads;
   const T* qrow = static_cast<const T*>(a.q) + b * a.sqb + (h * a.group + h0 + (mine ? col : 0)) * a.sqh;
 
   // Q as the second operand.  A row's last vector begins earlier, so that it
   // ends with the row: what the vector before it has is 0 here.
   typename C::Frag q[KC];
-  uint32_t kcol[KC];
+  uint32_t kcol[KC], vcol[VB];
 #pragma unroll
   for (uint32_t c = 0; c < KC; ++c) {
     const uint32_t want = c * C::KCHUNK + g * C::KVEC;
     kcol[c] = NARROW ? want : min(want, d - C::KVEC);
     T t[C::KVEC];
+    load_cols<T, C::KVEC, NARROW>(qrow + kcol[c], kcol[c], d, t);
 #pragma unroll
-    for (uint32_t i = 0; i < C::KVEC; ++i) {
-      const uint32_t at = kcol[c] + i;
-      t[i] = T{};
-      if (mine && at >= want && at < d) t[i] = qrow[at];
-    }
+    for (uint32_t i = 0; i < C::KVEC; ++i)
+      if (!mine || kcol[c] + i < want) t[i] = T{};
     __builtin_memcpy(&q[c], t, sizeof(q[c]));
   }
-  uint32_t vcol[VB];
 #pragma unroll
   for (uint32_t x = 0; x < VB; ++x) {
     const uint32_t want = x * 16 * VW + col * VW;
@@ -147,33 +150,39 @@ __global__ __launch_bounds__(ATT_THREADS) void k_attend(AttArgs a) {
   float m = -INFINITY, l = 0.f;   // of head `col`: m alike in the four lanes that share it, l of this lane's keys
   float* logit_row = a.logits ? a.logits + (first + (mine ? col : 0)) * a.n : nullptr;
 
-  for (uint32_t base = s0 + wave * C::STEP; base < s1; base += ATT_WAVES * C::STEP) {
-    const bool tail = s1 - base < C::STEP;
-    // K
-    T kv[TILES][KC][C::KVEC];
+  const uint32_t ldk = (uint32_t)a.skn * (uint32_t)sizeof(T), ldv = (uint32_t)a.svn * (uint32_t)sizeof(T);
+  uint32_t base = s0 + wave * C::STEP;
+  const T* kbase = static_cast<const T*>(a.k) + b * a.skb + h * a.skh + (int64_t)base * a.skn;
+  const T* vbase = static_cast<const T*>(a.v) + b * a.svb + h * a.svh + (int64_t)base * a.svn;
+  // This lane's place of key i of a step: the order in which S holds them.
+  auto key_of = [&](uint32_t i) { return (i / 4) * 16 + g * 4 + i % 4; };
+
+  // The step's keys; a step that the sequence does not fill reads its last row again.
+  T kv[TILES][KC][C::KVEC];
+  auto load_keys = [&](uint32_t have) {
+    const uint32_t last = min(have, C::STEP) - 1;
 #pragma unroll
     for (uint32_t t = 0; t < TILES; ++t) {
-      const uint32_t key = min(base + t * 16 + col, s1 - 1);
-      const T* row = kbase + (int64_t)key * a.skn;
+      const uint32_t row = min(t * 16 + col, last) * ldk;
 #pragma unroll
-      for (uint32_t c = 0; c < KC; ++c) load_cols<T, C::KVEC, NARROW>(row, kcol[c], d, kv[t][c]);
+      for (uint32_t c = 0; c < KC; ++c)
+        load_cols<T, C::KVEC, NARROW>(at_offset(kbase, row + kcol[c] * (uint32_t)sizeof(T)), kcol[c], d, kv[t][c]);
     }
-    // V: this lane's keys, in the order in which S holds them
-    T vv[TILES * 4][VB][VW];
+  };
+  if (base < s1) load_keys(s1 - base);
+  for (; base < s1; base += ATT_WAVES * C::STEP) {
+    const uint32_t have = s1 - base;
+    const bool tail = have < C::STEP;
+    T vv[KEYS][VB][VW];
 #pragma unroll
-    for (uint32_t i = 0; i < TILES * 4; ++i) {
-      const uint32_t key = base + (i / 4) * 16 + g * 4 + i % 4;
-      const T* row = vbase + (int64_t)min(key, s1 - 1) * a.svn;
+    for (uint32_t i = 0; i < KEYS; ++i) {
+      const uint32_t row = min(key_of(i), have - 1) * ldv;
 #pragma unroll
-      for (uint32_t x = 0; x < VB; ++x) load_cols<T, VW, NARROW>(row, vcol[x], d, vv[i][x]);
-      if (tail && key >= s1) {   // the rows behind the last may hold anything: 0 * inf
-#pragma unroll
-        for (uint32_t x = 0; x < VB; ++x)
-#pragma unroll
-          for (uint32_t j = 0; j < VW; ++j) vv[i][x][j] = T{};
-      }
+      for (uint32_t x = 0; x < VB; ++x)
+        load_cols<T, VW, NARROW>(at_offset(vbase, row + vcol[x] * (uint32_t)sizeof(T)), vcol[x], d, vv[i][x]);
     }
-    float s[TILES * 4];
+    vbase += (int64_t)(ATT_WAVES * C::STEP) * a.svn;
+    float s[KEYS];
 #pragma unroll
     for (uint32_t t = 0; t < TILES; ++t) {
       f32x4 acc = {0.f, 0.f, 0.f, 0.f};
@@ -191,26 +200,39 @@ __global__ __launch_bounds__(ATT_THREADS) void k_attend(AttArgs a) {
 #pragma unroll
       for (uint32_t r = 0; r < 4; ++r) s[t * 4 + r] = acc[r] * a.scale2;
     }
+    // the next step's keys are on their way while this one's values are used
+    kbase += (int64_t)(ATT_WAVES * C::STEP) * a.skn;
+    if (have > ATT_WAVES * C::STEP) load_keys(have - ATT_WAVES * C::STEP);
     if (logit_row && mine) {
+      if (!tail) {
 #pragma unroll
-      for (uint32_t i = 0; i < TILES * 4; ++i) {
-        const uint32_t key = base + (i / 4) * 16 + g * 4 + i % 4;
-        if (key < s1) logit_row[key] = s[i];
+        for (uint32_t t = 0; t < TILES; ++t) __builtin_memcpy(logit_row + base + t * 16 + g * 4, s + t * 4, 16);
+      } else {
+#pragma unroll
+        for (uint32_t i = 0; i < KEYS; ++i)
+          if (key_of(i) < have) logit_row[base + key_of(i)] = s[i];
       }
     }
-    if (tail) {
+    if (tail) {   // what the last row was read for once more does not count
 #pragma unroll
-      for (uint32_t i = 0; i < TILES * 4; ++i)
-        if (base + (i / 4) * 16 + g * 4 + i % 4 >= s1) s[i] = -INFINITY;
+      for (uint32_t i = 0; i < KEYS; ++i) {
+        const bool in = key_of(i) < have;
+        s[i] = in ? s[i] : -INFINITY;
+#pragma unroll
+        for (uint32_t x = 0; x < VB; ++x)
+#pragma unroll
+          for (uint32_t j = 0; j < VW; ++j)
+            if (!in) vv[i][x][j] = T{};   // not 0 * inf
+      }
     }
     float top = s[0];
 #pragma unroll
-    for (uint32_t i = 1; i < TILES * 4; ++i) top = fmaxf(top, s[i]);
+    for (uint32_t i = 1; i < KEYS; ++i) top = fmaxf(top, s[i]);
     if (__any(top > m)) {
       top = fmaxf(top, __shfl_xor(top, 16));
       top = fmaxf(top, __shfl_xor(top, 32));
       const float now = fmaxf(m, top);
-      const float down = m == -INFINITY ? 0.f : exp2f(m - now);
+      const float down = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - now);
       l *= down;
       m = now;
 #pragma unroll
@@ -223,9 +245,9 @@ __global__ __launch_bounds__(ATT_THREADS) void k_attend(AttArgs a) {
       }
     }
     const float ref = m == -INFINITY ? 0.f : m;
-    float p[TILES * 4];
+    float p[KEYS];
 #pragma unroll
-    for (uint32_t i = 0; i < TILES * 4; ++i) {
+    for (uint32_t i = 0; i < KEYS; ++i) {
       p[i] = __builtin_amdgcn_exp2f(s[i] - ref);
       l += p[i];
     }
@@ -239,7 +261,12 @@ __global__ __launch_bounds__(ATT_THREADS) void k_attend(AttArgs a) {
         for (uint32_t j = 0; j < VW; ++j) {
           u32x4 w;
 #pragma unroll
-          for (uint32_t i = 0; i < 4; ++i) w[i] = (uint32_t)vv[2 * i][x][j].u | (uint32_t)vv[2 * i + 1][x][j].u << 16;
+          for (uint32_t i = 0; i < 4; ++i) {
+            uint32_t lo, hi;   // two columns of two rows
+            __builtin_memcpy(&lo, &vv[2 * i][x][j & ~1u], 4);
+            __builtin_memcpy(&hi, &vv[2 * i + 1][x][j & ~1u], 4);
+            w[i] = __builtin_amdgcn_perm(hi, lo, j & 1 ? 0x07060302u : 0x05040100u);
+          }
           bf16x8 vf;
           __builtin_memcpy(&vf, &w, 16);
           o[x][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf, vf, o[x][j], 0, 0, 0);
@@ -273,7 +300,7 @@ __global__ __launch_bounds__(ATT_THREADS) void k_attend(AttArgs a) {
     for (uint32_t x = 0; x < VB; ++x)
 #pragma unroll
       for (uint32_t j = 0; j < VW; ++j)
-        if (vcol[x] + j < d) row[vcol[x] + j] = o[x][j][r];
+        if (!NARROW || vcol[x] + j < d) row[vcol[x] + j] = o[x][j][r];
   }
   __syncthreads();
   if (threadIdx.x < HEADS) {   // one maximum and sum for the workgroup; the waves' factors in place of their maxima
@@ -281,7 +308,7 @@ __global__ __launch_bounds__(ATT_THREADS) void k_attend(AttArgs a) {
     for (uint32_t w = 0; w < ATT_WAVES; ++w) top = fmaxf(top, wm[w * HEADS + threadIdx.x]);
     for (uint32_t w = 0; w < ATT_WAVES; ++w) {
       const float mw = wm[w * HEADS + threadIdx.x];
-      const float f = mw == -INFINITY ? 1.f : exp2f(mw - top);
+      const float f = mw == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(mw - top);
       wm[w * HEADS + threadIdx.x] = f;
       sum += f * wl[w * HEADS + threadIdx.x];
     }
@@ -313,7 +340,7 @@ __global__ __launch_bounds__(ATT_THREADS) void k_attend(AttArgs a) {
   float* srow = a.scores + b * a.ssb + h * a.ssh;
   for (uint32_t key = threadIdx.x; key < len; key += ATT_THREADS) {
     float sum = 0.f;
-    for (uint32_t i = 0; i < heads; ++i) sum += exp2f(a.logits[(first + i) * a.n + key] - wl[HEADS + i]) / wl[i];
+    for (uint32_t i = 0; i < heads; ++i) sum += __builtin_amdgcn_exp2f(a.logits[(first + i) * a.n + key] - wl[HEADS + i]) / wl[i];
     srow[key] += sum;
   }
 }
@@ -322,34 +349,56 @@ __global__ __launch_bounds__(ATT_THREADS) void k_attend(AttArgs a) {
 // output, the others add up JOIN_KEYS keys' probabilities each.
 template <class T>
 __global__ __launch_bounds__(JOIN_THREADS) void k_attend_join(AttArgs a, uint32_t outs, uint32_t chunks) {
-  extern __shared__ float shared[];   // scores: a maximum and the inverse of a sum for each head
+  // outputs: a factor for each split; scores: a maximum and the inverse of a sum for each head
+  extern __shared__ float shared[];
+  __shared__ float part[4][HEAD_MAX];
   const uint64_t id = block_id();
   if (id >= a.work) return;
-  const uint32_t part = (uint32_t)(id % (outs + chunks));
+  const uint32_t which = (uint32_t)(id % (outs + chunks));
   const uint64_t bh = id / (outs + chunks);
   const uint64_t b = bh / a.kv_heads, h = bh % a.kv_heads;
   const uint32_t len = length_of(a.lengths, b, a.n);
   const uint32_t live = (len + a.per - 1) / a.per;
   if (len == 0) return;   // the output is written, no weights are added
   const uint32_t wave = threadIdx.x / 64, lane = threadIdx.x % 64;
-  if (part < outs) {
-    const uint64_t head = bh * a.group + part;
+  if (which < outs) {
+    const uint64_t head = bh * a.group + which;
     const float* ml = a.ml + head * a.splits * 2;
-    float top = -INFINITY;
-    for (uint32_t s = 0; s < live; ++s) top = fmaxf(top, ml[2 * s]);
-    T* out = static_cast<T*>(a.out) + b * a.sob + (h * a.group + part) * a.soh;
-    for (uint32_t c = threadIdx.x; c < a.d; c += JOIN_THREADS) {
-      float sum = 0.f, v = 0.f;
-      for (uint32_t s = 0; s < live; ++s) {
-        const float f = exp2f(ml[2 * s] - top);
-        sum = fmaf(f, ml[2 * s + 1], sum);
-        v = fmaf(f, a.part[(head * a.splits + s) * a.d + c], v);
-      }
-      out[c] = from_f32<T>(v / sum);
+    float top = -INFINITY, sum = 0.f;     // every wave for itself
+    for (uint32_t s = lane; s < live; s += 64) top = fmaxf(top, ml[2 * s]);
+#pragma unroll
+    for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+    for (uint32_t s = lane; s < live; s += 64) {
+      const float f = __builtin_amdgcn_exp2f(ml[2 * s] - top);
+      sum = fmaf(f, ml[2 * s + 1], sum);
+      if (wave == 0) shared[s] = f;
     }
+    sum = wave_sum(sum);
+    __syncthreads();
+    // four waves share the splits, eight rows of theirs in flight; a lane has every 64th column
+    const float* rows = a.part + head * a.splits * a.d;
+    float v[HEAD_MAX / 64] = {};
+    for (uint32_t s0 = wave; s0 < live; s0 += 4 * 8) {
+#pragma unroll
+      for (uint32_t x = 0; x < HEAD_MAX / 64; ++x) {
+        const uint32_t c = x * 64 + lane;
+        if (x * 64 >= a.d) break;
+        float t[8];
+#pragma unroll
+        for (uint32_t i = 0; i < 8; ++i) t[i] = s0 + 4 * i < live && c < a.d ? rows[(uint64_t)(s0 + 4 * i) * a.d + c] : 0.f;
+#pragma unroll
+        for (uint32_t i = 0; i < 8; ++i) v[x] = fmaf(s0 + 4 * i < live ? shared[s0 + 4 * i] : 0.f, t[i], v[x]);
+      }
+    }
+#pragma unroll
+    for (uint32_t x = 0; x < HEAD_MAX / 64; ++x) part[wave][x * 64 + lane] = v[x];
+    __syncthreads();
+    T* out = static_cast<T*>(a.out) + b * a.sob + (h * a.group + which) * a.soh;
+    const uint32_t c = threadIdx.x;
+    if (c < a.d) out[c] = from_f32<T>(((part[0][c] + part[1][c]) + (part[2][c] + part[3][c])) / sum);
     return;
   }
-  const uint32_t k0 = (part - outs) * JOIN_KEYS;
+  const uint32_t k0 = (which - outs) * JOIN_KEYS;
   if (k0 >= len) return;
   for (uint32_t i = wave; i < a.group; i += JOIN_THREADS / 64) {
     const float* ml = a.ml + (bh * a.group + i) * a.splits * 2;
@@ -357,7 +406,7 @@ __global__ __launch_bounds__(JOIN_THREADS) void k_attend_join(AttArgs a, uint32_
     for (uint32_t s = lane; s < live; s += 64) top = fmaxf(top, ml[2 * s]);
 #pragma unroll
     for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
-    for (uint32_t s = lane; s < live; s += 64) sum = fmaf(exp2f(ml[2 * s] - top), ml[2 * s + 1], sum);
+    for (uint32_t s = lane; s < live; s += 64) sum = fmaf(__builtin_amdgcn_exp2f(ml[2 * s] - top), ml[2 * s + 1], sum);
     sum = wave_sum(sum);
     if (lane == 0) {
       shared[2 * i] = top;
@@ -365,14 +414,22 @@ __global__ __launch_bounds__(JOIN_THREADS) void k_attend_join(AttArgs a, uint32_
     }
   }
   __syncthreads();
+  constexpr uint32_t PER = JOIN_KEYS / JOIN_THREADS;
   float* srow = a.scores + b * a.ssb + h * a.ssh;
+  const float* rows = a.logits + bh * a.group * a.n;
+  float sum[PER] = {};
+  for (uint32_t i = 0; i < a.group; ++i) {
+    const float top = shared[2 * i], inv = shared[2 * i + 1];
 #pragma unroll
-  for (uint32_t x = 0; x < JOIN_KEYS / JOIN_THREADS; ++x) {
+    for (uint32_t x = 0; x < PER; ++x) {
+      const uint32_t key = k0 + x * JOIN_THREADS + threadIdx.x;
+      if (key < len) sum[x] = fmaf(__builtin_amdgcn_exp2f(rows[(uint64_t)i * a.n + key] - top), inv, sum[x]);
+    }
+  }
+#pragma unroll
+  for (uint32_t x = 0; x < PER; ++x) {
     const uint32_t key = k0 + x * JOIN_THREADS + threadIdx.x;
-    if (key >= len) break;
-    float sum = 0.f;
-    for (uint32_t i = 0; i < a.group; ++i) sum = fmaf(exp2f(a.logits[(bh * a.group + i) * a.n + key] - shared[2 * i]), shared[2 * i + 1], sum);
-    srow[key] += sum;
+    if (key < len) srow[key] += sum[x];
   }
 }
 
@@ -463,7 +520,7 @@ hipError_t attend_call(const topk_attend_args& in, const AttPlan& p, char* ws, h
   const uint32_t chunks = in.scores && (p.splits > 1 || p.blocks16 > 1) ? (a.n + JOIN_KEYS - 1) / JOIN_KEYS : 0;
   if (outs + chunks) {
     a.work = rows * (outs + chunks);
-    k_attend_join<T><<<wide_grid(a.work), JOIN_THREADS, a.group * 8, s>>>(a, outs, chunks);
+    k_attend_join<T><<<wide_grid(a.work), JOIN_THREADS, std::max(a.group * 8, a.splits * 4), s>>>(a, outs, chunks);
   }
   return hipGetLastError();
 }

@@ -26,6 +26,10 @@ hipError_t launch_combine_grad(const topk_combine_grad_args& a, void* ws, hipStr
 // Widest head of attend: its accumulators stay in registers.
 constexpr int64_t HEAD_MAX = 256;
 
+// Entries of attend's caches lie less than this many elements apart: a step's
+// rows are then within the range of a 32-bit offset in bytes.
+constexpr int64_t STEP_MAX = int64_t(1) << 24;
+
 size_t attend_workspace(const topk_attend_args& a, int cus);
 hipError_t launch_attend(const topk_attend_args& a, void* ws, int cus, hipStream_t s);
 

@@ -112,6 +112,7 @@ int check_attend(const topk_attend_args* a, bool pointers) {
     return TOPK_EINVAL;
   for (int64_t s : {a->sqb, a->sqh, a->skb, a->skh, a->skn, a->svb, a->svh, a->svn, a->ssb, a->ssh, a->sob, a->soh})
     if (bad_stride(s)) return TOPK_EINVAL;
+  if (a->n > 1 && (a->skn >= tk::STEP_MAX || a->svn >= tk::STEP_MAX)) return TOPK_EINVAL;
   if (overlapping(a->batch, a->sob, a->heads, a->soh, a->d)) return TOPK_EINVAL;
   if (a->scores && overlapping(a->batch, a->ssb, a->kv_heads, a->ssh, a->n)) return TOPK_EINVAL;
   if (!pointers) return TOPK_OK;
