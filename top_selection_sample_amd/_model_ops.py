@@ -19,6 +19,7 @@ from . import _lib
 from ._ops import _CODES, _check, _code, _gpu, _matrix, _no_tangents, _on, _ptr, _scratch, _stream, _wants_grad
 
 _byref = ctypes.byref
+_STEP_MAX = 1 << 24    # entries of a cache that attend reads in place lie less than this many elements apart
 _pack_dispatch = struct.Struct(_lib.DISPATCH_FORMAT).pack
 _pack_combine = struct.Struct(_lib.COMBINE_FORMAT).pack
 _pack_combine_grad = struct.Struct(_lib.COMBINE_GRAD_FORMAT).pack
@@ -253,6 +254,7 @@ def attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lengths: torch.Ten
     _, h, n, _ = k.shape
     _check(k, "k", q, (b, h, n, d))
     v = _cache(v, "v", q, (b, h, n, d))
+    k, v = (t if t.stride(2) < _STEP_MAX or n <= 1 else t.contiguous() for t in (k, v))
     if not 1 <= d <= 256 or h == 0 or hq % h or hq // h > 4096:
         raise ValueError(f"d: from 1 to 256; the heads of q a multiple of the cache's (up to 4096 times), not {hq} and {h}")
     lengths = _check_lengths(lengths, q, b)

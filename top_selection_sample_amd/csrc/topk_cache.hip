@@ -53,11 +53,12 @@ struct AttArgs {
   float* scores;      // null: not wanted
   void* out;
   float* logits;      // [batch * heads][n], in units of log 2; null: not wanted
-  float* part;        // [batch * heads][splits][d]
-  float* ml;          // [batch * heads][splits][2]: maximum and sum
+  float* part;        // [pieces][min(group, HEADS)][d]
+  float* ml;          // [pieces][HEADS][2]: maximum and sum
   int64_t sqb, sqh, skb, skh, skn, svb, svh, svn, ssb, ssh, sob, soh;
-  uint64_t work;      // workgroups
-  uint32_t kv_heads, group, blocks16, n, d, splits, per;   // per: keys of a split
+  uint64_t work;      // workgroups of the launch
+  uint32_t batch, kv_heads, group, blocks16, n, d;
+  uint32_t share;     // workgroups that share the keys; 0: each has a row to itself
   float scale2;
 };
 
@@ -92,291 +93,429 @@ __device__ __forceinline__ const T* at_offset(const T* base, uint32_t bytes) {
   return reinterpret_cast<const T*>(reinterpret_cast<const char*>(base) + bytes);
 }
 
+// The keys are shared out evenly, whatever the sequences' lengths: a sequence
+// is `rows` rows (a key-value head and up to 16 of its query heads) of units of
+// ATT_WAVES steps, all units of all sequences are numbered in that order, and
+// workgroup w of `share` (at most one a unit) has those from w * all / share on.
+// What it does of one row is a piece; row r of all and workgroup w make piece
+// r + w, for no two pieces have the same sum.
+struct Place {
+  uint64_t all;       // units of all sequences
+  uint64_t share;     // workgroups that have any
+  uint64_t before;    // those before sequence b
+  uint32_t b, units;  // the sequence, and the units of one of its rows
+};
+
+// a / b; a 64-bit division takes hundreds of instructions, and is seldom one.
+__device__ __forceinline__ uint64_t quotient(uint64_t a, uint64_t b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+
+template <uint32_t UNIT>
+__device__ __forceinline__ uint32_t units_of(const AttArgs& a, uint32_t b) {
+  return (length_of(a.lengths, b, a.n) + UNIT - 1) / UNIT;
+}
+
+// The sequence `want`, or where that is negative the one that the first unit of
+// workgroup ~want lies in.  Every wave for itself, a sequence to a lane.
+template <uint32_t UNIT>
+__device__ __forceinline__ Place place_of(const AttArgs& a, int64_t want) {
+  const uint32_t lane = threadIdx.x % 64, rows = a.kv_heads * a.blocks16;
+  Place p;
+  if (!a.lengths) {
+    p.units = (a.n + UNIT - 1) / UNIT;
+    const uint64_t each = (uint64_t)p.units * rows;
+    p.all = each * a.batch;
+    p.share = min((uint64_t)a.share, p.all);
+    p.b = want >= 0 ? (uint32_t)want : (uint32_t)quotient(quotient((uint64_t)~want * p.all, p.share), each);
+    p.before = p.b * each;
+    return p;
+  }
+  uint64_t all = 0, last = 0;     // `last`: of the last 64 sequences
+  uint32_t mine = 0;
+  for (uint32_t b0 = 0; b0 < a.batch; b0 += 64) {
+    mine = b0 + lane < a.batch ? units_of<UNIT>(a, b0 + lane) : 0u;
+    last = wave_sum((uint64_t)mine * rows);
+    all += last;
+  }
+  p.all = all;
+  p.share = min((uint64_t)a.share, all);
+  p.b = 0;
+  p.before = 0;
+  p.units = 0;
+  if (all == 0) return p;
+  const uint64_t unit = want >= 0 ? 0 : quotient((uint64_t)~want * all, p.share);
+  uint64_t base = 0;
+  for (uint32_t b0 = 0; b0 < a.batch; b0 += 64) {
+    if (a.batch > 64) mine = b0 + lane < a.batch ? units_of<UNIT>(a, b0 + lane) : 0u;
+    uint64_t up = (uint64_t)mine * rows;
+#pragma unroll
+    for (uint32_t o = 1; o < 64; o <<= 1) {
+      const uint64_t t = __shfl_up(up, o);
+      if (lane >= o) up += t;
+    }
+    const uint64_t hit = want >= 0 ? __ballot(b0 + lane == (uint64_t)want) : __ballot(base + up > unit);
+    if (hit) {
+      const int x = __builtin_ctzll(hit);
+      p.b = b0 + (uint32_t)x;
+      p.units = __shfl(mine, x);
+      p.before = base + __shfl(up, x) - (uint64_t)p.units * rows;
+      break;
+    }
+    base += __shfl(up, 63);
+  }
+  return p;
+}
+
 // KC: chunks of a key's columns; VB: blocks of 16 * VW columns of V.
 template <class T, uint32_t KC, uint32_t VB, uint32_t VW, bool NARROW>
 __global__ __launch_bounds__(ATT_THREADS, KC * VB > 8 ? 1 : 2) void k_attend(AttArgs a) {
   typedef Att<T> C;
   constexpr uint32_t TILES = C::STEP / 16, KEYS = TILES * 4;   // KEYS: a lane's keys of a step
+  constexpr uint32_t UNIT = ATT_WAVES * C::STEP;
   extern __shared__ float shared[];
   const uint64_t id = block_id();
   if (id >= a.work) return;
-  const uint32_t split = (uint32_t)(id % a.splits);
-  const uint64_t rest = id / a.splits;
-  const uint32_t hb = (uint32_t)(rest % a.blocks16);
-  const uint64_t bh = rest / a.blocks16;
-  const uint64_t b = bh / a.kv_heads, h = bh % a.kv_heads;
-  const uint32_t len = length_of(a.lengths, b, a.n);
-  const uint32_t s0 = split * a.per;
-  const uint32_t h0 = hb * HEADS, heads = min(HEADS, a.group - h0);   // of this workgroup
-  const uint32_t d = a.d;
-  const uint64_t first = bh * a.group + h0;                           // its first head, of all
-  T* out = static_cast<T*>(a.out) + b * a.sob + (h * a.group + h0) * a.soh;
-  if (s0 >= len) {
-    if (len == 0 && split == 0)
-      for (uint32_t i = threadIdx.x; i < heads * d; i += ATT_THREADS) out[(uint64_t)(i / d) * a.soh + i % d] = from_f32<T>(0.f);
-    return;
-  }
-  const uint32_t s1 = len - s0 < a.per ? len : s0 + a.per;
+  const uint32_t rows = a.kv_heads * a.blocks16, d = a.d;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const uint32_t lane = threadIdx.x % 64, col = lane % 16, g = lane / 16;
-  const bool mine = col < heads;
-  const T* qrow = static_cast<const T*>(a.q) + b * a.sqb + (h * a.group + h0 + (mine ? col : 0)) * a.sqh;
-
-  // Q as the second operand.  A row's last vector begins earlier, so that it
-  // ends with the row: what the vector before it has is 0 here.
-  typename C::Frag q[KC];
-  uint32_t kcol[KC], vcol[VB];
-#pragma unroll
-  for (uint32_t c = 0; c < KC; ++c) {
-    const uint32_t want = c * C::KCHUNK + g * C::KVEC;
-    kcol[c] = NARROW ? want : min(want, d - C::KVEC);
-    T t[C::KVEC];
-    load_cols<T, C::KVEC, NARROW>(qrow + kcol[c], kcol[c], d, t);
-#pragma unroll
-    for (uint32_t i = 0; i < C::KVEC; ++i)
-      if (!mine || kcol[c] + i < want) t[i] = T{};
-    __builtin_memcpy(&q[c], t, sizeof(q[c]));
-  }
-#pragma unroll
-  for (uint32_t x = 0; x < VB; ++x) {
-    const uint32_t want = x * 16 * VW + col * VW;
-    vcol[x] = NARROW ? want : min(want, d - VW);
-  }
-  f32x4 o[VB][VW];
-#pragma unroll
-  for (uint32_t x = 0; x < VB; ++x)
-#pragma unroll
-    for (uint32_t j = 0; j < VW; ++j) o[x][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  float m = -INFINITY, l = 0.f;   // of head `col`: m alike in the four lanes that share it, l of this lane's keys
-  float* logit_row = a.logits ? a.logits + (first + (mine ? col : 0)) * a.n : nullptr;
-
-  const uint32_t ldk = (uint32_t)a.skn * (uint32_t)sizeof(T), ldv = (uint32_t)a.svn * (uint32_t)sizeof(T);
-  uint32_t base = s0 + wave * C::STEP;
-  const T* kbase = static_cast<const T*>(a.k) + b * a.skb + h * a.skh + (int64_t)base * a.skn;
-  const T* vbase = static_cast<const T*>(a.v) + b * a.svb + h * a.svh + (int64_t)base * a.svn;
-  // This lane's place of key i of a step: the order in which S holds them.
-  auto key_of = [&](uint32_t i) { return (i / 4) * 16 + g * 4 + i % 4; };
-
-  // The step's keys; a step that the sequence does not fill reads its last row again.
-  T kv[TILES][KC][C::KVEC];
-  auto load_keys = [&](uint32_t have) {
-    const uint32_t last = min(have, C::STEP) - 1;
-#pragma unroll
-    for (uint32_t t = 0; t < TILES; ++t) {
-      const uint32_t row = min(t * 16 + col, last) * ldk;
-#pragma unroll
-      for (uint32_t c = 0; c < KC; ++c)
-        load_cols<T, C::KVEC, NARROW>(at_offset(kbase, row + kcol[c] * (uint32_t)sizeof(T)), kcol[c], d, kv[t][c]);
-    }
-  };
-  if (base < s1) load_keys(s1 - base);
-  for (; base < s1; base += ATT_WAVES * C::STEP) {
-    const uint32_t have = s1 - base;
-    const bool tail = have < C::STEP;
-    T vv[KEYS][VB][VW];
-#pragma unroll
-    for (uint32_t i = 0; i < KEYS; ++i) {
-      const uint32_t row = min(key_of(i), have - 1) * ldv;
-#pragma unroll
-      for (uint32_t x = 0; x < VB; ++x)
-        load_cols<T, VW, NARROW>(at_offset(vbase, row + vcol[x] * (uint32_t)sizeof(T)), vcol[x], d, vv[i][x]);
-    }
-    vbase += (int64_t)(ATT_WAVES * C::STEP) * a.svn;
-    float s[KEYS];
-#pragma unroll
-    for (uint32_t t = 0; t < TILES; ++t) {
-      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (uint32_t c = 0; c < KC; ++c) {
-        typename C::Frag kf;
-        __builtin_memcpy(&kf, kv[t][c], sizeof(kf));
-        if constexpr (sizeof(T) == 2) {
-          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, q[c], acc, 0, 0, 0);
-        } else {
-#pragma unroll
-          for (uint32_t j = 0; j < 4; ++j) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(kf[j], q[c][j], acc, 0, 0, 0);
-        }
-      }
-#pragma unroll
-      for (uint32_t r = 0; r < 4; ++r) s[t * 4 + r] = acc[r] * a.scale2;
-    }
-    // the next step's keys are on their way while this one's values are used
-    kbase += (int64_t)(ATT_WAVES * C::STEP) * a.skn;
-    if (have > ATT_WAVES * C::STEP) load_keys(have - ATT_WAVES * C::STEP);
-    if (logit_row && mine) {
-      if (!tail) {
-#pragma unroll
-        for (uint32_t t = 0; t < TILES; ++t) __builtin_memcpy(logit_row + base + t * 16 + g * 4, s + t * 4, 16);
-      } else {
-#pragma unroll
-        for (uint32_t i = 0; i < KEYS; ++i)
-          if (key_of(i) < have) logit_row[base + key_of(i)] = s[i];
-      }
-    }
-    if (tail) {   // what the last row was read for once more does not count
-#pragma unroll
-      for (uint32_t i = 0; i < KEYS; ++i) {
-        const bool in = key_of(i) < have;
-        s[i] = in ? s[i] : -INFINITY;
-#pragma unroll
-        for (uint32_t x = 0; x < VB; ++x)
-#pragma unroll
-          for (uint32_t j = 0; j < VW; ++j)
-            if (!in) vv[i][x][j] = T{};   // not 0 * inf
-      }
-    }
-    float top = s[0];
-#pragma unroll
-    for (uint32_t i = 1; i < KEYS; ++i) top = fmaxf(top, s[i]);
-    if (__any(top > m)) {
-      top = fmaxf(top, __shfl_xor(top, 16));
-      top = fmaxf(top, __shfl_xor(top, 32));
-      const float now = fmaxf(m, top);
-      const float down = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - now);
-      l *= down;
-      m = now;
-#pragma unroll
-      for (uint32_t r = 0; r < 4; ++r) {
-        const float f = __shfl(down, (int)(g * 4 + r));
-#pragma unroll
-        for (uint32_t x = 0; x < VB; ++x)
-#pragma unroll
-          for (uint32_t j = 0; j < VW; ++j) o[x][j][r] *= f;
-      }
-    }
-    const float ref = m == -INFINITY ? 0.f : m;
-    float p[KEYS];
-#pragma unroll
-    for (uint32_t i = 0; i < KEYS; ++i) {
-      p[i] = __builtin_amdgcn_exp2f(s[i] - ref);
-      l += p[i];
-    }
-    if constexpr (sizeof(T) == 2) {
-      const u32x4 pk = Vec<bf16_t>::pack(p);
-      bf16x8 pf;
-      __builtin_memcpy(&pf, &pk, 16);
-#pragma unroll
-      for (uint32_t x = 0; x < VB; ++x)
-#pragma unroll
-        for (uint32_t j = 0; j < VW; ++j) {
-          u32x4 w;
-#pragma unroll
-          for (uint32_t i = 0; i < 4; ++i) {
-            uint32_t lo, hi;   // two columns of two rows
-            __builtin_memcpy(&lo, &vv[2 * i][x][j & ~1u], 4);
-            __builtin_memcpy(&hi, &vv[2 * i + 1][x][j & ~1u], 4);
-            w[i] = __builtin_amdgcn_perm(hi, lo, j & 1 ? 0x07060302u : 0x05040100u);
-          }
-          bf16x8 vf;
-          __builtin_memcpy(&vf, &w, 16);
-          o[x][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf, vf, o[x][j], 0, 0, 0);
-        }
-    } else {
-#pragma unroll
-      for (uint32_t i = 0; i < 4; ++i)
-#pragma unroll
-        for (uint32_t x = 0; x < VB; ++x)
-#pragma unroll
-          for (uint32_t j = 0; j < VW; ++j) o[x][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(p[i], to_f32(vv[i][x][j]), o[x][j], 0, 0, 0);
+  uint64_t todo;           // units of this workgroup that are left
+  uint32_t b, row, unit;   // where they begin
+  uint32_t units;
+  if (a.share) {
+    const Place p = place_of<UNIT>(a, ~(int64_t)id);
+    if (id >= p.share) return;
+    const uint64_t from = quotient(id * p.all, p.share);
+    todo = quotient((id + 1) * p.all, p.share) - from;
+    b = p.b;
+    units = p.units;
+    row = (uint32_t)quotient(from - p.before, units);
+    unit = (uint32_t)(from - p.before - (uint64_t)row * units);
+  } else {
+    b = (uint32_t)quotient(id, rows);
+    row = (uint32_t)(id - (uint64_t)b * rows);
+    unit = 0;
+    units = units_of<UNIT>(a, b);
+    todo = units;
+    if (!todo) {
+      const uint32_t h = row / a.blocks16, h0 = row % a.blocks16 * HEADS;
+      T* out = static_cast<T*>(a.out) + (uint64_t)b * a.sob + (uint64_t)(h * a.group + h0) * a.soh;
+      for (uint32_t i = threadIdx.x; i < min(HEADS, a.group - h0) * d; i += ATT_THREADS) out[(uint64_t)(i / d) * a.soh + i % d] = from_f32<T>(0.f);
+      return;
     }
   }
-  l += __shfl_xor(l, 16);
-  l += __shfl_xor(l, 32);
+  for (;;) {
+    const uint32_t len = length_of(a.lengths, b, a.n);
+    const uint32_t now_units = todo < units - unit ? (uint32_t)todo : units - unit;
+    const uint32_t s0 = unit * UNIT, s1 = unit + now_units == units ? len : s0 + now_units * UNIT;
+    const uint32_t h = row / a.blocks16, h0 = row % a.blocks16 * HEADS;
+    const uint32_t heads = min(HEADS, a.group - h0);                    // of this row
+    const uint64_t bh = (uint64_t)b * a.kv_heads + h;
+    const uint64_t first = bh * a.group + h0;                           // its first head, of all
+    T* out = static_cast<T*>(a.out) + (uint64_t)b * a.sob + (uint64_t)(h * a.group + h0) * a.soh;
+    const bool mine = col < heads;
+    const T* qrow = static_cast<const T*>(a.q) + (uint64_t)b * a.sqb + (uint64_t)(h * a.group + h0 + (mine ? col : 0)) * a.sqh;
 
-  // the waves' parts through LDS: [wave][head][d], then (m, l) of each
-  float* wo = shared;
-  float* wm = shared + ATT_WAVES * heads * d;
-  float* wl = wm + ATT_WAVES * HEADS;
-  if (g == 0) {
-    wm[wave * HEADS + col] = m;
-    wl[wave * HEADS + col] = l;
-  }
+    // Q as the second operand.  A row's last vector begins earlier, so that it
+    // ends with the row: what the vector before it has is 0 here.
+    typename C::Frag q[KC];
+    uint32_t kcol[KC], vcol[VB];
 #pragma unroll
-  for (uint32_t r = 0; r < 4; ++r) {
-    const uint32_t head = g * 4 + r;
-    if (head >= heads) continue;
-    float* row = wo + (wave * heads + head) * d;
+    for (uint32_t c = 0; c < KC; ++c) {
+      const uint32_t want = c * C::KCHUNK + g * C::KVEC;
+      kcol[c] = NARROW ? want : min(want, d - C::KVEC);
+      T t[C::KVEC];
+      load_cols<T, C::KVEC, NARROW>(qrow + kcol[c], kcol[c], d, t);
+#pragma unroll
+      for (uint32_t i = 0; i < C::KVEC; ++i)
+        if (!mine || kcol[c] + i < want) t[i] = T{};
+      __builtin_memcpy(&q[c], t, sizeof(q[c]));
+    }
+#pragma unroll
+    for (uint32_t x = 0; x < VB; ++x) {
+      const uint32_t want = x * 16 * VW + col * VW;
+      vcol[x] = NARROW ? want : min(want, d - VW);
+    }
+    f32x4 o[VB][VW];
 #pragma unroll
     for (uint32_t x = 0; x < VB; ++x)
 #pragma unroll
-      for (uint32_t j = 0; j < VW; ++j)
-        if (!NARROW || vcol[x] + j < d) row[vcol[x] + j] = o[x][j][r];
-  }
-  __syncthreads();
-  if (threadIdx.x < HEADS) {   // one maximum and sum for the workgroup; the waves' factors in place of their maxima
-    float top = -INFINITY, sum = 0.f;
-    for (uint32_t w = 0; w < ATT_WAVES; ++w) top = fmaxf(top, wm[w * HEADS + threadIdx.x]);
-    for (uint32_t w = 0; w < ATT_WAVES; ++w) {
-      const float mw = wm[w * HEADS + threadIdx.x];
-      const float f = mw == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(mw - top);
-      wm[w * HEADS + threadIdx.x] = f;
-      sum += f * wl[w * HEADS + threadIdx.x];
-    }
-    wl[threadIdx.x] = sum;
-    wl[HEADS + threadIdx.x] = top == -INFINITY ? 0.f : top;
-  }
-  __syncthreads();
-  const bool alone = a.splits == 1;
-  for (uint32_t i = threadIdx.x; i < heads * d; i += ATT_THREADS) {
-    const uint32_t head = i / d, c = i % d;
-    float v = 0.f;
+      for (uint32_t j = 0; j < VW; ++j) o[x][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float m = -INFINITY, l = 0.f;   // of head `col`: m alike in the four lanes that share it, l of this lane's keys
+    float* logit_row = a.logits ? a.logits + (first + (mine ? col : 0)) * a.n : nullptr;
+
+    const uint32_t ldk = (uint32_t)a.skn * (uint32_t)sizeof(T), ldv = (uint32_t)a.svn * (uint32_t)sizeof(T);
+    uint32_t base = s0 + wave * C::STEP;
+    const T* kbase = static_cast<const T*>(a.k) + (int64_t)b * a.skb + (int64_t)h * a.skh + (int64_t)base * a.skn;
+    const T* vbase = static_cast<const T*>(a.v) + (int64_t)b * a.svb + (int64_t)h * a.svh + (int64_t)base * a.svn;
+    // This lane's place of key i of a step: the order in which S holds them.
+    auto key_of = [&](uint32_t i) { return (i / 4) * 16 + g * 4 + i % 4; };
+
+    // The step's keys; a step that the sequence does not fill reads its last row again.
+    T kv[TILES][KC][C::KVEC];
+    auto load_keys = [&](uint32_t have) {
+      const uint32_t last = min(have, C::STEP) - 1;
 #pragma unroll
-    for (uint32_t w = 0; w < ATT_WAVES; ++w) v = fmaf(wm[w * HEADS + head], wo[(w * heads + head) * d + c], v);
-    if (alone) out[(uint64_t)head * a.soh + c] = from_f32<T>(v / wl[head]);
-    else a.part[((first + head) * a.splits + split) * d + c] = v;
-  }
-  if (!alone || a.blocks16 > 1) {
-    if (threadIdx.x < heads) {
-      float* ml = a.ml + ((first + threadIdx.x) * a.splits + split) * 2;
-      ml[0] = wl[HEADS + threadIdx.x];
-      ml[1] = wl[threadIdx.x];
+      for (uint32_t t = 0; t < TILES; ++t) {
+        const uint32_t row = min(t * 16 + col, last) * ldk;
+#pragma unroll
+        for (uint32_t c = 0; c < KC; ++c)
+          load_cols<T, C::KVEC, NARROW>(at_offset(kbase, row + kcol[c] * (uint32_t)sizeof(T)), kcol[c], d, kv[t][c]);
+      }
+    };
+    if (base < s1) load_keys(s1 - base);
+    for (; base < s1; base += UNIT) {
+      const uint32_t have = s1 - base;
+      const bool tail = have < C::STEP;
+      T vv[KEYS][VB][VW];
+#pragma unroll
+      for (uint32_t i = 0; i < KEYS; ++i) {
+        const uint32_t row = min(key_of(i), have - 1) * ldv;
+#pragma unroll
+        for (uint32_t x = 0; x < VB; ++x)
+          load_cols<T, VW, NARROW>(at_offset(vbase, row + vcol[x] * (uint32_t)sizeof(T)), vcol[x], d, vv[i][x]);
+      }
+      vbase += (int64_t)UNIT * a.svn;
+      float s[KEYS];
+#pragma unroll
+      for (uint32_t t = 0; t < TILES; ++t) {
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (uint32_t c = 0; c < KC; ++c) {
+          typename C::Frag kf;
+          __builtin_memcpy(&kf, kv[t][c], sizeof(kf));
+          if constexpr (sizeof(T) == 2) {
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, q[c], acc, 0, 0, 0);
+          } else {
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(kf[j], q[c][j], acc, 0, 0, 0);
+          }
+        }
+#pragma unroll
+        for (uint32_t r = 0; r < 4; ++r) s[t * 4 + r] = acc[r] * a.scale2;
+      }
+      // the next step's keys are on their way while this one's values are used
+      kbase += (int64_t)UNIT * a.skn;
+      if (have > UNIT) load_keys(have - UNIT);
+      if (logit_row && mine) {
+        if (!tail) {
+#pragma unroll
+          for (uint32_t t = 0; t < TILES; ++t) __builtin_memcpy(logit_row + base + t * 16 + g * 4, s + t * 4, 16);
+        } else {
+#pragma unroll
+          for (uint32_t i = 0; i < KEYS; ++i)
+            if (key_of(i) < have) logit_row[base + key_of(i)] = s[i];
+        }
+      }
+      if (tail) {   // what the last row was read for once more does not count
+#pragma unroll
+        for (uint32_t i = 0; i < KEYS; ++i) {
+          const bool in = key_of(i) < have;
+          s[i] = in ? s[i] : -INFINITY;
+#pragma unroll
+          for (uint32_t x = 0; x < VB; ++x)
+#pragma unroll
+            for (uint32_t j = 0; j < VW; ++j)
+              if (!in) vv[i][x][j] = T{};   // not 0 * inf
+        }
+      }
+      float top = s[0];
+#pragma unroll
+      for (uint32_t i = 1; i < KEYS; ++i) top = fmaxf(top, s[i]);
+      if (__any(top > m)) {
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float now = fmaxf(m, top);
+        const float down = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - now);
+        l *= down;
+        m = now;
+#pragma unroll
+        for (uint32_t r = 0; r < 4; ++r) {
+          const float f = __shfl(down, (int)(g * 4 + r));
+#pragma unroll
+          for (uint32_t x = 0; x < VB; ++x)
+#pragma unroll
+            for (uint32_t j = 0; j < VW; ++j) o[x][j][r] *= f;
+        }
+      }
+      const float ref = m == -INFINITY ? 0.f : m;
+      float p[KEYS];
+#pragma unroll
+      for (uint32_t i = 0; i < KEYS; ++i) {
+        p[i] = __builtin_amdgcn_exp2f(s[i] - ref);
+        l += p[i];
+      }
+      if constexpr (sizeof(T) == 2) {
+        const u32x4 pk = Vec<bf16_t>::pack(p);
+        bf16x8 pf;
+        __builtin_memcpy(&pf, &pk, 16);
+#pragma unroll
+        for (uint32_t x = 0; x < VB; ++x)
+#pragma unroll
+          for (uint32_t j = 0; j < VW; ++j) {
+            u32x4 w;
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i) {
+              uint32_t lo, hi;   // two columns of two rows
+              __builtin_memcpy(&lo, &vv[2 * i][x][j & ~1u], 4);
+              __builtin_memcpy(&hi, &vv[2 * i + 1][x][j & ~1u], 4);
+              w[i] = __builtin_amdgcn_perm(hi, lo, j & 1 ? 0x07060302u : 0x05040100u);
+            }
+            bf16x8 vf;
+            __builtin_memcpy(&vf, &w, 16);
+            o[x][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf, vf, o[x][j], 0, 0, 0);
+          }
+      } else {
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i)
+#pragma unroll
+          for (uint32_t x = 0; x < VB; ++x)
+#pragma unroll
+            for (uint32_t j = 0; j < VW; ++j) o[x][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(p[i], to_f32(vv[i][x][j]), o[x][j], 0, 0, 0);
+      }
     }
-    return;
-  }
-  if (!a.scores) return;
-  // the whole row was this workgroup's: its logits, just written, become probabilities
-  __threadfence_block();
-  __syncthreads();
-  float* srow = a.scores + b * a.ssb + h * a.ssh;
-  for (uint32_t key = threadIdx.x; key < len; key += ATT_THREADS) {
-    float sum = 0.f;
-    for (uint32_t i = 0; i < heads; ++i) sum += __builtin_amdgcn_exp2f(a.logits[(first + i) * a.n + key] - wl[HEADS + i]) / wl[i];
-    srow[key] += sum;
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+
+    // the waves' parts through LDS: [wave][head][d], then (m, l) of each
+    float* wo = shared;
+    float* wm = shared + ATT_WAVES * heads * d;
+    float* wl = wm + ATT_WAVES * HEADS;
+    if (g == 0) {
+      wm[wave * HEADS + col] = m;
+      wl[wave * HEADS + col] = l;
+    }
+#pragma unroll
+    for (uint32_t r = 0; r < 4; ++r) {
+      const uint32_t head = g * 4 + r;
+      if (head >= heads) continue;
+      float* row = wo + (wave * heads + head) * d;
+#pragma unroll
+      for (uint32_t x = 0; x < VB; ++x)
+#pragma unroll
+        for (uint32_t j = 0; j < VW; ++j)
+          if (!NARROW || vcol[x] + j < d) row[vcol[x] + j] = o[x][j][r];
+    }
+    __syncthreads();
+    if (threadIdx.x < HEADS) {   // one maximum and sum for the workgroup; the waves' factors in place of their maxima
+      float top = -INFINITY, sum = 0.f;
+      for (uint32_t w = 0; w < ATT_WAVES; ++w) top = fmaxf(top, wm[w * HEADS + threadIdx.x]);
+      for (uint32_t w = 0; w < ATT_WAVES; ++w) {
+        const float mw = wm[w * HEADS + threadIdx.x];
+        const float f = mw == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(mw - top);
+        wm[w * HEADS + threadIdx.x] = f;
+        sum += f * wl[w * HEADS + threadIdx.x];
+      }
+      wl[threadIdx.x] = sum;
+      wl[HEADS + threadIdx.x] = top == -INFINITY ? 0.f : top;
+    }
+    __syncthreads();
+    const uint64_t piece = (uint64_t)b * rows + row + id;
+    for (uint32_t i = threadIdx.x; i < heads * d; i += ATT_THREADS) {
+      const uint32_t head = i / d, c = i % d;
+      float v = 0.f;
+#pragma unroll
+      for (uint32_t w = 0; w < ATT_WAVES; ++w) v = fmaf(wm[w * HEADS + head], wo[(w * heads + head) * d + c], v);
+      if (!a.share) out[(uint64_t)head * a.soh + c] = from_f32<T>(v / wl[head]);
+      else a.part[(piece * min(HEADS, a.group) + head) * d + c] = v;
+    }
+    if (a.share) {
+      if (threadIdx.x < heads) {
+        float* ml = a.ml + (piece * HEADS + threadIdx.x) * 2;
+        ml[0] = wl[HEADS + threadIdx.x];
+        ml[1] = wl[threadIdx.x];
+      }
+    } else if (a.scores) {
+      // the whole row was this workgroup's: its logits, just written, become
+      // probabilities (there is one row to a key-value head here)
+      __threadfence_block();
+      __syncthreads();
+      float* srow = a.scores + (int64_t)b * a.ssb + (int64_t)h * a.ssh;
+      for (uint32_t key = threadIdx.x; key < len; key += ATT_THREADS) {
+        float sum = 0.f;
+        for (uint32_t i = 0; i < heads; ++i) sum += __builtin_amdgcn_exp2f(a.logits[(first + i) * a.n + key] - wl[HEADS + i]) / wl[i];
+        srow[key] += sum;
+      }
+    }
+    todo -= now_units;
+    if (!todo) return;
+    __syncthreads();   // the next piece writes LDS again
+    unit = 0;
+    if (++row == rows) {
+      row = 0;
+      do units = units_of<UNIT>(a, ++b);
+      while (!units);    // as long as units are left there is a sequence that has them
+    }
   }
 }
 
-// The splits' parts of a key-value head: workgroups below `group` write a head's
+// The pieces of a key-value head joined: workgroups below `group` write a head's
 // output, the others add up JOIN_KEYS keys' probabilities each.
 template <class T>
-__global__ __launch_bounds__(JOIN_THREADS) void k_attend_join(AttArgs a, uint32_t outs, uint32_t chunks) {
-  // outputs: a factor for each split; scores: a maximum and the inverse of a sum for each head
+__global__ __launch_bounds__(JOIN_THREADS) void k_attend_join(AttArgs a, uint32_t chunks) {
+  // outputs: a factor for each piece; scores: a maximum and the inverse of a sum for each head
   extern __shared__ float shared[];
   __shared__ float part[4][HEAD_MAX];
+  constexpr uint32_t UNIT = ATT_WAVES * Att<T>::STEP;
+  constexpr uint32_t PER = JOIN_KEYS / JOIN_THREADS, AHEAD = 4;
   const uint64_t id = block_id();
   if (id >= a.work) return;
-  const uint32_t which = (uint32_t)(id % (outs + chunks));
-  const uint64_t bh = id / (outs + chunks);
-  const uint64_t b = bh / a.kv_heads, h = bh % a.kv_heads;
+  const uint64_t bh = quotient(id, a.group + chunks);
+  const uint32_t which = (uint32_t)(id - bh * (a.group + chunks));
+  const uint32_t b = (uint32_t)quotient(bh, a.kv_heads), h = (uint32_t)(bh - (uint64_t)b * a.kv_heads);
   const uint32_t len = length_of(a.lengths, b, a.n);
-  const uint32_t live = (len + a.per - 1) / a.per;
-  if (len == 0) return;   // the output is written, no weights are added
   const uint32_t wave = threadIdx.x / 64, lane = threadIdx.x % 64;
-  if (which < outs) {
-    const uint64_t head = bh * a.group + which;
-    const float* ml = a.ml + head * a.splits * 2;
-    float top = -INFINITY, sum = 0.f;     // every wave for itself
-    for (uint32_t s = lane; s < live; s += 64) top = fmaxf(top, ml[2 * s]);
+  T* out = static_cast<T*>(a.out) + (int64_t)b * a.sob + (int64_t)(h * a.group + which) * a.soh;
+  if (len == 0) {
+    if (which < a.group)
+      for (uint32_t c = threadIdx.x; c < a.d; c += JOIN_THREADS) out[c] = from_f32<T>(0.f);
+    return;
+  }
+  const uint32_t k0 = (which - a.group) * JOIN_KEYS;
+  if (which >= a.group && k0 >= len) return;
+  // the first heads' logits are on their way while the pieces are looked up
+  const float* logits = a.logits + bh * a.group * a.n + k0;
+  float* srow = a.scores + (int64_t)b * a.ssb + (int64_t)h * a.ssh + k0;
+  float ahead[AHEAD][PER], sum[PER];
+  if (which >= a.group) {
+#pragma unroll
+    for (uint32_t x = 0; x < PER; ++x) {
+      const uint32_t key = x * JOIN_THREADS + threadIdx.x;
+      sum[x] = 0.f;
+#pragma unroll
+      for (uint32_t i = 0; i < AHEAD; ++i) ahead[i][x] = i < a.group && k0 + key < len ? logits[(uint64_t)i * a.n + key] : 0.f;
+    }
+  }
+  const Place p = place_of<UNIT>(a, b);
+  const uint32_t rows = a.kv_heads * a.blocks16;
+  auto owner = [&](uint64_t unit) { return quotient((unit + 1) * p.share + p.all - 1, p.all) - 1; };
+  // first and number of the pieces of a row of this head
+  auto pieces_of = [&](uint32_t hb, uint64_t* from) {
+    const uint32_t row = h * a.blocks16 + hb;
+    const uint64_t u0 = p.before + (uint64_t)row * p.units;
+    const uint64_t w0 = owner(u0), w1 = owner(u0 + p.units - 1);
+    *from = (uint64_t)b * rows + row + w0;
+    return (uint32_t)(w1 - w0 + 1);
+  };
+  if (which < a.group) {
+    uint64_t from;
+    const uint32_t live = pieces_of(which / HEADS, &from);
+    const float* ml = a.ml + (from * HEADS + which % HEADS) * 2;
+    float top = -INFINITY, whole = 0.f;     // every wave for itself
+    for (uint32_t s = lane; s < live; s += 64) top = fmaxf(top, ml[s * HEADS * 2]);
 #pragma unroll
     for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
     for (uint32_t s = lane; s < live; s += 64) {
-      const float f = __builtin_amdgcn_exp2f(ml[2 * s] - top);
-      sum = fmaf(f, ml[2 * s + 1], sum);
+      const float f = __builtin_amdgcn_exp2f(ml[s * HEADS * 2] - top);
+      whole = fmaf(f, ml[s * HEADS * 2 + 1], whole);
       if (wave == 0) shared[s] = f;
     }
-    sum = wave_sum(sum);
+    whole = wave_sum(whole);
     __syncthreads();
-    // four waves share the splits, eight rows of theirs in flight; a lane has every 64th column
-    const float* rows = a.part + head * a.splits * a.d;
+    // four waves share the pieces, eight rows of theirs in flight; a lane has every 64th column
+    const uint64_t step = (uint64_t)min(HEADS, a.group) * a.d;
+    const float* rows_of = a.part + from * step + which % HEADS * a.d;
     float v[HEAD_MAX / 64] = {};
     for (uint32_t s0 = wave; s0 < live; s0 += 4 * 8) {
 #pragma unroll
@@ -385,7 +524,7 @@ __global__ __launch_bounds__(JOIN_THREADS) void k_attend_join(AttArgs a, uint32_
         if (x * 64 >= a.d) break;
         float t[8];
 #pragma unroll
-        for (uint32_t i = 0; i < 8; ++i) t[i] = s0 + 4 * i < live && c < a.d ? rows[(uint64_t)(s0 + 4 * i) * a.d + c] : 0.f;
+        for (uint32_t i = 0; i < 8; ++i) t[i] = s0 + 4 * i < live && c < a.d ? rows_of[(s0 + 4 * i) * step + c] : 0.f;
 #pragma unroll
         for (uint32_t i = 0; i < 8; ++i) v[x] = fmaf(s0 + 4 * i < live ? shared[s0 + 4 * i] : 0.f, t[i], v[x]);
       }
@@ -393,73 +532,75 @@ __global__ __launch_bounds__(JOIN_THREADS) void k_attend_join(AttArgs a, uint32_
 #pragma unroll
     for (uint32_t x = 0; x < HEAD_MAX / 64; ++x) part[wave][x * 64 + lane] = v[x];
     __syncthreads();
-    T* out = static_cast<T*>(a.out) + b * a.sob + (h * a.group + which) * a.soh;
     const uint32_t c = threadIdx.x;
-    if (c < a.d) out[c] = from_f32<T>(((part[0][c] + part[1][c]) + (part[2][c] + part[3][c])) / sum);
+    if (c < a.d) out[c] = from_f32<T>(((part[0][c] + part[1][c]) + (part[2][c] + part[3][c])) / whole);
     return;
   }
-  const uint32_t k0 = (which - outs) * JOIN_KEYS;
-  if (k0 >= len) return;
   for (uint32_t i = wave; i < a.group; i += JOIN_THREADS / 64) {
-    const float* ml = a.ml + (bh * a.group + i) * a.splits * 2;
-    float top = -INFINITY, sum = 0.f;
-    for (uint32_t s = lane; s < live; s += 64) top = fmaxf(top, ml[2 * s]);
+    uint64_t from;
+    const uint32_t live = pieces_of(i / HEADS, &from);
+    const float* ml = a.ml + (from * HEADS + i % HEADS) * 2;
+    float top = -INFINITY, whole = 0.f;
+    for (uint32_t s = lane; s < live; s += 64) top = fmaxf(top, ml[s * HEADS * 2]);
 #pragma unroll
     for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
-    for (uint32_t s = lane; s < live; s += 64) sum = fmaf(__builtin_amdgcn_exp2f(ml[2 * s] - top), ml[2 * s + 1], sum);
-    sum = wave_sum(sum);
+    for (uint32_t s = lane; s < live; s += 64) whole = fmaf(__builtin_amdgcn_exp2f(ml[s * HEADS * 2] - top), ml[s * HEADS * 2 + 1], whole);
+    whole = wave_sum(whole);
     if (lane == 0) {
       shared[2 * i] = top;
-      shared[2 * i + 1] = 1.f / sum;
+      shared[2 * i + 1] = 1.f / whole;
     }
   }
   __syncthreads();
-  constexpr uint32_t PER = JOIN_KEYS / JOIN_THREADS;
-  float* srow = a.scores + b * a.ssb + h * a.ssh;
-  const float* rows = a.logits + bh * a.group * a.n;
-  float sum[PER] = {};
-  for (uint32_t i = 0; i < a.group; ++i) {
-    const float top = shared[2 * i], inv = shared[2 * i + 1];
+  for (uint32_t i0 = 0; i0 < a.group; i0 += AHEAD) {
 #pragma unroll
-    for (uint32_t x = 0; x < PER; ++x) {
-      const uint32_t key = k0 + x * JOIN_THREADS + threadIdx.x;
-      if (key < len) sum[x] = fmaf(__builtin_amdgcn_exp2f(rows[(uint64_t)i * a.n + key] - top), inv, sum[x]);
+    for (uint32_t i = 0; i < AHEAD; ++i) {
+      if (i0 + i >= a.group) break;
+      const float top = shared[2 * (i0 + i)], inv = shared[2 * (i0 + i) + 1];
+#pragma unroll
+      for (uint32_t x = 0; x < PER; ++x) {
+        sum[x] = fmaf(__builtin_amdgcn_exp2f(ahead[i][x] - top), inv, sum[x]);
+        const uint32_t key = x * JOIN_THREADS + threadIdx.x;
+        ahead[i][x] = i0 + AHEAD + i < a.group && k0 + key < len ? logits[(uint64_t)(i0 + AHEAD + i) * a.n + key] : 0.f;
+      }
     }
   }
 #pragma unroll
   for (uint32_t x = 0; x < PER; ++x) {
-    const uint32_t key = k0 + x * JOIN_THREADS + threadIdx.x;
-    if (key < len) srow[key] += sum[x];
+    const uint32_t key = x * JOIN_THREADS + threadIdx.x;
+    if (k0 + key < len) srow[key] += sum[x];
   }
 }
 
 struct AttPlan {
-  uint32_t blocks16 = 1, splits = 1, per = 0;
+  uint32_t blocks16 = 1, share = 0;
   size_t off_logits = 0, off_part = 0, off_ml = 0, total = 0;
 };
 
-// Splits: enough workgroups for four to a compute unit, as long as each of a
-// workgroup's waves has a step of keys.
+// A row that one workgroup soon goes through is one workgroup's, in one launch;
+// otherwise the keys are shared out over as many workgroups as the card holds at
+// a time (two to a compute unit), as long as each has a unit.
 AttPlan attend_plan(const topk_attend_args& a, int cus) {
   AttPlan p;
   if (!a.batch || !a.heads || !a.n || !a.d) return p;
   const int64_t group = a.heads / a.kv_heads;
   p.blocks16 = (uint32_t)ceil_div(group, HEADS);
   const int64_t rows = a.batch * a.kv_heads * p.blocks16;
-  const int64_t least = ATT_WAVES * (a.dtype == TOPK_BF16 ? Att<bf16_t>::STEP : Att<float>::STEP);
-  const int64_t want = std::max<int64_t>(1, std::min(ceil_div(4 * cus, rows), ceil_div(a.n, least)));
-  p.per = (uint32_t)(ceil_div(ceil_div(a.n, want), least) * least);
-  p.splits = (uint32_t)ceil_div(a.n, p.per);
+  const int64_t unit = ATT_WAVES * (a.dtype == TOPK_BF16 ? Att<bf16_t>::STEP : Att<float>::STEP);
+  const int64_t units = ceil_div(a.n, unit);
+  if (units > 2 || (a.scores && p.blocks16 > 1)) p.share = (uint32_t)std::min<int64_t>(2 * cus, rows * units);
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t here = at;
     at += align256(bytes);
     return here;
   };
-  const size_t heads = (size_t)(a.batch * a.heads);
-  if (a.scores) p.off_logits = take(heads * a.n * 4);
-  if (p.splits > 1) p.off_part = take(heads * p.splits * a.d * 4);
-  if (p.splits > 1 || p.blocks16 > 1) p.off_ml = take(heads * p.splits * 8);
+  if (a.scores) p.off_logits = take((size_t)(a.batch * a.heads * a.n) * 4);
+  if (p.share) {
+    const size_t pieces = (size_t)(rows + p.share);
+    p.off_part = take(pieces * (size_t)(std::min<int64_t>(group, HEADS) * a.d) * 4);
+    p.off_ml = take(pieces * HEADS * 8);
+  }
   p.total = at;
   return p;
 }
@@ -507,20 +648,19 @@ hipError_t attend_call(const topk_attend_args& in, const AttPlan& p, char* ws, h
   a.blocks16 = p.blocks16;
   a.n = (uint32_t)in.n;
   a.d = (uint32_t)in.d;
-  a.splits = p.splits;
-  a.per = p.per;
+  a.batch = (uint32_t)in.batch;
+  a.share = p.share;
   a.scale2 = in.scale * LOG2E;
   a.logits = in.scores ? reinterpret_cast<float*>(ws + p.off_logits) : nullptr;
   a.part = reinterpret_cast<float*>(ws + p.off_part);
   a.ml = reinterpret_cast<float*>(ws + p.off_ml);
-  const uint64_t rows = (uint64_t)in.batch * a.kv_heads;
-  a.work = rows * p.blocks16 * p.splits;
+  const uint64_t heads = (uint64_t)in.batch * a.kv_heads;
+  a.work = p.share ? p.share : heads * p.blocks16;
   attend_typed(a, T{}, s);
-  const uint32_t outs = p.splits > 1 ? a.group : 0;
-  const uint32_t chunks = in.scores && (p.splits > 1 || p.blocks16 > 1) ? (a.n + JOIN_KEYS - 1) / JOIN_KEYS : 0;
-  if (outs + chunks) {
-    a.work = rows * (outs + chunks);
-    k_attend_join<T><<<wide_grid(a.work), JOIN_THREADS, std::max(a.group * 8, a.splits * 4), s>>>(a, outs, chunks);
+  if (p.share) {
+    const uint32_t chunks = in.scores ? (a.n + JOIN_KEYS - 1) / JOIN_KEYS : 0;
+    a.work = heads * (a.group + chunks);
+    k_attend_join<T><<<wide_grid(a.work), JOIN_THREADS, std::max(a.group * 8, p.share * 4), s>>>(a, chunks);
   }
   return hipGetLastError();
 }
