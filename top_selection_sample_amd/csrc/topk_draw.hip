@@ -16,16 +16,19 @@
 // top_k and top_p keep a beginning of the one order, so together they are one
 // cut: a logit and an index.  A row is cut into chunks, a workgroup each:
 //
-//   k_sample_max      the chunks' maxima
-//   k_sample_hist     counts and sums of weights by bins of m - z (its float's
-//                     leading bits: 128 bins to an octave)
-//   k_sample_plan     from those the bins that the cut can lie in
-//   k_sample_collect  their entries, and each chunk's sum over the bins before
-//   k_sample_finish   sorts the entries, finds the cut, then the chunk that the
-//                     token lies in, then the token
+//   k_sample_first    the chunks' maxima; where top_k is small, every chunk's
+//                     own largest entries too: the row's are among them
+//   k_sample_bins     other rows with a cut: counts and sums of weights by bins
+//                     of m - z (its float's leading bits: 128 bins to an octave)
+//   k_sample_collect  from those the bins that the cut can lie in, their
+//                     entries, and each chunk's sum over the bins before
+//   k_sample_finish   the entries sorted, the cut, the chunk that the token
+//                     lies in, the token
 //
-// Without top_k and top_p there is no cut: k_sample_sum stands in the place of
-// the middle three.
+// Calls without a cut do without the second, those whose top_k is small in all
+// rows without the middle two.  (A row's last workgroup doing the next step
+// saves a launch, but the fence that this takes in every workgroup writes its
+// cache back: 790 us for 256 rows of 65536, against 30.)
 #include <algorithm>
 
 #include "topk_model.hpp"
@@ -35,13 +38,17 @@ namespace tk {
 
 namespace {
 
-constexpr uint32_t CHUNK_THREADS = 256;
-constexpr uint32_t ROW_THREADS = 1024;
+constexpr uint32_t FIRST_THREADS = 256;
+constexpr uint32_t ROW_THREADS = 512;
 constexpr uint32_t ROW_WAVES = ROW_THREADS / 64;
+constexpr uint32_t TILE = 4096;             // entries that a workgroup takes at a time; a chunk is one or more
 constexpr uint32_t MAX_CHUNKS = 1024;       // of a row
 constexpr uint32_t BINS = 2048;             // 16 octaves of m - z from 2^-7 on, 128 to an octave
 constexpr uint32_t FIRST_BIN = (127 - 7) << 7;
 constexpr uint32_t CAP = 4096;              // entries of a row around its cut that are sorted
+constexpr uint32_t SMALL_K = 256;           // up to here every chunk picks its own entries,
+constexpr uint32_t SLOTS = 512;             // at most this many of them, and at least twice top_k
+constexpr uint32_t PAIRS = 512;             // entries that are compared each with each rather than sorted
 
 // What is known of a row between the launches.
 struct SampleRow {
@@ -51,7 +58,13 @@ struct SampleRow {
   uint32_t count, count_k;// entries of the bins below lo and bk
   uint32_t k;             // top_k, where bk says so
   uint32_t cut;           // whether there is a cut
-  uint32_t collected;
+};
+
+// The settings of a row, worked out once for all its workgroups.
+struct Settings {
+  double rate;       // log2(e) / temperature; 0 if greedy
+  float far;         // logits further than this below the maximum have no weight that counts
+  uint32_t greedy;
 };
 
 struct SampleArgs {
@@ -64,6 +77,10 @@ struct SampleArgs {
   const float* top_ps;
   const float* min_ps;
   float* maxima;          // [rows][chunks]
+  Settings* settings;     // [rows]
+  uint32_t* collected;    // [rows]: entries in `cand`, or more than CAP
+  uint64_t* own;          // [rows][chunks][slots]: a chunk's own entries, where top_k is small; null: it never is
+  uint32_t* own_count;    // [rows][chunks]
   uint64_t* sums;         // [rows][chunks]: weight that surely stays
   uint32_t* bin_count;    // [rows][BINS]
   uint64_t* bin_sum;
@@ -72,27 +89,27 @@ struct SampleArgs {
   uint64_t ld, work;
   int64_t top_k;
   float temperature, top_p, min_p;
-  uint32_t n, chunk, chunks, bits;   // bits: F
+  uint32_t n, chunk, chunks, slots, bits;   // bits: F
 };
 
-// The settings of a row.
-struct Settings {
-  double rate;       // log2(e) / temperature
-  bool greedy;
-};
-
-__device__ __forceinline__ Settings settings_of(const SampleArgs& a, uint64_t r) {
-  const float t = a.temperatures ? a.temperatures[r] : a.temperature;
-  Settings s;
-  s.greedy = !(t > 0.f);
-  s.rate = s.greedy ? 0.0 : 1.4426950408889634 / (double)t;
-  return s;
-}
-
+__device__ __forceinline__ float temperature_of(const SampleArgs& a, uint64_t r) { return a.temperatures ? a.temperatures[r] : a.temperature; }
 __device__ __forceinline__ float top_p_of(const SampleArgs& a, uint64_t r) { return a.top_ps ? a.top_ps[r] : a.top_p; }
 __device__ __forceinline__ double min_p_of(const SampleArgs& a, uint64_t r) {
   const float p = a.min_ps ? a.min_ps[r] : a.min_p;
   return p > 1.f ? 1.0 : (double)p;
+}
+
+// `far`: well below min_p, or below half of 2^-62.
+__device__ __forceinline__ Settings make_settings(const SampleArgs& a, uint64_t r) {
+  const float t = temperature_of(a, r);
+  const double p = min_p_of(a, r);
+  Settings s;
+  s.greedy = !(t > 0.f);
+  s.rate = s.greedy ? 0.0 : 1.4426950408889634 / (double)t;
+  const double least = p > 0.0 ? fmax(log2(p) - 1e-3, -64.0) : -64.0;
+  const double far = s.rate > 0.0 ? -least / s.rate * (1.0 + 1e-6) : INFINITY;
+  s.far = s.greedy ? 0.f : far < 3e38 ? (float)far : INFINITY;
+  return s;
 }
 
 template <class T>
@@ -166,6 +183,10 @@ __device__ __forceinline__ uint32_t bin_of(float z, float m) {
   return b <= FIRST_BIN ? 0u : min(b - FIRST_BIN, BINS - 1);
 }
 
+// m - z of all logits in bins up to b, but the equals of an infinite m, is below
+// this; that of a logit of -inf is not.
+__device__ __forceinline__ float bin_end(uint32_t b) { return b >= BINS - 1 ? INFINITY : __uint_as_float((FIRST_BIN + b + 1) << 16); }
+
 // ceil(p * w) and floor(p * w), exact; p a float in (0, 1).
 __device__ __forceinline__ void scaled(float p, uint64_t w, uint64_t* floor_, uint64_t* ceil_) {
   const uint32_t u = __float_as_uint(p);
@@ -207,6 +228,14 @@ __device__ __forceinline__ float row_max(const SampleArgs& a, uint64_t r) {
   return m;
 }
 
+// top_k of a row whose chunks pick their own entries; 0: they do not.
+__device__ __forceinline__ uint32_t small_k(const SampleArgs& a, uint64_t r) {
+  if (!a.own) return 0;
+  if (!(temperature_of(a, r) > 0.f)) return 1;
+  const int64_t k = a.top_ks ? a.top_ks[r] : a.top_k;
+  return k > 0 && k <= (int64_t)SMALL_K ? (uint32_t)k : 0u;
+}
+
 // Exclusive sums over the threads of a workgroup; *total: of all.
 template <uint32_t THREADS, class V>
 __device__ __forceinline__ V thread_scan(V v, V* part, V* total) {
@@ -219,6 +248,7 @@ __device__ __forceinline__ V thread_scan(V v, V* part, V* total) {
   if (threadIdx.x % 64 == 63) part[threadIdx.x / 64] = up;
   __syncthreads();
   V before = 0, all = 0;
+#pragma unroll
   for (uint32_t w = 0; w < THREADS / 64; ++w) {
     if (w < threadIdx.x / 64) before += part[w];
     all += part[w];
@@ -228,86 +258,151 @@ __device__ __forceinline__ V thread_scan(V v, V* part, V* total) {
   return before + up - v;
 }
 
+// TILE logits from i0 on, whole vectors to a thread; -inf behind `end`.  (NaN is
+// not live, and no maximum.)
+template <class T, uint32_t THREADS>
+struct Tile {
+  static constexpr uint32_t VEC = Vec<T>::N, PER = TILE / THREADS, VECS = PER / VEC;
+  static_assert(VECS * VEC == PER, "whole vectors");
+  float z[PER];
+  __device__ __forceinline__ static uint32_t index(uint32_t i0, uint32_t j) {
+    return i0 + (j / VEC * THREADS + threadIdx.x) * VEC + j % VEC;
+  }
+  __device__ __forceinline__ void load(const T* row, uint32_t i0, uint32_t end) {
+    if (i0 + TILE <= end) {
+#pragma unroll
+      for (uint32_t v = 0; v < VECS; ++v) Vec<T>::load(row + index(i0, v * VEC), z + v * VEC);
+    } else {
+#pragma unroll
+      for (uint32_t j = 0; j < PER; ++j) {
+        const uint32_t i = index(i0, j);
+        z[j] = i < end ? to_f32(row[i]) : -INFINITY;
+      }
+    }
+  }
+};
+
+// The first bin at which the counts reach k, or the last one; all threads get it.
+template <uint32_t THREADS>
+__device__ __forceinline__ uint32_t bin_reaching(const uint32_t* count, uint32_t k, uint32_t* part, uint32_t* found) {
+  constexpr uint32_t PER = BINS / THREADS;
+  if (threadIdx.x == 0) *found = BINS - 1;
+  uint32_t c[PER], sum = 0, all;
+#pragma unroll
+  for (uint32_t i = 0; i < PER; ++i) sum += c[i] = count[threadIdx.x * PER + i];
+  uint32_t at = thread_scan<THREADS>(sum, part, &all);
+  if (at < k && k <= at + sum) {
+#pragma unroll
+    for (uint32_t i = 0; i < PER; ++i) {
+      if (at < k && k <= at + c[i]) *found = threadIdx.x * PER + i;
+      at += c[i];
+    }
+  }
+  __syncthreads();
+  return *found;
+}
+
 template <class T>
-__global__ __launch_bounds__(CHUNK_THREADS) void k_sample_max(SampleArgs a) {
-  __shared__ float part[CHUNK_THREADS / 64];
+__global__ __launch_bounds__(FIRST_THREADS) void k_sample_first(SampleArgs a) {
+  __shared__ float part[FIRST_THREADS / 64];
+  __shared__ uint32_t count[BINS];
+  __shared__ uint32_t part32[FIRST_THREADS / 64], found, taken;
   const uint64_t id = block_id();
   if (id >= a.work) return;
   const uint64_t r = id / a.chunks;
-  const uint32_t c = (uint32_t)(id % a.chunks);
+  const uint32_t c = (uint32_t)(id - r * a.chunks);
   const T* row = static_cast<const T*>(a.logits) + r * a.ld;
   const uint32_t i0 = c * a.chunk, i1 = min(i0 + a.chunk, a.n);
+  Tile<T, FIRST_THREADS> tile;
+  tile.load(row, i0, i1);
+  const uint32_t k = small_k(a, r);
+  if (k)
+    for (uint32_t i = threadIdx.x; i < BINS; i += FIRST_THREADS) count[i] = 0;
   float m = -INFINITY;
-  for (uint32_t i = i0 + threadIdx.x; i < i1; i += CHUNK_THREADS) m = fmaxf(m, logit_of(row, i));
+  for (uint32_t at = i0;;) {
+#pragma unroll
+    for (uint32_t j = 0; j < tile.PER; ++j) m = fmaxf(m, tile.z[j]);
+    at += TILE;
+    if (at >= i1) break;
+    tile.load(row, at, i1);
+  }
+  const float mine = m;
 #pragma unroll
   for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
   if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = m;
+  if (threadIdx.x == 0) taken = 0;
   __syncthreads();
+#pragma unroll
+  for (uint32_t w = 0; w < FIRST_THREADS / 64; ++w) m = fmaxf(m, part[w]);
   if (threadIdx.x == 0) {
-    for (uint32_t w = 1; w < CHUNK_THREADS / 64; ++w) m = fmaxf(m, part[w]);
     a.maxima[id] = m;
-  }
-  if (a.bin_count) {   // the chunks of a row share the clearing of its bins
-    for (uint32_t i = c * CHUNK_THREADS + threadIdx.x; i < BINS; i += a.chunks * CHUNK_THREADS) {
-      a.bin_count[r * BINS + i] = 0;
-      a.bin_sum[r * BINS + i] = 0;
+    if (c == 0) {
+      a.settings[r] = make_settings(a, r);
+      if (a.collected) a.collected[r] = 0;
     }
   }
-}
-
-template <class T>
-__global__ __launch_bounds__(CHUNK_THREADS) void k_sample_hist(SampleArgs a) {
-  __shared__ uint64_t sum[BINS];
-  __shared__ uint32_t count[BINS];
-  __shared__ double table[64];
-  const uint64_t id = block_id();
-  if (id >= a.work) return;
-  const uint64_t r = id / a.chunks;
-  const uint32_t c = (uint32_t)(id % a.chunks);
-  const T* row = static_cast<const T*>(a.logits) + r * a.ld;
-  for (uint32_t i = threadIdx.x; i < BINS; i += CHUNK_THREADS) sum[i] = count[i] = 0;
-  load_powers(table);
-  const float m = row_max(a, r);
-  const Settings s = settings_of(a, r);
-  const uint32_t i0 = c * a.chunk, i1 = min(i0 + a.chunk, a.n);
-  for (uint32_t i = i0 + threadIdx.x; i < i1; i += CHUNK_THREADS) {
-    const float z = logit_of(row, i);
-    if (!live(z, m)) continue;
-    const uint32_t b = bin_of(z, m);
-    atomicAdd(&count[b], 1u);
-    const uint64_t w = fixed_of(weight_of(z, m, s, table), a.bits);
-    if (w) atomicAdd(reinterpret_cast<unsigned long long*>(&sum[b]), (unsigned long long)w);
+  if (!k) {
+    if (a.bin_count)   // the chunks of a row share the clearing of its bins
+      for (uint32_t i = c * FIRST_THREADS + threadIdx.x; i < BINS; i += a.chunks * FIRST_THREADS) {
+        a.bin_count[r * BINS + i] = 0;
+        a.bin_sum[r * BINS + i] = 0;
+      }
+    return;
   }
+  // One tile is the whole chunk here.  If k threads' largest entries lie in the
+  // bins up to one, so do the chunk's k largest entries; for small k not many
+  // others do.  Where they are too many for the slots, the bins of all entries
+  // are counted.  Bins are counted from the chunk's own maximum.
+  if (live(mine, m)) atomicAdd(&count[bin_of(mine, m)], 1u);
   __syncthreads();
-  for (uint32_t i = threadIdx.x; i < BINS; i += CHUNK_THREADS) {
-    if (!count[i]) continue;
-    atomicAdd(&a.bin_count[r * BINS + i], count[i]);
-    if (sum[i]) atomicAdd(reinterpret_cast<unsigned long long*>(&a.bin_sum[r * BINS + i]), (unsigned long long)sum[i]);
+  uint32_t last = bin_reaching<FIRST_THREADS>(count, k, part32, &found);
+  for (uint32_t round = 0;; ++round) {
+    const float below = bin_end(last);
+#pragma unroll
+    for (uint32_t j = 0; j < tile.PER; ++j)
+      if (m - tile.z[j] < below || (tile.z[j] == m && m > -INFINITY)) {
+        const uint32_t slot = atomicAdd(&taken, 1u);
+        if (slot < a.slots) a.own[id * a.slots + slot] = code_of(tile.z[j], tile.index(i0, j));
+      }
+    __syncthreads();
+    if (round || taken <= a.slots) break;
+    for (uint32_t i = threadIdx.x; i < BINS; i += FIRST_THREADS) count[i] = 0;
+    __syncthreads();
+#pragma unroll
+    for (uint32_t j = 0; j < tile.PER; ++j)
+      if (live(tile.z[j], m) && bin_of(tile.z[j], m) <= last) atomicAdd(&count[bin_of(tile.z[j], m)], 1u);
+    if (threadIdx.x == 0) taken = 0;
+    __syncthreads();
+    last = bin_reaching<FIRST_THREADS>(count, k, part32, &found);
   }
+  if (threadIdx.x == 0) a.own_count[id] = taken;   // beyond the slots: too many equal ones
 }
 
-// Two bins to a thread.
-__global__ __launch_bounds__(ROW_THREADS) void k_sample_plan(SampleArgs a) {
-  __shared__ uint32_t part32[ROW_WAVES];
-  __shared__ uint64_t part64[ROW_WAVES];
-  __shared__ uint32_t c_before[BINS + 1];
-  __shared__ uint64_t w_before[BINS + 1];
-  __shared__ uint32_t bk, lo, hi;
-  const uint64_t r = block_id();
-  if (r >= a.work) return;
+// From a row's bins: where its cut can lie.  Every workgroup of the row finds it
+// for itself; all threads get it.
+__device__ SampleRow plan_row(const SampleArgs& a, uint64_t r, uint32_t* c_before, uint64_t* w_before, uint32_t* part32, uint64_t* part64,
+                         uint32_t* mark) {
+  constexpr uint32_t PER = BINS / ROW_THREADS;
   const uint32_t t = threadIdx.x;
-  const uint32_t* bc = a.bin_count + r * BINS;
-  const uint64_t* bs = a.bin_sum + r * BINS;
-  const uint32_t c0 = bc[2 * t], c1 = bc[2 * t + 1];
-  const uint64_t s0 = bs[2 * t], s1 = bs[2 * t + 1];
-  uint32_t call;
-  uint64_t wall;
-  const uint32_t cb = thread_scan<ROW_THREADS>(c0 + c1, part32, &call);
-  const uint64_t wb = thread_scan<ROW_THREADS>(s0 + s1, part64, &wall);
-  c_before[2 * t] = cb;
-  c_before[2 * t + 1] = cb + c0;
-  w_before[2 * t] = wb;
-  w_before[2 * t + 1] = wb + s0;
+  uint32_t c[PER], call;
+  uint64_t w[PER], wall;
+  uint32_t cs = 0;
+  uint64_t ws = 0;
+#pragma unroll
+  for (uint32_t i = 0; i < PER; ++i) {
+    cs += c[i] = a.bin_count[r * BINS + t * PER + i];
+    ws += w[i] = a.bin_sum[r * BINS + t * PER + i];
+  }
+  uint32_t cb = thread_scan<ROW_THREADS>(cs, part32, &call);
+  uint64_t wb = thread_scan<ROW_THREADS>(ws, part64, &wall);
+#pragma unroll
+  for (uint32_t i = 0; i < PER; ++i) {
+    c_before[t * PER + i] = cb;
+    w_before[t * PER + i] = wb;
+    cb += c[i];
+    wb += w[i];
+  }
+  uint32_t &bk = mark[0], &lo = mark[1], &hi = mark[2];
   if (t == 0) {
     c_before[BINS] = call;
     w_before[BINS] = wall;
@@ -315,115 +410,150 @@ __global__ __launch_bounds__(ROW_THREADS) void k_sample_plan(SampleArgs a) {
     lo = hi = 0;
   }
   __syncthreads();
-  const Settings s = settings_of(a, r);
   int64_t k = a.top_ks ? a.top_ks[r] : a.top_k;
-  if (s.greedy) k = 1;
+  if (!(temperature_of(a, r) > 0.f)) k = 1;
   const bool cut_k = k > 0 && k < (int64_t)call;
   if (cut_k) {
 #pragma unroll
-    for (uint32_t i = 0; i < 2; ++i)
-      if (c_before[2 * t + i] < (uint64_t)k && (uint64_t)k <= c_before[2 * t + i + 1]) bk = 2 * t + i;
+    for (uint32_t i = 0; i < PER; ++i)
+      if (c_before[t * PER + i] < (uint64_t)k && (uint64_t)k <= c_before[t * PER + i + 1]) bk = t * PER + i;
   }
   __syncthreads();
   const float p = top_p_of(a, r);
   const bool cut_p = !(p >= 1.f);
-  const uint64_t least = bk < BINS ? w_before[bk] : wall, most = bk < BINS ? w_before[bk + 1] : wall;
   if (cut_p) {
-    // the last bin with an entry whose preceding weight is below the limit
-    const uint64_t l0 = limit_of(p, least), l1 = limit_of(p, most);
+    // the last bin with an entry whose preceding weight is below the limit, for
+    // the least and the most weight that top_k can leave
+    const uint64_t l0 = limit_of(p, bk < BINS ? w_before[bk] : wall), l1 = limit_of(p, bk < BINS ? w_before[bk + 1] : wall);
 #pragma unroll
-    for (uint32_t i = 0; i < 2; ++i) {
-      if (!(i ? c1 : c0)) continue;
-      if (w_before[2 * t + i] < l0) atomicMax(&lo, 2 * t + i);
-      if (w_before[2 * t + i] < l1) atomicMax(&hi, 2 * t + i);
+    for (uint32_t i = 0; i < PER; ++i) {
+      if (!c[i]) continue;
+      if (w_before[t * PER + i] < l0) atomicMax(&lo, t * PER + i);
+      if (w_before[t * PER + i] < l1) atomicMax(&hi, t * PER + i);
     }
   } else if (t == 0) {
     lo = hi = bk;
   }
   __syncthreads();
-  if (t == 0) {
-    SampleRow v;
-    v.cut = cut_k || cut_p;
-    const uint32_t last = bk < BINS ? max(hi, bk) : hi;
-    uint32_t from = lo;
-    if (v.cut && c_before[min(last, BINS - 1) + 1] <= CAP) from = 0, hi = last;   // few entries: all that can stay
-    v.lo = from;
-    v.hi = hi;
-    v.bk = bk;
-    v.before = w_before[from];
-    v.count = c_before[from];
-    v.before_k = bk < BINS ? w_before[bk] : wall;
-    v.count_k = bk < BINS ? c_before[bk] : call;
-    v.k = cut_k ? (uint32_t)k : 0u;
-    v.collected = 0;
-    a.row[r] = v;
-  }
+  SampleRow v;
+  v.cut = cut_k || cut_p;
+  const uint32_t last = bk < BINS ? max(hi, bk) : hi;
+  const bool few = v.cut && c_before[min(last, BINS - 1) + 1] <= CAP;   // few entries: all that can stay
+  v.lo = few ? 0 : lo;
+  v.hi = few ? last : hi;
+  v.bk = bk;
+  v.before = w_before[v.lo];
+  v.count = c_before[v.lo];
+  v.before_k = bk < BINS ? w_before[bk] : wall;
+  v.count_k = bk < BINS ? c_before[bk] : call;
+  v.k = cut_k ? (uint32_t)k : 0u;
+  __syncthreads();   // what is shared may be used anew
+  return v;
 }
 
 template <class T>
-__global__ __launch_bounds__(CHUNK_THREADS) void k_sample_collect(SampleArgs a) {
+__global__ __launch_bounds__(ROW_THREADS) void k_sample_bins(SampleArgs a) {
+  __shared__ uint64_t sum[BINS];
+  __shared__ uint32_t count[BINS];
   __shared__ double table[64];
-  __shared__ uint64_t part[CHUNK_THREADS / 64];
   const uint64_t id = block_id();
   if (id >= a.work) return;
   const uint64_t r = id / a.chunks;
-  const uint32_t c = (uint32_t)(id % a.chunks);
+  const uint32_t c = (uint32_t)(id - r * a.chunks);
+  if (small_k(a, r)) return;
+  const Settings s = a.settings[r];
   const T* row = static_cast<const T*>(a.logits) + r * a.ld;
+  const uint32_t i0 = c * a.chunk, i1 = min(i0 + a.chunk, a.n);
+  Tile<T, ROW_THREADS> tile;
+  tile.load(row, i0, i1);
+  for (uint32_t i = threadIdx.x; i < BINS; i += ROW_THREADS) sum[i] = count[i] = 0;
   load_powers(table);
   const float m = row_max(a, r);
-  const Settings s = settings_of(a, r);
-  const double min_p = min_p_of(a, r);
-  const SampleRow v = a.row[r];
-  const uint32_t i0 = c * a.chunk, i1 = min(i0 + a.chunk, a.n);
-  uint64_t sum = 0;
-  for (uint32_t i = i0 + threadIdx.x; i < i1; i += CHUNK_THREADS) {
-    const float z = logit_of(row, i);
-    if (!live(z, m)) continue;
-    const uint32_t b = bin_of(z, m);
-    if (!v.cut || b < v.lo) {
-      const double w = weight_of(z, m, s, table);
-      if (w >= min_p) sum += fixed_of(w, a.bits);
-    } else if (b <= v.hi || b == v.bk) {
-      const uint32_t at = atomicAdd(&a.row[r].collected, 1u);
-      if (at < CAP) a.cand[r * CAP + at] = code_of(z, i);
+  for (uint32_t at = i0;;) {
+#pragma unroll
+    for (uint32_t j = 0; j < tile.PER; ++j) {
+      const float z = tile.z[j];
+      if (!live(z, m)) continue;
+      const uint32_t b = bin_of(z, m);
+      atomicAdd(&count[b], 1u);
+      const uint64_t w = fixed_of(weight_of(z, m, s, table), a.bits);
+      if (w) atomicAdd(reinterpret_cast<unsigned long long*>(&sum[b]), (unsigned long long)w);
     }
+    at += TILE;
+    if (at >= i1) break;
+    tile.load(row, at, i1);
   }
-  sum = wave_sum(sum);
-  if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = sum;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    for (uint32_t w = 1; w < CHUNK_THREADS / 64; ++w) sum += part[w];
-    a.sums[id] = sum;
+  for (uint32_t i = threadIdx.x; i < BINS; i += ROW_THREADS) {
+    if (!count[i]) continue;
+    atomicAdd(&a.bin_count[r * BINS + i], count[i]);
+    if (sum[i]) atomicAdd(reinterpret_cast<unsigned long long*>(&a.bin_sum[r * BINS + i]), (unsigned long long)sum[i]);
   }
 }
 
-// The middle of a call without a cut.
-template <class T>
-__global__ __launch_bounds__(CHUNK_THREADS) void k_sample_sum(SampleArgs a) {
+// Of a row without a cut, every bin is before it.  CUT: some row has one.
+template <class T, bool CUT>
+__global__ __launch_bounds__(ROW_THREADS) void k_sample_collect(SampleArgs a) {
+  __shared__ uint64_t code[CUT ? TILE : 1];            // the plan's sums, then the entries to be handed on
+  __shared__ uint32_t counts[CUT ? BINS + 1 : 1];
+  static_assert(TILE > BINS, "the plan's sums fit");
   __shared__ double table[64];
-  __shared__ uint64_t part[CHUNK_THREADS / 64];
+  __shared__ uint32_t part32[ROW_WAVES], mark[3], taken, base;
+  __shared__ uint64_t part64[ROW_WAVES];
   const uint64_t id = block_id();
   if (id >= a.work) return;
   const uint64_t r = id / a.chunks;
-  const uint32_t c = (uint32_t)(id % a.chunks);
+  const uint32_t c = (uint32_t)(id - r * a.chunks);
+  if (small_k(a, r)) return;
+  const Settings s = a.settings[r];
   const T* row = static_cast<const T*>(a.logits) + r * a.ld;
-  load_powers(table);
-  const float m = row_max(a, r);
-  const Settings s = settings_of(a, r);
-  const double min_p = min_p_of(a, r);
   const uint32_t i0 = c * a.chunk, i1 = min(i0 + a.chunk, a.n);
+  Tile<T, ROW_THREADS> tile;
+  tile.load(row, i0, i1);
+  const float m = row_max(a, r);
+  if (threadIdx.x == 0) taken = 0;
+  load_powers(table);
+  SampleRow v;
+  v.cut = 0;
+  v.lo = v.hi = v.bk = BINS;
+  if constexpr (CUT) {
+    v = plan_row(a, r, counts, code, part32, part64, mark);
+    if (c == 0 && threadIdx.x == 0) a.row[r] = v;
+  }
+  const double min_p = min_p_of(a, r);
   uint64_t sum = 0;
-  for (uint32_t i = i0 + threadIdx.x; i < i1; i += CHUNK_THREADS) {
-    const float z = logit_of(row, i);
-    if (!live(z, m)) continue;
-    const double w = weight_of(z, m, s, table);
-    if (w >= min_p) sum += fixed_of(w, a.bits);
+  for (uint32_t at = i0;;) {
+#pragma unroll
+    for (uint32_t j = 0; j < tile.PER; ++j) {
+      const float z = tile.z[j];
+      const uint32_t b = v.cut && live(z, m) ? bin_of(z, m) : 0u;
+      const bool sure = !(m - z > s.far) && z > -INFINITY && (!v.cut || b < v.lo);
+      if (__any(sure)) {   // few waves hold a weight that counts
+        const double w = weight_of(z, m, s, table);
+        if (sure && w >= min_p) sum += fixed_of(w, a.bits);
+      }
+      if constexpr (CUT)
+        if (v.cut && live(z, m) && b >= v.lo && (b <= v.hi || b == v.bk)) code[atomicAdd(&taken, 1u)] = code_of(z, tile.index(at, j));
+    }
+    if (CUT && v.cut) {
+      __syncthreads();
+      if (threadIdx.x == 0 && taken) base = atomicAdd(&a.collected[r], taken);
+      __syncthreads();
+      for (uint32_t i = threadIdx.x; i < taken; i += ROW_THREADS)
+        if (base + i < CAP) a.cand[r * CAP + base + i] = code[i];
+      __syncthreads();
+      if (threadIdx.x == 0) taken = 0;
+      __syncthreads();
+    }
+    at += TILE;
+    if (at >= i1) break;
+    tile.load(row, at, i1);
   }
   sum = wave_sum(sum);
-  if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = sum;
+  if (threadIdx.x % 64 == 0) part64[threadIdx.x / 64] = sum;
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (uint32_t w = 1; w < CHUNK_THREADS / 64; ++w) sum += part[w];
+    for (uint32_t w = 1; w < ROW_WAVES; ++w) sum += part64[w];
     a.sums[id] = sum;
   }
 }
@@ -486,122 +616,162 @@ __device__ __forceinline__ uint64_t staying(const SampleArgs& a, const T* row, u
   return wave_sum(sum);
 }
 
-template <class T>
-__global__ __launch_bounds__(ROW_THREADS) void k_sample_finish(SampleArgs a) {
-  __shared__ uint64_t code[CAP];
-  __shared__ uint64_t sums[MAX_CHUNKS];
-  __shared__ uint64_t part[ROW_WAVES], found[2];
-  __shared__ double table[64];
-  __shared__ uint32_t pick;
-  __shared__ uint64_t rest;
-  const uint64_t r = block_id();
-  if (r >= a.work) return;
+// What a workgroup that ends a row keeps in LDS.
+struct RowShared {
+  uint64_t code[CAP];
+  uint64_t sums[MAX_CHUNKS];   // weight that stays, by chunk
+  uint64_t sorted[PAIRS];
+  uint64_t part64[ROW_WAVES], found[2], rest;
+  uint32_t count[BINS];
+  uint32_t rank[PAIRS];
+  uint32_t part32[ROW_WAVES], pick, taken, flag;
+  double table[64];
+};
+
+__device__ __forceinline__ void write_token(const SampleArgs& a, uint64_t r, int64_t token, uint64_t w, uint64_t all) {
+  a.tokens[r] = token;
+  a.logprobs[r] = token < 0 ? -INFINITY : (float)log((double)w / (double)all);
+}
+
+// The n entries of l.code in order, the first ones first.
+__device__ __forceinline__ void sort_codes(RowShared& l, uint32_t n) {
   const uint32_t t = threadIdx.x;
-  const T* row = static_cast<const T*>(a.logits) + r * a.ld;
-  load_powers(table);
-  const float m = row_max(a, r);
-  if (m == -INFINITY) {
-    if (t == 0) {
-      a.tokens[r] = -1;
-      a.logprobs[r] = -INFINITY;
+  if (n <= PAIRS) {
+    // an entry's rank is the number of larger ones: threads share the comparisons
+    uint32_t shift = 0;      // entries rounded up to a power of two, 1 << shift
+    while ((1u << shift) < n) ++shift;
+    const uint32_t i = t & ((1u << shift) - 1), parts = ROW_THREADS >> shift, part = t >> shift;
+    const uint32_t per = (n + parts - 1) / parts, j0 = part * per, j1 = min(j0 + per, n);
+    if (t < PAIRS) l.rank[t] = 0;
+    __syncthreads();
+    if (i < n) {
+      const uint64_t own = l.code[i];
+      uint32_t above = 0;
+      for (uint32_t j = j0; j < j1; ++j) above += l.code[j] > own;
+      if (above) atomicAdd(&l.rank[i], above);
     }
+    __syncthreads();
+    if (t < n) l.sorted[l.rank[t]] = l.code[t];
+    __syncthreads();
+    if (t < n) l.code[t] = l.sorted[t];
+    __syncthreads();
     return;
   }
-  const Settings s = settings_of(a, r);
+  uint32_t size = 2 * PAIRS;
+  while (size < n) size *= 2;
+  for (uint32_t i = n + t; i < size; i += ROW_THREADS) l.code[i] = 0;
+  __syncthreads();
+  for (uint32_t len = 2; len <= size; len *= 2)
+    for (uint32_t step = len / 2; step; step /= 2) {
+      for (uint32_t i = t; i < size / 2; i += ROW_THREADS) {
+        const uint32_t x = (i & ~(step - 1)) * 2 + (i & (step - 1)), y = x + step;
+        const uint64_t cx = l.code[x], cy = l.code[y];
+        if ((cx < cy) == ((x & len) == 0)) {   // falling
+          l.code[x] = cy;
+          l.code[y] = cx;
+        }
+      }
+      __syncthreads();
+    }
+}
+
+// The end of a row.  n_cand entries around the cut are in l.code (more than
+// CAP: they are not, and the whole row is gone through again); `inside`: all
+// that can stay is among them, and the chunks' sums are 0.
+template <class T>
+__device__ void finish_row(const SampleArgs& a, uint64_t r, const T* row, float m, const Settings& s, const SampleRow& v,
+                           uint32_t n_cand, bool inside, RowShared& l) {
+  const uint32_t t = threadIdx.x;
   const double min_p = min_p_of(a, r);
+  const double* table = l.table;
+  const float u = a.u[r];
   uint64_t cut = 0;
   bool whole = false;       // the chunks' sums have to be taken anew
-  uint32_t n_cand = 0;
-  SampleRow v;
-  v.cut = 0;
-  if (a.row) v = a.row[r];
+  uint32_t staying_cands = 0;
   if (v.cut) {
     const float p = top_p_of(a, r);
-    if (v.collected <= CAP) {
-      n_cand = v.collected;
-      uint32_t size = 64;
-      while (size < n_cand) size *= 2;
-      for (uint32_t i = t; i < size; i += ROW_THREADS) code[i] = i < n_cand ? a.cand[r * CAP + i] : 0;
-      __syncthreads();
-      for (uint32_t len = 2; len <= size; len *= 2)
-        for (uint32_t step = len / 2; step; step /= 2) {
-          for (uint32_t i = t; i < size / 2; i += ROW_THREADS) {
-            const uint32_t x = (i & ~(step - 1)) * 2 + (i & (step - 1)), y = x + step;
-            const uint64_t cx = code[x], cy = code[y];
-            if ((cx < cy) == ((x & len) == 0)) {   // falling
-              code[x] = cy;
-              code[y] = cx;
-            }
-          }
-          __syncthreads();
-        }
-      // CAP / ROW_THREADS entries to a thread: their weights' sums, and where the k-th is
-      constexpr uint32_t PER = CAP / ROW_THREADS;
-      uint64_t w[PER], own = 0, all;
+    if (n_cand <= CAP) {
+      sort_codes(l, n_cand);
+      // consecutive entries to a thread: their weights' sums, and where the k-th is
+      const uint32_t per = (n_cand + ROW_THREADS - 1) / ROW_THREADS;
+      const uint32_t x0 = min(t * per, n_cand), x1 = min(x0 + per, n_cand);
+      uint64_t own = 0, all;
       uint32_t low = 0;     // entries of bins up to hi: before those of a bin bk beyond
-#pragma unroll
-      for (uint32_t i = 0; i < PER; ++i) {
-        const uint32_t x = t * PER + i;
-        w[i] = 0;
-        if (x < n_cand) {
-          const float z = logit_of_code(code[x]);
-          w[i] = fixed_of(weight_of(z, m, s, table), a.bits);
-          low += bin_of(z, m) <= v.hi;
-        }
-        own += w[i];
+      for (uint32_t x = x0; x < x1; ++x) {
+        const float z = logit_of_code(l.code[x]);
+        own += fixed_of(weight_of(z, m, s, table), a.bits);
+        low += bin_of(z, m) <= v.hi;
       }
-      const uint64_t at = thread_scan<ROW_THREADS>(own, part, &all);
-      uint64_t lows;
-      thread_scan<ROW_THREADS>((uint64_t)low, part, &lows);
+      const uint64_t at = thread_scan<ROW_THREADS>(own, l.part64, &all);
+      uint32_t lows;
+      thread_scan<ROW_THREADS>(low, l.part32, &lows);
       const bool apart = v.bk < BINS && v.bk > v.hi;   // bin bk does not follow on the others
-      // sums of the list before an entry: of the first `lows` of bk's own, and up to the k-th
-      const uint32_t bk_at = v.bk >= BINS ? 0u : apart ? (uint32_t)lows : v.count_k - v.count;
+      // where bk's entries begin in the list, and where the k-th ends
+      const uint32_t bk_at = v.bk >= BINS ? 0u : apart ? lows : v.count_k - v.count;
       const uint32_t k_at = v.bk >= BINS ? 0u : bk_at + (v.k - v.count_k);
-      if (t == 0) found[0] = found[1] = all;
+      if (t == 0) {
+        l.found[0] = l.found[1] = all;
+        l.pick = 0;
+      }
       __syncthreads();
       uint64_t run = at;
-#pragma unroll
-      for (uint32_t i = 0; i < PER; ++i) {
-        const uint32_t x = t * PER + i;
-        if (v.bk < BINS && x < n_cand) {
-          if (x == bk_at) found[0] = run;
-          if (x == k_at) found[1] = run;
+      if (v.bk < BINS)
+        for (uint32_t x = x0; x < x1; ++x) {
+          if (x == bk_at) l.found[0] = run;
+          if (x == k_at) l.found[1] = run;
+          run += fixed_of(weight_of(logit_of_code(l.code[x]), m, s, table), a.bits);
         }
-        run += w[i];
-      }
       __syncthreads();
-      const uint64_t sum_k = v.bk < BINS ? v.before_k + (found[1] - found[0]) : v.before_k;
+      const uint64_t bk_start = l.found[0];
+      const uint64_t sum_k = v.bk < BINS ? v.before_k + (l.found[1] - bk_start) : v.before_k;
       const uint64_t limit = limit_of(p, sum_k);
-      const uint64_t bk_start = found[0];
-      if (t == 0) pick = 0;
-      __syncthreads();
       run = at;
-#pragma unroll
-      for (uint32_t i = 0; i < PER; ++i) {
-        const uint32_t x = t * PER + i;
-        if (x < n_cand) {
-          const bool second = apart && x >= lows;
-          const uint64_t before = second ? v.before_k + (run - bk_start) : v.before + run;
-          const bool in_k = v.bk >= BINS || x < k_at;
-          if (in_k && before < limit) atomicMax(&pick, x);
+      for (uint32_t x = x0; x < x1; ++x) {
+        const uint64_t before = apart && x >= lows ? v.before_k + (run - bk_start) : v.before + run;
+        const bool in_k = v.bk >= BINS || x < k_at;
+        if (in_k && before < limit) atomicMax(&l.pick, x);
+        run += fixed_of(weight_of(logit_of_code(l.code[x]), m, s, table), a.bits);
+      }
+      __syncthreads();
+      staying_cands = l.pick + 1;
+      cut = l.code[l.pick];
+      __syncthreads();
+      if (inside && staying_cands <= PAIRS) {
+        // few: the sum before an entry, by index, is over those of lower index
+        const bool mine = t < staying_cands;
+        uint64_t w = 0;
+        if (mine) {
+          const double f = weight_of(logit_of_code(l.code[t]), m, s, table);
+          w = f >= min_p ? fixed_of(f, a.bits) : 0;
+          l.sorted[t] = w;
         }
-        run += w[i];
+        thread_scan<ROW_THREADS>(w, l.part64, &all);   // waits for l.sorted as well
+        if (all == 0) {      // a min_p of NaN: nothing stays
+          if (t == 0) write_token(a, r, -1, 0, 1);
+          return;
+        }
+        uint64_t target, up;
+        if (!(u < 1.f)) target = all - 1;      // the last one
+        else if (!(u > 0.f)) target = 0;
+        else scaled(u, all, &target, &up);
+        if (w) {
+          const uint32_t own_index = ~(uint32_t)l.code[t];
+          uint64_t before = 0;
+          for (uint32_t j = 0; j < staying_cands; ++j) before += ~(uint32_t)l.code[j] < own_index ? l.sorted[j] : 0;
+          if (before <= target && target < before + w) write_token(a, r, own_index, w, all);
+        }
+        return;
       }
-      __syncthreads();
-      cut = code[pick];
-      __syncthreads();
     } else {
-      if (v.bk < BINS) {
-        cut = select_code(a, row, m, s, table, 0, true, v.k, sums, found);
-      }
+      if (v.bk < BINS) cut = select_code(a, row, m, s, table, 0, true, v.k, l.sums, l.found);
       if (!(p >= 1.f)) {
         uint64_t mine = 0, all;
         for (uint32_t c = t / 64; c < a.chunks; c += ROW_WAVES) {
           const uint32_t i0 = c * a.chunk;
           mine += staying(a, row, i0, min(i0 + a.chunk, a.n), m, s, -1.0, cut, table);
         }
-        thread_scan<ROW_THREADS>(t % 64 ? uint64_t(0) : mine, part, &all);
-        cut = select_code(a, row, m, s, table, cut, false, limit_of(p, all), sums, found);
+        thread_scan<ROW_THREADS>(t % 64 ? uint64_t(0) : mine, l.part64, &all);
+        cut = select_code(a, row, m, s, table, cut, false, limit_of(p, all), l.sums, l.found);
       }
       whole = true;
     }
@@ -611,87 +781,187 @@ __global__ __launch_bounds__(ROW_THREADS) void k_sample_finish(SampleArgs a) {
     for (uint32_t c = t / 64; c < a.chunks; c += ROW_WAVES) {
       const uint32_t i0 = c * a.chunk;
       const uint64_t sum = staying(a, row, i0, min(i0 + a.chunk, a.n), m, s, min_p, cut, table);
-      if (t % 64 == 0) sums[c] = sum;
+      if (t % 64 == 0) l.sums[c] = sum;
     }
   } else {
-    for (uint32_t c = t; c < a.chunks; c += ROW_THREADS) sums[c] = a.sums[r * a.chunks + c];
+    for (uint32_t c = t; c < a.chunks; c += ROW_THREADS) l.sums[c] = inside ? 0 : a.sums[r * a.chunks + c];
     __syncthreads();
-    for (uint32_t i = t; i < n_cand; i += ROW_THREADS) {
-      const uint64_t x = code[i];
-      if (x < cut) continue;
+    for (uint32_t i = t; i < staying_cands; i += ROW_THREADS) {
+      const uint64_t x = l.code[i];
       const double w = weight_of(logit_of_code(x), m, s, table);
-      if (w >= min_p) atomicAdd(reinterpret_cast<unsigned long long*>(&sums[(uint32_t)~(uint32_t)x / a.chunk]), (unsigned long long)fixed_of(w, a.bits));
+      if (w >= min_p) atomicAdd(reinterpret_cast<unsigned long long*>(&l.sums[~(uint32_t)x / a.chunk]), (unsigned long long)fixed_of(w, a.bits));
     }
   }
   __syncthreads();
-  const uint64_t mine = t < a.chunks ? sums[t] : 0;   // MAX_CHUNKS = ROW_THREADS
-  uint64_t all;
-  const uint64_t before = thread_scan<ROW_THREADS>(mine, part, &all);
+  constexpr uint32_t SUMS = MAX_CHUNKS / ROW_THREADS;
+  uint64_t own[SUMS], mine = 0, all;
+#pragma unroll
+  for (uint32_t i = 0; i < SUMS; ++i) mine += own[i] = t * SUMS + i < a.chunks ? l.sums[t * SUMS + i] : 0;
+  uint64_t before = thread_scan<ROW_THREADS>(mine, l.part64, &all);
   if (all == 0) {   // a min_p of NaN: nothing stays
-    if (t == 0) {
-      a.tokens[r] = -1;
-      a.logprobs[r] = -INFINITY;
-    }
+    if (t == 0) write_token(a, r, -1, 0, 1);
     return;
   }
-  const float u = a.u[r];
   uint64_t target, up;
   if (!(u < 1.f)) target = all - 1;      // the last one
   else if (!(u > 0.f)) target = 0;
   else scaled(u, all, &target, &up);
-  if (t == 0) {
-    pick = 0;
-    rest = 0;
-  }
-  __syncthreads();
-  if (before <= target && target < before + mine) {
-    pick = t;
-    rest = target - before;
-  }
-  __syncthreads();
-  // that chunk, consecutive entries to a thread
-  const uint32_t i0 = pick * a.chunk, i1 = min(i0 + a.chunk, a.n);
-  const uint32_t per = (a.chunk + ROW_THREADS - 1) / ROW_THREADS;
-  const uint32_t j0 = min(i0 + t * per, i1), j1 = min(j0 + per, i1);
-  uint64_t own = 0, chunk_all;
-  for (uint32_t i = j0; i < j1; ++i) {
-    const float z = logit_of(row, i);
-    if (!live(z, m) || code_of(z, i) < cut) continue;
-    const double w = weight_of(z, m, s, table);
-    if (w >= min_p) own += fixed_of(w, a.bits);
-  }
-  uint64_t run = thread_scan<ROW_THREADS>(own, part, &chunk_all);
-  if (run <= rest && rest < run + own) {
-    for (uint32_t i = j0; i < j1; ++i) {
-      const float z = logit_of(row, i);
-      if (!live(z, m) || code_of(z, i) < cut) continue;
-      const double w = weight_of(z, m, s, table);
-      if (!(w >= min_p)) continue;
-      const uint64_t f = fixed_of(w, a.bits);
-      if (rest < run + f) {
-        a.tokens[r] = i;
-        a.logprobs[r] = (float)log((double)f / (double)all);
-        break;
-      }
-      run += f;
+#pragma unroll
+  for (uint32_t i = 0; i < SUMS; ++i) {
+    if (before <= target && target < before + own[i]) {
+      l.pick = t * SUMS + i;
+      l.rest = target - before;
     }
+    before += own[i];
+  }
+  __syncthreads();
+  // that chunk, a tile at a time, consecutive entries to a thread
+  const uint32_t i1 = min((l.pick + 1) * a.chunk, a.n);
+  uint64_t rest = l.rest;
+  constexpr uint32_t PER = TILE / ROW_THREADS;
+  for (uint32_t i0 = l.pick * a.chunk; i0 < i1; i0 += TILE) {
+    const uint32_t j0 = i0 + t * PER;
+    uint64_t w[PER], sum = 0, tile_all;
+#pragma unroll
+    for (uint32_t j = 0; j < PER; ++j) {
+      const float z = j0 + j < i1 ? logit_of(row, j0 + j) : -INFINITY;
+      w[j] = 0;
+      if (live(z, m) && code_of(z, j0 + j) >= cut) {
+        const double f = weight_of(z, m, s, table);
+        if (f >= min_p) w[j] = fixed_of(f, a.bits);
+      }
+      sum += w[j];
+    }
+    uint64_t run = thread_scan<ROW_THREADS>(sum, l.part64, &tile_all);
+    if (rest < tile_all) {
+      if (run <= rest && rest < run + sum) {
+#pragma unroll
+        for (uint32_t j = 0; j < PER; ++j) {
+          if (run <= rest && rest < run + w[j]) write_token(a, r, j0 + j, w[j], all);
+          run += w[j];
+        }
+      }
+      return;
+    }
+    rest -= tile_all;
   }
 }
 
+// A row whose chunks picked their own entries: of those, the bins that hold the first k.
+template <class T>
+__device__ void finish_small(const SampleArgs& a, uint64_t r, const T* row, float m, const Settings& s, uint32_t k, RowShared& l) {
+  constexpr uint32_t PER = MAX_CHUNKS / ROW_THREADS, AHEAD = 4;
+  const uint32_t t = threadIdx.x, wave = t / 64, lane = t % 64;
+  const uint32_t* counts = a.own_count + r * a.chunks;
+  const uint64_t* lists = a.own + r * a.chunks * a.slots;
+  uint32_t n[PER], own = 0, total;
+#pragma unroll
+  for (uint32_t i = 0; i < PER; ++i) own += n[i] = t * PER + i < a.chunks ? counts[t * PER + i] : 0u;
+  for (uint32_t i = t; i < BINS; i += ROW_THREADS) l.count[i] = 0;
+  if (t == 0) l.taken = l.flag = 0;
+  thread_scan<ROW_THREADS>(own, l.part32, &total);
+  uint32_t* number = reinterpret_cast<uint32_t*>(l.sums);   // entries of each chunk
+#pragma unroll
+  for (uint32_t i = 0; i < PER; ++i) {
+    number[t * PER + i] = min(n[i], a.slots);
+    if (n[i] > a.slots) l.flag = 1;
+  }
+  __syncthreads();
+  // by a wave for a chunk, AHEAD rounds of 64 entries in flight (a chunk has at most SLOTS)
+  for (uint32_t c = wave; c < a.chunks; c += ROW_WAVES) {
+    const uint32_t have = number[c];
+    for (uint32_t i0 = lane; i0 < have; i0 += 64 * AHEAD) {
+      uint64_t code[AHEAD];
+#pragma unroll
+      for (uint32_t i = 0; i < AHEAD; ++i) code[i] = i0 + 64 * i < have ? lists[(uint64_t)c * a.slots + i0 + 64 * i] : 0;
+#pragma unroll
+      for (uint32_t i = 0; i < AHEAD; ++i) {
+        const float z = logit_of_code(code[i]);
+        if (i0 + 64 * i < have && live(z, m)) atomicAdd(&l.count[bin_of(z, m)], 1u);
+      }
+    }
+  }
+  __syncthreads();
+  const uint32_t last = bin_reaching<ROW_THREADS>(l.count, k, l.part32, &l.pick);
+  for (uint32_t c = wave; c < a.chunks; c += ROW_WAVES) {
+    const uint32_t have = number[c];
+    for (uint32_t i0 = lane; i0 < have; i0 += 64 * AHEAD) {
+      uint64_t code[AHEAD];
+#pragma unroll
+      for (uint32_t i = 0; i < AHEAD; ++i) code[i] = i0 + 64 * i < have ? lists[(uint64_t)c * a.slots + i0 + 64 * i] : 0;
+#pragma unroll
+      for (uint32_t i = 0; i < AHEAD; ++i) {
+        const float z = logit_of_code(code[i]);
+        if (i0 + 64 * i < have && live(z, m) && bin_of(z, m) <= last) {
+          const uint32_t at = atomicAdd(&l.taken, 1u);
+          if (at < CAP) l.code[at] = code[i];
+        }
+      }
+    }
+  }
+  __syncthreads();
+  SampleRow v;
+  v.cut = 1;
+  v.lo = v.count = v.count_k = 0;
+  v.hi = v.bk = BINS - 1;      // the list is a beginning of the row's order
+  v.before = v.before_k = 0;
+  v.k = k;
+  const uint32_t found = l.flag ? CAP + 1 : l.taken;
+  __syncthreads();
+  finish_row(a, r, row, m, s, v, found, true, l);
+}
+
+template <class T>
+__global__ __launch_bounds__(ROW_THREADS) void k_sample_finish(SampleArgs a) {
+  __shared__ RowShared l;
+  const uint64_t r = block_id();
+  if (r >= a.work) return;
+  const T* row = static_cast<const T*>(a.logits) + r * a.ld;
+  const Settings s = a.settings[r];
+  const uint32_t k = small_k(a, r);
+  const float m = row_max(a, r);
+  if (m == -INFINITY) {
+    if (threadIdx.x == 0) write_token(a, r, -1, 0, 1);
+    return;
+  }
+  load_powers(l.table);
+  if (k) {
+    finish_small(a, r, row, m, s, k, l);
+    return;
+  }
+  SampleRow v;
+  v.cut = 0;
+  v.lo = BINS;
+  uint32_t n = 0;
+  if (a.row) v = a.row[r];
+  if (v.cut) {
+    n = a.collected[r];
+    for (uint32_t i = threadIdx.x; i < min(n, CAP); i += ROW_THREADS) l.code[i] = a.cand[r * CAP + i];
+    __syncthreads();
+  }
+  finish_row(a, r, row, m, s, v, n, v.cut && v.lo == 0, l);
+}
+
 struct SamplePlan {
-  uint32_t chunk = 0, chunks = 0, bits = 0;
-  bool cut = true;
-  size_t off_max = 0, off_sums = 0, off_count = 0, off_bins = 0, off_cand = 0, off_row = 0, total = 0;
+  uint32_t chunk = TILE, chunks = 0, slots = SLOTS, bits = 62;
+  bool cut = true;       // some row has a cut that is not a small top_k
+  bool small = false;    // some row's top_k is small
+  size_t off_max = 0, off_settings = 0, off_collected = 0, off_sums = 0, off_own = 0, off_own_count = 0, off_count = 0, off_bins = 0, off_cand = 0, off_row = 0,
+         total = 0;
 };
 
 SamplePlan sample_plan(const topk_sample_args& a) {
   SamplePlan p;
-  p.cut = a.top_ks || a.top_ps || a.temperatures || (a.top_k > 0 && a.top_k < a.n) || !(a.top_p >= 1.f) || !(a.temperature > 0.f);
-  p.chunk = 1024;
-  while (ceil_div(a.n, p.chunk) > MAX_CHUNKS || (p.chunk < 8192 && a.rows * ceil_div(a.n, p.chunk) > 1024)) p.chunk *= 2;
+  while (ceil_div(a.n, p.chunk) > MAX_CHUNKS) p.chunk *= 2;
   p.chunks = (uint32_t)ceil_div(a.n, p.chunk);
-  p.bits = 62;
   while ((int64_t(1) << (62 - p.bits)) < a.n) --p.bits;
+  // what the numbers among the settings say of all rows
+  const bool tile = p.chunk == TILE;
+  const bool greedy = !a.temperatures && !(a.temperature > 0.f);
+  const bool k_small = greedy || (!a.top_ks && a.top_k > 0 && a.top_k <= (int64_t)SMALL_K);
+  p.small = tile && (k_small || a.top_ks || a.temperatures);
+  const bool cuts = a.top_ks || (a.top_k > 0 && a.top_k < a.n) || a.top_ps || !(a.top_p >= 1.f) || greedy || (a.temperatures && !tile);
+  p.cut = cuts && !(tile && k_small);
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t here = at;
@@ -700,11 +970,19 @@ SamplePlan sample_plan(const topk_sample_args& a) {
   };
   const size_t rows = (size_t)a.rows;
   p.off_max = take(rows * p.chunks * 4);
-  p.off_sums = take(rows * p.chunks * 8);
+  p.off_settings = take(rows * sizeof(Settings));
+    p.off_sums = take(rows * p.chunks * 8);
+  if (p.small) {
+    if (k_small && !a.temperatures)
+      while (p.slots > 64 && p.slots >= 4 * (greedy ? 1 : a.top_k)) p.slots /= 2;
+    p.off_own = take(rows * p.chunks * p.slots * 8);
+    p.off_own_count = take(rows * p.chunks * 4);
+  }
   if (p.cut) {
     p.off_count = take(rows * BINS * 4);
     p.off_bins = take(rows * BINS * 8);
     p.off_cand = take(rows * CAP * 8);
+    p.off_collected = take(rows * 4);
     p.off_row = take(rows * sizeof(SampleRow));
   }
   p.total = at;
@@ -712,20 +990,17 @@ SamplePlan sample_plan(const topk_sample_args& a) {
 }
 
 template <class T>
-hipError_t sample_call(SampleArgs a, const SamplePlan& p, uint64_t rows, hipStream_t s) {
+hipError_t sample_call(SampleArgs a, const SamplePlan& p, const topk_sample_args& in, hipStream_t s) {
+  const uint64_t rows = (uint64_t)in.rows;
   a.work = rows * p.chunks;
-  const dim3 chunks = wide_grid(a.work), whole = wide_grid(rows);
-  SampleArgs by_row = a;
-  by_row.work = rows;
-  k_sample_max<T><<<chunks, CHUNK_THREADS, 0, s>>>(a);
-  if (p.cut) {
-    k_sample_hist<T><<<chunks, CHUNK_THREADS, 0, s>>>(a);
-    k_sample_plan<<<whole, ROW_THREADS, 0, s>>>(by_row);
-    k_sample_collect<T><<<chunks, CHUNK_THREADS, 0, s>>>(a);
-  } else {
-    k_sample_sum<T><<<chunks, CHUNK_THREADS, 0, s>>>(a);
-  }
-  k_sample_finish<T><<<whole, ROW_THREADS, 0, s>>>(by_row);
+  const dim3 chunks = wide_grid(a.work);
+  k_sample_first<T><<<chunks, FIRST_THREADS, 0, s>>>(a);
+  if (p.cut) k_sample_bins<T><<<chunks, ROW_THREADS, 0, s>>>(a);
+  const bool all_small = p.small && !p.cut && ((!in.temperatures && !(in.temperature > 0.f)) || in.top_k > 0);
+  if (p.cut) k_sample_collect<T, true><<<chunks, ROW_THREADS, 0, s>>>(a);
+  else if (!all_small) k_sample_collect<T, false><<<chunks, ROW_THREADS, 0, s>>>(a);
+  a.work = rows;
+  k_sample_finish<T><<<wide_grid(rows), ROW_THREADS, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -741,7 +1016,11 @@ hipError_t launch_sample(const topk_sample_args& in, void* ws, hipStream_t s) {
   a.logits = in.logits, a.u = in.u, a.tokens = in.tokens, a.logprobs = in.logprobs;
   a.temperatures = in.temperatures, a.top_ks = in.top_ks, a.top_ps = in.top_ps, a.min_ps = in.min_ps;
   a.maxima = reinterpret_cast<float*>(w + p.off_max);
+  a.settings = reinterpret_cast<Settings*>(w + p.off_settings);
+  a.collected = p.cut ? reinterpret_cast<uint32_t*>(w + p.off_collected) : nullptr;
   a.sums = reinterpret_cast<uint64_t*>(w + p.off_sums);
+  a.own = p.small ? reinterpret_cast<uint64_t*>(w + p.off_own) : nullptr;
+  a.own_count = p.small ? reinterpret_cast<uint32_t*>(w + p.off_own_count) : nullptr;
   a.bin_count = p.cut ? reinterpret_cast<uint32_t*>(w + p.off_count) : nullptr;
   a.bin_sum = p.cut ? reinterpret_cast<uint64_t*>(w + p.off_bins) : nullptr;
   a.cand = p.cut ? reinterpret_cast<uint64_t*>(w + p.off_cand) : nullptr;
@@ -750,8 +1029,8 @@ hipError_t launch_sample(const topk_sample_args& in, void* ws, hipStream_t s) {
   a.top_k = in.top_k;
   a.temperature = in.temperature, a.top_p = in.top_p, a.min_p = in.min_p;
   a.n = (uint32_t)in.n;
-  a.chunk = p.chunk, a.chunks = p.chunks, a.bits = p.bits;
-  return in.dtype == TOPK_BF16 ? sample_call<bf16_t>(a, p, (uint64_t)in.rows, s) : sample_call<float>(a, p, (uint64_t)in.rows, s);
+  a.chunk = p.chunk, a.chunks = p.chunks, a.slots = p.slots, a.bits = p.bits;
+  return in.dtype == TOPK_BF16 ? sample_call<bf16_t>(a, p, in, s) : sample_call<float>(a, p, in, s);
 }
 
 }  // namespace tk
