@@ -10,14 +10,15 @@
 // weights are whole multiples of 2^-F, F = 62 - ceil(log2 n), in 64 bits: sums
 // are exact, in whatever order and whatever pieces they are taken (atomics
 // included), and the comparisons with top_p and u are exact as well.  The
-// exponential is a table of 64 powers and a polynomial in 64-bit floats, off
-// by less than 2^-50 of its value.
+// exponential is a polynomial in 64-bit floats, off by less than 2^-50 of its
+// value.
 //
 // top_k and top_p keep a beginning of the one order, so together they are one
 // cut: a logit and an index.  A row is cut into chunks, a workgroup each:
 //
-//   k_sample_first    the chunks' maxima; where top_k is small, every chunk's
-//                     own largest entries too: the row's are among them
+//   k_sample_first    the chunks' maxima; where top_k is small, those of every
+//                     GROUP entries too: if k groups reach a bin, the k largest
+//                     entries lie in the bins up to it, and in such groups
 //   k_sample_bins     other rows with a cut: counts and sums of weights by bins
 //                     of m - z (its float's leading bits: 128 bins to an octave)
 //   k_sample_collect  from those the bins that the cut can lie in, their
@@ -46,8 +47,8 @@ constexpr uint32_t MAX_CHUNKS = 1024;       // of a row
 constexpr uint32_t BINS = 2048;             // 16 octaves of m - z from 2^-7 on, 128 to an octave
 constexpr uint32_t FIRST_BIN = (127 - 7) << 7;
 constexpr uint32_t CAP = 4096;              // entries of a row around its cut that are sorted
-constexpr uint32_t SMALL_K = 256;           // up to here every chunk picks its own entries,
-constexpr uint32_t SLOTS = 512;             // at most this many of them, and at least twice top_k
+constexpr uint32_t GROUP = TILE / FIRST_THREADS;   // entries of a thread of k_sample_first
+constexpr uint32_t SMALL_K = 1024;          // a small top_k: up to here, and of a row of four groups for each
 constexpr uint32_t PAIRS = 512;             // entries that are compared each with each rather than sorted
 
 // What is known of a row between the launches.
@@ -79,8 +80,7 @@ struct SampleArgs {
   float* maxima;          // [rows][chunks]
   Settings* settings;     // [rows]
   uint32_t* collected;    // [rows]: entries in `cand`, or more than CAP
-  uint64_t* own;          // [rows][chunks][slots]: a chunk's own entries, where top_k is small; null: it never is
-  uint32_t* own_count;    // [rows][chunks]
+  float* groups;          // [rows][chunks * FIRST_THREADS]: the groups' maxima, where top_k is small; null: it never is
   uint64_t* sums;         // [rows][chunks]: weight that surely stays
   uint32_t* bin_count;    // [rows][BINS]
   uint64_t* bin_sum;
@@ -89,7 +89,7 @@ struct SampleArgs {
   uint64_t ld, work;
   int64_t top_k;
   float temperature, top_p, min_p;
-  uint32_t n, chunk, chunks, slots, bits;   // bits: F
+  uint32_t n, chunk, chunks, bits;   // bits: F
 };
 
 __device__ __forceinline__ float temperature_of(const SampleArgs& a, uint64_t r) { return a.temperatures ? a.temperatures[r] : a.temperature; }
@@ -118,47 +118,30 @@ __device__ __forceinline__ float logit_of(const T* row, uint32_t i) {
   return z != z ? -INFINITY : z;
 }
 
-// 2^(j / 64).
-__device__ const double POWERS[64] = {
-    0x1.0000000000000p+0, 0x1.02c9a3e778061p+0, 0x1.059b0d3158574p+0, 0x1.0874518759bc8p+0,
-    0x1.0b5586cf9890fp+0, 0x1.0e3ec32d3d1a2p+0, 0x1.11301d0125b51p+0, 0x1.1429aaea92de0p+0,
-    0x1.172b83c7d517bp+0, 0x1.1a35beb6fcb75p+0, 0x1.1d4873168b9aap+0, 0x1.2063b88628cd6p+0,
-    0x1.2387a6e756238p+0, 0x1.26b4565e27cddp+0, 0x1.29e9df51fdee1p+0, 0x1.2d285a6e4030bp+0,
-    0x1.306fe0a31b715p+0, 0x1.33c08b26416ffp+0, 0x1.371a7373aa9cbp+0, 0x1.3a7db34e59ff7p+0,
-    0x1.3dea64c123422p+0, 0x1.4160a21f72e2ap+0, 0x1.44e086061892dp+0, 0x1.486a2b5c13cd0p+0,
-    0x1.4bfdad5362a27p+0, 0x1.4f9b2769d2ca7p+0, 0x1.5342b569d4f82p+0, 0x1.56f4736b527dap+0,
-    0x1.5ab07dd485429p+0, 0x1.5e76f15ad2148p+0, 0x1.6247eb03a5585p+0, 0x1.6623882552225p+0,
-    0x1.6a09e667f3bcdp+0, 0x1.6dfb23c651a2fp+0, 0x1.71f75e8ec5f74p+0, 0x1.75feb564267c9p+0,
-    0x1.7a11473eb0187p+0, 0x1.7e2f336cf4e62p+0, 0x1.82589994cce13p+0, 0x1.868d99b4492edp+0,
-    0x1.8ace5422aa0dbp+0, 0x1.8f1ae99157736p+0, 0x1.93737b0cdc5e5p+0, 0x1.97d829fde4e50p+0,
-    0x1.9c49182a3f090p+0, 0x1.a0c667b5de565p+0, 0x1.a5503b23e255dp+0, 0x1.a9e6b5579fdbfp+0,
-    0x1.ae89f995ad3adp+0, 0x1.b33a2b84f15fbp+0, 0x1.b7f76f2fb5e47p+0, 0x1.bcc1e904bc1d2p+0,
-    0x1.c199bdd85529cp+0, 0x1.c67f12e57d14bp+0, 0x1.cb720dcef9069p+0, 0x1.d072d4a07897cp+0,
-    0x1.d5818dcfba487p+0, 0x1.da9e603db3285p+0, 0x1.dfc97337b9b5fp+0, 0x1.e502ee78b3ff6p+0,
-    0x1.ea4afa2a490dap+0, 0x1.efa1bee615a27p+0, 0x1.f50765b6e4540p+0, 0x1.fa7c1819e90d8p+0};
-
-__device__ __forceinline__ void load_powers(double* table) {
-  if (threadIdx.x < 64) table[threadIdx.x] = POWERS[threadIdx.x];
-  __syncthreads();
-}
-
-// The weight of a logit as a float, and in multiples of 2^-bits.  t = log2 of
-// the weight is split into j / 64 and |f| <= 1/128; the polynomial of 2^f has
-// the coefficients ln(2)^i / i!, and (f ln 2)^6 / 720 < 2^-54 is left out.
-__device__ __forceinline__ double weight_of(float z, float m, const Settings& s, const double* table) {
+// The weight of a logit: 2^t, t = (z - m) log2(e) / temperature, as 2^i times a
+// polynomial in f = t - i, |f| <= 1/2, with the coefficients ln(2)^j / j!; the
+// first one left out is below 2^-57.
+__device__ __forceinline__ double weight_of(float z, float m, const Settings& s) {
   if (z == m) return 1.0;
   if (s.greedy) return 0.0;
   const double t = ((double)z - (double)m) * s.rate;
   if (!(t > -64.0)) return 0.0;   // below half of 2^-62
-  const double q = rint(t * 64.0);
-  const double f = fma(q, -0.015625, t);
-  const int i = (int)q;
-  double p = fma(f, 0.0013333558146428443, 0.0096181291076284772);
-  p = fma(f, p, 0.055504108664821580);
-  p = fma(f, p, 0.24022650695910071);
-  p = fma(f, p, 0.69314718055994531);
+  const double i = rint(t), f = t - i;
+  double p = 1.3691488853904128e-12;
+  p = fma(f, p, 2.5678435993488206e-11);
+  p = fma(f, p, 4.4455382718708116e-10);
+  p = fma(f, p, 7.054911620801123e-09);
+  p = fma(f, p, 1.01780860092397e-07);
+  p = fma(f, p, 1.321548679014431e-06);
+  p = fma(f, p, 1.5252733804059841e-05);
+  p = fma(f, p, 0.0001540353039338161);
+  p = fma(f, p, 0.0013333558146428443);
+  p = fma(f, p, 0.009618129107628477);
+  p = fma(f, p, 0.05550410866482158);
+  p = fma(f, p, 0.24022650695910072);
+  p = fma(f, p, 0.6931471805599453);
   p = fma(f, p, 1.0);
-  return ldexp(table[i & 63] * p, i >> 6);
+  return ldexp(p, (int)i);
 }
 __device__ __forceinline__ uint64_t fixed_of(double w, uint32_t bits) { return (uint64_t)rint(ldexp(w, (int)bits)); }
 
@@ -228,12 +211,20 @@ __device__ __forceinline__ float row_max(const SampleArgs& a, uint64_t r) {
   return m;
 }
 
-// top_k of a row whose chunks pick their own entries; 0: they do not.
+// A row whose k is at most this gets its first k by way of its groups: not many
+// entries reach what k of many groups do, and all entries of a short row can be
+// sorted.
+__host__ __device__ __forceinline__ int64_t small_limit(int64_t n) {
+  const int64_t k = n <= (int64_t)CAP ? n : n / (4 * GROUP);
+  return k < (int64_t)SMALL_K ? k : (int64_t)SMALL_K;
+}
+
+// top_k of such a row; 0: it is none.
 __device__ __forceinline__ uint32_t small_k(const SampleArgs& a, uint64_t r) {
-  if (!a.own) return 0;
+  if (!a.groups) return 0;
   if (!(temperature_of(a, r) > 0.f)) return 1;
   const int64_t k = a.top_ks ? a.top_ks[r] : a.top_k;
-  return k > 0 && k <= (int64_t)SMALL_K ? (uint32_t)k : 0u;
+  return k > 0 && k <= small_limit(a.n) ? (uint32_t)k : 0u;
 }
 
 // Exclusive sums over the threads of a workgroup; *total: of all.
@@ -305,8 +296,6 @@ __device__ __forceinline__ uint32_t bin_reaching(const uint32_t* count, uint32_t
 template <class T>
 __global__ __launch_bounds__(FIRST_THREADS) void k_sample_first(SampleArgs a) {
   __shared__ float part[FIRST_THREADS / 64];
-  __shared__ uint32_t count[BINS];
-  __shared__ uint32_t part32[FIRST_THREADS / 64], found, taken;
   const uint64_t id = block_id();
   if (id >= a.work) return;
   const uint64_t r = id / a.chunks;
@@ -315,67 +304,34 @@ __global__ __launch_bounds__(FIRST_THREADS) void k_sample_first(SampleArgs a) {
   const uint32_t i0 = c * a.chunk, i1 = min(i0 + a.chunk, a.n);
   Tile<T, FIRST_THREADS> tile;
   tile.load(row, i0, i1);
-  const uint32_t k = small_k(a, r);
-  if (k)
-    for (uint32_t i = threadIdx.x; i < BINS; i += FIRST_THREADS) count[i] = 0;
+  const bool bins = a.bin_count && !small_k(a, r);
   float m = -INFINITY;
   for (uint32_t at = i0;;) {
 #pragma unroll
-    for (uint32_t j = 0; j < tile.PER; ++j) m = fmaxf(m, tile.z[j]);
+    for (uint32_t j = 0; j < GROUP; ++j) m = fmaxf(m, tile.z[j]);
     at += TILE;
     if (at >= i1) break;
     tile.load(row, at, i1);
   }
-  const float mine = m;
+  if (a.groups) a.groups[id * FIRST_THREADS + threadIdx.x] = m;   // one tile is the whole chunk here
 #pragma unroll
   for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
   if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = m;
-  if (threadIdx.x == 0) taken = 0;
+  if (bins)   // the chunks of a row share the clearing of its bins
+    for (uint32_t i = c * FIRST_THREADS + threadIdx.x; i < BINS; i += a.chunks * FIRST_THREADS) {
+      a.bin_count[r * BINS + i] = 0;
+      a.bin_sum[r * BINS + i] = 0;
+    }
   __syncthreads();
-#pragma unroll
-  for (uint32_t w = 0; w < FIRST_THREADS / 64; ++w) m = fmaxf(m, part[w]);
   if (threadIdx.x == 0) {
+#pragma unroll
+    for (uint32_t w = 1; w < FIRST_THREADS / 64; ++w) m = fmaxf(m, part[w]);
     a.maxima[id] = m;
     if (c == 0) {
       a.settings[r] = make_settings(a, r);
       if (a.collected) a.collected[r] = 0;
     }
   }
-  if (!k) {
-    if (a.bin_count)   // the chunks of a row share the clearing of its bins
-      for (uint32_t i = c * FIRST_THREADS + threadIdx.x; i < BINS; i += a.chunks * FIRST_THREADS) {
-        a.bin_count[r * BINS + i] = 0;
-        a.bin_sum[r * BINS + i] = 0;
-      }
-    return;
-  }
-  // One tile is the whole chunk here.  If k threads' largest entries lie in the
-  // bins up to one, so do the chunk's k largest entries; for small k not many
-  // others do.  Where they are too many for the slots, the bins of all entries
-  // are counted.  Bins are counted from the chunk's own maximum.
-  if (live(mine, m)) atomicAdd(&count[bin_of(mine, m)], 1u);
-  __syncthreads();
-  uint32_t last = bin_reaching<FIRST_THREADS>(count, k, part32, &found);
-  for (uint32_t round = 0;; ++round) {
-    const float below = bin_end(last);
-#pragma unroll
-    for (uint32_t j = 0; j < tile.PER; ++j)
-      if (m - tile.z[j] < below || (tile.z[j] == m && m > -INFINITY)) {
-        const uint32_t slot = atomicAdd(&taken, 1u);
-        if (slot < a.slots) a.own[id * a.slots + slot] = code_of(tile.z[j], tile.index(i0, j));
-      }
-    __syncthreads();
-    if (round || taken <= a.slots) break;
-    for (uint32_t i = threadIdx.x; i < BINS; i += FIRST_THREADS) count[i] = 0;
-    __syncthreads();
-#pragma unroll
-    for (uint32_t j = 0; j < tile.PER; ++j)
-      if (live(tile.z[j], m) && bin_of(tile.z[j], m) <= last) atomicAdd(&count[bin_of(tile.z[j], m)], 1u);
-    if (threadIdx.x == 0) taken = 0;
-    __syncthreads();
-    last = bin_reaching<FIRST_THREADS>(count, k, part32, &found);
-  }
-  if (threadIdx.x == 0) a.own_count[id] = taken;   // beyond the slots: too many equal ones
 }
 
 // From a row's bins: where its cut can lie.  Every workgroup of the row finds it
@@ -455,7 +411,6 @@ template <class T>
 __global__ __launch_bounds__(ROW_THREADS) void k_sample_bins(SampleArgs a) {
   __shared__ uint64_t sum[BINS];
   __shared__ uint32_t count[BINS];
-  __shared__ double table[64];
   const uint64_t id = block_id();
   if (id >= a.work) return;
   const uint64_t r = id / a.chunks;
@@ -467,7 +422,6 @@ __global__ __launch_bounds__(ROW_THREADS) void k_sample_bins(SampleArgs a) {
   Tile<T, ROW_THREADS> tile;
   tile.load(row, i0, i1);
   for (uint32_t i = threadIdx.x; i < BINS; i += ROW_THREADS) sum[i] = count[i] = 0;
-  load_powers(table);
   const float m = row_max(a, r);
   for (uint32_t at = i0;;) {
 #pragma unroll
@@ -476,7 +430,7 @@ __global__ __launch_bounds__(ROW_THREADS) void k_sample_bins(SampleArgs a) {
       if (!live(z, m)) continue;
       const uint32_t b = bin_of(z, m);
       atomicAdd(&count[b], 1u);
-      const uint64_t w = fixed_of(weight_of(z, m, s, table), a.bits);
+      const uint64_t w = fixed_of(weight_of(z, m, s), a.bits);
       if (w) atomicAdd(reinterpret_cast<unsigned long long*>(&sum[b]), (unsigned long long)w);
     }
     at += TILE;
@@ -497,7 +451,6 @@ __global__ __launch_bounds__(ROW_THREADS) void k_sample_collect(SampleArgs a) {
   __shared__ uint64_t code[CUT ? TILE : 1];            // the plan's sums, then the entries to be handed on
   __shared__ uint32_t counts[CUT ? BINS + 1 : 1];
   static_assert(TILE > BINS, "the plan's sums fit");
-  __shared__ double table[64];
   __shared__ uint32_t part32[ROW_WAVES], mark[3], taken, base;
   __shared__ uint64_t part64[ROW_WAVES];
   const uint64_t id = block_id();
@@ -512,7 +465,6 @@ __global__ __launch_bounds__(ROW_THREADS) void k_sample_collect(SampleArgs a) {
   tile.load(row, i0, i1);
   const float m = row_max(a, r);
   if (threadIdx.x == 0) taken = 0;
-  load_powers(table);
   SampleRow v;
   v.cut = 0;
   v.lo = v.hi = v.bk = BINS;
@@ -529,7 +481,7 @@ __global__ __launch_bounds__(ROW_THREADS) void k_sample_collect(SampleArgs a) {
       const uint32_t b = v.cut && live(z, m) ? bin_of(z, m) : 0u;
       const bool sure = !(m - z > s.far) && z > -INFINITY && (!v.cut || b < v.lo);
       if (__any(sure)) {   // few waves hold a weight that counts
-        const double w = weight_of(z, m, s, table);
+        const double w = weight_of(z, m, s);
         if (sure && w >= min_p) sum += fixed_of(w, a.bits);
       }
       if constexpr (CUT)
@@ -563,7 +515,7 @@ __global__ __launch_bounds__(ROW_THREADS) void k_sample_collect(SampleArgs a) {
 // only codes from there on count.  by_count: the entry of rank `want` - 1;
 // otherwise the last entry with less than `want` weight before it.
 template <class T>
-__device__ uint64_t select_code(const SampleArgs& a, const T* row, float m, const Settings& s, const double* table,
+__device__ uint64_t select_code(const SampleArgs& a, const T* row, float m, const Settings& s,
                                 uint64_t allowed, bool by_count, uint64_t want, uint64_t* hist, uint64_t* found) {
   uint64_t prefix = 0, base = 0;
   const uint32_t t = threadIdx.x;
@@ -575,7 +527,7 @@ __device__ uint64_t select_code(const SampleArgs& a, const T* row, float m, cons
       if (!live(z, m)) continue;
       const uint64_t c = code_of(z, i);
       if (c < allowed || (shift < 56 && (c ^ prefix) >> (shift + 8))) continue;
-      const uint64_t w = by_count ? 1 : fixed_of(weight_of(z, m, s, table), a.bits);
+      const uint64_t w = by_count ? 1 : fixed_of(weight_of(z, m, s), a.bits);
       if (w) atomicAdd(reinterpret_cast<unsigned long long*>(&hist[c >> shift & 255]), (unsigned long long)w);
     }
     __syncthreads();
@@ -605,27 +557,25 @@ __device__ uint64_t select_code(const SampleArgs& a, const T* row, float m, cons
 // Sum of the weights that stay in entries [i0, i1), by a wave.
 template <class T>
 __device__ __forceinline__ uint64_t staying(const SampleArgs& a, const T* row, uint32_t i0, uint32_t i1, float m, const Settings& s,
-                                            double min_p, uint64_t cut, const double* table) {
+                                            double min_p, uint64_t cut) {
   uint64_t sum = 0;
   for (uint32_t i = i0 + threadIdx.x % 64; i < i1; i += 64) {
     const float z = logit_of(row, i);
     if (!live(z, m) || code_of(z, i) < cut) continue;
-    const double w = weight_of(z, m, s, table);
+    const double w = weight_of(z, m, s);
     if (w >= min_p) sum += fixed_of(w, a.bits);
   }
   return wave_sum(sum);
 }
 
 // What a workgroup that ends a row keeps in LDS.
-struct RowShared {
+struct alignas(16) RowShared {
   uint64_t code[CAP];
+  uint64_t sorted[PAIRS], pair[PAIRS];
   uint64_t sums[MAX_CHUNKS];   // weight that stays, by chunk
-  uint64_t sorted[PAIRS];
   uint64_t part64[ROW_WAVES], found[2], rest;
   uint32_t count[BINS];
-  uint32_t rank[PAIRS];
   uint32_t part32[ROW_WAVES], pick, taken, flag;
-  double table[64];
 };
 
 __device__ __forceinline__ void write_token(const SampleArgs& a, uint64_t r, int64_t token, uint64_t w, uint64_t all) {
@@ -633,25 +583,46 @@ __device__ __forceinline__ void write_token(const SampleArgs& a, uint64_t r, int
   a.logprobs[r] = token < 0 ? -INFINITY : (float)log((double)w / (double)all);
 }
 
+// Each of the n <= PAIRS threads' value: the sum over all j < n of what `take`
+// says of l.code[j], l.sorted[j].  All threads share the pairs.
+template <class F>
+__device__ __forceinline__ uint64_t over_pairs(RowShared& l, uint32_t n, F take) {
+  constexpr uint32_t AHEAD = 8;
+  const uint32_t t = threadIdx.x;
+  uint32_t shift = 0;      // entries rounded up to a power of two, 1 << shift
+  while ((1u << shift) < n) ++shift;
+  const uint32_t i = t & ((1u << shift) - 1), parts = ROW_THREADS >> shift, part = t >> shift;
+  const uint32_t end = (n + AHEAD - 1) / AHEAD * AHEAD;     // zeros from n on
+  const uint32_t per = (end / AHEAD + parts - 1) / parts * AHEAD, j0 = part * per, j1 = min(j0 + per, end);
+  if (t < PAIRS) l.pair[t] = 0;
+  if (n + t < end) l.code[n + t] = l.sorted[n + t] = 0;
+  __syncthreads();
+  if (i < n) {
+    const uint64_t own = l.code[i];
+    uint64_t sum = 0;
+    for (uint32_t j = j0; j < j1; j += AHEAD) {
+      uint64_t c[AHEAD], w[AHEAD];
+#pragma unroll
+      for (uint32_t x = 0; x < AHEAD; ++x) {
+        c[x] = l.code[j + x];
+        w[x] = l.sorted[j + x];
+      }
+#pragma unroll
+      for (uint32_t x = 0; x < AHEAD; ++x) sum += take(own, c[x], w[x]);
+    }
+    if (parts == 1) l.pair[i] = sum;
+    else if (sum) atomicAdd(reinterpret_cast<unsigned long long*>(&l.pair[i]), (unsigned long long)sum);
+  }
+  __syncthreads();
+  return t < n ? l.pair[t] : 0;
+}
+
 // The n entries of l.code in order, the first ones first.
 __device__ __forceinline__ void sort_codes(RowShared& l, uint32_t n) {
   const uint32_t t = threadIdx.x;
-  if (n <= PAIRS) {
-    // an entry's rank is the number of larger ones: threads share the comparisons
-    uint32_t shift = 0;      // entries rounded up to a power of two, 1 << shift
-    while ((1u << shift) < n) ++shift;
-    const uint32_t i = t & ((1u << shift) - 1), parts = ROW_THREADS >> shift, part = t >> shift;
-    const uint32_t per = (n + parts - 1) / parts, j0 = part * per, j1 = min(j0 + per, n);
-    if (t < PAIRS) l.rank[t] = 0;
-    __syncthreads();
-    if (i < n) {
-      const uint64_t own = l.code[i];
-      uint32_t above = 0;
-      for (uint32_t j = j0; j < j1; ++j) above += l.code[j] > own;
-      if (above) atomicAdd(&l.rank[i], above);
-    }
-    __syncthreads();
-    if (t < n) l.sorted[l.rank[t]] = l.code[t];
+  if (n <= PAIRS) {   // an entry's place is the number of larger ones
+    const uint64_t place = over_pairs(l, n, [](uint64_t own, uint64_t c, uint64_t) { return (uint64_t)(c > own); });
+    if (t < n) l.sorted[place] = l.code[t];
     __syncthreads();
     if (t < n) l.code[t] = l.sorted[t];
     __syncthreads();
@@ -675,6 +646,44 @@ __device__ __forceinline__ void sort_codes(RowShared& l, uint32_t n) {
     }
 }
 
+// floor(u * all), of a u outside [0, 1) its end.
+__device__ __forceinline__ uint64_t target_of(float u, uint64_t all) {
+  if (!(u < 1.f)) return all - 1;
+  if (!(u > 0.f)) return 0;
+  uint64_t target, up;
+  scaled(u, all, &target, &up);
+  return target;
+}
+
+// The end of a row all of whose entries that can stay are in l.code, at most
+// PAIRS, one to a thread: sorted, cut, and the token found from each entry's sum
+// over those of lower index.
+__device__ void finish_few(const SampleArgs& a, uint64_t r, float m, const Settings& s, const SampleRow& v, uint32_t n, float p,
+                           double min_p, float u, RowShared& l) {
+  const uint32_t t = threadIdx.x;
+  sort_codes(l, n);
+  const uint64_t code = t < n ? l.code[t] : 0;
+  const double f = t < n ? weight_of(logit_of_code(code), m, s) : 0.0;
+  const uint64_t w = fixed_of(f, a.bits);
+  uint64_t all;
+  const uint64_t before = thread_scan<ROW_THREADS>(w, l.part64, &all);
+  if (t == 0) l.found[0] = all;
+  __syncthreads();
+  if (v.k && t == v.k) l.found[0] = before;   // the sum of the first k
+  __syncthreads();
+  const bool in = t < n && !(v.k && t >= v.k) && before < limit_of(p, v.k ? l.found[0] : v.before_k);
+  const uint64_t mine = in && f >= min_p ? w : 0;
+  if (t < PAIRS) l.sorted[t] = mine;
+  thread_scan<ROW_THREADS>(mine, l.part64, &all);   // waits for l.sorted as well
+  if (all == 0) {      // a min_p of NaN: nothing stays
+    if (t == 0) write_token(a, r, -1, 0, 1);
+    return;
+  }
+  const uint64_t target = target_of(u, all);
+  const uint64_t lower = over_pairs(l, n, [](uint64_t own, uint64_t c, uint64_t x) { return ~(uint32_t)c < ~(uint32_t)own ? x : 0; });
+  if (mine && lower <= target && target < lower + mine) write_token(a, r, ~(uint32_t)code, mine, all);
+}
+
 // The end of a row.  n_cand entries around the cut are in l.code (more than
 // CAP: they are not, and the whole row is gone through again); `inside`: all
 // that can stay is among them, and the chunks' sums are 0.
@@ -683,13 +692,16 @@ __device__ void finish_row(const SampleArgs& a, uint64_t r, const T* row, float 
                            uint32_t n_cand, bool inside, RowShared& l) {
   const uint32_t t = threadIdx.x;
   const double min_p = min_p_of(a, r);
-  const double* table = l.table;
   const float u = a.u[r];
   uint64_t cut = 0;
   bool whole = false;       // the chunks' sums have to be taken anew
   uint32_t staying_cands = 0;
   if (v.cut) {
     const float p = top_p_of(a, r);
+    if (inside && n_cand <= PAIRS) {
+      finish_few(a, r, m, s, v, n_cand, p, min_p, u, l);
+      return;
+    }
     if (n_cand <= CAP) {
       sort_codes(l, n_cand);
       // consecutive entries to a thread: their weights' sums, and where the k-th is
@@ -699,7 +711,7 @@ __device__ void finish_row(const SampleArgs& a, uint64_t r, const T* row, float 
       uint32_t low = 0;     // entries of bins up to hi: before those of a bin bk beyond
       for (uint32_t x = x0; x < x1; ++x) {
         const float z = logit_of_code(l.code[x]);
-        own += fixed_of(weight_of(z, m, s, table), a.bits);
+        own += fixed_of(weight_of(z, m, s), a.bits);
         low += bin_of(z, m) <= v.hi;
       }
       const uint64_t at = thread_scan<ROW_THREADS>(own, l.part64, &all);
@@ -719,7 +731,7 @@ __device__ void finish_row(const SampleArgs& a, uint64_t r, const T* row, float 
         for (uint32_t x = x0; x < x1; ++x) {
           if (x == bk_at) l.found[0] = run;
           if (x == k_at) l.found[1] = run;
-          run += fixed_of(weight_of(logit_of_code(l.code[x]), m, s, table), a.bits);
+          run += fixed_of(weight_of(logit_of_code(l.code[x]), m, s), a.bits);
         }
       __syncthreads();
       const uint64_t bk_start = l.found[0];
@@ -730,48 +742,22 @@ __device__ void finish_row(const SampleArgs& a, uint64_t r, const T* row, float 
         const uint64_t before = apart && x >= lows ? v.before_k + (run - bk_start) : v.before + run;
         const bool in_k = v.bk >= BINS || x < k_at;
         if (in_k && before < limit) atomicMax(&l.pick, x);
-        run += fixed_of(weight_of(logit_of_code(l.code[x]), m, s, table), a.bits);
+        run += fixed_of(weight_of(logit_of_code(l.code[x]), m, s), a.bits);
       }
       __syncthreads();
       staying_cands = l.pick + 1;
       cut = l.code[l.pick];
       __syncthreads();
-      if (inside && staying_cands <= PAIRS) {
-        // few: the sum before an entry, by index, is over those of lower index
-        const bool mine = t < staying_cands;
-        uint64_t w = 0;
-        if (mine) {
-          const double f = weight_of(logit_of_code(l.code[t]), m, s, table);
-          w = f >= min_p ? fixed_of(f, a.bits) : 0;
-          l.sorted[t] = w;
-        }
-        thread_scan<ROW_THREADS>(w, l.part64, &all);   // waits for l.sorted as well
-        if (all == 0) {      // a min_p of NaN: nothing stays
-          if (t == 0) write_token(a, r, -1, 0, 1);
-          return;
-        }
-        uint64_t target, up;
-        if (!(u < 1.f)) target = all - 1;      // the last one
-        else if (!(u > 0.f)) target = 0;
-        else scaled(u, all, &target, &up);
-        if (w) {
-          const uint32_t own_index = ~(uint32_t)l.code[t];
-          uint64_t before = 0;
-          for (uint32_t j = 0; j < staying_cands; ++j) before += ~(uint32_t)l.code[j] < own_index ? l.sorted[j] : 0;
-          if (before <= target && target < before + w) write_token(a, r, own_index, w, all);
-        }
-        return;
-      }
     } else {
-      if (v.bk < BINS) cut = select_code(a, row, m, s, table, 0, true, v.k, l.sums, l.found);
+      if (v.bk < BINS) cut = select_code(a, row, m, s, 0, true, v.k, l.sums, l.found);
       if (!(p >= 1.f)) {
         uint64_t mine = 0, all;
         for (uint32_t c = t / 64; c < a.chunks; c += ROW_WAVES) {
           const uint32_t i0 = c * a.chunk;
-          mine += staying(a, row, i0, min(i0 + a.chunk, a.n), m, s, -1.0, cut, table);
+          mine += staying(a, row, i0, min(i0 + a.chunk, a.n), m, s, -1.0, cut);
         }
         thread_scan<ROW_THREADS>(t % 64 ? uint64_t(0) : mine, l.part64, &all);
-        cut = select_code(a, row, m, s, table, cut, false, limit_of(p, all), l.sums, l.found);
+        cut = select_code(a, row, m, s, cut, false, limit_of(p, all), l.sums, l.found);
       }
       whole = true;
     }
@@ -780,7 +766,7 @@ __device__ void finish_row(const SampleArgs& a, uint64_t r, const T* row, float 
   if (whole) {
     for (uint32_t c = t / 64; c < a.chunks; c += ROW_WAVES) {
       const uint32_t i0 = c * a.chunk;
-      const uint64_t sum = staying(a, row, i0, min(i0 + a.chunk, a.n), m, s, min_p, cut, table);
+      const uint64_t sum = staying(a, row, i0, min(i0 + a.chunk, a.n), m, s, min_p, cut);
       if (t % 64 == 0) l.sums[c] = sum;
     }
   } else {
@@ -788,7 +774,7 @@ __device__ void finish_row(const SampleArgs& a, uint64_t r, const T* row, float 
     __syncthreads();
     for (uint32_t i = t; i < staying_cands; i += ROW_THREADS) {
       const uint64_t x = l.code[i];
-      const double w = weight_of(logit_of_code(x), m, s, table);
+      const double w = weight_of(logit_of_code(x), m, s);
       if (w >= min_p) atomicAdd(reinterpret_cast<unsigned long long*>(&l.sums[~(uint32_t)x / a.chunk]), (unsigned long long)fixed_of(w, a.bits));
     }
   }
@@ -802,10 +788,7 @@ __device__ void finish_row(const SampleArgs& a, uint64_t r, const T* row, float 
     if (t == 0) write_token(a, r, -1, 0, 1);
     return;
   }
-  uint64_t target, up;
-  if (!(u < 1.f)) target = all - 1;      // the last one
-  else if (!(u > 0.f)) target = 0;
-  else scaled(u, all, &target, &up);
+  const uint64_t target = target_of(u, all);
 #pragma unroll
   for (uint32_t i = 0; i < SUMS; ++i) {
     if (before <= target && target < before + own[i]) {
@@ -821,13 +804,20 @@ __device__ void finish_row(const SampleArgs& a, uint64_t r, const T* row, float 
   constexpr uint32_t PER = TILE / ROW_THREADS;
   for (uint32_t i0 = l.pick * a.chunk; i0 < i1; i0 += TILE) {
     const uint32_t j0 = i0 + t * PER;
+    float z[PER];
+    if (j0 + PER <= i1) {
+#pragma unroll
+      for (uint32_t j = 0; j < PER; j += Vec<T>::N) Vec<T>::load(row + j0 + j, z + j);
+    } else {
+#pragma unroll
+      for (uint32_t j = 0; j < PER; ++j) z[j] = j0 + j < i1 ? to_f32(row[j0 + j]) : -INFINITY;
+    }
     uint64_t w[PER], sum = 0, tile_all;
 #pragma unroll
     for (uint32_t j = 0; j < PER; ++j) {
-      const float z = j0 + j < i1 ? logit_of(row, j0 + j) : -INFINITY;
       w[j] = 0;
-      if (live(z, m) && code_of(z, j0 + j) >= cut) {
-        const double f = weight_of(z, m, s, table);
+      if (!(m - z[j] > s.far) && live(z[j], m) && code_of(z[j], j0 + j) >= cut) {
+        const double f = weight_of(z[j], m, s);
         if (f >= min_p) w[j] = fixed_of(f, a.bits);
       }
       sum += w[j];
@@ -847,68 +837,84 @@ __device__ void finish_row(const SampleArgs& a, uint64_t r, const T* row, float 
   }
 }
 
-// A row whose chunks picked their own entries: of those, the bins that hold the first k.
+// A row with a small top_k: the bin that k groups reach, those groups, and
+// their entries in the bins up to it.
 template <class T>
 __device__ void finish_small(const SampleArgs& a, uint64_t r, const T* row, float m, const Settings& s, uint32_t k, RowShared& l) {
-  constexpr uint32_t PER = MAX_CHUNKS / ROW_THREADS, AHEAD = 4;
-  const uint32_t t = threadIdx.x, wave = t / 64, lane = t % 64;
-  const uint32_t* counts = a.own_count + r * a.chunks;
-  const uint64_t* lists = a.own + r * a.chunks * a.slots;
-  uint32_t n[PER], own = 0, total;
+  constexpr uint32_t VEC = Vec<T>::N, VECS = GROUP / VEC, AHEAD = 4;
+  const uint32_t t = threadIdx.x;
+  const uint32_t groups = a.chunks * FIRST_THREADS;      // a multiple of 256
+  const float* tops = a.groups + r * groups;
+  constexpr uint32_t BATCH = ROW_THREADS * 4 * AHEAD;
+  f32x4 v[AHEAD];
+  auto load = [&](uint32_t g0) {
 #pragma unroll
-  for (uint32_t i = 0; i < PER; ++i) own += n[i] = t * PER + i < a.chunks ? counts[t * PER + i] : 0u;
+    for (uint32_t i = 0; i < AHEAD; ++i) {
+      v[i] = f32x4{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      if (g0 + i * ROW_THREADS * 4 < groups) v[i] = *reinterpret_cast<const f32x4*>(tops + g0 + i * ROW_THREADS * 4);
+    }
+  };
+  load(t * 4);
   for (uint32_t i = t; i < BINS; i += ROW_THREADS) l.count[i] = 0;
   if (t == 0) l.taken = l.flag = 0;
-  thread_scan<ROW_THREADS>(own, l.part32, &total);
-  uint32_t* number = reinterpret_cast<uint32_t*>(l.sums);   // entries of each chunk
-#pragma unroll
-  for (uint32_t i = 0; i < PER; ++i) {
-    number[t * PER + i] = min(n[i], a.slots);
-    if (n[i] > a.slots) l.flag = 1;
-  }
   __syncthreads();
-  // by a wave for a chunk, AHEAD rounds of 64 entries in flight (a chunk has at most SLOTS)
-  for (uint32_t c = wave; c < a.chunks; c += ROW_WAVES) {
-    const uint32_t have = number[c];
-    for (uint32_t i0 = lane; i0 < have; i0 += 64 * AHEAD) {
-      uint64_t code[AHEAD];
+  for (uint32_t g0 = t * 4;;) {
 #pragma unroll
-      for (uint32_t i = 0; i < AHEAD; ++i) code[i] = i0 + 64 * i < have ? lists[(uint64_t)c * a.slots + i0 + 64 * i] : 0;
+    for (uint32_t i = 0; i < AHEAD; ++i)
 #pragma unroll
-      for (uint32_t i = 0; i < AHEAD; ++i) {
-        const float z = logit_of_code(code[i]);
-        if (i0 + 64 * i < have && live(z, m)) atomicAdd(&l.count[bin_of(z, m)], 1u);
-      }
-    }
+      for (uint32_t j = 0; j < 4; ++j)
+        if (live(v[i][j], m)) atomicAdd(&l.count[bin_of(v[i][j], m)], 1u);
+    g0 += BATCH;
+    if (g0 >= groups) break;
+    load(g0);
   }
   __syncthreads();
   const uint32_t last = bin_reaching<ROW_THREADS>(l.count, k, l.part32, &l.pick);
-  for (uint32_t c = wave; c < a.chunks; c += ROW_WAVES) {
-    const uint32_t have = number[c];
-    for (uint32_t i0 = lane; i0 < have; i0 += 64 * AHEAD) {
-      uint64_t code[AHEAD];
+  const float below = bin_end(last);
+  auto near = [&](float z) { return m - z < below || z == m; };   // m > -inf
+  uint32_t* hits = reinterpret_cast<uint32_t*>(l.sums);           // 2 * MAX_CHUNKS of them
+  for (uint32_t g0 = t * 4; g0 < groups; g0 += BATCH) {
+    if (groups > BATCH) load(g0);
 #pragma unroll
-      for (uint32_t i = 0; i < AHEAD; ++i) code[i] = i0 + 64 * i < have ? lists[(uint64_t)c * a.slots + i0 + 64 * i] : 0;
+    for (uint32_t i = 0; i < AHEAD; ++i)
 #pragma unroll
-      for (uint32_t i = 0; i < AHEAD; ++i) {
-        const float z = logit_of_code(code[i]);
-        if (i0 + 64 * i < have && live(z, m) && bin_of(z, m) <= last) {
-          const uint32_t at = atomicAdd(&l.taken, 1u);
-          if (at < CAP) l.code[at] = code[i];
+      for (uint32_t j = 0; j < 4; ++j)
+        if (near(v[i][j])) {
+          const uint32_t at = atomicAdd(&l.flag, 1u);
+          if (at < 2 * MAX_CHUNKS) hits[at] = g0 + i * ROW_THREADS * 4 + j;
         }
+  }
+  __syncthreads();
+  const uint32_t found = l.flag;
+  if (found <= 2 * MAX_CHUNKS) {
+    for (uint32_t x = t; x < found * VECS; x += ROW_THREADS) {
+      const uint32_t g = hits[x / VECS];
+      const uint32_t i0 = g / FIRST_THREADS * TILE + (x % VECS * FIRST_THREADS + g % FIRST_THREADS) * VEC;
+      float z[VEC];
+      if (i0 + VEC <= a.n) {
+        Vec<T>::load(row + i0, z);
+      } else {
+#pragma unroll
+        for (uint32_t j = 0; j < VEC; ++j) z[j] = i0 + j < a.n ? to_f32(row[i0 + j]) : -INFINITY;
       }
+#pragma unroll
+      for (uint32_t j = 0; j < VEC; ++j)
+        if (near(z[j])) {
+          const uint32_t at = atomicAdd(&l.taken, 1u);
+          if (at < CAP) l.code[at] = code_of(z[j], i0 + j);
+        }
     }
   }
   __syncthreads();
-  SampleRow v;
-  v.cut = 1;
-  v.lo = v.count = v.count_k = 0;
-  v.hi = v.bk = BINS - 1;      // the list is a beginning of the row's order
-  v.before = v.before_k = 0;
-  v.k = k;
-  const uint32_t found = l.flag ? CAP + 1 : l.taken;
+  SampleRow w;
+  w.cut = 1;
+  w.lo = w.count = w.count_k = 0;
+  w.hi = w.bk = BINS - 1;      // the list is a beginning of the row's order
+  w.before = w.before_k = 0;
+  w.k = k;
+  const uint32_t n = found <= 2 * MAX_CHUNKS ? l.taken : CAP + 1;
   __syncthreads();
-  finish_row(a, r, row, m, s, v, found, true, l);
+  finish_row(a, r, row, m, s, w, n, true, l);
 }
 
 template <class T>
@@ -924,7 +930,6 @@ __global__ __launch_bounds__(ROW_THREADS) void k_sample_finish(SampleArgs a) {
     if (threadIdx.x == 0) write_token(a, r, -1, 0, 1);
     return;
   }
-  load_powers(l.table);
   if (k) {
     finish_small(a, r, row, m, s, k, l);
     return;
@@ -943,10 +948,10 @@ __global__ __launch_bounds__(ROW_THREADS) void k_sample_finish(SampleArgs a) {
 }
 
 struct SamplePlan {
-  uint32_t chunk = TILE, chunks = 0, slots = SLOTS, bits = 62;
+  uint32_t chunk = TILE, chunks = 0, bits = 62;
   bool cut = true;       // some row has a cut that is not a small top_k
   bool small = false;    // some row's top_k is small
-  size_t off_max = 0, off_settings = 0, off_collected = 0, off_sums = 0, off_own = 0, off_own_count = 0, off_count = 0, off_bins = 0, off_cand = 0, off_row = 0,
+  size_t off_max = 0, off_settings = 0, off_collected = 0, off_sums = 0, off_groups = 0, off_count = 0, off_bins = 0, off_cand = 0, off_row = 0,
          total = 0;
 };
 
@@ -958,7 +963,7 @@ SamplePlan sample_plan(const topk_sample_args& a) {
   // what the numbers among the settings say of all rows
   const bool tile = p.chunk == TILE;
   const bool greedy = !a.temperatures && !(a.temperature > 0.f);
-  const bool k_small = greedy || (!a.top_ks && a.top_k > 0 && a.top_k <= (int64_t)SMALL_K);
+  const bool k_small = greedy || (!a.top_ks && a.top_k > 0 && a.top_k <= small_limit(a.n));
   p.small = tile && (k_small || a.top_ks || a.temperatures);
   const bool cuts = a.top_ks || (a.top_k > 0 && a.top_k < a.n) || a.top_ps || !(a.top_p >= 1.f) || greedy || (a.temperatures && !tile);
   p.cut = cuts && !(tile && k_small);
@@ -972,12 +977,7 @@ SamplePlan sample_plan(const topk_sample_args& a) {
   p.off_max = take(rows * p.chunks * 4);
   p.off_settings = take(rows * sizeof(Settings));
     p.off_sums = take(rows * p.chunks * 8);
-  if (p.small) {
-    if (k_small && !a.temperatures)
-      while (p.slots > 64 && p.slots >= 4 * (greedy ? 1 : a.top_k)) p.slots /= 2;
-    p.off_own = take(rows * p.chunks * p.slots * 8);
-    p.off_own_count = take(rows * p.chunks * 4);
-  }
+  if (p.small) p.off_groups = take(rows * p.chunks * FIRST_THREADS * 4);
   if (p.cut) {
     p.off_count = take(rows * BINS * 4);
     p.off_bins = take(rows * BINS * 8);
@@ -1019,8 +1019,7 @@ hipError_t launch_sample(const topk_sample_args& in, void* ws, hipStream_t s) {
   a.settings = reinterpret_cast<Settings*>(w + p.off_settings);
   a.collected = p.cut ? reinterpret_cast<uint32_t*>(w + p.off_collected) : nullptr;
   a.sums = reinterpret_cast<uint64_t*>(w + p.off_sums);
-  a.own = p.small ? reinterpret_cast<uint64_t*>(w + p.off_own) : nullptr;
-  a.own_count = p.small ? reinterpret_cast<uint32_t*>(w + p.off_own_count) : nullptr;
+  a.groups = p.small ? reinterpret_cast<float*>(w + p.off_groups) : nullptr;
   a.bin_count = p.cut ? reinterpret_cast<uint32_t*>(w + p.off_count) : nullptr;
   a.bin_sum = p.cut ? reinterpret_cast<uint64_t*>(w + p.off_bins) : nullptr;
   a.cand = p.cut ? reinterpret_cast<uint64_t*>(w + p.off_cand) : nullptr;
@@ -1029,7 +1028,7 @@ hipError_t launch_sample(const topk_sample_args& in, void* ws, hipStream_t s) {
   a.top_k = in.top_k;
   a.temperature = in.temperature, a.top_p = in.top_p, a.min_p = in.min_p;
   a.n = (uint32_t)in.n;
-  a.chunk = p.chunk, a.chunks = p.chunks, a.slots = p.slots, a.bits = p.bits;
+  a.chunk = p.chunk, a.chunks = p.chunks, a.bits = p.bits;
   return in.dtype == TOPK_BF16 ? sample_call<bf16_t>(a, p, in, s) : sample_call<float>(a, p, in, s);
 }
 
