@@ -685,9 +685,10 @@ hipError_t attend_nothing(const topk_attend_args& a, hipStream_t s) {
 
 // ---------------------------------------------------------------- evict
 // k_evict_pick: a workgroup for each key-value head of each sequence.  Its
-// scores are radix-selected, eight bits at a time, for the key of the last
-// entry that stays and the number of equal ones; then every wave counts what
-// stays of its share, and writes it in order behind the waves before it.
+// scores are radix-selected, eleven bits at a time, for the key of the last
+// entry that stays and the number of equal ones; then what stays is numbered in
+// order, by ballots.  Rows of up to 16 K entries stay in registers
+// (k_evict_pick_held); longer ones are read again for each step.
 constexpr uint32_t PICK_THREADS = 1024;
 constexpr uint32_t PICK_WAVES = PICK_THREADS / 64;
 constexpr uint32_t COPY_THREADS = 256;
@@ -716,74 +717,190 @@ struct EvictArgs {
   uint32_t heads, n, d, budget, recent, fill;
 };
 
-__global__ __launch_bounds__(PICK_THREADS) void k_evict_pick(EvictArgs a) {
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t strict[PICK_WAVES], ties[PICK_WAVES];
-  __shared__ uint32_t found, left;
-  const uint64_t bh = block_id();
-  if (bh >= a.work) return;
-  const uint64_t b = bh / a.heads, h = bh % a.heads;
-  const uint32_t tid = threadIdx.x, wave = tid / 64, lane = tid % 64;
-  const uint32_t len = length_of(a.lengths, b, a.n);
-  const uint32_t kept = min(len, a.budget);
-  if (h == 0 && tid == 0) a.lengths_out[b] = kept;
-  const float* srow = a.scores + b * a.ssb + h * a.ssh;
-  float* so = a.scores_out + b * a.osb + h * a.osh;
-  int64_t* ko = a.kept + bh * a.budget;
-  for (uint32_t i = kept + tid; i < a.budget; i += PICK_THREADS) {
-    ko[i] = -1;
-    if (a.fill) so[i] = 0.f;
+// The bin, from the highest down, at which the counts reach `need` (at least 1,
+// at most their sum); *need becomes what is wanted of it.  Returns the bin, in
+// bit 31 whether all of it is wanted.
+//
+// The counts come in COPIES, one for every COPIES-th lane: scores crowd in few
+// bins, and lanes that count in the same place wait for one another.
+constexpr uint32_t PICK_BINS = 2048, COPIES = 4, COPY_STRIDE = PICK_BINS + 8, ALL_OF_BIN = 0x80000000u;
+constexpr uint32_t ZERO_KEY = 0x80000000u;
+__device__ __forceinline__ uint32_t bin_from_top(const uint32_t* hist, uint32_t* need, uint32_t* part, uint32_t* found) {
+  constexpr uint32_t PER = PICK_BINS / PICK_THREADS;
+  uint32_t c[PER], sum = 0, all;
+#pragma unroll
+  for (uint32_t i = 0; i < PER; ++i) {
+    c[i] = 0;
+#pragma unroll
+    for (uint32_t x = 0; x < COPIES; ++x) c[i] += hist[x * COPY_STRIDE + PICK_BINS - 1 - (threadIdx.x * PER + i)];
+    sum += c[i];
   }
-  const uint32_t old = len <= a.budget ? 0u : len - a.recent;   // entries that have to earn their place
-  uint32_t need = kept - (len - old);                           // and how many of them do
-  uint32_t key = 0;          // the least key that stays
-  if (old && need) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) hist[tid] = 0;
-      __syncthreads();
-      for (uint32_t i = tid; i < old; i += PICK_THREADS) {
-        const uint32_t x = score_key(srow[i]);
-        if (shift == 24 || (x ^ key) >> (shift + 8) == 0) atomicAdd(&hist[x >> shift & 255u], 1u);
+  uint32_t above = thread_scan<PICK_THREADS>(sum, part, &all);
+  if (above < *need && *need <= above + sum) {
+#pragma unroll
+    for (uint32_t i = 0; i < PER; ++i) {
+      if (above < *need && *need <= above + c[i]) {
+        found[0] = (PICK_BINS - 1 - (threadIdx.x * PER + i)) | (*need == above + c[i] ? ALL_OF_BIN : 0u);
+        found[1] = *need - above;
       }
-      __syncthreads();
-      if (tid < 64) {   // bins from the highest down, four to a lane
-        uint32_t c[4], sum = 0;
-#pragma unroll
-        for (uint32_t i = 0; i < 4; ++i) sum += c[i] = hist[255 - (lane * 4 + i)];
-        uint32_t up = sum;
-#pragma unroll
-        for (uint32_t o = 1; o < 64; o <<= 1) {
-          const uint32_t t = __shfl_up(up, o);
-          if (lane >= o) up += t;
-        }
-        uint32_t above = up - sum;
-        if (above < need && need <= up) {
-#pragma unroll
-          for (uint32_t i = 0; i < 4; ++i) {
-            if (above < need && need <= above + c[i]) {
-              found = 255 - (lane * 4 + i);
-              left = need - above;
-            }
-            above += c[i];
-          }
-        }
-      }
-      __syncthreads();
-      key |= found << shift;
-      need = left;
+      above += c[i];
     }
   }
-  // `need` of the entries equal to `key` stay: the first ones
-  const uint32_t per = ((len + PICK_THREADS - 1) / PICK_THREADS) * 64;
-  const uint32_t w0 = min(wave * per, len), w1 = min(w0 + per, len);
-  const bool any = old && a.budget > a.recent;
+  __syncthreads();
+  *need = found[1];
+  return found[0];
+}
+
+// What a workgroup knows of its row.
+struct PickRow {
+  const float* scores;
+  float* scores_out;
+  int64_t* kept;
+  uint32_t len, old, need;   // `need` of the first `old` entries stay, and all the others
+};
+
+__device__ __forceinline__ PickRow pick_row(const EvictArgs& a, uint64_t bh) {
+  const uint64_t b = bh / a.heads, h = bh - b * a.heads;
+  PickRow p;
+  p.len = length_of(a.lengths, b, a.n);
+  const uint32_t kept = min(p.len, a.budget);
+  if (h == 0 && threadIdx.x == 0) a.lengths_out[b] = kept;
+  p.scores = a.scores + (int64_t)b * a.ssb + (int64_t)h * a.ssh;
+  p.scores_out = a.scores_out + (int64_t)b * a.osb + (int64_t)h * a.osh;
+  p.kept = a.kept + bh * a.budget;
+  for (uint32_t i = kept + threadIdx.x; i < a.budget; i += PICK_THREADS) {
+    p.kept[i] = -1;
+    if (a.fill) p.scores_out[i] = 0.f;
+  }
+  p.old = p.len <= a.budget ? 0u : p.len - a.recent;
+  p.need = kept - (p.len - p.old);
+  return p;
+}
+
+// GROUPS groups of 64 consecutive entries to a wave, an entry of each to a lane.
+template <uint32_t GROUPS>
+__global__ __launch_bounds__(PICK_THREADS) void k_evict_pick_held(EvictArgs a) {
+  __shared__ uint32_t hist[COPIES * COPY_STRIDE], part32[PICK_WAVES], found[2];
+  __shared__ uint32_t strict[PICK_WAVES], ties[PICK_WAVES];
+  const uint64_t bh = block_id();
+  if (bh >= a.work) return;
+  const PickRow p = pick_row(a, bh);
+  const uint32_t tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / 64), lane = tid % 64;
+  const uint32_t per = ((p.len + PICK_THREADS - 1) / PICK_THREADS) * 64;
+  const uint32_t w0 = min(wave * per, p.len), w1 = min(w0 + per, p.len);
+  if (p.len == 0) return;
+  uint32_t x[GROUPS];      // the keys; 0, which is none, from p.old on
+  float v[GROUPS];         // all loads leave before the first is used
+#pragma unroll
+  for (uint32_t g = 0; g < GROUPS; ++g) v[g] = p.scores[min(w0 + g * 64 + lane, p.len - 1)];
+#pragma unroll
+  for (uint32_t g = 0; g < GROUPS; ++g) {
+    const uint32_t i = w0 + g * 64 + lane;
+    x[g] = i < w1 && i < p.old ? score_key(v[g]) : 0u;
+  }
+  // entries above `key` stay, and of those equal to it the first `need`
+  uint32_t key = 0xFFFFFFFFu, need = 0;
+  if (p.old && p.need) {
+    uint32_t prefix = 0, bits = 0;    // the first `bits` bits of the key
+    need = p.need;
+    for (;;) {
+      const uint32_t width = bits < 22 ? 11 : 10, shift = 32 - bits - width;
+      for (uint32_t i = tid; i < COPIES * COPY_STRIDE; i += PICK_THREADS) hist[i] = 0;
+      __syncthreads();
+      uint32_t* own = hist + lane % COPIES * COPY_STRIDE;
+      uint32_t zeros = 0;      // entries that nothing has looked at: many, and counted by ballots
+#pragma unroll
+      for (uint32_t g = 0; g < GROUPS; ++g) {
+        zeros += __popcll(__ballot(x[g] == ZERO_KEY));
+        if (x[g] && x[g] != ZERO_KEY && (bits == 0 || x[g] >> (32 - bits) == prefix)) atomicAdd(&own[x[g] >> shift & ((1u << width) - 1)], 1u);
+      }
+      if (lane == 0 && zeros && (bits == 0 || ZERO_KEY >> (32 - bits) == prefix)) atomicAdd(&own[ZERO_KEY >> shift & ((1u << width) - 1)], zeros);
+      __syncthreads();
+      const uint32_t bin = bin_from_top(hist, &need, part32, found);
+      prefix = prefix << width | (bin & ~ALL_OF_BIN);
+      bits += width;
+      if (bin & ALL_OF_BIN) {          // keys are at least 2^22: the least of this bin, less 1
+        key = (prefix << shift) - 1;
+        need = 0;
+        break;
+      }
+      if (bits == 32) {
+        key = prefix;
+        break;
+      }
+    }
+  }
+  // every wave counts what stays of its share, and writes it behind the waves before it
+  uint32_t ns = 0, nt = 0;
+#pragma unroll
+  for (uint32_t g = 0; g < GROUPS; ++g) {
+    const uint32_t i = w0 + g * 64 + lane;
+    ns += __popcll(__ballot(x[g] > key || (i >= p.old && i < w1)));
+    nt += __popcll(__ballot(x[g] == key));
+  }
+  if (lane == 0) {
+    strict[wave] = ns;
+    ties[wave] = nt;
+  }
+  __syncthreads();
+  uint32_t at = 0, tie = 0;
+#pragma unroll
+  for (uint32_t w = 0; w < PICK_WAVES; ++w) {
+    at += w < wave ? strict[w] : 0u;
+    tie += w < wave ? ties[w] : 0u;
+  }
+#pragma unroll
+  for (uint32_t g = 0; g < GROUPS; ++g) {
+    const uint32_t i = w0 + g * 64 + lane;
+    const bool stays = x[g] > key || (i >= p.old && i < w1), equal = x[g] == key;
+    const uint64_t ms = __ballot(stays), mt = __ballot(equal);
+    const uint32_t rank = tie + rank_below(mt);
+    if (stays || (equal && rank < need)) {
+      const uint32_t slot = at + rank_below(ms) + min(rank, need);
+      p.kept[slot] = i;
+      p.scores_out[slot] = v[g];
+    }
+    at += __popcll(ms);
+    tie += __popcll(mt);
+  }
+}
+
+__global__ __launch_bounds__(PICK_THREADS) void k_evict_pick(EvictArgs a) {
+  __shared__ uint32_t hist[COPIES * COPY_STRIDE], part32[PICK_WAVES], found[2];
+  __shared__ uint32_t strict[PICK_WAVES], ties[PICK_WAVES];
+  const uint64_t bh = block_id();
+  if (bh >= a.work) return;
+  const PickRow p = pick_row(a, bh);
+  const uint32_t tid = threadIdx.x, wave = tid / 64, lane = tid % 64;
+  uint32_t key = 0xFFFFFFFFu, need = 0;
+  if (p.old && p.need) {
+    uint32_t prefix = 0, bits = 0;
+    need = p.need;
+    while (bits < 32) {
+      const uint32_t width = bits < 22 ? 11 : 10, shift = 32 - bits - width;
+      for (uint32_t i = tid; i < COPIES * COPY_STRIDE; i += PICK_THREADS) hist[i] = 0;
+      __syncthreads();
+      for (uint32_t i = tid; i < p.old; i += PICK_THREADS) {
+        const uint32_t x = score_key(p.scores[i]);
+        if (bits == 0 || x >> (32 - bits) == prefix) atomicAdd(&hist[lane % COPIES * COPY_STRIDE + (x >> shift & ((1u << width) - 1))], 1u);
+      }
+      __syncthreads();
+      prefix = prefix << width | (bin_from_top(hist, &need, part32, found) & ~ALL_OF_BIN);
+      bits += width;
+    }
+    key = prefix;
+  }
+  // every wave counts what stays of its share, and writes it behind the waves before it
+  const uint32_t per = ((p.len + PICK_THREADS - 1) / PICK_THREADS) * 64;
+  const uint32_t w0 = min(wave * per, p.len), w1 = min(w0 + per, p.len);
   uint32_t ns = 0, nt = 0;
   for (uint32_t c = w0; c < w1; c += 64) {
     const uint32_t i = c + lane;
-    const uint32_t x = i < old && any ? score_key(srow[i]) : 0u;
     const bool in = i < w1;
-    ns += __popcll(__ballot(in && (i >= old || (any && x > key))));
-    nt += __popcll(__ballot(in && i < old && any && x == key));
+    const uint32_t x = in ? score_key(p.scores[i]) : 0u;
+    const bool stays = in && (i >= p.old || x > key);
+    ns += __popcll(__ballot(stays));
+    nt += __popcll(__ballot(in && !stays && x == key));
   }
   if (lane == 0) {
     strict[wave] = ns;
@@ -799,15 +916,15 @@ __global__ __launch_bounds__(PICK_THREADS) void k_evict_pick(EvictArgs a) {
   for (uint32_t c = w0; c < w1; c += 64) {
     const uint32_t i = c + lane;
     const bool in = i < w1;
-    const float v = in ? srow[i] : 0.f;
-    const uint32_t x = i < old && any ? score_key(v) : 0u;
-    const bool sure = in && (i >= old || (any && x > key)), equal = in && i < old && any && x == key;
-    const uint64_t ms = __ballot(sure), mt = __ballot(equal);
+    const float v = in ? p.scores[i] : 0.f;
+    const uint32_t x = score_key(v);
+    const bool stays = in && (i >= p.old || x > key), equal = in && !stays && x == key;
+    const uint64_t ms = __ballot(stays), mt = __ballot(equal);
     const uint32_t rank = tie + __popcll(mt & below);
-    const uint32_t slot = at + __popcll(ms & below) + min(rank, need);
-    if (sure || (equal && rank < need)) {
-      ko[slot] = i;
-      so[slot] = v;
+    if (stays || (equal && rank < need)) {
+      const uint32_t slot = at + __popcll(ms & below) + min(rank, need);
+      p.kept[slot] = i;
+      p.scores_out[slot] = v;
     }
     at += __popcll(ms);
     tie += __popcll(mt);
@@ -900,7 +1017,9 @@ hipError_t launch_evict(const topk_evict_args& in, void*, hipStream_t s) {
   a.recent = (uint32_t)in.recent;
   a.fill = in.fill != 0;
   a.work = (uint64_t)in.batch * a.heads;
-  k_evict_pick<<<wide_grid(a.work), PICK_THREADS, 0, s>>>(a);
+  if (a.n <= 4 * PICK_THREADS) k_evict_pick_held<4><<<wide_grid(a.work), PICK_THREADS, 0, s>>>(a);
+  else if (a.n <= 16 * PICK_THREADS) k_evict_pick_held<16><<<wide_grid(a.work), PICK_THREADS, 0, s>>>(a);
+  else k_evict_pick<<<wide_grid(a.work), PICK_THREADS, 0, s>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !a.budget || !a.d) return e;
   if (in.dtype == TOPK_BF16) return a.d >= 8 ? evict_copy<uint16_t, 8>(a, s) : evict_copy<uint16_t, 1>(a, s);

@@ -206,9 +206,7 @@ __device__ __forceinline__ uint64_t limit_of(float p, uint64_t w) {
 __device__ __forceinline__ float row_max(const SampleArgs& a, uint64_t r) {
   float m = -INFINITY;
   for (uint32_t i = threadIdx.x % 64; i < a.chunks; i += 64) m = fmaxf(m, a.maxima[r * a.chunks + i]);
-#pragma unroll
-  for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-  return m;
+  return wave_top(m);
 }
 
 // A row whose k is at most this gets its first k by way of its groups: not many
@@ -225,28 +223,6 @@ __device__ __forceinline__ uint32_t small_k(const SampleArgs& a, uint64_t r) {
   if (!(temperature_of(a, r) > 0.f)) return 1;
   const int64_t k = a.top_ks ? a.top_ks[r] : a.top_k;
   return k > 0 && k <= small_limit(a.n) ? (uint32_t)k : 0u;
-}
-
-// Exclusive sums over the threads of a workgroup; *total: of all.
-template <uint32_t THREADS, class V>
-__device__ __forceinline__ V thread_scan(V v, V* part, V* total) {
-  V up = v;
-#pragma unroll
-  for (uint32_t o = 1; o < 64; o <<= 1) {
-    const V t = __shfl_up(up, o);
-    if (threadIdx.x % 64 >= o) up += t;
-  }
-  if (threadIdx.x % 64 == 63) part[threadIdx.x / 64] = up;
-  __syncthreads();
-  V before = 0, all = 0;
-#pragma unroll
-  for (uint32_t w = 0; w < THREADS / 64; ++w) {
-    if (w < threadIdx.x / 64) before += part[w];
-    all += part[w];
-  }
-  __syncthreads();
-  *total = all;
-  return before + up - v;
 }
 
 // TILE logits from i0 on, whole vectors to a thread; -inf behind `end`.  (NaN is
@@ -314,8 +290,7 @@ __global__ __launch_bounds__(FIRST_THREADS) void k_sample_first(SampleArgs a) {
     tile.load(row, at, i1);
   }
   if (a.groups) a.groups[id * FIRST_THREADS + threadIdx.x] = m;   // one tile is the whole chunk here
-#pragma unroll
-  for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+  m = wave_top(m);
   if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = m;
   if (bins)   // the chunks of a row share the clearing of its bins
     for (uint32_t i = c * FIRST_THREADS + threadIdx.x; i < BINS; i += a.chunks * FIRST_THREADS) {
@@ -501,7 +476,7 @@ __global__ __launch_bounds__(ROW_THREADS) void k_sample_collect(SampleArgs a) {
     if (at >= i1) break;
     tile.load(row, at, i1);
   }
-  sum = wave_sum(sum);
+  sum = wave_total(sum);
   if (threadIdx.x % 64 == 0) part64[threadIdx.x / 64] = sum;
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -565,7 +540,7 @@ __device__ __forceinline__ uint64_t staying(const SampleArgs& a, const T* row, u
     const double w = weight_of(z, m, s);
     if (w >= min_p) sum += fixed_of(w, a.bits);
   }
-  return wave_sum(sum);
+  return wave_total(sum);
 }
 
 // What a workgroup that ends a row keeps in LDS.

@@ -228,4 +228,53 @@ __device__ __forceinline__ V wave_sum(V v) {
   return v;
 }
 
+// Whole numbers over the lanes of a wave, all of them active: the scan by DPP
+// moves takes a fraction of one by lane exchanges through LDS.
+__device__ __forceinline__ uint64_t wave_incl_sum(uint64_t v) {
+  v += dpp_take64<0x111, 0xf, 0>(v);
+  v += dpp_take64<0x112, 0xf, 0>(v);
+  v += dpp_take64<0x114, 0xf, 0>(v);
+  v += dpp_take64<0x118, 0xf, 0>(v);
+  v += dpp_take64<0x142, 0xa, 0>(v);
+  v += dpp_take64<0x143, 0xc, 0>(v);
+  uint32_t lo = (uint32_t)v, hi = (uint32_t)(v >> 32);
+  asm volatile("" : "+v"(lo), "+v"(hi));
+  return (uint64_t)hi << 32 | lo;
+}
+__device__ __forceinline__ uint64_t wave_total(uint64_t v) { return bcast64(wave_incl_sum(v), 63u); }
+
+// The largest value of a wave (NaN counts as none), in every lane.
+__device__ __forceinline__ float wave_top(float v) {
+#define TK_STEP(ctrl, rows) \
+  v = fmaxf(v, __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp((int)0xFF800000u, (int)__float_as_uint(v), ctrl, rows, 0xf, false)))
+  TK_STEP(0x111, 0xf);
+  TK_STEP(0x112, 0xf);
+  TK_STEP(0x114, 0xf);
+  TK_STEP(0x118, 0xf);
+  TK_STEP(0x142, 0xa);
+  TK_STEP(0x143, 0xc);
+#undef TK_STEP
+  uint32_t u = __float_as_uint(v);
+  asm volatile("" : "+v"(u));
+  return __uint_as_float(wave_bcast(u, 63u));
+}
+
+// Exclusive sums of whole numbers over the threads of a workgroup; *total: of
+// all.  `part`: shared, one for each wave; it may be used anew when this returns.
+template <uint32_t THREADS, class V>
+__device__ __forceinline__ V thread_scan(V v, V* part, V* total) {
+  const V up = wave_incl_sum(v);
+  if (threadIdx.x % 64 == 63) part[threadIdx.x / 64] = up;
+  __syncthreads();
+  V before = 0, all = 0;
+#pragma unroll
+  for (uint32_t w = 0; w < THREADS / 64; ++w) {
+    if (w < threadIdx.x / 64) before += part[w];
+    all += part[w];
+  }
+  __syncthreads();
+  *total = all;
+  return before + up - v;
+}
+
 }  // namespace tk
