@@ -37,12 +37,24 @@ def _not_recorded(what: str, *tensors):
                 raise RuntimeError(f"{what} has no gradient: call it under torch.no_grad, or with detached tensors")
 
 
-def _run(name: str, args: bytes, like: torch.Tensor, stream):
-    """A call whose workspace is asked for with its own arguments."""
-    size = ctypes.c_size_t()
-    _lib.check(getattr(_lib.lib, f"topk_{name}_workspace_size")(args, _byref(size)), name)
-    ws = _scratch(size.value, like)
-    _lib.check(getattr(_lib.lib, "topk_" + name)(args, _ptr(ws), size.value, stream), name)
+_sizes: dict = {}    # workspace bytes by operator, device and what they depend on
+
+
+def _run(name: str, args: bytes, like: torch.Tensor, dev: int, *key):
+    """A call whose workspace is asked for with its own arguments, once for each
+    ``key``: all of the arguments that its size depends on."""
+    key = (name, dev, *key)
+    size = _sizes.get(key)
+    if size is None:
+        out = ctypes.c_size_t()
+        _lib.check(getattr(_lib.lib, f"topk_{name}_workspace_size")(args, _byref(out)), name)
+        if len(_sizes) >= 4096:    # shapes that come once
+            _sizes.clear()
+        size = _sizes[key] = out.value
+    ws = like.new_empty(size, dtype=torch.uint8) if size else None
+    status = getattr(_lib.lib, "topk_" + name)(args, ws.data_ptr() if size else None, size, _stream(dev))
+    if status:
+        _lib.check(status, name)
 
 
 # ---------------------------------------------------------------- tokens by expert
@@ -56,12 +68,14 @@ def _dispatch_run(x, experts, n_experts):
         rows = x.new_empty((t * k, d))
         places = torch.empty_like(experts)
         offsets = experts.new_empty((n_experts + 1,))
-        size = ctypes.c_size_t()
-        _lib.check(_lib.lib.topk_dispatch_workspace_size(t, k, n_experts, _byref(size)), "dispatch")
-        ws = _scratch(size.value, x)
         a = _pack_dispatch(x.data_ptr(), experts.data_ptr(), rows.data_ptr(), places.data_ptr(), offsets.data_ptr(),
                            t, k, n_experts, d, ldx, d or 1, _CODES[x.dtype], 0)
-        _lib.check(_lib.lib.topk_dispatch(a, _ptr(ws), size.value, _stream(dev)), "dispatch")
+        # few entries need no scratch: ask only when the call says so
+        if t * k > 4096 or _lib.lib.topk_dispatch(a, None, 0, _stream(dev)) != _lib.TOPK_OK:
+            size = ctypes.c_size_t()
+            _lib.check(_lib.lib.topk_dispatch_workspace_size(t, k, n_experts, _byref(size)), "dispatch")
+            ws = _scratch(size.value, x)
+            _lib.check(_lib.lib.topk_dispatch(a, _ptr(ws), size.value, _stream(dev)), "dispatch")
     return rows, places, offsets
 
 
@@ -143,7 +157,7 @@ def _combine_grad_run(grad, y, places, weights, need):
             return dy, dw
         a = _pack_combine_grad(grad.data_ptr(), y.data_ptr(), places.data_ptr(), _ptr(weights), _ptr(dy), _ptr(dw),
                                t, k, n, d, ldg, ldy, d or 1, _CODES[y.dtype], wcode)
-        _run("combine_grad", a, grad, _stream(dev))
+        _run("combine_grad", a, grad, dev, t * k, n, d, need[0])
     return dy, dw
 
 
@@ -276,7 +290,7 @@ def attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lengths: torch.Ten
         a = _pack_attend(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(lengths), _ptr(scores), out.data_ptr(),
                          b, hq, h, n, d, *q.stride()[:2], *k.stride()[:3], *v.stride()[:3], sb, sh, hq * d, d,
                          scale, _CODES[q.dtype])
-        _run("attend", a, q, _stream(dev))
+        _run("attend", a, q, dev, b, hq, h, n, d, q.dtype, scores is None)
         if scores is not None:
             torch.autograd.graph.increment_version(scores)   # changed in place, which autograd cannot see
     return out
@@ -338,7 +352,7 @@ def evict(k: torch.Tensor, v: torch.Tensor, scores: torch.Tensor, budget: int, r
                             so.data_ptr(), kept.data_ptr(), lengths_out.data_ptr(), b, h, n, d, budget, recent,
                             *k.stride()[:3], *v.stride()[:3], *scores.stride()[:2], *ko.stride()[:3], *vo.stride()[:3],
                             *so.stride()[:2], _CODES[k.dtype], 1 if out is None else 0)
-            _run("evict", a, k, _stream(dev))
+            _lib.check(_lib.lib.topk_evict(a, None, 0, _stream(dev)), "evict")   # it takes no workspace
             if out is not None:
                 torch.autograd.graph.increment_version((ko, vo, so))   # changed in place, which autograd cannot see
         elif b:   # no heads: only the lengths are left
@@ -405,5 +419,5 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_
         logprobs = torch.empty((rows,), dtype=torch.float32, device=z.device)
         a = _pack_sample(z.data_ptr(), u.data_ptr(), tokens.data_ptr(), logprobs.data_ptr(), _ptr(ts), _ptr(ks), _ptr(ps), _ptr(ms),
                          rows, n, ld, min(int(top_k), 1 << 62), temperature, top_p, min_p, _CODES[z.dtype])
-        _run("sample", a, z, _stream(dev))
+        _run("sample", a, z, dev, rows, n, ts is None, ks is None, ps is None, temperature > 0, top_k, top_p < 1)
     return (tokens[0], logprobs[0]) if squeeze else (tokens, logprobs)

@@ -25,6 +25,7 @@ constexpr uint32_t SMALL_TOTAL = 4096;      // entries that every workgroup coun
 constexpr uint32_t SMALL_EXPERTS = 1024;
 constexpr uint32_t SMALL_PER = 16;          // entries that one of those workgroups moves
 constexpr uint32_t SORT_THREADS = 1024;
+constexpr uint32_t SELF_SCAN = 32768;       // counts that every block of the sort adds up for itself
 constexpr uint32_t MOVE_THREADS = 256;
 constexpr uint32_t PIECE = 2;               // vectors of a row that a lane moves at a time
 
@@ -203,19 +204,40 @@ __global__ __launch_bounds__(SORT_THREADS) void k_route_scan(uint32_t* __restric
   if (wave == 0 && bin < bins) all[bin] = whole;
 }
 
+// SCANNED: cnt holds the sums over the blocks and `all` their totals
+// (k_route_scan); otherwise every block adds the counts up for itself, which
+// for up to SELF_SCAN of them takes less than a launch (16384 x 8 entries, 128
+// experts: 11 us in three launches, 8 in two).
+template <bool SCANNED>
 __global__ __launch_bounds__(SORT_THREADS) void k_route_place(const int64_t* __restrict__ experts, const uint32_t* __restrict__ cnt,
                                                               const uint32_t* __restrict__ all, int64_t* __restrict__ places,
                                                               int64_t* __restrict__ offsets, uint32_t* __restrict__ pos,
                                                               uint32_t total, uint32_t per_block, uint32_t bins, uint32_t digit_bits) {
-  extern __shared__ uint32_t next[];   // the place of the next entry of each expert
+  extern __shared__ uint32_t next[];   // the place of the next entry of each expert; without SCANNED also the blocks' before
   const uint32_t wave = threadIdx.x / 64, lane = threadIdx.x % 64;
-  for (uint32_t i = threadIdx.x; i < bins; i += SORT_THREADS) next[i] = all[i];
+  if constexpr (SCANNED) {
+    for (uint32_t i = threadIdx.x; i < bins; i += SORT_THREADS) next[i] = all[i];
+  } else {
+    for (uint32_t i = threadIdx.x; i < 2 * bins; i += SORT_THREADS) next[i] = 0;
+    __syncthreads();
+    for (uint32_t b = lane; b < bins; b += 64) {
+      uint32_t sum = 0, before = 0;
+#pragma unroll 8
+      for (uint32_t i = wave; i < gridDim.x; i += SORT_THREADS / 64) {
+        const uint32_t v = cnt[(size_t)i * bins + b];
+        sum += v;
+        before += i < blockIdx.x ? v : 0u;
+      }
+      atomicAdd(&next[b], sum);
+      atomicAdd(&next[bins + b], before);
+    }
+  }
   __syncthreads();
   block_scan<SORT_THREADS>(next, bins);
   if (blockIdx.x == 0)
     for (uint32_t i = threadIdx.x; i < bins; i += SORT_THREADS) offsets[i] = next[i];
   __syncthreads();
-  for (uint32_t i = threadIdx.x; i < bins; i += SORT_THREADS) next[i] += cnt[(size_t)blockIdx.x * bins + i];
+  for (uint32_t i = threadIdx.x; i < bins; i += SORT_THREADS) next[i] += SCANNED ? cnt[(size_t)blockIdx.x * bins + i] : next[bins + i];
   __syncthreads();
   const uint32_t e0 = blockIdx.x * per_block;
   const uint32_t e1 = total - e0 < per_block ? total : e0 + per_block;
@@ -289,9 +311,14 @@ hipError_t dispatch_typed(const topk_dispatch_args& a, const RoutePlan& p, char*
   uint32_t* all = reinterpret_cast<uint32_t*>(ws + p.off_all);
   uint32_t* pos = reinterpret_cast<uint32_t*>(ws + p.off_pos);
   k_route_count<<<p.blocks, SORT_THREADS, p.bins * 4, s>>>(a.experts, cnt, p.total, p.per_block, p.bins);
-  k_route_scan<<<(p.bins + 63) / 64, SORT_THREADS, 0, s>>>(cnt, all, p.blocks, p.bins);
-  k_route_place<<<p.blocks, SORT_THREADS, p.bins * 4, s>>>(a.experts, cnt, all, a.places, a.offsets, pos, p.total, p.per_block,
-                                                           p.bins, p.digit_bits);
+  if (p.blocks * p.bins <= SELF_SCAN) {
+    k_route_place<false><<<p.blocks, SORT_THREADS, p.bins * 8, s>>>(a.experts, cnt, all, a.places, a.offsets, pos, p.total, p.per_block,
+                                                                    p.bins, p.digit_bits);
+  } else {
+    k_route_scan<<<(p.bins + 63) / 64, SORT_THREADS, 0, s>>>(cnt, all, p.blocks, p.bins);
+    k_route_place<true><<<p.blocks, SORT_THREADS, p.bins * 4, s>>>(a.experts, cnt, all, a.places, a.offsets, pos, p.total, p.per_block,
+                                                                   p.bins, p.digit_bits);
+  }
   if (d) {
     const uint32_t pieces = (d + 64 * VEC * PIECE - 1) / (64 * VEC * PIECE);
     const uint64_t items = (uint64_t)a.tokens * pieces;
@@ -373,6 +400,24 @@ __global__ __launch_bounds__(MOVE_THREADS) void k_owner_link(const int64_t* __re
   if (e >= total) return;
   const int64_t p = places[e];
   next[e] = (uint64_t)p < n ? atomicExch(&owner[p], (uint32_t)e) : NONE;
+}
+
+// Few entries: every workgroup goes through all of them for MOVE_THREADS places
+// of its own, in one launch.
+constexpr uint32_t MAP_TOTAL = 8192;
+__global__ __launch_bounds__(MOVE_THREADS) void k_owner_map(const int64_t* __restrict__ places, uint32_t* __restrict__ owner,
+                                                            uint32_t* __restrict__ next, uint64_t n, uint32_t total) {
+  __shared__ uint32_t own[MOVE_THREADS];
+  own[threadIdx.x] = NONE;
+  __syncthreads();
+  const uint64_t p0 = (uint64_t)block_id() * MOVE_THREADS;
+#pragma unroll 4
+  for (uint32_t e = threadIdx.x; e < total; e += MOVE_THREADS) {
+    const uint64_t p = (uint64_t)places[e] - p0;
+    if (p < MOVE_THREADS && p0 + p < n) next[e] = atomicExch(&own[p], e);
+  }
+  __syncthreads();
+  if (p0 + threadIdx.x < n) owner[p0 + threadIdx.x] = own[threadIdx.x];
 }
 
 // Items below `total`: the entries, a wave each: dw_e, and dy's row if the
@@ -462,10 +507,11 @@ hipError_t combine_grad_typed(const topk_combine_grad_args& a, char* ws, hipStre
   const bool rows = a.dy && a.n > 0 && d > 0;
   uint32_t* owner = reinterpret_cast<uint32_t*>(ws);
   uint32_t* next = reinterpret_cast<uint32_t*>(ws + align256((size_t)a.n * 4));
-  if (rows) {
+  if (rows && total <= MAP_TOTAL) {
+    k_owner_map<<<wide_grid((uint64_t)ceil_div(a.n, MOVE_THREADS)), MOVE_THREADS, 0, s>>>(a.places, owner, next, (uint64_t)a.n, total);
+  } else if (rows) {
     k_owner_clear<<<wide_grid((uint64_t)ceil_div(a.n, MOVE_THREADS)), MOVE_THREADS, 0, s>>>(owner, (uint64_t)a.n);
-    if (total)
-      k_owner_link<<<wide_grid((uint64_t)ceil_div(total, MOVE_THREADS)), MOVE_THREADS, 0, s>>>(a.places, owner, next, (uint64_t)a.n, total);
+    k_owner_link<<<wide_grid((uint64_t)ceil_div(total, MOVE_THREADS)), MOVE_THREADS, 0, s>>>(a.places, owner, next, (uint64_t)a.n, total);
   }
   const uint64_t items = (uint64_t)total + (rows ? (uint64_t)ceil_div(a.n, 64) : 0);
   if (!items) return hipGetLastError();
