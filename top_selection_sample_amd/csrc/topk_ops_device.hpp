@@ -43,6 +43,12 @@ __device__ __forceinline__ u32x4 read16(const void* p) {
   return q;
 }
 
+// The same, of what is read once: it does not push out what others read again.
+__device__ __forceinline__ u32x4 read16_once(const void* p) {
+  typedef u32x4 any_u32x4 __attribute__((aligned(2)));
+  return __builtin_nontemporal_load(static_cast<const any_u32x4*>(p));
+}
+
 template <class T> struct Vec;
 template <> struct Vec<float> {
   static constexpr int N = 4;
@@ -111,6 +117,7 @@ __device__ __forceinline__ void store_vec(T* p, const float* v) {
 template <class U, int VEC> struct Bits {
   typedef u32x4 type;
   __device__ static type load(const U* p) { return read16(p); }
+  __device__ static type load_once(const U* p) { return read16_once(p); }
   __device__ static type zero() { return u32x4{0, 0, 0, 0}; }
   __device__ static void store(U* p, type v) { __builtin_memcpy(p, &v, 16); }
   __device__ static void stream(U* p, type v) {
@@ -121,6 +128,7 @@ template <class U, int VEC> struct Bits {
 template <class U> struct Bits<U, 1> {
   typedef U type;
   __device__ static type load(const U* p) { return *p; }
+  __device__ static type load_once(const U* p) { return *p; }
   __device__ static type zero() { return 0; }
   __device__ static void store(U* p, type v) { *p = v; }
   __device__ static void stream(U* p, type v) { *p = v; }
