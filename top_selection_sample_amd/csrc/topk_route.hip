@@ -265,10 +265,10 @@ __global__ __launch_bounds__(SORT_THREADS) void k_route_place(const int64_t* __r
 
 // Each row of x is read once and written to the places of its token's entries.
 // An item: PIECE * 64 vectors of one token's row, by a wave.
-template <class U, int VEC>
+template <class U, int VEC, bool STREAM>
 __global__ __launch_bounds__(MOVE_THREADS) void k_dispatch_move(const U* __restrict__ x, const uint32_t* __restrict__ pos,
                                                                 U* __restrict__ rows, uint64_t ldx, uint64_t ldr, uint32_t k,
-                                                                uint32_t d, uint32_t pieces, uint64_t items, bool stream) {
+                                                                uint32_t d, uint32_t pieces, uint64_t items) {
   typedef Bits<U, VEC> B;
   const uint32_t lane = threadIdx.x % 64;
   const uint64_t item = (uint64_t)block_id() * (MOVE_THREADS / 64) + threadIdx.x / 64;
@@ -290,7 +290,7 @@ __global__ __launch_bounds__(MOVE_THREADS) void k_dispatch_move(const U* __restr
       const uint32_t c = c0 + (i * 64 + lane) * VEC;
       if (c >= d) continue;
       const typename B::type w = p & DROPPED ? B::zero() : v[i];
-      if (stream) B::stream(dst + column_of<VEC>(c, d), w);
+      if constexpr (STREAM) B::stream(dst + column_of<VEC>(c, d), w);
       else B::store(dst + column_of<VEC>(c, d), w);
     }
   }
@@ -322,9 +322,8 @@ hipError_t dispatch_typed(const topk_dispatch_args& a, const RoutePlan& p, char*
   if (d) {
     const uint32_t pieces = (d + 64 * VEC * PIECE - 1) / (64 * VEC * PIECE);
     const uint64_t items = (uint64_t)a.tokens * pieces;
-    const bool stream = (int64_t)p.total * a.d * (int64_t)sizeof(U) >= STREAM_BYTES;
-    k_dispatch_move<U, VEC><<<wide_grid((items + 3) / 4), MOVE_THREADS, 0, s>>>(x, pos, rows, (uint64_t)a.ldx, (uint64_t)a.ldr, k, d,
-                                                                               pieces, items, stream);
+    auto* move = (int64_t)p.total * a.d * (int64_t)sizeof(U) >= STREAM_BYTES ? k_dispatch_move<U, VEC, true> : k_dispatch_move<U, VEC, false>;
+    move<<<wide_grid((items + 3) / 4), MOVE_THREADS, 0, s>>>(x, pos, rows, (uint64_t)a.ldx, (uint64_t)a.ldr, k, d, pieces, items);
   }
   return hipGetLastError();
 }
@@ -402,35 +401,49 @@ __global__ __launch_bounds__(MOVE_THREADS) void k_owner_link(const int64_t* __re
   next[e] = (uint64_t)p < n ? atomicExch(&owner[p], (uint32_t)e) : NONE;
 }
 
-// Few entries: every workgroup goes through all of them for MOVE_THREADS places
-// of its own, in one launch.
-constexpr uint32_t MAP_TOTAL = 8192;
-__global__ __launch_bounds__(MOVE_THREADS) void k_owner_map(const int64_t* __restrict__ places, uint32_t* __restrict__ owner,
-                                                            uint32_t* __restrict__ next, uint64_t n, uint32_t total) {
-  __shared__ uint32_t own[MOVE_THREADS];
+// Up to MAP_TOTAL entries: every workgroup goes through all of them for
+// MAP_PLACES places of its own, in one launch instead of two (8 and 65536
+// entries 3 and 6 us against 4 and 10).
+constexpr uint32_t MAP_TOTAL = 8192, MAP_PLACES = 1024;
+__global__ __launch_bounds__(MAP_PLACES) void k_owner_map(const int64_t* __restrict__ places, uint32_t* __restrict__ owner,
+                                                          uint32_t* __restrict__ next, uint64_t n, uint32_t total) {
+  __shared__ uint32_t own[MAP_PLACES];
+  constexpr uint32_t AHEAD = 8;
   own[threadIdx.x] = NONE;
   __syncthreads();
-  const uint64_t p0 = (uint64_t)block_id() * MOVE_THREADS;
-#pragma unroll 4
-  for (uint32_t e = threadIdx.x; e < total; e += MOVE_THREADS) {
-    const uint64_t p = (uint64_t)places[e] - p0;
-    if (p < MOVE_THREADS && p0 + p < n) next[e] = atomicExch(&own[p], e);
+  const uint64_t p0 = (uint64_t)block_id() * MAP_PLACES;
+  for (uint32_t e0 = threadIdx.x; e0 < total; e0 += MAP_PLACES * AHEAD) {
+    uint64_t p[AHEAD];
+#pragma unroll
+    for (uint32_t i = 0; i < AHEAD; ++i) p[i] = (uint64_t)places[min(e0 + i * MAP_PLACES, total - 1)] - p0;
+#pragma unroll
+    for (uint32_t i = 0; i < AHEAD; ++i) {
+      const uint32_t e = e0 + i * MAP_PLACES;
+      if (e < total && p[i] < MAP_PLACES && p0 + p[i] < n) next[e] = atomicExch(&own[p[i]], e);
+    }
   }
   __syncthreads();
   if (p0 + threadIdx.x < n) owner[p0 + threadIdx.x] = own[threadIdx.x];
 }
 
-// Items below `total`: the entries, a wave each: dw_e, and dy's row if the
-// entry owns it.  Items from `total` on: 64 rows of y each, of which the ones
-// that no entry names are set to zero.
-template <class T, class W, int VEC>
+// Items below `total`: the entries, a wave each: dw_e, and dy's row if the entry
+// owns it, PIECE vectors of both rows a lane in flight.  Items from `total` on:
+// 64 rows of y each, of which the ones that no entry names are set to zero.
+// STREAM: y is read, and dy stored, past the caches.  (Two, four and eight
+// entries to a wave, their places looked up side by side, are slower: 8192 x 8
+// entries of 1024 bf16 take 65, 71 and 82 us against 62.)
+template <class T, class W, int VEC, bool STREAM>
 __global__ __launch_bounds__(MOVE_THREADS) void k_combine_grad(
     const T* __restrict__ g, const T* __restrict__ y, const int64_t* __restrict__ places, const W* __restrict__ weights,
     const uint32_t* __restrict__ owner, const uint32_t* __restrict__ next, T* __restrict__ dy, W* __restrict__ dw, uint64_t ldg,
-    uint64_t ldy, uint64_t lddy, uint64_t n, uint32_t total, uint32_t k, uint32_t d, uint64_t items, bool stream) {
+    uint64_t ldy, uint64_t lddy, uint64_t n, uint32_t total, uint32_t k, uint32_t d, uint64_t items) {
   const uint32_t lane = threadIdx.x % 64;
-  const uint64_t item = (uint64_t)block_id() * (MOVE_THREADS / 64) + threadIdx.x / 64;
+  const uint64_t item = (uint64_t)block_id() * (MOVE_THREADS / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   if (item >= items) return;
+  auto put = [&](T* p, const float* v) {
+    if constexpr (STREAM && VEC > 1) stream_vec<T>(p, v);
+    else store_vec<T, VEC>(p, v);
+  };
   if (item >= total) {
     const uint64_t r0 = (item - total) * 64;
     const bool bare = r0 + lane < n && owner[r0 + lane] == NONE;
@@ -439,7 +452,7 @@ __global__ __launch_bounds__(MOVE_THREADS) void k_combine_grad(
     for (int q = 0; q < VEC; ++q) z[q] = 0.f;
     for (uint64_t m = __ballot(bare); m; m &= m - 1) {
       T* row = dy + (r0 + __builtin_ctzll(m)) * lddy;
-      for (uint32_t c = lane * VEC; c < d; c += 64 * VEC) store_vec<T, VEC>(row + column_of<VEC>(c, d), z);
+      for (uint32_t c = lane * VEC; c < d; c += 64 * VEC) put(row + column_of<VEC>(c, d), z);
     }
     return;
   }
@@ -456,44 +469,50 @@ __global__ __launch_bounds__(MOVE_THREADS) void k_combine_grad(
   const bool chain = mine && next[e] != NONE;
   const float w = weight_of(weights, e);
   float dot = 0.f;
-  for (uint32_t c = lane * VEC; c < d; c += 64 * VEC) {
-    const uint32_t at = column_of<VEC>(c, d);
-    float a[VEC], b[VEC];
-    load_vec<T, VEC>(grow + at, a);
-    if (dw) {
-      load_vec<T, VEC>(yrow + at, b);
+  for (uint32_t c0 = 0; c0 < d; c0 += 64 * VEC * PIECE) {
+    float a[PIECE][VEC], b[PIECE][VEC];
 #pragma unroll
-      for (int q = 0; q < VEC; ++q)
-        if (at + q >= c) dot = fmaf(a[q], b[q], dot);   // a row's last vector counts its new columns only
-    }
-    if (!mine) continue;
-    if (!chain) {
-#pragma unroll
-      for (int q = 0; q < VEC; ++q) a[q] *= w;
-    } else {
-      // the chain's entries by rising number: the least one above the last taken
-#pragma unroll
-      for (int q = 0; q < VEC; ++q) a[q] = 0.f;
-      int64_t last = -1;
-      for (;;) {
-        uint32_t least = NONE;
-        for (uint32_t i = e; i != NONE; i = next[i])
-          if ((int64_t)i > last && i < least) least = i;
-        if (least == NONE) break;
-        const float wi = weight_of(weights, least);
-        load_vec<T, VEC>(g + (uint64_t)(least / k) * ldg + at, b);
-#pragma unroll
-        for (int q = 0; q < VEC; ++q) a[q] = fmaf(wi, b[q], a[q]);
-        last = least;
+    for (uint32_t x = 0; x < PIECE; ++x) {
+      const uint32_t at = column_of<VEC>(min(c0 + (x * 64 + lane) * VEC, d - 1), d);
+      load_vec<T, VEC>(grow + at, a[x]);
+      if (dw) {
+        if constexpr (STREAM && VEC > 1) Vec<T>::unpack(read16_once(yrow + at), b[x]);
+        else load_vec<T, VEC>(yrow + at, b[x]);
       }
     }
-    if constexpr (VEC > 1) {
-      if (stream) {
-        stream_vec<T>(dyrow + at, a);
-        continue;
+#pragma unroll
+    for (uint32_t x = 0; x < PIECE; ++x) {
+      const uint32_t c = c0 + (x * 64 + lane) * VEC;
+      if (c >= d) continue;
+      const uint32_t at = column_of<VEC>(c, d);
+      if (dw) {
+#pragma unroll
+        for (int q = 0; q < VEC; ++q)
+          if (at + q >= c) dot = fmaf(a[x][q], b[x][q], dot);   // a row's last vector counts its new columns only
       }
+      if (!mine) continue;
+      if (!chain) {
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) a[x][q] *= w;
+      } else {
+        // the chain's entries by rising number: the least one above the last taken
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) a[x][q] = 0.f;
+        int64_t last = -1;
+        for (;;) {
+          uint32_t least = NONE;
+          for (uint32_t j = e; j != NONE; j = next[j])
+            if ((int64_t)j > last && j < least) least = j;
+          if (least == NONE) break;
+          const float wi = weight_of(weights, least);
+          load_vec<T, VEC>(g + (uint64_t)(least / k) * ldg + at, b[x]);
+#pragma unroll
+          for (int q = 0; q < VEC; ++q) a[x][q] = fmaf(wi, b[x][q], a[x][q]);
+          last = least;
+        }
+      }
+      put(dyrow + at, a[x]);
     }
-    store_vec<T, VEC>(dyrow + at, a);
   }
   if (dw) {
     dot = wave_sum(dot);
@@ -508,18 +527,18 @@ hipError_t combine_grad_typed(const topk_combine_grad_args& a, char* ws, hipStre
   uint32_t* owner = reinterpret_cast<uint32_t*>(ws);
   uint32_t* next = reinterpret_cast<uint32_t*>(ws + align256((size_t)a.n * 4));
   if (rows && total <= MAP_TOTAL) {
-    k_owner_map<<<wide_grid((uint64_t)ceil_div(a.n, MOVE_THREADS)), MOVE_THREADS, 0, s>>>(a.places, owner, next, (uint64_t)a.n, total);
+    k_owner_map<<<wide_grid((uint64_t)ceil_div(a.n, MAP_PLACES)), MAP_PLACES, 0, s>>>(a.places, owner, next, (uint64_t)a.n, total);
   } else if (rows) {
     k_owner_clear<<<wide_grid((uint64_t)ceil_div(a.n, MOVE_THREADS)), MOVE_THREADS, 0, s>>>(owner, (uint64_t)a.n);
     k_owner_link<<<wide_grid((uint64_t)ceil_div(total, MOVE_THREADS)), MOVE_THREADS, 0, s>>>(a.places, owner, next, (uint64_t)a.n, total);
   }
   const uint64_t items = (uint64_t)total + (rows ? (uint64_t)ceil_div(a.n, 64) : 0);
   if (!items) return hipGetLastError();
-  const bool stream = a.n * a.d * (int64_t)sizeof(T) >= STREAM_BYTES;
-  k_combine_grad<T, W, VEC><<<wide_grid((items + 3) / 4), MOVE_THREADS, 0, s>>>(
+  auto* grad = a.n * a.d * (int64_t)sizeof(T) >= STREAM_BYTES ? k_combine_grad<T, W, VEC, true> : k_combine_grad<T, W, VEC, false>;
+  grad<<<wide_grid((items + 3) / 4), MOVE_THREADS, 0, s>>>(
       static_cast<const T*>(a.grad), static_cast<const T*>(a.y), a.places, static_cast<const W*>(a.weights), owner, next,
       static_cast<T*>(rows ? a.dy : nullptr), static_cast<W*>(a.dweights), (uint64_t)a.ldg, (uint64_t)a.ldy, (uint64_t)a.lddy,
-      (uint64_t)a.n, total, std::max((uint32_t)a.k, 1u), d, items, stream);
+      (uint64_t)a.n, total, std::max((uint32_t)a.k, 1u), d, items);
   return hipGetLastError();
 }
 
