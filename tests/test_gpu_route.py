@@ -132,8 +132,34 @@ def test_many_entries_at_one_place():
     (dy, _), (ey, _) = M.combine_grad64(g, y, places, w)
     first, _ = tss().combine_grad(g, y, places, w)
     U.within(first.cpu(), dy, ey, "dy")
-    for _ in range(5):     # whichever entry owns the place, the order of the sum is the entries'
+    for _ in range(5):     # in whatever order the entries came
         assert torch.equal(tss().combine_grad(g, y, places, w)[0], first)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_very_many_entries_at_few_places(dt):
+    # linear in the entries, however they crowd; more of them than one launch maps
+    t, k, d = 40000, 3, 20
+    places = ints(1, 0, 5, t, k)
+    places[:1000] = ints(2, 0, 900, 1000, k)
+    y, w, g = rnd(3, 1000, d, dt=dt), rnd(4, t, k), rnd(5, t, d, dt=dt)
+    (dy, dw), (ey, ew) = M.combine_grad64(g, y, places, w)
+    gy, gw = tss().combine_grad(g, y, places, w)
+    U.within(gy.cpu(), dy, ey, "dy")
+    U.within(gw.cpu(), dw, ew, "dw")
+    assert torch.equal(tss().combine_grad(g, y, places, w)[0], gy)
+
+
+def test_chains_of_extremes():
+    inf, nan, big = float("inf"), float("nan"), 3e38
+    places = torch.zeros(4, 1, dtype=torch.int64, device="cuda")
+    g = torch.tensor([[1.0, big, inf, inf, nan, 1e-45, 0.0, big], [1.0, big, 1.0, -inf, 1.0, 1e-45, 0.0, -big],
+                      [1e-20, -big, 1.0, 1.0, 1.0, 1e-45, -0.0, big], [-2.0, -big, 1.0, 1.0, 1.0, -1e-45, 0.0, -big]], device="cuda")
+    dy, _ = tss().combine_grad(g, torch.zeros(2, 8, device="cuda"), places)
+    # terms up to 2 are multiples of 2^-57 (62 bits, less 3 for up to 7 terms and 2 for the largest): four roundings
+    assert abs(float(dy[0, 0]) - 1e-20) <= 4 * 2.0 ** -58
+    assert dy[0, 1:3].tolist() == [0.0, inf] and bool(torch.isnan(dy[0, 3:5]).all())
+    assert float(dy[0, 5]) == float(torch.tensor(1e-45) * 2) and dy[0, 6:].tolist() == [0.0, 0.0] and bool((dy[1] == 0).all())
 
 
 @pytest.mark.parametrize("t", [40, 3000])

@@ -386,8 +386,8 @@ hipError_t combine_typed(const topk_combine_args& a, hipStream_t s) {
 
 // ---------------------------------------------------------------- combine's gradient
 // owner[p]: one entry at place p, or NONE; next[e]: another entry at the same
-// place, or NONE.  A place that several entries name is a chain; its gradient
-// is summed in the order of the entries, whichever of them came to own it.
+// place, or NONE.  A place that several entries name is a chain, linked in
+// whatever order they came.
 __global__ __launch_bounds__(MOVE_THREADS) void k_owner_clear(uint32_t* __restrict__ owner, uint64_t n) {
   const uint64_t i = (uint64_t)block_id() * MOVE_THREADS + threadIdx.x;
   if (i < n) owner[i] = NONE;
@@ -424,6 +424,31 @@ __global__ __launch_bounds__(MAP_PLACES) void k_owner_map(const int64_t* __restr
   }
   __syncthreads();
   if (p0 + threadIdx.x < n) owner[p0 + threadIdx.x] = own[threadIdx.x];
+}
+
+// One column of the sum over a chain.  Its order is not the same from call to
+// call, so the terms are added as whole multiples of a power of two that 62 bits
+// hold (the largest term tells which): such a sum has no order.  Where a term is
+// not finite, neither is the sum, in any order.  (A column at a time: chains are
+// rare, and registers are what the others run on.)
+template <class T, class W>
+__device__ __forceinline__ float chain_sum(const T* column, const W* weights, const uint32_t* next, uint64_t ldg, uint32_t k, uint32_t e) {
+  float top = 0.f;
+  double plain = 0.0;
+  uint32_t count = 0;
+  for (uint32_t j = e; j != NONE; j = next[j], ++count) {
+    const float t = weight_of(weights, j) * to_f32(column[(uint64_t)(j / k) * ldg]);
+    top = fmaxf(top, fabsf(t));
+    plain += t;
+  }
+  if (!(fabs(plain) < INFINITY)) return (float)plain;
+  int exponent = 0;
+  frexpf(top, &exponent);   // top < 2^exponent
+  const int shift = 62 - (32 - __builtin_clz(count)) - exponent;
+  int64_t sum = 0;
+  for (uint32_t j = e; j != NONE; j = next[j])
+    sum += (int64_t)rint(ldexp((double)(weight_of(weights, j) * to_f32(column[(uint64_t)(j / k) * ldg])), shift));
+  return (float)ldexp((double)sum, -shift);
 }
 
 // Items below `total`: the entries, a wave each: dw_e, and dy's row if the entry
@@ -491,26 +516,13 @@ __global__ __launch_bounds__(MOVE_THREADS) void k_combine_grad(
           if (at + q >= c) dot = fmaf(a[x][q], b[x][q], dot);   // a row's last vector counts its new columns only
       }
       if (!mine) continue;
-      if (!chain) {
-#pragma unroll
-        for (int q = 0; q < VEC; ++q) a[x][q] *= w;
-      } else {
-        // the chain's entries by rising number: the least one above the last taken
-#pragma unroll
-        for (int q = 0; q < VEC; ++q) a[x][q] = 0.f;
-        int64_t last = -1;
-        for (;;) {
-          uint32_t least = NONE;
-          for (uint32_t j = e; j != NONE; j = next[j])
-            if ((int64_t)j > last && j < least) least = j;
-          if (least == NONE) break;
-          const float wi = weight_of(weights, least);
-          load_vec<T, VEC>(g + (uint64_t)(least / k) * ldg + at, b[x]);
-#pragma unroll
-          for (int q = 0; q < VEC; ++q) a[x][q] = fmaf(wi, b[x][q], a[x][q]);
-          last = least;
-        }
+      if (chain) {
+#pragma unroll 1
+        for (uint32_t q = 0; q < VEC; ++q) dyrow[at + q] = from_f32<T>(chain_sum<T, W>(g + at + q, weights, next, ldg, k, e));
+        continue;
       }
+#pragma unroll
+      for (int q = 0; q < VEC; ++q) a[x][q] *= w;
       put(dyrow + at, a[x]);
     }
   }
