@@ -269,16 +269,40 @@ def test_evict_into_buffers(dt):
             assert bool((t[i, :, e:] == mark).all())      # rows behind the last, as they were
 
 
+def test_evict_into_interleaved_buffers():
+    # keys beside values, old ones and new ones in one tensor
+    b, h, n, d = 2, 2, 60, 8
+    pool = rnd(1, b, h, n, 4, d)
+    k, v, ko, vo = (pool[:, :, :, i] for i in range(4))
+    s = rnd(2, b, h, n, 2).abs()
+    want = M.evict64(s[..., 0], None, 20, 3)[0]
+    k0, v0 = k.clone(), v.clone()
+    got = tss().evict(k, v, s[..., 0].contiguous(), 20, 3, out=(ko, vo, torch.zeros(b, h, 20, device="cuda")))
+    assert torch.equal(got[3].cpu(), want)
+    assert torch.equal(ko[:, :, :20].cpu(), M.rows_of(k0, want)) and torch.equal(vo[:, :, :20].cpu(), M.rows_of(v0, want))
+    assert torch.equal(k, k0) and torch.equal(v, v0)
+
+
+def test_attend_nothing_at_all():
+    for n in (5, 5000):
+        q, k = rnd(1, 3, 4, 40), torch.full((3, 2, n, 40), NAN, device="cuda")
+        s = torch.ones(3, 2, n, device="cuda")
+        assert bool((tss().attend(q, k, k, ends(0, 0, 0), s) == 0).all()) and bool((s == 1).all())
+        assert bool((tss().attend(q, k, k, ends(0, 0, -1)) == 0).all())
+
+
 def test_evict_refusals():
     T = tss()
     k, s = rnd(1, 2, 2, 50, 16), torch.rand(2, 2, 50, device="cuda")
     out = (rnd(2, 2, 2, 20, 16), rnd(3, 2, 2, 20, 16), torch.zeros(2, 2, 20, device="cuda"))
+    wide = rnd(4, 2, 2, 20, 32)
     for bad in (lambda: T.evict(k, k, s, 0), lambda: T.evict(k, k, s, 10, 11), lambda: T.evict(k, k, s, 10, -1), lambda: T.evict(k, k[:, :, :9], s, 10),
                 lambda: T.evict(k, k, s[:, :, :9], 10), lambda: T.evict(k, k, s.double(), 10), lambda: T.evict(k, k, s, 10, lengths=ends(1)),
                 lambda: T.evict(k[0], k[0], s[0], 10), lambda: T.evict(k, k, s, 21, out=out), lambda: T.evict(k, k, s, 10, out=(out[0], out[0], out[2])),
                 lambda: T.evict(k, k, s, 10, out=(k, out[1], out[2])), lambda: T.evict(k, k, s, 10, out=(out[0], out[1], s)),
                 lambda: T.evict(k, k, s, 10, out=(out[0].bfloat16(), out[1], out[2])), lambda: T.evict(k, k, s, 10, out=(out[0][:1], out[1], out[2])),
-                lambda: T.evict(k, k, s, 10, out=(k[:, :, 30:], out[1], out[2]))):
+                lambda: T.evict(k, k, s, 10, out=(k[:, :, 30:], out[1], out[2])),
+                lambda: T.evict(k, k, s, 10, out=(wide[..., :16], wide[..., 8:24], out[2]))):
         with pytest.raises(ValueError):
             bad()
     with pytest.raises(T.TopkError):

@@ -40,7 +40,7 @@ def check_dispatch(x, experts, count, label):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
-@pytest.mark.parametrize("t,k,count", [(0, 2, 4), (1, 1, 1), (3, 0, 5), (1, 8, 8), (7, 2, 3), (64, 1, 64), (100, 6, 257), (512, 8, 1024),
+@pytest.mark.parametrize("t,k,count", [(0, 2, 4), (0, 3, 8192), (0, 0, 2000), (5, 0, 1500), (1, 1, 1), (3, 0, 5), (1, 8, 8), (7, 2, 3), (64, 1, 64), (100, 6, 257), (512, 8, 1024),
                                        (513, 8, 7), (4096, 1, 1025), (3, 2, 8192), (2500, 4, 8192), (40000, 2, 16), (5000, 3, 63)])
 def test_dispatch_counts(t, k, count, dt):
     check_dispatch(rnd(t, t, 24, dt=dt), ints(k, -1, count + 1, t, k), count, (t, k, count))

@@ -108,6 +108,7 @@ def test_workspace(name):
 
 def test_sizes_that_are_taken():
     assert need("dispatch", tokens=0) == (OK, 0)
+    assert need("dispatch", tokens=0, n_experts=8192)[0] == OK
     assert need("dispatch", n_experts=0)[0] == OK
     assert need("dispatch", tokens=(1 << 31) - 1, k=1)[0] == OK
     assert need("evict", b=0)[0] == OK

@@ -235,12 +235,27 @@ def _check_lengths(lengths, like, b):
     return lengths.contiguous()
 
 
-def _span(t: torch.Tensor):
-    """Addresses from the first element's to behind the last one's."""
-    if not t.numel():
-        return 0, 0
-    last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
-    return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+def _may_share(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether two tensors with a contiguous last axis can have memory in common.
+    Not if they lie apart; nor if they are interleaved, their rows beginning at
+    multiples of one distance and not meeting within it (keys beside values)."""
+    if not a.numel() or not b.numel():
+        return False
+    parts = []
+    step = 0
+    for t in (a, b):
+        size = t.element_size()
+        last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+        parts.append((t.data_ptr(), t.data_ptr() + (last + 1) * size, t.shape[-1] * size))
+        for n, s in list(zip(t.shape, t.stride()))[:-1]:
+            if n > 1:
+                step = math.gcd(step, s * size)
+    (a0, a1, wa), (b0, b1, wb) = parts
+    if a1 <= b0 or b1 <= a0:
+        return False
+    if not step:
+        return True
+    return not (wa <= (b0 - a0) % step and wb <= (a0 - b0) % step)
 
 
 def attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lengths: torch.Tensor | None = None,
@@ -341,9 +356,8 @@ def evict(k: torch.Tensor, v: torch.Tensor, scores: torch.Tensor, budget: int, r
                 if last != 1 and t.shape[-1] > 1:
                     raise ValueError(f"out {what}: the last axis contiguous")
             _not_recorded("evict", ko, vo, so)
-            spans = [_span(t) for t in (ko, vo, so)]
-            for i, (lo, hi) in enumerate(spans):
-                if any(lo < top and low < hi for low, top in [_span(t) for t in (k, v, scores)] + spans[:i]):
+            for i, t in enumerate((ko, vo, so)):
+                if any(_may_share(t, o) for o in (k, v, scores, ko, vo)[:3 + min(i, 2)]):
                     raise ValueError("out: no memory shared with the old cache, or with one another")
         kept = torch.empty((b, h, budget), dtype=torch.int64, device=k.device)
         lengths_out = torch.empty((b,), dtype=torch.int64, device=k.device)

@@ -48,7 +48,7 @@ constexpr uint32_t BINS = 2048;             // 16 octaves of m - z from 2^-7 on,
 constexpr uint32_t FIRST_BIN = (127 - 7) << 7;
 constexpr uint32_t CAP = 4096;              // entries of a row around its cut that are sorted
 constexpr uint32_t GROUP = TILE / FIRST_THREADS;   // entries of a thread of k_sample_first
-constexpr uint32_t SMALL_K = 1024;          // a small top_k: up to here, and of a row of four groups for each
+constexpr uint32_t SMALL_K = 1024;          // a small top_k of a long row: up to here, and of a row of four groups for each
 constexpr uint32_t PAIRS = 512;             // entries that are compared each with each rather than sorted
 
 // What is known of a row between the launches.
@@ -214,15 +214,17 @@ __device__ __forceinline__ float row_max(const SampleArgs& a, uint64_t r) {
 // sorted.
 __host__ __device__ __forceinline__ int64_t small_limit(int64_t n) {
   const int64_t k = n <= (int64_t)CAP ? n : n / (4 * GROUP);
-  return k < (int64_t)SMALL_K ? k : (int64_t)SMALL_K;
+  return k < (int64_t)SMALL_K || n <= (int64_t)CAP ? k : (int64_t)SMALL_K;
 }
 
-// top_k of such a row; 0: it is none.
+// How many of a row's first entries are looked at, where that is a small number
+// (of a short row with top_p all of them); 0: it is not, or there is no cut.
 __device__ __forceinline__ uint32_t small_k(const SampleArgs& a, uint64_t r) {
   if (!a.groups) return 0;
   if (!(temperature_of(a, r) > 0.f)) return 1;
   const int64_t k = a.top_ks ? a.top_ks[r] : a.top_k;
-  return k > 0 && k <= small_limit(a.n) ? (uint32_t)k : 0u;
+  if (k > 0 && k <= small_limit(a.n)) return (uint32_t)k;
+  return a.n <= CAP && !(top_p_of(a, r) >= 1.f) ? a.n : 0u;
 }
 
 // TILE logits from i0 on, whole vectors to a thread; -inf behind `end`.  (NaN is
@@ -924,8 +926,9 @@ __global__ __launch_bounds__(ROW_THREADS) void k_sample_finish(SampleArgs a) {
 
 struct SamplePlan {
   uint32_t chunk = TILE, chunks = 0, bits = 62;
-  bool cut = true;       // some row has a cut that is not a small top_k
-  bool small = false;    // some row's top_k is small
+  bool cut = true;       // some row may have a cut that is not among a small number of its first entries
+  bool small = false;    // some row may have one that is,
+  bool all_small = false;// all rows have
   size_t off_max = 0, off_settings = 0, off_collected = 0, off_sums = 0, off_groups = 0, off_count = 0, off_bins = 0, off_cand = 0, off_row = 0,
          total = 0;
 };
@@ -936,12 +939,13 @@ SamplePlan sample_plan(const topk_sample_args& a) {
   p.chunks = (uint32_t)ceil_div(a.n, p.chunk);
   while ((int64_t(1) << (62 - p.bits)) < a.n) --p.bits;
   // what the numbers among the settings say of all rows
-  const bool tile = p.chunk == TILE;
+  const bool tile = p.chunk == TILE, brief = a.n <= (int64_t)CAP;
   const bool greedy = !a.temperatures && !(a.temperature > 0.f);
-  const bool k_small = greedy || (!a.top_ks && a.top_k > 0 && a.top_k <= small_limit(a.n));
-  p.small = tile && (k_small || a.top_ks || a.temperatures);
-  const bool cuts = a.top_ks || (a.top_k > 0 && a.top_k < a.n) || a.top_ps || !(a.top_p >= 1.f) || greedy || (a.temperatures && !tile);
-  p.cut = cuts && !(tile && k_small);
+  const bool nucleus = !a.top_ps && !(a.top_p >= 1.f);
+  p.all_small = tile && (greedy || (!a.top_ks && a.top_k > 0 && a.top_k <= small_limit(a.n)) || (brief && nucleus));
+  const bool cuts = a.top_ks || (a.top_k > 0 && a.top_k < a.n) || a.top_ps || nucleus;
+  p.small = p.all_small || (tile && (a.top_ks || a.temperatures || (brief && cuts)));
+  p.cut = !p.all_small && !brief && (cuts || (!tile && (greedy || a.temperatures)));
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t here = at;
@@ -951,7 +955,7 @@ SamplePlan sample_plan(const topk_sample_args& a) {
   const size_t rows = (size_t)a.rows;
   p.off_max = take(rows * p.chunks * 4);
   p.off_settings = take(rows * sizeof(Settings));
-    p.off_sums = take(rows * p.chunks * 8);
+  p.off_sums = take(rows * p.chunks * 8);
   if (p.small) p.off_groups = take(rows * p.chunks * FIRST_THREADS * 4);
   if (p.cut) {
     p.off_count = take(rows * BINS * 4);
@@ -965,15 +969,13 @@ SamplePlan sample_plan(const topk_sample_args& a) {
 }
 
 template <class T>
-hipError_t sample_call(SampleArgs a, const SamplePlan& p, const topk_sample_args& in, hipStream_t s) {
-  const uint64_t rows = (uint64_t)in.rows;
+hipError_t sample_call(SampleArgs a, const SamplePlan& p, uint64_t rows, hipStream_t s) {
   a.work = rows * p.chunks;
   const dim3 chunks = wide_grid(a.work);
   k_sample_first<T><<<chunks, FIRST_THREADS, 0, s>>>(a);
   if (p.cut) k_sample_bins<T><<<chunks, ROW_THREADS, 0, s>>>(a);
-  const bool all_small = p.small && !p.cut && ((!in.temperatures && !(in.temperature > 0.f)) || in.top_k > 0);
   if (p.cut) k_sample_collect<T, true><<<chunks, ROW_THREADS, 0, s>>>(a);
-  else if (!all_small) k_sample_collect<T, false><<<chunks, ROW_THREADS, 0, s>>>(a);
+  else if (!p.all_small) k_sample_collect<T, false><<<chunks, ROW_THREADS, 0, s>>>(a);
   a.work = rows;
   k_sample_finish<T><<<wide_grid(rows), ROW_THREADS, 0, s>>>(a);
   return hipGetLastError();
@@ -1004,7 +1006,7 @@ hipError_t launch_sample(const topk_sample_args& in, void* ws, hipStream_t s) {
   a.temperature = in.temperature, a.top_p = in.top_p, a.min_p = in.min_p;
   a.n = (uint32_t)in.n;
   a.chunk = p.chunk, a.chunks = p.chunks, a.bits = p.bits;
-  return in.dtype == TOPK_BF16 ? sample_call<bf16_t>(a, p, in, s) : sample_call<float>(a, p, in, s);
+  return in.dtype == TOPK_BF16 ? sample_call<bf16_t>(a, p, (uint64_t)in.rows, s) : sample_call<float>(a, p, (uint64_t)in.rows, s);
 }
 
 }  // namespace tk

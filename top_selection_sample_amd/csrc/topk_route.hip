@@ -42,9 +42,10 @@ RoutePlan route_plan(int64_t tokens, int64_t k, int64_t experts) {
   while ((uint64_t(1) << p.digit_bits) < p.bins) ++p.digit_bits;
   p.small = p.total <= SMALL_TOTAL && experts <= SMALL_EXPERTS;
   if (p.small) return p;
-  const int64_t blocks = std::min<int64_t>(256, ceil_div(p.total, SORT_THREADS));
-  p.per_block = (uint32_t)(ceil_div(p.total, blocks * SORT_THREADS) * SORT_THREADS);
-  p.blocks = (uint32_t)ceil_div(p.total, p.per_block);
+  const int64_t total = std::max<int64_t>(p.total, 1);
+  const int64_t blocks = std::min<int64_t>(256, ceil_div(total, SORT_THREADS));
+  p.per_block = (uint32_t)(ceil_div(total, blocks * SORT_THREADS) * SORT_THREADS);
+  p.blocks = (uint32_t)ceil_div(total, p.per_block);
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t here = at;
@@ -319,7 +320,7 @@ hipError_t dispatch_typed(const topk_dispatch_args& a, const RoutePlan& p, char*
     k_route_place<true><<<p.blocks, SORT_THREADS, p.bins * 4, s>>>(a.experts, cnt, all, a.places, a.offsets, pos, p.total, p.per_block,
                                                                    p.bins, p.digit_bits);
   }
-  if (d) {
+  if (d && p.total) {
     const uint32_t pieces = (d + 64 * VEC * PIECE - 1) / (64 * VEC * PIECE);
     const uint64_t items = (uint64_t)a.tokens * pieces;
     auto* move = (int64_t)p.total * a.d * (int64_t)sizeof(U) >= STREAM_BYTES ? k_dispatch_move<U, VEC, true> : k_dispatch_move<U, VEC, false>;
