@@ -423,10 +423,15 @@ __global__ __launch_bounds__(ROW_THREADS) void k_sample_bins(SampleArgs a) {
 }
 
 // Of a row without a cut, every bin is before it.  CUT: some row has one.
+//
+// Without CUT the logits whose weight counts are listed first and then looked at
+// by consecutive threads: with a min_p few do, and a weight takes a wave the
+// same time for one of them as for 64.
 template <class T, bool CUT>
 __global__ __launch_bounds__(ROW_THREADS) void k_sample_collect(SampleArgs a) {
   __shared__ uint64_t code[CUT ? TILE : 1];            // the plan's sums, then the entries to be handed on
   __shared__ uint32_t counts[CUT ? BINS + 1 : 1];
+  __shared__ float listed[CUT ? 1 : TILE];
   static_assert(TILE > BINS, "the plan's sums fit");
   __shared__ uint32_t part32[ROW_WAVES], mark[3], taken, base;
   __shared__ uint64_t part64[ROW_WAVES];
@@ -451,20 +456,34 @@ __global__ __launch_bounds__(ROW_THREADS) void k_sample_collect(SampleArgs a) {
   }
   const double min_p = min_p_of(a, r);
   uint64_t sum = 0;
+  if constexpr (!CUT) __syncthreads();
   for (uint32_t at = i0;;) {
 #pragma unroll
     for (uint32_t j = 0; j < tile.PER; ++j) {
       const float z = tile.z[j];
       const uint32_t b = v.cut && live(z, m) ? bin_of(z, m) : 0u;
       const bool sure = !(m - z > s.far) && z > -INFINITY && (!v.cut || b < v.lo);
-      if (__any(sure)) {   // few waves hold a weight that counts
-        const double w = weight_of(z, m, s);
-        if (sure && w >= min_p) sum += fixed_of(w, a.bits);
-      }
-      if constexpr (CUT)
+      if constexpr (!CUT) {
+        if (sure) listed[atomicAdd(&taken, 1u)] = z;
+      } else {
+        if (__any(sure)) {
+          const double w = weight_of(z, m, s);
+          if (sure && w >= min_p) sum += fixed_of(w, a.bits);
+        }
         if (v.cut && live(z, m) && b >= v.lo && (b <= v.hi || b == v.bk)) code[atomicAdd(&taken, 1u)] = code_of(z, tile.index(at, j));
+      }
     }
-    if (CUT && v.cut) {
+    if constexpr (!CUT) {
+      __syncthreads();
+      const uint32_t n = taken;
+      for (uint32_t i = threadIdx.x; i < n; i += ROW_THREADS) {
+        const double w = weight_of(listed[i], m, s);
+        if (w >= min_p) sum += fixed_of(w, a.bits);
+      }
+      __syncthreads();
+      if (threadIdx.x == 0) taken = 0;
+      __syncthreads();
+    } else if (v.cut) {
       __syncthreads();
       if (threadIdx.x == 0 && taken) base = atomicAdd(&a.collected[r], taken);
       __syncthreads();
