@@ -571,7 +571,7 @@ struct alignas(16) RowShared {
   uint64_t sums[MAX_CHUNKS];   // weight that stays, by chunk
   uint64_t part64[ROW_WAVES], found[2], rest;
   uint32_t count[BINS];
-  uint32_t part32[ROW_WAVES], pick, taken, flag;
+  uint32_t part32[ROW_WAVES], pick;
 };
 
 __device__ __forceinline__ void write_token(const SampleArgs& a, uint64_t r, int64_t token, uint64_t w, uint64_t all) {
@@ -580,22 +580,24 @@ __device__ __forceinline__ void write_token(const SampleArgs& a, uint64_t r, int
 }
 
 // Each of the n <= PAIRS threads' value: the sum over all j < n of what `take`
-// says of l.code[j], l.sorted[j].  All threads share the pairs.
+// says of l.code[j], l.sorted[j].  All threads share the pairs; one holds two
+// rows of them, which halves what is read from LDS.
 template <class F>
 __device__ __forceinline__ uint64_t over_pairs(RowShared& l, uint32_t n, F take) {
   constexpr uint32_t AHEAD = 8;
   const uint32_t t = threadIdx.x;
-  uint32_t shift = 0;      // entries rounded up to a power of two, 1 << shift
-  while ((1u << shift) < n) ++shift;
-  const uint32_t i = t & ((1u << shift) - 1), parts = ROW_THREADS >> shift, part = t >> shift;
+  uint32_t shift = 0;      // half the entries, rounded up to a power of two, 1 << shift
+  while ((2u << shift) < n) ++shift;
+  const uint32_t half = 1u << shift, i = t & (half - 1), parts = ROW_THREADS >> shift, part = t >> shift;
   const uint32_t end = (n + AHEAD - 1) / AHEAD * AHEAD;     // zeros from n on
   const uint32_t per = (end / AHEAD + parts - 1) / parts * AHEAD, j0 = part * per, j1 = min(j0 + per, end);
   if (t < PAIRS) l.pair[t] = 0;
   if (n + t < end) l.code[n + t] = l.sorted[n + t] = 0;
   __syncthreads();
-  if (i < n) {
-    const uint64_t own = l.code[i];
-    uint64_t sum = 0;
+  const bool low = i < n, high = i + half < n;
+  if (low) {
+    const uint64_t own0 = l.code[i], own1 = l.code[high ? i + half : i];
+    uint64_t sum0 = 0, sum1 = 0;
     for (uint32_t j = j0; j < j1; j += AHEAD) {
       uint64_t c[AHEAD], w[AHEAD];
 #pragma unroll
@@ -604,10 +606,13 @@ __device__ __forceinline__ uint64_t over_pairs(RowShared& l, uint32_t n, F take)
         w[x] = l.sorted[j + x];
       }
 #pragma unroll
-      for (uint32_t x = 0; x < AHEAD; ++x) sum += take(own, c[x], w[x]);
+      for (uint32_t x = 0; x < AHEAD; ++x) {
+        sum0 += take(own0, c[x], w[x]);
+        sum1 += take(own1, c[x], w[x]);
+      }
     }
-    if (parts == 1) l.pair[i] = sum;
-    else if (sum) atomicAdd(reinterpret_cast<unsigned long long*>(&l.pair[i]), (unsigned long long)sum);
+    if (sum0) atomicAdd(reinterpret_cast<unsigned long long*>(&l.pair[i]), (unsigned long long)sum0);
+    if (high && sum1) atomicAdd(reinterpret_cast<unsigned long long*>(&l.pair[i + half]), (unsigned long long)sum1);
   }
   __syncthreads();
   return t < n ? l.pair[t] : 0;
@@ -852,7 +857,6 @@ __device__ void finish_small(const SampleArgs& a, uint64_t r, const T* row, floa
   };
   load(t * 4);
   for (uint32_t i = t; i < BINS; i += ROW_THREADS) l.count[i] = 0;
-  if (t == 0) l.taken = l.flag = 0;
   __syncthreads();
   for (uint32_t g0 = t * 4;;) {
 #pragma unroll
@@ -869,22 +873,29 @@ __device__ void finish_small(const SampleArgs& a, uint64_t r, const T* row, floa
   const float below = bin_end(last);
   auto near = [&](float z) { return m - z < below || z == m; };   // m > -inf
   uint32_t* hits = reinterpret_cast<uint32_t*>(l.sums);           // 2 * MAX_CHUNKS of them
-  for (uint32_t g0 = t * 4; g0 < groups; g0 += BATCH) {
+  uint32_t found = 0;
+  for (uint32_t b0 = 0; b0 < groups; b0 += BATCH) {
+    const uint32_t g0 = b0 + t * 4;
     if (groups > BATCH) load(g0);
+    uint32_t mask = 0, all;
 #pragma unroll
     for (uint32_t i = 0; i < AHEAD; ++i)
 #pragma unroll
-      for (uint32_t j = 0; j < 4; ++j)
-        if (near(v[i][j])) {
-          const uint32_t at = atomicAdd(&l.flag, 1u);
-          if (at < 2 * MAX_CHUNKS) hits[at] = g0 + i * ROW_THREADS * 4 + j;
-        }
+      for (uint32_t j = 0; j < 4; ++j) mask |= near(v[i][j]) ? 1u << (i * 4 + j) : 0u;
+    uint32_t at = found + thread_scan<ROW_THREADS>((uint32_t)__popc(mask), l.part32, &all);
+    for (; mask; mask &= mask - 1, ++at) {
+      const uint32_t x = __builtin_ctz(mask);
+      if (at < 2 * MAX_CHUNKS) hits[at] = g0 + x / 4 * ROW_THREADS * 4 + x % 4;
+    }
+    found += all;
   }
   __syncthreads();
-  const uint32_t found = l.flag;
+  uint32_t taken = 0;
   if (found <= 2 * MAX_CHUNKS) {
-    for (uint32_t x = t; x < found * VECS; x += ROW_THREADS) {
-      const uint32_t g = hits[x / VECS];
+    for (uint32_t x0 = 0; x0 < found * VECS; x0 += ROW_THREADS) {
+      const uint32_t x = x0 + t;
+      const bool there = x < found * VECS;
+      const uint32_t g = hits[there ? x / VECS : 0];
       const uint32_t i0 = g / FIRST_THREADS * TILE + (x % VECS * FIRST_THREADS + g % FIRST_THREADS) * VEC;
       float z[VEC];
       if (i0 + VEC <= a.n) {
@@ -893,12 +904,17 @@ __device__ void finish_small(const SampleArgs& a, uint64_t r, const T* row, floa
 #pragma unroll
         for (uint32_t j = 0; j < VEC; ++j) z[j] = i0 + j < a.n ? to_f32(row[i0 + j]) : -INFINITY;
       }
+      uint32_t mine = 0, all;
+#pragma unroll
+      for (uint32_t j = 0; j < VEC; ++j) mine += there && near(z[j]);
+      uint32_t at = taken + thread_scan<ROW_THREADS>(mine, l.part32, &all);
 #pragma unroll
       for (uint32_t j = 0; j < VEC; ++j)
-        if (near(z[j])) {
-          const uint32_t at = atomicAdd(&l.taken, 1u);
+        if (there && near(z[j])) {
           if (at < CAP) l.code[at] = code_of(z[j], i0 + j);
+          ++at;
         }
+      taken += all;
     }
   }
   __syncthreads();
@@ -908,7 +924,7 @@ __device__ void finish_small(const SampleArgs& a, uint64_t r, const T* row, floa
   w.hi = w.bk = BINS - 1;      // the list is a beginning of the row's order
   w.before = w.before_k = 0;
   w.k = k;
-  const uint32_t n = found <= 2 * MAX_CHUNKS ? l.taken : CAP + 1;
+  const uint32_t n = found <= 2 * MAX_CHUNKS ? taken : CAP + 1;
   __syncthreads();
   finish_row(a, r, row, m, s, w, n, true, l);
 }
