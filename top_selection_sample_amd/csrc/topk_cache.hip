@@ -745,8 +745,10 @@ struct EvictArgs {
 // at most their sum); *need becomes what is wanted of it.  Returns the bin, in
 // bit 31 whether all of it is wanted.
 //
-// The counts come in COPIES, one for every COPIES-th lane: scores crowd in few
-// bins, and lanes that count in the same place wait for one another.
+// The counts come in COPIES, one for every COPIES-th lane: lanes that count in
+// the same place wait for one another (128 rows of 16384 with a copy of 8
+// columns: all scores equal 59 us with one copy, 30 with four, 27 with eight;
+// spread scores 30, 31 and 32).
 constexpr uint32_t PICK_BINS = 2048, COPIES = 4, COPY_STRIDE = PICK_BINS + 8, ALL_OF_BIN = 0x80000000u;
 constexpr uint32_t ZERO_KEY = 0x80000000u;
 __device__ __forceinline__ uint32_t bin_from_top(const uint32_t* hist, uint32_t* need, uint32_t* part, uint32_t* found) {
