@@ -283,6 +283,15 @@ def test_evict_into_interleaved_buffers():
     assert torch.equal(k, k0) and torch.equal(v, v0)
 
 
+def test_attend_many_sequences():
+    # more of them than lanes, and than lanes squared; most are empty, and one is long
+    for b, n, d in ((70, 400, 16), (700, 300, 8), (5000, 300, 8)):
+        q, k, v = rnd(1, b, 2, d), rnd(2, b, 1, n, d), rnd(3, b, 1, n, d)
+        lengths = torch.randint(-n, n + 1, (b,), generator=torch.Generator().manual_seed(b)).cuda()
+        lengths[b // 3] = n
+        check_attend(q, k, v, lengths, label=b)
+
+
 def test_attend_nothing_at_all():
     for n in (5, 5000):
         q, k = rnd(1, 3, 4, 40), torch.full((3, 2, n, 40), NAN, device="cuda")

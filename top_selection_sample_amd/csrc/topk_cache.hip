@@ -62,6 +62,7 @@ struct AttArgs {
   float* logits;      // [batch * heads][n], in units of log 2; null: not wanted
   float* part;        // [pieces][min(group, HEADS)][d]
   float* ml;          // [pieces][HEADS][2]: maximum and sum
+  uint32_t* ends;     // [rows][2]: the first and the last workgroup of a row's pieces
   int64_t sqb, sqh, skb, skh, skn, svb, svh, svn, ssb, ssh, sob, soh;
   uint64_t work;      // workgroups of the launch
   uint32_t batch, kv_heads, group, blocks16, n, d;
@@ -110,12 +111,13 @@ __device__ __forceinline__ const T* at_offset(const T* base, uint32_t bytes) {
 // ATT_WAVES steps, all units of all sequences are numbered in that order, and
 // workgroup w of `share` (at most one a unit) has those from w * all / share on.
 // What it does of one row is a piece; row r of all and workgroup w make piece
-// r + w, for no two pieces have the same sum.
+// r + w, for no two pieces have the same sum, and those of a row are
+// consecutive.
 struct Place {
   uint64_t all;       // units of all sequences
-  uint64_t share;     // workgroups that have any
-  uint64_t before;    // those before sequence b
-  uint32_t b, units;  // the sequence, and the units of one of its rows
+  uint64_t from, to;  // the workgroup's
+  uint64_t before;    // those before sequence b, in which `from` lies
+  uint32_t b, units;  // units: of one of b's rows
 };
 
 // a / b; a 64-bit division takes hundreds of instructions, and is seldom one.
@@ -129,55 +131,52 @@ __device__ __forceinline__ uint32_t units_of(const AttArgs& a, uint32_t b) {
   return (length_of(a.lengths, b, a.n) + UNIT - 1) / UNIT;
 }
 
-// The sequence `want`, or where that is negative the one that the first unit of
-// workgroup ~want lies in.  Every wave for itself, a sequence to a lane.
+// Where workgroup w begins; false if nothing is left for it.  Every wave for
+// itself: a lane adds up a 64th of the sequences, then the 64th that holds the
+// unit looked for is divided in the same way.
 template <uint32_t UNIT>
-__device__ __forceinline__ Place place_of(const AttArgs& a, int64_t want) {
+__device__ __forceinline__ bool place_of(const AttArgs& a, uint64_t w, Place* p) {
   const uint32_t lane = threadIdx.x % 64, rows = a.kv_heads * a.blocks16;
-  Place p;
+  auto share_out = [&](uint64_t all) {
+    p->all = all;
+    const uint64_t share = min((uint64_t)a.share, all);
+    if (w >= share) return false;
+    p->from = quotient(w * all, share);
+    p->to = quotient((w + 1) * all, share);
+    return true;
+  };
   if (!a.lengths) {
-    p.units = (a.n + UNIT - 1) / UNIT;
-    const uint64_t each = (uint64_t)p.units * rows;
-    p.all = each * a.batch;
-    p.share = min((uint64_t)a.share, p.all);
-    p.b = want >= 0 ? (uint32_t)want : (uint32_t)quotient(quotient((uint64_t)~want * p.all, p.share), each);
-    p.before = p.b * each;
-    return p;
+    p->units = (a.n + UNIT - 1) / UNIT;
+    const uint64_t each = (uint64_t)p->units * rows;
+    if (!share_out(each * a.batch)) return false;
+    p->b = (uint32_t)quotient(p->from, each);
+    p->before = p->b * each;
+    return true;
   }
-  uint64_t all = 0, last = 0;     // `last`: of the last 64 sequences
-  uint32_t mine = 0;
-  for (uint32_t b0 = 0; b0 < a.batch; b0 += 64) {
-    mine = b0 + lane < a.batch ? units_of<UNIT>(a, b0 + lane) : 0u;
-    last = wave_sum((uint64_t)mine * rows);
-    all += last;
-  }
-  p.all = all;
-  p.share = min((uint64_t)a.share, all);
-  p.b = 0;
-  p.before = 0;
-  p.units = 0;
-  if (all == 0) return p;
-  const uint64_t unit = want >= 0 ? 0 : quotient((uint64_t)~want * all, p.share);
-  uint64_t base = 0;
-  for (uint32_t b0 = 0; b0 < a.batch; b0 += 64) {
-    if (a.batch > 64) mine = b0 + lane < a.batch ? units_of<UNIT>(a, b0 + lane) : 0u;
-    uint64_t up = (uint64_t)mine * rows;
-#pragma unroll
-    for (uint32_t o = 1; o < 64; o <<= 1) {
-      const uint64_t t = __shfl_up(up, o);
-      if (lane >= o) up += t;
+  uint32_t lo = 0, count = a.batch;
+  p->before = 0;
+  for (bool first = true;; first = false) {
+    const uint32_t per = (count + 63) / 64;
+    uint64_t mine = 0;
+#pragma unroll 8
+    for (uint32_t i = 0; i < per; ++i) {
+      const uint32_t x = lane * per + i;
+      const uint32_t units = units_of<UNIT>(a, min(lo + x, a.batch - 1));   // loads that nothing hangs on
+      mine += x < count ? units : 0u;
     }
-    const uint64_t hit = want >= 0 ? __ballot(b0 + lane == (uint64_t)want) : __ballot(base + up > unit);
-    if (hit) {
-      const int x = __builtin_ctzll(hit);
-      p.b = b0 + (uint32_t)x;
-      p.units = __shfl(mine, x);
-      p.before = base + __shfl(up, x) - (uint64_t)p.units * rows;
-      break;
+    mine *= rows;
+    const uint64_t up = wave_incl_sum(mine);
+    if (first && !share_out(bcast64(up, 63u))) return false;
+    const uint32_t x = (uint32_t)__builtin_ctzll(__ballot(p->before + up > p->from));   // some lane's is: from < all
+    p->before += bcast64(up - mine, x);
+    lo += x * per;
+    if (per == 1) {
+      p->b = lo;
+      p->units = (uint32_t)quotient(bcast64(mine, x), rows);
+      return true;
     }
-    base += __shfl(up, 63);
+    count = min(per, count - x * per);
   }
-  return p;
 }
 
 // KC: chunks of a key's columns; VB: blocks of 16 * VW columns of V.  ONCE: the
@@ -200,14 +199,13 @@ __global__ __launch_bounds__(ATT_THREADS, KC * VB > 8 ? 1 : 2) void k_attend(Att
   uint32_t b, row, unit;   // where they begin
   uint32_t units;
   if (a.share) {
-    const Place p = place_of<UNIT>(a, ~(int64_t)id);
-    if (id >= p.share) return;
-    const uint64_t from = quotient(id * p.all, p.share);
-    todo = quotient((id + 1) * p.all, p.share) - from;
+    Place p;
+    if (!place_of<UNIT>(a, id, &p)) return;
+    todo = p.to - p.from;
     b = p.b;
     units = p.units;
-    row = (uint32_t)quotient(from - p.before, units);
-    unit = (uint32_t)(from - p.before - (uint64_t)row * units);
+    row = (uint32_t)quotient(p.from - p.before, units);
+    unit = (uint32_t)(p.from - p.before - (uint64_t)row * units);
   } else {
     b = (uint32_t)quotient(id, rows);
     row = (uint32_t)(id - (uint64_t)b * rows);
@@ -437,6 +435,11 @@ __global__ __launch_bounds__(ATT_THREADS, KC * VB > 8 ? 1 : 2) void k_attend(Att
       else a.part[(piece * min(HEADS, a.group) + head) * d + c] = v;
     }
     if (a.share) {
+      if (threadIdx.x == 0) {
+        const uint64_t r = (uint64_t)b * rows + row;
+        if (s0 == 0) a.ends[2 * r] = (uint32_t)id;
+        if (unit + now_units == units) a.ends[2 * r + 1] = (uint32_t)id;
+      }
       if (threadIdx.x < heads) {
         float* ml = a.ml + (piece * HEADS + threadIdx.x) * 2;
         ml[0] = wl[HEADS + threadIdx.x];
@@ -473,7 +476,6 @@ __global__ __launch_bounds__(JOIN_THREADS) void k_attend_join(AttArgs a, uint32_
   // outputs: a factor for each piece; scores: a maximum and the inverse of a sum for each head
   extern __shared__ float shared[];
   __shared__ float part[4][HEAD_MAX];
-  constexpr uint32_t UNIT = ATT_WAVES * Att<T>::STEP;
   constexpr uint32_t PER = JOIN_KEYS / JOIN_THREADS, AHEAD = 4;
   const uint64_t id = block_id();
   if (id >= a.work) return;
@@ -503,16 +505,12 @@ __global__ __launch_bounds__(JOIN_THREADS) void k_attend_join(AttArgs a, uint32_
       for (uint32_t i = 0; i < AHEAD; ++i) ahead[i][x] = i < a.group && k0 + key < len ? logits[(uint64_t)i * a.n + key] : 0.f;
     }
   }
-  const Place p = place_of<UNIT>(a, b);
-  const uint32_t rows = a.kv_heads * a.blocks16;
-  auto owner = [&](uint64_t unit) { return quotient((unit + 1) * p.share + p.all - 1, p.all) - 1; };
   // first and number of the pieces of a row of this head
   auto pieces_of = [&](uint32_t hb, uint64_t* from) {
-    const uint32_t row = h * a.blocks16 + hb;
-    const uint64_t u0 = p.before + (uint64_t)row * p.units;
-    const uint64_t w0 = owner(u0), w1 = owner(u0 + p.units - 1);
-    *from = (uint64_t)b * rows + row + w0;
-    return (uint32_t)(w1 - w0 + 1);
+    const uint64_t row = bh * a.blocks16 + hb;
+    const uint32_t w0 = a.ends[2 * row], w1 = a.ends[2 * row + 1];
+    *from = row + w0;
+    return w1 - w0 + 1;
   };
   if (which < a.group) {
     uint64_t from;
@@ -590,7 +588,7 @@ __global__ __launch_bounds__(JOIN_THREADS) void k_attend_join(AttArgs a, uint32_
 
 struct AttPlan {
   uint32_t blocks16 = 1, share = 0;
-  size_t off_logits = 0, off_part = 0, off_ml = 0, total = 0;
+  size_t off_logits = 0, off_part = 0, off_ml = 0, off_ends = 0, total = 0;
 };
 
 // A row that one workgroup soon goes through is one workgroup's, in one launch;
@@ -616,6 +614,7 @@ AttPlan attend_plan(const topk_attend_args& a, int cus) {
     const size_t pieces = (size_t)(rows + p.share);
     p.off_part = take(pieces * (size_t)(std::min<int64_t>(group, HEADS) * a.d) * 4);
     p.off_ml = take(pieces * HEADS * 8);
+    p.off_ends = take((size_t)rows * 8);
   }
   p.total = at;
   return p;
@@ -678,6 +677,7 @@ hipError_t attend_call(const topk_attend_args& in, const AttPlan& p, char* ws, h
   a.logits = in.scores ? reinterpret_cast<float*>(ws + p.off_logits) : nullptr;
   a.part = reinterpret_cast<float*>(ws + p.off_part);
   a.ml = reinterpret_cast<float*>(ws + p.off_ml);
+  a.ends = reinterpret_cast<uint32_t*>(ws + p.off_ends);
   const uint64_t heads = (uint64_t)in.batch * a.kv_heads;
   a.work = p.share ? p.share : heads * p.blocks16;
   attend_typed(a, T{}, s);

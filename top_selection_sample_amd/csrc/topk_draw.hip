@@ -114,7 +114,7 @@ __device__ __forceinline__ Settings make_settings(const SampleArgs& a, uint64_t 
   s.rate = s.greedy ? 0.0 : 1.4426950408889634 / (double)t;
   const double least = p > 0.0 ? fmax(log2(p) - 1e-3, -64.0) : -64.0;
   const double far = s.rate > 0.0 ? -least / s.rate * (1.0 + 1e-6) : INFINITY;
-  s.far = s.greedy ? 0.f : far < 3e38 ? (float)far : INFINITY;
+  s.far = s.greedy ? 0.f : far < 3e38 ? __uint_as_float(__float_as_uint((float)far) + 1) : INFINITY;   // rounded up
   return s;
 }
 
