@@ -518,7 +518,8 @@ int topk_combine(const topk_combine_args* args, void* stream);
 
 /* Gradients of topk_combine from grad = dL/dout:
  *   dy[p] = sum over the entries e at place p of weights[e] * grad[token e]
- *           (every row written: 0 where there is none)
+ *           (every row written: 0 where there is none; products of 32 bits, of
+ *           which several are added without a further rounding to 32 bits)
  *   dweights[e] = <grad[token e], y[places[e]]>; 0 where the place is out of range
  * Each output may be null: not wanted; y is not read without dweights. */
 typedef struct {
@@ -550,7 +551,7 @@ typedef struct {
   const int64_t* lengths;    /* [batch], or null: all n */
   float* scores;             /* [batch, kv_heads, n], strides ssb, ssh, no two rows overlapping; null: not wanted */
   void* out;                 /* [batch, heads, d], strides sob, soh */
-  int64_t batch, heads, kv_heads, n, d;   /* heads a multiple of kv_heads, up to 4096 times; d <= 256 */
+  int64_t batch, heads, kv_heads, n, d;   /* heads a multiple of kv_heads, up to 4096 times; d <= 256; skn, svn < 2^24 */
   int64_t sqb, sqh, skb, skh, skn, svb, svh, svn, ssb, ssh, sob, soh;
   float scale;
   int32_t dtype;

@@ -129,6 +129,29 @@ def test_cut_in_two_places():
         check(z, uni(4, 3), kw, **kw)
 
 
+def test_cut_inside_the_first_logits():
+    # the nucleus ends among a few logits next to the largest, the k-th is far behind, and most of what p counts lies between
+    z = rnd(2, 4, 60000, scale=0.5) - 3.0
+    z[:, 100:105] = torch.tensor([5.0, 4.9999, 4.9998, 4.9997, 4.9996])
+    z[1:3, 7] = 4.99985
+    for k in (40000, 59000, 0):
+        for p in (0.02, 0.05, 0.08, 0.1):
+            check(z, uni(5, 4), (k, p), top_k=k, top_p=p)
+    check(z[:, :3000].contiguous(), uni(6, 4), "short", top_k=2000, top_p=0.5)
+
+
+@pytest.mark.parametrize("n", [511, 512, 513, 700, 2000, 4096, 6143, 6144, 20000])
+def test_limits_of_the_ways(n):
+    # k around those at which another way is taken, with and without top_p
+    z = rnd(n, 2, n, scale=1.5)
+    for k in sorted({3 * n // 64, 3 * n // 64 + 1, n // 64, n // 64 + 1, 384, 385, 512, 513, n - 1}):
+        if 0 < k <= n:
+            check(z, uni(k, 2), (n, k), top_k=k)
+            check(z, uni(k + 1, 2), (n, k, "p"), top_k=k, top_p=0.9)
+    for p in (0.3, 0.9, 0.99):
+        check(z, uni(n, 2), (n, p), top_p=p)
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("kw", [dict(), dict(top_k=3), dict(top_p=0.9), dict(top_k=2, top_p=0.5, min_p=0.1), dict(temperature=0.0)])
 def test_masks(dt, kw):

@@ -54,7 +54,7 @@ constexpr uint32_t BINS = 2048;             // 16 octaves of m - z from 2^-7 on,
 constexpr uint32_t FIRST_BIN = (127 - 7) << 7;
 constexpr uint32_t CAP = 4096;              // entries of a row around its cut that are sorted
 constexpr uint32_t GROUP = TILE / FIRST_THREADS;   // entries of a thread of k_sample_first
-constexpr uint32_t SMALL_K = 1024;          // a small top_k of a long row: up to here, and of a row of four groups for each
+constexpr uint32_t SMALL_K = 384;           // a small top_k
 constexpr uint32_t PAIRS = 512;             // entries that are compared each with each rather than sorted
 
 // What is known of a row between the launches.
@@ -65,6 +65,7 @@ struct SampleRow {
   uint32_t count, count_k;// entries of the bins below lo and bk
   uint32_t k;             // top_k, where bk says so
   uint32_t cut;           // whether there is a cut
+  uint32_t inside;        // all that can stay is collected
 };
 
 // The settings of a row, worked out once for all its workgroups.
@@ -215,12 +216,14 @@ __device__ __forceinline__ float row_max(const SampleArgs& a, uint64_t r) {
   return wave_top(m);
 }
 
-// A row whose k is at most this gets its first k by way of its groups: not many
-// entries reach what k of many groups do, and all entries of a short row can be
-// sorted.
+// A row whose k is at most this gets its first k by way of its groups.  Where k
+// of G groups reach a bin, about n (1 - (1 - k / G)^(1 / GROUP)) entries do: 1.15
+// k for a quarter of the groups, an eighth of the row for three quarters.  So
+// many are compared each with each, if they are at most PAIRS.
 __host__ __device__ __forceinline__ int64_t small_limit(int64_t n) {
-  const int64_t k = n <= (int64_t)CAP ? n : n / (4 * GROUP);
-  return k < (int64_t)SMALL_K || n <= (int64_t)CAP ? k : (int64_t)SMALL_K;
+  if (n <= (int64_t)PAIRS) return n;
+  const int64_t k = n < 12 * (int64_t)PAIRS ? 3 * n / (4 * GROUP) : n / (4 * GROUP);
+  return k < (int64_t)SMALL_K ? k : (int64_t)SMALL_K;
 }
 
 // How many of a row's first entries are looked at, where that is a small number
@@ -230,7 +233,7 @@ __device__ __forceinline__ uint32_t small_k(const SampleArgs& a, uint64_t r) {
   if (!(temperature_of(a, r) > 0.f)) return 1;
   const int64_t k = a.top_ks ? a.top_ks[r] : a.top_k;
   if (k > 0 && k <= small_limit(a.n)) return (uint32_t)k;
-  return a.n <= CAP && !(top_p_of(a, r) >= 1.f) ? a.n : 0u;
+  return a.n <= PAIRS && !(top_p_of(a, r) >= 1.f) ? a.n : 0u;
 }
 
 // TILE logits from i0 on, whole vectors to a thread; -inf behind `end`.  (NaN is
@@ -327,10 +330,12 @@ __device__ SampleRow plan_row(const SampleArgs& a, uint64_t r, uint32_t* c_befor
   uint64_t w[PER], wall;
   uint32_t cs = 0;
   uint64_t ws = 0;
+  int64_t k = a.top_ks ? a.top_ks[r] : a.top_k;
+  if (!(temperature_of(a, r) > 0.f)) k = 1;
 #pragma unroll
   for (uint32_t i = 0; i < PER; ++i) {
-    cs += c[i] = a.bin_count[r * BINS + t * PER + i];
     ws += w[i] = a.bin_sum[r * BINS + t * PER + i];
+    cs += c[i] = k > 0 ? a.bin_count[r * BINS + t * PER + i] : w[i] != 0;   // without top_k only whether there are any counts
   }
   uint32_t cb = thread_scan<ROW_THREADS>(cs, part32, &call);
   uint64_t wb = thread_scan<ROW_THREADS>(ws, part64, &wall);
@@ -349,8 +354,6 @@ __device__ SampleRow plan_row(const SampleArgs& a, uint64_t r, uint32_t* c_befor
     lo = hi = 0;
   }
   __syncthreads();
-  int64_t k = a.top_ks ? a.top_ks[r] : a.top_k;
-  if (!(temperature_of(a, r) > 0.f)) k = 1;
   const bool cut_k = k > 0 && k < (int64_t)call;
   if (cut_k) {
 #pragma unroll
@@ -377,7 +380,8 @@ __device__ SampleRow plan_row(const SampleArgs& a, uint64_t r, uint32_t* c_befor
   SampleRow v;
   v.cut = cut_k || cut_p;
   const uint32_t last = bk < BINS ? max(hi, bk) : hi;
-  const bool few = v.cut && c_before[min(last, BINS - 1) + 1] <= CAP;   // few entries: all that can stay
+  const bool few = v.cut && k > 0 && c_before[min(last, BINS - 1) + 1] <= PAIRS;   // few entries: all that can stay
+  v.inside = few;
   v.lo = few ? 0 : lo;
   v.hi = few ? last : hi;
   v.bk = bk;
@@ -406,13 +410,15 @@ __global__ __launch_bounds__(ROW_THREADS) void k_sample_bins(SampleArgs a) {
   tile.load(row, i0, i1);
   for (uint32_t i = threadIdx.x; i < BINS; i += ROW_THREADS) sum[i] = count[i] = 0;
   const float m = row_max(a, r);
+  const bool counted = (a.top_ks ? a.top_ks[r] : a.top_k) > 0 || s.greedy;
+  __syncthreads();
   for (uint32_t at = i0;;) {
 #pragma unroll
     for (uint32_t j = 0; j < tile.PER; ++j) {
       const float z = tile.z[j];
       if (!live(z, m)) continue;
       const uint32_t b = bin_of(z, m);
-      atomicAdd(&count[b], 1u);
+      if (counted) atomicAdd(&count[b], 1u);
       const uint64_t w = fixed_of(weight_of(z, m, s), a.bits);
       if (w) atomicAdd(reinterpret_cast<unsigned long long*>(&sum[b]), (unsigned long long)w);
     }
@@ -422,24 +428,23 @@ __global__ __launch_bounds__(ROW_THREADS) void k_sample_bins(SampleArgs a) {
   }
   __syncthreads();
   for (uint32_t i = threadIdx.x; i < BINS; i += ROW_THREADS) {
-    if (!count[i]) continue;
-    atomicAdd(&a.bin_count[r * BINS + i], count[i]);
+    if (count[i]) atomicAdd(&a.bin_count[r * BINS + i], count[i]);
     if (sum[i]) atomicAdd(reinterpret_cast<unsigned long long*>(&a.bin_sum[r * BINS + i]), (unsigned long long)sum[i]);
   }
 }
 
 // Of a row without a cut, every bin is before it.  CUT: some row has one.
 //
-// Without CUT the logits whose weight counts are listed first and then looked at
-// by consecutive threads: with a min_p few do, and a weight takes a wave the
-// same time for one of them as for 64.
+// The logits that surely stay and whose weight counts are listed first and then
+// looked at by consecutive threads: few do, and a weight takes a wave the same
+// time for one of them as for 64.
 template <class T, bool CUT>
 __global__ __launch_bounds__(ROW_THREADS) void k_sample_collect(SampleArgs a) {
   __shared__ uint64_t code[CUT ? TILE : 1];            // the plan's sums, then the entries to be handed on
   __shared__ uint32_t counts[CUT ? BINS + 1 : 1];
-  __shared__ float listed[CUT ? 1 : TILE];
+  __shared__ float listed[TILE];
   static_assert(TILE > BINS, "the plan's sums fit");
-  __shared__ uint32_t part32[ROW_WAVES], mark[3], taken, base;
+  __shared__ uint32_t part32[ROW_WAVES], mark[3], taken, sures, base;
   __shared__ uint64_t part64[ROW_WAVES];
   const uint64_t id = block_id();
   if (id >= a.work) return;
@@ -452,7 +457,7 @@ __global__ __launch_bounds__(ROW_THREADS) void k_sample_collect(SampleArgs a) {
   Tile<T, ROW_THREADS> tile;
   tile.load(row, i0, i1);
   const float m = row_max(a, r);
-  if (threadIdx.x == 0) taken = 0;
+  if (threadIdx.x == 0) taken = sures = 0;
   SampleRow v;
   v.cut = 0;
   v.lo = v.hi = v.bk = BINS;
@@ -460,45 +465,38 @@ __global__ __launch_bounds__(ROW_THREADS) void k_sample_collect(SampleArgs a) {
     v = plan_row(a, r, counts, code, part32, part64, mark);
     if (c == 0 && threadIdx.x == 0) a.row[r] = v;
   }
+  const float near = v.lo ? bin_end(v.lo - 1) : 0.f;   // logits nearer to the maximum than this lie in bins before lo
   const double min_p = min_p_of(a, r);
   uint64_t sum = 0;
-  if constexpr (!CUT) __syncthreads();
+  __syncthreads();
   for (uint32_t at = i0;;) {
 #pragma unroll
     for (uint32_t j = 0; j < tile.PER; ++j) {
       const float z = tile.z[j];
-      const uint32_t b = v.cut && live(z, m) ? bin_of(z, m) : 0u;
-      const bool sure = !(m - z > s.far) && z > -INFINITY && (!v.cut || b < v.lo);
-      if constexpr (!CUT) {
-        if (sure) listed[atomicAdd(&taken, 1u)] = z;
-      } else {
-        if (__any(sure)) {
-          const double w = weight_of(z, m, s);
-          if (sure && w >= min_p) sum += fixed_of(w, a.bits);
+      bool sure = !(m - z > s.far) && z > -INFINITY;
+      if constexpr (CUT) sure = sure && (!v.cut || (z == m ? v.lo > 0 : m - z < near));
+      if (sure) listed[atomicAdd(&sures, 1u)] = z;
+      if constexpr (CUT)
+        if (v.cut && live(z, m)) {
+          const uint32_t b = bin_of(z, m);
+          if (b >= v.lo && (b <= v.hi || b == v.bk)) code[atomicAdd(&taken, 1u)] = code_of(z, tile.index(at, j));
         }
-        if (v.cut && live(z, m) && b >= v.lo && (b <= v.hi || b == v.bk)) code[atomicAdd(&taken, 1u)] = code_of(z, tile.index(at, j));
-      }
     }
-    if constexpr (!CUT) {
-      __syncthreads();
-      const uint32_t n = taken;
-      for (uint32_t i = threadIdx.x; i < n; i += ROW_THREADS) {
-        const double w = weight_of(listed[i], m, s);
-        if (w >= min_p) sum += fixed_of(w, a.bits);
-      }
-      __syncthreads();
-      if (threadIdx.x == 0) taken = 0;
-      __syncthreads();
-    } else if (v.cut) {
-      __syncthreads();
+    __syncthreads();
+    const uint32_t n = sures;
+    for (uint32_t i = threadIdx.x; i < n; i += ROW_THREADS) {
+      const double w = weight_of(listed[i], m, s);
+      if (w >= min_p) sum += fixed_of(w, a.bits);
+    }
+    if (CUT && v.cut) {
       if (threadIdx.x == 0 && taken) base = atomicAdd(&a.collected[r], taken);
       __syncthreads();
       for (uint32_t i = threadIdx.x; i < taken; i += ROW_THREADS)
         if (base + i < CAP) a.cand[r * CAP + base + i] = code[i];
-      __syncthreads();
-      if (threadIdx.x == 0) taken = 0;
-      __syncthreads();
     }
+    __syncthreads();
+    if (threadIdx.x == 0) taken = sures = 0;
+    __syncthreads();
     at += TILE;
     if (at >= i1) break;
     tile.load(row, at, i1);
@@ -925,7 +923,7 @@ __device__ void finish_small(const SampleArgs& a, uint64_t r, const T* row, floa
   }
   __syncthreads();
   SampleRow w;
-  w.cut = 1;
+  w.cut = w.inside = 1;
   w.lo = w.count = w.count_k = 0;
   w.hi = w.bk = BINS - 1;      // the list is a beginning of the row's order
   w.before = w.before_k = 0;
@@ -962,7 +960,7 @@ __global__ __launch_bounds__(ROW_THREADS) void k_sample_finish(SampleArgs a) {
     for (uint32_t i = threadIdx.x; i < min(n, CAP); i += ROW_THREADS) l.code[i] = a.cand[r * CAP + i];
     __syncthreads();
   }
-  finish_row(a, r, row, m, s, v, n, v.cut && v.lo == 0, l);
+  finish_row(a, r, row, m, s, v, n, v.cut && v.inside, l);
 }
 
 struct SamplePlan {
@@ -980,7 +978,7 @@ SamplePlan sample_plan(const topk_sample_args& a) {
   p.chunks = (uint32_t)ceil_div(a.n, p.chunk);
   while ((int64_t(1) << (62 - p.bits)) < a.n) --p.bits;
   // what the numbers among the settings say of all rows
-  const bool tile = p.chunk == TILE, brief = a.n <= (int64_t)CAP;
+  const bool tile = p.chunk == TILE, brief = a.n <= (int64_t)PAIRS;
   const bool greedy = !a.temperatures && !(a.temperature > 0.f);
   const bool nucleus = !a.top_ps && !(a.top_p >= 1.f);
   p.all_small = tile && (greedy || (!a.top_ks && a.top_k > 0 && a.top_k <= small_limit(a.n)) || (brief && nucleus));
