@@ -21,13 +21,13 @@
 //                     entries lie in the bins up to it, and in such groups
 //   k_sample_bins     other rows with a cut: counts and sums of weights by bins
 //                     of m - z (its float's leading bits: 128 bins to an octave)
-//   k_sample_collect  from those the bins that the cut can lie in, their
-//                     entries, and each chunk's sum over the bins before
+//   k_sample_plan     from those the bins that the cut can lie in
+//   k_sample_collect  their entries, and each chunk's sum over the bins before
 //   k_sample_finish   the entries sorted, the cut, the chunk that the token
 //                     lies in, the token
 //
-// Calls without a cut do without the second, those whose top_k is small in all
-// rows without the middle two.  (A row's last workgroup doing the next step
+// Calls without a cut do without the second and third, those whose top_k is small
+// in all rows without the middle three.  (A row's last workgroup doing the next step
 // saves a launch, but the fence that this takes in every workgroup writes its
 // cache back: 790 us for 256 rows of 65536, against 30.)
 //
@@ -210,6 +210,15 @@ __device__ __forceinline__ uint64_t limit_of(float p, uint64_t w) {
   return c ? c : 1;
 }
 
+// *to, shared and no less than 0, becomes the most of all threads' x.  One lane of
+// a wave takes part for all: as atomics of whole waves, one for each of a thread's
+// bins, this took two thirds of k_sample_plan (16.5 us, now 5.2).
+__device__ __forceinline__ void raise_to(uint32_t* to, uint32_t x) {
+#pragma unroll
+  for (uint32_t d = 32; d; d /= 2) x = max(x, (uint32_t)__shfl_xor((int)x, d));
+  if (threadIdx.x % 64 == 0 && x) atomicMax(to, x);
+}
+
 __device__ __forceinline__ float row_max(const SampleArgs& a, uint64_t r) {
   float m = -INFINITY;
   for (uint32_t i = threadIdx.x % 64; i < a.chunks; i += 64) m = fmaxf(m, a.maxima[r * a.chunks + i]);
@@ -320,10 +329,15 @@ __global__ __launch_bounds__(FIRST_THREADS) void k_sample_first(SampleArgs a) {
   }
 }
 
-// From a row's bins: where its cut can lie.  Every workgroup of the row finds it
-// for itself; all threads get it.
-__device__ SampleRow plan_row(const SampleArgs& a, uint64_t r, uint32_t* c_before, uint64_t* w_before, uint32_t* part32, uint64_t* part64,
-                         uint32_t* mark) {
+// A workgroup for each row.  (Found by every chunk's workgroup for itself, it
+// took most of k_sample_collect: 153 rows of 78201 109 us.)
+__global__ __launch_bounds__(ROW_THREADS) void k_sample_plan(SampleArgs a) {
+  __shared__ uint64_t w_before[BINS + 1];
+  __shared__ uint32_t c_before[BINS + 1];
+  __shared__ uint32_t part32[ROW_WAVES], mark[3];
+  __shared__ uint64_t part64[ROW_WAVES];
+  const uint64_t r = block_id();
+  if (r >= a.work || small_k(a, r)) return;
   constexpr uint32_t PER = BINS / ROW_THREADS;
   const uint32_t t = threadIdx.x;
   uint32_t c[PER], call;
@@ -367,12 +381,14 @@ __device__ SampleRow plan_row(const SampleArgs& a, uint64_t r, uint32_t* c_befor
     // the last bin with an entry whose preceding weight is below the limit, for
     // the least and the most weight that top_k can leave
     const uint64_t l0 = limit_of(p, bk < BINS ? w_before[bk] : wall), l1 = limit_of(p, bk < BINS ? w_before[bk + 1] : wall);
+    uint32_t x = 0, y = 0;
 #pragma unroll
     for (uint32_t i = 0; i < PER; ++i) {
-      if (!c[i]) continue;
-      if (w_before[t * PER + i] < l0) atomicMax(&lo, t * PER + i);
-      if (w_before[t * PER + i] < l1) atomicMax(&hi, t * PER + i);
+      if (c[i] && w_before[t * PER + i] < l0) x = t * PER + i;
+      if (c[i] && w_before[t * PER + i] < l1) y = t * PER + i;
     }
+    raise_to(&lo, x);
+    raise_to(&hi, y);
   } else if (t == 0) {
     lo = hi = bk;
   }
@@ -390,8 +406,7 @@ __device__ SampleRow plan_row(const SampleArgs& a, uint64_t r, uint32_t* c_befor
   v.before_k = bk < BINS ? w_before[bk] : wall;
   v.count_k = bk < BINS ? c_before[bk] : call;
   v.k = cut_k ? (uint32_t)k : 0u;
-  __syncthreads();   // what is shared may be used anew
-  return v;
+  if (t == 0) a.row[r] = v;
 }
 
 template <class T>
@@ -440,11 +455,9 @@ __global__ __launch_bounds__(ROW_THREADS) void k_sample_bins(SampleArgs a) {
 // time for one of them as for 64.
 template <class T, bool CUT>
 __global__ __launch_bounds__(ROW_THREADS) void k_sample_collect(SampleArgs a) {
-  __shared__ uint64_t code[CUT ? TILE : 1];            // the plan's sums, then the entries to be handed on
-  __shared__ uint32_t counts[CUT ? BINS + 1 : 1];
+  __shared__ uint64_t code[CUT ? TILE : 1];   // entries to be handed on
   __shared__ float listed[TILE];
-  static_assert(TILE > BINS, "the plan's sums fit");
-  __shared__ uint32_t part32[ROW_WAVES], mark[3], taken, sures, base;
+  __shared__ uint32_t part32[ROW_WAVES], base;
   __shared__ uint64_t part64[ROW_WAVES];
   const uint64_t id = block_id();
   if (id >= a.work) return;
@@ -457,49 +470,49 @@ __global__ __launch_bounds__(ROW_THREADS) void k_sample_collect(SampleArgs a) {
   Tile<T, ROW_THREADS> tile;
   tile.load(row, i0, i1);
   const float m = row_max(a, r);
-  if (threadIdx.x == 0) taken = sures = 0;
   SampleRow v;
   v.cut = 0;
   v.lo = v.hi = v.bk = BINS;
-  if constexpr (CUT) {
-    v = plan_row(a, r, counts, code, part32, part64, mark);
-    if (c == 0 && threadIdx.x == 0) a.row[r] = v;
-  }
+  if constexpr (CUT) v = a.row[r];
   const float near = v.lo ? bin_end(v.lo - 1) : 0.f;   // logits nearer to the maximum than this lie in bins before lo
   const double min_p = min_p_of(a, r);
   uint64_t sum = 0;
-  __syncthreads();
   for (uint32_t at = i0;;) {
+    uint32_t sure = 0, cand = 0, all;   // a bit for each of this thread's logits
 #pragma unroll
     for (uint32_t j = 0; j < tile.PER; ++j) {
       const float z = tile.z[j];
-      bool sure = !(m - z > s.far) && z > -INFINITY;
-      if constexpr (CUT) sure = sure && (!v.cut || (z == m ? v.lo > 0 : m - z < near));
-      if (sure) listed[atomicAdd(&sures, 1u)] = z;
-      if constexpr (CUT)
-        if (v.cut && live(z, m)) {
-          const uint32_t b = bin_of(z, m);
-          if (b >= v.lo && (b <= v.hi || b == v.bk)) code[atomicAdd(&taken, 1u)] = code_of(z, tile.index(at, j));
-        }
+      bool in = !(m - z > s.far) && z > -INFINITY;
+      if constexpr (CUT) in = in && (!v.cut || (z == m ? v.lo > 0 : m - z < near));
+      sure |= in ? 1u << j : 0u;
+      if constexpr (CUT) {
+        const uint32_t b = bin_of(z, m);
+        cand |= v.cut && live(z, m) && b >= v.lo && (b <= v.hi || b == v.bk) ? 1u << j : 0u;
+      }
     }
+    // places of both, in the halves of one sum (a tile has 4096)
+    const uint32_t place = thread_scan<ROW_THREADS>((uint32_t)__popc(sure) | (uint32_t)__popc(cand) << 16, part32, &all);
+    uint32_t to = place & 0xFFFF, hand = place >> 16;
+#pragma unroll
+    for (uint32_t j = 0; j < tile.PER; ++j) {
+      if (sure >> j & 1) listed[to++] = tile.z[j];
+      if constexpr (CUT)
+        if (cand >> j & 1) code[hand++] = code_of(tile.z[j], tile.index(at, j));
+    }
+    const uint32_t sures = all & 0xFFFF, cands = all >> 16;
+    if (CUT && cands && threadIdx.x == 0) base = atomicAdd(&a.collected[r], cands);
     __syncthreads();
-    const uint32_t n = sures;
-    for (uint32_t i = threadIdx.x; i < n; i += ROW_THREADS) {
+    for (uint32_t i = threadIdx.x; i < sures; i += ROW_THREADS) {
       const double w = weight_of(listed[i], m, s);
       if (w >= min_p) sum += fixed_of(w, a.bits);
     }
-    if (CUT && v.cut) {
-      if (threadIdx.x == 0 && taken) base = atomicAdd(&a.collected[r], taken);
-      __syncthreads();
-      for (uint32_t i = threadIdx.x; i < taken; i += ROW_THREADS)
+    if constexpr (CUT)
+      for (uint32_t i = threadIdx.x; i < cands; i += ROW_THREADS)
         if (base + i < CAP) a.cand[r * CAP + base + i] = code[i];
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) taken = sures = 0;
-    __syncthreads();
     at += TILE;
     if (at >= i1) break;
     tile.load(row, at, i1);
+    __syncthreads();
   }
   sum = wave_total(sum);
   if (threadIdx.x % 64 == 0) part64[threadIdx.x / 64] = sum;
@@ -743,12 +756,14 @@ __device__ void finish_row(const SampleArgs& a, uint64_t r, const T* row, float 
       const uint64_t sum_k = v.bk < BINS ? v.before_k + (l.found[1] - bk_start) : v.before_k;
       const uint64_t limit = limit_of(p, sum_k);
       run = at;
+      uint32_t last = 0;
       for (uint32_t x = x0; x < x1; ++x) {
         const uint64_t before = apart && x >= lows ? v.before_k + (run - bk_start) : v.before + run;
         const bool in_k = v.bk >= BINS || x < k_at;
-        if (in_k && before < limit) atomicMax(&l.pick, x);
+        if (in_k && before < limit) last = x;
         run += fixed_of(weight_of(logit_of_code(l.code[x]), m, s), a.bits);
       }
+      raise_to(&l.pick, last);
       __syncthreads();
       staying_cands = l.pick + 1;
       cut = l.code[l.pick];
@@ -1012,11 +1027,16 @@ hipError_t sample_call(SampleArgs a, const SamplePlan& p, uint64_t rows, hipStre
   a.work = rows * p.chunks;
   const dim3 chunks = wide_grid(a.work);
   k_sample_first<T><<<chunks, FIRST_THREADS, 0, s>>>(a);
-  if (p.cut) k_sample_bins<T><<<chunks, ROW_THREADS, 0, s>>>(a);
-  if (p.cut) k_sample_collect<T, true><<<chunks, ROW_THREADS, 0, s>>>(a);
-  else if (!p.all_small) k_sample_collect<T, false><<<chunks, ROW_THREADS, 0, s>>>(a);
-  a.work = rows;
-  k_sample_finish<T><<<wide_grid(rows), ROW_THREADS, 0, s>>>(a);
+  SampleArgs by_row = a;
+  by_row.work = rows;
+  if (p.cut) {
+    k_sample_bins<T><<<chunks, ROW_THREADS, 0, s>>>(a);
+    k_sample_plan<<<wide_grid(rows), ROW_THREADS, 0, s>>>(by_row);
+    k_sample_collect<T, true><<<chunks, ROW_THREADS, 0, s>>>(a);
+  } else if (!p.all_small) {
+    k_sample_collect<T, false><<<chunks, ROW_THREADS, 0, s>>>(a);
+  }
+  k_sample_finish<T><<<wide_grid(rows), ROW_THREADS, 0, s>>>(by_row);
   return hipGetLastError();
 }
 
