@@ -32,10 +32,12 @@
 // cache back: 790 us for 256 rows of 65536, against 30.)
 //
 // One row of 131072 f32 with top_k 50 and top_p takes 3 + 9 us, each a chain of
-// dependent steps; 64 rows of 100003 bf16 with settings of their own 25 (6 the
-// first pass, 15 the last); 256 rows of 65536 f32 (67 MB) with min_p 32: 11.8 for
-// the maxima, 5.7 TB/s, 14.5 for the sums, which reads the logits once more, and
-// 6.8.
+// dependent steps; 64 rows of 100003 bf16 with settings of their own 27 (6 the
+// first pass, 15 the last, 2 to 3 each of the three that find nothing to do); 256
+// rows of 65536 f32 (67 MB) with min_p 33: 11.8 for the maxima, 5.7 TB/s, 15 for
+// the sums, which reads the logits once more, and 6.7.  153 rows of 78201 bf16
+// with top_p alone 95: 7, 30 for the bins, bound by their atomics in LDS, 5, 30
+// and 24.
 #include <algorithm>
 
 #include "topk_model.hpp"
