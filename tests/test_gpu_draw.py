@@ -194,6 +194,18 @@ def test_extreme_settings():
     assert tss().sample(z, u, min_p=nan)[0].tolist() == [-1] * 4
 
 
+def test_settings_are_float32():
+    # a number counts as the float32 next to it, also for what the call's scratch memory is sized by
+    z = rnd(13, 3, 1501, scale=2.0)
+    u = uni(14, 3)
+    check(z, u, "as 1", top_p=1 - 1e-12)
+    check(z, u, "below 1", top_p=0.8)
+    check(z, u, "as 0", temperature=1e-50)
+    check(z, u, "above 0", temperature=0.9)
+    check(z, u, "as inf", temperature=1e39)
+    check(z, u, "as 0, of everything", min_p=1e-60)
+
+
 def test_distribution():
     # the shares of 2^16 evenly spaced numbers are the probabilities, to one of them
     z = torch.tensor([[0.5, -1.0, 2.0, 0.0, 1.0, -3.0]], device="cuda")

@@ -294,7 +294,7 @@ def attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lengths: torch.Ten
         if n > 1 and scores.stride(2) != 1:
             raise ValueError("scores: the last axis contiguous")
         sb, sh, _ = scores.stride()
-    scale = d ** -0.5 if scale is None else float(scale)
+    scale = d ** -0.5 if scale is None else ctypes.c_float(float(scale)).value
     if not math.isfinite(scale):
         raise ValueError("scale: a finite number")
     if q.stride(2) != 1 and d > 1:
@@ -381,7 +381,7 @@ def _setting(value, what, rows, like, lo, hi):
     if isinstance(value, torch.Tensor):
         _check(value, what, like, (rows,), torch.float32)
         return 0.0, value.contiguous()
-    value = float(value)
+    value = ctypes.c_float(float(value)).value   # as the library takes it
     if not lo <= value <= hi:
         raise ValueError(f"{what}: a number from {lo} to {hi}, or a float32 tensor of one for each row")
     return value, None
