@@ -433,29 +433,48 @@ __global__ __launch_bounds__(MAP_PLACES) void k_owner_map(const int64_t* __restr
   if (p0 + threadIdx.x < n) owner[p0 + threadIdx.x] = own[threadIdx.x];
 }
 
-// One column of the sum over a chain.  Its order is not the same from call to
+// VEC columns of the sum over a chain.  Its order is not the same from call to
 // call, so the terms are added as whole multiples of a power of two that 62 bits
-// hold (the largest term tells which): such a sum has no order.  Where a term is
-// not finite, neither is the sum, in any order.  (A column at a time: chains are
-// rare, and registers are what the others run on.)
-template <class T, class W>
-__device__ __forceinline__ float chain_sum(const T* column, const W* weights, const uint32_t* next, uint64_t ldg, uint32_t k, uint32_t e) {
-  float top = 0.f;
-  double plain = 0.0;
+// hold (a column's largest term tells which): such a sum has no order.  Where a
+// term is not finite, neither is the sum, in any order.  A chain is two walks, each
+// bound by the latency of its links: 8192 x 8 entries of 1024 bf16 at random places
+// among 65536 take 127 us (distinct ones 61), among 512 376, among 64 1890.
+template <class T, class W, int VEC>
+__device__ __forceinline__ void chain_sum(const T* column, const W* weights, const uint32_t* next, uint64_t ldg, uint32_t k, uint32_t e,
+                                          float* out) {
+  float top[VEC], bad[VEC], v[VEC];
   uint32_t count = 0;
+#pragma unroll
+  for (int q = 0; q < VEC; ++q) top[q] = bad[q] = 0.f;
+#pragma unroll 1
   for (uint32_t j = e; j != NONE; j = next[j], ++count) {
-    const float t = weight_of(weights, j) * to_f32(column[(uint64_t)(j / k) * ldg]);
-    top = fmaxf(top, fabsf(t));
-    plain += t;
+    const float w = weight_of(weights, j);
+    load_vec<T, VEC>(column + (uint64_t)(j / k) * ldg, v);
+#pragma unroll
+    for (int q = 0; q < VEC; ++q) {
+      const float t = w * v[q];
+      top[q] = fmaxf(top[q], fabsf(t));
+      if (!(fabsf(t) < INFINITY)) bad[q] += t;
+    }
   }
-  if (!(fabs(plain) < INFINITY)) return (float)plain;
-  int exponent = 0;
-  frexpf(top, &exponent);   // top < 2^exponent
-  const int shift = 62 - (32 - __builtin_clz(count)) - exponent;
-  int64_t sum = 0;
-  for (uint32_t j = e; j != NONE; j = next[j])
-    sum += (int64_t)rint(ldexp((double)(weight_of(weights, j) * to_f32(column[(uint64_t)(j / k) * ldg])), shift));
-  return (float)ldexp((double)sum, -shift);
+  const int bits = 62 - (32 - __builtin_clz(count));
+  int64_t sum[VEC];
+#pragma unroll
+  for (int q = 0; q < VEC; ++q) {
+    int exponent = 0;
+    frexpf(top[q], &exponent);   // top < 2^exponent
+    top[q] = (float)(bits - exponent);
+    sum[q] = 0;
+  }
+#pragma unroll 1
+  for (uint32_t j = e; j != NONE; j = next[j]) {
+    const float w = weight_of(weights, j);
+    load_vec<T, VEC>(column + (uint64_t)(j / k) * ldg, v);
+#pragma unroll
+    for (int q = 0; q < VEC; ++q) sum[q] += (int64_t)rint(ldexp((double)(w * v[q]), (int)top[q]));
+  }
+#pragma unroll
+  for (int q = 0; q < VEC; ++q) out[q] = bad[q] != 0.f ? bad[q] : (float)ldexp((double)sum[q], -(int)top[q]);
 }
 
 // Items below `total`: the entries, a wave each: dw_e, and dy's row if the entry
@@ -523,11 +542,7 @@ __global__ __launch_bounds__(MOVE_THREADS) void k_combine_grad(
           if (at + q >= c) dot = fmaf(a[x][q], b[x][q], dot);   // a row's last vector counts its new columns only
       }
       if (!mine) continue;
-      if (chain) {
-#pragma unroll 1
-        for (uint32_t q = 0; q < VEC; ++q) dyrow[at + q] = from_f32<T>(chain_sum<T, W>(g + at + q, weights, next, ldg, k, e));
-        continue;
-      }
+      if (chain) continue;
 #pragma unroll
       for (int q = 0; q < VEC; ++q) a[x][q] *= w;
       put(dyrow + at, a[x]);
@@ -536,6 +551,14 @@ __global__ __launch_bounds__(MOVE_THREADS) void k_combine_grad(
   if (dw) {
     dot = wave_sum(dot);
     if (lane == 0) dw[e] = from_f32<W>(dot);
+  }
+  if (!chain) return;
+#pragma unroll 1
+  for (uint32_t c = lane * VEC; c < d; c += 64 * VEC) {
+    const uint32_t at = column_of<VEC>(c, d);
+    float sum[VEC];
+    chain_sum<T, W, VEC>(g + at, weights, next, ldg, k, e, sum);
+    put(dyrow + at, sum);
   }
 }
 
