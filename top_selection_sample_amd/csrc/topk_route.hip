@@ -438,7 +438,7 @@ __global__ __launch_bounds__(MAP_PLACES) void k_owner_map(const int64_t* __restr
 // hold (a column's largest term tells which): such a sum has no order.  Where a
 // term is not finite, neither is the sum, in any order.  A chain is two walks, each
 // bound by the latency of its links: 8192 x 8 entries of 1024 bf16 at random places
-// among 65536 take 127 us (distinct ones 61), among 512 376, among 64 1890.
+// among 65536 take 118 us (distinct ones 61), among 512 413, among 64 2240.
 template <class T, class W, int VEC>
 __device__ __forceinline__ void chain_sum(const T* column, const W* weights, const uint32_t* next, uint64_t ldg, uint32_t k, uint32_t e,
                                           float* out) {
@@ -482,9 +482,11 @@ __device__ __forceinline__ void chain_sum(const T* column, const W* weights, con
 // 64 rows of y each, of which the ones that no entry names are set to zero.
 // STREAM: y is read, and dy stored, past the caches.  (Two, four and eight
 // entries to a wave, their places looked up side by side, are slower: 8192 x 8
-// entries of 1024 bf16 take 65, 71 and 82 us against 62.)
+// entries of 1024 bf16 take 65, 71 and 82 us against 62.  The chains' sums would
+// take 70 registers, and 62.0 us instead of 61.3: eight waves to a SIMD are asked
+// for, which 51 without a spill allow.)
 template <class T, class W, int VEC, bool STREAM>
-__global__ __launch_bounds__(MOVE_THREADS) void k_combine_grad(
+__global__ __launch_bounds__(MOVE_THREADS) __attribute__((amdgpu_waves_per_eu(8))) void k_combine_grad(
     const T* __restrict__ g, const T* __restrict__ y, const int64_t* __restrict__ places, const W* __restrict__ weights,
     const uint32_t* __restrict__ owner, const uint32_t* __restrict__ next, T* __restrict__ dy, W* __restrict__ dw, uint64_t ldg,
     uint64_t ldy, uint64_t lddy, uint64_t n, uint32_t total, uint32_t k, uint32_t d, uint64_t items) {
