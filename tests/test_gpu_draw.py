@@ -122,6 +122,18 @@ def test_equal_logits(dt):
         check(z, uni(3, 4), kw, **kw)
 
 
+@pytest.mark.parametrize("n", [65535, 65536, 65537, 131072])
+def test_equal_logits_by_index(n):
+    # of equal logits the lowest indices stay: the last of them is the largest number's token
+    z = torch.zeros(1, n, device="cuda")
+    u = torch.tensor([LAST], device="cuda")
+    for k in (5000, 32768, n - 1, n):
+        assert int(tss().sample(z, u, top_k=k)[0]) == k - 1, k
+    for p in (0.25, 0.5, 0.75):
+        assert int(tss().sample(z, u, top_p=p)[0]) == math.ceil(p * n) - 1, p
+    assert int(tss().sample(z, u, top_k=40000, top_p=0.5)[0]) == 19999
+
+
 def test_cut_in_two_places():
     # the k-th and the nucleus' end are many bins apart, with too many entries between to sort them all
     z = rnd(1, 3, 60000, scale=1.0)

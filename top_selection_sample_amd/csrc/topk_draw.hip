@@ -535,6 +535,10 @@ __device__ uint64_t select_code(const SampleArgs& a, const T* row, float m, cons
   uint64_t prefix = 0, base = 0;
   const uint32_t t = threadIdx.x;
   for (int shift = 56; shift >= 0; shift -= 8) {
+    if (shift == 24 || (shift == 16 && a.n <= 1u << 16)) {   // a digit that all indices have: n is at most 2^24
+      prefix |= uint64_t(255) << shift;
+      continue;
+    }
     if (t < 256) hist[t] = 0;
     __syncthreads();
     for (uint32_t i = t; i < a.n; i += ROW_THREADS) {
