@@ -8,10 +8,10 @@
 // 8, 128 wide bf16 (537 MB) take 86 us without the scores, 6.2 TB/s, and 112
 // with them: the logits go through memory once, for a probability is known only
 // when the whole row is (17 MB written and read).  Lengths spread evenly up to
-// 8192 take 60 to 72, with the lengths drawn: 45 to 60 the first launch, 7.5 the second.  One sequence of 4099, 12
-// heads on 4, 80 wide f32: 8.3 + 6 us, latency.  Eviction of 16 x 8 heads of
-// 16384 down to 4096, 128 wide bf16 (549 MB): 18 us to choose, 93 to copy, 5.9
-// TB/s.
+// 8192 take 60 to 72, with the lengths drawn: 45 to 60 the first launch, 7.5 the
+// second.  One sequence of 4099, 12 heads on 4, 80 wide f32: 8.3 + 6 us, latency.
+// Eviction of 16 x 8 heads of 16384 down to 4096, 128 wide bf16 (549 MB): 18 us
+// to choose, 93 to copy, 5.9 TB/s.
 #include <algorithm>
 
 #include "topk_model.hpp"
