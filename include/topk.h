@@ -541,9 +541,10 @@ int topk_combine_grad(const topk_combine_grad_args* args, void* workspace, size_
  * sequence's entries j of scale * <q, k_j>:
  *   out = sum of p_j v_j;  scores[j] += sum of p_j over the heads that share
  *   the key-value head.
- * A sequence of length 0 has an output of 0 and adds nothing.  In bf16 the
- * probabilities are rounded to bf16 for the product with v (its matrix
- * operand); the sums of p and the scores take them unrounded. */
+ * A sequence of length 0 has an output of 0 and adds nothing.  In bf16 a
+ * probability's product with v is of two bf16 numbers that add up to it but
+ * for 2^-14 of it (the matrix operands); the sums of p and the scores take it
+ * as it is. */
 typedef struct {
   const void* q;             /* [batch, heads, d], strides sqb, sqh */
   const void* k;             /* [batch, kv_heads, n, d], strides skb, skh, skn */

@@ -361,9 +361,24 @@ __global__ __launch_bounds__(ATT_THREADS, KC * VB > 8 ? 1 : 2) void k_attend(Att
         l += p[i];
       }
       if constexpr (sizeof(T) == 2) {
-        const u32x4 pk = Vec<bf16_t>::pack(p);
-        bf16x8 pf;
-        __builtin_memcpy(&pf, &pk, 16);
+        // A probability is the sum of two operands: its leading bits, less half a
+        // step, and the rest, rounded to bf16.  The rest is between half a step and
+        // one and a half, so 1.5 * 2^-15 of the probability is lost at most, and both
+        // have its sign: an infinite value stays infinite.
+        u32x4 near;
+        float rest[KEYS];
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) {
+          const uint32_t lo = __builtin_elementwise_sub_sat(__float_as_uint(p[2 * i]), 0x8000u);
+          const uint32_t hi = __builtin_elementwise_sub_sat(__float_as_uint(p[2 * i + 1]), 0x8000u);
+          near[i] = __builtin_amdgcn_perm(hi, lo, 0x07060302u);
+          rest[2 * i] = p[2 * i] - __uint_as_float(lo & 0xFFFF0000u);
+          rest[2 * i + 1] = p[2 * i + 1] - __uint_as_float(hi & 0xFFFF0000u);
+        }
+        const u32x4 far = Vec<bf16_t>::pack(rest);
+        bf16x8 pn, pr;
+        __builtin_memcpy(&pn, &near, 16);
+        __builtin_memcpy(&pr, &far, 16);
 #pragma unroll
         for (uint32_t x = 0; x < VB; ++x)
 #pragma unroll
@@ -378,7 +393,8 @@ __global__ __launch_bounds__(ATT_THREADS, KC * VB > 8 ? 1 : 2) void k_attend(Att
             }
             bf16x8 vf;
             __builtin_memcpy(&vf, &w, 16);
-            o[x][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf, vf, o[x][j], 0, 0, 0);
+            o[x][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pr, vf, o[x][j], 0, 0, 0);
+            o[x][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pn, vf, o[x][j], 0, 0, 0);
           }
       } else {
 #pragma unroll
