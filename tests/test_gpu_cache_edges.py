@@ -86,3 +86,22 @@ def test_infinite_values_stay_infinite(dt):
     out = tss().attend(q, k, v, scale=1.0)[0]
     assert bool((out[:, 0] == math.inf).all()) and bool((out[:, 1] == -math.inf).all())
     assert bool(torch.isfinite(out[:, 2]).all()) and bool(torch.isnan(out[:, 3]).all())
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [1, 3, 7, 8, 9, 15, 17, 20, 31, 33, 40, 50, 63, 65, 75, 80, 95, 97, 100, 127, 129, 130, 150, 161, 191, 193, 200, 225, 255, 256])
+def test_keys_of_minus_infinity(d, dt):
+    # whichever column is infinite, the entry has no probability and all others keep theirs
+    for n in (40, 700):
+        q, k, v = rnd(d, 1, 3, d, dt=dt).abs() + 0.25, rnd(d + 1, 1, 1, n, d, dt=dt, scale=0.5), rnd(d + 2, 1, 1, n, d, dt=dt)
+        cols = sorted({0, d - 1, max(0, d - 2), max(0, d - 3), max(0, d - 4), max(0, d - 5), max(0, d - 8), max(0, d - 9), d // 2, d // 3})
+        bad = [(7 * i + 3) % n for i in range(len(cols))]
+        for c, j in zip(cols, bad):
+            k[0, 0, j, c] = -math.inf
+        good = [j for j in range(n) if j not in bad]
+        out, eo, add, ea = M.attend64(q, k[:, :, good], v[:, :, good], None, None, q.dtype)
+        scores = torch.full((1, 1, n), 0.25, device="cuda")
+        U.within(tss().attend(q, k, v, scores=scores).cpu(), out, eo, (n, "out"))
+        U.within(tss().attend(q, k, v).cpu(), out, eo, (n, "out alone"))
+        U.within(scores[:, :, good].cpu(), 0.25 + add, ea, (n, "scores"))
+        assert bool((scores[0, 0, bad] == 0.25).all())

@@ -70,6 +70,13 @@ struct AttArgs {
   float scale2;
 };
 
+// Word i of a vector without the vector's first `seen` elements.
+template <class T>
+__device__ __forceinline__ uint32_t unseen(uint32_t word, uint32_t i, uint32_t seen) {
+  if constexpr (sizeof(T) == 4) return i < seen ? 0u : word;
+  return 2 * i >= seen ? word : 2 * i + 1 == seen ? word & 0xFFFF0000u : 0u;
+}
+
 template <class T> struct Att;
 template <> struct Att<bf16_t> {
   static constexpr uint32_t STEP = 32, KVEC = 8, KCHUNK = 32;
@@ -179,12 +186,13 @@ __device__ __forceinline__ bool place_of(const AttArgs& a, uint64_t w, Place* p)
   }
 }
 
-// KC: chunks of a key's columns; VB: blocks of 16 * VW columns of V.  ONCE: the
+// KC: chunks of a key's columns, of which the first FULL surely lie within d (all
+// of them where d is their width); VB: blocks of 16 * VW columns of V.  ONCE: the
 // cache is read past the caches.  That is for large ones that no second row of
 // heads reads: 16 sequences of 4096, 32 heads on 8, 128 wide bf16 take 50 us
 // against 55, but 64 heads on 2 of 8192 46 against 40, and a cache of 33 MB 15.8
 // against 14.2.
-template <class T, uint32_t KC, uint32_t VB, uint32_t VW, bool NARROW, bool ONCE>
+template <class T, uint32_t KC, uint32_t FULL, uint32_t VB, uint32_t VW, bool NARROW, bool ONCE>
 __global__ __launch_bounds__(ATT_THREADS, KC * VB > 8 ? 1 : 2) void k_attend(AttArgs a) {
   typedef Att<T> C;
   constexpr uint32_t TILES = C::STEP / 16, KEYS = TILES * 4;   // KEYS: a lane's keys of a step
@@ -232,7 +240,8 @@ __global__ __launch_bounds__(ATT_THREADS, KC * VB > 8 ? 1 : 2) void k_attend(Att
     const T* qrow = static_cast<const T*>(a.q) + (uint64_t)b * a.sqb + (uint64_t)(h * a.group + h0 + (mine ? col : 0)) * a.sqh;
 
     // Q as the second operand.  A row's last vector begins earlier, so that it
-    // ends with the row: what the vector before it has is 0 here.
+    // ends with the row: what the vector before it has is 0 here, and in the keys
+    // too (0 * inf is not 0).
     typename C::Frag q[KC];
     uint32_t kcol[KC], vcol[VB];
 #pragma unroll
@@ -292,13 +301,28 @@ __global__ __launch_bounds__(ATT_THREADS, KC * VB > 8 ? 1 : 2) void k_attend(Att
       }
       vbase += (int64_t)UNIT * a.svn;
       float s[KEYS];
+      // what a row's last vector shares with the one before it is 0, not only in Q
+      u32x4 keep[KC];
+      if constexpr (!NARROW) {
+#pragma unroll
+        for (uint32_t c = FULL; c < KC; ++c) {
+          uint32_t seen = c * C::KCHUNK + g * C::KVEC - kcol[c];   // of the vector's columns
+          asm volatile("" : "+v"(seen));   // masks held through the loop cost a wave a SIMD up to 64 wide
+#pragma unroll
+          for (uint32_t i = 0; i < 4; ++i) keep[c][i] = unseen<T>(~0u, i, seen);
+        }
+      }
 #pragma unroll
       for (uint32_t t = 0; t < TILES; ++t) {
         f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (uint32_t c = 0; c < KC; ++c) {
+          u32x4 kw;
+          __builtin_memcpy(&kw, kv[t][c], 16);
+          if constexpr (!NARROW)
+            if (c >= FULL) kw &= keep[c];
           typename C::Frag kf;
-          __builtin_memcpy(&kf, kv[t][c], sizeof(kf));
+          __builtin_memcpy(&kf, &kw, sizeof(kf));
           if constexpr (sizeof(T) == 2) {
             acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, q[c], acc, 0, 0, 0);
           } else {
@@ -638,34 +662,43 @@ AttPlan attend_plan(const topk_attend_args& a, int cus) {
 
 constexpr int64_t ONCE_BYTES = int64_t(64) << 20;   // keys and values that are read past the caches
 
-template <class T, uint32_t KC, uint32_t VB, uint32_t VW, bool NARROW>
-void attend_one(const AttArgs& a, hipStream_t s) {
+template <class T, uint32_t KC, uint32_t FULL, uint32_t VB, uint32_t VW, bool NARROW>
+void attend_launch(const AttArgs& a, hipStream_t s) {
   const uint32_t heads = std::min(a.group, HEADS);
   const size_t lds = (ATT_WAVES * heads * a.d + 2 * ATT_WAVES * HEADS) * sizeof(float);
   if constexpr (!NARROW) {
     if (a.blocks16 == 1 && 2 * (int64_t)a.batch * a.kv_heads * a.n * a.d * (int64_t)sizeof(T) >= ONCE_BYTES) {
-      k_attend<T, KC, VB, VW, false, true><<<wide_grid(a.work), ATT_THREADS, lds, s>>>(a);
+      k_attend<T, KC, FULL, VB, VW, false, true><<<wide_grid(a.work), ATT_THREADS, lds, s>>>(a);
       return;
     }
   }
-  k_attend<T, KC, VB, VW, NARROW, false><<<wide_grid(a.work), ATT_THREADS, lds, s>>>(a);
+  k_attend<T, KC, FULL, VB, VW, NARROW, false><<<wide_grid(a.work), ATT_THREADS, lds, s>>>(a);
+}
+
+// FULL: of the narrowest d that comes here.
+template <class T, uint32_t KC, uint32_t FULL, uint32_t VB, uint32_t VW, bool NARROW>
+void attend_one(const AttArgs& a, hipStream_t s) {
+  if constexpr (!NARROW) {
+    if (a.d == KC * Att<T>::KCHUNK) return attend_launch<T, KC, KC, VB, VW, false>(a, s);
+  }
+  attend_launch<T, KC, FULL, VB, VW, NARROW>(a, s);
 }
 
 void attend_typed(const AttArgs& a, bf16_t, hipStream_t s) {
-  if (a.d < 8) attend_one<bf16_t, 1, 1, 4, true>(a, s);
-  else if (a.d <= 64) attend_one<bf16_t, 2, 1, 4, false>(a, s);
-  else if (a.d <= 96) attend_one<bf16_t, 3, 1, 8, false>(a, s);
-  else if (a.d <= 128) attend_one<bf16_t, 4, 1, 8, false>(a, s);
-  else if (a.d <= 192) attend_one<bf16_t, 6, 2, 8, false>(a, s);
-  else attend_one<bf16_t, 8, 2, 8, false>(a, s);
+  if (a.d < 8) attend_one<bf16_t, 1, 0, 1, 4, true>(a, s);
+  else if (a.d <= 64) attend_one<bf16_t, 2, 0, 1, 4, false>(a, s);
+  else if (a.d <= 96) attend_one<bf16_t, 3, 2, 1, 8, false>(a, s);
+  else if (a.d <= 128) attend_one<bf16_t, 4, 3, 1, 8, false>(a, s);
+  else if (a.d <= 192) attend_one<bf16_t, 6, 4, 2, 8, false>(a, s);
+  else attend_one<bf16_t, 8, 6, 2, 8, false>(a, s);
 }
 void attend_typed(const AttArgs& a, float, hipStream_t s) {
-  if (a.d < 4) attend_one<float, 1, 1, 4, true>(a, s);
-  else if (a.d <= 64) attend_one<float, 4, 1, 4, false>(a, s);
-  else if (a.d <= 96) attend_one<float, 6, 2, 4, false>(a, s);
-  else if (a.d <= 128) attend_one<float, 8, 2, 4, false>(a, s);
-  else if (a.d <= 192) attend_one<float, 12, 3, 4, false>(a, s);
-  else attend_one<float, 16, 4, 4, false>(a, s);
+  if (a.d < 4) attend_one<float, 1, 0, 1, 4, true>(a, s);
+  else if (a.d <= 64) attend_one<float, 4, 0, 1, 4, false>(a, s);
+  else if (a.d <= 96) attend_one<float, 6, 4, 2, 4, false>(a, s);
+  else if (a.d <= 128) attend_one<float, 8, 6, 2, 4, false>(a, s);
+  else if (a.d <= 192) attend_one<float, 12, 8, 3, 4, false>(a, s);
+  else attend_one<float, 16, 12, 4, 4, false>(a, s);
 }
 
 template <class T>
