@@ -105,3 +105,21 @@ def test_keys_of_minus_infinity(d, dt):
         U.within(tss().attend(q, k, v).cpu(), out, eo, (n, "out alone"))
         U.within(scores[:, :, good].cpu(), 0.25 + add, ea, (n, "scores"))
         assert bool((scores[0, 0, bad] == 0.25).all())
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_pieces_of_minus_infinity(dt):
+    # whole workgroups' shares of entries without a probability, and all other logits far below 0
+    for n, first, last in ((1000, 0, 513), (1000, 300, 999), (3000, 0, 2999), (3000, 1, 3000), (200, 0, 199), (260, 0, 256)):
+        q = torch.zeros(2, 20, 16, dtype=DT[dt], device="cuda")
+        q[..., 0] = 1.0
+        k, v = rnd(n, 2, 1, n, 16, dt=dt), rnd(n + 1, 2, 1, n, 16, dt=dt)
+        k[..., 0] -= 200.0
+        k[:, :, first:last, 0] = -math.inf
+        good = [j for j in range(n) if not first <= j < last]
+        out, eo, add, ea = M.attend64(q, k[:, :, good], v[:, :, good], None, 1.0, q.dtype)
+        scores = torch.full((2, 1, n), 0.25, device="cuda")
+        U.within(tss().attend(q, k, v, scores=scores, scale=1.0).cpu(), out, eo, (n, "out"))
+        U.within(tss().attend(q, k, v, scale=1.0).cpu(), out, eo, (n, "out alone"))
+        U.within(scores[:, :, good].cpu(), 0.25 + add, ea, (n, "scores"))
+        assert bool((scores[:, :, first:last] == 0.25).all())

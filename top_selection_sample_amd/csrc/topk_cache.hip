@@ -462,7 +462,7 @@ __global__ __launch_bounds__(ATT_THREADS, KC * VB > 8 ? 1 : 2) void k_attend(Att
         sum += f * wl[w * HEADS + threadIdx.x];
       }
       wl[threadIdx.x] = sum;
-      wl[HEADS + threadIdx.x] = top == -INFINITY ? 0.f : top;
+      wl[HEADS + threadIdx.x] = top;   // -inf: a piece without a probability, which the join gives the factor 0
     }
     __syncthreads();
     const uint64_t piece = (uint64_t)b * rows + row + id;
