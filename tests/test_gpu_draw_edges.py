@@ -1,0 +1,58 @@
+"""The next token at the ends of its ranges: tokens of little weight and their
+probabilities, distances that overflow float32, settings that want a gradient."""
+import math
+
+import pytest
+
+import model_util as M
+import ops_util as U
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+LAST = 1 - 2.0 ** -24     # the largest float32 below 1
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def tss():
+    import top_selection_sample_amd
+    return top_selection_sample_amd
+
+
+def rnd(seed, *shape, dt="f32", scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g) * scale).to(DT[dt]).cuda()
+
+
+def check(z, u, label="", off=1e-9, **kw):
+    full = dict(temperature=1.0, top_k=0, top_p=1.0, min_p=0.0) | kw
+    token, logprob = tss().sample(z, u, **kw)
+    rows = z.shape[0]
+    zc, uc = z.cpu(), u.tolist()
+    want = [M.sample64(zc[r], uc[r], *(M.f32(full["temperature"]), full["top_k"], M.f32(full["top_p"]), M.f32(full["min_p"]))) for r in range(rows)]
+    assert token.tolist() == [t for t, _ in want], label
+    U.within(logprob.cpu(), torch.tensor([p for _, p in want], dtype=torch.float64), torch.full((rows,), off, dtype=torch.float64), label)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [12, 400, 3000, 9000])
+def test_distances_that_overflow(n, dt):
+    # logits at both ends of the type, at temperatures that make something of their distance: it is no float32, but counts
+    z = rnd(n, 4, n, scale=1e38).cpu().clamp(-3.2e38, 3.2e38)
+    z[0, 0], z[0, 1:] = 3.2e38, -3.2e38
+    z[1, n // 2] = 3.3e38
+    z[1, ::3] = -3.3e38
+    z[2, :] = -3.3e38
+    z[2, n - 1] = 3.3e38
+    z = z.to(DT[dt]).cuda()
+    assert bool(torch.isfinite(z).all())
+    for u in (2.0 ** -20, 0.5, 0.9, LAST):
+        for t in (1e37, 1.5e38, 3.4e38):
+            for kw in (dict(), dict(top_k=1), dict(top_k=2), dict(top_k=7), dict(top_k=n - 1), dict(top_k=n), dict(top_p=0.5), dict(top_p=0.97),
+                       dict(top_k=9, top_p=0.9), dict(min_p=0.02)):
+                check(z, torch.full((4,), u, device="cuda"), (u, t, kw), temperature=t, **kw)

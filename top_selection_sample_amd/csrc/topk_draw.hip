@@ -176,7 +176,7 @@ __device__ __forceinline__ uint32_t bin_of(float z, float m) {
 }
 
 // m - z of all logits in bins up to b, but the equals of an infinite m, is below
-// this; that of a logit of -inf is not.
+// this; that of a logit of -inf is not, nor is one that overflows (last bin).
 __device__ __forceinline__ float bin_end(uint32_t b) { return b >= BINS - 1 ? INFINITY : __uint_as_float((FIRST_BIN + b + 1) << 16); }
 
 // ceil(p * w) and floor(p * w), exact; p a float in (0, 1).
@@ -895,8 +895,9 @@ __device__ void finish_small(const SampleArgs& a, uint64_t r, const T* row, floa
   }
   __syncthreads();
   const uint32_t last = bin_reaching<ROW_THREADS>(l.count, k, l.part32, &l.pick);
-  const float below = bin_end(last);
-  auto near = [&](float z) { return m - z < below || z == m; };   // m > -inf
+  // By half the distance: of finite logits it does not overflow, and it rounds as the whole does.
+  const float half_below = 0.5f * bin_end(last), half_m = 0.5f * m;
+  auto near = [&](float z) { return fmaf(-0.5f, z, half_m) < half_below || z == m; };   // m > -inf
   uint32_t* hits = reinterpret_cast<uint32_t*>(l.sums);           // 2 * MAX_CHUNKS of them
   uint32_t found = 0;
   for (uint32_t b0 = 0; b0 < groups; b0 += BATCH) {
