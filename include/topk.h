@@ -606,6 +606,7 @@ int topk_evict(const topk_evict_args* args, void* workspace, size_t workspace_by
  *
  * w is held in 64 bits, as whole multiples of 2^-(62 - ceil(log2 n)), and so
  * every sum is exact: the token does not depend on how the row was divided.
+ * (The w of logprob is not rounded to a multiple.)
  *
  * Each of the four settings is a number for all rows, or, where its pointer is
  * not null, an array of one for each row in device memory. */

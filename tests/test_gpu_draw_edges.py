@@ -56,3 +56,30 @@ def test_distances_that_overflow(n, dt):
             for kw in (dict(), dict(top_k=1), dict(top_k=2), dict(top_k=7), dict(top_k=n - 1), dict(top_k=n), dict(top_p=0.5), dict(top_p=0.97),
                        dict(top_k=9, top_p=0.9), dict(min_p=0.02)):
                 check(z, torch.full((4,), u, device="cuda"), (u, t, kw), temperature=t, **kw)
+
+
+@pytest.mark.parametrize("n", [40, 300, 513, 3000, 131072, 300007])
+def test_probability_of_a_rare_token(n):
+    # a number of 0 draws the first token with any weight, here one of down to 2^-40 of the largest.  Its own weight counts
+    # as it is; the sum of all is of weights rounded to multiples of 2^-(62 - log2 n), off by less than n^2 2^-63 of the
+    # largest one, of which the logprob has as much
+    unit = 2.0 ** -(62 - math.ceil(math.log2(n)))
+    off = 1e-9 + n * unit
+    for others in (-math.inf, -2.0):
+        low = [2.0, 9.7, 16.1, 20.3, 23.9, 26.8, 28.1] if n <= 3000 or others == -math.inf else [16.1, 20.3, 26.8]
+        z = torch.full((len(low), n), others)
+        if others > -math.inf:
+            z += torch.randn(len(low), n, generator=torch.Generator().manual_seed(n)) * 0.5
+        for r, far in enumerate(low):
+            assert math.exp(-far) > 2 * unit
+            z[r, 0] = -far
+            z[r, n // 2] = 0.0
+        z = z.cuda()
+        u = torch.zeros(len(low), device="cuda")
+        check(z, u, "plain", off)
+        check(z, u, "top_k", off, top_k=n - 1)
+        if n <= 3000:
+            check(z, u, "top_k and p", off, top_k=n, top_p=LAST)
+        for kw in (dict(top_k=2), dict(top_k=20)):
+            if others == -math.inf:
+                check(z, u, kw, off, **kw)

@@ -597,9 +597,11 @@ struct alignas(16) RowShared {
   uint32_t part32[ROW_WAVES], pick;
 };
 
-__device__ __forceinline__ void write_token(const SampleArgs& a, uint64_t r, int64_t token, uint64_t w, uint64_t all) {
+// A token of weight w, the whole in fixed point; -1: none.  The weight counts as it
+// is, not as the multiple that it is drawn by: of a rare token's that has few bits.
+__device__ __forceinline__ void write_token(const SampleArgs& a, uint64_t r, int64_t token, double w, uint64_t all) {
   a.tokens[r] = token;
-  a.logprobs[r] = token < 0 ? -INFINITY : (float)log((double)w / (double)all);
+  a.logprobs[r] = token < 0 ? -INFINITY : (float)log(ldexp(w, (int)a.bits) / (double)all);
 }
 
 // Each of the n <= PAIRS threads' value: the sum over all j < n of what `take`
@@ -700,12 +702,12 @@ __device__ void finish_few(const SampleArgs& a, uint64_t r, float m, const Setti
   if (t < PAIRS) l.sorted[t] = mine;
   thread_scan<ROW_THREADS>(mine, l.part64, &all);   // waits for l.sorted as well
   if (all == 0) {      // a min_p of NaN: nothing stays
-    if (t == 0) write_token(a, r, -1, 0, 1);
+    if (t == 0) write_token(a, r, -1, 0.0, 1);
     return;
   }
   const uint64_t target = target_of(u, all);
   const uint64_t lower = over_pairs(l, n, [](uint64_t own, uint64_t c, uint64_t x) { return ~(uint32_t)c < ~(uint32_t)own ? x : 0; });
-  if (mine && lower <= target && target < lower + mine) write_token(a, r, ~(uint32_t)code, mine, all);
+  if (mine && lower <= target && target < lower + mine) write_token(a, r, ~(uint32_t)code, f, all);
 }
 
 // The end of a row.  n_cand entries around the cut are in l.code (more than
@@ -811,7 +813,7 @@ __device__ void finish_row(const SampleArgs& a, uint64_t r, const T* row, float 
   for (uint32_t i = 0; i < SUMS; ++i) mine += own[i] = t * SUMS + i < a.chunks ? l.sums[t * SUMS + i] : 0;
   uint64_t before = thread_scan<ROW_THREADS>(mine, l.part64, &all);
   if (all == 0) {   // a min_p of NaN: nothing stays
-    if (t == 0) write_token(a, r, -1, 0, 1);
+    if (t == 0) write_token(a, r, -1, 0.0, 1);
     return;
   }
   const uint64_t target = target_of(u, all);
@@ -853,7 +855,7 @@ __device__ void finish_row(const SampleArgs& a, uint64_t r, const T* row, float 
       if (run <= rest && rest < run + sum) {
 #pragma unroll
         for (uint32_t j = 0; j < PER; ++j) {
-          if (run <= rest && rest < run + w[j]) write_token(a, r, j0 + j, w[j], all);
+          if (run <= rest && rest < run + w[j]) write_token(a, r, j0 + j, weight_of(z[j], m, s), all);
           run += w[j];
         }
       }
@@ -965,7 +967,7 @@ __global__ __launch_bounds__(ROW_THREADS) void k_sample_finish(SampleArgs a) {
   const uint32_t k = small_k(a, r);
   const float m = row_max(a, r);
   if (m == -INFINITY) {
-    if (threadIdx.x == 0) write_token(a, r, -1, 0, 1);
+    if (threadIdx.x == 0) write_token(a, r, -1, 0.0, 1);
     return;
   }
   if (k) {
