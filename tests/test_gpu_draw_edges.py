@@ -83,3 +83,20 @@ def test_probability_of_a_rare_token(n):
         for kw in (dict(top_k=2), dict(top_k=20)):
             if others == -math.inf:
                 check(z, u, kw, off, **kw)
+
+
+def test_settings_that_want_a_gradient():
+    # the results would be constants to autograd: refused, as logits that want one are
+    T, z, u = tss(), rnd(1, 3, 50), torch.rand(3, device="cuda")
+    one = torch.full((3,), 0.5, device="cuda", requires_grad=True)
+    for f in (lambda: T.sample(z, u, temperature=one), lambda: T.sample(z, u, top_p=one), lambda: T.sample(z, u, min_p=one), lambda: T.sample(z, one)):
+        with pytest.raises(RuntimeError, match="no gradient"):
+            f()
+        with torch.no_grad():
+            f()
+    from torch.autograd import forward_ad as F
+    with F.dual_level():
+        dual = F.make_dual(one.detach(), torch.ones(3, device="cuda"))
+        for f in (lambda: T.sample(z, u, temperature=dual), lambda: T.sample(z, u, top_p=dual), lambda: T.sample(z, u, min_p=dual)):
+            with pytest.raises(RuntimeError, match="forward-mode"):
+                f()

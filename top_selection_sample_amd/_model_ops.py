@@ -404,7 +404,7 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_
 
     A logit of -inf or NaN is never taken; a row of nothing else gives token -1
     and logprob -inf.  Sums are exact, so a row's token does not depend on the
-    rows beside it.  No gradient (logits that want one are refused)."""
+    rows beside it.  No gradient (tensors that want one are refused)."""
     _gpu(logits, "logits")
     _code(logits, "logits")
     squeeze = logits.dim() == 1
@@ -425,7 +425,7 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_
         top_k, ks = 0, top_k.contiguous()
     elif int(top_k) != top_k or top_k < 0:
         raise ValueError("top_k: a whole number from 0, or an int64 tensor of one for each row")
-    _not_recorded("sample", logits)
+    _not_recorded("sample", logits, u, ts, ps, ms)
     z, ld, _ = _matrix(z)
     dev = z.get_device()
     with _on(dev):
