@@ -123,3 +123,118 @@ def test_pieces_of_minus_infinity(dt):
         U.within(tss().attend(q, k, v, scale=1.0).cpu(), out, eo, (n, "out alone"))
         U.within(scores[:, :, good].cpu(), 0.25 + add, ea, (n, "scores"))
         assert bool((scores[:, :, first:last] == 0.25).all())
+
+
+def check_attend(q, k, v, lengths=None, label=""):
+    b, h, n, _ = k.shape
+    out, eo, add, ea = attend_bound(q, k, v, lengths)
+    U.within(tss().attend(q, k, v, lengths).cpu(), out, eo, f"{label} out alone")
+    before = torch.rand(b, h, n, generator=torch.Generator().manual_seed(1)).cuda()
+    scores = before.clone()
+    U.within(tss().attend(q, k, v, lengths, scores).cpu(), out, eo, f"{label} out")
+    U.within(scores.cpu(), before.cpu().double() + add, ea, f"{label} scores")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [5, 36, 65, 80, 96, 100, 128, 130, 192, 200, 256])
+def test_attend_shared_keys_of_every_width(d, dt):
+    check_attend(rnd(d, 3, 6, d, dt=dt), rnd(d + 1, 3, 2, 700, d, dt=dt), rnd(d + 2, 3, 2, 700, d, dt=dt), ends(700, 0, 411), d)
+    # more units than workgroups: several steps to a wave, pieces that end inside a row
+    check_attend(rnd(d, 9, 34, d, dt=dt), rnd(d + 1, 9, 2, 5003, d, dt=dt), rnd(d + 2, 9, 2, 5003, d, dt=dt),
+                 ends(5003, 1, 4096, 4097, 0, 2500, 5002, 3333, 4700), (d, "long"))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("hq,h,n", [(100, 1, 70), (100, 1, 700), (1000, 2, 300), (4096, 1, 40), (4096, 1, 600), (8192, 2, 130)])
+def test_attend_many_heads_on_one(hq, h, n, dt):
+    check_attend(rnd(hq, 2, hq, 16, dt=dt), rnd(h, 2, h, n, 16, dt=dt), rnd(h + 1, 2, h, n, 16, dt=dt), ends(n, n - 13), (hq, h, n))
+
+
+@pytest.mark.parametrize("dt,d", [("f32", 80), ("f32", 128), ("bf16", 96), ("bf16", 200)])
+def test_attend_past_the_caches(dt, d):
+    # 64 MB of keys and values and more, every head its own rows
+    n = (1 << 26) // (2 * 8 * d * (4 if dt == "f32" else 2)) + 5
+    check_attend(rnd(d, 2, 8, d, dt=dt), rnd(d + 1, 2, 4, n, d, dt=dt), rnd(d + 2, 2, 4, n, d, dt=dt), ends(n, n - 77), (dt, d))
+
+
+def test_attend_f32_offsets_beyond_32_bits():
+    n, d = (1 << 24) + 1000, 128
+    kv = torch.empty(1, 1, n, d, device="cuda")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    for i in range(0, n, 1 << 20):
+        kv[0, 0, i:i + (1 << 20)].normal_(generator=g)
+    # the last entries, far beyond 2^31 elements, take nearly all
+    kv[0, 0, n - 3:] = torch.eye(3, d, device="cuda") * 60
+    q = torch.zeros(1, 3, d, device="cuda")
+    for i in range(3):
+        q[0, i, i] = 12.0
+    scores = torch.zeros(1, 1, n, device="cuda")
+    out = tss().attend(q, kv, kv, scores=scores)
+    s = torch.cat([(kv[0, 0, i:i + (1 << 20)].double() @ q[0].double().t().contiguous()) for i in range(0, n, 1 << 20)]) * d ** -0.5
+    p = torch.softmax(s, 0)
+    # a logit of the others is below 10, that of the last ones 63: 2^24 of them have less than 2^24 e^-53 together
+    near = torch.zeros(3, d, dtype=torch.float64, device="cuda")
+    for i in range(0, n, 1 << 20):
+        near += p[i:i + (1 << 20)].t().contiguous() @ kv[0, 0, i:i + (1 << 20)].double()
+    r = 1.1 * (2 * (d + 4) * U.U32 * 64 + 2 * (64 + 15 + 4) * U.U32 + 20000 * U.U32)
+    U.within(out[0].cpu(), near.cpu(), torch.full((3, d), 60 * r, dtype=torch.float64), "out")
+    U.within(scores[0, 0].cpu(), p.sum(1).cpu(), p.sum(1).cpu() * r, "scores")
+    assert bool((scores[0, 0, n - 3:] > 0.99).all())
+
+
+# ---------------------------------------------------------------- evict
+def bits(t):
+    """NaN are equal to themselves."""
+    return t.cpu().contiguous().view(torch.int16 if t.dtype == torch.bfloat16 else torch.int32)
+
+
+def check_evict(k, v, s, budget, recent=0, lengths=None, out=None, label=""):
+    want, end = M.evict64(s, lengths, budget, recent)
+    marks = None if out is None else [t.clone() for t in out]
+    k2, v2, s2, kept, ln = tss().evict(k, v, s, budget, recent, lengths, out=out)
+    assert torch.equal(kept.cpu(), want), label
+    assert torch.equal(ln.cpu(), end), label
+    for x, (got, old) in enumerate(((k2, k), (v2, v), (s2, s))):
+        if out is None:
+            assert torch.equal(bits(got), bits(M.rows_of(old, want))), label
+            continue
+        for i, e in enumerate(end.tolist()):     # rows behind the last, as they were
+            assert torch.equal(bits(got[i, :, :e]), bits(M.rows_of(old, want)[i, :, :e])), label
+            assert torch.equal(bits(got[i, :, e:]), bits(marks[x][i, :, e:])), label
+
+
+@pytest.mark.parametrize("n", [16383, 16384, 16385, 20000, 40001])
+def test_evict_long_rows(n):
+    g = torch.Generator().manual_seed(n)
+    k, v = rnd(1, 3, 2, n, 6), rnd(2, 3, 2, n, 6, dt="f32")
+    for name, s in (("spread", torch.rand(3, 2, n, generator=g)), ("few values", torch.randint(0, 4, (3, 2, n), generator=g).float()),
+                    ("zeros", torch.zeros(3, 2, n)), ("ones", torch.ones(3, 2, n)),
+                    ("signs", torch.randn(3, 2, n, generator=g).mul(100).round().div(100))):
+        s = s.clone()
+        if name == "signs":
+            s[0, 0, ::5] = -0.0
+            s[0, 1, 1::7] = NAN
+            s[1, 0, ::3] = math.inf
+            s[1, 0, 1::3] = -math.inf
+            s[2, 1, ::2] = 1e-45
+        s = s.cuda()
+        for budget, recent in ((1, 0), (n // 4, 100), (n - 1, 0), (12000, 12000), (5000, 1)):
+            check_evict(k, v, s, budget, recent, ends(n, n - 3000, 5001), label=(name, budget, recent))
+        check_evict(k, v, s, 4000, 64, label=(name, "all"))
+
+
+@pytest.mark.parametrize("dt,d", [("f32", 515), ("bf16", 515), ("bf16", 128), ("f32", 3)])
+def test_evict_past_the_caches(dt, d):
+    # 16 MB of rows and more in each output
+    size = 4 if dt == "f32" else 2
+    budget = (1 << 24) // (2 * 2 * d * size) + 3
+    n = budget + budget // 3
+    k, v = rnd(1, 2, 2, n, d, dt=dt), rnd(2, 2, 2, n, d, dt=dt)
+    s = torch.rand(2, 2, n, generator=torch.Generator().manual_seed(3)).cuda()
+    for lengths in (ends(n, n - 5), ends(budget // 2, n)):
+        check_evict(k, v, s, budget, budget // 8, lengths, label=(dt, d))
+        out = (torch.full((2, 2, budget + 2, d), 7.0, dtype=DT[dt], device="cuda"),
+               torch.full((2, budget + 1, 2, d), 8.0, dtype=DT[dt], device="cuda").transpose(1, 2),
+               torch.full((2, 2, budget), 9.0, device="cuda"))
+        check_evict(k, v, s, budget, budget // 8, lengths, out=out, label=(dt, d, "out"))
