@@ -189,11 +189,14 @@ __device__ __forceinline__ bool place_of(const AttArgs& a, uint64_t w, Place* p)
 // KC: chunks of a key's columns, of which the first FULL surely lie within d (all
 // of them where d is their width); VB: blocks of 16 * VW columns of V.  ONCE: the
 // cache is read past the caches.  That is for large ones that no second row of
-// heads reads: 16 sequences of 4096, 32 heads on 8, 128 wide bf16 take 50 us
-// against 55, but 64 heads on 2 of 8192 46 against 40, and a cache of 33 MB 15.8
-// against 14.2.
+// heads reads: 16 sequences of 8192, 32 heads on 8, 128 wide bf16 take 84 us
+// against 99, of 4096 48 both ways, but 64 heads on 2 of 8192 44 against 33.
+//
+// Waves to a SIMD: what the registers leave, but three are asked for from 65 to 96
+// wide, where they are four short of it (1024 sequences of 200, 8 heads, 80 wide
+// bf16 98 us against 124 with two; 16 of 4096 38 both ways).
 template <class T, uint32_t KC, uint32_t FULL, uint32_t VB, uint32_t VW, bool NARROW, bool ONCE>
-__global__ __launch_bounds__(ATT_THREADS, KC * VB > 8 ? 1 : 2) void k_attend(AttArgs a) {
+__global__ __launch_bounds__(ATT_THREADS, KC * VB > 8 ? 1 : sizeof(T) == 2 && KC == 3 && ONCE ? 3 : 2) void k_attend(AttArgs a) {
   typedef Att<T> C;
   constexpr uint32_t TILES = C::STEP / 16, KEYS = TILES * 4;   // KEYS: a lane's keys of a step
   constexpr uint32_t UNIT = ATT_WAVES * C::STEP;
@@ -250,10 +253,13 @@ __global__ __launch_bounds__(ATT_THREADS, KC * VB > 8 ? 1 : 2) void k_attend(Att
       kcol[c] = NARROW ? want : min(want, d - C::KVEC);
       T t[C::KVEC];
       load_cols<T, C::KVEC, NARROW, false>(qrow + kcol[c], kcol[c], d, t);
+      uint32_t seen = mine ? want - kcol[c] : C::KVEC;
+      asm volatile("" : "+v"(seen));   // as conditions held for the next piece they fill the scalar registers
+      u32x4 w;
+      __builtin_memcpy(&w, t, 16);
 #pragma unroll
-      for (uint32_t i = 0; i < C::KVEC; ++i)
-        if (!mine || kcol[c] + i < want) t[i] = T{};
-      __builtin_memcpy(&q[c], t, sizeof(q[c]));
+      for (uint32_t i = 0; i < 4; ++i) w[i] = unseen<T>(w[i], i, seen);
+      __builtin_memcpy(&q[c], &w, sizeof(q[c]));
     }
 #pragma unroll
     for (uint32_t x = 0; x < VB; ++x) {
