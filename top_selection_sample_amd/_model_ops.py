@@ -205,6 +205,8 @@ def combine_grad(grad: torch.Tensor, y: torch.Tensor, places: torch.Tensor, weig
                  need: tuple = (True, True)) -> tuple:
     """Gradients (dy, dweights) of ``combine`` from ``grad`` = dL/dout [t, d].
     Rows of y that no place names get 0, weights of places out of range too.
+    Entries that name one row are added one after another (1.2 us each at 1024
+    columns of bfloat16): dropped ones have the place -1, not one row for all.
     ``need``: which of the two to compute; None stands for the other, and for
     dweights where there are no weights."""
     _check_combine(y, places, weights)

@@ -5,7 +5,7 @@
 //   evict    the entries with the largest scores, and the newest, in their old order
 //
 // Both are bound by the cache that they read.  16 sequences of 8192, 32 heads on
-// 8, 128 wide bf16 (537 MB) take 86 us without the scores, 6.2 TB/s, and 112
+// 8, 128 wide bf16 (537 MB) take 85 us without the scores, 6.3 TB/s, and 109
 // with them: the logits go through memory once, for a probability is known only
 // when the whole row is (17 MB written and read).  Lengths spread evenly up to
 // 8192 take 60 to 72, with the lengths drawn: 45 to 60 the first launch, 7.5 the
@@ -638,8 +638,8 @@ struct AttPlan {
 };
 
 // A row that one workgroup soon goes through is one workgroup's, in one launch;
-// otherwise the keys are shared out over as many workgroups as the card holds at
-// a time (two to a compute unit), as long as each has a unit.
+// otherwise the keys are shared out over two workgroups to a compute unit, as long
+// as each has a unit.  (Heads wider than 128 leave room for one at a time.)
 AttPlan attend_plan(const topk_attend_args& a, int cus) {
   AttPlan p;
   if (!a.batch || !a.heads || !a.n || !a.d) return p;
@@ -802,8 +802,8 @@ struct EvictArgs {
 //
 // The counts come in COPIES, one for every COPIES-th lane: lanes that count in
 // the same place wait for one another (128 rows of 16384 with a copy of 8
-// columns: all scores equal 59 us with one copy, 30 with four, 27 with eight;
-// spread scores 30, 31 and 32).
+// columns down to 4096: all scores 1 59 us with one copy, 30 with four, 28 with
+// eight; spread scores 34, 34 and 35).
 constexpr uint32_t PICK_BINS = 2048, COPIES = 4, COPY_STRIDE = PICK_BINS + 8, ALL_OF_BIN = 0x80000000u;
 constexpr uint32_t ZERO_KEY = 0x80000000u;
 __device__ __forceinline__ uint32_t bin_from_top(const uint32_t* hist, uint32_t* need, uint32_t* part, uint32_t* found) {

@@ -10,8 +10,10 @@
 // weights are whole multiples of 2^-F, F = 62 - ceil(log2 n), in 64 bits: sums
 // are exact, in whatever order and whatever pieces they are taken (atomics
 // included), and the comparisons with top_p and u are exact as well.  The
-// exponential is a polynomial in 64-bit floats, off by less than 2^-50 of its
-// value.
+// exponential is a polynomial in 64-bit floats: of 2^t, t = (z - m) log2(e) /
+// temperature, it is off by less than (1 + |t|) 2^-51 of its value (three roundings
+// of t, each up to 2^-53 of it, and those of the polynomial), so by less than 2^-50
+// of the largest weight.
 //
 // top_k and top_p keep a beginning of the one order, so together they are one
 // cut: a logit and an index.  A row is cut into chunks, a workgroup each:
@@ -36,8 +38,8 @@
 // first pass, 15 the last, 2 to 3 each of the three that find nothing to do); 256
 // rows of 65536 f32 (67 MB) with min_p 33: 11.8 for the maxima, 5.7 TB/s, 15 for
 // the sums, which reads the logits once more, and 6.7.  153 rows of 78201 bf16
-// with top_p alone 95: 7, 30 for the bins, bound by their atomics in LDS, 5, 30
-// and 24.
+// with top_p alone 92: 6, 30 for the bins, bound by their atomics in LDS, 5, 32
+// and 23.
 #include <algorithm>
 
 #include "topk_model.hpp"
@@ -229,7 +231,7 @@ __device__ __forceinline__ float row_max(const SampleArgs& a, uint64_t r) {
 
 // A row whose k is at most this gets its first k by way of its groups.  Where k
 // of G groups reach a bin, about n (1 - (1 - k / G)^(1 / GROUP)) entries do: 1.15
-// k for a quarter of the groups, an eighth of the row for three quarters.  So
+// k for a quarter of the groups, a twelfth of the row for three quarters.  So
 // many are compared each with each, if they are at most PAIRS.
 __host__ __device__ __forceinline__ int64_t small_limit(int64_t n) {
   if (n <= (int64_t)PAIRS) return n;
