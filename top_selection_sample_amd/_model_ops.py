@@ -275,7 +275,8 @@ def attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lengths: torch.Ten
 
     Returns [b, hq, d]; 0 for a sequence of length 0.  Softmax statistics and
     sums are held in 32 bits; in bfloat16 a probability's product with v is of
-    two bfloat16 numbers, off by less than 2 ** -14 of it.  No gradient (tensors that want one are refused)."""
+    two bfloat16 numbers, off by less than 2 ** -14 of it.  No gradient (tensors
+    that want one are refused)."""
     _gpu(q, "q")
     _code(q, "q")
     if q.dim() != 3:

@@ -192,9 +192,9 @@ __device__ __forceinline__ bool place_of(const AttArgs& a, uint64_t w, Place* p)
 // heads reads: 16 sequences of 8192, 32 heads on 8, 128 wide bf16 take 84 us
 // against 99, of 4096 48 both ways, but 64 heads on 2 of 8192 44 against 33.
 //
-// Waves to a SIMD: what the registers leave, but three are asked for from 65 to 96
-// wide, where they are four short of it (1024 sequences of 200, 8 heads, 80 wide
-// bf16 98 us against 124 with two; 16 of 4096 38 both ways).
+// Waves to a SIMD: what the registers leave, but three are asked for where they are
+// a few short of it, in bf16 from 65 to 96 wide past the caches (1024 sequences of
+// 200, 8 heads, 80 wide 98 us against 124 with two; 16 of 4096 38 both ways).
 template <class T, uint32_t KC, uint32_t FULL, uint32_t VB, uint32_t VW, bool NARROW, bool ONCE>
 __global__ __launch_bounds__(ATT_THREADS, KC * VB > 8 ? 1 : sizeof(T) == 2 && KC == 3 && ONCE ? 3 : 2) void k_attend(AttArgs a) {
   typedef Att<T> C;
